@@ -543,6 +543,126 @@ qnre_status_t ulysses_sage2_scatter_qkv(const qnre_tensor4_t* q, const qnre_tens
                                         float* v_scale, void* workspace, uint64_t workspace_bytes,
                                         qnre_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Speculative decoding over a paged cache: what a serving step runs on the
+ * projection's q, k, v.  The drafted tokens of a request form a tree whose
+ * node 0 is the last emitted token; every parent comes before its children.
+ * ------------------------------------------------------------------------ */
+
+#define QNRE_MAX_NODES 64 /* drafted nodes of one request, the root among them */
+#define QNRE_MAX_CALL_ROWS 1024 /* requests one call serves */
+
+/* Bits of a cache's status word (set by kernels, never cleared by them). */
+#define QNRE_CACHE_NO_PAGES 0x1u   /* a reserve needed more free pages than there were: it changed nothing */
+#define QNRE_CACHE_BAD_ROW 0x2u    /* a row index outside [0, rows), a fork onto a row in use: skipped */
+#define QNRE_CACHE_BAD_PAGE 0x4u   /* a token's page was missing or outside the cache: a write or move was skipped,
+                                      an attention read it as zeros */
+#define QNRE_CACHE_BAD_REFS 0x8u   /* a page was released more often than it was taken */
+#define QNRE_CACHE_WAIT_TIMEOUT 0x10u /* a pipeline wait of the attention kernel ran past its limit; outputs incomplete */
+
+/*
+ * A paged cache (host struct; every pointer is device memory of the caller).
+ * Row r holds seq_lens[r] tokens; token p of it lies in slot p % page_size of
+ * page block_table[r][p / page_size].  A page of one layer keeps each head's
+ * tokens together: page_size * head_dim values in a run.  page_refs counts
+ * the rows that hold a page; 0 means free.  Blocks a row does not hold are -1.
+ */
+typedef struct {
+  void* k;              /* [layers, pages, heads, page_size, head_dim], contiguous, 16-byte aligned */
+  void* v;              /* the same */
+  int32_t* block_table; /* [rows, max_blocks] */
+  int32_t* seq_lens;    /* [rows] */
+  int32_t* page_refs;   /* [pages], 16-byte aligned */
+  uint32_t* status;     /* [1], QNRE_CACHE_* bits */
+  int32_t* scratch;     /* 4 * pages + 4 words, overwritten by qnre_cache_reserve */
+  int32_t layers, pages, heads, page_size, head_dim, rows, max_blocks;
+  int32_t dtype; /* QNRE_DTYPE_BF16 or QNRE_DTYPE_FP16 */
+} qnre_cache_t;
+
+/*
+ * Checks common to the cache calls: NULL pointers or extents below 1 ->
+ * QNRE_ERR_INVALID_ARG; head_dim other than 64 or 128, a dtype other than bf16
+ * or fp16, a page_size that is not a multiple of 8 -> QNRE_ERR_UNSUPPORTED; k, v
+ * or page_refs off 16 bytes -> QNRE_ERR_ALIGNMENT; layers*pages, rows*max_blocks or
+ * max_blocks*page_size above 2^31-1, n above QNRE_MAX_CALL_ROWS -> QNRE_ERR_CAPACITY.
+ * n == 0 is an empty call.  The rows of one call are distinct.
+ *
+ * qnre_cache_truncate -- row rows[i] keeps its first lens[i] tokens (no more than it
+ *   has); every block past them is released.  lens[i] = 0 frees the row.
+ * qnre_cache_fork -- row dst[i] (empty, no source of the call) becomes a copy of row src[i]
+ *   that shares its pages.
+ * qnre_cache_reserve -- gives row rows[i] pages of its own for tokens
+ *   [seq_lens, seq_lens + counts[i]): missing blocks get the lowest-numbered free
+ *   pages, in the order of the call's rows and of each row's blocks; a block that
+ *   other rows held too when the call began is replaced by a new page, with the old one's
+ *   contents in every layer where the row has tokens in it.  Lengths do not change.
+ *   All or nothing: with too few free pages, or a row that would pass max_blocks, only
+ *   QNRE_CACHE_NO_PAGES is set.
+ * qnre_cache_compact -- keeps the accepted nodes of a drafted tree: token
+ *   seq_lens + path[i][j] moves to seq_lens + j for j < counts[i], in every layer; the
+ *   length grows by counts[i] and blocks past it are released.  path[i] ascends
+ *   strictly from path[i][0] >= 0.  path is [n, nodes] int32, nodes <= QNRE_MAX_NODES.
+ * qnre_cache_copy_pages -- page src[i] to page dst[i] in every layer; the destinations
+ *   are distinct and no source.
+ *   rows, lens, counts, src, dst: device int32 [n].
+ */
+qnre_status_t qnre_cache_truncate(const qnre_cache_t* cache, const int32_t* rows, const int32_t* lens, int n,
+                                  qnre_stream_t stream);
+qnre_status_t qnre_cache_fork(const qnre_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
+                              qnre_stream_t stream);
+qnre_status_t qnre_cache_reserve(const qnre_cache_t* cache, const int32_t* rows, const int32_t* counts, int n,
+                                 qnre_stream_t stream);
+qnre_status_t qnre_cache_compact(const qnre_cache_t* cache, const int32_t* rows, const int32_t* path,
+                                 const int32_t* counts, int n, int nodes, qnre_stream_t stream);
+qnre_status_t qnre_cache_copy_pages(const qnre_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
+                                    qnre_stream_t stream);
+
+/*
+ * qnre_qk_norm_rope -- the epilogue's per-head RMSNorm and rotation on q and k that
+ * lie in memory, with any number of query and key heads:
+ *
+ *   o = R(pos) (y * rsqrt(mean(y^2) + 1e-6) * w)      in fp32, rounded once
+ *
+ *   q, k        views [B, S, Hq, D] and [B, S, Hk, D], bf16 or fp16, D = 64 or 128, the
+ *               channel axis contiguous, every row and the base 16-byte aligned.
+ *   q_norm_w, k_norm_w  device [D] of that dtype, 16-byte aligned.
+ *   cos_sin     device fp32 [n_pos, rot], row p = [cos_0.. | sin_0..], 16-byte aligned;
+ *               rot is a multiple of 16 up to D: the first rot channels rotate (ROTATE_HALF
+ *               pairs i with i + rot/2, INTERLEAVED 2i with 2i+1), the rest pass.
+ *   positions   device int32 [B, S]; NULL: token s of each sequence is at position s.  A
+ *               position outside the table gives NaN rows.
+ *   q_out, k_out  views of the same shapes and dtype with the same alignment; each may be
+ *               its own input exactly (same base and strides), and overlaps nothing else.
+ *
+ * qnre_qk_norm_rope_backward -- the gradient: dq, dk in the inputs' dtype (views; each may
+ *   be its gradient input exactly), and the fp32 [D] sums dq_norm_w, dk_norm_w over all
+ *   tokens and heads, taken in a fixed order.  gq, gk: the output gradients (views).
+ *   Rows at a bad position get NaN and make the weights' gradients NaN.
+ *   workspace: qnre_qk_norm_rope_workspace_bytes(D), 16-byte aligned.
+ *
+ * qnre_qkv_norm_rope_append -- qnre_qk_norm_rope over the new tokens [n, S, ...] of the
+ *   rows rows[i] (device int32 [n]), with k and v written into layer `layer` of the cache
+ *   as tokens seq_lens + s, s < min(counts[i], S) (counts NULL: all S).  The pages must be
+ *   there (qnre_cache_reserve); lengths do not change (qnre_cache_compact).  v is a view like k.
+ *   positions NULL: seq_lens + s.  Every token's q_out is written.
+ */
+qnre_status_t qnre_qk_norm_rope(const qnre_tensor4_t* q, const qnre_tensor4_t* k, const void* q_norm_w,
+                                const void* k_norm_w, const float* cos_sin, int64_t n_pos, int rot, int rope_style,
+                                const int32_t* positions, const qnre_tensor4_t* q_out, const qnre_tensor4_t* k_out,
+                                qnre_stream_t stream);
+qnre_status_t qnre_qk_norm_rope_workspace_bytes(int head_dim, uint64_t* bytes);
+qnre_status_t qnre_qk_norm_rope_backward(const qnre_tensor4_t* gq, const qnre_tensor4_t* gk, const qnre_tensor4_t* q,
+                                         const qnre_tensor4_t* k, const void* q_norm_w, const void* k_norm_w,
+                                         const float* cos_sin, int64_t n_pos, int rot, int rope_style,
+                                         const int32_t* positions, const qnre_tensor4_t* dq, const qnre_tensor4_t* dk,
+                                         float* dq_norm_w, float* dk_norm_w, void* workspace, uint64_t workspace_bytes,
+                                         qnre_stream_t stream);
+qnre_status_t qnre_qkv_norm_rope_append(const qnre_tensor4_t* q, const qnre_tensor4_t* k, const qnre_tensor4_t* v,
+                                        const void* q_norm_w, const void* k_norm_w, const float* cos_sin,
+                                        int64_t n_pos, int rot, int rope_style, const int32_t* positions,
+                                        const qnre_tensor4_t* q_out, const qnre_cache_t* cache, int layer,
+                                        const int32_t* rows, const int32_t* counts, qnre_stream_t stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

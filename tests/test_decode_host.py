@@ -1,0 +1,181 @@
+"""Refusals of the speculative-decoding calls: status codes before anything reaches a GPU."""
+import ctypes
+import os
+
+import pytest
+
+from ulysses_qkv_proj_gb300 import binding as qb
+
+A = 1 << 32  # addresses that are only ever checked, 16-byte aligned and far apart
+MB = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(qb.LIB_PATH):
+        from ulysses_qkv_proj_gb300 import build
+        build.build()
+    return qb.load_library()
+
+
+def cache(**kw):
+    f = dict(k=A, v=A + 64 * MB, block_table=A + 128 * MB, seq_lens=A + 129 * MB, page_refs=A + 130 * MB,
+             status=A + 131 * MB, scratch=A + 132 * MB, layers=2, pages=4, heads=2, page_size=16, head_dim=128, rows=4,
+             max_blocks=4, dtype=0)
+    f.update(kw)
+    return qb._Cache(*[f[n] for n, _ in qb._Cache._fields_])
+
+
+def view(ptr, shape, stride=None, dtype=0):
+    t = qb._Tensor4()
+    t.data = ptr
+    if stride is None:
+        stride, n = [0] * 4, 1
+        for i in reversed(range(4)):
+            stride[i], n = n, n * max(1, shape[i])
+    for i in range(4):
+        t.shape[i], t.stride[i] = shape[i], stride[i]
+    t.dtype = dtype
+    return t
+
+
+CACHE_BAD = [
+    (dict(k=None), 1), (dict(scratch=None), 1), (dict(pages=0), 1), (dict(max_blocks=0), 1), (dict(rows=-1), 1),
+    (dict(head_dim=96), 2), (dict(dtype=2), 2), (dict(page_size=12), 2), (dict(k=A + 8), 3),
+    (dict(page_refs=A + 130 * MB + 4), 3), (dict(seq_lens=A + 129 * MB + 2), 3),
+    (dict(layers=1 << 16, pages=1 << 16), 5), (dict(rows=1 << 20, max_blocks=1 << 12), 5),
+    (dict(max_blocks=1 << 28), 5),
+]
+
+
+@pytest.mark.parametrize("kw,want", CACHE_BAD)
+def test_cache_checks(lib, kw, want):
+    c = ctypes.byref(cache(**kw))
+    L = A + 256 * MB
+    assert lib.qnre_cache_truncate(c, L, L + MB, 1, None) == want
+    assert lib.qnre_cache_fork(c, L, L + MB, 1, None) == want
+    assert lib.qnre_cache_reserve(c, L, L + MB, 1, None) == want
+    assert lib.qnre_cache_copy_pages(c, L, L + MB, 1, None) == want
+    assert lib.qnre_cache_compact(c, L, L + MB, L + 2 * MB, 1, 4, None) == want
+
+
+def test_cache_call_arguments(lib):
+    c, L = ctypes.byref(cache()), A + 256 * MB
+    assert lib.qnre_cache_truncate(None, L, L + MB, 1, None) == 1
+    assert lib.qnre_cache_truncate(c, None, L, 1, None) == 1
+    assert lib.qnre_cache_truncate(c, L + 2, L, 1, None) == 3
+    assert lib.qnre_cache_truncate(c, L, L + MB, -1, None) == 1
+    assert lib.qnre_cache_truncate(c, L, L + MB, 1025, None) == 5
+    assert lib.qnre_cache_compact(c, L, L + MB, L + 2 * MB, 1, 0, None) == 1
+    assert lib.qnre_cache_compact(c, L, L + MB, L + 2 * MB, 1, 65, None) == 5
+    for call in (lib.qnre_cache_truncate, lib.qnre_cache_fork, lib.qnre_cache_reserve, lib.qnre_cache_copy_pages):
+        assert call(c, None, None, 0, None) == 0
+
+
+def norm_args(**kw):
+    f = dict(q=view(A, [1, 4, 4, 128]), k=view(A + MB, [1, 4, 2, 128]), wq=A + 2 * MB, wk=A + 2 * MB + 256,
+             cs=A + 3 * MB, n_pos=8, rot=128, style=0, pos=None, qo=view(A + 4 * MB, [1, 4, 4, 128]),
+             ko=view(A + 5 * MB, [1, 4, 2, 128]))
+    f.update(kw)
+    return f
+
+
+NORM_BAD = [
+    (dict(q=view(None, [1, 4, 4, 128])), 1),
+    (dict(q=view(A, [1, 4, 4, 96])), 2),
+    (dict(q=view(A, [1, 4, 4, 128], dtype=2)), 2),
+    (dict(q=view(A + 8, [1, 4, 4, 128])), 3),
+    (dict(q=view(A, [1, 4, 4, 128], [2048, 516, 128, 1])), 3),
+    (dict(q=view(A, [1, 4, 4, 128], [2048, 1, 512, 4])), 3),
+    (dict(q=view(A, [1, 3, 4, 128])), 1),
+    (dict(k=view(A + MB, [1, 4, 2, 128], dtype=1)), 1),
+    (dict(k=view(A + MB, [1, 4, 2, 64])), 1),
+    (dict(wq=None), 1), (dict(wk=A + 8), 3), (dict(cs=None), 1), (dict(cs=A + 4), 3), (dict(n_pos=0), 1),
+    (dict(rot=130), 1), (dict(rot=0), 1), (dict(rot=24), 1), (dict(style=2), 1), (dict(pos=A + 6 * MB + 2), 3),
+]
+
+
+@pytest.mark.parametrize("kw,want", NORM_BAD)
+def test_norm_checks(lib, kw, want):
+    a = norm_args(**kw)
+    head = [ctypes.byref(a["q"]), ctypes.byref(a["k"]), a["wq"], a["wk"], a["cs"], a["n_pos"], a["rot"], a["style"], a["pos"]]
+    assert lib.qnre_qk_norm_rope(*head, ctypes.byref(a["qo"]), ctypes.byref(a["ko"]), None) == want
+    g = view(A + 8 * MB, [1, 4, 4, 128]), view(A + 9 * MB, [1, 4, 2, 128])
+    assert lib.qnre_qk_norm_rope_backward(ctypes.byref(g[0]), ctypes.byref(g[1]), *head, ctypes.byref(a["qo"]),
+                                          ctypes.byref(a["ko"]), A + 10 * MB, A + 10 * MB + 512, A + 11 * MB, 1 << 24,
+                                          None) == want
+    v = view(A + 12 * MB, [1, 4, 2, 128])
+    c = cache(k=A + 200 * MB, v=A + 264 * MB)
+    assert lib.qnre_qkv_norm_rope_append(head[0], head[1], ctypes.byref(v), *head[2:], ctypes.byref(a["qo"]),
+                                         ctypes.byref(c), 0, A + 13 * MB, None, None) == want
+
+
+def test_norm_aliases(lib):
+    def run(**kw):
+        a = norm_args(**kw)
+        return lib.qnre_qk_norm_rope(ctypes.byref(a["q"]), ctypes.byref(a["k"]), a["wq"], a["wk"], a["cs"], a["n_pos"],
+                                     a["rot"], a["style"], a["pos"], ctypes.byref(a["qo"]), ctypes.byref(a["ko"]), None)
+    assert run(qo=view(A + 256, [1, 4, 4, 128])) == 4                     # over its own input, shifted
+    assert run(qo=view(A + MB, [1, 4, 4, 128])) == 4                      # over the other input
+    assert run(qo=view(A + 4 * MB, [1, 4, 4, 128]), ko=view(A + 4 * MB + 1024, [1, 4, 2, 128])) == 4
+    assert run(qo=view(A + 4 * MB, [1, 4, 4, 128], [512, 128, 128, 1])) == 1  # writes an element twice
+    # head bands of one buffer: overlapping spans, no shared element
+    s = [4 * 768, 768, 128, 1]
+    ok = dict(q=view(A, [0, 4, 4, 128], s), k=view(A + 1024, [0, 4, 2, 128], s), qo=view(A, [0, 4, 4, 128], s),
+              ko=view(A + 1024, [0, 4, 2, 128], s))
+    assert run(**ok) == 0
+    s = [4 * 768, 768, 128, 1]
+    bad = dict(q=view(A, [1, 4, 4, 128], s), k=view(A + 1024 - 256, [1, 4, 2, 128], s), qo=view(A, [1, 4, 4, 128], s),
+               ko=view(A + 5 * MB, [1, 4, 2, 128]))
+    assert run(**bad) == 4
+
+
+def test_norm_backward_and_append_arguments(lib):
+    a = norm_args()
+    head = [ctypes.byref(a["q"]), ctypes.byref(a["k"]), a["wq"], a["wk"], a["cs"], 8, 128, 0, None]
+    g = view(A + 8 * MB, [1, 4, 4, 128]), view(A + 9 * MB, [1, 4, 2, 128])
+
+    def back(gq=g[0], dq=a["qo"], dw=A + 10 * MB, ws=A + 11 * MB, n=1 << 24):
+        return lib.qnre_qk_norm_rope_backward(ctypes.byref(gq), ctypes.byref(g[1]), *head, ctypes.byref(dq),
+                                              ctypes.byref(a["ko"]), dw, A + 10 * MB + 512, ws, n, None)
+    assert back(gq=view(A + 8 * MB, [1, 4, 3, 128])) == 1
+    assert back(dq=view(A, [1, 4, 4, 128])) == 4
+    assert back(dw=None) == 1
+    assert back(dw=A + 10 * MB + 2) == 3
+    assert back(dw=A + 10 * MB + 512) == 4
+    assert back(ws=None) == 1
+    assert back(ws=A + 11 * MB + 4) == 3
+    assert back(n=64) == 5
+    v = view(A + 12 * MB, [1, 4, 2, 128])
+
+    def append(c=None, v=v, layer=0, rows=A + 13 * MB):
+        c = c or cache(k=A + 200 * MB, v=A + 264 * MB)
+        return lib.qnre_qkv_norm_rope_append(head[0], head[1], ctypes.byref(v), *head[2:], ctypes.byref(a["qo"]),
+                                             ctypes.byref(c), layer, rows, None, None)
+    assert append(v=view(A + 12 * MB, [1, 4, 3, 128])) == 1
+    assert append(layer=2) == 1
+    assert append(layer=-1) == 1
+    assert append(rows=None) == 1
+    assert append(rows=A + 13 * MB + 1) == 3
+    assert append(c=cache(heads=3)) == 1
+    assert append(c=cache(dtype=1)) == 1
+    assert append(c=cache(k=A)) == 4
+    n = ctypes.c_uint64()
+    assert lib.qnre_qk_norm_rope_workspace_bytes(96, ctypes.byref(n)) == 2
+    assert lib.qnre_qk_norm_rope_workspace_bytes(128, None) == 1
+
+
+def test_binding_checks_types_and_shapes():
+    torch = pytest.importorskip("torch")
+    k = torch.zeros((1, 2, 1, 8, 64), dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    with pytest.raises(qb.QnreError):
+        qb.PagedCache(k[0], k[0], i(1, 1), i(1), i(2))
+    with pytest.raises(qb.QnreError):
+        qb.PagedCache(k, k.half(), i(1, 1), i(1), i(2))
+    with pytest.raises(qb.QnreError):
+        qb.PagedCache(k, k.clone(), i(1, 1), i(2), i(2))
+    with pytest.raises(qb.QnreError):
+        qb.PagedCache(k, k.clone(), i(1, 1).long(), i(1), i(2))
+    with pytest.raises(qb.QnreError):
+        qb._i32("x", i(3), 4)

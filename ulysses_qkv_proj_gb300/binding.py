@@ -5,7 +5,9 @@ The names follow the C ABI: `qnre_forward`, `qnre_forward_noalloc`,
 `ulysses_scatter_heads`, `ulysses_gather_heads`,
 `ulysses_pack_output_sequence_chunk`, `ulysses_gather_output_head_chunk`,
 `ulysses_scatter_qkv_head_chunk`, plus the `Plan` wrapper around
-`qnre_plan_create` / `qnre_plan_destroy`.  Tensors are torch CUDA tensors;
+`qnre_plan_create` / `qnre_plan_destroy`, and the speculative-decoding calls
+over a `PagedCache` (`qnre_qk_norm_rope` and its gradient,
+`qnre_qkv_norm_rope_append`, `qnre_cache_*`).  Tensors are torch CUDA tensors;
 torch supplies device memory and the current stream, nothing else.  Every
 failure status raises `QnreError`; a missing library raises at first use.
 """
@@ -57,6 +59,12 @@ class _PlanInfo(ctypes.Structure):
 class _Tensor4(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("shape", ctypes.c_int64 * 4),
                 ("stride", ctypes.c_int64 * 4), ("dtype", ctypes.c_int32)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "block_table", "seq_lens", "page_refs", "status", "scratch")] + \
+        [(n, ctypes.c_int32) for n in ("layers", "pages", "heads", "page_size", "head_dim", "rows", "max_blocks",
+                                       "dtype")]
 
 
 _lib = None
@@ -127,6 +135,22 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ulysses_sage2_scatter_qkv.restype = c_int
     lib.ulysses_sage2_scatter_qkv.argtypes = [ctypes.POINTER(_Tensor4)] * 3 + [c_int, c_int] + [c_vp] * 7 + \
         [ctypes.c_uint64, c_vp]
+    t4, cache = ctypes.POINTER(_Tensor4), ctypes.POINTER(_Cache)
+    for name in ("truncate", "fork", "reserve", "copy_pages"):
+        fn = getattr(lib, "qnre_cache_" + name)
+        fn.restype = c_int
+        fn.argtypes = [cache, c_vp, c_vp, c_int, c_vp]
+    lib.qnre_cache_compact.restype = c_int
+    lib.qnre_cache_compact.argtypes = [cache, c_vp, c_vp, c_vp, c_int, c_int, c_vp]
+    table = [c_vp, c_vp, c_vp, c_i64, c_int, c_int, c_vp]  # norm weights, cos_sin, n_pos, rot, style, positions
+    lib.qnre_qk_norm_rope.restype = c_int
+    lib.qnre_qk_norm_rope.argtypes = [t4, t4, *table, t4, t4, c_vp]
+    lib.qnre_qk_norm_rope_workspace_bytes.restype = c_int
+    lib.qnre_qk_norm_rope_workspace_bytes.argtypes = [c_int, ctypes.POINTER(ctypes.c_uint64)]
+    lib.qnre_qk_norm_rope_backward.restype = c_int
+    lib.qnre_qk_norm_rope_backward.argtypes = [t4, t4, t4, t4, *table, t4, t4, c_vp, c_vp, c_vp, ctypes.c_uint64, c_vp]
+    lib.qnre_qkv_norm_rope_append.restype = c_int
+    lib.qnre_qkv_norm_rope_append.argtypes = [t4, t4, t4, *table, t4, cache, c_int, c_vp, c_vp, c_vp]
     _lib = lib
     return lib
 
@@ -438,3 +462,179 @@ def ulysses_sage2_scatter_qkv(q, k, v, P: int, used_sequence: int, out: Dict[str
                                                     ws.numel() * ws.element_size(), _stream_ptr(stream)),
            "ulysses_sage2_scatter_qkv")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Speculative decoding over a paged cache
+# ---------------------------------------------------------------------------
+MAX_NODES = 64
+CACHE_NO_PAGES = 0x1
+CACHE_BAD_ROW = 0x2
+CACHE_BAD_PAGE = 0x4
+CACHE_BAD_REFS = 0x8
+CACHE_WAIT_TIMEOUT = 0x10
+
+
+class PagedCache:
+    """A paged K/V cache over tensors the caller owns (qnre_cache_t).
+
+    k, v         bf16 or fp16 [layers, pages, heads, page_size, head_dim]
+    block_table  int32 [rows, max_blocks], -1 where a row holds no page
+    seq_lens     int32 [rows];  page_refs  int32 [pages], 0 = free
+    """
+
+    def __init__(self, k, v, block_table, seq_lens, page_refs):
+        import torch
+        if k.dim() != 5 or v.shape != k.shape or v.dtype != k.dtype:
+            raise QnreError(1, "PagedCache: k and v must be [layers, pages, heads, page_size, head_dim] alike")
+        layers, pages, heads, page_size, head_dim = k.shape
+        rows = seq_lens.numel()
+        if block_table.dim() != 2 or block_table.shape[0] != rows or page_refs.numel() != pages:
+            raise QnreError(1, "PagedCache: block_table [rows, max_blocks], seq_lens [rows], page_refs [pages]")
+        self.k, self.v = k, v
+        self.block_table, self.seq_lens, self.page_refs = block_table, seq_lens, page_refs
+        self.status_word = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.scratch = torch.empty(4 * pages + 4, dtype=torch.int32, device=k.device)
+        self._struct = _Cache(_contig(k, "PagedCache"), _contig(v, "PagedCache"),
+                              _i32("PagedCache", block_table), _i32("PagedCache", seq_lens),
+                              _i32("PagedCache", page_refs), self.status_word.data_ptr(), self.scratch.data_ptr(),
+                              layers, pages, heads, page_size, head_dim, rows, block_table.shape[1], _dtype_code(k))
+
+    @property
+    def handle(self):
+        return ctypes.byref(self._struct)
+
+    def status(self, clear: bool = True) -> int:
+        """The CACHE_* bits kernels have set (waits for the current stream)."""
+        bits = int(self.status_word.item())
+        if clear and bits:
+            self.status_word.zero_()
+        return bits
+
+
+def alloc_paged_cache(layers: int, pages: int, heads: int, page_size: int, head_dim: int, rows: int, max_blocks: int,
+                      dtype=None, device="cuda") -> PagedCache:
+    """An empty cache (pools uninitialised, every page free)."""
+    import torch
+    shape = (layers, pages, heads, page_size, head_dim)
+    pools = [torch.empty(shape, dtype=dtype or torch.bfloat16, device=device) for _ in range(2)]
+    return PagedCache(*pools, torch.full((rows, max_blocks), -1, dtype=torch.int32, device=device),
+                      torch.zeros(rows, dtype=torch.int32, device=device),
+                      torch.zeros(pages, dtype=torch.int32, device=device))
+
+
+def _i32(where: str, t, *shape):
+    """Pointer of a contiguous int32 tensor (None passes), its shape checked where given."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise QnreError(1, f"{where}: expected int32")
+    if shape and tuple(t.shape) != shape:
+        raise QnreError(1, f"{where}: expected shape {list(shape)}")
+    return _contig(t, where)
+
+
+def _f32(where: str, t, *shape):
+    import torch
+    if t.dtype != torch.float32:
+        raise QnreError(1, f"{where}: expected float32")
+    if shape and tuple(t.shape) != shape:
+        raise QnreError(1, f"{where}: expected shape {list(shape)}")
+    return _contig(t, where)
+
+
+def _weight(where: str, w, like):
+    if w.dtype != like.dtype or w.numel() != like.shape[-1]:
+        raise QnreError(1, f"{where}: norm weights are [{like.shape[-1]}] of the input's dtype")
+    return _contig(w, where)
+
+
+def qnre_cache_truncate(cache: PagedCache, rows, lens, stream=None) -> None:
+    """Row rows[i] keeps its first lens[i] tokens; the blocks past them are released (0 frees the row)."""
+    where, n = "qnre_cache_truncate", rows.numel()
+    _check(load_library().qnre_cache_truncate(cache.handle, _i32(where, rows), _i32(where, lens, n), n,
+                                              _stream_ptr(stream)), where)
+
+
+def qnre_cache_fork(cache: PagedCache, src, dst, stream=None) -> None:
+    """Empty row dst[i] becomes a copy of row src[i] that shares its pages."""
+    where, n = "qnre_cache_fork", src.numel()
+    _check(load_library().qnre_cache_fork(cache.handle, _i32(where, src), _i32(where, dst, n), n,
+                                          _stream_ptr(stream)), where)
+
+
+def qnre_cache_reserve(cache: PagedCache, rows, counts, stream=None) -> None:
+    """Pages of its own for the next counts[i] tokens of row rows[i] (lowest free pages, copy on write)."""
+    where, n = "qnre_cache_reserve", rows.numel()
+    _check(load_library().qnre_cache_reserve(cache.handle, _i32(where, rows), _i32(where, counts, n), n,
+                                             _stream_ptr(stream)), where)
+
+
+def qnre_cache_compact(cache: PagedCache, rows, path, counts, stream=None) -> None:
+    """Keep the accepted nodes path[i][:counts[i]] of row rows[i]'s drafts; its length grows by counts[i]."""
+    where, n = "qnre_cache_compact", rows.numel()
+    if path.dim() != 2:
+        raise QnreError(1, f"{where}: path must be [n, nodes]")
+    _check(load_library().qnre_cache_compact(cache.handle, _i32(where, rows), _i32(where, path, n, path.shape[1]),
+                                             _i32(where, counts, n), n, path.shape[1], _stream_ptr(stream)), where)
+
+
+def qnre_cache_copy_pages(cache: PagedCache, src, dst, stream=None) -> None:
+    """Page src[i] to page dst[i] in every layer."""
+    where, n = "qnre_cache_copy_pages", src.numel()
+    _check(load_library().qnre_cache_copy_pages(cache.handle, _i32(where, src), _i32(where, dst, n), n,
+                                                _stream_ptr(stream)), where)
+
+
+def _norm_inputs(where: str, q, k, q_norm_w, k_norm_w, cos_sin, positions):
+    tq, tk = _tensor4(q), _tensor4(k)
+    if cos_sin.dim() != 2:
+        raise QnreError(1, f"{where}: cos_sin must be [n_pos, rot]")
+    head = (ctypes.byref(tq), ctypes.byref(tk), _weight(where, q_norm_w, q), _weight(where, k_norm_w, k),
+            _f32(where, cos_sin), cos_sin.shape[0], cos_sin.shape[1])
+    return (tq, tk), head, _i32(where, positions, q.shape[0], q.shape[1])
+
+
+def qnre_qk_norm_rope(q, k, q_norm_w, k_norm_w, cos_sin, positions, q_out, k_out, rope_style: str = "rotate_half",
+                      stream=None) -> None:
+    """Per-head RMSNorm and rotation of q [B, S, Hq, D] and k [B, S, Hk, D] (views; in place allowed)."""
+    where = "qnre_qk_norm_rope"
+    keep, head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
+    oq, ok = _tensor4(q_out), _tensor4(k_out)
+    _check(load_library().qnre_qk_norm_rope(*head, ROPE_STYLES.get(rope_style, -1), pos, ctypes.byref(oq),
+                                            ctypes.byref(ok), _stream_ptr(stream)), where)
+
+
+def qk_norm_rope_workspace(q, k=None):
+    """The scratch tensor qnre_qk_norm_rope_backward needs for heads like q's."""
+    import torch
+    n = ctypes.c_uint64()
+    _check(load_library().qnre_qk_norm_rope_workspace_bytes(q.shape[-1], ctypes.byref(n)),
+           "qnre_qk_norm_rope_workspace_bytes")
+    return torch.empty(n.value, dtype=torch.uint8, device=q.device)
+
+
+def qnre_qk_norm_rope_backward(gq, gk, q, k, q_norm_w, k_norm_w, cos_sin, positions, dq, dk, dq_norm_w, dk_norm_w,
+                               workspace, rope_style: str = "rotate_half", stream=None) -> None:
+    """Gradient of qnre_qk_norm_rope: dq, dk (input dtype) and the fp32 weight gradients."""
+    where = "qnre_qk_norm_rope_backward"
+    keep, head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
+    tgq, tgk, tdq, tdk = _tensor4(gq), _tensor4(gk), _tensor4(dq), _tensor4(dk)
+    D = q.shape[-1]
+    _check(load_library().qnre_qk_norm_rope_backward(
+        ctypes.byref(tgq), ctypes.byref(tgk), *head, ROPE_STYLES.get(rope_style, -1), pos, ctypes.byref(tdq),
+        ctypes.byref(tdk), _f32(where, dq_norm_w, D), _f32(where, dk_norm_w, D), _contig(workspace, where),
+        workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
+
+
+def qnre_qkv_norm_rope_append(q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q_out, cache: PagedCache, layer: int,
+                              rows, counts=None, rope_style: str = "rotate_half", stream=None) -> None:
+    """qnre_qk_norm_rope of the rows' new tokens [n, S, ...]; k and v go into the cache behind seq_lens."""
+    where = "qnre_qkv_norm_rope_append"
+    keep, head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
+    tv, oq = _tensor4(v), _tensor4(q_out)
+    n = q.shape[0]
+    _check(load_library().qnre_qkv_norm_rope_append(
+        head[0], head[1], ctypes.byref(tv), *head[2:], ROPE_STYLES.get(rope_style, -1), pos, ctypes.byref(oq),
+        cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)

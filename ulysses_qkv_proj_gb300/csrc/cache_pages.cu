@@ -1,0 +1,434 @@
+// cache_pages.cu -- bookkeeping and copies of a paged cache: truncate / free,
+// fork, reserve (allocation with copy on write), compact, copy pages.
+//
+// The only allocator state is page_refs: a page is free when no row holds it,
+// and a reserve takes the lowest-numbered free pages.  Releases are integer
+// decrements, which commute, so every table and every count is the same on
+// every run, whatever order the blocks of a launch run in.
+//
+// Bound: the bookkeeping is launch and load latency (a few microseconds); the
+// page copies of a fork's reserve are HBM bandwidth.
+#include "../../include/qnre.h"
+#include "cache.cuh"
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <initializer_list>
+
+namespace {
+
+using namespace qnre;
+using namespace qnre::api;
+
+constexpr int kReserveThreads = 1024;
+constexpr int kCopyThreads = 256;
+
+// Every launch here is a programmatic dependent launch: its blocks may start while the
+// previous kernel drains, and see that kernel's writes after this.
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Releases the blocks of `row` from `first` on (one warp).
+__device__ __forceinline__ void release_from(const CacheView& c, int row, int first, int lane) {
+  int32_t* table = c.table + static_cast<long long>(row) * c.max_blocks;
+  for (int j = first + lane; j < c.max_blocks; j += 32) {
+    const int page = table[j];
+    if (page < 0) continue;
+    table[j] = -1;
+    if (page >= c.pages) {
+      atomicOr(c.status, QNRE_CACHE_BAD_PAGE);
+    } else if (atomicSub(c.refs + page, 1) < 1) {
+      atomicAdd(c.refs + page, 1);
+      atomicOr(c.status, QNRE_CACHE_BAD_REFS);
+    }
+  }
+}
+
+// One warp a row.  kGrow: the row's length grows by values[i] (after a compact's moves);
+// else it becomes min(length, values[i]).
+// Values above `limit` count as `limit`.
+template <bool kGrow>
+__global__ void __launch_bounds__(128) trim_kernel(CacheView c, const int32_t* rows, const int32_t* values, int n,
+                                                   int limit) {
+  pdl_wait();
+  const int i = blockIdx.x * 4 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (i >= n) return;
+  const int row = rows[i];
+  if (!c.row_ok(row)) return;
+  const int old = c.lens[row];
+  const int want = min(max(values[i], 0), limit);
+  const int len = kGrow ? static_cast<int>(min(static_cast<long long>(old) + want, 0x7FFFFFFFll)) : min(old, want);
+  __syncwarp();
+  if (lane == 0) c.lens[row] = len;
+  const long long first = (static_cast<long long>(len) + c.page_size - 1) / c.page_size;
+  if (first < c.max_blocks) release_from(c, row, static_cast<int>(first), lane);
+}
+
+// One warp a fork: the destination's table is the source's, each page held once more.
+__global__ void __launch_bounds__(128) fork_kernel(CacheView c, const int32_t* src, const int32_t* dst, int n) {
+  pdl_wait();
+  const int i = blockIdx.x * 4 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (i >= n) return;
+  const int s = src[i], d = dst[i];
+  if (!c.row_ok(s) || !c.row_ok(d)) return;
+  const int32_t* from = c.table + static_cast<long long>(s) * c.max_blocks;
+  int32_t* to = c.table + static_cast<long long>(d) * c.max_blocks;
+  const int len = c.lens[s];
+  const bool used = s == d || c.lens[d] != 0 || to[0] >= 0;
+  __syncwarp();
+  if (used) {
+    if (lane == 0) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
+    return;
+  }
+  const int blocks = min((len + c.page_size - 1) / c.page_size, c.max_blocks);
+  for (int j = lane; j < blocks; j += 32) {
+    const int page = from[j];
+    to[j] = page;
+    if (page >= 0 && page < c.pages) atomicAdd(c.refs + page, 1);
+  }
+  if (lane == 0) c.lens[d] = len;
+}
+
+// Inclusive scan over the block's threads; `total` is the last value.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int s = warp_sums[lane];  // kReserveThreads / 32 == 32 warps
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+    if (lane >= o) s += u;
+  }
+  total = __shfl_sync(0xFFFFFFFFu, s, 31);
+  const int before = __shfl_sync(0xFFFFFFFFu, s, max(warp - 1, 0));
+  return v + (warp > 0 ? before : 0);
+}
+
+// The words of `scratch`: [0] pages to copy, then free[pages], old[pages], copy
+// sources[pages], copy destinations[pages].
+struct Scratch {
+  int32_t *count, *free, *old, *src, *dst;
+  __device__ explicit Scratch(const CacheView& c)
+      : count(c.scratch), free(c.scratch + 4), old(free + c.pages), src(old + c.pages), dst(src + c.pages) {}
+};
+
+// Blocks of a row that tokens [len, len + count) touch.
+struct Window {
+  int row, len, first, last;
+  bool fits;
+};
+
+__device__ __forceinline__ Window window_of(const CacheView& c, const int32_t* rows, const int32_t* counts, int i) {
+  Window w{rows[i], 0, 0, 0, true};
+  if (w.row < 0 || w.row >= c.rows) return w;
+  w.len = max(c.lens[w.row], 0);
+  const int count = counts[i];
+  if (count <= 0) return w;
+  w.first = w.len / c.page_size;
+  const long long last = (static_cast<long long>(w.len) + count + c.page_size - 1) / c.page_size;
+  w.fits = last <= c.max_blocks;
+  w.last = static_cast<int>(min(last, static_cast<long long>(c.max_blocks)));
+  return w;
+}
+
+// true when block j needs a new page; `shared` when it replaces a page other rows hold.
+__device__ __forceinline__ bool needs_page(const CacheView& c, int page, bool& shared) {
+  shared = page >= 0 && page < c.pages && c.refs[page] > 1;
+  return page < 0 || shared;
+}
+
+// One block does a reserve's whole bookkeeping: count each row's new pages, scan, find
+// as many free pages from the lowest up, and hand them out.  The decisions read
+// the counts of the call's start; releases of replaced pages come last.
+__global__ void __launch_bounds__(kReserveThreads) reserve_kernel(CacheView c, const int32_t* rows,
+                                                                  const int32_t* counts, int n) {
+  __shared__ int need[QNRE_MAX_CALL_ROWS];
+  __shared__ int sums[32];
+  __shared__ int copies, refused;
+  pdl_wait();
+  const Scratch s(c);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  if (tid == 0) copies = refused = 0;
+  __syncthreads();
+  for (int i = warp; i < n; i += 32) {
+    const Window w = window_of(c, rows, counts, i);
+    if (lane == 0 && (w.row < 0 || w.row >= c.rows)) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
+    if (lane == 0 && !w.fits) refused = 1;
+    int mine = 0;
+    for (int j = w.first + lane; j < w.last; j += 32) {
+      bool shared;
+      mine += needs_page(c, c.table[static_cast<long long>(w.row) * c.max_blocks + j], shared) ? 1 : 0;
+    }
+    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+    if (lane == 0) need[i] = mine;
+  }
+  __syncthreads();
+  int total;
+  {
+    const int mine = tid < n ? need[tid] : 0;
+    const int incl = block_scan(mine, sums, total);
+    __syncthreads();
+    if (tid < n) need[tid] = incl - mine;  // first of the row's pages in the list
+  }
+  // free pages, lowest first: 16 counts a thread and step, so that a cache of 16384 pages is one step
+  int found = 0;
+  if (total <= c.pages) {
+    for (long long base = 0; base < c.pages && found < total; base += kReserveThreads * 16) {
+      const long long at = base + tid * 16;
+      unsigned zero = 0;
+      if (at + 16 <= c.pages) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int4 r = reinterpret_cast<const int4*>(c.refs + at)[q];
+          zero |= (r.x == 0 ? 1u : 0u) << (4 * q) | (r.y == 0 ? 2u : 0u) << (4 * q) |
+                  (r.z == 0 ? 4u : 0u) << (4 * q) | (r.w == 0 ? 8u : 0u) << (4 * q);
+        }
+      } else {
+        for (int e = 0; e < 16 && at + e < c.pages; ++e) zero |= (c.refs[at + e] == 0 ? 1u : 0u) << e;
+      }
+      int step;
+      int pos = found + block_scan(__popc(zero), sums, step) - __popc(zero);
+      while (zero != 0 && pos < total) {
+        s.free[pos++] = static_cast<int>(at) + __ffs(zero) - 1;
+        zero &= zero - 1;
+      }
+      found += step;
+    }
+  }
+  __syncthreads();
+  if (found < total || refused) {
+    if (tid == 0) {
+      atomicOr(c.status, QNRE_CACHE_NO_PAGES);
+      s.count[0] = 0;
+    }
+    return;
+  }
+  for (int i = warp; i < n; i += 32) {
+    const Window w = window_of(c, rows, counts, i);
+    int at = need[i];
+    for (int j0 = w.first; j0 < w.last; j0 += 32) {
+      const int j = j0 + lane;
+      int page = -1;
+      bool shared = false, take = false;
+      int32_t* entry = c.table + static_cast<long long>(w.row) * c.max_blocks + j;
+      if (j < w.last) {
+        page = *entry;
+        take = needs_page(c, page, shared);
+      }
+      const unsigned takers = __ballot_sync(0xFFFFFFFFu, take);
+      if (take) {
+        const int p = at + __popc(takers & ((1u << lane) - 1u));
+        const int fresh = s.free[p];
+        s.old[p] = shared ? page : -1;
+        *entry = fresh;
+        if (shared && static_cast<long long>(j) * c.page_size < w.len) {
+          const int slot = atomicAdd(&copies, 1);  // copies run in any order; at most `total` of them
+          s.src[slot] = page;
+          s.dst[slot] = fresh;
+        }
+      }
+      at += __popc(takers);
+    }
+  }
+  __syncthreads();
+  for (int p = tid; p < total; p += kReserveThreads) {
+    c.refs[s.free[p]] = 1;
+    const int old = s.old[p];
+    if (old >= 0) atomicSub(c.refs + old, 1);
+  }
+  if (tid == 0) s.count[0] = copies;
+}
+
+// Copies whole pages of every layer, K and V: item = (pair, layer, K or V, piece).
+// 256 threads move 32 KiB an item, eight 16-byte loads in flight a thread.
+constexpr int kPieceVecs = kCopyThreads * 8;
+
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(CacheView c, const int32_t* src, const int32_t* dst,
+                                                                  const int32_t* count, int n) {
+  pdl_wait();
+  const int pairs = count != nullptr ? *count : n;
+  const long long page_vecs = static_cast<long long>(c.heads) * c.page_size * c.head_dim / 8;
+  const int pieces = static_cast<int>((page_vecs + kPieceVecs - 1) / kPieceVecs);
+  const long long items = static_cast<long long>(pairs) * c.layers * 2 * pieces;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int piece = static_cast<int>(it % pieces);
+    long long rest = it / pieces;
+    const int kv = static_cast<int>(rest & 1);
+    rest >>= 1;
+    const int layer = static_cast<int>(rest % c.layers);
+    const int p = static_cast<int>(rest / c.layers);
+    const int a = src[p], b = dst[p];
+    if (a < 0 || a >= c.pages || b < 0 || b >= c.pages) {
+      if (threadIdx.x == 0) atomicOr(c.status, QNRE_CACHE_BAD_PAGE);
+      continue;
+    }
+    uint4* pool = reinterpret_cast<uint4*>(kv ? c.v : c.k);
+    const uint4* from = pool + (static_cast<long long>(layer) * c.pages + a) * page_vecs;
+    uint4* to = pool + (static_cast<long long>(layer) * c.pages + b) * page_vecs;
+    const long long at = static_cast<long long>(piece) * kPieceVecs + threadIdx.x;
+    uint4 r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (at + e * kCopyThreads < page_vecs) r[e] = from[at + e * kCopyThreads];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (at + e * kCopyThreads < page_vecs) to[at + e * kCopyThreads] = r[e];
+  }
+}
+
+// The moves of a compact.  One thread owns 16 bytes of a head's channels for one
+// (row, layer, K or V, head) and takes the accepted tokens in ascending order, eight at
+// a time: a later token's source can lie in an earlier one's destination never
+// (path ascends strictly, so path[j'] >= j' > j), so reads stay ahead of writes
+// without any ordering between threads.
+__global__ void __launch_bounds__(kCopyThreads) compact_kernel(CacheView c, const int32_t* rows, const int32_t* path,
+                                                               const int32_t* counts, int nodes, int lanes) {
+  __shared__ long long from[QNRE_MAX_NODES], to[QNRE_MAX_NODES];  // head 0's byte offsets in layer 0, -1: skip
+  pdl_wait();
+  const int i = blockIdx.x;
+  const int row = rows[i];
+  const int count = min(counts[i], nodes);
+  if (row < 0 || row >= c.rows) {
+    if (threadIdx.x == 0) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
+    return;
+  }
+  const int len = c.lens[row];
+  for (int j = threadIdx.x; j < count; j += kCopyThreads) {
+    const int node = path[static_cast<long long>(i) * nodes + j];
+    from[j] = to[j] = -1;
+    if (node == j) continue;
+    const int ps = node >= 0 && len <= 0x7FFFFFFF - node ? c.page_of(row, len + node) : -1;
+    const int pd = len <= 0x7FFFFFFF - j ? c.page_of(row, len + j) : -1;
+    if (ps < 0 || pd < 0) {
+      atomicOr(c.status, QNRE_CACHE_BAD_PAGE);
+      continue;
+    }
+    from[j] = c.token_offset(0, ps, 0, len + node);
+    to[j] = c.token_offset(0, pd, 0, len + j);
+  }
+  __syncthreads();
+  const int row_vecs = c.head_dim / 8;
+  const long long head_bytes = static_cast<long long>(c.page_size) * c.head_dim * 2;
+  const long long layer_bytes = static_cast<long long>(c.pages) * c.heads * head_bytes;
+  for (long long t = static_cast<long long>(blockIdx.y) * kCopyThreads + threadIdx.x; t < lanes;
+       t += static_cast<long long>(gridDim.y) * kCopyThreads) {
+    const int vec = static_cast<int>(t % row_vecs);
+    long long rest = t / row_vecs;
+    const int head = static_cast<int>(rest % c.heads);
+    rest /= c.heads;
+    char* pool = (rest & 1) ? c.v : c.k;
+    pool += (rest >> 1) * layer_bytes + head * head_bytes + vec * 16;
+    for (int j0 = 0; j0 < count; j0 += 8) {
+      uint4 r[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j0 + e < count && from[j0 + e] >= 0) r[e] = *reinterpret_cast<const uint4*>(pool + from[j0 + e]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j0 + e < count && from[j0 + e] >= 0) *reinterpret_cast<uint4*>(pool + to[j0 + e]) = r[e];
+    }
+  }
+}
+
+template <typename K, typename... A>
+qnre_status_t launch(K kernel, dim3 grid, dim3 block, qnre_stream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return from_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
+dim3 copy_grid(const qnre_cache_t* c, int n) {
+  const int64_t vecs = static_cast<int64_t>(c->heads) * c->page_size * c->head_dim / 8;
+  const int64_t items = static_cast<int64_t>(n) * c->layers * 2 * ((vecs + kPieceVecs - 1) / kPieceVecs);
+  return dim3(static_cast<unsigned>(std::min<int64_t>(items, 152 * 8)));
+}
+
+qnre_status_t check_call(const qnre_cache_t* cache, std::initializer_list<const void*> lists, int n) {
+  const qnre_status_t st = check_cache(cache, n);
+  if (st != QNRE_OK) return st;
+  for (const void* p : lists) {
+    if (p == nullptr && n > 0) return QNRE_ERR_INVALID_ARG;
+    if (!aligned(p, 4)) return QNRE_ERR_ALIGNMENT;
+  }
+  return QNRE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qnre_status_t qnre_cache_truncate(const qnre_cache_t* cache, const int32_t* rows, const int32_t* lens, int n,
+                                  qnre_stream_t stream) {
+  const qnre_status_t st = check_call(cache, {rows, lens}, n);
+  if (st != QNRE_OK || n == 0) return st;
+  return launch(trim_kernel<false>, dim3((n + 3) / 4), dim3(128), stream, view_of(cache), rows, lens, n,
+                0x7FFFFFFF);
+}
+
+qnre_status_t qnre_cache_fork(const qnre_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
+                              qnre_stream_t stream) {
+  const qnre_status_t st = check_call(cache, {src, dst}, n);
+  if (st != QNRE_OK || n == 0) return st;
+  return launch(fork_kernel, dim3((n + 3) / 4), dim3(128), stream, view_of(cache), src, dst, n);
+}
+
+qnre_status_t qnre_cache_reserve(const qnre_cache_t* cache, const int32_t* rows, const int32_t* counts, int n,
+                                 qnre_stream_t stream) {
+  qnre_status_t st = check_call(cache, {rows, counts}, n);
+  if (st != QNRE_OK || n == 0) return st;
+  const CacheView c = view_of(cache);
+  st = launch(reserve_kernel, dim3(1), dim3(kReserveThreads), stream, c, rows, counts, n);
+  if (st != QNRE_OK) return st;
+  const int32_t* src = c.scratch + 4 + 2 * static_cast<int64_t>(c.pages);
+  const int32_t* count = c.scratch;
+  return launch(copy_pages_kernel, copy_grid(cache, n), dim3(kCopyThreads), stream, c, src, src + c.pages,
+                count, n);
+}
+
+qnre_status_t qnre_cache_compact(const qnre_cache_t* cache, const int32_t* rows, const int32_t* path,
+                                 const int32_t* counts, int n, int nodes, qnre_stream_t stream) {
+  qnre_status_t st = check_call(cache, {rows, path, counts}, n);
+  if (st != QNRE_OK) return st;
+  if (nodes < 1) return QNRE_ERR_INVALID_ARG;
+  if (nodes > QNRE_MAX_NODES) return QNRE_ERR_CAPACITY;
+  if (n == 0) return QNRE_OK;
+  const int64_t lanes = static_cast<int64_t>(cache->layers) * 2 * cache->heads * (cache->head_dim / 8);
+  if (lanes > (int64_t{1} << 31) - 1) return QNRE_ERR_CAPACITY;
+  const unsigned ys = static_cast<unsigned>(std::min<int64_t>((lanes + kCopyThreads - 1) / kCopyThreads, 1024));
+  const CacheView c = view_of(cache);
+  st = launch(compact_kernel, dim3(n, ys), dim3(kCopyThreads), stream, c, rows, path, counts, nodes,
+              static_cast<int>(lanes));
+  if (st != QNRE_OK) return st;
+  return launch(trim_kernel<true>, dim3((n + 3) / 4), dim3(128), stream, c, rows, counts, n, nodes);
+}
+
+qnre_status_t qnre_cache_copy_pages(const qnre_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
+                                    qnre_stream_t stream) {
+  // any number of pages: the lists are read by every block, so the row limit does not apply
+  const qnre_status_t st = check_call(cache, {src, dst}, std::min(n, 1));
+  if (st != QNRE_OK || n == 0) return st;
+  return launch(copy_pages_kernel, copy_grid(cache, n), dim3(kCopyThreads), stream, view_of(cache), src, dst,
+                static_cast<const int32_t*>(nullptr), n);
+}
+
+}  // extern "C"
