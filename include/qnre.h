@@ -663,6 +663,69 @@ qnre_status_t qnre_qkv_norm_rope_append(const qnre_tensor4_t* q, const qnre_tens
                                         const qnre_tensor4_t* q_out, const qnre_cache_t* cache, int layer,
                                         const int32_t* rows, const int32_t* counts, qnre_stream_t stream);
 
+/*
+ * qnre_tree_attention -- attention of every drafted node over its row's cached tokens
+ * and the nodes its mask names (appended as tokens seq_lens + j, lengths not yet grown):
+ *
+ *   out[i, t, h] = sum_x softmax_x(scale q[i, t, h] . k_x) v_x
+ *   x over tokens [0, seq_lens[rows[i]]) and seq_lens + j with bit j of mask[i][t], j < counts[i]
+ *
+ *   q        view [n, nodes, Hq, D], the cache's dtype, aligned as above; Hq a multiple of the
+ *            cache's heads (query head h reads head h / (Hq / heads)); nodes <= QNRE_MAX_NODES.
+ *   rows     device int32 [n].
+ *   mask     device uint64 [n, nodes]; NULL: node t sees nodes 0..t.
+ *   counts   device int32 [n]: the nodes of each request (NULL: all); later nodes see nothing.
+ *   scale    > 0, finite.
+ *   out      device, contiguous [n, nodes, Hq, D] of the dtype, 16-byte aligned; a node that sees nothing gets 0.
+ *   lse      device fp32 [n, nodes, Hq] or NULL: log of the softmax sum (-inf where nothing is seen).
+ *   workspace  qnre_tree_attention_workspace_bytes(D), 16-byte aligned.
+ * What lies in slots that a node does not see never reaches its result, not even NaN.
+ * The result does not depend on timing: sums are taken in an order that the lengths fix.
+ */
+qnre_status_t qnre_tree_attention_workspace_bytes(int head_dim, uint64_t* bytes);
+qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* cache, int layer, const int32_t* rows,
+                                  const uint64_t* mask, const int32_t* counts, float scale, void* out, float* lse,
+                                  void* workspace, uint64_t workspace_bytes, qnre_stream_t stream);
+
+/*
+ * qnre_verify_tree -- walks each request's drafted tree against the target model's
+ * probabilities with given random numbers, so that the emitted tokens are distributed
+ * as the target alone would emit them.  From the root, at node c with target row p and
+ * draft row q, the children i = 1, 2, .. of c are tried in order against
+ * p_i = max(p - a q, 0) / R, at first a = 0, R = 1:
+ *
+ *   accepted when accept_u[i] q(x) < p_i(x), x = tokens[i]: the walk moves to node i;
+ *   else a <- a + R, R <- sum max(p - a q, 0).
+ *
+ * Without draft rows (draft_probs NULL: drafts chosen outright) q(x) counts as 1, and a rejection
+ * takes token x out of p instead (R <- R - p(x)).  Where no child is left, next_token
+ * is the lowest x with sum_{y<=x} r(y) > sample_u sum r, r = max(p - a q, 0) (or p without
+ * the rejected tokens; p itself where r sums to nothing; -1 where p does too).
+ *
+ *   target_probs, draft_probs  device fp32, row (i, c) at base + i*stride0 + c*stride1
+ *               elements, vocab values each; draft row c is what c's children were drawn from.
+ *   tokens, parents  device int32 [n, nodes]; parents[i][0] is not read; a node whose parent
+ *               is not an earlier node, or whose token is outside the vocabulary, is left out.
+ *   node_counts device int32 [n] or NULL (all).
+ *   accept_u    device fp32 [n, nodes];  sample_u device fp32 [n]; both in [0, 1).
+ *   path        device int32 [n, nodes]: the accepted nodes from node 0 on, then -1.
+ *   counts      device int32 [n]: how many (>= 1);  next_token device int32 [n].
+ * nodes <= QNRE_MAX_NODES, vocab < 2^31 - 65536.  Probabilities are finite, >= 0, at most 64 a row in sum.
+ * Sums carry 48 bits or more, so the integers agree with a 64-bit evaluation except where a
+ * number lies within about 1e-13 of a border.
+ *
+ * qnre_tree_masks -- masks uint64 [n, nodes] (bit j: node j is node i or one of its
+ *   ancestors) and depths int32 [n, nodes] from parents int32 [n, nodes] (a parent that is not an
+ *   earlier node makes a root).  Either output may be NULL.
+ */
+qnre_status_t qnre_verify_tree(const float* target_probs, int64_t target_stride0, int64_t target_stride1,
+                               const float* draft_probs, int64_t draft_stride0, int64_t draft_stride1, int n, int nodes,
+                               int64_t vocab, const int32_t* tokens, const int32_t* parents, const int32_t* node_counts,
+                               const float* accept_u, const float* sample_u, int32_t* path, int32_t* counts,
+                               int32_t* next_token, qnre_stream_t stream);
+qnre_status_t qnre_tree_masks(const int32_t* parents, int n, int nodes, uint64_t* masks, int32_t* depths,
+                              qnre_stream_t stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

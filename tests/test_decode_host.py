@@ -179,3 +179,61 @@ def test_binding_checks_types_and_shapes():
         qb.PagedCache(k, k.clone(), i(1, 1).long(), i(1), i(2))
     with pytest.raises(qb.QnreError):
         qb._i32("x", i(3), 4)
+
+
+def attention(lib, **kw):
+    f = dict(q=view(A + 200 * MB, [2, 4, 8, 128]), c=cache(), layer=0, rows=A + 210 * MB, mask=None, counts=None,
+             scale=0.1, out=A + 220 * MB, lse=A + 230 * MB, ws=A + 240 * MB, size=1 << 30)
+    f.update(kw)
+    return lib.qnre_tree_attention(ctypes.byref(f["q"]) if f["q"] else None, ctypes.byref(f["c"]), f["layer"], f["rows"],
+                                   f["mask"], f["counts"], f["scale"], f["out"], f["lse"], f["ws"], f["size"], None)
+
+
+@pytest.mark.parametrize("kw,want", CACHE_BAD)
+def test_attention_checks_the_cache(lib, kw, want):
+    assert attention(lib, c=cache(**kw)) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=None), 1), (dict(q=view(A + 200 * MB, [2, 4, 7, 128])), 1), (dict(q=view(A + 200 * MB, [2, 4, 8, 64])), 1),
+    (dict(q=view(A + 200 * MB, [2, 4, 8, 128], dtype=1)), 1), (dict(q=view(A + 200 * MB, [2, 65, 8, 128])), 5),
+    (dict(q=view(A + 200 * MB, [1025, 1, 8, 128])), 5), (dict(q=view(A + 200 * MB + 8, [2, 4, 8, 128])), 3),
+    (dict(layer=2), 1), (dict(layer=-1), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(rows=None), 1), (dict(rows=A + 2), 3), (dict(mask=A + 210 * MB + 4), 3),
+    (dict(counts=A + 210 * MB + 2), 3), (dict(out=None), 1), (dict(out=A + 220 * MB + 8), 3), (dict(ws=None), 1),
+    (dict(size=1000), 5), (dict(out=A + 200 * MB), 4), (dict(out=A), 4), (dict(lse=A + 64 * MB), 4),
+    (dict(lse=A + 220 * MB + 16), 4), (dict(ws=A + 219 * MB), 4), (dict(q=view(A + 200 * MB, [0, 4, 8, 128]), rows=None), 0),
+])
+def test_attention_arguments(lib, kw, want):
+    assert attention(lib, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n=-1), 1), (dict(nodes=0), 1), (dict(vocab=0), 1), (dict(nodes=65), 5), (dict(vocab=1 << 31), 5),
+    (dict(p=None), 1), (dict(tokens=None), 1), (dict(u=None), 1), (dict(path=None), 1), (dict(nxt=None), 1),
+    (dict(ps0=-1), 1), (dict(qs1=1 << 41), 5), (dict(p=A + 2), 3), (dict(path=A + 40 * MB + 1), 3),
+    (dict(path=A + 64), 4), (dict(kept=A + 30 * MB), 4), (dict(nxt=A + 50 * MB), 4), (dict(n=0, p=None), 0),
+])
+def test_verify_arguments(lib, kw, want):
+    f = dict(p=A, ps0=4000, ps1=1000, q=A + 10 * MB, qs0=4000, qs1=1000, n=3, nodes=4, vocab=1000, tokens=A + 20 * MB,
+             parents=A + 30 * MB, node_counts=None, u=A + 35 * MB, s=A + 36 * MB, path=A + 40 * MB, kept=A + 50 * MB,
+             nxt=A + 60 * MB)
+    f.update(kw)
+    assert lib.qnre_verify_tree(*[f[k] for k in ("p", "ps0", "ps1", "q", "qs0", "qs1", "n", "nodes", "vocab", "tokens",
+                                                 "parents", "node_counts", "u", "s", "path", "kept", "nxt")], None) == want
+
+
+def test_tree_mask_arguments(lib):
+    f = lib.qnre_tree_masks
+    assert f(None, 1, 4, A, A + MB, None) == 1
+    assert f(A, -1, 4, None, None, None) == 1
+    assert f(A, 1, 0, None, None, None) == 1
+    assert f(A, 1, 65, None, None, None) == 5
+    assert f(A + 2, 1, 4, None, None, None) == 3
+    assert f(A, 1, 4, A + MB + 4, None, None) == 3
+    assert f(A, 1, 4, A + 8, None, None) == 4
+    assert f(A, 1, 4, A + MB, A + MB, None) == 4
+    assert f(None, 0, 4, None, None, None) == 0
+    n = ctypes.c_uint64()
+    assert lib.qnre_tree_attention_workspace_bytes(96, ctypes.byref(n)) == 2
+    assert lib.qnre_tree_attention_workspace_bytes(64, None) == 1

@@ -1,0 +1,236 @@
+"""qnre_tree_attention against the 64-bit plain form.
+
+Tolerance, element by element: half a step of the output type on the value; each
+weight p is rounded to the inputs' type before the product (half a step of sum p |v|);
+the scores' fp32 products of D terms, scaled to base 2, and the exponential move each p by
+at most (D + 16) 2^-24 |scale q.k| + 2^-20 relative, times sum p |v|, and lse by that."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import _decode as D
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def _qb():
+    from ulysses_qkv_proj_gb300 import binding as qb
+    return qb
+
+
+class Case:
+    """A cache with random pages in random order, every unused slot NaN, and q for drafted trees."""
+
+    def __init__(self, lens, nodes, Hq, Hk, dim, page, dtype, branch=3, layers=2, layer=1, seed=0, counts=None):
+        qb, dt = _qb(), DT[dtype]
+        self.rng = random.Random(seed)
+        gen = torch.Generator().manual_seed(seed)
+        n = len(lens)
+        self.lens, self.nodes, self.layer, self.page, self.dt = lens, nodes, layer, page, dt
+        self.counts = counts or [nodes] * n
+        need = [-(-(L + c) // page) for L, c in zip(lens, self.counts)]
+        blocks, rows_total = max(need) + 1, n + 2
+        pages = sum(need) + 3
+        order = torch.randperm(pages, generator=gen).tolist()
+        self.table = torch.full((rows_total, blocks), -1, dtype=torch.int32)
+        self.rows = self.rng.sample(range(rows_total), n)
+        seq = torch.zeros(rows_total, dtype=torch.int32)
+        nan = float("nan")
+        self.k, self.v = (torch.full((layers, pages, Hk, page, dim), nan, dtype=dt) for _ in range(2))
+        self.keys, self.values = [], []
+        at = 0
+        for i, r in enumerate(self.rows):
+            ids = order[at:at + need[i]]
+            at += need[i]
+            self.table[r, :need[i]] = torch.tensor(ids, dtype=torch.int32)
+            seq[r] = lens[i]
+            T = lens[i] + self.counts[i]
+            kk, vv = (torch.randn((T, Hk, dim), generator=gen).to(dt) for _ in range(2))
+            self.keys.append(kk)
+            self.values.append(vv)
+            for x in range(T):
+                self.k[layer, ids[x // page], :, x % page] = kk[x]
+                self.v[layer, ids[x // page], :, x % page] = vv[x]
+        self.seq = seq
+        self.q = torch.randn((n, nodes, Hq, dim), generator=gen).to(dt)
+        self.parents = [D.random_tree(self.rng, nodes, branch) for _ in lens]
+        self.masks = [D.ancestors(p)[0] for p in self.parents]
+        self.scale = dim ** -0.5
+
+    def visible(self, i):
+        L, c = self.lens[i], self.counts[i]
+        vis = torch.zeros((self.nodes, L + c), dtype=torch.bool)
+        for t in range(min(c, self.nodes)):
+            vis[t, :L] = True
+            for j in range(c):
+                vis[t, L + j] = bool(self.masks[i][t] >> j & 1)
+        return vis
+
+    def run(self, mask="tree", use_counts=False, q=None):
+        qb = _qb()
+        pages = self.k.shape[1]
+        self.cache = qb.PagedCache(self.k.cuda(), self.v.cuda(), self.table.cuda(), self.seq.cuda(),
+                                   torch.ones(pages, dtype=torch.int32, device="cuda"))
+        q = self.q.cuda() if q is None else q
+        out = torch.full(q.shape, 5.0, dtype=self.dt, device="cuda")
+        lse = torch.full(q.shape[:3], 5.0, device="cuda")
+        ws = qb.tree_attention_workspace(q, self.cache)
+        ws.fill_(255)
+        masks = D.signed(self.masks).cuda() if mask == "tree" else None
+        counts = torch.tensor(self.counts, dtype=torch.int32).cuda() if use_counts else None
+        rows = torch.tensor(self.rows, dtype=torch.int32).cuda()
+        qb.qnre_tree_attention(q, self.cache, self.layer, rows, masks, out, lse=lse, counts=counts, workspace=ws)
+        return out.cpu(), lse.cpu()
+
+    def check(self, out, lse, status=0):
+        assert self.cache.status() == status
+        half, dim = D.half_step(self.dt), self.q.shape[-1]
+        for i in range(len(self.lens)):
+            ref, rl, size = D.attention(self.q[i], self.keys[i], self.values[i], self.visible(i), self.scale)
+            s = (self.q[i].double().norm(dim=-1).max() * (self.keys[i].double().norm(dim=-1).max() if len(self.keys[i])
+                                                           else 0.0) * self.scale)
+            rel = float((dim + 16) * 2.0 ** -24 * s + 2.0 ** -20)
+            tol = half * ref.abs() * 1.02 + (half + 2 * rel) * size + 1e-7
+            err = (out[i].double() - ref).abs()
+            assert not torch.isnan(err).any(), f"request {i}: NaN"
+            assert (err <= tol).all(), f"request {i}: worst excess {(err - tol).max():.3g}"
+            same = torch.isinf(rl)
+            assert torch.equal(torch.isinf(lse[i]) & (lse[i] < 0), same)
+            assert ((lse[i].double() - rl)[~same].abs() <= 2 * rel + 1e-6 * rl[~same].abs() + 1e-6).all()
+
+
+SHAPES = [  # lens, nodes, Hq, Hk, dim, page, dtype
+    ([1], 1, 1, 1, 128, 16, "bf16"),
+    ([0], 1, 4, 4, 64, 8, "fp16"),                      # no context at all
+    ([127, 128, 129, 0, 255], 1, 8, 2, 128, 16, "bf16"),
+    ([300, 5, 1000], 3, 6, 1, 64, 24, "bf16"),          # pages that end inside a tile, group of 6
+    ([700], 1, 32, 8, 128, 128, "fp16"),
+    ([40, 513], 9, 8, 2, 128, 64, "bf16"),              # 36 rows: two copies
+    ([90, 200, 3], 16, 7, 1, 128, 48, "fp16"),          # 112 rows: one copy
+    ([260, 77], 33, 8, 1, 64, 32, "bf16"),              # 264 rows: three row tiles
+    ([65, 1], 64, 4, 2, 128, 16, "bf16"),               # 64 nodes, drafts across a tile's edge
+    ([5000, 1], 2, 4, 2, 128, 256, "bf16"),
+    ([11, 130, 64, 64, 200, 1, 0, 90], 61, 3, 3, 64, 16, "fp16"),
+]
+
+
+@pytest.mark.parametrize("lens,nodes,Hq,Hk,dim,page,dtype", SHAPES)
+def test_trees(lens, nodes, Hq, Hk, dim, page, dtype):
+    c = Case(lens, nodes, Hq, Hk, dim, page, dtype, seed=len(lens) + nodes)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("nodes,G", [(1, 4), (5, 8), (40, 8)])
+def test_long_context_spread_over_the_machine(nodes, G):
+    c = Case([20011], nodes, 2 * G, 2, 128, 64, "bf16", seed=9)
+    c.check(*c.run())
+
+
+def test_chain_mask_and_ragged_counts():
+    c = Case([50, 0, 300, 128], 7, 8, 2, 128, 16, "bf16", seed=4, counts=[7, 3, 0, 1])
+    c.masks = [[(1 << (t + 1)) - 1 for t in range(7)] for _ in range(4)]
+    out, lse = c.run(mask=None, use_counts=True)
+    c.check(out, lse)
+    assert not out[2].any() and not out[0, 7:].any() and torch.isinf(lse[2]).all()
+
+
+def test_masks_that_leave_a_row_empty_or_see_single_nodes():
+    c = Case([0, 0, 10], 5, 4, 2, 64, 8, "fp16", seed=5)
+    c.masks = [[0, 1 << 3, 0, 0b11111, 1 << 4], [0] * 5, [0, 0, 1, 0, -1 & ((1 << 64) - 1)]]
+    out, lse = c.run()
+    c.check(out, lse)
+    assert not out[1].any() and (lse[1] == float("-inf")).all()
+
+
+def test_what_is_not_seen_never_arrives():
+    """NaN and infinities in drafted slots that only some nodes see."""
+    c = Case([120], 12, 8, 2, 128, 16, "bf16", seed=6)
+    c.masks = [[1 << t for t in range(12)]]
+    clean = c.run()
+    c.check(*clean)
+    for x, val in ((124, float("nan")), (130, float("inf")), (131, float("-inf"))):
+        page, slot = c.table[c.rows[0], x // 16], x % 16
+        c.k[1, page, :, slot, 3] = float("nan") if x == 124 else 0.0
+        c.v[1, page, :, slot, 7] = val
+    out, lse = c.run()
+    keep = [t for t in range(12) if t not in (4, 10, 11)]
+    # the other nodes' keys changed nowhere but in slots they do not see
+    assert torch.equal(out[0, keep], clean[0][0, keep]) and torch.equal(lse[0, keep], clean[1][0, keep])
+    assert torch.isnan(out[0, 4]).all()                       # its own key is NaN
+    assert torch.isinf(out[0, 10, :, 7]).all() and (out[0, 10, :, 7] > 0).all()
+    assert torch.isinf(out[0, 11, :, 7]).all() and (out[0, 11, :, 7] < 0).all()
+    cols = [i for i in range(128) if i != 7]
+    assert torch.isfinite(out[0, 10][:, cols]).all() and torch.isfinite(out[0, 11][:, cols]).all()
+
+
+def test_large_scores_and_rising_maxima():
+    """Scores far apart, rising along the context: the running maximum moves many times."""
+    c = Case([900], 2, 4, 2, 64, 16, "fp16", seed=7)
+    with torch.no_grad():
+        ramp = torch.linspace(0.1, 6.0, 902)[:, None, None]
+        c.keys[0] = (c.q[0, 0, :2].float()[None] * ramp * 0.5).to(c.dt)
+        for x in range(902):
+            c.k[1, c.table[c.rows[0], x // 16], :, x % 16] = c.keys[0][x]
+    c.check(*c.run())
+
+
+def test_strided_queries_and_repeatability():
+    c = Case([333, 20, 1500], 6, 8, 2, 128, 32, "bf16", seed=8)
+    buf = torch.zeros((6, 3, 12, 128), dtype=torch.bfloat16, device="cuda")
+    view = buf.transpose(0, 1)[:, :, 2:10]
+    view.copy_(c.q)
+    a = c.run(q=view)
+    c.check(*a)
+    b = c.run()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_many_requests():
+    rng = random.Random(3)
+    c = Case([rng.randint(0, 60) for _ in range(300)], 1, 2, 1, 64, 8, "bf16", seed=10)
+    c.check(*c.run())
+
+
+def test_bad_tables_are_reported():
+    """A missing page reads as zeros, a bad row sees nothing; the other requests keep their results."""
+    qb = _qb()
+    c = Case([100, 40], 2, 4, 2, 128, 16, "bf16", seed=11)
+    c.table[c.rows[1], 1] = 10 ** 6
+    out, lse = c.run()
+    assert c.cache.status() == qb.CACHE_BAD_PAGE
+    c.keys[1][16:32] = 0
+    c.values[1][16:32] = 0
+    c.check(out, lse)
+    c.rows = [c.rows[0], 99]
+    out, lse = c.run()
+    assert c.cache.status() == qb.CACHE_BAD_ROW and not out[1].any() and torch.isinf(lse[1]).all()
+
+
+def test_graph_replay_on_grown_rows():
+    """A captured call follows the cache's lengths and contents."""
+    qb = _qb()
+    c = Case([70, 10], 3, 8, 2, 128, 16, "bf16", seed=12)
+    c.run()
+    q, cache = c.q.cuda(), c.cache
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    ws = qb.tree_attention_workspace(q, cache)
+    rows, masks = torch.tensor(c.rows, dtype=torch.int32).cuda(), D.signed(c.masks).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        qb.qnre_tree_attention(q, cache, 1, rows, masks, out, lse=lse, workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(out.cpu(), lse.cpu())
+    c.lens = [66, 7]
+    cache.seq_lens[rows.long()] = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    g.replay()
+    torch.cuda.synchronize()
+    c.keys = [k[:L + 3] for k, L in zip(c.keys, c.lens)]
+    c.values = [v[:L + 3] for v, L in zip(c.values, c.lens)]
+    c.check(out.cpu(), lse.cpu())

@@ -7,7 +7,8 @@ The names follow the C ABI: `qnre_forward`, `qnre_forward_noalloc`,
 `ulysses_scatter_qkv_head_chunk`, plus the `Plan` wrapper around
 `qnre_plan_create` / `qnre_plan_destroy`, and the speculative-decoding calls
 over a `PagedCache` (`qnre_qk_norm_rope` and its gradient,
-`qnre_qkv_norm_rope_append`, `qnre_cache_*`).  Tensors are torch CUDA tensors;
+`qnre_qkv_norm_rope_append`, `qnre_cache_*`, `qnre_tree_masks`,
+`qnre_tree_attention`, `qnre_verify_tree`).  Tensors are torch CUDA tensors;
 torch supplies device memory and the current stream, nothing else.  Every
 failure status raises `QnreError`; a missing library raises at first use.
 """
@@ -151,6 +152,15 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.qnre_qk_norm_rope_backward.argtypes = [t4, t4, t4, t4, *table, t4, t4, c_vp, c_vp, c_vp, ctypes.c_uint64, c_vp]
     lib.qnre_qkv_norm_rope_append.restype = c_int
     lib.qnre_qkv_norm_rope_append.argtypes = [t4, t4, t4, *table, t4, cache, c_int, c_vp, c_vp, c_vp]
+    lib.qnre_tree_attention_workspace_bytes.restype = c_int
+    lib.qnre_tree_attention_workspace_bytes.argtypes = [c_int, ctypes.POINTER(ctypes.c_uint64)]
+    lib.qnre_tree_attention.restype = c_int
+    lib.qnre_tree_attention.argtypes = [t4, cache, c_int, c_vp, c_vp, c_vp, ctypes.c_float, c_vp, c_vp, c_vp,
+                                        ctypes.c_uint64, c_vp]
+    lib.qnre_verify_tree.restype = c_int
+    lib.qnre_verify_tree.argtypes = [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_int, c_int, c_i64] + [c_vp] * 9
+    lib.qnre_tree_masks.restype = c_int
+    lib.qnre_tree_masks.argtypes = [c_vp, c_int, c_int, c_vp, c_vp, c_vp]
     _lib = lib
     return lib
 
@@ -638,3 +648,68 @@ def qnre_qkv_norm_rope_append(q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q
     _check(load_library().qnre_qkv_norm_rope_append(
         head[0], head[1], ctypes.byref(tv), *head[2:], ROPE_STYLES.get(rope_style, -1), pos, ctypes.byref(oq),
         cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)
+
+
+def qnre_tree_masks(parents, masks=None, depths=None, stream=None) -> None:
+    """Ancestor masks (int64 [n, nodes], bit j: node j) and depths (int32) of trees given by parents int32 [n, nodes]."""
+    import torch
+    where = "qnre_tree_masks"
+    if parents.dim() != 2 or (masks is not None and (masks.dtype != torch.int64 or masks.shape != parents.shape)):
+        raise QnreError(1, f"{where}: parents int32 [n, nodes], masks int64 alike")
+    n, nodes = parents.shape
+    _check(load_library().qnre_tree_masks(_i32(where, parents), n, nodes,
+                                          None if masks is None else _contig(masks, where),
+                                          _i32(where, depths, n, nodes), _stream_ptr(stream)), where)
+
+
+def tree_attention_workspace(q, cache: PagedCache):
+    """The scratch tensor qnre_tree_attention needs on this cache (any batch)."""
+    import torch
+    n = ctypes.c_uint64()
+    _check(load_library().qnre_tree_attention_workspace_bytes(cache.k.shape[-1], ctypes.byref(n)),
+           "qnre_tree_attention_workspace_bytes")
+    return torch.empty(n.value, dtype=torch.uint8, device=q.device)
+
+
+def qnre_tree_attention(q, cache: PagedCache, layer: int, rows, mask, out, lse=None, counts=None, scale=None,
+                        workspace=None, stream=None) -> None:
+    """Attention of drafted nodes q [n, nodes, Hq, D] over their rows' tokens and the nodes of mask (int64 [n, nodes];
+    None: a chain) into out (contiguous); scale defaults to 1/sqrt(D)."""
+    import torch
+    where = "qnre_tree_attention"
+    tq = _tensor4(q)
+    n, nodes, heads, dim = q.shape
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise QnreError(1, f"{where}: out must be contiguous, of q's shape and dtype")
+    if mask is not None and (mask.dtype != torch.int64 or tuple(mask.shape) != (n, nodes)):
+        raise QnreError(1, f"{where}: mask must be int64 [n, nodes]")
+    if workspace is None:
+        raise QnreError(1, f"{where}: workspace is missing (tree_attention_workspace)")
+    _check(load_library().qnre_tree_attention(
+        ctypes.byref(tq), cache.handle, layer, _i32(where, rows, n), None if mask is None else _contig(mask, where),
+        _i32(where, counts, n), dim ** -0.5 if scale is None else scale, _contig(out, where),
+        None if lse is None else _f32(where, lse, n, nodes, heads), _contig(workspace, where),
+        workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
+
+
+def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sample_u, path, counts, next_token,
+                     node_counts=None, stream=None) -> None:
+    """Walk drafted trees against target_probs [n, nodes, V] (fp32; draft_probs alike or None) with given random
+    numbers; fills path [n, nodes], counts [n] and next_token [n] (int32)."""
+    import torch
+    where = "qnre_verify_tree"
+    if target_probs.dim() != 3:
+        raise QnreError(1, f"{where}: target_probs must be [n, nodes, vocab]")
+    n, nodes, vocab = target_probs.shape
+    rows = []
+    for t in (target_probs, draft_probs):
+        if t is None:
+            rows += [None, 0, 0]
+            continue
+        if t.dtype != torch.float32 or t.shape != target_probs.shape or (t.stride(2) != 1 and vocab > 1):
+            raise QnreError(1, f"{where}: probabilities are float32 [n, nodes, vocab], each row contiguous")
+        rows += [t.data_ptr(), t.stride(0), t.stride(1)]
+    _check(load_library().qnre_verify_tree(
+        *rows, n, nodes, vocab, _i32(where, tokens, n, nodes), _i32(where, parents, n, nodes),
+        _i32(where, node_counts, n), _f32(where, accept_u, n, nodes), _f32(where, sample_u, n),
+        _i32(where, path, n, nodes), _i32(where, counts, n), _i32(where, next_token, n), _stream_ptr(stream)), where)

@@ -1,0 +1,970 @@
+// tree_attention.cu -- attention of drafted tree nodes (or of one new token) over a
+// paged K/V cache, on the sm_103a tensor cores.
+//
+//   o = sum_x p_x v_x,  p = softmax(scale q.k_x) over the tokens a node sees
+//
+// Work is cut into units (request, K head, 128 rows of (node, query head of the group)) and
+// each unit into tiles of 128 cached tokens; the concatenated tiles of all units are dealt out
+// in equal consecutive runs, one to a CTA, so batches of any raggedness load every
+// SM alike.  Each CTA takes the lengths from device memory and finds its own run.  A unit that spans
+// CTAs leaves an unnormalised (m, l, O) in the workspace from each, joined by combine_kernel in
+// CTA order: the result depends on the lengths alone, never on timing.
+//
+// In a CTA: warp 4 brings K and V tiles by TMA into a ring (a page's tokens of one head are one
+// run of memory; boxes of the largest power of two that divides the page); warp 5's
+// one thread issues tcgen05.mma: S = Q K^T (both operands in shared memory, fp32 S in
+// tensor memory, two buffers) and O += P V (P from tensor memory); warps 0-3 own one S row a thread:
+// one pass with a running maximum and sum in base 2, P rounded to the inputs' type
+// (relative 2^-9 for bf16, 2^-12 for fp16, against sums kept in fp32), O rescaled only
+// when a row's maximum grows by more than 2^8, so that P stays below 2^8 and O below 2^8 sum|v|.
+//
+// Units of few rows (one token, small groups) would leave three of the four softmax warps idle.
+// Their rows are laid out kRep = 2 or 4 times instead, copy c looking at its own 128 / kRep tokens of each
+// tile: P is zero outside that block, so one O accumulator of 128 rows holds kRep
+// independent partial results, joined at the end through shared memory.  The tensor work is the
+// same; each softmax thread has 1 / kRep of the exponentials.
+//
+// Slots that a row does not see must not reach it, whatever they hold: scores are replaced before use; V rows of
+// slots past the drafts are zeroed in shared memory, and non-finite V elements of drafted nodes (which
+// some rows see and others do not) are zeroed there and added to the rows that see them at the end.
+//
+// Bound: HBM while nodes * group is small (4 D bytes and 4 D rows flops a token and K head), the
+// softmax's exponentials and the tensor cores from about 128 rows up.
+#include "../../include/qnre.h"
+#include "cache.cuh"
+#include "ptx.cuh"
+#include "tma_map.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+namespace {
+
+using namespace qnre;
+using namespace qnre::api;
+
+constexpr int kTile = 128;     // cached tokens a tile, rows a unit
+constexpr int kThreads = 192;  // 4 softmax warps, the TMA warp, the MMA warp
+constexpr int kMaxCtas = 152;  // one a SM
+constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D, P 2 x 64
+constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
+constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that O is rescaled at
+
+struct Desc {  // a unit that spans CTAs, written by its second CTA for combine_kernel
+  int valid, req, kvh, rt, c0, c1, slot0, pad;
+};
+
+struct AttnArgs {
+  CUtensorMap tk, tv;
+  const char* q;
+  long long q_sb, q_ss, q_sh;
+  CacheView c;
+  const int32_t* rows;
+  const int32_t* counts;
+  const uint64_t* mask;
+  char* out;
+  float* lse;
+  Desc* desc;
+  float* part_ml;  // [2 * kMaxCtas][128][2]: maximum (base 2), sum
+  float* part_o;   // [2 * kMaxCtas][128][D]
+  float scale_log2;
+  int layer, n, nodes, Hq, Hk, G, unit_rows, row_tiles, box;
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kTileBytes;
+  static constexpr int kJoin = kRing + kStages * kTileBytes;      // float [128][33]
+  static constexpr int kMl = kJoin + 128 * 33 * 4;                // float [128][2]
+  static constexpr int kPre = kMl + 128 * 2 * 4;                  // int [QNRE_MAX_CALL_ROWS + 1]
+  static constexpr int kLen = kPre + (QNRE_MAX_CALL_ROWS + 4) * 4;  // int2 [QNRE_MAX_CALL_ROWS]
+  static constexpr int kBars = kLen + QNRE_MAX_CALL_ROWS * 8;
+  static constexpr int kBytes = kBars + 512 + 1024;               // + alignment of the base
+};
+
+struct Bars {
+  uint32_t full, empty, sfull, sfree, pready, pvdone, qready, ofree, drain;
+};
+
+// One unit's part of a CTA's run.
+struct Seg {
+  int req, kvh, rt, t0, t1, len, total;
+  bool whole;
+  int slot;
+};
+
+struct Cursor {
+  const int* pre;
+  const int2* lens;
+  int cur, end, start, req, units, row_tiles;
+  __device__ __forceinline__ static int tiles_of(int total) { return total > 0 ? (total + kTile - 1) / kTile : 1; }
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (cur >= end) return false;
+    while (cur >= pre[req + 1]) ++req;
+    s.req = req;
+    s.len = lens[req].x;
+    s.total = lens[req].y;
+    const int tiles = tiles_of(s.total);
+    const int off = cur - pre[req];
+    const int unit = off / tiles;
+    s.kvh = unit / row_tiles;
+    s.rt = unit - s.kvh * row_tiles;
+    s.t0 = off - unit * tiles;
+    s.t1 = min(tiles, s.t0 + end - cur);
+    s.whole = s.t0 == 0 && s.t1 == tiles;
+    s.slot = 2 * static_cast<int>(blockIdx.x) + (cur > start ? 1 : 0);
+    cur += s.t1 - s.t0;
+    return true;
+  }
+};
+
+// Waits for a phase; false (and the abort word set) after the time limit or an abort elsewhere.
+__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* status) {
+  const uint64_t t0 = ptx::global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 31u) == 0) {
+      if (*abort_flag) return false;
+      if (ptx::global_timer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1u;
+        atomicOr(status, QNRE_CACHE_WAIT_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* status) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  return slow_wait(bar, parity, abort_flag, status);
+}
+
+__device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float to_float(uint32_t bits16) {
+  if (BF16) return __uint_as_float(bits16 << 16);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(bits16)));
+}
+
+// Non-finite halves of a word as a mask of 0xFFFF fields.
+template <bool BF16>
+__device__ __forceinline__ uint32_t nonfinite_mask(uint32_t w) {
+  const uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+  return ((w & e) == e ? 0xFFFFu : 0u) | (((w >> 16) & e) == e ? 0xFFFF0000u : 0u);
+}
+
+__device__ __forceinline__ void tmem_fence_regs(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem desc].
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const void* tmap, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ TMA warp
+template <int D>
+__device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem, Cursor cur,
+                             volatile uint32_t* abort_flag) {
+  using L = Smem<D>;
+  constexpr int kHalves = D / 64;
+  const int lane = threadIdx.x % 32;
+  const int chunks = kTile / a.box;
+  const int chunk = lane / kHalves, half = lane % kHalves;
+  const bool active = chunk < chunks;
+  uint32_t r = 0;
+  Seg s;
+  while (cur.next(s)) {
+    const int row = a.rows[s.req];
+    const bool row_ok = row >= 0 && row < a.c.rows;
+    for (int t = s.t0; t < s.t1; ++t) {
+      const int pos = t * kTile + chunk * a.box;
+      int page = a.layer * a.c.pages;
+      if (active && row_ok) {
+        const int p = a.c.page_of(row, pos);
+        if (p < 0 && pos < s.total) atomicOr(a.c.status, QNRE_CACHE_BAD_PAGE);
+        page = p >= 0 ? page + p : a.c.layers * a.c.pages;  // past the end: the box is filled with zeros
+      } else {
+        page = a.c.layers * a.c.pages;
+      }
+      for (int kv = 0; kv < 2; ++kv, ++r) {
+        const uint32_t slot = r % L::kStages, ph = (r / L::kStages) & 1u;
+        if (!wait(bars.empty + 8 * slot, ph ^ 1u, abort_flag, a.c.status)) {
+          // stop: what is in flight settles in microseconds; the kernel's end waits for it
+          const uint64_t t0 = ptx::global_timer_ns();
+          while (ptx::global_timer_ns() - t0 < 50000) {
+          }
+          return;
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bars.full + 8 * slot, L::kTileBytes);
+        __syncwarp();
+        if (active)
+          tma_load_4d(smem + L::kRing + slot * L::kTileBytes + half * (kTile * 128) + chunk * a.box * 128,
+                      kv ? &a.tv : &a.tk, bars.full + 8 * slot, half * 64, pos % a.c.page_size, s.kvh, page);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ MMA thread
+template <int D, bool BF16>
+__device__ void run_mma(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
+                        volatile uint32_t* abort_flag) {
+  using L = Smem<D>;
+  constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
+  constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
+  constexpr uint32_t kIdescO = (1u << 4) | kFmt | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
+  uint32_t g = 0;  // tiles of the run
+  uint32_t seg = 0;
+  Seg s;
+  bool ok = true;
+
+  auto pv = [&](uint32_t x, bool first) {
+    const uint32_t b = x & 1u, ring = 2 * x + 1;
+    const uint32_t slot = ring % L::kStages;
+    ok = ok && wait(bars.pready + 8 * b, (x >> 1) & 1u, abort_flag, a.c.status);
+    ok = ok && wait(bars.full + 8 * slot, (ring / L::kStages) & 1u, abort_flag, a.c.status);
+    if (first) ok = ok && wait(bars.ofree, (seg & 1u) ^ 1u, abort_flag, a.c.status);
+    if (!ok) return;
+    ptx::tc_fence_after_sync();
+    const uint32_t v = smem + L::kRing + slot * L::kTileBytes;
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+      umma_f16_ts(tmem + kTmemO, tmem + kTmemP + b * 64 + kk * 8,
+                  ptx::smem_desc_sw128(v + kk * 2048, kTile * 128, 1024), kIdescO, (!first || kk > 0) ? 1u : 0u);
+    ptx::umma_commit(bars.empty + 8 * slot);
+    ptx::umma_commit(bars.pvdone + 8 * b);
+  };
+
+  for (; ok && cur.next(s); ++seg) {
+    ok = wait(bars.qready, seg & 1u, abort_flag, a.c.status);
+    for (int t = s.t0; ok && t < s.t1; ++t, ++g) {
+      const uint32_t b = g & 1u, ring = 2 * g;
+      const uint32_t slot = ring % L::kStages;
+      ok = wait(bars.full + 8 * slot, (ring / L::kStages) & 1u, abort_flag, a.c.status) &&
+           wait(bars.sfree + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
+      if (!ok) break;
+      ptx::tc_fence_after_sync();
+      const uint32_t k = smem + L::kRing + slot * L::kTileBytes, q = smem + L::kQ;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
+        ptx::umma_f16(tmem + kTmemS + b * 128, ptx::smem_desc_sw128(q + off, 16, 1024),
+                      ptx::smem_desc_sw128(k + off, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+      }
+      ptx::umma_commit(bars.sfull + 8 * b);
+      ptx::umma_commit(bars.empty + 8 * slot);
+      if (t > s.t0) pv(g - 1, t - 1 == s.t0);
+    }
+    if (ok) pv(g - 1, s.t1 - 1 == s.t0);
+  }
+  if (!ok) {
+    ptx::umma_commit(bars.drain);
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (!ptx::mbar_try_wait(bars.drain, 0) && ptx::global_timer_ns() - t0 < kWaitLimitNs) {
+    }
+  }
+}
+
+// ------------------------------------------------------------------ softmax warps
+template <int D, bool BF16, int REP>
+__device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base, uint32_t smem, uint32_t tmem,
+                            Cursor cur, volatile uint32_t* abort_flag, unsigned long long* bad_nodes) {
+  using L = Smem<D>;
+  constexpr int kCols = kTile / REP;   // tokens of a tile this thread looks at
+  constexpr int kRows = 128 / REP;     // unit rows
+  constexpr int kVecs = D / 8;         // 16-byte pieces of a row
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int ur = tid % kRows, copy = tid / kRows, c0 = copy * kCols;
+  const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+  float* join = reinterpret_cast<float*>(smem_base + L::kJoin);
+  float* ml = reinterpret_cast<float*>(smem_base + L::kMl);
+
+  if (REP > 1) {  // P outside this copy's tokens stays zero
+    uint32_t zero[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) zero[i] = 0;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) tmem_st_x32(tmem + lane_base + kTmemP + c, zero);
+    tmem_st_wait();
+  }
+
+  // what unit row r of segment s sees of the drafts; false when it is no row or a node past the count
+  auto row_bits = [&](const Seg& s, int r, int& node, int& head, uint64_t& bits) -> bool {
+    const int R = s.rt * kTile + r;
+    node = R / a.G;
+    head = s.kvh * a.G + R - node * a.G;
+    bits = 0;
+    if (R >= a.unit_rows) return false;
+    const int cnt = a.counts != nullptr ? min(max(a.counts[s.req], 0), a.nodes) : a.nodes;
+    if (node >= cnt) return false;
+    bits = a.mask != nullptr ? a.mask[static_cast<long long>(s.req) * a.nodes + node] : (2ull << node) - 1;
+    const int drafts = s.total - s.len;  // slots that exist
+    if (drafts < 64) bits &= (1ull << drafts) - 1;
+    return true;
+  };
+
+  uint32_t g = 0;
+  Seg s;
+  while (cur.next(s)) {
+    int node, head;
+    uint64_t bits;
+    const bool row_ok = row_bits(s, ur, node, head, bits);
+    {  // Q row -> shared memory, K-major with the 128-byte swizzle
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + s.req * a.q_sb + node * a.q_ss + head * a.q_sh);
+      uint4 v[kVecs];
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) v[i] = row_ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        *reinterpret_cast<uint4*>(smem_base + L::kQ + (i / 8) * (kTile * 128) + tid * 128 +
+                                  (((i % 8) ^ (tid & 7)) * 16)) = v[i];
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(bars.qready);
+    }
+    float m = -INFINITY, l = 0.f;
+    for (int t = s.t0; t < s.t1; ++t, ++g) {
+      const uint32_t b = g & 1u;
+      const int x0 = t * kTile + c0;
+      uint32_t v[kCols / 32][32];
+      wait(bars.sfull + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status);
+      __syncwarp();  // the tensor-memory instructions are warp-wide
+      ptx::tc_fence_after_sync();
+#pragma unroll
+      for (int j = 0; j < kCols / 32; ++j)
+        ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemS + b * 128 + c0 + 32 * j, v[j]);
+      ptx::tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < kCols / 32; ++j) tmem_fence_regs(v[j]);
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars.sfree + 8 * b);
+
+      const bool tail = (t + 1) * kTile > s.len;
+      if (tail || !row_ok) {
+#pragma unroll
+        for (int j = 0; j < kCols / 32; ++j)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int d = x0 + 32 * j + i - s.len;
+            const bool see = row_ok && (d < 0 || (d < 64 && ((bits >> d) & 1)));
+            if (!see) v[j][i] = 0xFF800000u;
+          }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kCols / 32; ++j)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[j][i]));
+      mx *= a.scale_log2;
+      const bool grow = mx > m + kRescale;
+      if (t == s.t0) {
+        m = mx;
+      } else if (__any_sync(0xFFFFFFFFu, grow)) {
+        const uint32_t last = g - 1;
+        wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        const float f = grow ? exp2_fast(m - mx) : 1.f;
+        if (grow) m = mx;
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
+          ptx::tmem_ld_wait();
+          tmem_fence_regs(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st_x32(tmem + lane_base + kTmemO + c, o);
+        }
+        tmem_st_wait();
+      }
+      const float ms = m == -INFINITY ? 0.f : m;
+      uint32_t p[kCols / 2];
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) {
+        const float e0 = exp2_fast(fmaf(__uint_as_float(v[i / 16][(2 * i) % 32]), a.scale_log2, -ms));
+        const float e1 = exp2_fast(fmaf(__uint_as_float(v[i / 16][(2 * i + 1) % 32]), a.scale_log2, -ms));
+        sum0 += e0;
+        sum1 += e1;
+        p[i] = pack2<BF16>(e0, e1);
+      }
+      l += sum0 + sum1;
+      // P's buffer is free once the product two tiles back is done
+      wait(bars.pvdone + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
+      __syncwarp();
+      ptx::tc_fence_after_sync();
+      const uint32_t pt = tmem + lane_base + kTmemP + b * 64 + c0 / 2;
+      if (kCols == 128) {
+        tmem_st_x32(pt, p);
+        tmem_st_x32(pt + 32, p + (kCols == 128 ? 32 : 0));
+      } else if (kCols == 64) {
+        tmem_st_x32(pt, p);
+      } else {
+        tmem_st_x16(pt, p);
+      }
+      if (tail) {
+        const uint32_t ring = 2 * g + 1, slot = ring % L::kStages;
+        wait(bars.full + 8 * slot, (ring / L::kStages) & 1u, abort_flag, a.c.status);
+        const int pos = t * kTile + tid;
+        if (pos >= s.len) {
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(smem_base + L::kRing + slot * L::kTileBytes + (i / 8) * (kTile * 128) +
+                                                 tid * 128 + (i % 8) * 16);
+            if (pos >= s.total) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else {
+              uint4 w = *at;
+              const uint4 z = make_uint4(nonfinite_mask<BF16>(w.x), nonfinite_mask<BF16>(w.y),
+                                         nonfinite_mask<BF16>(w.z), nonfinite_mask<BF16>(w.w));
+              if (z.x | z.y | z.z | z.w) {
+                found = true;
+                *at = make_uint4(w.x & ~z.x, w.y & ~z.y, w.z & ~z.z, w.w & ~z.w);
+              }
+            }
+          }
+          if (found) atomicOr(bad_nodes, 1ull << (pos - s.len));
+          ptx::fence_proxy_async_smem();
+        }
+        __syncwarp();
+      }
+      tmem_st_wait();
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars.pready + 8 * b);
+    }
+
+    // ---------------- the segment's result
+    const uint32_t last = g - 1;
+    wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
+    __syncwarp();
+    ptx::tc_fence_after_sync();
+    unsigned long long bad = 0;
+    if (s.t1 * kTile > s.len) {
+      named_sync();
+      bad = *bad_nodes;
+      named_sync();
+      if (tid == 0 && bad != 0) *bad_nodes = 0;
+    }
+    // non-finite V elements of the drafts a row sees
+    auto add_bad = [&](uint64_t seen, int c, float x) -> float {
+      const int row = a.rows[s.req];
+      for (uint64_t todo = seen; todo != 0; todo &= todo - 1) {
+        const int pos = s.len + __ffsll(static_cast<long long>(todo)) - 1;
+        if (pos < s.t0 * kTile || pos >= s.t1 * kTile) continue;
+        const int page = a.c.page_of(row, pos);
+        if (page < 0) continue;
+        const uint16_t w = *reinterpret_cast<const uint16_t*>(a.c.v + a.c.token_offset(a.layer, page, s.kvh, pos) + c * 2);
+        if (nonfinite_mask<BF16>(w) & 0xFFFFu) x += to_float<BF16>(w);
+      }
+      return x;
+    };
+
+    if (REP == 1) {
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      const long long orow = (static_cast<long long>(s.req) * a.nodes + node) * a.Hq + head;
+      const bool store = s.rt * kTile + ur < a.unit_rows;
+      const long long prow = static_cast<long long>(s.slot) * 128 + ur;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
+        ptx::tmem_ld_wait();
+        tmem_fence_regs(o);
+        if (row_ok && (bad & bits) != 0) {
+#pragma unroll 1
+          for (int i = 0; i < 32; ++i) join[tid * 33 + i] = add_bad(bad & bits, c + i, 0.f);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + join[tid * 33 + i]);
+        }
+        if (store && s.whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c) * 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack2<BF16>(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (store) {
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+        __syncwarp();
+      }
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars.ofree);
+      if (store) {
+        if (s.whole) {
+          if (a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        } else {
+          reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(m, l);
+        }
+      }
+    } else {
+      // the copies' common maximum and sum, then their O in blocks of 32 columns
+      ml[2 * tid] = m;
+      ml[2 * tid + 1] = l;
+      named_sync();
+      auto joined = [&](int r, float& M, float& Lsum) {
+        M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < REP; ++c) M = fmaxf(M, ml[2 * (c * kRows + r)]);
+        Lsum = 0.f;
+#pragma unroll
+        for (int c = 0; c < REP; ++c) {
+          const float mc = ml[2 * (c * kRows + r)];
+          Lsum += ml[2 * (c * kRows + r) + 1] * (mc == -INFINITY ? 0.f : exp2_fast(mc - M));
+        }
+      };
+      float M, Lsum;
+      joined(ur, M, Lsum);
+      const float f = m == -INFINITY ? 0.f : exp2_fast(m - M);
+      constexpr int kPer = 32 / REP;  // columns of a block this thread sums and writes
+      const int jr = tid / REP, jc = (tid % REP) * kPer;
+      int jnode, jhead;
+      uint64_t jbits;
+      const bool jok = row_bits(s, jr, jnode, jhead, jbits);
+      const bool store = s.rt * kTile + jr < a.unit_rows;
+      float jM, jL;
+      joined(jr, jM, jL);
+      const float inv = jL > 0.f ? 1.f / jL : (jL == 0.f ? 0.f : jL);
+      const long long orow = (static_cast<long long>(s.req) * a.nodes + jnode) * a.Hq + jhead;
+      const long long prow = static_cast<long long>(s.slot) * 128 + jr;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
+        ptx::tmem_ld_wait();
+        tmem_fence_regs(o);
+        if (c + 32 == D) {
+          ptx::tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bars.ofree);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) join[tid * 33 + i] = __uint_as_float(o[i]) * f;
+        named_sync();
+        float x[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          x[i] = 0.f;
+#pragma unroll
+          for (int k = 0; k < REP; ++k) x[i] += join[(k * kRows + jr) * 33 + jc + i];
+          if (jok && (bad & jbits) != 0) x[i] = add_bad(bad & jbits, c + jc + i, x[i]);
+        }
+        if (store) {
+          if (s.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c + jc) * 2);
+#pragma unroll
+            for (int i = 0; i < kPer / 8; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = pack2<BF16>(x[8 * i + 2 * e] * inv, x[8 * i + 2 * e + 1] * inv);
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c + jc);
+#pragma unroll
+            for (int i = 0; i < kPer / 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
+        }
+        named_sync();
+      }
+      if (store && jc == 0) {
+        if (s.whole) {
+          if (a.lse != nullptr) a.lse[orow] = jL == 0.f ? -INFINITY : (jM + log2f(jL)) * 0.6931471805599453f;
+        } else {
+          reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(jM, jL);
+        }
+      }
+    }
+  }
+}
+
+template <int D, bool BF16, int REP>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
+  using L = Smem<D>;
+  extern __shared__ char raw[];
+  __shared__ uint32_t tmem_slot, abort_word;
+  __shared__ unsigned long long bad_nodes;
+  char* smem_base = raw + ((1024u - (ptx::smem_addr(raw) & 1023u)) & 1023u);
+  const uint32_t smem = ptx::smem_addr(smem_base);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int* pre = reinterpret_cast<int*>(smem_base + L::kPre);
+  int2* lens = reinterpret_cast<int2*>(smem_base + L::kLen);
+  Bars bars;
+  {
+    uint32_t at = smem + L::kBars;
+    auto take = [&](int n) {
+      const uint32_t r = at;
+      at += 8 * n;
+      return r;
+    };
+    bars.full = take(L::kStages);
+    bars.empty = take(L::kStages);
+    bars.sfull = take(2);
+    bars.sfree = take(2);
+    bars.pready = take(2);
+    bars.pvdone = take(2);
+    bars.qready = take(1);
+    bars.ofree = take(1);
+    bars.drain = take(1);
+  }
+  if (warp == 4) ptx::tmem_alloc(ptx::smem_addr(&tmem_slot), 512);
+  if (tid == 0) {
+    abort_word = 0;
+    bad_nodes = 0;
+    for (int i = 0; i < L::kStages; ++i) {
+      ptx::mbar_init(bars.full + 8 * i, 1);
+      ptx::mbar_init(bars.empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bars.sfull + 8 * i, 1);
+      ptx::mbar_init(bars.sfree + 8 * i, 4);
+      ptx::mbar_init(bars.pready + 8 * i, 4);
+      ptx::mbar_init(bars.pvdone + 8 * i, 1);
+    }
+    ptx::mbar_init(bars.qready, 128);
+    ptx::mbar_init(bars.ofree, 4);
+    ptx::mbar_init(bars.drain, 1);
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&a.tk);
+    ptx::prefetch_tensormap(&a.tv);
+  }
+  // the rows' lengths, and the first tile of each request in the concatenated run
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int units = a.Hk * a.row_tiles;
+  const int room = a.c.max_blocks * a.c.page_size;
+  for (int i = tid; i < a.n; i += kThreads) {
+    const int row = a.rows[i];
+    int len = 0, cnt = 0;
+    if (row >= 0 && row < a.c.rows) {
+      len = min(max(a.c.lens[row], 0), room);
+      cnt = a.counts != nullptr ? min(max(a.counts[i], 0), a.nodes) : a.nodes;
+    } else if (blockIdx.x == 0) {
+      atomicOr(a.c.status, QNRE_CACHE_BAD_ROW);
+    }
+    const int total = min(len + cnt, room);
+    lens[i] = make_int2(len, total);
+    pre[i + 1] = Cursor::tiles_of(total) * units;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int carry = 0;
+    if (lane == 0) pre[0] = 0;
+    for (int base = 0; base < a.n; base += 32) {
+      int v = base + lane < a.n ? pre[base + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (base + lane < a.n) pre[base + lane + 1] = carry + v;
+      carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+  }
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  const long long W = pre[a.n];
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
+  const int cta = blockIdx.x;
+  Cursor cur;
+  cur.pre = pre;
+  cur.lens = lens;
+  cur.row_tiles = a.row_tiles;
+  cur.units = units;
+  cur.start = cur.cur = cta < ctas ? static_cast<int>(W * cta / ctas) : 0;
+  cur.end = cta < ctas ? static_cast<int>(W * (cta + 1) / ctas) : 0;
+  int lo = 0, hi = a.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (pre[mid] <= cur.start) lo = mid; else hi = mid - 1;
+  }
+  cur.req = lo;
+
+  if (tid == 0) {  // this CTA begins inside a unit that the CTA before began: name it for the join
+    Desc d{};
+    if (cur.cur < cur.end) {
+      Cursor look = cur;
+      Seg s;
+      look.next(s);
+      const long long first = cur.start - s.t0;
+      const long long end = first + Cursor::tiles_of(s.total);
+      const int c0 = static_cast<int>(((first + 1) * ctas - 1) / W);
+      if (s.t0 > 0 && c0 == cta - 1) {
+        const int c1 = static_cast<int>((end * ctas - 1) / W);
+        d = Desc{1, s.req, s.kvh, s.rt, c0, c1, 2 * c0 + (first > W * c0 / ctas ? 1 : 0), 0};
+      }
+    }
+    a.desc[cta] = d;
+  }
+
+  if (warp < 4) {
+    run_softmax<D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &abort_word, &bad_nodes);
+  } else if (warp == 4) {
+    run_producer<D>(a, bars, smem, cur, &abort_word);
+  } else if (lane == 0) {
+    run_mma<D, BF16>(a, bars, smem, tmem, cur, &abort_word);
+  }
+  __syncwarp();
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  ptx::tc_fence_after_sync();
+  if (warp == 4) {
+    ptx::tmem_relinquish_alloc_permit();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the units that span CTAs: block x is the unit's second CTA, a warp a row.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const float* part_ml, const float* part_o,
+                                                      char* out, float* lse, int nodes, int Hq, int G, int unit_rows) {
+  constexpr int kPer = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Desc d = desc[blockIdx.x];
+  if (!d.valid) return;
+  const int lane = threadIdx.x % 32, r = blockIdx.y * 8 + threadIdx.x / 32;
+  const int R = d.rt * kTile + r;
+  if (r >= kTile || R >= unit_rows) return;
+  const int parts = d.c1 - d.c0 + 1;
+  auto row_of = [&](int i) { return static_cast<long long>(i == 0 ? d.slot0 : 2 * (d.c0 + i)) * 128 + r; };
+  float M = -INFINITY;
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, part_ml[2 * row_of(i)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float acc[kPer] = {}, l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const long long at = row_of(i);
+    const float2 ml = reinterpret_cast<const float2*>(part_ml)[at];
+    const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
+    const float* o = part_o + at * D + lane * kPer;
+    l = fmaf(ml.y, w, l);
+    if (kPer == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(o);
+      acc[0] = fmaf(v.x, w, acc[0]);
+      acc[1] = fmaf(v.y, w, acc[1]);
+      acc[kPer - 2] = fmaf(v.z, w, acc[kPer - 2]);
+      acc[kPer - 1] = fmaf(v.w, w, acc[kPer - 1]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(o);
+      acc[0] = fmaf(v.x, w, acc[0]);
+      acc[1] = fmaf(v.y, w, acc[1]);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const int node = R / G;
+  const long long orow = (static_cast<long long>(d.req) * nodes + node) * Hq + d.kvh * G + (R - node * G);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(out + (orow * D + lane * kPer) * 2);
+#pragma unroll
+  for (int i = 0; i < kPer / 2; ++i) dst[i] = pack2<BF16>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (lse != nullptr && lane == 0) lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+constexpr uint64_t kDescBytes = 152 * sizeof(Desc);
+constexpr uint64_t kMlBytes = 2ull * kMaxCtas * 128 * 2 * 4;
+
+template <int D, bool BF16, int REP>
+qnre_status_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return QNRE_ERR_CUDA;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load() & bit)) {
+    if (cudaFuncSetAttribute(attention_kernel<D, BF16, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem<D>::kBytes) != cudaSuccess)
+      return QNRE_ERR_CUDA;
+    ready.fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<D>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attention_kernel<D, BF16, REP>, a) != cudaSuccess) return QNRE_ERR_CUDA;
+  cfg.gridDim = dim3(ctas, (std::min(a.unit_rows, kTile) + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return from_cuda(cudaLaunchKernelEx(&cfg, combine_kernel<D, BF16>, static_cast<const Desc*>(a.desc),
+                                      static_cast<const float*>(a.part_ml), static_cast<const float*>(a.part_o), a.out,
+                                      a.lse, a.nodes, a.Hq, a.G, a.unit_rows));
+}
+
+template <int D, bool BF16>
+qnre_status_t launch_rep(const AttnArgs& a, int ctas, cudaStream_t stream) {
+  if (a.unit_rows <= 32) return launch_attention<D, BF16, 4>(a, ctas, stream);
+  if (a.unit_rows <= 64) return launch_attention<D, BF16, 2>(a, ctas, stream);
+  return launch_attention<D, BF16, 1>(a, ctas, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+qnre_status_t qnre_tree_attention_workspace_bytes(int head_dim, uint64_t* bytes) {
+  if (bytes == nullptr) return QNRE_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return QNRE_ERR_UNSUPPORTED;
+  *bytes = kDescBytes + kMlBytes + 2ull * kMaxCtas * 128 * head_dim * 4;
+  return QNRE_OK;
+}
+
+qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* cache, int layer, const int32_t* rows,
+                                  const uint64_t* mask, const int32_t* counts, float scale, void* out, float* lse,
+                                  void* workspace, uint64_t workspace_bytes, qnre_stream_t stream) {
+  if (q == nullptr) return QNRE_ERR_INVALID_ARG;
+  qnre_tensor4_t own = *q;
+  alignas(16) static char nothing[16];
+  const bool empty = own.shape[0] == 0 || own.shape[1] == 0;
+  if (own.data == nullptr && empty) own.data = nothing;
+  ByteRange rq;
+  qnre_status_t st = check_view(&own, &rq);
+  if (st == QNRE_OK) st = check_cache(cache, static_cast<int>(std::min<int64_t>(own.shape[0], 0x7FFFFFFF)));
+  if (st != QNRE_OK) return st;
+  if (own.dtype != cache->dtype || own.shape[3] != cache->head_dim || own.shape[2] % cache->heads != 0 || layer < 0 ||
+      layer >= cache->layers || !(scale > 0.f) || !std::isfinite(scale))
+    return QNRE_ERR_INVALID_ARG;
+  if (own.shape[1] > QNRE_MAX_NODES || own.shape[2] > 65535) return QNRE_ERR_CAPACITY;
+  if (!rows_vectorisable(&own, 2)) return QNRE_ERR_ALIGNMENT;
+  uint64_t need = 0;
+  qnre_tree_attention_workspace_bytes(cache->head_dim, &need);
+  if (empty) return QNRE_OK;
+  if (rows == nullptr || out == nullptr || workspace == nullptr) return QNRE_ERR_INVALID_ARG;
+  if (!aligned(rows, 4) || !aligned(counts, 4) || !aligned(mask, 8) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(workspace, 16))
+    return QNRE_ERR_ALIGNMENT;
+  if (workspace_bytes < need) return QNRE_ERR_CAPACITY;
+  const int64_t out_rows = own.shape[0] * own.shape[1] * own.shape[2];
+  const ByteRange ro = span(out, static_cast<uint64_t>(out_rows) * cache->head_dim * 2), rw = span(workspace, need);
+  const ByteRange rl = lse != nullptr ? span(lse, static_cast<uint64_t>(out_rows) * 4) : ByteRange{0, 0};
+  const ByteRange pools[2] = {span(cache->k, pool_bytes(cache)), span(cache->v, pool_bytes(cache))};
+  for (const ByteRange& w : {ro, rw, rl})
+    for (const ByteRange& r : {rq, pools[0], pools[1]})
+      if (overlaps(w, r)) return QNRE_ERR_ALIAS;
+  if (overlaps(ro, rw) || overlaps(ro, rl) || overlaps(rw, rl)) return QNRE_ERR_ALIAS;
+
+  AttnArgs a{};
+  a.c = view_of(cache);
+  a.layer = layer;
+  a.n = static_cast<int>(own.shape[0]);
+  a.nodes = static_cast<int>(own.shape[1]);
+  a.Hq = static_cast<int>(own.shape[2]);
+  a.Hk = cache->heads;
+  a.G = a.Hq / a.Hk;
+  a.unit_rows = a.nodes * a.G;
+  a.row_tiles = (a.unit_rows + kTile - 1) / kTile;
+  const int64_t tiles = (static_cast<int64_t>(cache->max_blocks) * cache->page_size + kTile - 1) / kTile;
+  if (a.n * tiles * a.Hk * a.row_tiles > 0x7FFFFFFF) return QNRE_ERR_CAPACITY;
+  a.box = std::min(kTile, cache->page_size & -cache->page_size);
+  a.q = static_cast<const char*>(own.data);
+  a.q_sb = own.stride[0] * 2;
+  a.q_ss = own.stride[1] * 2;
+  a.q_sh = own.stride[2] * 2;
+  a.rows = rows;
+  a.counts = counts;
+  a.mask = mask;
+  a.out = static_cast<char*>(out);
+  a.lse = lse;
+  a.desc = static_cast<Desc*>(workspace);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + kDescBytes);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kDescBytes + kMlBytes);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const bool bf16 = cache->dtype == QNRE_DTYPE_BF16;
+  const uint64_t D = cache->head_dim, ps = cache->page_size, H = cache->heads;
+  const uint64_t dims[4] = {D, ps, H, static_cast<uint64_t>(cache->layers) * cache->pages};
+  const uint64_t strides[3] = {D * 2, ps * D * 2, H * ps * D * 2};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(a.box), 1, 1};
+  if (!encode_tiled_16bit(&a.tk, cache->k, bf16, 4, dims, strides, box) ||
+      !encode_tiled_16bit(&a.tv, cache->v, bf16, 4, dims, strides, box))
+    return QNRE_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QNRE_ERR_CUDA;
+  const int ctas = std::min(sms, kMaxCtas);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (D == 128) return bf16 ? launch_rep<128, true>(a, ctas, s) : launch_rep<128, false>(a, ctas, s);
+  return bf16 ? launch_rep<64, true>(a, ctas, s) : launch_rep<64, false>(a, ctas, s);
+}
+
+}  // extern "C"
