@@ -671,7 +671,8 @@ qnre_status_t qnre_qkv_norm_rope_append(const qnre_tensor4_t* q, const qnre_tens
  *   x over tokens [0, seq_lens[rows[i]]) and seq_lens + j with bit j of mask[i][t], j < counts[i]
  *
  *   q        view [n, nodes, Hq, D], the cache's dtype, aligned as above; Hq a multiple of the
- *            cache's heads (query head h reads head h / (Hq / heads)); nodes <= QNRE_MAX_NODES.
+ *            cache's heads, at most 128 to one (query head h reads head h / (Hq / heads));
+ *            nodes <= QNRE_MAX_NODES.
  *   rows     device int32 [n].
  *   mask     device uint64 [n, nodes]; NULL: node t sees nodes 0..t.
  *   counts   device int32 [n]: the nodes of each request (NULL: all); later nodes see nothing.

@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Dict, List, Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -60,6 +61,9 @@ class _PlanInfo(ctypes.Structure):
 class _Tensor4(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("shape", ctypes.c_int64 * 4),
                 ("stride", ctypes.c_int64 * 4), ("dtype", ctypes.c_int32)]
+
+
+_pack_tensor4 = struct.Struct("P4q4qi4x").pack  # the layout of _Tensor4
 
 
 class _Cache(ctypes.Structure):
@@ -178,18 +182,26 @@ def _check(status: int, where: str) -> None:
         raise QnreError(status, where)
 
 
+_dtype_codes: Dict[object, int] = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if t.dtype not in codes:
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise QnreError(2, f"dtype {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
+# A decode step's kernels run for a few microseconds, so the calls' own cost counts: the current
+# stream is read as a raw handle (0.2 us on a Grace core; building the Stream object takes 2.9) and a view
+# is packed in one go (0.7 us; field by field 2.4).
 def _stream_ptr(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -200,13 +212,7 @@ def _ptr(t) -> Optional[int]:
 def _tensor4(t) -> _Tensor4:
     if t.dim() != 4:
         raise QnreError(1, "expected a rank-4 view")
-    d = _Tensor4()
-    d.data = t.data_ptr()
-    for i in range(4):
-        d.shape[i] = t.shape[i]
-        d.stride[i] = t.stride(i)
-    d.dtype = _dtype_code(t)
-    return d
+    return _Tensor4.from_buffer_copy(_pack_tensor4(t.data_ptr(), *t.shape, *t.stride(), _dtype_code(t)))
 
 
 class Plan:
@@ -509,10 +515,7 @@ class PagedCache:
                               _i32("PagedCache", block_table), _i32("PagedCache", seq_lens),
                               _i32("PagedCache", page_refs), self.status_word.data_ptr(), self.scratch.data_ptr(),
                               layers, pages, heads, page_size, head_dim, rows, block_table.shape[1], _dtype_code(k))
-
-    @property
-    def handle(self):
-        return ctypes.byref(self._struct)
+        self.handle = ctypes.byref(self._struct)
 
     def status(self, clear: bool = True) -> int:
         """The CACHE_* bits kernels have set (waits for the current stream)."""
@@ -533,25 +536,40 @@ def alloc_paged_cache(layers: int, pages: int, heads: int, page_size: int, head_
                       torch.zeros(pages, dtype=torch.int32, device=device))
 
 
+_int32 = _int64 = _float32 = None
+
+
+def _load_dtypes():
+    global _int32, _int64, _float32
+    import torch
+    _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
+
+
 def _i32(where: str, t, *shape):
     """Pointer of a contiguous int32 tensor (None passes), its shape checked where given."""
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.int32:
+    if _int32 is None:
+        _load_dtypes()
+    if t.dtype is not _int32:
         raise QnreError(1, f"{where}: expected int32")
-    if shape and tuple(t.shape) != shape:
+    if shape and t.shape != shape:
         raise QnreError(1, f"{where}: expected shape {list(shape)}")
-    return _contig(t, where)
+    if not t.is_contiguous():
+        raise QnreError(1, f"{where}: tensor must be contiguous")
+    return t.data_ptr()
 
 
 def _f32(where: str, t, *shape):
-    import torch
-    if t.dtype != torch.float32:
+    if _int32 is None:
+        _load_dtypes()
+    if t.dtype is not _float32:
         raise QnreError(1, f"{where}: expected float32")
-    if shape and tuple(t.shape) != shape:
+    if shape and t.shape != shape:
         raise QnreError(1, f"{where}: expected shape {list(shape)}")
-    return _contig(t, where)
+    if not t.is_contiguous():
+        raise QnreError(1, f"{where}: tensor must be contiguous")
+    return t.data_ptr()
 
 
 def _weight(where: str, w, like):
@@ -598,22 +616,21 @@ def qnre_cache_copy_pages(cache: PagedCache, src, dst, stream=None) -> None:
 
 
 def _norm_inputs(where: str, q, k, q_norm_w, k_norm_w, cos_sin, positions):
-    tq, tk = _tensor4(q), _tensor4(k)
     if cos_sin.dim() != 2:
         raise QnreError(1, f"{where}: cos_sin must be [n_pos, rot]")
-    head = (ctypes.byref(tq), ctypes.byref(tk), _weight(where, q_norm_w, q), _weight(where, k_norm_w, k),
-            _f32(where, cos_sin), cos_sin.shape[0], cos_sin.shape[1])
-    return (tq, tk), head, _i32(where, positions, q.shape[0], q.shape[1])
+    n_pos, rot = cos_sin.shape
+    head = (_tensor4(q), _tensor4(k), _weight(where, q_norm_w, q), _weight(where, k_norm_w, k), _f32(where, cos_sin),
+            n_pos, rot)
+    return head, _i32(where, positions, *q.shape[:2])
 
 
 def qnre_qk_norm_rope(q, k, q_norm_w, k_norm_w, cos_sin, positions, q_out, k_out, rope_style: str = "rotate_half",
                       stream=None) -> None:
     """Per-head RMSNorm and rotation of q [B, S, Hq, D] and k [B, S, Hk, D] (views; in place allowed)."""
     where = "qnre_qk_norm_rope"
-    keep, head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
-    oq, ok = _tensor4(q_out), _tensor4(k_out)
-    _check(load_library().qnre_qk_norm_rope(*head, ROPE_STYLES.get(rope_style, -1), pos, ctypes.byref(oq),
-                                            ctypes.byref(ok), _stream_ptr(stream)), where)
+    head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
+    _check(load_library().qnre_qk_norm_rope(*head, ROPE_STYLES.get(rope_style, -1), pos, _tensor4(q_out),
+                                            _tensor4(k_out), _stream_ptr(stream)), where)
 
 
 def qk_norm_rope_workspace(q, k=None):
@@ -629,12 +646,10 @@ def qnre_qk_norm_rope_backward(gq, gk, q, k, q_norm_w, k_norm_w, cos_sin, positi
                                workspace, rope_style: str = "rotate_half", stream=None) -> None:
     """Gradient of qnre_qk_norm_rope: dq, dk (input dtype) and the fp32 weight gradients."""
     where = "qnre_qk_norm_rope_backward"
-    keep, head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
-    tgq, tgk, tdq, tdk = _tensor4(gq), _tensor4(gk), _tensor4(dq), _tensor4(dk)
+    head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
     D = q.shape[-1]
     _check(load_library().qnre_qk_norm_rope_backward(
-        ctypes.byref(tgq), ctypes.byref(tgk), *head, ROPE_STYLES.get(rope_style, -1), pos, ctypes.byref(tdq),
-        ctypes.byref(tdk), _f32(where, dq_norm_w, D), _f32(where, dk_norm_w, D), _contig(workspace, where),
+        _tensor4(gq), _tensor4(gk), *head, ROPE_STYLES.get(rope_style, -1), pos, _tensor4(dq), _tensor4(dk), _f32(where, dq_norm_w, D), _f32(where, dk_norm_w, D), _contig(workspace, where),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
 
 
@@ -642,12 +657,10 @@ def qnre_qkv_norm_rope_append(q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q
                               rows, counts=None, rope_style: str = "rotate_half", stream=None) -> None:
     """qnre_qk_norm_rope of the rows' new tokens [n, S, ...]; k and v go into the cache behind seq_lens."""
     where = "qnre_qkv_norm_rope_append"
-    keep, head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
-    tv, oq = _tensor4(v), _tensor4(q_out)
+    head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
     n = q.shape[0]
     _check(load_library().qnre_qkv_norm_rope_append(
-        head[0], head[1], ctypes.byref(tv), *head[2:], ROPE_STYLES.get(rope_style, -1), pos, ctypes.byref(oq),
-        cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)
+        head[0], head[1], _tensor4(v), *head[2:], ROPE_STYLES.get(rope_style, -1), pos, _tensor4(q_out), cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)
 
 
 def qnre_tree_masks(parents, masks=None, depths=None, stream=None) -> None:
@@ -675,18 +688,19 @@ def qnre_tree_attention(q, cache: PagedCache, layer: int, rows, mask, out, lse=N
                         workspace=None, stream=None) -> None:
     """Attention of drafted nodes q [n, nodes, Hq, D] over their rows' tokens and the nodes of mask (int64 [n, nodes];
     None: a chain) into out (contiguous); scale defaults to 1/sqrt(D)."""
-    import torch
     where = "qnre_tree_attention"
     tq = _tensor4(q)
     n, nodes, heads, dim = q.shape
     if out.shape != q.shape or out.dtype != q.dtype:
         raise QnreError(1, f"{where}: out must be contiguous, of q's shape and dtype")
-    if mask is not None and (mask.dtype != torch.int64 or tuple(mask.shape) != (n, nodes)):
+    if _int64 is None:
+        _load_dtypes()
+    if mask is not None and (mask.dtype is not _int64 or mask.shape != (n, nodes)):
         raise QnreError(1, f"{where}: mask must be int64 [n, nodes]")
     if workspace is None:
         raise QnreError(1, f"{where}: workspace is missing (tree_attention_workspace)")
     _check(load_library().qnre_tree_attention(
-        ctypes.byref(tq), cache.handle, layer, _i32(where, rows, n), None if mask is None else _contig(mask, where),
+        tq, cache.handle, layer, _i32(where, rows, n), None if mask is None else _contig(mask, where),
         _i32(where, counts, n), dim ** -0.5 if scale is None else scale, _contig(out, where),
         None if lse is None else _f32(where, lse, n, nodes, heads), _contig(workspace, where),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
@@ -696,8 +710,9 @@ def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sampl
                      node_counts=None, stream=None) -> None:
     """Walk drafted trees against target_probs [n, nodes, V] (fp32; draft_probs alike or None) with given random
     numbers; fills path [n, nodes], counts [n] and next_token [n] (int32)."""
-    import torch
     where = "qnre_verify_tree"
+    if _float32 is None:
+        _load_dtypes()
     if target_probs.dim() != 3:
         raise QnreError(1, f"{where}: target_probs must be [n, nodes, vocab]")
     n, nodes, vocab = target_probs.shape
@@ -706,7 +721,7 @@ def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sampl
         if t is None:
             rows += [None, 0, 0]
             continue
-        if t.dtype != torch.float32 or t.shape != target_probs.shape or (t.stride(2) != 1 and vocab > 1):
+        if t.dtype is not _float32 or t.shape != target_probs.shape or (t.stride(2) != 1 and vocab > 1):
             raise QnreError(1, f"{where}: probabilities are float32 [n, nodes, vocab], each row contiguous")
         rows += [t.data_ptr(), t.stride(0), t.stride(1)]
     _check(load_library().qnre_verify_tree(

@@ -3,15 +3,16 @@
 //
 //   o = sum_x p_x v_x,  p = softmax(scale q.k_x) over the tokens a node sees
 //
-// Work is cut into units (request, K head, 128 rows of (node, query head of the group)) and
-// each unit into tiles of 128 cached tokens; the concatenated tiles of all units are dealt out
-// in equal consecutive runs, one to a CTA, so batches of any raggedness load every
-// SM alike.  Each CTA takes the lengths from device memory and finds its own run.  A unit that spans
+// Work is cut into units (request, K head, up to 128 rows of (node, query head of the group)) and
+// each unit into tiles of 128 cached tokens; the concatenated tiles of all units, with a fixed cost
+// for each unit's start and end, are dealt out in equal consecutive runs, one to a CTA, so batches
+// of any raggedness load every SM alike.  Each CTA takes the lengths from device memory and finds its own run.  A unit that spans
 // CTAs leaves an unnormalised (m, l, O) in the workspace from each, joined by combine_kernel in
 // CTA order: the result depends on the lengths alone, never on timing.
 //
 // In a CTA: warp 4 brings K and V tiles by TMA into a ring (a page's tokens of one head are one
-// run of memory; boxes of the largest power of two that divides the page); warp 5's
+// run of memory; boxes of the largest power of two that divides the page) and the next unit's Q
+// rows into one of two buffers; warp 5's
 // one thread issues tcgen05.mma: S = Q K^T (both operands in shared memory, fp32 S in
 // tensor memory, two buffers) and O += P V (P from tensor memory); warps 0-3 own one S row a thread:
 // one pass with a running maximum and sum in base 2, P rounded to the inputs' type
@@ -53,16 +54,15 @@ constexpr int kThreads = 192;  // 4 softmax warps, the TMA warp, the MMA warp
 constexpr int kMaxCtas = 152;  // one a SM
 constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D, P 2 x 64
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
+constexpr int kUnitCost = 2;  // a unit's start and end, in tiles
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that O is rescaled at
 
 struct Desc {  // a unit that spans CTAs, written by its second CTA for combine_kernel
-  int valid, req, kvh, rt, c0, c1, slot0, pad;
+  int valid, req, kvh, rt, c0, c1, pad[2];
 };
 
 struct AttnArgs {
-  CUtensorMap tk, tv;
-  const char* q;
-  long long q_sb, q_ss, q_sh;
+  CUtensorMap tk, tv, tq;
   CacheView c;
   const int32_t* rows;
   const int32_t* counts;
@@ -73,15 +73,15 @@ struct AttnArgs {
   float* part_ml;  // [2 * kMaxCtas][128][2]: maximum (base 2), sum
   float* part_o;   // [2 * kMaxCtas][128][D]
   float scale_log2;
-  int layer, n, nodes, Hq, Hk, G, unit_rows, row_tiles, box;
+  int layer, n, nodes, Hq, Hk, G, unit_nodes, row_tiles, box;
 };
 
 template <int D>
 struct Smem {
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kStages = D == 128 ? 4 : 9;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kQ = 0;
-  static constexpr int kRing = kTileBytes;
+  static constexpr int kQ = 0;                                    // two buffers
+  static constexpr int kRing = 2 * kTileBytes;
   static constexpr int kJoin = kRing + kStages * kTileBytes;      // float [128][33]
   static constexpr int kMl = kJoin + 128 * 33 * 4;                // float [128][2]
   static constexpr int kPre = kMl + 128 * 2 * 4;                  // int [QNRE_MAX_CALL_ROWS + 1]
@@ -91,7 +91,7 @@ struct Smem {
 };
 
 struct Bars {
-  uint32_t full, empty, sfull, sfree, pready, pvdone, qready, ofree, drain;
+  uint32_t full, empty, qfull, qempty, sfull, sfree, pready, pvdone, ofree, drain;
 };
 
 // One unit's part of a CTA's run.
@@ -104,25 +104,30 @@ struct Seg {
 struct Cursor {
   const int* pre;
   const int2* lens;
-  int cur, end, start, req, units, row_tiles;
+  int cur, end, req, row_tiles;
   __device__ __forceinline__ static int tiles_of(int total) { return total > 0 ? (total + kTile - 1) / kTile : 1; }
   __device__ __forceinline__ bool next(Seg& s) {
-    if (cur >= end) return false;
-    while (cur >= pre[req + 1]) ++req;
-    s.req = req;
-    s.len = lens[req].x;
-    s.total = lens[req].y;
-    const int tiles = tiles_of(s.total);
-    const int off = cur - pre[req];
-    const int unit = off / tiles;
-    s.kvh = unit / row_tiles;
-    s.rt = unit - s.kvh * row_tiles;
-    s.t0 = off - unit * tiles;
-    s.t1 = min(tiles, s.t0 + end - cur);
-    s.whole = s.t0 == 0 && s.t1 == tiles;
-    s.slot = 2 * static_cast<int>(blockIdx.x) + (cur > start ? 1 : 0);
-    cur += s.t1 - s.t0;
-    return true;
+    while (cur < end) {
+      while (cur >= pre[req + 1]) ++req;
+      s.req = req;
+      s.len = lens[req].x;
+      s.total = lens[req].y;
+      const int tiles = tiles_of(s.total), per = tiles + kUnitCost;
+      const int off = cur - pre[req];
+      const int unit = off / per, o = off - unit * per;
+      const int take = min(per - o, end - cur);
+      cur += take;
+      s.t0 = max(0, o - kUnitCost);
+      s.t1 = max(0, o + take - kUnitCost);
+      if (s.t0 == s.t1) continue;  // the unit's cost falls to this CTA, its tiles to the next
+      s.kvh = unit / row_tiles;
+      s.rt = unit - s.kvh * row_tiles;
+      s.whole = s.t0 == 0 && s.t1 == tiles;
+      // a CTA goes on with one unit at most, and leaves one unfinished at most
+      s.slot = 2 * static_cast<int>(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
+      return true;
+    }
+    return false;
   }
 };
 
@@ -226,7 +231,7 @@ __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const void* tmap,
 }
 
 // ------------------------------------------------------------------ TMA warp
-template <int D>
+template <int D, int REP>
 __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem, Cursor cur,
                              volatile uint32_t* abort_flag) {
   using L = Smem<D>;
@@ -235,11 +240,28 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
   const int chunks = kTile / a.box;
   const int chunk = lane / kHalves, half = lane % kHalves;
   const bool active = chunk < chunks;
+  const int q_nodes = min(a.unit_nodes, a.nodes);
+  const uint32_t q_bytes = static_cast<uint32_t>(REP * D * 2 * a.G * q_nodes);
   uint32_t r = 0;
+  auto settle = [] {  // stop: what is in flight lands in microseconds; the kernel's end waits for it
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (ptx::global_timer_ns() - t0 < 50000) {
+    }
+  };
   Seg s;
-  while (cur.next(s)) {
+  for (uint32_t seg = 0; cur.next(s); ++seg) {
     const int row = a.rows[s.req];
     const bool row_ok = row >= 0 && row < a.c.rows;
+    {  // the unit's Q rows, REP times
+      const uint32_t buf = seg & 1u;
+      if (!wait(bars.qempty + 8 * buf, ((seg >> 1) & 1u) ^ 1u, abort_flag, a.c.status)) return settle();
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bars.qfull + 8 * buf, q_bytes);
+      __syncwarp();
+      if (lane < REP * kHalves)
+        tma_load_4d(smem + L::kQ + buf * L::kTileBytes + (lane % kHalves) * (kTile * 128) +
+                        (lane / kHalves) * (kTile / REP) * 128,
+                    &a.tq, bars.qfull + 8 * buf, (lane % kHalves) * 64, s.kvh * a.G, s.rt * a.unit_nodes, s.req);
+    }
     for (int t = s.t0; t < s.t1; ++t) {
       const int pos = t * kTile + chunk * a.box;
       int page = a.layer * a.c.pages;
@@ -252,13 +274,7 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
       }
       for (int kv = 0; kv < 2; ++kv, ++r) {
         const uint32_t slot = r % L::kStages, ph = (r / L::kStages) & 1u;
-        if (!wait(bars.empty + 8 * slot, ph ^ 1u, abort_flag, a.c.status)) {
-          // stop: what is in flight settles in microseconds; the kernel's end waits for it
-          const uint64_t t0 = ptx::global_timer_ns();
-          while (ptx::global_timer_ns() - t0 < 50000) {
-          }
-          return;
-        }
+        if (!wait(bars.empty + 8 * slot, ph ^ 1u, abort_flag, a.c.status)) return settle();
         if (lane == 0) ptx::mbar_arrive_expect_tx(bars.full + 8 * slot, L::kTileBytes);
         __syncwarp();
         if (active)
@@ -278,15 +294,14 @@ __device__ void run_mma(const AttnArgs& a, const Bars& bars, uint32_t smem, uint
   constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t kIdescO = (1u << 4) | kFmt | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
   uint32_t g = 0;  // tiles of the run
-  uint32_t seg = 0;
-  Seg s;
   bool ok = true;
 
-  auto pv = [&](uint32_t x, bool first) {
+  // O += P V of tile x, the first of segment `seg` or a later one
+  auto pv = [&](uint32_t x, bool first, uint32_t seg) {
     const uint32_t b = x & 1u, ring = 2 * x + 1;
     const uint32_t slot = ring % L::kStages;
-    ok = ok && wait(bars.pready + 8 * b, (x >> 1) & 1u, abort_flag, a.c.status);
     ok = ok && wait(bars.full + 8 * slot, (ring / L::kStages) & 1u, abort_flag, a.c.status);
+    ok = ok && wait(bars.pready + 8 * b, (x >> 1) & 1u, abort_flag, a.c.status);
     if (first) ok = ok && wait(bars.ofree, (seg & 1u) ^ 1u, abort_flag, a.c.status);
     if (!ok) return;
     ptx::tc_fence_after_sync();
@@ -295,12 +310,17 @@ __device__ void run_mma(const AttnArgs& a, const Bars& bars, uint32_t smem, uint
     for (int kk = 0; kk < kTile / 16; ++kk)
       umma_f16_ts(tmem + kTmemO, tmem + kTmemP + b * 64 + kk * 8,
                   ptx::smem_desc_sw128(v + kk * 2048, kTile * 128, 1024), kIdescO, (!first || kk > 0) ? 1u : 0u);
-    ptx::umma_commit(bars.empty + 8 * slot);
     ptx::umma_commit(bars.pvdone + 8 * b);
+    ptx::umma_commit(bars.empty + 8 * slot);
   };
 
+  // S of tile g goes before O of tile g - 1, across units too: the tensor core is never behind the softmax
+  bool first = false;
+  uint32_t seg = 0;
+  Seg s;
   for (; ok && cur.next(s); ++seg) {
-    ok = wait(bars.qready, seg & 1u, abort_flag, a.c.status);
+    const uint32_t q = smem + L::kQ + (seg & 1u) * L::kTileBytes;
+    ok = wait(bars.qfull + 8 * (seg & 1u), (seg >> 1) & 1u, abort_flag, a.c.status);
     for (int t = s.t0; ok && t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u, ring = 2 * g;
       const uint32_t slot = ring % L::kStages;
@@ -308,7 +328,7 @@ __device__ void run_mma(const AttnArgs& a, const Bars& bars, uint32_t smem, uint
            wait(bars.sfree + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
       if (!ok) break;
       ptx::tc_fence_after_sync();
-      const uint32_t k = smem + L::kRing + slot * L::kTileBytes, q = smem + L::kQ;
+      const uint32_t k = smem + L::kRing + slot * L::kTileBytes;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
@@ -317,10 +337,12 @@ __device__ void run_mma(const AttnArgs& a, const Bars& bars, uint32_t smem, uint
       }
       ptx::umma_commit(bars.sfull + 8 * b);
       ptx::umma_commit(bars.empty + 8 * slot);
-      if (t > s.t0) pv(g - 1, t - 1 == s.t0);
+      if (t + 1 == s.t1) ptx::umma_commit(bars.qempty + 8 * (seg & 1u));
+      if (g > 0) pv(g - 1, first, t == s.t0 ? seg - 1 : seg);
+      first = t == s.t0;
     }
-    if (ok) pv(g - 1, s.t1 - 1 == s.t0);
   }
+  if (ok && g > 0) pv(g - 1, first, seg - 1);
   if (!ok) {
     ptx::umma_commit(bars.drain);
     const uint64_t t0 = ptx::global_timer_ns();
@@ -330,18 +352,89 @@ __device__ void run_mma(const AttnArgs& a, const Bars& bars, uint32_t smem, uint
 }
 
 // ------------------------------------------------------------------ softmax warps
+// Packed pairs of floats (one instruction for two).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Bits of the 32 tokens from d0 on (relative to the row's length) that a row sees: the context, then `bits`.
+__device__ __forceinline__ uint32_t seen_word(int d0, uint64_t bits) {
+  if (d0 <= -32) return 0xFFFFFFFFu;
+  if (d0 < 0) return (1u << -d0) - 1u | static_cast<uint32_t>(bits << -d0);
+  return d0 < 64 ? static_cast<uint32_t>(bits >> d0) : 0u;
+}
+
+// x + the non-finite elements in column c of V over the drafts in `seen` (all below slot `last`).
+template <bool BF16>
+__device__ __noinline__ float add_nonfinite(const AttnArgs& a, int row, int kvh, int len, int first, int last,
+                                            uint64_t seen, int c, float x) {
+  for (; seen != 0; seen &= seen - 1) {
+    const int pos = len + __ffsll(static_cast<long long>(seen)) - 1;
+    if (pos < first || pos >= last) continue;
+    const int page = a.c.page_of(row, pos);
+    if (page < 0) continue;
+    const uint16_t w = *reinterpret_cast<const uint16_t*>(a.c.v + a.c.token_offset(a.layer, page, kvh, pos) + c * 2);
+    if (nonfinite_mask<BF16>(w) & 0xFFFFu) x += to_float<BF16>(w);
+  }
+  return x;
+}
+
+// This thread's V row of a tile past the context: slots without a token are zeroed; in drafted ones the non-finite
+// elements are, and true is returned.
+template <int D, bool BF16>
+__device__ __noinline__ bool clean_v_row(char* row, bool token) {
+  bool found = false;
+#pragma unroll 4
+  for (int i = 0; i < D / 8; ++i) {
+    uint4* at = reinterpret_cast<uint4*>(row + (i / 8) * (kTile * 128) + (i % 8) * 16);
+    if (!token) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 w = *at;
+    const uint4 z = make_uint4(nonfinite_mask<BF16>(w.x), nonfinite_mask<BF16>(w.y), nonfinite_mask<BF16>(w.z),
+                               nonfinite_mask<BF16>(w.w));
+    if (z.x | z.y | z.z | z.w) {
+      found = true;
+      *at = make_uint4(w.x & ~z.x, w.y & ~z.y, w.z & ~z.z, w.w & ~z.w);
+    }
+  }
+  ptx::fence_proxy_async_smem();
+  return found;
+}
+
 template <int D, bool BF16, int REP>
 __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base, uint32_t smem, uint32_t tmem,
                             Cursor cur, volatile uint32_t* abort_flag, unsigned long long* bad_nodes) {
   using L = Smem<D>;
   constexpr int kCols = kTile / REP;   // tokens of a tile this thread looks at
   constexpr int kRows = 128 / REP;     // unit rows
-  constexpr int kVecs = D / 8;         // 16-byte pieces of a row
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int ur = tid % kRows, copy = tid / kRows, c0 = copy * kCols;
   const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
   float* join = reinterpret_cast<float*>(smem_base + L::kJoin);
   float* ml = reinterpret_cast<float*>(smem_base + L::kMl);
+  const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
 
   if (REP > 1) {  // P outside this copy's tokens stays zero
     uint32_t zero[32];
@@ -351,44 +444,24 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
     for (int c = 0; c < 128; c += 32) tmem_st_x32(tmem + lane_base + kTmemP + c, zero);
     tmem_st_wait();
   }
-
-  // what unit row r of segment s sees of the drafts; false when it is no row or a node past the count
-  auto row_bits = [&](const Seg& s, int r, int& node, int& head, uint64_t& bits) -> bool {
-    const int R = s.rt * kTile + r;
-    node = R / a.G;
-    head = s.kvh * a.G + R - node * a.G;
-    bits = 0;
-    if (R >= a.unit_rows) return false;
-    const int cnt = a.counts != nullptr ? min(max(a.counts[s.req], 0), a.nodes) : a.nodes;
-    if (node >= cnt) return false;
-    bits = a.mask != nullptr ? a.mask[static_cast<long long>(s.req) * a.nodes + node] : (2ull << node) - 1;
-    const int drafts = s.total - s.len;  // slots that exist
-    if (drafts < 64) bits &= (1ull << drafts) - 1;
-    return true;
-  };
+  const int ur_node = ur / a.G, ur_head = ur - ur_node * a.G;
 
   uint32_t g = 0;
   Seg s;
   while (cur.next(s)) {
-    int node, head;
-    uint64_t bits;
-    const bool row_ok = row_bits(s, ur, node, head, bits);
-    {  // Q row -> shared memory, K-major with the 128-byte swizzle
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + s.req * a.q_sb + node * a.q_ss + head * a.q_sh);
-      uint4 v[kVecs];
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) v[i] = row_ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        *reinterpret_cast<uint4*>(smem_base + L::kQ + (i / 8) * (kTile * 128) + tid * 128 +
-                                  (((i % 8) ^ (tid & 7)) * 16)) = v[i];
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(bars.qready);
+    const int node = s.rt * a.unit_nodes + ur_node, head = s.kvh * a.G + ur_head;
+    const bool in_out = ur_node < a.unit_nodes && node < a.nodes;  // a row of the output
+    bool row_ok = in_out;                                          // and of a node that sees anything
+    uint64_t bits = 0;
+    if (in_out) {
+      if (a.counts != nullptr) row_ok = node < a.counts[s.req];
+      bits = a.mask != nullptr ? a.mask[static_cast<long long>(s.req) * a.nodes + node] : (2ull << node) - 1;
+      const int drafts = s.total - s.len;  // slots that exist
+      if (drafts < 64) bits &= (1ull << drafts) - 1;
     }
     float m = -INFINITY, l = 0.f;
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
-      const int x0 = t * kTile + c0;
       uint32_t v[kCols / 32][32];
       wait(bars.sfull + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status);
       __syncwarp();  // the tensor-memory instructions are warp-wide
@@ -404,22 +477,24 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       if (lane == 0) ptx::mbar_arrive(bars.sfree + 8 * b);
 
       const bool tail = (t + 1) * kTile > s.len;
-      if (tail || !row_ok) {
+      if (tail) {
 #pragma unroll
-        for (int j = 0; j < kCols / 32; ++j)
+        for (int j = 0; j < kCols / 32; ++j) {
+          const uint32_t see = seen_word(t * kTile + c0 + 32 * j - s.len, bits);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int d = x0 + 32 * j + i - s.len;
-            const bool see = row_ok && (d < 0 || (d < 64 && ((bits >> d) & 1)));
-            if (!see) v[j][i] = 0xFF800000u;
-          }
+          for (int i = 0; i < 32; ++i)
+            if (!(see & (1u << i))) v[j][i] = 0xFF800000u;
+        }
       }
-      float mx = -INFINITY;
+      float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
       for (int j = 0; j < kCols / 32; ++j)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[j][i]));
-      mx *= a.scale_log2;
+        for (int i = 0; i < 32; i += 4) {
+          mx0 = max3(mx0, __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
+          mx1 = max3(mx1, __uint_as_float(v[j][i + 2]), __uint_as_float(v[j][i + 3]));
+        }
+      const float mx = fmaxf(mx0, mx1) * a.scale_log2;
       const bool grow = mx > m + kRescale;
       if (t == s.t0) {
         m = mx;
@@ -431,7 +506,7 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         const float f = grow ? exp2_fast(m - mx) : 1.f;
         if (grow) m = mx;
         l *= f;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
@@ -444,17 +519,24 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         tmem_st_wait();
       }
       const float ms = m == -INFINITY ? 0.f : m;
+      const uint64_t neg = pair(-ms, -ms);
       uint32_t p[kCols / 2];
-      float sum0 = 0.f, sum1 = 0.f;
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) {
-        const float e0 = exp2_fast(fmaf(__uint_as_float(v[i / 16][(2 * i) % 32]), a.scale_log2, -ms));
-        const float e1 = exp2_fast(fmaf(__uint_as_float(v[i / 16][(2 * i + 1) % 32]), a.scale_log2, -ms));
-        sum0 += e0;
-        sum1 += e1;
+        float e0, e1;
+        unpair(fma2(pair(__uint_as_float(v[i / 16][(2 * i) % 32]), __uint_as_float(v[i / 16][(2 * i + 1) % 32])), scale2,
+                    neg), e0, e1);
+        e0 = exp2_fast(e0);
+        e1 = exp2_fast(e1);
+        sum[i & 1] = add2(sum[i & 1], pair(e0, e1));
         p[i] = pack2<BF16>(e0, e1);
       }
-      l += sum0 + sum1;
+      {
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+      }
       // P's buffer is free once the product two tiles back is done
       wait(bars.pvdone + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
       __syncwarp();
@@ -472,27 +554,9 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         const uint32_t ring = 2 * g + 1, slot = ring % L::kStages;
         wait(bars.full + 8 * slot, (ring / L::kStages) & 1u, abort_flag, a.c.status);
         const int pos = t * kTile + tid;
-        if (pos >= s.len) {
-          bool found = false;
-#pragma unroll
-          for (int i = 0; i < kVecs; ++i) {
-            uint4* at = reinterpret_cast<uint4*>(smem_base + L::kRing + slot * L::kTileBytes + (i / 8) * (kTile * 128) +
-                                                 tid * 128 + (i % 8) * 16);
-            if (pos >= s.total) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else {
-              uint4 w = *at;
-              const uint4 z = make_uint4(nonfinite_mask<BF16>(w.x), nonfinite_mask<BF16>(w.y),
-                                         nonfinite_mask<BF16>(w.z), nonfinite_mask<BF16>(w.w));
-              if (z.x | z.y | z.z | z.w) {
-                found = true;
-                *at = make_uint4(w.x & ~z.x, w.y & ~z.y, w.z & ~z.z, w.w & ~z.w);
-              }
-            }
-          }
-          if (found) atomicOr(bad_nodes, 1ull << (pos - s.len));
-          ptx::fence_proxy_async_smem();
-        }
+        if (pos >= s.len &&
+            clean_v_row<D, BF16>(smem_base + L::kRing + slot * L::kTileBytes + tid * 128, pos < s.total))
+          atomicOr(bad_nodes, 1ull << (pos - s.len));
         __syncwarp();
       }
       tmem_st_wait();
@@ -500,154 +564,103 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bars.pready + 8 * b);
     }
+    if (!row_ok) {  // nothing seen: its scores were those of some other row's place
+      m = -INFINITY;
+      l = 0.f;
+    }
 
     // ---------------- the segment's result
+    if (REP > 1) {
+      ml[2 * tid] = m;
+      ml[2 * tid + 1] = l;
+    }
+    const bool drafts = s.t1 * kTile > s.len;
+    if (REP > 1 || drafts) named_sync();
     const uint32_t last = g - 1;
     wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
     __syncwarp();
     ptx::tc_fence_after_sync();
-    unsigned long long bad = 0;
-    if (s.t1 * kTile > s.len) {
-      named_sync();
-      bad = *bad_nodes;
-      named_sync();
-      if (tid == 0 && bad != 0) *bad_nodes = 0;
+    const uint64_t bad = drafts && row_ok ? *bad_nodes & bits : 0;
+    float f = 1.f;  // of this copy's part
+    if (REP > 1) {
+      float M = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < REP; ++c) M = fmaxf(M, ml[2 * (c * kRows + ur)]);
+#pragma unroll
+      for (int c = 0; c < REP; ++c) {
+        const float mc = ml[2 * (c * kRows + ur)];
+        sum += ml[2 * (c * kRows + ur) + 1] * (mc == -INFINITY ? 0.f : exp2_fast(mc - M));
+      }
+      f = m == -INFINITY ? 0.f : exp2_fast(m - M);
+      m = M;
+      l = sum;
     }
-    // non-finite V elements of the drafts a row sees
-    auto add_bad = [&](uint64_t seen, int c, float x) -> float {
-      const int row = a.rows[s.req];
-      for (uint64_t todo = seen; todo != 0; todo &= todo - 1) {
-        const int pos = s.len + __ffsll(static_cast<long long>(todo)) - 1;
-        if (pos < s.t0 * kTile || pos >= s.t1 * kTile) continue;
-        const int page = a.c.page_of(row, pos);
-        if (page < 0) continue;
-        const uint16_t w = *reinterpret_cast<const uint16_t*>(a.c.v + a.c.token_offset(a.layer, page, s.kvh, pos) + c * 2);
-        if (nonfinite_mask<BF16>(w) & 0xFFFFu) x += to_float<BF16>(w);
-      }
-      return x;
-    };
-
-    if (REP == 1) {
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-      const long long orow = (static_cast<long long>(s.req) * a.nodes + node) * a.Hq + head;
-      const bool store = s.rt * kTile + ur < a.unit_rows;
-      const long long prow = static_cast<long long>(s.slot) * 128 + ur;
+    const float inv = !s.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
+    const long long orow = (static_cast<long long>(s.req) * a.nodes + node) * a.Hq + head;
+    const long long prow = static_cast<long long>(s.slot) * 128 + ur;
+    constexpr int kPer = 32 / REP;  // columns of a block of 32 this thread writes, from jc on
+    const int jc = copy * kPer;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
-        ptx::tmem_ld_wait();
-        tmem_fence_regs(o);
-        if (row_ok && (bad & bits) != 0) {
-#pragma unroll 1
-          for (int i = 0; i < 32; ++i) join[tid * 33 + i] = add_bad(bad & bits, c + i, 0.f);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + join[tid * 33 + i]);
-        }
-        if (store && s.whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c) * 2);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack2<BF16>(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (store) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
+      ptx::tmem_ld_wait();
+      tmem_fence_regs(o);
+      if (c + 32 == D) {
+        ptx::tc_fence_before_sync();
         __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars.ofree);
       }
-      ptx::tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars.ofree);
-      if (store) {
-        if (s.whole) {
-          if (a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-        } else {
-          reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(m, l);
-        }
-      }
-    } else {
-      // the copies' common maximum and sum, then their O in blocks of 32 columns
-      ml[2 * tid] = m;
-      ml[2 * tid + 1] = l;
-      named_sync();
-      auto joined = [&](int r, float& M, float& Lsum) {
-        M = -INFINITY;
+      float x[kPer];
+      if (REP == 1) {
 #pragma unroll
-        for (int c = 0; c < REP; ++c) M = fmaxf(M, ml[2 * (c * kRows + r)]);
-        Lsum = 0.f;
-#pragma unroll
-        for (int c = 0; c < REP; ++c) {
-          const float mc = ml[2 * (c * kRows + r)];
-          Lsum += ml[2 * (c * kRows + r) + 1] * (mc == -INFINITY ? 0.f : exp2_fast(mc - M));
-        }
-      };
-      float M, Lsum;
-      joined(ur, M, Lsum);
-      const float f = m == -INFINITY ? 0.f : exp2_fast(m - M);
-      constexpr int kPer = 32 / REP;  // columns of a block this thread sums and writes
-      const int jr = tid / REP, jc = (tid % REP) * kPer;
-      int jnode, jhead;
-      uint64_t jbits;
-      const bool jok = row_bits(s, jr, jnode, jhead, jbits);
-      const bool store = s.rt * kTile + jr < a.unit_rows;
-      float jM, jL;
-      joined(jr, jM, jL);
-      const float inv = jL > 0.f ? 1.f / jL : (jL == 0.f ? 0.f : jL);
-      const long long orow = (static_cast<long long>(s.req) * a.nodes + jnode) * a.Hq + jhead;
-      const long long prow = static_cast<long long>(s.slot) * 128 + jr;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
-        ptx::tmem_ld_wait();
-        tmem_fence_regs(o);
-        if (c + 32 == D) {
-          ptx::tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bars.ofree);
-        }
+        for (int i = 0; i < kPer; ++i) x[i] = __uint_as_float(o[i]);
+      } else {  // the copies of a row lie in different warps
 #pragma unroll
         for (int i = 0; i < 32; ++i) join[tid * 33 + i] = __uint_as_float(o[i]) * f;
         named_sync();
-        float x[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           x[i] = 0.f;
 #pragma unroll
-          for (int k = 0; k < REP; ++k) x[i] += join[(k * kRows + jr) * 33 + jc + i];
-          if (jok && (bad & jbits) != 0) x[i] = add_bad(bad & jbits, c + jc + i, x[i]);
-        }
-        if (store) {
-          if (s.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c + jc) * 2);
-#pragma unroll
-            for (int i = 0; i < kPer / 8; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = pack2<BF16>(x[8 * i + 2 * e] * inv, x[8 * i + 2 * e + 1] * inv);
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c + jc);
-#pragma unroll
-            for (int i = 0; i < kPer / 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-          }
+          for (int k = 0; k < REP; ++k) x[i] += join[(k * kRows + ur) * 33 + jc + i];
         }
         named_sync();
       }
-      if (store && jc == 0) {
-        if (s.whole) {
-          if (a.lse != nullptr) a.lse[orow] = jL == 0.f ? -INFINITY : (jM + log2f(jL)) * 0.6931471805599453f;
-        } else {
-          reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(jM, jL);
-        }
+      if (bad != 0) {
+        const int row = a.rows[s.req];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          x[i] = add_nonfinite<BF16>(a, row, s.kvh, s.len, s.t0 * kTile, s.t1 * kTile, bad, c + jc + i, x[i]);
       }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = row_ok ? x[i] * inv : 0.f;
+      if (in_out && s.whole) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c + jc) * 2);
+#pragma unroll
+        for (int i = 0; i < kPer / 8; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = pack2<BF16>(x[8 * i + 2 * e], x[8 * i + 2 * e + 1]);
+          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else if (in_out) {
+        float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c + jc);
+#pragma unroll
+        for (int i = 0; i < kPer / 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      }
+      __syncwarp();
+    }
+    if (in_out && copy == 0) {
+      if (!s.whole)
+        reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(m, l);
+      else if (a.lse != nullptr)
+        a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+    if (drafts) {
+      named_sync();  // all have read it
+      if (tid == 0) *bad_nodes = 0;
+      named_sync();
     }
   }
 }
@@ -673,11 +686,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
     bars.full = take(L::kStages);
     bars.empty = take(L::kStages);
+    bars.qfull = take(2);
+    bars.qempty = take(2);
     bars.sfull = take(2);
     bars.sfree = take(2);
     bars.pready = take(2);
     bars.pvdone = take(2);
-    bars.qready = take(1);
     bars.ofree = take(1);
     bars.drain = take(1);
   }
@@ -690,17 +704,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       ptx::mbar_init(bars.empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bars.qfull + 8 * i, 1);
+      ptx::mbar_init(bars.qempty + 8 * i, 1);
       ptx::mbar_init(bars.sfull + 8 * i, 1);
       ptx::mbar_init(bars.sfree + 8 * i, 4);
       ptx::mbar_init(bars.pready + 8 * i, 4);
       ptx::mbar_init(bars.pvdone + 8 * i, 1);
     }
-    ptx::mbar_init(bars.qready, 128);
     ptx::mbar_init(bars.ofree, 4);
     ptx::mbar_init(bars.drain, 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&a.tk);
     ptx::prefetch_tensormap(&a.tv);
+    ptx::prefetch_tensormap(&a.tq);
   }
   // the rows' lengths, and the first tile of each request in the concatenated run
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -718,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     const int total = min(len + cnt, room);
     lens[i] = make_int2(len, total);
-    pre[i + 1] = Cursor::tiles_of(total) * units;
+    pre[i + 1] = (Cursor::tiles_of(total) + kUnitCost) * units;
   }
   __syncthreads();
   if (warp == 0) {
@@ -746,29 +762,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   cur.pre = pre;
   cur.lens = lens;
   cur.row_tiles = a.row_tiles;
-  cur.units = units;
-  cur.start = cur.cur = cta < ctas ? static_cast<int>(W * cta / ctas) : 0;
+  cur.cur = cta < ctas ? static_cast<int>(W * cta / ctas) : 0;
   cur.end = cta < ctas ? static_cast<int>(W * (cta + 1) / ctas) : 0;
   int lo = 0, hi = a.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (pre[mid] <= cur.start) lo = mid; else hi = mid - 1;
+    if (pre[mid] <= cur.cur) lo = mid; else hi = mid - 1;
   }
   cur.req = lo;
 
-  if (tid == 0) {  // this CTA begins inside a unit that the CTA before began: name it for the join
+  if (tid == 0) {  // this CTA goes on with a unit that the CTA before it began: name it for the join
     Desc d{};
-    if (cur.cur < cur.end) {
-      Cursor look = cur;
-      Seg s;
-      look.next(s);
-      const long long first = cur.start - s.t0;
-      const long long end = first + Cursor::tiles_of(s.total);
-      const int c0 = static_cast<int>(((first + 1) * ctas - 1) / W);
-      if (s.t0 > 0 && c0 == cta - 1) {
-        const int c1 = static_cast<int>((end * ctas - 1) / W);
-        d = Desc{1, s.req, s.kvh, s.rt, c0, c1, 2 * c0 + (first > W * c0 / ctas ? 1 : 0), 0};
-      }
+    Cursor look = cur;
+    Seg s;
+    if (look.next(s) && s.t0 > 0) {
+      const int tiles = Cursor::tiles_of(s.total);
+      const long long first = pre[s.req] + static_cast<long long>(s.kvh * a.row_tiles + s.rt) * (tiles + kUnitCost) + kUnitCost;
+      const int c0 = static_cast<int>(((first + 1) * ctas - 1) / W);  // who has its first and its last tile
+      const int c1 = static_cast<int>(((first + tiles) * ctas - 1) / W);
+      if (c0 == cta - 1) d = Desc{1, s.req, s.kvh, s.rt, c0, c1, {0, 0}};
     }
     a.desc[cta] = d;
   }
@@ -776,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (warp < 4) {
     run_softmax<D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &abort_word, &bad_nodes);
   } else if (warp == 4) {
-    run_producer<D>(a, bars, smem, cur, &abort_word);
+    run_producer<D, REP>(a, bars, smem, cur, &abort_word);
   } else if (lane == 0) {
     run_mma<D, BF16>(a, bars, smem, tmem, cur, &abort_word);
   }
@@ -793,17 +805,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 // Joins the parts of the units that span CTAs: block x is the unit's second CTA, a warp a row.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const float* part_ml, const float* part_o,
-                                                      char* out, float* lse, int nodes, int Hq, int G, int unit_rows) {
+                                                      char* out, float* lse, int nodes, int Hq, int G, int unit_nodes) {
   constexpr int kPer = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Desc d = desc[blockIdx.x];
   if (!d.valid) return;
   const int lane = threadIdx.x % 32, r = blockIdx.y * 8 + threadIdx.x / 32;
-  const int R = d.rt * kTile + r;
-  if (r >= kTile || R >= unit_rows) return;
+  const int node = d.rt * unit_nodes + r / G, head = d.kvh * G + r % G;
+  if (r >= unit_nodes * G || node >= nodes) return;
   const int parts = d.c1 - d.c0 + 1;
-  auto row_of = [&](int i) { return static_cast<long long>(i == 0 ? d.slot0 : 2 * (d.c0 + i)) * 128 + r; };
+  auto row_of = [&](int i) { return static_cast<long long>(2 * (d.c0 + i) + (i == 0 ? 1 : 0)) * 128 + r; };
   float M = -INFINITY;
   for (int i = lane; i < parts; i += 32) M = fmaxf(M, part_ml[2 * row_of(i)]);
 #pragma unroll
@@ -829,8 +841,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
     }
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  const int node = R / G;
-  const long long orow = (static_cast<long long>(d.req) * nodes + node) * Hq + d.kvh * G + (R - node * G);
+  const long long orow = (static_cast<long long>(d.req) * nodes + node) * Hq + head;
   uint32_t* dst = reinterpret_cast<uint32_t*>(out + (orow * D + lane * kPer) * 2);
 #pragma unroll
   for (int i = 0; i < kPer / 2; ++i) dst[i] = pack2<BF16>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
@@ -863,18 +874,19 @@ qnre_status_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, attention_kernel<D, BF16, REP>, a) != cudaSuccess) return QNRE_ERR_CUDA;
-  cfg.gridDim = dim3(ctas, (std::min(a.unit_rows, kTile) + 7) / 8);
+  cfg.gridDim = dim3(ctas, (std::min(a.nodes, a.unit_nodes) * a.G + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return from_cuda(cudaLaunchKernelEx(&cfg, combine_kernel<D, BF16>, static_cast<const Desc*>(a.desc),
                                       static_cast<const float*>(a.part_ml), static_cast<const float*>(a.part_o), a.out,
-                                      a.lse, a.nodes, a.Hq, a.G, a.unit_rows));
+                                      a.lse, a.nodes, a.Hq, a.G, a.unit_nodes));
 }
 
 template <int D, bool BF16>
 qnre_status_t launch_rep(const AttnArgs& a, int ctas, cudaStream_t stream) {
-  if (a.unit_rows <= 32) return launch_attention<D, BF16, 4>(a, ctas, stream);
-  if (a.unit_rows <= 64) return launch_attention<D, BF16, 2>(a, ctas, stream);
+  const int rows = std::min(a.nodes, a.unit_nodes) * a.G;
+  if (rows <= 32) return launch_attention<D, BF16, 4>(a, ctas, stream);
+  if (rows <= 64) return launch_attention<D, BF16, 2>(a, ctas, stream);
   return launch_attention<D, BF16, 1>(a, ctas, stream);
 }
 
@@ -904,6 +916,7 @@ qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* c
   if (own.dtype != cache->dtype || own.shape[3] != cache->head_dim || own.shape[2] % cache->heads != 0 || layer < 0 ||
       layer >= cache->layers || !(scale > 0.f) || !std::isfinite(scale))
     return QNRE_ERR_INVALID_ARG;
+  if (own.shape[2] / cache->heads > kTile) return QNRE_ERR_UNSUPPORTED;
   if (own.shape[1] > QNRE_MAX_NODES || own.shape[2] > 65535) return QNRE_ERR_CAPACITY;
   if (!rows_vectorisable(&own, 2)) return QNRE_ERR_ALIGNMENT;
   uint64_t need = 0;
@@ -931,15 +944,11 @@ qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* c
   a.Hq = static_cast<int>(own.shape[2]);
   a.Hk = cache->heads;
   a.G = a.Hq / a.Hk;
-  a.unit_rows = a.nodes * a.G;
-  a.row_tiles = (a.unit_rows + kTile - 1) / kTile;
-  const int64_t tiles = (static_cast<int64_t>(cache->max_blocks) * cache->page_size + kTile - 1) / kTile;
+  a.unit_nodes = kTile / a.G;
+  a.row_tiles = (a.nodes + a.unit_nodes - 1) / a.unit_nodes;
+  const int64_t tiles = (static_cast<int64_t>(cache->max_blocks) * cache->page_size + kTile - 1) / kTile + kUnitCost;
   if (a.n * tiles * a.Hk * a.row_tiles > 0x7FFFFFFF) return QNRE_ERR_CAPACITY;
   a.box = std::min(kTile, cache->page_size & -cache->page_size);
-  a.q = static_cast<const char*>(own.data);
-  a.q_sb = own.stride[0] * 2;
-  a.q_ss = own.stride[1] * 2;
-  a.q_sh = own.stride[2] * 2;
   a.rows = rows;
   a.counts = counts;
   a.mask = mask;
@@ -954,7 +963,12 @@ qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* c
   const uint64_t dims[4] = {D, ps, H, static_cast<uint64_t>(cache->layers) * cache->pages};
   const uint64_t strides[3] = {D * 2, ps * D * 2, H * ps * D * 2};
   const uint32_t box[4] = {64, static_cast<uint32_t>(a.box), 1, 1};
-  if (!encode_tiled_16bit(&a.tk, cache->k, bf16, 4, dims, strides, box) ||
+  const uint64_t q_dims[4] = {D, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.nodes), static_cast<uint64_t>(a.n)};
+  const uint64_t q_strides[3] = {static_cast<uint64_t>(own.stride[2]) * 2, static_cast<uint64_t>(own.stride[1]) * 2,
+                                 static_cast<uint64_t>(own.stride[0]) * 2};
+  const uint32_t q_box[4] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(std::min(a.nodes, a.unit_nodes)), 1};
+  if (!encode_tiled_16bit(&a.tq, own.data, bf16, 4, q_dims, q_strides, q_box) ||
+      !encode_tiled_16bit(&a.tk, cache->k, bf16, 4, dims, strides, box) ||
       !encode_tiled_16bit(&a.tv, cache->v, bf16, 4, dims, strides, box))
     return QNRE_ERR_CUDA;
   int dev = 0, sms = 0;
