@@ -6,11 +6,17 @@
 //   r = rsqrt(mean(y^2) + 1e-6),  n = y r w,  o = R n          (R: rotation by the token's angles)
 //   gradient:  t = R^T g,  h = y r,  dw = sum t h,  dy = r (t w - h mean(t w h))
 //
-// Bound: HBM (4 bytes an element forward, 6 backward).  A head row is D/8 lanes of 16
-// bytes; a warp takes one token and kHeads heads at a time, so the angles
-// and weights are read once into registers per work item, and all of an item's
-// loads are in flight before the first is used.  In 32-bit the pair of channels a
-// rotation mixes is one word-wise shuffle away (half-rotation) or in the same lane.
+// Bound: HBM (4 bytes an element forward, 6 backward), with the issue slots close behind: a row pair of
+// 512 bytes costs about 100 instructions of the 174 slots its bytes take.  A head row is D/8 lanes of 16
+// bytes; a warp takes one token's run of heads, so angles and weights sit in registers
+// (weights already times cosines and sines), the channel a rotation mixes in is four word
+// shuffles away (half-rotation) or in the same lane, and the arithmetic is on packed pairs of floats.
+// Measured on 32768 tokens of 72 heads, D = 128 bf16 (1.22 GB): plain floats 264 us at 155 instructions;
+// packed, four blocks of 256 threads a SM, 217; the first loads issued before the position's angles are
+// asked for, 209; one resident wave that strides over the items, 199 (three blocks 215, two 268; 128-thread
+// blocks 205; streaming stores +2 %).  The gradient (18881 tokens of 70 heads, fp16, 1.02 GB): 282 us
+// with plain loads, 209 with the next heads' loads in flight, 182 packed with all heads of a token in one
+// item; two blocks a SM (three 197, four spill: 272).
 #include "../../include/qnre.h"
 #include "cache.cuh"
 
@@ -54,36 +60,69 @@ struct NormArgs {
   float* partial;  // gradient: [kGradBlocks][2][D]
 };
 
-template <bool BF16>
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (BF16) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    } else {
-      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = p.x;
-      f[2 * i + 1] = p.y;
-    }
-  }
+// Eight 16-bit values as four packed pairs of floats; sm_103 has multiply-adds of such pairs.
+using Pairs = uint64_t[4];
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+__device__ __forceinline__ uint64_t unpack2(uint32_t w) {
+  if (BF16) return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pair(p.x, p.y);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(const uint4& u, Pairs& f) {
+  f[0] = unpack2<BF16>(u.x);
+  f[1] = unpack2<BF16>(u.y);
+  f[2] = unpack2<BF16>(u.z);
+  f[3] = unpack2<BF16>(u.w);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack(const Pairs& f) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    const float2 v = halves(f[i]);
     if (BF16) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     } else {
-      const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      const __half2 p = __floats2half2_rn(v.x, v.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The dot product of two lanes' eight channels, before the row's lanes are added.
+__device__ __forceinline__ float dot(const Pairs& a, const Pairs& b) {
+  uint64_t t = mul2(a[0], b[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) t = fma2(a[i], b[i], t);
+  const float2 v = halves(t);
+  return v.x + v.y;
 }
 
 template <int LANES>
@@ -94,22 +133,20 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 // One lane's share of a token's rotation: channel 8*l + e of the output is
-// c[e] n[e] + s[e] n'[e], n' the other channel of its pair (sign in s).  kRH: the
-// pair lies in lane `partner`, else in the neighbouring element.  Channels past `rot` have
-// c = 1, and their n' is taken as 0.
+// c[e] n[e] + s[e] n'[e], n' the other channel of its pair (sign in s).  Half-rotation: the
+// pair lies in lane `partner`, else in the neighbouring element.  Channels past the rotated ones have
+// c = 1, s = 0 and themselves for a pair.
 struct Angles {
   float c[8], s[8];
   int partner;
-  bool rotates;
 };
 
 template <bool RH, bool BACK>
 __device__ __forceinline__ Angles load_angles(const float* row, int rot, int l, int lane) {
   Angles a;
   const int half = rot / 2;
-  a.rotates = 8 * l < rot;
   a.partner = lane;
-  if (!a.rotates) {
+  if (8 * l >= rot) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       a.c[e] = 1.f;
@@ -145,38 +182,30 @@ __device__ __forceinline__ Angles load_angles(const float* row, int rot, int l, 
   return a;
 }
 
-// x' of the rotation for one head row held as `raw`; every lane of the warp takes part.
+// The pairs' other channels of one head row held as `raw`; every lane of the warp takes part.
 template <bool RH, bool BF16>
-__device__ __forceinline__ void pair_of(const uint4& raw, const float (&x)[8], const Angles& a, float (&y)[8]) {
+__device__ __forceinline__ void other_channels(const uint4& raw, const Angles& a, Pairs& y) {
+  uint4 o;
   if (RH) {
-    uint4 o;
     o.x = __shfl_sync(0xFFFFFFFFu, raw.x, a.partner);
     o.y = __shfl_sync(0xFFFFFFFFu, raw.y, a.partner);
     o.z = __shfl_sync(0xFFFFFFFFu, raw.z, a.partner);
     o.w = __shfl_sync(0xFFFFFFFFu, raw.w, a.partner);
-    unpack<BF16>(o, y);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+    o = make_uint4(__byte_perm(raw.x, 0, 0x1032), __byte_perm(raw.y, 0, 0x1032), __byte_perm(raw.z, 0, 0x1032),
+                   __byte_perm(raw.w, 0, 0x1032));
   }
-  if (!a.rotates) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = 0.f;
-  }
+  unpack<BF16>(o, y);
 }
 
-// The weights of a lane's channels and of the channels they are paired with.
-template <bool RH, bool BF16>
-__device__ __forceinline__ void load_weights(const void* w, int l, const Angles& a, float (&own)[8],
-                                             float (&pair)[8]) {
-  const uint4 raw = __ldg(static_cast<const uint4*>(w) + l);
-  unpack<BF16>(raw, own);
-  pair_of<RH, BF16>(raw, own, a, pair);
+__device__ __forceinline__ void pairs_of(const float (&f)[8], Pairs& p) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
 }
 
 // Forward.  Work item = (token, chunk of q, k or v heads); kAppend sends k and v to the cache.
 template <int D, bool BF16, bool RH, bool APPEND>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -220,37 +249,52 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         reinterpret_cast<uint4*>(out_row(h))[l] = reinterpret_cast<const uint4*>(in.row(b, s, h))[l];
       continue;
     }
+    // the first heads are on their way before the position and its angles are asked for
+    uint4 raw[kUnroll];
+    const char* src = in.row(b, s, h0 + sub) + 16 * l;
+    const long long src_step = in.sh * kRows;
+    auto load = [&](int h) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        raw[u] = h + u * kRows < h1 ? __ldcs(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+        src += src_step;
+      }
+    };
+    load(h0 + sub);
     if (a.positions != nullptr) pos = a.positions[token];
     const bool bad = pos < 0 || pos >= a.n_pos;
     const Angles ang = load_angles<RH, false>(a.cos_sin + (bad ? 0 : pos) * a.rot, a.rot, l, lane);
-    float w[8], wp[8];
-    load_weights<RH, BF16>(kind == 0 ? a.wq : a.wk, l, ang, w, wp);
+    Pairs w, wp;  // weights times cosines, the other channels' weights times sines
+    {
+      Pairs c, sn;
+      pairs_of(ang.c, c);
+      pairs_of(ang.s, sn);
+      const uint4 raw = __ldg(static_cast<const uint4*>(kind == 0 ? a.wq : a.wk) + l);
+      unpack<BF16>(raw, w);
+      other_channels<RH, BF16>(raw, ang, wp);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[e] *= ang.c[e];
-      wp[e] *= ang.s[e];
-    }
-    for (int hb = h0; hb < h1; hb += kRows * kUnroll) {
-      uint4 raw[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = hb + u * kRows + sub;
-        raw[u] = h < h1 ? __ldcs(reinterpret_cast<const uint4*>(in.row(b, s, h)) + l) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) {
+        w[i] = mul2(w[i], c[i]);
+        wp[i] = mul2(wp[i], sn[i]);
       }
+    }
+    char* dst = out_row(h0 + sub) + 16 * l;
+    const long long dst_step = (APPEND && kind != 0 ? static_cast<long long>(a.cache.page_size) * (D * 2)
+                                                    : (kind == 0 ? a.q_out : a.k_out).sh) * kRows;
+    for (int h = h0 + sub; h - sub < h1; h += kRows * kUnroll) {
+      if (h != h0 + sub) load(h);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int h = hb + u * kRows + sub;
-        float x[8], y[8], o[8];
+        Pairs x, y, o;
         unpack<BF16>(raw[u], x);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        float r = rsqrtf(row_sum<kLanes>(ss) * (1.0f / D) + kEps);
+        float r = rsqrtf(row_sum<kLanes>(dot(x, x)) * (1.0f / D) + kEps);
         if (bad) r = __uint_as_float(0x7FC00000u);
-        pair_of<RH, BF16>(raw[u], x, ang, y);
+        const uint64_t r2 = pair(r, r);
+        other_channels<RH, BF16>(raw[u], ang, y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = (x[e] * w[e] + y[e] * wp[e]) * r;
-        if (h < h1) reinterpret_cast<uint4*>(out_row(h))[l] = pack<BF16>(o);
+        for (int i = 0; i < 4; ++i) o[i] = mul2(fma2(x[i], w[i], mul2(y[i], wp[i])), r2);
+        if (h + u * kRows < h1) *reinterpret_cast<uint4*>(dst) = pack<BF16>(o);
+        dst += dst_step;
       }
     }
   }
@@ -259,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 // Gradient.  The same items; each thread sums dw of its channels over its items, the block
 // sums its threads in a fixed order and leaves one partial row for grad_weights_kernel.
 template <int D, bool BF16, bool RH>
-__global__ void __launch_bounds__(kThreads) norm_rope_grad_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_grad_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = 2;
   __shared__ float sums[kThreads / 32 * kRows][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -270,9 +314,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_grad_kernel(const __grid_c
     const View& in = kind == 0 ? a.q : a.k;
     const View& grad = kind == 0 ? a.gq : a.gk;
     const View& out = kind == 0 ? a.q_out : a.k_out;
-    float dw[8] = {};
+    Pairs dw = {0, 0, 0, 0};
     const long long items = static_cast<long long>(a.B) * a.S * chunks;
     const long long stride = static_cast<long long>(gridDim.x) * (kThreads / 32);
+    Pairs w;
+    unpack<BF16>(__ldg(static_cast<const uint4*>(kind == 0 ? a.wq : a.wk) + l), w);
     for (long long it = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp; it < items; it += stride) {
       const long long token = it / chunks;
       const int chunk = static_cast<int>(it - token * chunks);
@@ -281,47 +327,62 @@ __global__ void __launch_bounds__(kThreads) norm_rope_grad_kernel(const __grid_c
       const long long pos = a.positions != nullptr ? a.positions[token] : s;
       const bool bad = pos < 0 || pos >= a.n_pos;
       const Angles ang = load_angles<RH, true>(a.cos_sin + (bad ? 0 : pos) * a.rot, a.rot, l, lane);
-      float w[8];
-      unpack<BF16>(__ldg(static_cast<const uint4*>(kind == 0 ? a.wq : a.wk) + l), w);
-      for (int hb = h0; hb < h1; hb += kRows * kUnroll) {
-        uint4 xr[kUnroll], gr[kUnroll];
+      Pairs c, sn;
+      pairs_of(ang.c, c);
+      pairs_of(ang.s, sn);
+      const char* px = in.row(b, s, h0 + sub) + 16 * l;
+      const char* pg = grad.row(b, s, h0 + sub) + 16 * l;
+      char* po = out.row(b, s, h0 + sub) + 16 * l;
+      const long long x_step = in.sh * kRows, g_step = grad.sh * kRows, o_step = out.sh * kRows;
+      // the next heads' loads are in flight while these are worked on
+      uint4 xr[kUnroll], gr[kUnroll], xn[kUnroll], gn[kUnroll];
+      auto load = [&](int h, uint4 (&xs)[kUnroll], uint4 (&gs)[kUnroll]) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const int h = hb + u * kRows + sub;
-          const bool live = h < h1;
-          xr[u] = live ? __ldcs(reinterpret_cast<const uint4*>(in.row(b, s, h)) + l) : make_uint4(0, 0, 0, 0);
-          gr[u] = live ? __ldcs(reinterpret_cast<const uint4*>(grad.row(b, s, h)) + l) : make_uint4(0, 0, 0, 0);
+          const bool live = h + u * kRows < h1;
+          xs[u] = live ? __ldcs(reinterpret_cast<const uint4*>(px)) : make_uint4(0, 0, 0, 0);
+          gs[u] = live ? __ldcs(reinterpret_cast<const uint4*>(pg)) : make_uint4(0, 0, 0, 0);
+          px += x_step;
+          pg += g_step;
+        }
+      };
+      load(h0 + sub, xr, gr);
+      for (int h = h0 + sub; h - sub < h1; h += kRows * kUnroll) {
+        load(h + kRows * kUnroll, xn, gn);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const bool live = h + u * kRows < h1;
+          Pairs x, g, gp, o;
+          unpack<BF16>(xr[u], x);
+          unpack<BF16>(gr[u], g);
+          float r = rsqrtf(row_sum<kLanes>(dot(x, x)) * (1.0f / D) + kEps);
+          if (bad && live) r = __uint_as_float(0x7FC00000u);
+          const uint64_t r2 = pair(r, r);
+          other_channels<RH, BF16>(gr[u], ang, gp);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t t = fma2(g[i], c[i], mul2(gp[i], sn[i]));
+            x[i] = mul2(x[i], r2);
+            dw[i] = fma2(t, x[i], dw[i]);
+            o[i] = mul2(t, w[i]);
+          }
+          const float mean = row_sum<kLanes>(dot(o, x)) * (1.0f / D);
+          const uint64_t minus = pair(-mean, -mean);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = mul2(r2, fma2(x[i], minus, o[i]));
+          if (live) *reinterpret_cast<uint4*>(po) = pack<BF16>(o);
+          po += o_step;
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const int h = hb + u * kRows + sub;
-          float x[8], g[8], gp[8], o[8];
-          unpack<BF16>(xr[u], x);
-          unpack<BF16>(gr[u], g);
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-          float r = rsqrtf(row_sum<kLanes>(ss) * (1.0f / D) + kEps);
-          if (bad && h < h1) r = __uint_as_float(0x7FC00000u);
-          pair_of<RH, BF16>(gr[u], g, ang, gp);
-          float dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float t = g[e] * ang.c[e] + gp[e] * ang.s[e];
-            x[e] *= r;
-            dw[e] = fmaf(t, x[e], dw[e]);
-            o[e] = t * w[e];
-            dot = fmaf(o[e], x[e], dot);
-          }
-          dot = row_sum<kLanes>(dot) * (1.0f / D);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = r * (o[e] - x[e] * dot);
-          if (h < h1) reinterpret_cast<uint4*>(out.row(b, s, h))[l] = pack<BF16>(o);
+          xr[u] = xn[u];
+          gr[u] = gn[u];
         }
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[warp * kRows + sub][8 * l + e] = dw[e];
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float2*>(&sums[warp * kRows + sub][8 * l + 2 * i]) = halves(dw[i]);
     __syncthreads();
     if (threadIdx.x < D) {
       float t = 0.f;
@@ -447,7 +508,7 @@ template <bool APPEND>
 qnre_status_t run_forward(NormArgs& a, int D, bool bf16, bool rh, qnre_stream_t stream) {
   set_chunks(a, D, 8);
   const int64_t items = static_cast<int64_t>(a.B) * a.S * (a.cq + a.ck * (APPEND ? 2 : 1));
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + 7) / 8, 152 * 64));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + 7) / 8, 152 * 4));
   using Fn = void (*)(NormArgs);
   static const Fn fns[8] = {
       norm_rope_kernel<64, false, false, APPEND>, norm_rope_kernel<64, false, true, APPEND>,
@@ -579,7 +640,7 @@ qnre_status_t qnre_qk_norm_rope_backward(const qnre_tensor4_t* gq, const qnre_te
   a.q_out = view4(dq);
   a.k_out = view4(dk);
   a.partial = static_cast<float*>(workspace);
-  set_chunks(a, D, 8);
+  set_chunks(a, D, 32);
   // no tokens: the kernels run all the same and leave zero weight gradients
   const int64_t items = static_cast<int64_t>(a.B) * a.S * std::max(a.cq, a.ck);
   const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((items + 7) / 8, kGradBlocks)));
