@@ -3,17 +3,23 @@
 //
 // The walk itself is a few comparisons a node; what costs is a rejection, whose sum
 // over the vocabulary is R = sum max(p - a q, 0), and the last one's running sum, from which the next token is
-// drawn.  A cluster of up to eight CTAs takes one request: every warp of it owns one run of the vocabulary,
+// drawn.  A cluster of up to 16 CTAs takes one request: every warp of it owns one run of the vocabulary,
 // in order, so the sums of a pass are also the prefix that locates the drawn token, and only
 // the run that holds it is read again (from L2).  All p(x), q(x) of the drafted tokens are fetched before
 // the walk, so a level without a rejection reads nothing.
 //
 // Numbers.  The integers must not depend on the order of a sum, so sums are exact where it matters: an element
 // p - a q is formed as an unevaluated pair of floats (2^-48 relative; a is split the same way), a lane
-// adds pairs with the error kept, and lanes, warps and CTAs add 64-bit integers of 2^-56.
+// adds pairs with the error kept, and lanes, warps and CTAs add 64-bit integers of 2^-56.  The first child of a
+// node is tested exactly in fp32 (u q as a product and its error).
 // fp64 would serve too, but this chip issues two of its operations a cycle and SM, 64 times fewer.
 //
-// Bound: latency for few requests, HBM / L2 for many (8 bytes a vocabulary entry and rejection).
+// Bound: latency (start, fetch, one pass, search: 8 us for four requests of 32003 entries); for
+// many requests the passes' arithmetic and loads, the longest walk last.  48 trees of 32 nodes over 131075
+// entries (1.8 passes a request, four at most): 54 us with 512 threads a CTA, eight CTAs a request
+// and fp64 at the ends of a pass (two waves of clusters); 45 with integer conversions by shifts, exact fp32 first tests
+// and 256 threads; 35 with 16 CTAs of 128 threads, eight places a thread in the search and the short residual.
+// Two or eight loads a lane in flight instead of four: +5 %, +15 %.
 #include "../../include/qnre.h"
 #include "api_util.cuh"
 #include "ptx.cuh"
@@ -21,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 namespace {
@@ -28,12 +35,11 @@ namespace {
 using namespace qnre;
 using namespace qnre::api;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 8;
-constexpr double kFixed = 72057594037927936.0;  // 2^56
-constexpr float kFixedF = 72057594037927936.0f;
+constexpr int kMaxCluster = 16;
+constexpr int kUnroll = 4;  // 16-byte loads of p and of q a lane has in flight
+constexpr double kUnfix = 1.0 / 72057594037927936.0;  // 2^-56, the unit of the integer sums
 
 struct VerifyArgs {
   const float* p;
@@ -43,38 +49,103 @@ struct VerifyArgs {
   const float *accept_u, *sample_u;
   int32_t *path, *counts, *next;
   long long vocab;
-  int nodes, seg;  // seg: vocabulary entries a warp owns
+  int nodes, seg;  // seg: places a warp owns
 };
 
-// max(p - a q, 0) as an unevaluated sum hi + lo, a = ah + al.
-__device__ __forceinline__ void residual(float p, float q, float ah, float al, float& hi, float& lo) {
-  const float ph = __fmul_rn(ah, q);
-  const float pl = __fmaf_rn(al, q, __fmaf_rn(ah, q, -ph));
-  const float s = __fsub_rn(p, ph);
-  const float t = __fsub_rn(s, p);
-  float e = __fadd_rn(__fsub_rn(p, __fsub_rn(s, t)), __fsub_rn(-ph, t));  // s + e = p - ph exactly
-  e = __fsub_rn(e, pl);
-  hi = __fadd_rn(s, e);
-  lo = __fsub_rn(e, __fsub_rn(hi, s));
-  if (!(hi > 0.f)) hi = lo = 0.f;
+// Packed pairs of floats: one instruction for two vocabulary entries.  Every operation is one IEEE rounding.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves(f2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 sub2(f2 a, f2 b) { return fma2(b, pair(-1.f, -1.f), a); }
+
+// s + e = a + b exactly (Knuth).
+__device__ __forceinline__ void two_sum(f2 a, f2 b, f2& s, f2& e) {
+  s = add2(a, b);
+  const f2 t = sub2(s, a);
+  e = add2(sub2(a, sub2(s, t)), sub2(b, t));
 }
 
-__device__ __forceinline__ long long to_fixed(float hi, float lo) {
-  return __float2ll_rn(__fmul_rn(hi, kFixedF)) + __float2ll_rn(__fmul_rn(lo, kFixedF));
+// max(p - a q, 0) as an unevaluated sum hi + lo, a = ah + al; `neg_ah` is -ah twice.
+__device__ __forceinline__ void residual(f2 p, f2 q, f2 neg_ah, f2 neg_al, f2& hi, f2& lo) {
+  const f2 ph = fma2(neg_ah, q, 0);                            // -ah q, rounded
+  const f2 pl = fma2(neg_al, q, fma2(neg_ah, q, sub2(0, ph)));  // what that lost, and -al q
+  hi = add2(p, ph);
+  lo = add2(add2(sub2(p, hi), ph), pl);  // exact where p >= ah q; elsewhere nothing is kept
+  const float2 v = halves(add2(hi, lo));
+  const float2 h = halves(hi), l = halves(lo);
+  hi = pair(v.x > 0.f ? h.x : 0.f, v.y > 0.f ? h.y : 0.f);
+  lo = pair(v.x > 0.f ? l.x : 0.f, v.y > 0.f ? l.y : 0.f);
+}
+
+// x in units of 2^-56, |x| < 64, by shifts (the 64-bit conversion instruction runs at fp64's rate).
+__device__ __forceinline__ long long to_fixed(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const int e = static_cast<int>((b >> 23) & 0xFFu);
+  const uint32_t m = (b & 0x7FFFFFu) | (e != 0 ? 0x800000u : 0u);
+  const int up = max(e, 1) - (127 + 23 - 56);
+  const long long v = up >= 0 ? static_cast<long long>(static_cast<uint64_t>(m) << up) : (up > -32 ? m >> -up : 0u);
+  return (b >> 31) ? -v : v;
 }
 
 struct Shared {
   long long warp_sum[kWarps];
   long long cta_sum[2][kMaxCluster];
-  unsigned long long lane_scan[kWarps];
+  long long lane_scan[kWarps];
   float px[QNRE_MAX_NODES], qx[QNRE_MAX_NODES], u[QNRE_MAX_NODES];
   int token[QNRE_MAX_NODES], parent[QNRE_MAX_NODES], path[QNRE_MAX_NODES], gone[QNRE_MAX_NODES];
   double a, R;
+  long long t;
+  float ah, al;  // a as a pair of floats
   int node, todo, gone_count, length, found, last;
 };
 
+// The probability rows of a node.  Warps own runs of places y = x + shift, where place 0 lies on a
+// 16-byte boundary of p's row; q is read the same way where its row lies alike, else entry by entry.
+struct Row {
+  const float *p, *q;  // of place 0
+  int shift, end;
+  bool drafts, alike;
+  __device__ __forceinline__ Row(const VerifyArgs& g, int req, int node, bool with_drafts) {
+    p = g.p + req * g.ps0 + node * g.ps1;
+    q = with_drafts ? g.q + req * g.qs0 + node * g.qs1 : p;
+    shift = static_cast<int>((reinterpret_cast<uintptr_t>(p) >> 2) & 3);
+    alike = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    drafts = with_drafts;
+    end = static_cast<int>(g.vocab) + shift;
+    p -= shift;
+    q -= shift;
+  }
+  __device__ __forceinline__ float4 load(const float* row, int y) const {
+    if (y >= shift && y + 4 <= end && (row == p || alike)) return __ldg(reinterpret_cast<const float4*>(row + y));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (y >= shift && y < end) v.x = __ldg(row + y);
+    if (y + 1 >= shift && y + 1 < end) v.y = __ldg(row + y + 1);
+    if (y + 2 >= shift && y + 2 < end) v.z = __ldg(row + y + 2);
+    if (y + 3 >= shift && y + 3 < end) v.w = __ldg(row + y + 3);
+    return v;
+  }
+};
+
 template <bool HAS_Q>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
+__global__ void __launch_bounds__(kThreads, 6) verify_kernel(const VerifyArgs g) {
   __shared__ Shared sh;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -83,8 +154,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
   const uint32_t rank = ptx::cluster_ctarank();
   const int req = blockIdx.x / ncta;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const long long seg0 = static_cast<long long>(rank * kWarps + warp) * g.seg;
-  const long long seg1 = min(seg0 + g.seg, g.vocab);
+  const int seg0 = static_cast<int>(rank * kWarps + warp) * g.seg, seg1 = seg0 + g.seg;
 
   if (tid < g.nodes) {
     const long long at = static_cast<long long>(req) * g.nodes + tid;
@@ -101,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
   if (tid == 0) {
     sh.a = 0.0;
     sh.R = 1.0;
+    sh.ah = sh.al = 0.f;
     sh.node = sh.path[0] = 0;
     sh.length = 1;
     sh.gone_count = 0;
@@ -111,37 +182,43 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
   unsigned pass = 0;
   // The sum of max(p - a q, 0) over the vocabulary at `node` (without the tokens in sh.gone where they count),
   // by runs: each warp's in sh.warp_sum, each CTA's in sh.cta_sum, the total returned.
-  auto sum_pass = [&](int node, double a, int gone) -> long long {
-    const float* p = g.p + req * g.ps0 + node * g.ps1;
-    const float* q = HAS_Q ? g.q + req * g.qs0 + node * g.qs1 : nullptr;
-    const float ah = static_cast<float>(a), al = static_cast<float>(a - static_cast<double>(ah));
-    const bool drafts = HAS_Q && a != 0.0;
-    float hi = 0.f, lo = 0.f;
-    for (long long x0 = seg0 + lane; x0 < seg1; x0 += 32 * kUnroll) {
-      float pv[kUnroll], qv[kUnroll];
+  auto sum_pass = [&](int node, float ah, float al, int gone) -> long long {
+    const Row r(g, req, node, HAS_Q && ah != 0.f);
+    const f2 nh = pair(-ah, -ah), nl = pair(-al, -al);
+    f2 hi2 = 0, lo2 = 0;
+    for (int y0 = seg0 + 4 * lane; y0 < seg1; y0 += 128 * kUnroll) {
+      float4 pv[kUnroll], qv[kUnroll];
 #pragma unroll
       for (int e = 0; e < kUnroll; ++e) {
-        const bool in = x0 + 32 * e < seg1;
-        pv[e] = in ? __ldg(p + x0 + 32 * e) : 0.f;
-        qv[e] = in && drafts ? __ldg(q + x0 + 32 * e) : 0.f;
-      }
-      if (!HAS_Q) {
-        for (int i = 0; i < gone; ++i)
-#pragma unroll
-          for (int e = 0; e < kUnroll; ++e)
-            if (x0 + 32 * e == sh.gone[i]) pv[e] = 0.f;
+        const int y = y0 + 128 * e;
+        pv[e] = qv[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (y < seg1) {
+          pv[e] = r.load(r.p, y);
+          if (HAS_Q && r.drafts) qv[e] = r.load(r.q, y);
+        }
       }
 #pragma unroll
       for (int e = 0; e < kUnroll; ++e) {
-        float dh, dl;
-        residual(pv[e], qv[e], ah, al, dh, dl);
-        const float s = __fadd_rn(hi, dh), t = __fsub_rn(s, hi);
-        const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(dh, t));
-        hi = s;
-        lo = __fadd_rn(lo, __fadd_rn(err, dl));
+        if (!HAS_Q) {
+          for (int i = 0; i < gone; ++i) {
+            const int k = sh.gone[i] + r.shift - (y0 + 128 * e);
+            if (k == 0) pv[e].x = 0.f;
+            if (k == 1) pv[e].y = 0.f;
+            if (k == 2) pv[e].z = 0.f;
+            if (k == 3) pv[e].w = 0.f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          f2 dh = k ? pair(pv[e].z, pv[e].w) : pair(pv[e].x, pv[e].y), dl = 0, err;
+          if (HAS_Q && r.drafts) residual(dh, k ? pair(qv[e].z, qv[e].w) : pair(qv[e].x, qv[e].y), nh, nl, dh, dl);
+          two_sum(hi2, dh, hi2, err);
+          lo2 = add2(lo2, add2(err, dl));
+        }
       }
     }
-    long long v = to_fixed(hi, lo);
+    const float2 hs = halves(hi2), ls = halves(lo2);
+    long long v = to_fixed(hs.x) + to_fixed(hs.y) + to_fixed(ls.x) + to_fixed(ls.y);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (lane == 0) sh.warp_sum[warp] = v;
@@ -164,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
   // The walk, by warp 0 of every CTA alike (all see the same sums); it stops for a
   // sum (todo 1) or at the last node (todo 0).
   uint64_t children = 0;
-  bool fresh = true;
+  bool fresh = true, untried = true;  // children not listed yet; none of them refused yet
   long long Z = 0;
   bool have_sum = false;
   while (true) {
@@ -183,13 +260,23 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
         if (children == 0) break;
         const int i = __ffsll(static_cast<long long>(children)) - 1;
         children &= children - 1;
-        const double qx = sh.qx[i];
-        double left = __dsub_rn(static_cast<double>(sh.px[i]), HAS_Q ? __dmul_rn(a, qx) : 0.0);
-        if (!HAS_Q)
-          for (int k = 0; k < gone; ++k)
-            if (sh.gone[k] == sh.token[i]) left = 0.0;
-        if (!(left > 0.0)) left = 0.0;
-        if (__dmul_rn(__dmul_rn(static_cast<double>(sh.u[i]), qx), R) < left) {
+        const float px = sh.px[i], qx = sh.qx[i], u = sh.u[i];
+        double left = 0.0;
+        bool accepted;
+        if (untried) {  // u q < p, the product with its error: exact
+          const float m = __fmul_rn(u, qx), err = __fmaf_rn(u, qx, -m);
+          accepted = m < px || (m == px && err < 0.f);
+          if (!HAS_Q) left = px > 0.f ? px : 0.0;
+        } else {
+          left = __dsub_rn(static_cast<double>(px), HAS_Q ? __dmul_rn(a, static_cast<double>(qx)) : 0.0);
+          if (!HAS_Q)
+            for (int k = 0; k < gone; ++k)
+              if (sh.gone[k] == sh.token[i]) left = 0.0;
+          if (!(left > 0.0)) left = 0.0;
+          accepted = __dmul_rn(__dmul_rn(static_cast<double>(u), static_cast<double>(qx)), R) < left;
+        }
+        untried = accepted;
+        if (accepted) {
           node = i;
           a = 0.0;
           R = 1.0;
@@ -212,6 +299,8 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
       if (lane == 0) {
         sh.node = node;
         sh.a = a;
+        sh.ah = static_cast<float>(a);
+        sh.al = static_cast<float>(a - static_cast<double>(sh.ah));
         sh.R = R;
         sh.gone_count = gone;
         sh.length = length;
@@ -222,24 +311,23 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
     const int todo = sh.todo;
     if (todo == 0) {
       // sums of an earlier pass stand only if it was at this node
-      if (sh.a == 0.0) have_sum = false;
+      if (sh.ah == 0.f) have_sum = false;
       break;
     }
-    const double a = sh.a;
-    Z = sum_pass(sh.node, a, 0);
+    Z = sum_pass(sh.node, sh.ah, sh.al, 0);
     have_sum = true;
-    if (tid == 0) sh.R = static_cast<double>(Z) / kFixed;
+    if (tid == 0) sh.R = static_cast<double>(Z) * kUnfix;
     __syncthreads();
   }
 
   const int node = sh.node;
-  double a = sh.a;
+  float ah = sh.ah, al = sh.al;
   int gone = sh.gone_count;
-  if (!have_sum) Z = sum_pass(node, a, gone);
-  if (Z <= 0 && (a != 0.0 || gone != 0)) {  // nothing is left: the target itself
-    a = 0.0;
+  if (!have_sum) Z = sum_pass(node, ah, al, gone);
+  if (Z <= 0 && (ah != 0.f || gone != 0)) {  // nothing is left: the target itself
+    ah = al = 0.f;
     gone = 0;
-    Z = sum_pass(node, a, gone);
+    Z = sum_pass(node, ah, al, gone);
   }
   const unsigned buf = (pass - 1) & 1u;
 
@@ -250,47 +338,79 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs g) {
   }
   if (Z > 0) {
     // the lowest token whose running sum passes t: its CTA, its warp's run, then itself
-    const long long t = min(static_cast<long long>(static_cast<double>(g.sample_u[req]) * static_cast<double>(Z)), Z - 1);
+    if (tid == 0)
+      sh.t = min(static_cast<long long>(static_cast<double>(g.sample_u[req]) * static_cast<double>(Z)), Z - 1);
+    __syncthreads();
+    const long long t = sh.t;
     long long before = 0;
     uint32_t owner = 0;
     while (owner + 1 < ncta && before + sh.cta_sum[buf][owner] <= t) before += sh.cta_sum[buf][owner++];
     if (owner == rank) {
       int w = 0;
       while (w + 1 < kWarps && before + sh.warp_sum[w] <= t) before += sh.warp_sum[w++];
-      const long long s0 = static_cast<long long>(rank * kWarps + w) * g.seg, s1 = min(s0 + g.seg, g.vocab);
-      const float* p = g.p + req * g.ps0 + node * g.ps1;
-      const float* q = HAS_Q ? g.q + req * g.qs0 + node * g.qs1 : nullptr;
-      const float ah = static_cast<float>(a), al = static_cast<float>(a - static_cast<double>(ah));
+      const int s0 = static_cast<int>(rank * kWarps + w) * g.seg, s1 = s0 + g.seg;
+      const Row r(g, req, node, HAS_Q && ah != 0.f);
       if (tid == 0) {
         sh.found = 0x7FFFFFFF;
         sh.last = -1;
       }
       __syncthreads();
-      for (long long base = s0; base < s1; base += kThreads) {
-        const long long x = base + tid;
-        float hi = 0.f, lo = 0.f;
-        if (x < s1) {
-          float pv = __ldg(p + x);
-          if (!HAS_Q)
-            for (int i = 0; i < gone; ++i)
-              if (sh.gone[i] == x) pv = 0.f;
-          residual(pv, HAS_Q && a != 0.0 ? __ldg(q + x) : 0.f, ah, al, hi, lo);
+      // a thread takes eight places in a row, so one scan of the block covers the run
+      for (int base = s0; base < s1; base += kThreads * 8) {
+        const int y0 = base + tid * 8;
+        float4 pv[2], qv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool in = y0 + 4 * e < s1;
+          pv[e] = in ? r.load(r.p, y0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+          qv[e] = in && HAS_Q && r.drafts ? r.load(r.q, y0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        long long v = to_fixed(hi, lo);
+        long long mine[8];
+        const float ps[8] = {pv[0].x, pv[0].y, pv[0].z, pv[0].w, pv[1].x, pv[1].y, pv[1].z, pv[1].w};
+        const float qs[8] = {qv[0].x, qv[0].y, qv[0].z, qv[0].w, qv[1].x, qv[1].y, qv[1].z, qv[1].w};
+        long long v = 0;
+        uint32_t mass = 0;  // places with anything left
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          f2 dh = pair(ps[e], ps[e + 1]), dl = 0;
+          if (!HAS_Q) {
+            float2 d = halves(dh);
+            for (int i = 0; i < gone; ++i) {
+              if (sh.gone[i] + r.shift == y0 + e) d.x = 0.f;
+              if (sh.gone[i] + r.shift == y0 + e + 1) d.y = 0.f;
+            }
+            dh = pair(d.x, d.y);
+          } else if (r.drafts) {
+            residual(dh, pair(qs[e], qs[e + 1]), pair(-ah, -ah), pair(-al, -al), dh, dl);
+          }
+          const float2 h = halves(dh), l = halves(dl);
+          mine[e] = to_fixed(h.x) + to_fixed(l.x);
+          mine[e + 1] = to_fixed(h.y) + to_fixed(l.y);
+          v += mine[e] + mine[e + 1];
+          mass |= (h.x + l.x > 0.f ? 1u << e : 0u) | (h.y + l.y > 0.f ? 2u << e : 0u);
+        }
+        const long long own = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long up = __shfl_up_sync(0xFFFFFFFFu, v, o);
           if (lane >= o) v += up;
         }
-        if (lane == 31) sh.lane_scan[warp] = static_cast<unsigned long long>(v);
+        if (lane == 31) sh.lane_scan[warp] = v;
         __syncthreads();
-        long long add = before;
-        for (int i = 0; i < warp; ++i) add += static_cast<long long>(sh.lane_scan[i]);
-        if (x < s1 && hi > 0.f) {
-          atomicMax(&sh.last, static_cast<int>(x));
-          if (add + v > t) atomicMin(&sh.found, static_cast<int>(x));
+        long long run = before + v - own;
+        for (int i = 0; i < warp; ++i) run += sh.lane_scan[i];
+        if (mass != 0) atomicMax(&sh.last, y0 - r.shift + 31 - __clz(mass));
+        if (run + own > t) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            run += mine[e];
+            if ((mass >> e & 1) && run > t) {
+              atomicMin(&sh.found, y0 - r.shift + e);
+              break;
+            }
+          }
         }
-        for (int i = 0; i < kWarps; ++i) before += static_cast<long long>(sh.lane_scan[i]);
+        for (int i = 0; i < kWarps; ++i) before += sh.lane_scan[i];
         __syncthreads();
         if (sh.found != 0x7FFFFFFF) break;
       }
@@ -327,6 +447,20 @@ __global__ void __launch_bounds__(QNRE_MAX_NODES) masks_kernel(const int32_t* pa
     if (masks != nullptr) masks[at] = anc[i];
     if (depths != nullptr) depths[at] = __popcll(anc[i]) - 1;
   }
+}
+
+// A cluster of more than eight CTAs has to be asked for once a device and kernel.
+template <bool HAS_Q>
+bool allow_large_clusters() {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (ready.load() & bit) return true;
+  if (cudaFuncSetAttribute(verify_kernel<HAS_Q>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return false;
+  ready.fetch_or(bit);
+  return true;
 }
 
 template <typename K, typename... A>
@@ -386,15 +520,18 @@ qnre_status_t qnre_verify_tree(const float* target_probs, int64_t target_stride0
       if (overlaps(outs[i], r)) return QNRE_ERR_ALIAS;
     if (overlaps(outs[i], outs[(i + 1) % 3])) return QNRE_ERR_ALIAS;
   }
-  // As many CTAs a request as fill the machine once (four of 512 threads a SM), while each keeps
-  // 2048 entries or more.
+  // As many CTAs a request as the machine about holds at once (six to eight a SM), while each keeps 1024
+  // entries or more: walks differ in length, and a lone long one is spread over as many SMs as
+  // its cluster has CTAs.
   unsigned cluster = kMaxCluster;
-  while (cluster > 1 && (static_cast<int64_t>(n) * cluster > 152 * 4 || vocab < static_cast<int64_t>(cluster) * 2048))
+  while (cluster > 1 && (static_cast<int64_t>(n) * cluster > 152 * 8 || vocab < static_cast<int64_t>(cluster) * 1024))
     cluster /= 2;
   const int64_t warps = static_cast<int64_t>(cluster) * kWarps;
-  const int seg = static_cast<int>(((vocab + warps - 1) / warps + 31) / 32 * 32);
+  const int seg = static_cast<int>(((vocab + 3 + warps - 1) / warps + 127) / 128 * 128);  // + 3: the shift
   const VerifyArgs a{target_probs, draft_probs, target_stride0, target_stride1, draft_stride0, draft_stride1, tokens,
                      parents, node_counts, accept_u, sample_u, path, counts, next_token, vocab, nodes, seg};
+  if (cluster > 8 && !(draft_probs != nullptr ? allow_large_clusters<true>() : allow_large_clusters<false>()))
+    return QNRE_ERR_CUDA;
   return draft_probs != nullptr ? launch(verify_kernel<true>, n * cluster, kThreads, cluster, stream, a)
                                 : launch(verify_kernel<false>, n * cluster, kThreads, cluster, stream, a);
 }
