@@ -13,8 +13,8 @@
 // In a CTA: warp 4 brings K and V tiles by TMA into a ring (a page's tokens of one head are one
 // run of memory; boxes of the largest power of two that divides the page) and the next unit's Q
 // rows into one of two buffers; warp 5's
-// one thread issues tcgen05.mma: S = Q K^T (both operands in shared memory, fp32 S in
-// tensor memory, two buffers) and O += P V (P from tensor memory); warps 0-3 own one S row a thread:
+// one thread issues S = Q K^T (tcgen05.mma, both operands in shared memory, fp32 S in tensor memory, two
+// buffers) and warp 6's O += P V (P from tensor memory), so that neither waits behind the other; warps 0-3 own one S row a thread:
 // one pass with a running maximum and sum in base 2, P rounded to the inputs' type
 // (relative 2^-9 for bf16, 2^-12 for fp16, against sums kept in fp32), O rescaled only
 // when a row's maximum grows by more than 2^8, so that P stays below 2^8 and O below 2^8 sum|v|.
@@ -50,7 +50,7 @@ using namespace qnre;
 using namespace qnre::api;
 
 constexpr int kTile = 128;     // cached tokens a tile, rows a unit
-constexpr int kThreads = 192;  // 4 softmax warps, the TMA warp, the MMA warp
+constexpr int kThreads = 224;  // 4 softmax warps, the TMA warp, the warps that issue S and O products
 constexpr int kMaxCtas = 152;  // one a SM
 constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D, P 2 x 64
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
@@ -91,7 +91,7 @@ struct Smem {
 };
 
 struct Bars {
-  uint32_t full, empty, qfull, qempty, sfull, sfree, pready, pvdone, ofree, drain;
+  uint32_t full, empty, qfull, qempty, sfull, sfree, pready, pvdone, ofree, drain, drain2;
 };
 
 // One unit's part of a CTA's run.
@@ -285,68 +285,89 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
   }
 }
 
-// ------------------------------------------------------------------ MMA thread
+// ------------------------------------------------------------------ MMA threads
+// The low word of a shared-memory descriptor moves with the address; the rest is fixed.  (Built
+// whole for each instruction, a descriptor cost its one thread more than the instruction.)
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) { return base + (bytes >> 4); }
+
+// Lets the products issued so far end before the thread leaves its loop early.
+__device__ __forceinline__ void drain_mma(uint32_t bar) {
+  ptx::umma_commit(bar);
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (!ptx::mbar_try_wait(bar, 0) && ptx::global_timer_ns() - t0 < kWaitLimitNs) {
+  }
+}
+
+// S = Q K^T, tile after tile, across units: two ahead of the softmax as far as S's two buffers allow.
 template <int D, bool BF16>
-__device__ void run_mma(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
-                        volatile uint32_t* abort_flag) {
+__device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
+                           volatile uint32_t* abort_flag) {
   using L = Smem<D>;
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
-  constexpr uint32_t kIdescS = (1u << 4) | kFmt | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
-  constexpr uint32_t kIdescO = (1u << 4) | kFmt | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
-  uint32_t g = 0;  // tiles of the run
-  bool ok = true;
-
-  // O += P V of tile x, the first of segment `seg` or a later one
-  auto pv = [&](uint32_t x, bool first, uint32_t seg) {
-    const uint32_t b = x & 1u, ring = 2 * x + 1;
-    const uint32_t slot = ring % L::kStages;
-    ok = ok && wait(bars.full + 8 * slot, (ring / L::kStages) & 1u, abort_flag, a.c.status);
-    ok = ok && wait(bars.pready + 8 * b, (x >> 1) & 1u, abort_flag, a.c.status);
-    if (first) ok = ok && wait(bars.ofree, (seg & 1u) ^ 1u, abort_flag, a.c.status);
-    if (!ok) return;
-    ptx::tc_fence_after_sync();
-    const uint32_t v = smem + L::kRing + slot * L::kTileBytes;
-#pragma unroll
-    for (int kk = 0; kk < kTile / 16; ++kk)
-      umma_f16_ts(tmem + kTmemO, tmem + kTmemP + b * 64 + kk * 8,
-                  ptx::smem_desc_sw128(v + kk * 2048, kTile * 128, 1024), kIdescO, (!first || kk > 0) ? 1u : 0u);
-    ptx::umma_commit(bars.pvdone + 8 * b);
-    ptx::umma_commit(bars.empty + 8 * slot);
-  };
-
-  // S of tile g goes before O of tile g - 1, across units too: the tensor core is never behind the softmax
-  bool first = false;
-  uint32_t seg = 0;
+  constexpr uint32_t kIdesc = (1u << 4) | kFmt | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
+  const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kRing, 16, 1024);
+  const uint64_t q0 = ptx::smem_desc_sw128(smem + L::kQ, 16, 1024);
+  uint32_t g = 0, slot = 0, phase = 0;  // tile g's K lies in ring entry 2 g
   Seg s;
-  for (; ok && cur.next(s); ++seg) {
-    const uint32_t q = smem + L::kQ + (seg & 1u) * L::kTileBytes;
-    ok = wait(bars.qfull + 8 * (seg & 1u), (seg >> 1) & 1u, abort_flag, a.c.status);
-    for (int t = s.t0; ok && t < s.t1; ++t, ++g) {
-      const uint32_t b = g & 1u, ring = 2 * g;
-      const uint32_t slot = ring % L::kStages;
-      ok = wait(bars.full + 8 * slot, (ring / L::kStages) & 1u, abort_flag, a.c.status) &&
-           wait(bars.sfree + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
-      if (!ok) break;
+  for (uint32_t seg = 0; cur.next(s); ++seg) {
+    const uint64_t q = desc_at(q0, (seg & 1u) * L::kTileBytes);
+    if (!wait(bars.qfull + 8 * (seg & 1u), (seg >> 1) & 1u, abort_flag, a.c.status)) return drain_mma(bars.drain);
+    for (int t = s.t0; t < s.t1; ++t, ++g) {
+      const uint32_t b = g & 1u;
+      if (!wait(bars.full + 8 * slot, phase, abort_flag, a.c.status) ||
+          !wait(bars.sfree + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status))
+        return drain_mma(bars.drain);
       ptx::tc_fence_after_sync();
-      const uint32_t k = smem + L::kRing + slot * L::kTileBytes;
+      const uint64_t k = desc_at(ring0, slot * L::kTileBytes);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * (kTile * 128) + (kk % 4) * 32;
-        ptx::umma_f16(tmem + kTmemS + b * 128, ptx::smem_desc_sw128(q + off, 16, 1024),
-                      ptx::smem_desc_sw128(k + off, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+        ptx::umma_f16(tmem + kTmemS + b * 128, desc_at(q, off), desc_at(k, off), kIdesc, kk > 0 ? 1u : 0u);
       }
       ptx::umma_commit(bars.sfull + 8 * b);
       ptx::umma_commit(bars.empty + 8 * slot);
       if (t + 1 == s.t1) ptx::umma_commit(bars.qempty + 8 * (seg & 1u));
-      if (g > 0) pv(g - 1, first, t == s.t0 ? seg - 1 : seg);
-      first = t == s.t0;
+      slot += 2;
+      if (slot >= L::kStages) {
+        slot -= L::kStages;
+        phase ^= 1u;
+      }
     }
   }
-  if (ok && g > 0) pv(g - 1, first, seg - 1);
-  if (!ok) {
-    ptx::umma_commit(bars.drain);
-    const uint64_t t0 = ptx::global_timer_ns();
-    while (!ptx::mbar_try_wait(bars.drain, 0) && ptx::global_timer_ns() - t0 < kWaitLimitNs) {
+}
+
+// O += P V, tile after tile.
+template <int D, bool BF16>
+__device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
+                            volatile uint32_t* abort_flag) {
+  using L = Smem<D>;
+  constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
+  constexpr uint32_t kIdesc =
+      (1u << 4) | kFmt | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
+  const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kRing, kTile * 128, 1024);
+  uint32_t g = 0, slot = 1, phase = 0;  // tile g's V lies in ring entry 2 g + 1
+  Seg s;
+  for (uint32_t seg = 0; cur.next(s); ++seg) {
+    for (int t = s.t0; t < s.t1; ++t, ++g) {
+      const uint32_t b = g & 1u;
+      const bool first = t == s.t0;
+      if (!wait(bars.full + 8 * slot, phase, abort_flag, a.c.status) ||
+          (first && !wait(bars.ofree, (seg & 1u) ^ 1u, abort_flag, a.c.status)) ||
+          !wait(bars.pready + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status))
+        return drain_mma(bars.drain2);
+      ptx::tc_fence_after_sync();
+      const uint64_t v = desc_at(ring0, slot * L::kTileBytes);
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        umma_f16_ts(tmem + kTmemO, tmem + kTmemP + b * 64 + kk * 8, desc_at(v, kk * 2048), kIdesc,
+                    (!first || kk > 0) ? 1u : 0u);
+      ptx::umma_commit(bars.pvdone + 8 * b);
+      ptx::umma_commit(bars.empty + 8 * slot);
+      slot += 2;
+      if (slot >= L::kStages) {
+        slot -= L::kStages;
+        phase ^= 1u;
+      }
     }
   }
 }
@@ -635,7 +656,35 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) x[i] = row_ok ? x[i] * inv : 0.f;
-      if (in_out && s.whole) {
+      if (REP == 1) {
+        // a row is a lane, so turned around in shared memory: then four or eight lanes write a row's 32 columns
+        float* mine = join + warp * (32 * 33);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mine[lane * 33 + i] = x[REP == 1 ? i : 0];
+        __syncwarp();
+        if (s.whole) {
+          const int part = (lane % 4) * 8;
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 8) {
+            const int r = r0 + lane / 4;
+            const long long at = __shfl_sync(0xFFFFFFFFu, in_out ? orow : -1ll, r);
+            const float* y = mine + r * 33 + part;
+            if (at >= 0)
+              *reinterpret_cast<uint4*>(a.out + (at * D + c + part) * 2) =
+                  make_uint4(pack2<BF16>(y[0], y[1]), pack2<BF16>(y[2], y[3]), pack2<BF16>(y[4], y[5]), pack2<BF16>(y[6], y[7]));
+          }
+        } else {
+          const int part = (lane % 8) * 4;
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + lane / 8;
+            const bool store = __shfl_sync(0xFFFFFFFFu, in_out ? 1 : 0, r) != 0;
+            const float* y = mine + r * 33 + part;
+            if (store)
+              *reinterpret_cast<float4*>(a.part_o + (prow - lane + r) * D + c + part) = make_float4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      } else if (in_out && s.whole) {
         uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c + jc) * 2);
 #pragma unroll
         for (int i = 0; i < kPer / 8; ++i) {
@@ -694,9 +743,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bars.pvdone = take(2);
     bars.ofree = take(1);
     bars.drain = take(1);
+    bars.drain2 = take(1);
   }
   if (warp == 4) ptx::tmem_alloc(ptx::smem_addr(&tmem_slot), 512);
-  if (tid == 0) {
+  if (tid == 5 * 32) {
     abort_word = 0;
     bad_nodes = 0;
     for (int i = 0; i < L::kStages; ++i) {
@@ -713,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     ptx::mbar_init(bars.ofree, 4);
     ptx::mbar_init(bars.drain, 1);
+    ptx::mbar_init(bars.drain2, 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&a.tk);
     ptx::prefetch_tensormap(&a.tv);
@@ -789,8 +840,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     run_softmax<D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &abort_word, &bad_nodes);
   } else if (warp == 4) {
     run_producer<D, REP>(a, bars, smem, cur, &abort_word);
+  } else if (warp == 5) {
+    if (lane == 0) run_scores<D, BF16>(a, bars, smem, tmem, cur, &abort_word);
   } else if (lane == 0) {
-    run_mma<D, BF16>(a, bars, smem, tmem, cur, &abort_word);
+    run_outputs<D, BF16>(a, bars, smem, tmem, cur, &abort_word);
   }
   __syncwarp();
   ptx::tc_fence_before_sync();
@@ -821,7 +874,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
   float acc[kPer] = {}, l = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < parts; ++i) {
     const long long at = row_of(i);
     const float2 ml = reinterpret_cast<const float2*>(part_ml)[at];
