@@ -124,6 +124,24 @@ def test_trees(lens, nodes, Hq, Hk, dim, page, dtype):
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("lens,nodes,Hq,Hk,dim,page,dtype", [
+    ([300, 0, 77], 20, 14, 2, 128, 16, "bf16"),         # 18 nodes a tile: two row tiles share K and V
+    ([200, 1000], 64, 8, 1, 64, 128, "fp16"),           # four
+    ([90, 129], 40, 16, 1, 128, 8, "bf16"),             # five: two groups, the second with three idle CTAs
+    ([500], 64, 32, 2, 128, 24, "bf16"),                # eight
+    ([260], 2, 128, 1, 128, 64, "fp16"),                # 128 heads to one
+])
+def test_row_tiles_that_share_tokens(lens, nodes, Hq, Hk, dim, page, dtype):
+    c = Case(lens, nodes, Hq, Hk, dim, page, dtype, seed=nodes + Hq)
+    c.check(*c.run())
+
+
+def test_queries_laid_out_by_heads():
+    c = Case([150, 3], 5, 8, 2, 128, 16, "bf16", seed=13)
+    q = c.q.cuda().transpose(1, 2).contiguous().transpose(1, 2)
+    c.check(*c.run(q=q))
+
+
 @pytest.mark.parametrize("nodes,G", [(1, 4), (5, 8), (40, 8)])
 def test_long_context_spread_over_the_machine(nodes, G):
     c = Case([20011], nodes, 2 * G, 2, 128, 64, "bf16", seed=9)

@@ -50,15 +50,18 @@ using namespace qnre;
 using namespace qnre::api;
 
 constexpr int kTile = 128;     // cached tokens a tile, rows a unit
-constexpr int kThreads = 224;  // 4 softmax warps, the TMA warp, the warps that issue S and O products
+constexpr int kThreads = 256;  // 4 softmax warps, the K and V TMA warps, the warps that issue S and O products
 constexpr int kMaxCtas = 152;  // one a SM
 constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D, P 2 x 64
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
+constexpr int kMaxCluster = 4;  // row tiles that share K and V
 constexpr int kUnitCost = 2;  // a unit's start and end, in tiles
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that O is rescaled at
 
-struct Desc {  // a unit that spans CTAs, written by its second CTA for combine_kernel
-  int valid, req, kvh, rt, c0, c1, pad[2];
+// A unit that spans clusters, written by its second one for combine_kernel: cluster c's run starts at
+// c * quot + c * rem / clusters.
+struct Desc {
+  int valid, req, kvh, rt, c0, last, quot, rem;
 };
 
 struct AttnArgs {
@@ -73,7 +76,7 @@ struct AttnArgs {
   float* part_ml;  // [2 * kMaxCtas][128][2]: maximum (base 2), sum
   float* part_o;   // [2 * kMaxCtas][128][D]
   float scale_log2;
-  int layer, n, nodes, Hq, Hk, G, unit_nodes, row_tiles, box;
+  int layer, n, nodes, Hq, Hk, G, unit_nodes, row_groups, box, cl;  // cl: CTAs a cluster, row tiles a group
 };
 
 template <int D>
@@ -104,7 +107,7 @@ struct Seg {
 struct Cursor {
   const int* pre;
   const int2* lens;
-  int cur, end, req, row_tiles;
+  int cur, end, req, row_groups, cl, rank;
   __device__ __forceinline__ static int tiles_of(int total) { return total > 0 ? (total + kTile - 1) / kTile : 1; }
   __device__ __forceinline__ bool next(Seg& s) {
     while (cur < end) {
@@ -120,8 +123,8 @@ struct Cursor {
       s.t0 = max(0, o - kUnitCost);
       s.t1 = max(0, o + take - kUnitCost);
       if (s.t0 == s.t1) continue;  // the unit's cost falls to this CTA, its tiles to the next
-      s.kvh = unit / row_tiles;
-      s.rt = unit - s.kvh * row_tiles;
+      s.kvh = unit / row_groups;
+      s.rt = (unit - s.kvh * row_groups) * cl + rank;
       s.whole = s.t0 == 0 && s.t1 == tiles;
       // a CTA goes on with one unit at most, and leaves one unfinished at most
       s.slot = 2 * static_cast<int>(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
@@ -230,19 +233,43 @@ __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const void* tmap,
       : "memory");
 }
 
-// ------------------------------------------------------------------ TMA warp
-template <int D, int REP>
-__device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem, Cursor cur,
+// The same load into every CTA of `mask` at the same place, each one's barrier told of its bytes.
+__device__ __forceinline__ void tma_load_4d_multicast(uint32_t smem_dst, const void* tmap, uint32_t bar, int c0, int c1,
+                                                      int c2, int c3, uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "h"(mask)
+      : "memory");
+}
+
+// One arrival on the barrier at this place in every CTA of `mask` when this thread's products are done.
+__device__ __forceinline__ void umma_commit_multicast(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ TMA warps
+// One warp brings Q and K, another V: tile g's K goes to ring entry 2 g, its V to 2 g + 1.  With MC each CTA of
+// the cluster fetches its share of a tile's boxes for all of them.
+template <int D, int REP, bool MC>
+__device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem, Cursor cur, int kv,
                              volatile uint32_t* abort_flag) {
   using L = Smem<D>;
   constexpr int kHalves = D / 64;
   const int lane = threadIdx.x % 32;
-  const int chunks = kTile / a.box;
   const int chunk = lane / kHalves, half = lane % kHalves;
-  const bool active = chunk < chunks;
+  const bool active = chunk < kTile / a.box && (!MC || lane % a.cl == cur.rank);
+  const int ps = a.c.page_size, step = kTile / ps, step_off = kTile - step * ps;
+  const int none = a.c.layers * a.c.pages;  // past the end: the box is filled with zeros
+  const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
+  const CUtensorMap* map = kv ? &a.tv : &a.tk;
+  const uint32_t dst = smem + L::kRing + half * (kTile * 128) + chunk * a.box * 128;
   const int q_nodes = min(a.unit_nodes, a.nodes);
   const uint32_t q_bytes = static_cast<uint32_t>(REP * D * 2 * a.G * q_nodes);
-  uint32_t r = 0;
+  uint32_t slot = kv, phase = 1;
   auto settle = [] {  // stop: what is in flight lands in microseconds; the kernel's end waits for it
     const uint64_t t0 = ptx::global_timer_ns();
     while (ptx::global_timer_ns() - t0 < 50000) {
@@ -251,8 +278,13 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
   Seg s;
   for (uint32_t seg = 0; cur.next(s); ++seg) {
     const int row = a.rows[s.req];
-    const bool row_ok = row >= 0 && row < a.c.rows;
-    {  // the unit's Q rows, REP times
+    const bool fetches = active && row >= 0 && row < a.c.rows;
+    const int32_t* table = a.c.table + static_cast<long long>(fetches ? row : 0) * a.c.max_blocks;
+    int pos = s.t0 * kTile + chunk * a.box;
+    int block = pos / ps, off = pos - block * ps;
+    auto look = [&]() -> int { return fetches && block < a.c.max_blocks ? __ldg(table + block) : -1; };
+    int entry = look();
+    if (kv == 0) {  // the unit's Q rows, REP times
       const uint32_t buf = seg & 1u;
       if (!wait(bars.qempty + 8 * buf, ((seg >> 1) & 1u) ^ 1u, abort_flag, a.c.status)) return settle();
       if (lane == 0) ptx::mbar_arrive_expect_tx(bars.qfull + 8 * buf, q_bytes);
@@ -263,23 +295,31 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
                     &a.tq, bars.qfull + 8 * buf, (lane % kHalves) * 64, s.kvh * a.G, s.rt * a.unit_nodes, s.req);
     }
     for (int t = s.t0; t < s.t1; ++t) {
-      const int pos = t * kTile + chunk * a.box;
-      int page = a.layer * a.c.pages;
-      if (active && row_ok) {
-        const int p = a.c.page_of(row, pos);
-        if (p < 0 && pos < s.total) atomicOr(a.c.status, QNRE_CACHE_BAD_PAGE);
-        page = p >= 0 ? page + p : a.c.layers * a.c.pages;  // past the end: the box is filled with zeros
-      } else {
-        page = a.c.layers * a.c.pages;
+      const bool there = entry >= 0 && entry < a.c.pages;
+      if (fetches && !there && pos < s.total) atomicOr(a.c.status, QNRE_CACHE_BAD_PAGE);
+      const int page = there ? a.layer * a.c.pages + entry : none, at = off;
+      pos += kTile;
+      block += step;
+      off += step_off;
+      if (off >= ps) {
+        off -= ps;
+        ++block;
       }
-      for (int kv = 0; kv < 2; ++kv, ++r) {
-        const uint32_t slot = r % L::kStages, ph = (r / L::kStages) & 1u;
-        if (!wait(bars.empty + 8 * slot, ph ^ 1u, abort_flag, a.c.status)) return settle();
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bars.full + 8 * slot, L::kTileBytes);
-        __syncwarp();
-        if (active)
-          tma_load_4d(smem + L::kRing + slot * L::kTileBytes + half * (kTile * 128) + chunk * a.box * 128,
-                      kv ? &a.tv : &a.tk, bars.full + 8 * slot, half * 64, pos % a.c.page_size, s.kvh, page);
+      entry = look();  // on its way while this tile's place is waited for
+      if (!wait(bars.empty + 8 * slot, phase, abort_flag, a.c.status)) return settle();
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bars.full + 8 * slot, L::kTileBytes);
+      __syncwarp();
+      if (active) {
+        if (MC)
+          tma_load_4d_multicast(dst + slot * L::kTileBytes, map, bars.full + 8 * slot, half * 64, at, s.kvh, page,
+                                everyone);
+        else
+          tma_load_4d(dst + slot * L::kTileBytes, map, bars.full + 8 * slot, half * 64, at, s.kvh, page);
+      }
+      slot += 2;
+      if (slot >= L::kStages) {
+        slot -= L::kStages;
+        phase ^= 1u;
       }
     }
   }
@@ -299,7 +339,7 @@ __device__ __forceinline__ void drain_mma(uint32_t bar) {
 }
 
 // S = Q K^T, tile after tile, across units: two ahead of the softmax as far as S's two buffers allow.
-template <int D, bool BF16>
+template <int D, bool BF16, bool MC>
 __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
                            volatile uint32_t* abort_flag) {
   using L = Smem<D>;
@@ -307,6 +347,7 @@ __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, u
   constexpr uint32_t kIdesc = (1u << 4) | kFmt | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
   const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kRing, 16, 1024);
   const uint64_t q0 = ptx::smem_desc_sw128(smem + L::kQ, 16, 1024);
+  const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
   uint32_t g = 0, slot = 0, phase = 0;  // tile g's K lies in ring entry 2 g
   Seg s;
   for (uint32_t seg = 0; cur.next(s); ++seg) {
@@ -325,7 +366,10 @@ __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, u
         ptx::umma_f16(tmem + kTmemS + b * 128, desc_at(q, off), desc_at(k, off), kIdesc, kk > 0 ? 1u : 0u);
       }
       ptx::umma_commit(bars.sfull + 8 * b);
-      ptx::umma_commit(bars.empty + 8 * slot);
+      if (MC)
+        umma_commit_multicast(bars.empty + 8 * slot, everyone);
+      else
+        ptx::umma_commit(bars.empty + 8 * slot);
       if (t + 1 == s.t1) ptx::umma_commit(bars.qempty + 8 * (seg & 1u));
       slot += 2;
       if (slot >= L::kStages) {
@@ -337,7 +381,7 @@ __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, u
 }
 
 // O += P V, tile after tile.
-template <int D, bool BF16>
+template <int D, bool BF16, bool MC>
 __device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
                             volatile uint32_t* abort_flag) {
   using L = Smem<D>;
@@ -345,6 +389,7 @@ __device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, 
   constexpr uint32_t kIdesc =
       (1u << 4) | kFmt | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
   const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kRing, kTile * 128, 1024);
+  const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
   uint32_t g = 0, slot = 1, phase = 0;  // tile g's V lies in ring entry 2 g + 1
   Seg s;
   for (uint32_t seg = 0; cur.next(s); ++seg) {
@@ -362,7 +407,10 @@ __device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, 
         umma_f16_ts(tmem + kTmemO, tmem + kTmemP + b * 64 + kk * 8, desc_at(v, kk * 2048), kIdesc,
                     (!first || kk > 0) ? 1u : 0u);
       ptx::umma_commit(bars.pvdone + 8 * b);
-      ptx::umma_commit(bars.empty + 8 * slot);
+      if (MC)
+        umma_commit_multicast(bars.empty + 8 * slot, everyone);
+      else
+        ptx::umma_commit(bars.empty + 8 * slot);
       slot += 2;
       if (slot >= L::kStages) {
         slot -= L::kStages;
@@ -714,7 +762,7 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
   }
 }
 
-template <int D, bool BF16, int REP>
+template <int D, bool BF16, int REP, bool MC>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
   using L = Smem<D>;
   extern __shared__ char raw[];
@@ -751,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bad_nodes = 0;
     for (int i = 0; i < L::kStages; ++i) {
       ptx::mbar_init(bars.full + 8 * i, 1);
-      ptx::mbar_init(bars.empty + 8 * i, 1);
+      ptx::mbar_init(bars.empty + 8 * i, a.cl);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars.qfull + 8 * i, 1);
@@ -772,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   // the rows' lengths, and the first tile of each request in the concatenated run
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int units = a.Hk * a.row_tiles;
+  const int units = a.Hk * a.row_groups;
   const int room = a.c.max_blocks * a.c.page_size;
   for (int i = tid; i < a.n; i += kThreads) {
     const int row = a.rows[i];
@@ -804,17 +852,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   ptx::tc_fence_before_sync();
   __syncthreads();
+  if (MC) ptx::cluster_sync();  // every CTA's barriers stand before another arrives on them
   ptx::tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  const long long W = pre[a.n];
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
-  const int cta = blockIdx.x;
+  // this cluster's run of the W tiles: clusters get equal runs, in 32-bit arithmetic
+  const int rank = MC ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+  const int cluster = MC ? static_cast<int>(blockIdx.x) / a.cl : static_cast<int>(blockIdx.x);
+  const int W = pre[a.n];
+  const int clusters = min(static_cast<int>(gridDim.x) / a.cl, W);
+  const int quot = W / clusters, rem = W - quot * clusters;
+  auto start_of = [&](int c) { return c * quot + c * rem / clusters; };
   Cursor cur;
   cur.pre = pre;
   cur.lens = lens;
-  cur.row_tiles = a.row_tiles;
-  cur.cur = cta < ctas ? static_cast<int>(W * cta / ctas) : 0;
-  cur.end = cta < ctas ? static_cast<int>(W * (cta + 1) / ctas) : 0;
+  cur.row_groups = a.row_groups;
+  cur.cl = a.cl;
+  cur.rank = rank;
+  cur.cur = cluster < clusters ? start_of(cluster) : 0;
+  cur.end = cluster < clusters ? start_of(cluster + 1) : 0;
   int lo = 0, hi = a.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -822,28 +877,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   cur.req = lo;
 
-  if (tid == 0) {  // this CTA goes on with a unit that the CTA before it began: name it for the join
+  if (warp < 4) {
+    run_softmax<D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &abort_word, &bad_nodes);
+  } else if (warp == 4 || warp == 7) {
+    run_producer<D, REP, MC>(a, bars, smem, cur, warp == 4 ? 0 : 1, &abort_word);
+  } else if (warp == 5) {
+    if (lane == 0) run_scores<D, BF16, MC>(a, bars, smem, tmem, cur, &abort_word);
+  } else if (lane == 0) {
+    // does this run go on with a unit that the one before it began?  Then name it for the join
     Desc d{};
     Cursor look = cur;
     Seg s;
     if (look.next(s) && s.t0 > 0) {
       const int tiles = Cursor::tiles_of(s.total);
-      const long long first = pre[s.req] + static_cast<long long>(s.kvh * a.row_tiles + s.rt) * (tiles + kUnitCost) + kUnitCost;
-      const int c0 = static_cast<int>(((first + 1) * ctas - 1) / W);  // who has its first and its last tile
-      const int c1 = static_cast<int>(((first + tiles) * ctas - 1) / W);
-      if (c0 == cta - 1) d = Desc{1, s.req, s.kvh, s.rt, c0, c1, {0, 0}};
+      const int first = pre[s.req] + (s.kvh * a.row_groups + s.rt / a.cl) * (tiles + kUnitCost) + kUnitCost;
+      if (first >= start_of(cluster - 1)) d = Desc{1, s.req, s.kvh, s.rt, cluster - 1, first + tiles - 1, quot, rem};
     }
-    a.desc[cta] = d;
-  }
-
-  if (warp < 4) {
-    run_softmax<D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &abort_word, &bad_nodes);
-  } else if (warp == 4) {
-    run_producer<D, REP>(a, bars, smem, cur, &abort_word);
-  } else if (warp == 5) {
-    if (lane == 0) run_scores<D, BF16>(a, bars, smem, tmem, cur, &abort_word);
-  } else if (lane == 0) {
-    run_outputs<D, BF16>(a, bars, smem, tmem, cur, &abort_word);
+    a.desc[blockIdx.x] = d;
+    run_outputs<D, BF16, MC>(a, bars, smem, tmem, cur, &abort_word);
   }
   __syncwarp();
   ptx::tc_fence_before_sync();
@@ -853,12 +904,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     ptx::tmem_relinquish_alloc_permit();
     ptx::tmem_dealloc(tmem, 512);
   }
+  if (MC) {
+    __syncwarp();
+    ptx::cluster_sync();  // none leaves while another may still write to it
+  }
 }
 
 // Joins the parts of the units that span CTAs: block x is the unit's second CTA, a warp a row.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const float* part_ml, const float* part_o,
-                                                      char* out, float* lse, int nodes, int Hq, int G, int unit_nodes) {
+                                                      char* out, float* lse, int nodes, int Hq, int G, int unit_nodes,
+                                                      int cl) {
   constexpr int kPer = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -867,8 +923,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
   const int lane = threadIdx.x % 32, r = blockIdx.y * 8 + threadIdx.x / 32;
   const int node = d.rt * unit_nodes + r / G, head = d.kvh * G + r % G;
   if (r >= unit_nodes * G || node >= nodes) return;
-  const int parts = d.c1 - d.c0 + 1;
-  auto row_of = [&](int i) { return static_cast<long long>(2 * (d.c0 + i) + (i == 0 ? 1 : 0)) * 128 + r; };
+  // its clusters: those whose run starts by its last tile
+  const int clusters = gridDim.x / cl;
+  int parts = 1;
+  for (int c = d.c0 + 1 + lane; c < clusters; c += 32)
+    parts += c * d.quot + c * d.rem / clusters <= d.last ? 1 : 0;
+  parts = __reduce_add_sync(0xFFFFFFFFu, parts) - 31;
+  const int rank = blockIdx.x % cl;
+  auto row_of = [&](int i) { return static_cast<long long>(2 * ((d.c0 + i) * cl + rank) + (i == 0 ? 1 : 0)) * 128 + r; };
   float M = -INFINITY;
   for (int i = lane; i < parts; i += 32) M = fmaxf(M, part_ml[2 * row_of(i)]);
 #pragma unroll
@@ -904,43 +966,64 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
 constexpr uint64_t kDescBytes = 152 * sizeof(Desc);
 constexpr uint64_t kMlBytes = 2ull * kMaxCtas * 128 * 2 * 4;
 
-template <int D, bool BF16, int REP>
-qnre_status_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream) {
-  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+template <int D, bool BF16, int REP, bool MC>
+qnre_status_t launch_attention(const AttnArgs& a, int sms, cudaStream_t stream) {
+  const auto kernel = attention_kernel<D, BF16, REP, MC>;
+  // per device, kept: the raised shared-memory limit, and how many clusters of each size are resident at once
+  static std::atomic<uint64_t> ready{0};
+  static std::atomic<int> resident[64][kMaxCluster + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return QNRE_ERR_CUDA;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(ready.load() & bit)) {
-    if (cudaFuncSetAttribute(attention_kernel<D, BF16, REP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Smem<D>::kBytes) != cudaSuccess)
+  dev &= 63;
+  if (!(ready.load() >> dev & 1)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes) != cudaSuccess)
       return QNRE_ERR_CUDA;
-    ready.fetch_or(bit);
+    ready.fetch_or(1ull << dev);
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Smem<D>::kBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cl;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attention_kernel<D, BF16, REP>, a) != cudaSuccess) return QNRE_ERR_CUDA;
+  cfg.numAttrs = MC ? 2 : 1;
+  int ctas = std::min(sms, kMaxCtas);
+  if (MC) {
+    int fit = resident[dev][a.cl].load();
+    if (fit == 0) {
+      cudaLaunchConfig_t ask = cfg;
+      ask.gridDim = dim3(kMaxCtas / a.cl * a.cl);
+      ask.attrs = attr + 1;
+      ask.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&fit, kernel, &ask) != cudaSuccess || fit < 1) return QNRE_ERR_CUDA;
+      resident[dev][a.cl].store(fit);
+    }
+    ctas = std::min(fit, ctas / a.cl) * a.cl;
+  }
+  cfg.gridDim = dim3(ctas);
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return QNRE_ERR_CUDA;
   cfg.gridDim = dim3(ctas, (std::min(a.nodes, a.unit_nodes) * a.G + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
   return from_cuda(cudaLaunchKernelEx(&cfg, combine_kernel<D, BF16>, static_cast<const Desc*>(a.desc),
                                       static_cast<const float*>(a.part_ml), static_cast<const float*>(a.part_o), a.out,
-                                      a.lse, a.nodes, a.Hq, a.G, a.unit_nodes));
+                                      a.lse, a.nodes, a.Hq, a.G, a.unit_nodes, a.cl));
 }
 
 template <int D, bool BF16>
-qnre_status_t launch_rep(const AttnArgs& a, int ctas, cudaStream_t stream) {
+qnre_status_t launch_rep(const AttnArgs& a, int sms, cudaStream_t stream) {
   const int rows = std::min(a.nodes, a.unit_nodes) * a.G;
-  if (rows <= 32) return launch_attention<D, BF16, 4>(a, ctas, stream);
-  if (rows <= 64) return launch_attention<D, BF16, 2>(a, ctas, stream);
-  return launch_attention<D, BF16, 1>(a, ctas, stream);
+  if (a.cl > 1) return launch_attention<D, BF16, 1, true>(a, sms, stream);
+  if (rows <= 32) return launch_attention<D, BF16, 4, false>(a, sms, stream);
+  if (rows <= 64) return launch_attention<D, BF16, 2, false>(a, sms, stream);
+  return launch_attention<D, BF16, 1, false>(a, sms, stream);
 }
 
 }  // namespace
@@ -998,10 +1081,12 @@ qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* c
   a.Hk = cache->heads;
   a.G = a.Hq / a.Hk;
   a.unit_nodes = kTile / a.G;
-  a.row_tiles = (a.nodes + a.unit_nodes - 1) / a.unit_nodes;
+  const int row_tiles = (a.nodes + a.unit_nodes - 1) / a.unit_nodes;
+  a.cl = std::min(row_tiles, kMaxCluster);
+  a.row_groups = (row_tiles + a.cl - 1) / a.cl;
   const int64_t tiles = (static_cast<int64_t>(cache->max_blocks) * cache->page_size + kTile - 1) / kTile + kUnitCost;
-  if (a.n * tiles * a.Hk * a.row_tiles > 0x7FFFFFFF) return QNRE_ERR_CAPACITY;
-  a.box = std::min(kTile, cache->page_size & -cache->page_size);
+  if (a.n * tiles * a.Hk * a.row_groups > 0x7FFFFFFF) return QNRE_ERR_CAPACITY;
+  a.box = std::min(a.cl > 1 ? kTile / kMaxCluster : kTile, cache->page_size & -cache->page_size);
   a.rows = rows;
   a.counts = counts;
   a.mask = mask;
@@ -1028,10 +1113,9 @@ qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* c
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return QNRE_ERR_CUDA;
-  const int ctas = std::min(sms, kMaxCtas);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 128) return bf16 ? launch_rep<128, true>(a, ctas, s) : launch_rep<128, false>(a, ctas, s);
-  return bf16 ? launch_rep<64, true>(a, ctas, s) : launch_rep<64, false>(a, ctas, s);
+  if (D == 128) return bf16 ? launch_rep<128, true>(a, sms, s) : launch_rep<128, false>(a, sms, s);
+  return bf16 ? launch_rep<64, true>(a, sms, s) : launch_rep<64, false>(a, sms, s);
 }
 
 }  // extern "C"
