@@ -11,8 +11,8 @@
 // CTA order: the result depends on the lengths alone, never on timing.
 //
 // In a CTA: warp 4 brings K and V tiles by TMA into a ring (a page's tokens of one head are one
-// run of memory; boxes of the largest power of two that divides the page) and the next unit's Q
-// rows into one of two buffers; warp 5's
+// run of memory; boxes of the largest power of two that divides the page) and a unit's Q
+// rows; warp 5's
 // one thread issues S = Q K^T (tcgen05.mma, both operands in shared memory, fp32 S in tensor memory, two
 // buffers) and warp 6's O += P V (P from tensor memory), so that neither waits behind the other; warps 0-3 own one S row a thread:
 // one pass with a running maximum and sum in base 2, P rounded to the inputs' type
@@ -55,7 +55,7 @@ constexpr int kMaxCtas = 152;  // one a SM
 constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D, P 2 x 64
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 constexpr int kMaxCluster = 4;  // row tiles that share K and V
-constexpr int kUnitCost = 2;  // a unit's start and end, in tiles
+constexpr int kUnitCost = 4;  // a unit's start and end, in tiles
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that O is rescaled at
 
 // A unit that spans clusters, written by its second one for combine_kernel: cluster c's run starts at
@@ -79,22 +79,36 @@ struct AttnArgs {
   int layer, n, nodes, Hq, Hk, G, unit_nodes, row_groups, box, cl;  // cl: CTAs a cluster, row tiles a group
 };
 
-template <int D>
+// Shared memory.  Loads take about 2900 cycles from request to use when every SM loads, a tile of scores or of
+// outputs some 1200, so three tiles of K and of V are wanted: at D = 128 they fit next to Q when one row tile needs
+// no join (REP = 1) and the batch's lengths are few (SMALL: 128 requests); else V has two.
+template <int D, int REP, bool SMALL>
 struct Smem {
-  static constexpr int kStages = D == 128 ? 4 : 9;
+  static constexpr int kRequests = SMALL ? 128 : QNRE_MAX_CALL_ROWS;
+  static constexpr int kKStages = D == 128 ? 3 : 5;
+  static constexpr int kVStages = D == 128 ? (REP == 1 && SMALL ? 3 : 2) : 5;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kQ = 0;                                    // two buffers
-  static constexpr int kRing = 2 * kTileBytes;
-  static constexpr int kJoin = kRing + kStages * kTileBytes;      // float [128][33]
-  static constexpr int kMl = kJoin + 128 * 33 * 4;                // float [128][2]
-  static constexpr int kPre = kMl + 128 * 2 * 4;                  // int [QNRE_MAX_CALL_ROWS + 1]
-  static constexpr int kLen = kPre + (QNRE_MAX_CALL_ROWS + 4) * 4;  // int2 [QNRE_MAX_CALL_ROWS]
-  static constexpr int kBars = kLen + QNRE_MAX_CALL_ROWS * 8;
-  static constexpr int kBytes = kBars + 512 + 1024;               // + alignment of the base
+  static constexpr int kQ = 0;
+  static constexpr int kK = kTileBytes;
+  static constexpr int kV = kK + kKStages * kTileBytes;
+  static constexpr int kJoin = kV + kVStages * kTileBytes;               // REP > 1: float [128][33]
+  static constexpr int kMl = kJoin + (REP > 1 ? 128 * 33 * 4 : 0);       // REP > 1: float [128][2]
+  static constexpr int kLen = kMl + (REP > 1 ? 128 * 2 * 4 : 0);         // int2 [kRequests]
+  static constexpr int kPre = kLen + kRequests * 8;                      // int [kRequests + 1]
+  static constexpr int kBars = (kPre + (kRequests + 1) * 4 + 15) / 16 * 16;
+  static constexpr int kWords = kBars + 8 * (2 * kKStages + 2 * kVStages + 13);
+  static constexpr int kBytes = kWords + 24;
+  static_assert(kBytes <= 232448, "one CTA's shared memory");
+};
+
+// Words shared by the roles.
+struct Words {
+  unsigned long long bad_nodes[2];  // drafts with non-finite V elements, of even and odd segments
+  uint32_t tmem, abort;
 };
 
 struct Bars {
-  uint32_t full, empty, qfull, qempty, sfull, sfree, pready, pvdone, ofree, drain, drain2;
+  uint32_t kfull, kempty, vfull, vempty, qfull, qempty, sfull, sfree, pready, pvdone, ofree, drain, drain2;
 };
 
 // One unit's part of a CTA's run.
@@ -252,12 +266,11 @@ __device__ __forceinline__ void umma_commit_multicast(uint32_t bar, uint16_t mas
 }
 
 // ------------------------------------------------------------------ TMA warps
-// One warp brings Q and K, another V: tile g's K goes to ring entry 2 g, its V to 2 g + 1.  With MC each CTA of
-// the cluster fetches its share of a tile's boxes for all of them.
-template <int D, int REP, bool MC>
+// One warp brings Q and K, another V.  With MC each CTA of the cluster fetches its share of a tile's boxes for
+// all of them.
+template <typename L, int D, int REP, bool MC>
 __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem, Cursor cur, int kv,
                              volatile uint32_t* abort_flag) {
-  using L = Smem<D>;
   constexpr int kHalves = D / 64;
   const int lane = threadIdx.x % 32;
   const int chunk = lane / kHalves, half = lane % kHalves;
@@ -266,10 +279,12 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
   const int none = a.c.layers * a.c.pages;  // past the end: the box is filled with zeros
   const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
   const CUtensorMap* map = kv ? &a.tv : &a.tk;
-  const uint32_t dst = smem + L::kRing + half * (kTile * 128) + chunk * a.box * 128;
+  const uint32_t dst = smem + (kv ? L::kV : L::kK) + half * (kTile * 128) + chunk * a.box * 128;
   const int q_nodes = min(a.unit_nodes, a.nodes);
   const uint32_t q_bytes = static_cast<uint32_t>(REP * D * 2 * a.G * q_nodes);
-  uint32_t slot = kv, phase = 1;
+  const uint32_t full = kv ? bars.vfull : bars.kfull, empty = kv ? bars.vempty : bars.kempty;
+  const uint32_t stages = kv ? L::kVStages : L::kKStages;
+  uint32_t slot = 0, phase = 1;
   auto settle = [] {  // stop: what is in flight lands in microseconds; the kernel's end waits for it
     const uint64_t t0 = ptx::global_timer_ns();
     while (ptx::global_timer_ns() - t0 < 50000) {
@@ -285,14 +300,13 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
     auto look = [&]() -> int { return fetches && block < a.c.max_blocks ? __ldg(table + block) : -1; };
     int entry = look();
     if (kv == 0) {  // the unit's Q rows, REP times
-      const uint32_t buf = seg & 1u;
-      if (!wait(bars.qempty + 8 * buf, ((seg >> 1) & 1u) ^ 1u, abort_flag, a.c.status)) return settle();
-      if (lane == 0) ptx::mbar_arrive_expect_tx(bars.qfull + 8 * buf, q_bytes);
+      // (one buffer: the last unit's results are still being written when its last scores are done)
+      if (!wait(bars.qempty, (seg & 1u) ^ 1u, abort_flag, a.c.status)) return settle();
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bars.qfull, q_bytes);
       __syncwarp();
       if (lane < REP * kHalves)
-        tma_load_4d(smem + L::kQ + buf * L::kTileBytes + (lane % kHalves) * (kTile * 128) +
-                        (lane / kHalves) * (kTile / REP) * 128,
-                    &a.tq, bars.qfull + 8 * buf, (lane % kHalves) * 64, s.kvh * a.G, s.rt * a.unit_nodes, s.req);
+        tma_load_4d(smem + L::kQ + (lane % kHalves) * (kTile * 128) + (lane / kHalves) * (kTile / REP) * 128, &a.tq,
+                    bars.qfull, (lane % kHalves) * 64, s.kvh * a.G, s.rt * a.unit_nodes, s.req);
     }
     for (int t = s.t0; t < s.t1; ++t) {
       const bool there = entry >= 0 && entry < a.c.pages;
@@ -306,19 +320,18 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
         ++block;
       }
       entry = look();  // on its way while this tile's place is waited for
-      if (!wait(bars.empty + 8 * slot, phase, abort_flag, a.c.status)) return settle();
-      if (lane == 0) ptx::mbar_arrive_expect_tx(bars.full + 8 * slot, L::kTileBytes);
+      if (!wait(empty + 8 * slot, phase, abort_flag, a.c.status)) return settle();
+      if (lane == 0) ptx::mbar_arrive_expect_tx(full + 8 * slot, L::kTileBytes);
       __syncwarp();
       if (active) {
         if (MC)
-          tma_load_4d_multicast(dst + slot * L::kTileBytes, map, bars.full + 8 * slot, half * 64, at, s.kvh, page,
+          tma_load_4d_multicast(dst + slot * L::kTileBytes, map, full + 8 * slot, half * 64, at, s.kvh, page,
                                 everyone);
         else
-          tma_load_4d(dst + slot * L::kTileBytes, map, bars.full + 8 * slot, half * 64, at, s.kvh, page);
+          tma_load_4d(dst + slot * L::kTileBytes, map, full + 8 * slot, half * 64, at, s.kvh, page);
       }
-      slot += 2;
-      if (slot >= L::kStages) {
-        slot -= L::kStages;
+      if (++slot == stages) {
+        slot = 0;
         phase ^= 1u;
       }
     }
@@ -339,23 +352,21 @@ __device__ __forceinline__ void drain_mma(uint32_t bar) {
 }
 
 // S = Q K^T, tile after tile, across units: two ahead of the softmax as far as S's two buffers allow.
-template <int D, bool BF16, bool MC>
+template <typename L, int D, bool BF16, bool MC>
 __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
                            volatile uint32_t* abort_flag) {
-  using L = Smem<D>;
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
   constexpr uint32_t kIdesc = (1u << 4) | kFmt | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
-  const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kRing, 16, 1024);
-  const uint64_t q0 = ptx::smem_desc_sw128(smem + L::kQ, 16, 1024);
+  const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kK, 16, 1024);
+  const uint64_t q = ptx::smem_desc_sw128(smem + L::kQ, 16, 1024);
   const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
-  uint32_t g = 0, slot = 0, phase = 0;  // tile g's K lies in ring entry 2 g
+  uint32_t g = 0, slot = 0, phase = 0;
   Seg s;
   for (uint32_t seg = 0; cur.next(s); ++seg) {
-    const uint64_t q = desc_at(q0, (seg & 1u) * L::kTileBytes);
-    if (!wait(bars.qfull + 8 * (seg & 1u), (seg >> 1) & 1u, abort_flag, a.c.status)) return drain_mma(bars.drain);
+    if (!wait(bars.qfull, seg & 1u, abort_flag, a.c.status)) return drain_mma(bars.drain);
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
-      if (!wait(bars.full + 8 * slot, phase, abort_flag, a.c.status) ||
+      if (!wait(bars.kfull + 8 * slot, phase, abort_flag, a.c.status) ||
           !wait(bars.sfree + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status))
         return drain_mma(bars.drain);
       ptx::tc_fence_after_sync();
@@ -367,13 +378,12 @@ __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, u
       }
       ptx::umma_commit(bars.sfull + 8 * b);
       if (MC)
-        umma_commit_multicast(bars.empty + 8 * slot, everyone);
+        umma_commit_multicast(bars.kempty + 8 * slot, everyone);
       else
-        ptx::umma_commit(bars.empty + 8 * slot);
-      if (t + 1 == s.t1) ptx::umma_commit(bars.qempty + 8 * (seg & 1u));
-      slot += 2;
-      if (slot >= L::kStages) {
-        slot -= L::kStages;
+        ptx::umma_commit(bars.kempty + 8 * slot);
+      if (t + 1 == s.t1) ptx::umma_commit(bars.qempty);
+      if (++slot == L::kKStages) {
+        slot = 0;
         phase ^= 1u;
       }
     }
@@ -381,22 +391,21 @@ __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, u
 }
 
 // O += P V, tile after tile.
-template <int D, bool BF16, bool MC>
+template <typename L, int D, bool BF16, bool MC>
 __device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
                             volatile uint32_t* abort_flag) {
-  using L = Smem<D>;
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
   constexpr uint32_t kIdesc =
       (1u << 4) | kFmt | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
-  const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kRing, kTile * 128, 1024);
+  const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kV, kTile * 128, 1024);
   const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
-  uint32_t g = 0, slot = 1, phase = 0;  // tile g's V lies in ring entry 2 g + 1
+  uint32_t g = 0, slot = 0, phase = 0;
   Seg s;
   for (uint32_t seg = 0; cur.next(s); ++seg) {
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
       const bool first = t == s.t0;
-      if (!wait(bars.full + 8 * slot, phase, abort_flag, a.c.status) ||
+      if (!wait(bars.vfull + 8 * slot, phase, abort_flag, a.c.status) ||
           (first && !wait(bars.ofree, (seg & 1u) ^ 1u, abort_flag, a.c.status)) ||
           !wait(bars.pready + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status))
         return drain_mma(bars.drain2);
@@ -408,12 +417,11 @@ __device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, 
                     (!first || kk > 0) ? 1u : 0u);
       ptx::umma_commit(bars.pvdone + 8 * b);
       if (MC)
-        umma_commit_multicast(bars.empty + 8 * slot, everyone);
+        umma_commit_multicast(bars.vempty + 8 * slot, everyone);
       else
-        ptx::umma_commit(bars.empty + 8 * slot);
-      slot += 2;
-      if (slot >= L::kStages) {
-        slot -= L::kStages;
+        ptx::umma_commit(bars.vempty + 8 * slot);
+      if (++slot == L::kVStages) {
+        slot = 0;
         phase ^= 1u;
       }
     }
@@ -475,7 +483,8 @@ __device__ __noinline__ bool clean_v_row(char* row, bool token) {
   bool found = false;
 #pragma unroll 4
   for (int i = 0; i < D / 8; ++i) {
-    uint4* at = reinterpret_cast<uint4*>(row + (i / 8) * (kTile * 128) + (i % 8) * 16);
+    // each lane its own order of the row's pieces: rows are 128 bytes apart, so equal pieces share banks
+    uint4* at = reinterpret_cast<uint4*>(row + (i / 8) * (kTile * 128) + ((i ^ threadIdx.x) % 8) * 16);
     if (!token) {
       *at = make_uint4(0, 0, 0, 0);
       continue;
@@ -492,10 +501,9 @@ __device__ __noinline__ bool clean_v_row(char* row, bool token) {
   return found;
 }
 
-template <int D, bool BF16, int REP>
+template <typename L, int D, bool BF16, int REP>
 __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base, uint32_t smem, uint32_t tmem,
                             Cursor cur, volatile uint32_t* abort_flag, unsigned long long* bad_nodes) {
-  using L = Smem<D>;
   constexpr int kCols = kTile / REP;   // tokens of a tile this thread looks at
   constexpr int kRows = 128 / REP;     // unit rows
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -515,19 +523,33 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
   }
   const int ur_node = ur / a.G, ur_head = ur - ur_node * a.G;
 
+  // what this thread's row of a segment is
+  struct RowInfo {
+    int node, head;
+    bool in_out, row_ok;  // a row of the output; of a node that sees anything
+    uint64_t bits;        // the drafts it sees
+  };
+  auto row_info = [&](const Seg& s) {
+    RowInfo r{s.rt * a.unit_nodes + ur_node, s.kvh * a.G + ur_head, false, false, 0};
+    r.in_out = ur_node < a.unit_nodes && r.node < a.nodes;
+    r.row_ok = r.in_out && (a.counts == nullptr || r.node < a.counts[s.req]);
+    if (r.in_out)
+      r.bits = a.mask != nullptr ? a.mask[static_cast<long long>(s.req) * a.nodes + r.node] : (2ull << r.node) - 1;
+    return r;
+  };
+
   uint32_t g = 0;
-  Seg s;
-  while (cur.next(s)) {
-    const int node = s.rt * a.unit_nodes + ur_node, head = s.kvh * a.G + ur_head;
-    const bool in_out = ur_node < a.unit_nodes && node < a.nodes;  // a row of the output
-    bool row_ok = in_out;                                          // and of a node that sees anything
-    uint64_t bits = 0;
-    if (in_out) {
-      if (a.counts != nullptr) row_ok = node < a.counts[s.req];
-      bits = a.mask != nullptr ? a.mask[static_cast<long long>(s.req) * a.nodes + node] : (2ull << node) - 1;
-      const int drafts = s.total - s.len;  // slots that exist
-      if (drafts < 64) bits &= (1ull << drafts) - 1;
-    }
+  Seg s, next;
+  RowInfo row{}, next_row{};
+  bool more = cur.next(next);
+  if (more) next_row = row_info(next);
+  for (uint32_t seg = 0; more; ++seg) {
+    s = next;
+    row = next_row;
+    const int node = row.node, head = row.head;
+    const bool in_out = row.in_out, row_ok = row.row_ok;
+    const int slots = s.total - s.len;  // drafts that have a place
+    const uint64_t bits = slots < 64 ? row.bits & ((1ull << slots) - 1) : row.bits;
     float m = -INFINITY, l = 0.f;
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
@@ -620,12 +642,12 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         tmem_st_x16(pt, p);
       }
       if (tail) {
-        const uint32_t ring = 2 * g + 1, slot = ring % L::kStages;
-        wait(bars.full + 8 * slot, (ring / L::kStages) & 1u, abort_flag, a.c.status);
+        const uint32_t slot = g % L::kVStages;
+        wait(bars.vfull + 8 * slot, (g / L::kVStages) & 1u, abort_flag, a.c.status);
         const int pos = t * kTile + tid;
         if (pos >= s.len &&
-            clean_v_row<D, BF16>(smem_base + L::kRing + slot * L::kTileBytes + tid * 128, pos < s.total))
-          atomicOr(bad_nodes, 1ull << (pos - s.len));
+            clean_v_row<D, BF16>(smem_base + L::kV + slot * L::kTileBytes + tid * 128, pos < s.total))
+          atomicOr(bad_nodes + (seg & 1u), 1ull << (pos - s.len));
         __syncwarp();
       }
       tmem_st_wait();
@@ -637,19 +659,21 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       m = -INFINITY;
       l = 0.f;
     }
+    more = cur.next(next);
+    if (more) next_row = row_info(next);  // on its way during this segment's end
 
     // ---------------- the segment's result
     if (REP > 1) {
       ml[2 * tid] = m;
       ml[2 * tid + 1] = l;
     }
-    const bool drafts = s.t1 * kTile > s.len;
-    if (REP > 1 || drafts) named_sync();
     const uint32_t last = g - 1;
     wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
-    __syncwarp();
+    // every warp has come past the segment before: its word is the next one's
+    if (tid == 0) bad_nodes[(seg & 1u) ^ 1u] = 0;
+    named_sync();
     ptx::tc_fence_after_sync();
-    const uint64_t bad = drafts && row_ok ? *bad_nodes & bits : 0;
+    const uint64_t bad = row_ok ? bad_nodes[seg & 1u] & bits : 0;
     float f = 1.f;  // of this copy's part
     if (REP > 1) {
       float M = -INFINITY, sum = 0.f;
@@ -697,42 +721,13 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         named_sync();
       }
       if (bad != 0) {
-        const int row = a.rows[s.req];
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          x[i] = add_nonfinite<BF16>(a, row, s.kvh, s.len, s.t0 * kTile, s.t1 * kTile, bad, c + jc + i, x[i]);
+          x[i] = add_nonfinite<BF16>(a, a.rows[s.req], s.kvh, s.len, s.t0 * kTile, s.t1 * kTile, bad, c + jc + i, x[i]);
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) x[i] = row_ok ? x[i] * inv : 0.f;
-      if (REP == 1) {
-        // a row is a lane, so turned around in shared memory: then four or eight lanes write a row's 32 columns
-        float* mine = join + warp * (32 * 33);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) mine[lane * 33 + i] = x[REP == 1 ? i : 0];
-        __syncwarp();
-        if (s.whole) {
-          const int part = (lane % 4) * 8;
-#pragma unroll
-          for (int r0 = 0; r0 < 32; r0 += 8) {
-            const int r = r0 + lane / 4;
-            const long long at = __shfl_sync(0xFFFFFFFFu, in_out ? orow : -1ll, r);
-            const float* y = mine + r * 33 + part;
-            if (at >= 0)
-              *reinterpret_cast<uint4*>(a.out + (at * D + c + part) * 2) =
-                  make_uint4(pack2<BF16>(y[0], y[1]), pack2<BF16>(y[2], y[3]), pack2<BF16>(y[4], y[5]), pack2<BF16>(y[6], y[7]));
-          }
-        } else {
-          const int part = (lane % 8) * 4;
-#pragma unroll
-          for (int r0 = 0; r0 < 32; r0 += 4) {
-            const int r = r0 + lane / 8;
-            const bool store = __shfl_sync(0xFFFFFFFFu, in_out ? 1 : 0, r) != 0;
-            const float* y = mine + r * 33 + part;
-            if (store)
-              *reinterpret_cast<float4*>(a.part_o + (prow - lane + r) * D + c + part) = make_float4(y[0], y[1], y[2], y[3]);
-          }
-        }
-      } else if (in_out && s.whole) {
+      if (in_out && s.whole) {
         uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c + jc) * 2);
 #pragma unroll
         for (int i = 0; i < kPer / 8; ++i) {
@@ -754,22 +749,15 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       else if (a.lse != nullptr)
         a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-    if (drafts) {
-      named_sync();  // all have read it
-      if (tid == 0) *bad_nodes = 0;
-      named_sync();
-    }
   }
 }
 
-template <int D, bool BF16, int REP, bool MC>
+template <int D, bool BF16, int REP, bool MC, bool SMALL>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
-  using L = Smem<D>;
-  extern __shared__ char raw[];
-  __shared__ uint32_t tmem_slot, abort_word;
-  __shared__ unsigned long long bad_nodes;
-  char* smem_base = raw + ((1024u - (ptx::smem_addr(raw) & 1023u)) & 1023u);
+  using L = Smem<D, REP, SMALL>;
+  extern __shared__ __align__(1024) char smem_base[];
   const uint32_t smem = ptx::smem_addr(smem_base);
+  Words* words = reinterpret_cast<Words*>(smem_base + L::kWords);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   int* pre = reinterpret_cast<int*>(smem_base + L::kPre);
   int2* lens = reinterpret_cast<int2*>(smem_base + L::kLen);
@@ -781,10 +769,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       at += 8 * n;
       return r;
     };
-    bars.full = take(L::kStages);
-    bars.empty = take(L::kStages);
-    bars.qfull = take(2);
-    bars.qempty = take(2);
+    bars.kfull = take(L::kKStages);
+    bars.kempty = take(L::kKStages);
+    bars.vfull = take(L::kVStages);
+    bars.vempty = take(L::kVStages);
+    bars.qfull = take(1);
+    bars.qempty = take(1);
     bars.sfull = take(2);
     bars.sfree = take(2);
     bars.pready = take(2);
@@ -793,17 +783,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bars.drain = take(1);
     bars.drain2 = take(1);
   }
-  if (warp == 4) ptx::tmem_alloc(ptx::smem_addr(&tmem_slot), 512);
+  if (warp == 4) ptx::tmem_alloc(ptx::smem_addr(&words->tmem), 512);
   if (tid == 5 * 32) {
-    abort_word = 0;
-    bad_nodes = 0;
-    for (int i = 0; i < L::kStages; ++i) {
-      ptx::mbar_init(bars.full + 8 * i, 1);
-      ptx::mbar_init(bars.empty + 8 * i, a.cl);
+    words->abort = 0;
+    words->bad_nodes[0] = words->bad_nodes[1] = 0;
+    for (int i = 0; i < L::kKStages; ++i) {
+      ptx::mbar_init(bars.kfull + 8 * i, 1);
+      ptx::mbar_init(bars.kempty + 8 * i, a.cl);
     }
+    for (int i = 0; i < L::kVStages; ++i) {
+      ptx::mbar_init(bars.vfull + 8 * i, 1);
+      ptx::mbar_init(bars.vempty + 8 * i, a.cl);
+    }
+    ptx::mbar_init(bars.qfull, 1);
+    ptx::mbar_init(bars.qempty, 1);
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bars.qfull + 8 * i, 1);
-      ptx::mbar_init(bars.qempty + 8 * i, 1);
       ptx::mbar_init(bars.sfull + 8 * i, 1);
       ptx::mbar_init(bars.sfree + 8 * i, 4);
       ptx::mbar_init(bars.pready + 8 * i, 4);
@@ -854,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   __syncthreads();
   if (MC) ptx::cluster_sync();  // every CTA's barriers stand before another arrives on them
   ptx::tc_fence_after_sync();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = words->tmem;
   // this cluster's run of the W tiles: clusters get equal runs, in 32-bit arithmetic
   const int rank = MC ? static_cast<int>(ptx::cluster_ctarank()) : 0;
   const int cluster = MC ? static_cast<int>(blockIdx.x) / a.cl : static_cast<int>(blockIdx.x);
@@ -878,11 +872,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   cur.req = lo;
 
   if (warp < 4) {
-    run_softmax<D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &abort_word, &bad_nodes);
+    run_softmax<L, D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &words->abort, words->bad_nodes);
   } else if (warp == 4 || warp == 7) {
-    run_producer<D, REP, MC>(a, bars, smem, cur, warp == 4 ? 0 : 1, &abort_word);
+    run_producer<L, D, REP, MC>(a, bars, smem, cur, warp == 4 ? 0 : 1, &words->abort);
   } else if (warp == 5) {
-    if (lane == 0) run_scores<D, BF16, MC>(a, bars, smem, tmem, cur, &abort_word);
+    if (lane == 0) run_scores<L, D, BF16, MC>(a, bars, smem, tmem, cur, &words->abort);
   } else if (lane == 0) {
     // does this run go on with a unit that the one before it began?  Then name it for the join
     Desc d{};
@@ -894,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (first >= start_of(cluster - 1)) d = Desc{1, s.req, s.kvh, s.rt, cluster - 1, first + tiles - 1, quot, rem};
     }
     a.desc[blockIdx.x] = d;
-    run_outputs<D, BF16, MC>(a, bars, smem, tmem, cur, &abort_word);
+    run_outputs<L, D, BF16, MC>(a, bars, smem, tmem, cur, &words->abort);
   }
   __syncwarp();
   ptx::tc_fence_before_sync();
@@ -966,9 +960,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
 constexpr uint64_t kDescBytes = 152 * sizeof(Desc);
 constexpr uint64_t kMlBytes = 2ull * kMaxCtas * 128 * 2 * 4;
 
-template <int D, bool BF16, int REP, bool MC>
+template <int D, bool BF16, int REP, bool MC, bool SMALL>
 qnre_status_t launch_attention(const AttnArgs& a, int sms, cudaStream_t stream) {
-  const auto kernel = attention_kernel<D, BF16, REP, MC>;
+  const auto kernel = attention_kernel<D, BF16, REP, MC, SMALL>;
   // per device, kept: the raised shared-memory limit, and how many clusters of each size are resident at once
   static std::atomic<uint64_t> ready{0};
   static std::atomic<int> resident[64][kMaxCluster + 1];
@@ -976,13 +970,13 @@ qnre_status_t launch_attention(const AttnArgs& a, int sms, cudaStream_t stream) 
   if (cudaGetDevice(&dev) != cudaSuccess) return QNRE_ERR_CUDA;
   dev &= 63;
   if (!(ready.load() >> dev & 1)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, REP, SMALL>::kBytes) != cudaSuccess)
       return QNRE_ERR_CUDA;
     ready.fetch_or(1ull << dev);
   }
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Smem<D>::kBytes;
+  cfg.dynamicSmemBytes = Smem<D, REP, SMALL>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1017,13 +1011,19 @@ qnre_status_t launch_attention(const AttnArgs& a, int sms, cudaStream_t stream) 
                                       a.lse, a.nodes, a.Hq, a.G, a.unit_nodes, a.cl));
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SMALL>
 qnre_status_t launch_rep(const AttnArgs& a, int sms, cudaStream_t stream) {
   const int rows = std::min(a.nodes, a.unit_nodes) * a.G;
-  if (a.cl > 1) return launch_attention<D, BF16, 1, true>(a, sms, stream);
-  if (rows <= 32) return launch_attention<D, BF16, 4, false>(a, sms, stream);
-  if (rows <= 64) return launch_attention<D, BF16, 2, false>(a, sms, stream);
-  return launch_attention<D, BF16, 1, false>(a, sms, stream);
+  if (a.cl > 1) return launch_attention<D, BF16, 1, true, SMALL>(a, sms, stream);
+  if (rows > 64) return launch_attention<D, BF16, 1, false, SMALL>(a, sms, stream);
+  if (rows > 32) return launch_attention<D, BF16, 2, false, false>(a, sms, stream);
+  return launch_attention<D, BF16, 4, false, false>(a, sms, stream);
+}
+
+template <int D, bool BF16>
+qnre_status_t launch_size(const AttnArgs& a, int sms, cudaStream_t stream) {
+  // only REP = 1 at D = 128 has a use for the smaller table
+  return D == 128 && a.n <= 128 ? launch_rep<D, BF16, D == 128>(a, sms, stream) : launch_rep<D, BF16, false>(a, sms, stream);
 }
 
 }  // namespace
@@ -1114,8 +1114,8 @@ qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* c
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return QNRE_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 128) return bf16 ? launch_rep<128, true>(a, sms, s) : launch_rep<128, false>(a, sms, s);
-  return bf16 ? launch_rep<64, true>(a, sms, s) : launch_rep<64, false>(a, sms, s);
+  if (D == 128) return bf16 ? launch_size<128, true>(a, sms, s) : launch_size<128, false>(a, sms, s);
+  return bf16 ? launch_size<64, true>(a, sms, s) : launch_size<64, false>(a, sms, s);
 }
 
 }  // extern "C"
