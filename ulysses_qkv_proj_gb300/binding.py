@@ -140,7 +140,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ulysses_sage2_scatter_qkv.restype = c_int
     lib.ulysses_sage2_scatter_qkv.argtypes = [ctypes.POINTER(_Tensor4)] * 3 + [c_int, c_int] + [c_vp] * 7 + \
         [ctypes.c_uint64, c_vp]
-    t4, cache = ctypes.POINTER(_Tensor4), ctypes.POINTER(_Cache)
+    t4, cache = c_vp, ctypes.POINTER(_Cache)  # views go over as packed bytes (_view4)
     for name in ("truncate", "fork", "reserve", "copy_pages"):
         fn = getattr(lib, "qnre_cache_" + name)
         fn.restype = c_int
@@ -572,10 +572,17 @@ def _f32(where: str, t, *shape):
     return t.data_ptr()
 
 
-def _weight(where: str, w, like):
-    if w.dtype != like.dtype or w.numel() != like.shape[-1]:
-        raise QnreError(1, f"{where}: norm weights are [{like.shape[-1]}] of the input's dtype")
-    return _contig(w, where)
+def _view4(t) -> bytes:
+    """A rank-4 view as the bytes of a qnre_tensor4_t."""
+    if t.dim() != 4:
+        raise QnreError(1, "expected a rank-4 view")
+    return _pack_tensor4(t.data_ptr(), *t.shape, *t.stride(), _dtype_codes.get(t.dtype) or _dtype_code(t))
+
+
+def _weight(where: str, w, dim: int, dtype) -> int:
+    if w.dtype is not dtype or w.shape != (dim,) or not w.is_contiguous():
+        raise QnreError(1, f"{where}: norm weights are contiguous [{dim}] of the input's dtype")
+    return w.data_ptr()
 
 
 def qnre_cache_truncate(cache: PagedCache, rows, lens, stream=None) -> None:
@@ -619,9 +626,11 @@ def _norm_inputs(where: str, q, k, q_norm_w, k_norm_w, cos_sin, positions):
     if cos_sin.dim() != 2:
         raise QnreError(1, f"{where}: cos_sin must be [n_pos, rot]")
     n_pos, rot = cos_sin.shape
-    head = (_tensor4(q), _tensor4(k), _weight(where, q_norm_w, q), _weight(where, k_norm_w, k), _f32(where, cos_sin),
-            n_pos, rot)
-    return head, _i32(where, positions, *q.shape[:2])
+    vq, vk = _view4(q), _view4(k)
+    B, S, _, dim = q.shape
+    head = (vq, vk, _weight(where, q_norm_w, dim, q.dtype), _weight(where, k_norm_w, dim, k.dtype),
+            _f32(where, cos_sin), n_pos, rot)
+    return head, _i32(where, positions, B, S)
 
 
 def qnre_qk_norm_rope(q, k, q_norm_w, k_norm_w, cos_sin, positions, q_out, k_out, rope_style: str = "rotate_half",
@@ -629,8 +638,8 @@ def qnre_qk_norm_rope(q, k, q_norm_w, k_norm_w, cos_sin, positions, q_out, k_out
     """Per-head RMSNorm and rotation of q [B, S, Hq, D] and k [B, S, Hk, D] (views; in place allowed)."""
     where = "qnre_qk_norm_rope"
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
-    _check(load_library().qnre_qk_norm_rope(*head, ROPE_STYLES.get(rope_style, -1), pos, _tensor4(q_out),
-                                            _tensor4(k_out), _stream_ptr(stream)), where)
+    _check(load_library().qnre_qk_norm_rope(*head, ROPE_STYLES.get(rope_style, -1), pos, _view4(q_out),
+                                            _view4(k_out), _stream_ptr(stream)), where)
 
 
 def qk_norm_rope_workspace(q, k=None):
@@ -649,7 +658,7 @@ def qnre_qk_norm_rope_backward(gq, gk, q, k, q_norm_w, k_norm_w, cos_sin, positi
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
     D = q.shape[-1]
     _check(load_library().qnre_qk_norm_rope_backward(
-        _tensor4(gq), _tensor4(gk), *head, ROPE_STYLES.get(rope_style, -1), pos, _tensor4(dq), _tensor4(dk), _f32(where, dq_norm_w, D), _f32(where, dk_norm_w, D), _contig(workspace, where),
+        _view4(gq), _view4(gk), *head, ROPE_STYLES.get(rope_style, -1), pos, _view4(dq), _view4(dk), _f32(where, dq_norm_w, D), _f32(where, dk_norm_w, D), _contig(workspace, where),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
 
 
@@ -660,7 +669,7 @@ def qnre_qkv_norm_rope_append(q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
     n = q.shape[0]
     _check(load_library().qnre_qkv_norm_rope_append(
-        head[0], head[1], _tensor4(v), *head[2:], ROPE_STYLES.get(rope_style, -1), pos, _tensor4(q_out), cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)
+        head[0], head[1], _view4(v), *head[2:], ROPE_STYLES.get(rope_style, -1), pos, _view4(q_out), cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)
 
 
 def qnre_tree_masks(parents, masks=None, depths=None, stream=None) -> None:
@@ -689,7 +698,7 @@ def qnre_tree_attention(q, cache: PagedCache, layer: int, rows, mask, out, lse=N
     """Attention of drafted nodes q [n, nodes, Hq, D] over their rows' tokens and the nodes of mask (int64 [n, nodes];
     None: a chain) into out (contiguous); scale defaults to 1/sqrt(D)."""
     where = "qnre_tree_attention"
-    tq = _tensor4(q)
+    tq = _view4(q)
     n, nodes, heads, dim = q.shape
     if out.shape != q.shape or out.dtype != q.dtype:
         raise QnreError(1, f"{where}: out must be contiguous, of q's shape and dtype")
