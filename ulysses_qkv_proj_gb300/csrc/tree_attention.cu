@@ -50,7 +50,12 @@ using namespace qnre;
 using namespace qnre::api;
 
 constexpr int kTile = 128;     // cached tokens a tile, rows a unit
-constexpr int kThreads = 256;  // 4 softmax warps, the K and V TMA warps, the warps that issue S and O products
+// Softmax warps: with REP = 1 two threads share a row, each half of a tile's tokens.  Then the K and V TMA warps and
+// the warps that issue S and O products.
+template <int REP>
+constexpr int kSoftThreads = REP == 1 ? 256 : 128;
+template <int REP>
+constexpr int kThreads = kSoftThreads<REP> + 128;
 constexpr int kMaxCtas = 152;  // one a SM
 constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D, P 2 x 64
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
@@ -81,10 +86,10 @@ struct AttnArgs {
 
 // Shared memory.  Loads take about 2900 cycles from request to use when every SM loads, a tile of scores or of
 // outputs some 1200, so three tiles of K and of V are wanted: at D = 128 they fit next to Q when one row tile needs
-// no join (REP = 1) and the batch's lengths are few (SMALL: 128 requests); else V has two.
+// no join (REP = 1) and the batch's lengths are few (SMALL: 64 requests); else V has two.
 template <int D, int REP, bool SMALL>
 struct Smem {
-  static constexpr int kRequests = SMALL ? 128 : QNRE_MAX_CALL_ROWS;
+  static constexpr int kRequests = SMALL ? 64 : QNRE_MAX_CALL_ROWS;
   static constexpr int kKStages = D == 128 ? 3 : 5;
   static constexpr int kVStages = D == 128 ? (REP == 1 && SMALL ? 3 : 2) : 5;
   static constexpr int kTileBytes = kTile * D * 2;
@@ -92,8 +97,8 @@ struct Smem {
   static constexpr int kK = kTileBytes;
   static constexpr int kV = kK + kKStages * kTileBytes;
   static constexpr int kJoin = kV + kVStages * kTileBytes;               // REP > 1: float [128][33]
-  static constexpr int kMl = kJoin + (REP > 1 ? 128 * 33 * 4 : 0);       // REP > 1: float [128][2]
-  static constexpr int kLen = kMl + (REP > 1 ? 128 * 2 * 4 : 0);         // int2 [kRequests]
+  static constexpr int kMl = kJoin + (REP > 1 ? 128 * 33 * 4 : 0);       // float [128][2]; REP = 1: [2][2][128]
+  static constexpr int kLen = kMl + (REP > 1 ? 128 * 2 * 4 : 2048);      // int2 [kRequests]
   static constexpr int kPre = kLen + kRequests * 8;                      // int [kRequests + 1]
   static constexpr int kBars = (kPre + (kRequests + 1) * 4 + 15) / 16 * 16;
   static constexpr int kWords = kBars + 8 * (2 * kKStages + 2 * kVStages + 13);
@@ -168,7 +173,12 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
   return slow_wait(bar, parity, abort_flag, status);
 }
 
-__device__ __forceinline__ void named_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Among the softmax threads; among the two warps that share 32 rows.
+template <int REP>
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads<REP>) : "memory");
+}
+__device__ __forceinline__ void pair_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory"); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -476,13 +486,13 @@ __device__ __noinline__ float add_nonfinite(const AttnArgs& a, int row, int kvh,
   return x;
 }
 
-// This thread's V row of a tile past the context: slots without a token are zeroed; in drafted ones the non-finite
+// Pieces [first, last) of a V row of a tile past the context: slots without a token are zeroed; in drafted ones the non-finite
 // elements are, and true is returned.
 template <int D, bool BF16>
-__device__ __noinline__ bool clean_v_row(char* row, bool token) {
+__device__ __noinline__ bool clean_v_row(char* row, bool token, int first, int last) {
   bool found = false;
 #pragma unroll 4
-  for (int i = 0; i < D / 8; ++i) {
+  for (int i = first; i < last; ++i) {
     // each lane its own order of the row's pieces: rows are 128 bytes apart, so equal pieces share banks
     uint4* at = reinterpret_cast<uint4*>(row + (i / 8) * (kTile * 128) + ((i ^ threadIdx.x) % 8) * 16);
     if (!token) {
@@ -504,11 +514,14 @@ __device__ __noinline__ bool clean_v_row(char* row, bool token) {
 template <typename L, int D, bool BF16, int REP>
 __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base, uint32_t smem, uint32_t tmem,
                             Cursor cur, volatile uint32_t* abort_flag, unsigned long long* bad_nodes) {
-  constexpr int kCols = kTile / REP;   // tokens of a tile this thread looks at
+  constexpr bool kSplit = REP == 1;    // two threads a row, one maximum and one O
+  constexpr int kCols = kSplit ? 64 : kTile / REP;  // tokens of a tile this thread looks at
   constexpr int kRows = 128 / REP;     // unit rows
+  constexpr int kOut = kSplit ? D / 2 : D;  // columns of O this thread scales and writes
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int ur = tid % kRows, copy = tid / kRows, c0 = copy * kCols;
-  const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+  const int o0 = kSplit ? copy * kOut : 0;
+  const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
   float* join = reinterpret_cast<float*>(smem_base + L::kJoin);
   float* ml = reinterpret_cast<float*>(smem_base + L::kMl);
   const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
@@ -585,7 +598,13 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
           mx0 = max3(mx0, __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
           mx1 = max3(mx1, __uint_as_float(v[j][i + 2]), __uint_as_float(v[j][i + 3]));
         }
-      const float mx = fmaxf(mx0, mx1) * a.scale_log2;
+      float mx = fmaxf(mx0, mx1) * a.scale_log2;
+      if (kSplit) {  // with the other half's; two buffers, as the next tile's may be written before this is read
+        float* at = ml + b * 256 + ur;
+        at[copy * 128] = mx;
+        pair_sync(warp % 4);
+        mx = fmaxf(mx, at[(copy ^ 1) * 128]);
+      }
       const bool grow = mx > m + kRescale;
       if (t == s.t0) {
         m = mx;
@@ -598,7 +617,7 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         if (grow) m = mx;
         l *= f;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = o0; c < o0 + kOut; c += 32) {
           uint32_t o[32];
           ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
           ptx::tmem_ld_wait();
@@ -633,10 +652,7 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       __syncwarp();
       ptx::tc_fence_after_sync();
       const uint32_t pt = tmem + lane_base + kTmemP + b * 64 + c0 / 2;
-      if (kCols == 128) {
-        tmem_st_x32(pt, p);
-        tmem_st_x32(pt + 32, p + (kCols == 128 ? 32 : 0));
-      } else if (kCols == 64) {
+      if (kCols == 64) {
         tmem_st_x32(pt, p);
       } else {
         tmem_st_x16(pt, p);
@@ -644,9 +660,9 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       if (tail) {
         const uint32_t slot = g % L::kVStages;
         wait(bars.vfull + 8 * slot, (g / L::kVStages) & 1u, abort_flag, a.c.status);
-        const int pos = t * kTile + tid;
-        if (pos >= s.len &&
-            clean_v_row<D, BF16>(smem_base + L::kV + slot * L::kTileBytes + tid * 128, pos < s.total))
+        const int x = tid % 128, pos = t * kTile + x, pieces = D / 8 / (kSplit ? 2 : 1);
+        if (pos >= s.len && clean_v_row<D, BF16>(smem_base + L::kV + slot * L::kTileBytes + x * 128, pos < s.total,
+                                                 kSplit ? copy * pieces : 0, (kSplit ? copy * pieces : 0) + pieces))
           atomicOr(bad_nodes + (seg & 1u), 1ull << (pos - s.len));
         __syncwarp();
       }
@@ -663,7 +679,9 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
     if (more) next_row = row_info(next);  // on its way during this segment's end
 
     // ---------------- the segment's result
-    if (REP > 1) {
+    if (kSplit) {
+      ml[(g & 1u) * 256 + tid] = l;  // (the buffer that the last tile did not use)
+    } else {
       ml[2 * tid] = m;
       ml[2 * tid + 1] = l;
     }
@@ -671,11 +689,14 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
     wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
     // every warp has come past the segment before: its word is the next one's
     if (tid == 0) bad_nodes[(seg & 1u) ^ 1u] = 0;
-    named_sync();
+    soft_sync<REP>();
     ptx::tc_fence_after_sync();
     const uint64_t bad = row_ok ? bad_nodes[seg & 1u] & bits : 0;
     float f = 1.f;  // of this copy's part
-    if (REP > 1) {
+    if (kSplit) {
+      l += ml[(g & 1u) * 256 + (tid ^ 128)];
+      pair_sync(warp % 4);  // read by both before the next tile's maxima go there
+    } else {
       float M = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int c = 0; c < REP; ++c) M = fmaxf(M, ml[2 * (c * kRows + ur)]);
@@ -692,14 +713,14 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
     const long long orow = (static_cast<long long>(s.req) * a.nodes + node) * a.Hq + head;
     const long long prow = static_cast<long long>(s.slot) * 128 + ur;
     constexpr int kPer = 32 / REP;  // columns of a block of 32 this thread writes, from jc on
-    const int jc = copy * kPer;
+    const int jc = kSplit ? 0 : copy * kPer;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
+    for (int c = o0; c < o0 + kOut; c += 32) {
       uint32_t o[32];
       ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
       ptx::tmem_ld_wait();
       tmem_fence_regs(o);
-      if (c + 32 == D) {
+      if (c + 32 == o0 + kOut) {
         ptx::tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars.ofree);
@@ -711,14 +732,14 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       } else {  // the copies of a row lie in different warps
 #pragma unroll
         for (int i = 0; i < 32; ++i) join[tid * 33 + i] = __uint_as_float(o[i]) * f;
-        named_sync();
+        soft_sync<REP>();
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           x[i] = 0.f;
 #pragma unroll
           for (int k = 0; k < REP; ++k) x[i] += join[(k * kRows + ur) * 33 + jc + i];
         }
-        named_sync();
+        soft_sync<REP>();
       }
       if (bad != 0) {
 #pragma unroll
@@ -753,11 +774,12 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
 }
 
 template <int D, bool BF16, int REP, bool MC, bool SMALL>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
   using L = Smem<D, REP, SMALL>;
   extern __shared__ __align__(1024) char smem_base[];
   const uint32_t smem = ptx::smem_addr(smem_base);
   Words* words = reinterpret_cast<Words*>(smem_base + L::kWords);
+  constexpr int kSoftWarps = kSoftThreads<REP> / 32;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   int* pre = reinterpret_cast<int*>(smem_base + L::kPre);
   int2* lens = reinterpret_cast<int2*>(smem_base + L::kLen);
@@ -783,8 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bars.drain = take(1);
     bars.drain2 = take(1);
   }
-  if (warp == 4) ptx::tmem_alloc(ptx::smem_addr(&words->tmem), 512);
-  if (tid == 5 * 32) {
+  if (warp == kSoftWarps) ptx::tmem_alloc(ptx::smem_addr(&words->tmem), 512);
+  if (warp == kSoftWarps + 1 && lane == 0) {
     words->abort = 0;
     words->bad_nodes[0] = words->bad_nodes[1] = 0;
     for (int i = 0; i < L::kKStages; ++i) {
@@ -799,11 +821,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     ptx::mbar_init(bars.qempty, 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars.sfull + 8 * i, 1);
-      ptx::mbar_init(bars.sfree + 8 * i, 4);
-      ptx::mbar_init(bars.pready + 8 * i, 4);
+      ptx::mbar_init(bars.sfree + 8 * i, kSoftWarps);
+      ptx::mbar_init(bars.pready + 8 * i, kSoftWarps);
       ptx::mbar_init(bars.pvdone + 8 * i, 1);
     }
-    ptx::mbar_init(bars.ofree, 4);
+    ptx::mbar_init(bars.ofree, kSoftWarps);
     ptx::mbar_init(bars.drain, 1);
     ptx::mbar_init(bars.drain2, 1);
     ptx::fence_mbar_init();
@@ -816,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int units = a.Hk * a.row_groups;
   const int room = a.c.max_blocks * a.c.page_size;
-  for (int i = tid; i < a.n; i += kThreads) {
+  for (int i = tid; i < a.n; i += kThreads<REP>) {
     const int row = a.rows[i];
     int len = 0, cnt = 0;
     if (row >= 0 && row < a.c.rows) {
@@ -871,11 +893,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   cur.req = lo;
 
-  if (warp < 4) {
+  if (warp < kSoftWarps) {
     run_softmax<L, D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &words->abort, words->bad_nodes);
-  } else if (warp == 4 || warp == 7) {
-    run_producer<L, D, REP, MC>(a, bars, smem, cur, warp == 4 ? 0 : 1, &words->abort);
-  } else if (warp == 5) {
+  } else if (warp == kSoftWarps || warp == kSoftWarps + 3) {
+    run_producer<L, D, REP, MC>(a, bars, smem, cur, warp == kSoftWarps ? 0 : 1, &words->abort);
+  } else if (warp == kSoftWarps + 1) {
     if (lane == 0) run_scores<L, D, BF16, MC>(a, bars, smem, tmem, cur, &words->abort);
   } else if (lane == 0) {
     // does this run go on with a unit that the one before it began?  Then name it for the join
@@ -894,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   ptx::tc_fence_before_sync();
   __syncthreads();
   ptx::tc_fence_after_sync();
-  if (warp == 4) {
+  if (warp == kSoftWarps) {
     ptx::tmem_relinquish_alloc_permit();
     ptx::tmem_dealloc(tmem, 512);
   }
@@ -975,7 +997,7 @@ qnre_status_t launch_attention(const AttnArgs& a, int sms, cudaStream_t stream) 
     ready.fetch_or(1ull << dev);
   }
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<REP>);
   cfg.dynamicSmemBytes = Smem<D, REP, SMALL>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -1023,7 +1045,7 @@ qnre_status_t launch_rep(const AttnArgs& a, int sms, cudaStream_t stream) {
 template <int D, bool BF16>
 qnre_status_t launch_size(const AttnArgs& a, int sms, cudaStream_t stream) {
   // only REP = 1 at D = 128 has a use for the smaller table
-  return D == 128 && a.n <= 128 ? launch_rep<D, BF16, D == 128>(a, sms, stream) : launch_rep<D, BF16, false>(a, sms, stream);
+  return D == 128 && a.n <= 64 ? launch_rep<D, BF16, D == 128>(a, sms, stream) : launch_rep<D, BF16, false>(a, sms, stream);
 }
 
 }  // namespace
