@@ -185,6 +185,25 @@ def test_what_is_not_seen_never_arrives():
     assert torch.isfinite(out[0, 10][:, cols]).all() and torch.isfinite(out[0, 11][:, cols]).all()
 
 
+def test_what_is_not_seen_never_arrives_in_a_pair_of_row_tiles():
+    """The same where two row tiles share K and V, in both halves of V's channels."""
+    c = Case([120, 300], 40, 16, 2, 128, 16, "bf16", seed=14)
+    c.masks = [[1 << t for t in range(40)] for _ in range(2)]
+    clean = c.run()
+    c.check(*clean)
+    for i, L in enumerate(c.lens):
+        for t, col in ((5, 3), (39, 90)):
+            page, slot = c.table[c.rows[i], (L + t) // 16], (L + t) % 16
+            c.v[1, page, :, slot, col] = float("inf")
+    out, lse = c.run()
+    keep = [t for t in range(40) if t not in (5, 39)]
+    assert torch.equal(out[:, keep], clean[0][:, keep]) and torch.equal(lse, clean[1])
+    for t, col in ((5, 3), (39, 90)):
+        assert torch.isinf(out[:, t, :, col]).all()
+        cols = [x for x in range(128) if x != col]
+        assert torch.isfinite(out[:, t][..., cols]).all()
+
+
 def test_large_scores_and_rising_maxima():
     """Scores far apart, rising along the context: the running maximum moves many times."""
     c = Case([900], 2, 4, 2, 64, 16, "fp16", seed=7)

@@ -10,27 +10,35 @@
 // CTAs leaves an unnormalised (m, l, O) in the workspace from each, joined by combine_kernel in
 // CTA order: the result depends on the lengths alone, never on timing.
 //
-// In a CTA: warp 4 brings K and V tiles by TMA into a ring (a page's tokens of one head are one
-// run of memory; boxes of the largest power of two that divides the page) and a unit's Q
-// rows; warp 5's
-// one thread issues S = Q K^T (tcgen05.mma, both operands in shared memory, fp32 S in tensor memory, two
-// buffers) and warp 6's O += P V (P from tensor memory), so that neither waits behind the other; warps 0-3 own one S row a thread:
-// one pass with a running maximum and sum in base 2, P rounded to the inputs' type
-// (relative 2^-9 for bf16, 2^-12 for fp16, against sums kept in fp32), O rescaled only
-// when a row's maximum grows by more than 2^8, so that P stays below 2^8 and O below 2^8 sum|v|.
+// In a CTA: one warp brings K tiles and Q by TMA, one V tiles (a page's tokens of one head are one run of
+// memory; boxes of the largest power of two that divides the page, the page numbers fetched a tile ahead); one
+// thread issues S = Q K^T (tcgen05.mma, fp32 S in tensor memory, two buffers), another O += P V (P from tensor
+// memory), so that neither waits behind the other; the softmax warps make one pass over S with a running
+// maximum and sum in base 2.  P is rounded to the inputs' type (relative 2^-8 for bf16, 2^-11 for fp16; its sum
+// is kept of the unrounded values in fp32); O is rescaled only when a row's maximum grows by more than 2^8, so
+// that P stays below 2^8 and O below 2^8 sum|v|.
 //
-// Units of few rows (one token, small groups) would leave three of the four softmax warps idle.
-// Their rows are laid out kRep = 2 or 4 times instead, copy c looking at its own 128 / kRep tokens of each
-// tile: P is zero outside that block, so one O accumulator of 128 rows holds kRep
-// independent partial results, joined at the end through shared memory.  The tensor work is the
-// same; each softmax thread has 1 / kRep of the exponentials.
+// Units of few rows would leave lanes idle: with up to 32 (64) rows they are laid out REP = 4 (2) times, copy
+// c looking at its own 128 / REP tokens of each tile.  P is zero outside that block, so one O accumulator of 128
+// rows holds REP independent partial results, joined at the end through shared memory; the tensor work is
+// the same and each softmax thread has 1 / REP of the exponentials.  With more rows two threads share a row,
+// half a tile each.  Row tiles of one head (more than 128 rows) run as a cluster of up to four CTAs that
+// fetch K and V for one another by multicast.
 //
 // Slots that a row does not see must not reach it, whatever they hold: scores are replaced before use; V rows of
 // slots past the drafts are zeroed in shared memory, and non-finite V elements of drafted nodes (which
 // some rows see and others do not) are zeroed there and added to the rows that see them at the end.
 //
-// Bound: HBM while nodes * group is small (4 D bytes and 4 D rows flops a token and K head), the
-// softmax's exponentials and the tensor cores from about 128 rows up.
+// Bound: HBM up to 128 rows; above, the bytes that enter an SM (64 KB of K and V a tile of 1024 cycles of
+// tensor work, at 35 bytes a cycle and SM).  Measured (device time): 64 requests of 130..32000 tokens, 64 heads on 8,
+// D = 128 bf16: 234 us, 6.68 TB/s; 16 trees of 32 nodes over 900..16001 tokens: 91 us, 1.0 PFLOP/s; 6 trees of 61
+// nodes, D = 64 fp16: 37 us; one request of 4097 tokens, 32 heads on 8: 14 us, of which the join is four.  Steps, in
+// that order: first form 431 / 229 / 270 / 20.6; Q by TMA, scores of the next unit before the last product, masks as
+// words, a unit's cost in the split 258 / 147 / 50 / 17; two issuing threads, descriptors by one add 239 / 142 / 50 /
+// 17; multicast, page numbers ahead - / 109 / 48 / 15.3; three tiles of K and of V in flight 237 / 100 / 48 / 15.2;
+// cheaper unit ends, a unit's cost four tiles (2: 102 / 53, 8: 100 / 48 cold) 234 / 91 / 37 / 14.3.  Tried and left: Q in
+// tensor memory with P over S (108) or one P buffer (106), the pass with a standing maximum 32 columns at a time
+// (101), a CTA pair multiplying as one (169).
 #include "../../include/qnre.h"
 #include "cache.cuh"
 #include "ptx.cuh"
