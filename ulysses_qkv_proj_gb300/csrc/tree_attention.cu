@@ -30,7 +30,7 @@
 // some rows see and others do not) are zeroed there and added to the rows that see them at the end.
 //
 // Bound: HBM up to 128 rows; above, the bytes that enter an SM (64 KB of K and V a tile of 1024 cycles of
-// tensor work, at 35 bytes a cycle and SM).  Measured (device time): 64 requests of 130..32000 tokens, 64 heads on 8,
+// tensor work, at 34 bytes a cycle and SM).  Measured (device time): 64 requests of 130..32000 tokens, 64 heads on 8,
 // D = 128 bf16: 234 us, 6.68 TB/s; 16 trees of 32 nodes over 900..16001 tokens: 91 us, 1.0 PFLOP/s; 6 trees of 61
 // nodes, D = 64 fp16: 37 us; one request of 4097 tokens, 32 heads on 8: 14 us, of which the join is four.  Steps, in
 // that order: first form 431 / 229 / 270 / 20.6; Q by TMA, scores of the next unit before the last product, masks as
@@ -38,7 +38,7 @@
 // 17; multicast, page numbers ahead - / 109 / 48 / 15.3; three tiles of K and of V in flight 237 / 100 / 48 / 15.2;
 // cheaper unit ends, a unit's cost four tiles (2: 102 / 53, 8: 100 / 48 cold) 234 / 91 / 37 / 14.3.  Tried and left: Q in
 // tensor memory with P over S (108) or one P buffer (106), the pass with a standing maximum 32 columns at a time
-// (101), a CTA pair multiplying as one (169).
+// (101), a CTA pair multiplying as one (98).
 #include "../../include/qnre.h"
 #include "cache.cuh"
 #include "ptx.cuh"
