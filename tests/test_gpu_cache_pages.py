@@ -153,6 +153,23 @@ def test_sixty_four_nodes_and_many_pages():
     b.check()
 
 
+def test_reserve_of_thousands_of_blocks():
+    """Windows longer than one round of the bookkeeping, free pages far apart, a shared open block among them."""
+    b = Both(page=8, pages=40003, rows=5, blocks=2600, layers=1, heads=1)
+    held = torch.arange(40003) % 3 != 0
+    held[30000:] = False
+    b.cache.page_refs[held.nonzero()[:, 0].cuda()] = 1
+    b.sim.refs = held.int().tolist()
+    b.grow([1], [13])
+    b.fork([1], [4])
+    assert b.reserve([0, 4, 2, 3], [8 * 1024, 8 * 2500, 0, 8 * 2600])
+    b.check()
+    assert not b.reserve([1], [8 * 2600])                 # past max_blocks
+    b.check(b.qb.CACHE_NO_PAGES)
+    b.truncate([0, 1, 2, 3, 4], [0, 0, 0, 0, 0])
+    b.check()
+
+
 def test_misuse_is_reported():
     b = Both(page=8, pages=10)
     qb, c = b.qb, b.cache

@@ -6,11 +6,14 @@
 // decrements, which commute, so every table and every count is the same on
 // every run, whatever order the blocks of a launch run in.
 //
-// Bound: the bookkeeping is launch and load latency (three calls of a serving step, five launches, for 64
-// rows: 19 us on the device); the page copies of a fork's reserve are HBM bandwidth (64 copies of a 2 MB
-// page: 34.4 us with the fork and the release before it, 235 MB at 6.8 TB/s).
+// Bound: the bookkeeping is launch and load latency.  Release, reserve and compact of a serving step, 64 rows and
+// 8 layers: 18.8 us on the device with a warp a row in the reserve (each round a chain of four loads, done twice) and the
+// lengths in a launch of their own after the moves; 14.2 with the windows as one list, a thread a block, and a
+// cluster a row in the compact.  The page copies of a fork's reserve are HBM bandwidth (64 copies of a 2 MB page: 32.4 us
+// with the fork and the release before it, 235 MB).
 #include "../../include/qnre.h"
 #include "cache.cuh"
+#include "ptx.cuh"
 
 #include <cuda_runtime.h>
 
@@ -49,12 +52,8 @@ __device__ __forceinline__ void release_from(const CacheView& c, int row, int fi
   }
 }
 
-// One warp a row.  kGrow: the row's length grows by values[i] (after a compact's moves);
-// else it becomes min(length, values[i]).
-// Values above `limit` count as `limit`.
-template <bool kGrow>
-__global__ void __launch_bounds__(128) trim_kernel(CacheView c, const int32_t* rows, const int32_t* values, int n,
-                                                   int limit) {
+// One warp a row: its length becomes min(length, lens[i]).
+__global__ void __launch_bounds__(128) truncate_kernel(CacheView c, const int32_t* rows, const int32_t* lens, int n) {
   pdl_wait();
   const int i = blockIdx.x * 4 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -62,8 +61,7 @@ __global__ void __launch_bounds__(128) trim_kernel(CacheView c, const int32_t* r
   const int row = rows[i];
   if (!c.row_ok(row)) return;
   const int old = c.lens[row];
-  const int want = min(max(values[i], 0), limit);
-  const int len = kGrow ? static_cast<int>(min(static_cast<long long>(old) + want, 0x7FFFFFFFll)) : min(old, want);
+  const int len = min(old, max(lens[i], 0));
   __syncwarp();
   if (lane == 0) c.lens[row] = len;
   const long long first = (static_cast<long long>(len) + c.page_size - 1) / c.page_size;
@@ -151,55 +149,84 @@ __device__ __forceinline__ bool needs_page(const CacheView& c, int page, bool& s
   return page < 0 || shared;
 }
 
-// One block does a reserve's whole bookkeeping: count each row's new pages, scan, find
-// as many free pages from the lowest up, and hand them out.  The decisions read
-// the counts of the call's start; releases of replaced pages come last.
+// Bit e: count at + e is 0, for 16 counts (fewer at the end).
+__device__ __forceinline__ unsigned zero_counts(const CacheView& c, long long at) {
+  unsigned zero = 0;
+  if (at + 16 <= c.pages) {
+    int4 r[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) r[q] = reinterpret_cast<const int4*>(c.refs + at)[q];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      zero |= (r[q].x == 0 ? 1u : 0u) << (4 * q) | (r[q].y == 0 ? 2u : 0u) << (4 * q) |
+              (r[q].z == 0 ? 4u : 0u) << (4 * q) | (r[q].w == 0 ? 8u : 0u) << (4 * q);
+  } else {
+    for (int e = 0; e < 16 && at + e < c.pages; ++e) zero |= (c.refs[at + e] == 0 ? 1u : 0u) << e;
+  }
+  return zero;
+}
+
+// One block does a reserve's whole bookkeeping.  The rows' windows lie one after another as a list of blocks, a thread
+// a block: which ones need a page (by the counts of the call's start), a scan, as many free pages from the lowest up,
+// and a second round that hands them out.  A usual step is one round of 1024 blocks and one of 16384 pages, whose
+// counts are fetched first.  Releases of replaced pages come last.
 __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(CacheView c, const int32_t* rows,
                                                                   const int32_t* counts, int n) {
-  __shared__ int need[QNRE_MAX_CALL_ROWS];
+  __shared__ int row_of[QNRE_MAX_CALL_ROWS], len_of[QNRE_MAX_CALL_ROWS], first_of[QNRE_MAX_CALL_ROWS];
+  __shared__ int start_of[QNRE_MAX_CALL_ROWS + 1];  // of a row's window in the list
   __shared__ int sums[32];
   __shared__ int copies, refused;
   pdl_wait();
   const Scratch s(c);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int tid = threadIdx.x;
+  const unsigned zero0 = zero_counts(c, static_cast<long long>(tid) * 16);
   if (tid == 0) copies = refused = 0;
   __syncthreads();
-  for (int i = warp; i < n; i += 32) {
-    const Window w = window_of(c, rows, counts, i);
-    if (lane == 0 && (w.row < 0 || w.row >= c.rows)) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
-    if (lane == 0 && !w.fits) refused = 1;
-    int mine = 0;
-    for (int j = w.first + lane; j < w.last; j += 32) {
-      bool shared;
-      mine += needs_page(c, c.table[static_cast<long long>(w.row) * c.max_blocks + j], shared) ? 1 : 0;
-    }
-    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-    if (lane == 0) need[i] = mine;
+  int blocks = 0;
+  if (tid < n) {
+    const Window w = window_of(c, rows, counts, tid);
+    if (w.row < 0 || w.row >= c.rows) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
+    if (!w.fits) refused = 1;
+    blocks = w.last - w.first;
+    row_of[tid] = w.row;
+    len_of[tid] = w.len;
+    first_of[tid] = w.first;
+  }
+  int items;
+  {
+    const int incl = block_scan(blocks, sums, items);
+    if (tid < n) start_of[tid + 1] = incl;
+    if (tid == 0) start_of[0] = 0;
   }
   __syncthreads();
-  int total;
-  {
-    const int mine = tid < n ? need[tid] : 0;
-    const int incl = block_scan(mine, sums, total);
-    __syncthreads();
-    if (tid < n) need[tid] = incl - mine;  // first of the row's pages in the list
+
+  // block i of the list: its row (in the call), its number in the row and its page
+  auto item = [&](int i, int& k, int& j, int& page, bool& shared) -> bool {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (start_of[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    k = lo;
+    j = first_of[k] + i - start_of[k];
+    page = c.table[static_cast<long long>(row_of[k]) * c.max_blocks + j];
+    return needs_page(c, page, shared);
+  };
+
+  int k = 0, j = 0, page = -1;
+  bool shared = false, take = false;
+  int total = 0, before = 0;  // pages wanted; by the blocks of the round before this thread's
+  for (int base = 0; base < items; base += kReserveThreads) {
+    take = base + tid < items && item(base + tid, k, j, page, shared);
+    int step;
+    before = block_scan(take ? 1 : 0, sums, step) - (take ? 1 : 0);
+    total += step;
   }
-  // free pages, lowest first: 16 counts a thread and step, so that a cache of 16384 pages is one step
   int found = 0;
-  if (total <= c.pages) {
+  if (total <= c.pages && !refused) {
     for (long long base = 0; base < c.pages && found < total; base += kReserveThreads * 16) {
       const long long at = base + tid * 16;
-      unsigned zero = 0;
-      if (at + 16 <= c.pages) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int4 r = reinterpret_cast<const int4*>(c.refs + at)[q];
-          zero |= (r.x == 0 ? 1u : 0u) << (4 * q) | (r.y == 0 ? 2u : 0u) << (4 * q) |
-                  (r.z == 0 ? 4u : 0u) << (4 * q) | (r.w == 0 ? 8u : 0u) << (4 * q);
-        }
-      } else {
-        for (int e = 0; e < 16 && at + e < c.pages; ++e) zero |= (c.refs[at + e] == 0 ? 1u : 0u) << e;
-      }
+      unsigned zero = base == 0 ? zero0 : zero_counts(c, at);
       int step;
       int pos = found + block_scan(__popc(zero), sums, step) - __popc(zero);
       while (zero != 0 && pos < total) {
@@ -217,31 +244,24 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(CacheView c, c
     }
     return;
   }
-  for (int i = warp; i < n; i += 32) {
-    const Window w = window_of(c, rows, counts, i);
-    int at = need[i];
-    for (int j0 = w.first; j0 < w.last; j0 += 32) {
-      const int j = j0 + lane;
-      int page = -1;
-      bool shared = false, take = false;
-      int32_t* entry = c.table + static_cast<long long>(w.row) * c.max_blocks + j;
-      if (j < w.last) {
-        page = *entry;
-        take = needs_page(c, page, shared);
+  int done = 0;
+  for (int base = 0; base < items; base += kReserveThreads) {
+    if (items > kReserveThreads) {  // else the one round's findings still stand
+      take = base + tid < items && item(base + tid, k, j, page, shared);
+      int step;
+      before = block_scan(take ? 1 : 0, sums, step) - (take ? 1 : 0);
+      before += done;
+      done += step;
+    }
+    if (take) {
+      const int fresh = s.free[before];
+      s.old[before] = shared ? page : -1;
+      c.table[static_cast<long long>(row_of[k]) * c.max_blocks + j] = fresh;
+      if (shared && static_cast<long long>(j) * c.page_size < len_of[k]) {
+        const int slot = atomicAdd(&copies, 1);  // copies run in any order; at most `total` of them
+        s.src[slot] = page;
+        s.dst[slot] = fresh;
       }
-      const unsigned takers = __ballot_sync(0xFFFFFFFFu, take);
-      if (take) {
-        const int p = at + __popc(takers & ((1u << lane) - 1u));
-        const int fresh = s.free[p];
-        s.old[p] = shared ? page : -1;
-        *entry = fresh;
-        if (shared && static_cast<long long>(j) * c.page_size < w.len) {
-          const int slot = atomicAdd(&copies, 1);  // copies run in any order; at most `total` of them
-          s.src[slot] = page;
-          s.dst[slot] = fresh;
-        }
-      }
-      at += __popc(takers);
     }
   }
   __syncthreads();
@@ -290,20 +310,20 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(CacheView c, c
   }
 }
 
-// The moves of a compact.  One thread owns 16 bytes of a head's channels for one
-// (row, layer, K or V, head) and takes the accepted tokens in ascending order, eight at
-// a time: a later token's source can lie in an earlier one's destination never
-// (path ascends strictly, so path[j'] >= j' > j), so reads stay ahead of writes
+// A compact: a cluster of CTAs takes a row, moves its accepted tokens, and when all of them have, its first CTA grows
+// the length and releases the blocks past it.  One thread owns 16 bytes of a head's channels for one
+// (layer, K or V, head) and takes the tokens in ascending order, eight at a time: a later token's source is
+// never an earlier one's destination (path ascends strictly, so path[j'] >= j' > j), so reads stay ahead of writes
 // without any ordering between threads.
 __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CacheView c, const int32_t* rows, const int32_t* path,
-                                                               const int32_t* counts, int nodes, int lanes) {
+                                                               const int32_t* counts, int nodes, int lanes, int ctas) {
   __shared__ long long from[QNRE_MAX_NODES], to[QNRE_MAX_NODES];  // head 0's byte offsets in layer 0, -1: skip
   pdl_wait();
-  const int i = blockIdx.x;
+  const int i = blockIdx.x / ctas, part = blockIdx.x % ctas;
   const int row = rows[i];
-  const int count = min(counts[i], nodes);
+  const int count = min(max(counts[i], 0), nodes);
   if (row < 0 || row >= c.rows) {
-    if (threadIdx.x == 0) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
+    if (part == 0 && threadIdx.x == 0) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
     return;
   }
   const int len = c.lens[row];
@@ -324,8 +344,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CacheView c, cons
   const int row_vecs = c.head_dim / 8;
   const long long head_bytes = static_cast<long long>(c.page_size) * c.head_dim * 2;
   const long long layer_bytes = static_cast<long long>(c.pages) * c.heads * head_bytes;
-  for (long long t = static_cast<long long>(blockIdx.y) * kCopyThreads + threadIdx.x; t < lanes;
-       t += static_cast<long long>(gridDim.y) * kCopyThreads) {
+  for (long long t = part * kCopyThreads + threadIdx.x; t < lanes; t += ctas * kCopyThreads) {
     const int vec = static_cast<int>(t % row_vecs);
     long long rest = t / row_vecs;
     const int head = static_cast<int>(rest % c.heads);
@@ -342,26 +361,39 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CacheView c, cons
         if (j0 + e < count && from[j0 + e] >= 0) *reinterpret_cast<uint4*>(pool + to[j0 + e]) = r[e];
     }
   }
+  // every CTA of the row has read its length and table and made its moves
+  __syncwarp();
+  ptx::cluster_sync();
+  if (part == 0 && threadIdx.x < 32) {
+    const int grown = static_cast<int>(min(static_cast<long long>(len) + count, 0x7FFFFFFFll));
+    if (threadIdx.x == 0) c.lens[row] = grown;
+    const long long first = (static_cast<long long>(grown) + c.page_size - 1) / c.page_size;
+    if (first < c.max_blocks) release_from(c, row, static_cast<int>(first), threadIdx.x);
+  }
 }
 
 template <typename K, typename... A>
-qnre_status_t launch(K kernel, dim3 grid, dim3 block, qnre_stream_t stream, A... args) {
+qnre_status_t launch(K kernel, dim3 grid, dim3 block, unsigned cluster, qnre_stream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return from_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 dim3 copy_grid(const qnre_cache_t* c, int n) {
   const int64_t vecs = static_cast<int64_t>(c->heads) * c->page_size * c->head_dim / 8;
   const int64_t items = static_cast<int64_t>(n) * c->layers * 2 * ((vecs + kPieceVecs - 1) / kPieceVecs);
-  return dim3(static_cast<unsigned>(std::min<int64_t>(items, 152 * 8)));
+  return dim3(static_cast<unsigned>(std::min<int64_t>(items, 152 * 4)));
 }
 
 qnre_status_t check_call(const qnre_cache_t* cache, std::initializer_list<const void*> lists, int n) {
@@ -382,15 +414,14 @@ qnre_status_t qnre_cache_truncate(const qnre_cache_t* cache, const int32_t* rows
                                   qnre_stream_t stream) {
   const qnre_status_t st = check_call(cache, {rows, lens}, n);
   if (st != QNRE_OK || n == 0) return st;
-  return launch(trim_kernel<false>, dim3((n + 3) / 4), dim3(128), stream, view_of(cache), rows, lens, n,
-                0x7FFFFFFF);
+  return launch(truncate_kernel, dim3((n + 3) / 4), dim3(128), 1, stream, view_of(cache), rows, lens, n);
 }
 
 qnre_status_t qnre_cache_fork(const qnre_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
                               qnre_stream_t stream) {
   const qnre_status_t st = check_call(cache, {src, dst}, n);
   if (st != QNRE_OK || n == 0) return st;
-  return launch(fork_kernel, dim3((n + 3) / 4), dim3(128), stream, view_of(cache), src, dst, n);
+  return launch(fork_kernel, dim3((n + 3) / 4), dim3(128), 1, stream, view_of(cache), src, dst, n);
 }
 
 qnre_status_t qnre_cache_reserve(const qnre_cache_t* cache, const int32_t* rows, const int32_t* counts, int n,
@@ -398,11 +429,11 @@ qnre_status_t qnre_cache_reserve(const qnre_cache_t* cache, const int32_t* rows,
   qnre_status_t st = check_call(cache, {rows, counts}, n);
   if (st != QNRE_OK || n == 0) return st;
   const CacheView c = view_of(cache);
-  st = launch(reserve_kernel, dim3(1), dim3(kReserveThreads), stream, c, rows, counts, n);
+  st = launch(reserve_kernel, dim3(1), dim3(kReserveThreads), 1, stream, c, rows, counts, n);
   if (st != QNRE_OK) return st;
   const int32_t* src = c.scratch + 4 + 2 * static_cast<int64_t>(c.pages);
   const int32_t* count = c.scratch;
-  return launch(copy_pages_kernel, copy_grid(cache, n), dim3(kCopyThreads), stream, c, src, src + c.pages,
+  return launch(copy_pages_kernel, copy_grid(cache, n), dim3(kCopyThreads), 1, stream, c, src, src + c.pages,
                 count, n);
 }
 
@@ -415,12 +446,11 @@ qnre_status_t qnre_cache_compact(const qnre_cache_t* cache, const int32_t* rows,
   if (n == 0) return QNRE_OK;
   const int64_t lanes = static_cast<int64_t>(cache->layers) * 2 * cache->heads * (cache->head_dim / 8);
   if (lanes > (int64_t{1} << 31) - 1) return QNRE_ERR_CAPACITY;
-  const unsigned ys = static_cast<unsigned>(std::min<int64_t>((lanes + kCopyThreads - 1) / kCopyThreads, 1024));
-  const CacheView c = view_of(cache);
-  st = launch(compact_kernel, dim3(n, ys), dim3(kCopyThreads), stream, c, rows, path, counts, nodes,
-              static_cast<int>(lanes));
-  if (st != QNRE_OK) return st;
-  return launch(trim_kernel<true>, dim3((n + 3) / 4), dim3(128), stream, c, rows, counts, n, nodes);
+  // as many CTAs a row as its vectors fill, up to a cluster
+  unsigned ctas = 1;
+  while (ctas < 8 && lanes > static_cast<int64_t>(ctas) * kCopyThreads) ctas *= 2;
+  return launch(compact_kernel, dim3(n * ctas), dim3(kCopyThreads), ctas, stream, view_of(cache), rows, path, counts,
+                nodes, static_cast<int>(lanes), static_cast<int>(ctas));
 }
 
 qnre_status_t qnre_cache_copy_pages(const qnre_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
@@ -428,7 +458,7 @@ qnre_status_t qnre_cache_copy_pages(const qnre_cache_t* cache, const int32_t* sr
   // any number of pages: the lists are read by every block, so the row limit does not apply
   const qnre_status_t st = check_call(cache, {src, dst}, std::min(n, 1));
   if (st != QNRE_OK || n == 0) return st;
-  return launch(copy_pages_kernel, copy_grid(cache, n), dim3(kCopyThreads), stream, view_of(cache), src, dst,
+  return launch(copy_pages_kernel, copy_grid(cache, n), dim3(kCopyThreads), 1, stream, view_of(cache), src, dst,
                 static_cast<const int32_t*>(nullptr), n);
 }
 
