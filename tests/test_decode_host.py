@@ -237,3 +237,45 @@ def test_tree_mask_arguments(lib):
     n = ctypes.c_uint64()
     assert lib.qnre_tree_attention_workspace_bytes(96, ctypes.byref(n)) == 2
     assert lib.qnre_tree_attention_workspace_bytes(64, None) == 1
+
+
+def test_native_reads_agree_with_python_ones(lib, monkeypatch):
+    """_marshal gives what the Python reads give, and lets them name what is wrong."""
+    torch = pytest.importorskip("torch")
+    native = qb._native
+    if native is None:
+        pytest.skip("_marshal is not built")
+    base = torch.zeros((3, 4, 10, 64), dtype=torch.float16)
+    views = [base, base[:, :, 2:7], base.transpose(0, 1), base.to(torch.bfloat16)[1:, ::2], base.float(), base[:0]]
+    ints = [torch.zeros(5, dtype=torch.int32), torch.zeros((2, 3), dtype=torch.int32), torch.zeros((2, 3), dtype=torch.int32).t(),
+            torch.zeros(5, dtype=torch.int64), torch.zeros(5)]
+
+    def all_of():
+        r = []
+        for v in views + [base[0], base.double(), base.int()]:
+            try:
+                r.append(qb._view4(v))
+            except qb.QnreError as e:
+                r.append(str(e))
+        for t in ints:
+            for read in (lambda t, *s: qb._i32("x", t, *s), lambda t, *s: qb._f32("x", t, *s), lambda t, *s: qb._i64("x", t, *s)):
+                for shape in ((5,), (2, 3), (3, 2)):
+                    try:
+                        r.append(read(t, *shape))
+                    except qb.QnreError as e:
+                        r.append(str(e))
+        for w, like in ((base[0, 0, 0], base), (base[0, 0, 0], base.float()), (base[0, 0, :, 0], base), (base[0, 0, 0, :32], base)):
+            try:
+                r.append(qb._weight("x", w, 64, like))
+            except qb.QnreError as e:
+                r.append(str(e))
+        return r
+
+    views = [v for v in views]
+    with_native = all_of()
+    assert [tuple(qb._sizes(v)) for v in views] == [tuple(v.shape) for v in views]
+    monkeypatch.setattr(qb, "_native", None)
+    without = all_of()
+    # base.float() makes a new tensor each time only in the list above, so addresses agree
+    assert with_native == without
+    assert any(isinstance(x, str) for x in without) and any(isinstance(x, bytes) for x in without)

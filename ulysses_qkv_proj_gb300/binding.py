@@ -78,9 +78,14 @@ _lib = None
 def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     """Load libqnre.so (built by ulysses_qkv_proj_gb300.build), or the library the
     QNRE_LIB environment variable names (the debug build); raises if it is missing."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
+    try:
+        import torch  # noqa: F401  (its libraries, before the module that links to them)
+        from . import _marshal as _native
+    except ImportError:
+        _native = None
     path = path or os.environ.get("QNRE_LIB") or LIB_PATH
     if not os.path.exists(path):
         raise RuntimeError(f"libqnre.so not built ({path}); run `python -m ulysses_qkv_proj_gb300.build`")
@@ -196,8 +201,9 @@ def _dtype_code(t) -> int:
 
 
 # A decode step's kernels run for a few microseconds, so the calls' own cost counts: the current
-# stream is read as a raw handle (0.2 us on a Grace core; building the Stream object takes 2.9) and a view
-# is packed in one go (0.7 us; field by field 2.4).
+# stream is read as a raw handle (0.4 us on a Grace core; building the Stream object takes 2.9), a view
+# is packed in one go (1.0 us; field by field 2.4), and the decoding calls read their tensors natively (_marshal)
+# where that module was built: None from it means that a check failed, and the Python checks then say which.
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
         import torch
@@ -545,10 +551,21 @@ def _load_dtypes():
     _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
 
 
+_native = None  # the _marshal module once load_library has found it
+
+
+def _sizes(t):
+    return t.shape if _native is None else _native.sizes(t)
+
+
 def _i32(where: str, t, *shape):
     """Pointer of a contiguous int32 tensor (None passes), its shape checked where given."""
     if t is None:
         return None
+    if _native is not None:
+        p = _native.pointer(t, 3, *shape)
+        if p is not None:
+            return p
     if _int32 is None:
         _load_dtypes()
     if t.dtype is not _int32:
@@ -561,6 +578,10 @@ def _i32(where: str, t, *shape):
 
 
 def _f32(where: str, t, *shape):
+    if _native is not None:
+        p = _native.pointer(t, 2, *shape)
+        if p is not None:
+            return p
     if _int32 is None:
         _load_dtypes()
     if t.dtype is not _float32:
@@ -574,12 +595,21 @@ def _f32(where: str, t, *shape):
 
 def _view4(t) -> bytes:
     """A rank-4 view as the bytes of a qnre_tensor4_t."""
+    if _native is not None:
+        b = _native.view4(t)
+        if b is not None:
+            return b
     if t.dim() != 4:
         raise QnreError(1, "expected a rank-4 view")
     return _pack_tensor4(t.data_ptr(), *t.shape, *t.stride(), _dtype_codes.get(t.dtype) or _dtype_code(t))
 
 
-def _weight(where: str, w, dim: int, dtype) -> int:
+def _weight(where: str, w, dim: int, like) -> int:
+    if _native is not None:
+        p = _native.pointer(w, _native.type_code(like), dim)
+        if p is not None:
+            return p
+    dtype = like.dtype
     if w.dtype is not dtype or w.shape != (dim,) or not w.is_contiguous():
         raise QnreError(1, f"{where}: norm weights are contiguous [{dim}] of the input's dtype")
     return w.data_ptr()
@@ -588,48 +618,48 @@ def _weight(where: str, w, dim: int, dtype) -> int:
 def qnre_cache_truncate(cache: PagedCache, rows, lens, stream=None) -> None:
     """Row rows[i] keeps its first lens[i] tokens; the blocks past them are released (0 frees the row)."""
     where, n = "qnre_cache_truncate", rows.numel()
-    _check(load_library().qnre_cache_truncate(cache.handle, _i32(where, rows), _i32(where, lens, n), n,
+    _check(load_library().qnre_cache_truncate(cache.handle, _i32(where, rows, n), _i32(where, lens, n), n,
                                               _stream_ptr(stream)), where)
 
 
 def qnre_cache_fork(cache: PagedCache, src, dst, stream=None) -> None:
     """Empty row dst[i] becomes a copy of row src[i] that shares its pages."""
     where, n = "qnre_cache_fork", src.numel()
-    _check(load_library().qnre_cache_fork(cache.handle, _i32(where, src), _i32(where, dst, n), n,
+    _check(load_library().qnre_cache_fork(cache.handle, _i32(where, src, n), _i32(where, dst, n), n,
                                           _stream_ptr(stream)), where)
 
 
 def qnre_cache_reserve(cache: PagedCache, rows, counts, stream=None) -> None:
     """Pages of its own for the next counts[i] tokens of row rows[i] (lowest free pages, copy on write)."""
     where, n = "qnre_cache_reserve", rows.numel()
-    _check(load_library().qnre_cache_reserve(cache.handle, _i32(where, rows), _i32(where, counts, n), n,
+    _check(load_library().qnre_cache_reserve(cache.handle, _i32(where, rows, n), _i32(where, counts, n), n,
                                              _stream_ptr(stream)), where)
 
 
 def qnre_cache_compact(cache: PagedCache, rows, path, counts, stream=None) -> None:
     """Keep the accepted nodes path[i][:counts[i]] of row rows[i]'s drafts; its length grows by counts[i]."""
     where, n = "qnre_cache_compact", rows.numel()
-    if path.dim() != 2:
+    shape = _sizes(path)
+    if len(shape) != 2:
         raise QnreError(1, f"{where}: path must be [n, nodes]")
-    _check(load_library().qnre_cache_compact(cache.handle, _i32(where, rows), _i32(where, path, n, path.shape[1]),
-                                             _i32(where, counts, n), n, path.shape[1], _stream_ptr(stream)), where)
+    _check(load_library().qnre_cache_compact(cache.handle, _i32(where, rows, n), _i32(where, path, n, shape[1]),
+                                             _i32(where, counts, n), n, shape[1], _stream_ptr(stream)), where)
 
 
 def qnre_cache_copy_pages(cache: PagedCache, src, dst, stream=None) -> None:
     """Page src[i] to page dst[i] in every layer."""
     where, n = "qnre_cache_copy_pages", src.numel()
-    _check(load_library().qnre_cache_copy_pages(cache.handle, _i32(where, src), _i32(where, dst, n), n,
+    _check(load_library().qnre_cache_copy_pages(cache.handle, _i32(where, src, n), _i32(where, dst, n), n,
                                                 _stream_ptr(stream)), where)
 
 
 def _norm_inputs(where: str, q, k, q_norm_w, k_norm_w, cos_sin, positions):
-    if cos_sin.dim() != 2:
+    table = _sizes(cos_sin)
+    if len(table) != 2:
         raise QnreError(1, f"{where}: cos_sin must be [n_pos, rot]")
-    n_pos, rot = cos_sin.shape
     vq, vk = _view4(q), _view4(k)
-    B, S, _, dim = q.shape
-    head = (vq, vk, _weight(where, q_norm_w, dim, q.dtype), _weight(where, k_norm_w, dim, k.dtype),
-            _f32(where, cos_sin), n_pos, rot)
+    B, S, _, dim = _sizes(q)
+    head = (vq, vk, _weight(where, q_norm_w, dim, q), _weight(where, k_norm_w, dim, k), _f32(where, cos_sin), *table)
     return head, _i32(where, positions, B, S)
 
 
@@ -674,13 +704,11 @@ def qnre_qkv_norm_rope_append(q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q
 
 def qnre_tree_masks(parents, masks=None, depths=None, stream=None) -> None:
     """Ancestor masks (int64 [n, nodes], bit j: node j) and depths (int32) of trees given by parents int32 [n, nodes]."""
-    import torch
     where = "qnre_tree_masks"
-    if parents.dim() != 2 or (masks is not None and (masks.dtype != torch.int64 or masks.shape != parents.shape)):
-        raise QnreError(1, f"{where}: parents int32 [n, nodes], masks int64 alike")
-    n, nodes = parents.shape
-    _check(load_library().qnre_tree_masks(_i32(where, parents), n, nodes,
-                                          None if masks is None else _contig(masks, where),
+    if parents.dim() != 2:
+        raise QnreError(1, f"{where}: parents must be [n, nodes]")
+    n, nodes = _sizes(parents)
+    _check(load_library().qnre_tree_masks(_i32(where, parents), n, nodes, _i64(where, masks, n, nodes),
                                           _i32(where, depths, n, nodes), _stream_ptr(stream)), where)
 
 
@@ -693,24 +721,46 @@ def tree_attention_workspace(q, cache: PagedCache):
     return torch.empty(n.value, dtype=torch.uint8, device=q.device)
 
 
+def _same(where: str, t, like):
+    """Pointer of a contiguous tensor of like's shape and type."""
+    if _native is not None:
+        p = _native.pointer(t, _native.type_code(like), *_native.sizes(like))
+        if p is not None:
+            return p
+    if t.shape != like.shape or t.dtype != like.dtype:
+        raise QnreError(1, f"{where}: the output must be contiguous, of the input's shape and dtype")
+    return _contig(t, where)
+
+
+def _i64(where: str, t, *shape):
+    """Pointer of a contiguous int64 tensor of that shape (None passes)."""
+    if t is None:
+        return None
+    if _native is not None:
+        p = _native.pointer(t, 4, *shape)
+        if p is not None:
+            return p
+    if _int64 is None:
+        _load_dtypes()
+    if t.dtype is not _int64 or t.shape != shape:
+        raise QnreError(1, f"{where}: expected int64 {list(shape)}")
+    return _contig(t, where)
+
+
 def qnre_tree_attention(q, cache: PagedCache, layer: int, rows, mask, out, lse=None, counts=None, scale=None,
                         workspace=None, stream=None) -> None:
     """Attention of drafted nodes q [n, nodes, Hq, D] over their rows' tokens and the nodes of mask (int64 [n, nodes];
     None: a chain) into out (contiguous); scale defaults to 1/sqrt(D)."""
     where = "qnre_tree_attention"
     tq = _view4(q)
-    n, nodes, heads, dim = q.shape
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise QnreError(1, f"{where}: out must be contiguous, of q's shape and dtype")
-    if _int64 is None:
-        _load_dtypes()
-    if mask is not None and (mask.dtype is not _int64 or mask.shape != (n, nodes)):
-        raise QnreError(1, f"{where}: mask must be int64 [n, nodes]")
+    n, nodes, heads, dim = _sizes(q)
+    to = _same(where, out, q)
+    tm = _i64(where, mask, n, nodes)
     if workspace is None:
         raise QnreError(1, f"{where}: workspace is missing (tree_attention_workspace)")
     _check(load_library().qnre_tree_attention(
-        tq, cache.handle, layer, _i32(where, rows, n), None if mask is None else _contig(mask, where),
-        _i32(where, counts, n), dim ** -0.5 if scale is None else scale, _contig(out, where),
+        tq, cache.handle, layer, _i32(where, rows, n), tm, _i32(where, counts, n),
+        dim ** -0.5 if scale is None else scale, to,
         None if lse is None else _f32(where, lse, n, nodes, heads), _contig(workspace, where),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
 
@@ -720,19 +770,23 @@ def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sampl
     """Walk drafted trees against target_probs [n, nodes, V] (fp32; draft_probs alike or None) with given random
     numbers; fills path [n, nodes], counts [n] and next_token [n] (int32)."""
     where = "qnre_verify_tree"
-    if _float32 is None:
-        _load_dtypes()
-    if target_probs.dim() != 3:
+    shape = _sizes(target_probs)
+    if len(shape) != 3:
         raise QnreError(1, f"{where}: target_probs must be [n, nodes, vocab]")
-    n, nodes, vocab = target_probs.shape
+    n, nodes, vocab = shape
     rows = []
     for t in (target_probs, draft_probs):
+        p = None if t is None or _native is None else _native.pointer(t, 2, n, nodes, vocab)
         if t is None:
             rows += [None, 0, 0]
-            continue
-        if t.dtype is not _float32 or t.shape != target_probs.shape or (t.stride(2) != 1 and vocab > 1):
-            raise QnreError(1, f"{where}: probabilities are float32 [n, nodes, vocab], each row contiguous")
-        rows += [t.data_ptr(), t.stride(0), t.stride(1)]
+        elif p is not None:
+            rows += [p, nodes * vocab, vocab]
+        else:
+            if _float32 is None:
+                _load_dtypes()
+            if t.dtype is not _float32 or t.shape != shape or (t.stride(2) != 1 and vocab > 1):
+                raise QnreError(1, f"{where}: probabilities are float32 [n, nodes, vocab], each row contiguous")
+            rows += [t.data_ptr(), t.stride(0), t.stride(1)]
     _check(load_library().qnre_verify_tree(
         *rows, n, nodes, vocab, _i32(where, tokens, n, nodes), _i32(where, parents, n, nodes),
         _i32(where, node_counts, n), _f32(where, accept_u, n, nodes), _f32(where, sample_u, n),

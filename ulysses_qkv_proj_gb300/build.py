@@ -15,12 +15,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libqnre.so")
+MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
 DEBUG_BUILD_DIR = os.path.join(HERE, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(HERE, "libqnre_debug.so")
 
@@ -38,6 +40,29 @@ def _nvcc() -> str:
 
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+def build_marshal() -> str:
+    """Compile _marshal.so (csrc/marshal.cpp), the binding's native reads of torch tensors.  Returns its path, or
+    "" where torch's or Python's headers are missing: the binding then reads tensors in Python."""
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError:
+        return ""
+    includes = [sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    if not os.path.exists(os.path.join(includes[0], "Python.h")) or shutil.which("g++") is None:
+        return ""
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{i}" for i in includes], "-w", os.path.join(CSRC, "marshal.cpp"), "-o", tmp, f"-L{libs}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{libs}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, MARSHAL_PATH)
+    return MARSHAL_PATH
 
 
 def build(verbose: bool = False, ptxas_info: bool = False, debug_bounds: bool = False) -> str:
@@ -63,8 +88,11 @@ def build(verbose: bool = False, ptxas_info: bool = False, debug_bounds: bool = 
             sys.stdout.write(res.stdout + res.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        marshal = None if debug_bounds else ex.submit(build_marshal)
         objs = list(ex.map(compile_one, srcs))
+        if marshal is not None:
+            marshal.result()
     tmp = lib_path + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     res = subprocess.run(cmd, capture_output=True, text=True)
