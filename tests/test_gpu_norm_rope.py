@@ -248,3 +248,31 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     ref = D.norm_rope(again[:, :, :8], qw, cs.cpu(), torch.arange(64)[None], "rotate_half")
     _close(out[:, :, :8], ref, _fwd_tol(ref, again[:, :, :8], qw, cs.cpu(), "rotate_half", dt), "graph")
+
+
+def test_gradient_replays_from_a_graph():
+    """A captured gradient gives the eager one's bits on new inputs."""
+    qb, dt = _qb(), torch.bfloat16
+    proj, qw, kw, gen = _inputs(2, 90, 8, 2, 128, dt, 9)
+    g = torch.randn((2, 90, 10, 128), generator=gen).to(dt).cuda()
+    d, cs, w = proj.cuda(), D.angles(90, 128).cuda(), (qw.cuda(), kw.cuda())
+    ws = qb.qk_norm_rope_workspace(d)
+
+    def run(out):
+        qb.qnre_qk_norm_rope_backward(g[:, :, :8], g[:, :, 8:], d[:, :, :8], d[:, :, 8:10], *w, cs, None, *out, ws)
+
+    make = lambda: [torch.empty((2, 90, 8, 128), dtype=dt, device="cuda"), torch.empty((2, 90, 2, 128), dtype=dt, device="cuda"),
+                    torch.empty(128, device="cuda"), torch.empty(128, device="cuda")]
+    captured, eager = make(), make()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run(captured)
+    again, _, _, gen = _inputs(2, 90, 8, 2, 128, dt, 10)
+    d.copy_(again)
+    g.copy_(torch.randn((2, 90, 10, 128), generator=gen).to(dt))
+    graph.replay()
+    run(eager)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(captured, eager))

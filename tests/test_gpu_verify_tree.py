@@ -152,3 +152,25 @@ def test_masks(n, N):
     assert depths.tolist() == [w[1] for w in want]
     qb.qnre_tree_masks(par, depths=depths)
     qb.qnre_tree_masks(par, masks)
+
+
+def test_replay_from_a_graph():
+    from ulysses_qkv_proj_gb300 import binding as qb
+    n, N, V = 6, 9, 20011
+    args = [_inputs(n, N, V, 2, seed) for seed in (11, 12)]
+    dev = lambda a: [torch.from_numpy(np.ascontiguousarray(a[0])).cuda(), torch.from_numpy(np.ascontiguousarray(a[1])).cuda(),
+                     torch.tensor(a[2], dtype=torch.int32).cuda(), torch.tensor(a[3], dtype=torch.int32).cuda(),
+                     torch.from_numpy(a[4]).cuda(), torch.from_numpy(a[5]).cuda()]
+    first, second = dev(args[0]), dev(args[1])
+    out = [torch.empty((n, N), dtype=torch.int32).cuda(), torch.empty(n, dtype=torch.int32).cuda(),
+           torch.empty(n, dtype=torch.int32).cuda()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        qb.qnre_verify_tree(*first, *out)
+    for a, b in zip(first, second):
+        a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert [t.tolist() for t in out] == [*_run(*args[1])]
