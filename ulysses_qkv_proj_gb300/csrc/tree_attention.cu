@@ -575,6 +575,8 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
       uint32_t v[kCols / 32][32];
+      // P's buffer is free once the product two tiles back is done (long ago, by now)
+      wait(bars.pvdone + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
       wait(bars.sfull + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status);
       __syncwarp();  // the tensor-memory instructions are warp-wide
       ptx::tc_fence_after_sync();
@@ -655,10 +657,6 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         unpair(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
       }
-      // P's buffer is free once the product two tiles back is done
-      wait(bars.pvdone + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
-      __syncwarp();
-      ptx::tc_fence_after_sync();
       const uint32_t pt = tmem + lane_base + kTmemP + b * 64 + c0 / 2;
       if (kCols == 64) {
         tmem_st_x32(pt, p);
