@@ -31,12 +31,13 @@
 //
 // Bound: HBM up to 128 rows; above, the bytes that enter an SM (64 KB of K and V a tile of 1024 cycles of
 // tensor work, at 34 bytes a cycle and SM).  Measured (device time): 64 requests of 130..32000 tokens, 64 heads on 8,
-// D = 128 bf16: 234 us, 6.68 TB/s; 16 trees of 32 nodes over 900..16001 tokens: 91 us, 1.0 PFLOP/s; 6 trees of 61
-// nodes, D = 64 fp16: 37 us; one request of 4097 tokens, 32 heads on 8: 14 us, of which the join is four.  Steps, in
+// D = 128 bf16: 234 us, 6.68 TB/s; 16 trees of 32 nodes over 900..16001 tokens: 86 us, 1.07 PFLOP/s; 6 trees of 61
+// nodes, D = 64 fp16: 37 us; one request of 4097 tokens, 32 heads on 8: 13 us, of which the join is three.  Steps, in
 // that order: first form 431 / 229 / 270 / 20.6; Q by TMA, scores of the next unit before the last product, masks as
 // words, a unit's cost in the split 258 / 147 / 50 / 17; two issuing threads, descriptors by one add 239 / 142 / 50 /
 // 17; multicast, page numbers ahead - / 109 / 48 / 15.3; three tiles of K and of V in flight 237 / 100 / 48 / 15.2;
-// cheaper unit ends, a unit's cost four tiles (2: 102 / 53, 8: 100 / 48 cold) 234 / 91 / 37 / 14.3.  Tried and left: Q in
+// cheaper unit ends, a unit's cost four tiles (2: 102 / 53, 8: 100 / 48 cold) 234 / 91 / 37 / 14.3; eight warps a row in
+// the join of few rows, its parts counted beforehand 234 / 86 / 37 / 13.2.  Tried and left: Q in
 // tensor memory with P over S (108) or one P buffer (106), the pass with a standing maximum 32 columns at a time
 // (101), a CTA pair multiplying as one (98).
 #include "../../include/qnre.h"
@@ -71,10 +72,9 @@ constexpr int kMaxCluster = 4;  // row tiles that share K and V
 constexpr int kUnitCost = 4;  // a unit's start and end, in tiles
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that O is rescaled at
 
-// A unit that spans clusters, written by its second one for combine_kernel: cluster c's run starts at
-// c * quot + c * rem / clusters.
+// A unit that spans clusters c0 .. c0 + parts - 1, written by its second one for combine_kernel.
 struct Desc {
-  int valid, req, kvh, rt, c0, last, quot, rem;
+  int parts, req, kvh, rt, c0, pad[3];
 };
 
 struct AttnArgs {
@@ -913,7 +913,14 @@ __global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __gri
     if (look.next(s) && s.t0 > 0) {
       const int tiles = Cursor::tiles_of(s.total);
       const int first = pre[s.req] + (s.kvh * a.row_groups + s.rt / a.cl) * (tiles + kUnitCost) + kUnitCost;
-      if (first >= start_of(cluster - 1)) d = Desc{1, s.req, s.kvh, s.rt, cluster - 1, first + tiles - 1, quot, rem};
+      if (first >= start_of(cluster - 1)) {
+        int lo = cluster, hi = clusters - 1;  // the last cluster whose run starts by its last tile
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (start_of(mid) <= first + tiles - 1) lo = mid; else hi = mid - 1;
+        }
+        d = Desc{lo - cluster + 2, s.req, s.kvh, s.rt, cluster - 1, {0, 0, 0}};
+      }
     }
     a.desc[blockIdx.x] = d;
     run_outputs<L, D, BF16, MC>(a, bars, smem, tmem, cur, &words->abort);
@@ -932,34 +939,31 @@ __global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __gri
   }
 }
 
-// Joins the parts of the units that span CTAs: block x is the unit's second CTA, a warp a row.
-template <int D, bool BF16>
+// Joins the parts of the units that span CTAs: block x is the unit's second CTA; WARPS warps a row, each with every
+// WARPS-th part, so that a row of many parts (few rows of a long context) costs one round of loads.
+template <int D, bool BF16, int WARPS>
 __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const float* part_ml, const float* part_o,
                                                       char* out, float* lse, int nodes, int Hq, int G, int unit_nodes,
                                                       int cl) {
   constexpr int kPer = D / 32;
+  __shared__ float join[WARPS > 1 ? WARPS : 1][D + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Desc d = desc[blockIdx.x];
-  if (!d.valid) return;
-  const int lane = threadIdx.x % 32, r = blockIdx.y * 8 + threadIdx.x / 32;
+  if (d.parts == 0) return;
+  const int lane = threadIdx.x % 32, sub = threadIdx.x / 32 % WARPS;
+  const int r = blockIdx.y * (8 / WARPS) + threadIdx.x / 32 / WARPS;  // with WARPS = 8 the same for a whole block
   const int node = d.rt * unit_nodes + r / G, head = d.kvh * G + r % G;
   if (r >= unit_nodes * G || node >= nodes) return;
-  // its clusters: those whose run starts by its last tile
-  const int clusters = gridDim.x / cl;
-  int parts = 1;
-  for (int c = d.c0 + 1 + lane; c < clusters; c += 32)
-    parts += c * d.quot + c * d.rem / clusters <= d.last ? 1 : 0;
-  parts = __reduce_add_sync(0xFFFFFFFFu, parts) - 31;
   const int rank = blockIdx.x % cl;
   auto row_of = [&](int i) { return static_cast<long long>(2 * ((d.c0 + i) * cl + rank) + (i == 0 ? 1 : 0)) * 128 + r; };
   float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, part_ml[2 * row_of(i)]);
+  for (int i = lane; i < d.parts; i += 32) M = fmaxf(M, part_ml[2 * row_of(i)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
   float acc[kPer] = {}, l = 0.f;
 #pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
+  for (int i = sub; i < d.parts; i += WARPS) {
     const long long at = row_of(i);
     const float2 ml = reinterpret_cast<const float2*>(part_ml)[at];
     const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
@@ -975,6 +979,22 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
       const float2 v = *reinterpret_cast<const float2*>(o);
       acc[0] = fmaf(v.x, w, acc[0]);
       acc[1] = fmaf(v.y, w, acc[1]);
+    }
+  }
+  if (WARPS > 1) {  // the warps' sums, in their order
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) join[sub][e * 32 + lane] = acc[e];
+    if (lane == 0) join[sub][D] = l;
+    __syncthreads();
+    if (sub != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      l += join[k][D];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += join[k][e * 32 + lane];
     }
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
@@ -1030,11 +1050,15 @@ qnre_status_t launch_attention(const AttnArgs& a, int sms, cudaStream_t stream) 
   }
   cfg.gridDim = dim3(ctas);
   if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return QNRE_ERR_CUDA;
-  cfg.gridDim = dim3(ctas, (std::min(a.nodes, a.unit_nodes) * a.G + 7) / 8);
+  const int rows = std::min(a.nodes, a.unit_nodes) * a.G;
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return from_cuda(cudaLaunchKernelEx(&cfg, combine_kernel<D, BF16>, static_cast<const Desc*>(a.desc),
+  // Up to 32 rows a unit leave the machine room for eight warps a row: one request 13.2 us against 15.2, while units
+  // of 61 rows take 42 against 37.
+  const auto join = rows <= 32 ? combine_kernel<D, BF16, 8> : combine_kernel<D, BF16, 1>;
+  cfg.gridDim = dim3(ctas, rows <= 32 ? rows : (rows + 7) / 8);
+  return from_cuda(cudaLaunchKernelEx(&cfg, join, static_cast<const Desc*>(a.desc),
                                       static_cast<const float*>(a.part_ml), static_cast<const float*>(a.part_o), a.out,
                                       a.lse, a.nodes, a.Hq, a.G, a.unit_nodes, a.cl));
 }
