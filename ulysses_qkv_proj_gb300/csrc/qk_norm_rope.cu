@@ -15,8 +15,9 @@
 // packed, four blocks of 256 threads a SM, 217; the first loads issued before the position's angles are
 // asked for, 209; one resident wave that strides over the items, 199 (three blocks 215, two 268; 128-thread
 // blocks 205; streaming stores +2 %).  The gradient (18881 tokens of 70 heads, fp16, 1.02 GB): 282 us
-// with plain loads, 209 with the next heads' loads in flight, 182 packed with all heads of a token in one
-// item; two blocks a SM (three 197, four spill: 272).
+// with plain loads, 209 with the next heads' loads in flight, 183 packed with all heads of a token in one
+// item, 175 with the loads through a ring in shared memory (two stages of 16 KB a block in flight; three
+// blocks a SM 185, four 246; 16 heads an item 174, 8 205), 164 back to back on warm pages (178 before).
 #include "../../include/qnre.h"
 #include "cache.cuh"
 
@@ -300,64 +301,120 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
   }
 }
 
-// Gradient.  The same items; each thread sums dw of its channels over its items, the block
-// sums its threads in a fixed order and leaves one partial row for grad_weights_kernel.
+// 16 bytes from global to this lane's place in shared memory, in flight until waited for; zeros where !live.
+__device__ __forceinline__ void copy_async(uint32_t dst, const char* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+// Gradient.  An item is a token's run of heads, taken kRows * kUnroll heads a step; the steps of all of a warp's items
+// follow one another through a ring of kStages in shared memory (a lane reads back only what it asked for itself), so
+// that loads of two or three steps are in flight whatever the registers hold.  Each thread sums dw of its channels
+// over its items, the block sums its threads in a fixed order and leaves one partial row for grad_weights_kernel.
 template <int D, bool BF16, bool RH>
 __global__ void __launch_bounds__(kThreads, 2) norm_rope_grad_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = 2;
-  __shared__ float sums[kThreads / 32 * kRows][D];
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = 2, kStep = kRows * kUnroll, kStages = 3;
+  // [warp][stage][x or g][head of the step][lane]; afterwards the threads' sums [warp * kRows][D]
+  __shared__ uint4 ring[kThreads / 32][kStages][2][kUnroll][32];
+  static_assert(sizeof(ring) >= kThreads / 32 * kRows * D * sizeof(float), "the sums fit in the ring");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % 32, l = lane % kLanes, sub = lane / kLanes, warp = threadIdx.x / 32;
+  const uint32_t place = static_cast<uint32_t>(__cvta_generic_to_shared(&ring[warp][0][0][0][lane]));
+  constexpr uint32_t kStageBytes = sizeof(ring[0][0]), kSideBytes = sizeof(ring[0][0][0]), kHeadBytes = sizeof(ring[0][0][0][0]);
   for (int kind = 0; kind < 2; ++kind) {
     const int chunks = kind == 0 ? a.cq : a.ck, step = kind == 0 ? a.hq : a.hk, heads = kind == 0 ? a.Hq : a.Hk;
     const View& in = kind == 0 ? a.q : a.k;
     const View& grad = kind == 0 ? a.gq : a.gk;
     const View& out = kind == 0 ? a.q_out : a.k_out;
+    const long long x_step = in.sh * kRows, g_step = grad.sh * kRows, o_step = out.sh * kRows;
     Pairs dw = {0, 0, 0, 0};
     const long long items = static_cast<long long>(a.B) * a.S * chunks;
     const long long stride = static_cast<long long>(gridDim.x) * (kThreads / 32);
+    // k's items from the other end: the warps that had one of q's more than others get one of k's less
+    const long long place_of = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp;
+    const long long first = kind == 0 ? place_of : stride - 1 - place_of;
     Pairs w;
     unpack<BF16>(__ldg(static_cast<const uint4*>(kind == 0 ? a.wq : a.wk) + l), w);
-    for (long long it = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp; it < items; it += stride) {
-      const long long token = it / chunks;
-      const int chunk = static_cast<int>(it - token * chunks);
-      const int b = static_cast<int>(token / a.S), s = static_cast<int>(token - static_cast<long long>(b) * a.S);
-      const int h0 = chunk * step, h1 = min(h0 + step, heads);
-      const long long pos = a.positions != nullptr ? a.positions[token] : s;
+
+    struct Item {
+      long long token;
+      int b, s, h0, h1;
+    };
+    auto item_of = [&](long long it) {
+      Item r;
+      r.token = it / chunks;
+      const int chunk = static_cast<int>(it - r.token * chunks);
+      r.b = static_cast<int>(r.token / a.S);
+      r.s = static_cast<int>(r.token - static_cast<long long>(r.b) * a.S);
+      r.h0 = chunk * step;
+      r.h1 = min(r.h0 + step, heads);
+      return r;
+    };
+    // the step to be asked for next
+    long long ask_it = first;
+    int ask_h = 0, ask_h1 = 0;
+    const char *px = nullptr, *pg = nullptr;
+    auto begin = [&] {
+      if (ask_it >= items) return;
+      const Item r = item_of(ask_it);
+      ask_h = r.h0 + sub;
+      ask_h1 = r.h1;
+      px = in.row(r.b, r.s, ask_h) + 16 * l;
+      pg = grad.row(r.b, r.s, ask_h) + 16 * l;
+    };
+    uint32_t ask_stage = 0, stage = 0;
+    auto ask = [&] {
+      if (ask_it < items) {
+        const uint32_t at = place + ask_stage * kStageBytes;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const bool live = ask_h + u * kRows < ask_h1;
+          copy_async(at + u * kHeadBytes, live ? px : in.data, live);
+          copy_async(at + kSideBytes + u * kHeadBytes, live ? pg : grad.data, live);
+          px += x_step;
+          pg += g_step;
+        }
+        ask_h += kStep;
+        if (ask_h - sub >= ask_h1) {
+          ask_it += stride;
+          begin();
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ask_stage = ask_stage + 1 == kStages ? 0 : ask_stage + 1;
+    };
+    begin();
+    for (int i = 0; i < kStages - 1; ++i) ask();
+
+    for (long long it = first; it < items; it += stride) {
+      const Item r = item_of(it);
+      const long long pos = a.positions != nullptr ? a.positions[r.token] : r.s;
       const bool bad = pos < 0 || pos >= a.n_pos;
       const Angles ang = load_angles<RH, true>(a.cos_sin + (bad ? 0 : pos) * a.rot, a.rot, l, lane);
       Pairs c, sn;
       pairs_of(ang.c, c);
       pairs_of(ang.s, sn);
-      const char* px = in.row(b, s, h0 + sub) + 16 * l;
-      const char* pg = grad.row(b, s, h0 + sub) + 16 * l;
-      char* po = out.row(b, s, h0 + sub) + 16 * l;
-      const long long x_step = in.sh * kRows, g_step = grad.sh * kRows, o_step = out.sh * kRows;
-      // the next heads' loads are in flight while these are worked on
-      uint4 xr[kUnroll], gr[kUnroll], xn[kUnroll], gn[kUnroll];
-      auto load = [&](int h, uint4 (&xs)[kUnroll], uint4 (&gs)[kUnroll]) {
+      char* po = out.row(r.b, r.s, r.h0 + sub) + 16 * l;
+      for (int h = r.h0 + sub; h - sub < r.h1; h += kStep) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        const uint4(*here)[kUnroll][32] = ring[warp][stage];
+        uint4 xr[kUnroll], gr[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const bool live = h + u * kRows < h1;
-          xs[u] = live ? __ldcs(reinterpret_cast<const uint4*>(px)) : make_uint4(0, 0, 0, 0);
-          gs[u] = live ? __ldcs(reinterpret_cast<const uint4*>(pg)) : make_uint4(0, 0, 0, 0);
-          px += x_step;
-          pg += g_step;
+          xr[u] = here[0][u][lane];
+          gr[u] = here[1][u][lane];
         }
-      };
-      load(h0 + sub, xr, gr);
-      for (int h = h0 + sub; h - sub < h1; h += kRows * kUnroll) {
-        load(h + kRows * kUnroll, xn, gn);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        ask();
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          const bool live = h + u * kRows < h1;
+          const bool live = h + u * kRows < r.h1;
           Pairs x, g, gp, o;
           unpack<BF16>(xr[u], x);
           unpack<BF16>(gr[u], g);
-          float r = rsqrtf(row_sum<kLanes>(dot(x, x)) * (1.0f / D) + kEps);
-          if (bad && live) r = __uint_as_float(0x7FC00000u);
-          const uint64_t r2 = pair(r, r);
+          float rs = rsqrtf(row_sum<kLanes>(dot(x, x)) * (1.0f / D) + kEps);
+          if (bad && live) rs = __uint_as_float(0x7FC00000u);
+          const uint64_t r2 = pair(rs, rs);
           other_channels<RH, BF16>(gr[u], ang, gp);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -373,13 +430,11 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_grad_kernel(const __gri
           if (live) *reinterpret_cast<uint4*>(po) = pack<BF16>(o);
           po += o_step;
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          xr[u] = xn[u];
-          gr[u] = gn[u];
-        }
       }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // every warp is done with the ring
+    float(*sums)[D] = reinterpret_cast<float(*)[D]>(ring);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float2*>(&sums[warp * kRows + sub][8 * l + 2 * i]) = halves(dw[i]);
