@@ -31,15 +31,16 @@
 //
 // Bound: HBM up to 128 rows; above, the bytes that enter an SM (64 KB of K and V a tile of 1024 cycles of
 // tensor work, at 34 bytes a cycle and SM).  Measured (device time): 64 requests of 130..32000 tokens, 64 heads on 8,
-// D = 128 bf16: 234 us, 6.68 TB/s; 16 trees of 32 nodes over 900..16001 tokens: 86 us, 1.07 PFLOP/s; 6 trees of 61
+// D = 128 bf16: 234 us, 6.68 TB/s; 16 trees of 32 nodes over 900..16001 tokens: 84 us, 1.10 PFLOP/s; 6 trees of 61
 // nodes, D = 64 fp16: 37 us; one request of 4097 tokens, 32 heads on 8: 13 us, of which the join is three.  Steps, in
 // that order: first form 431 / 229 / 270 / 20.6; Q by TMA, scores of the next unit before the last product, masks as
 // words, a unit's cost in the split 258 / 147 / 50 / 17; two issuing threads, descriptors by one add 239 / 142 / 50 /
 // 17; multicast, page numbers ahead - / 109 / 48 / 15.3; three tiles of K and of V in flight 237 / 100 / 48 / 15.2;
 // cheaper unit ends, a unit's cost four tiles (2: 102 / 53, 8: 100 / 48 cold) 234 / 91 / 37 / 14.3; eight warps a row in
-// the join of few rows, its parts counted beforehand 234 / 86 / 37 / 13.2.  Tried and left: Q in
-// tensor memory with P over S (108) or one P buffer (106), the pass with a standing maximum 32 columns at a time
-// (101), a CTA pair multiplying as one (98).
+// the join of few rows, its parts counted beforehand 234 / 87 / 37 / 13.2; parts of more than 64 rows written eight
+// rows to a line - / 84 / - / -.  Tried and left: Q in tensor memory with P over S (108) or one P buffer (106), the pass
+// with a standing maximum 32 columns at a time (101), a CTA pair multiplying as one (98), two row tiles a CTA on the same
+// K and V (117: P lies in S's place, so each tile is product, scores, softmax in a row, 4170 cycles for the two).
 #include "../../include/qnre.h"
 #include "cache.cuh"
 #include "ptx.cuh"
@@ -87,7 +88,7 @@ struct AttnArgs {
   float* lse;
   Desc* desc;
   float* part_ml;  // [2 * kMaxCtas][128][2]: maximum (base 2), sum
-  float* part_o;   // [2 * kMaxCtas][128][D]
+  float* part_o;   // [2 * kMaxCtas] of 128 rows of D, laid out by part_at
   float scale_log2;
   int layer, n, nodes, Hq, Hk, G, unit_nodes, row_groups, box, cl;  // cl: CTAs a cluster, row tiles a group
 };
@@ -123,6 +124,15 @@ struct Words {
 struct Bars {
   uint32_t kfull, kempty, vfull, vempty, qfull, qempty, sfull, sfree, pready, pvdone, ofree, drain, drain2;
 };
+
+// Where columns [4 * i, 4 * i + 4) of row r of a part lie, in 16-byte pieces.  The threads that write hold a row each, so
+// GROUPED has eight rows side by side, 128 bytes, and a warp's store touches 4 lines instead of 32; with few rows the
+// join wants a row's columns together.
+template <int D, bool GROUPED>
+__device__ __forceinline__ long long part_at(int slot, int r, int i) {
+  return GROUPED ? ((static_cast<long long>(slot) * 16 + r / 8) * (D / 4) + i) * 8 + r % 8
+                 : (static_cast<long long>(slot) * 128 + r) * (D / 4) + i;
+}
 
 // One unit's part of a CTA's run.
 struct Seg {
@@ -764,9 +774,11 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
           dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       } else if (in_out) {
-        float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c + jc);
+        float4* dst = reinterpret_cast<float4*>(a.part_o);
 #pragma unroll
-        for (int i = 0; i < kPer / 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        for (int i = 0; i < kPer / 4; ++i)
+          dst[part_at<D, REP == 1>(s.slot, ur, (c + jc) / 4 + i)] =
+              make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
       }
       __syncwarp();
     }
@@ -939,12 +951,13 @@ __global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __gri
   }
 }
 
-// Joins the parts of the units that span CTAs: block x is the unit's second CTA; WARPS warps a row, each with every
-// WARPS-th part, so that a row of many parts (few rows of a long context) costs one round of loads.
+// Joins the parts of the units that span CTAs: block x is the unit's second CTA.
+// Up to 64 rows: WARPS warps a row, each with every WARPS-th part, so that a row of many parts (few rows of a long
+// context) costs one round of loads.
 template <int D, bool BF16, int WARPS>
-__global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const float* part_ml, const float* part_o,
-                                                      char* out, float* lse, int nodes, int Hq, int G, int unit_nodes,
-                                                      int cl) {
+__global__ void __launch_bounds__(256) combine_few_kernel(const Desc* desc, const float* part_ml, const float* part_o,
+                                                          char* out, float* lse, int nodes, int Hq, int G,
+                                                          int unit_nodes, int cl) {
   constexpr int kPer = D / 32;
   __shared__ float join[WARPS > 1 ? WARPS : 1][D + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1005,6 +1018,61 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
   if (lse != nullptr && lane == 0) lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
+// More rows: a thread has four columns of a row, a warp eight rows' (one line of a part each load and four columns).
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const float* part_ml, const float* part_o,
+                                                      char* out, float* lse, int nodes, int Hq, int G, int unit_nodes,
+                                                      int cl) {
+  constexpr int kWarps = D / 16;  // that share eight rows
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Desc d = desc[blockIdx.x];
+  if (d.parts == 0) return;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int r = (blockIdx.y * (8 / kWarps) + warp / kWarps) * 8 + lane % 8, i4 = warp % kWarps * 4 + lane / 8;
+  const int node = d.rt * unit_nodes + r / G, head = d.kvh * G + r % G;
+  if (r >= unit_nodes * G || node >= nodes) return;
+  const int rank = blockIdx.x % cl;
+  auto slot_of = [&](int i) { return 2 * ((d.c0 + i) * cl + rank) + (i == 0 ? 1 : 0); };
+  const float2* mls = reinterpret_cast<const float2*>(part_ml);
+  float M = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < d.parts; i0 += 4) {  // four parts' loads at once
+    float2 ml[4];
+    float4 v[4];
+    float mx = M;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool there = i0 + k < d.parts;
+      const int slot = slot_of(there ? i0 + k : i0);
+      ml[k] = mls[slot * 128 + r];
+      v[k] = reinterpret_cast<const float4*>(part_o)[part_at<D, true>(slot, r, i4)];
+      if (!there) ml[k].x = -INFINITY;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, ml[k].x);
+    const float f = M == -INFINITY ? 0.f : exp2_fast(M - mx);
+    M = mx;
+    l *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i0 + k >= d.parts) break;
+      const float w = ml[k].x == -INFINITY ? 0.f : exp2_fast(ml[k].x - M);
+      l = fmaf(ml[k].y, w, l);
+      acc.x = fmaf(v[k].x, w, acc.x);
+      acc.y = fmaf(v[k].y, w, acc.y);
+      acc.z = fmaf(v[k].z, w, acc.z);
+      acc.w = fmaf(v[k].w, w, acc.w);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const long long orow = (static_cast<long long>(d.req) * nodes + node) * Hq + head;
+  *reinterpret_cast<uint2*>(out + (orow * D + 4 * i4) * 2) =
+      make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+  if (lse != nullptr && i4 == 0) lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
 constexpr uint64_t kDescBytes = 152 * sizeof(Desc);
 constexpr uint64_t kMlBytes = 2ull * kMaxCtas * 128 * 2 * 4;
 
@@ -1055,9 +1123,13 @@ qnre_status_t launch_attention(const AttnArgs& a, int sms, cudaStream_t stream) 
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   // Up to 32 rows a unit leave the machine room for eight warps a row: one request 13.2 us against 15.2, while units
-  // of 61 rows take 42 against 37.
-  const auto join = rows <= 32 ? combine_kernel<D, BF16, 8> : combine_kernel<D, BF16, 1>;
-  cfg.gridDim = dim3(ctas, rows <= 32 ? rows : (rows + 7) / 8);
+  // of 61 rows take 42 against 37.  More than 64 rows: parts grouped by eight rows, 16 trees of 32 nodes 84 us against
+  // 87, units of 61 rows 38.2 against 37.2.
+  const auto join = REP == 4   ? combine_few_kernel<D, BF16, 8>
+                    : REP == 2 ? combine_few_kernel<D, BF16, 1>
+                               : combine_kernel<D, BF16>;
+  constexpr int kJoinRows = REP == 4 ? 1 : (REP == 2 ? 8 : 1024 / D);  // a block
+  cfg.gridDim = dim3(ctas, (rows + kJoinRows - 1) / kJoinRows);
   return from_cuda(cudaLaunchKernelEx(&cfg, join, static_cast<const Desc*>(a.desc),
                                       static_cast<const float*>(a.part_ml), static_cast<const float*>(a.part_o), a.out,
                                       a.lse, a.nodes, a.Hq, a.G, a.unit_nodes, a.cl));
