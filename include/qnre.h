@@ -574,7 +574,7 @@ typedef struct {
   int32_t* seq_lens;    /* [rows] */
   int32_t* page_refs;   /* [pages], 16-byte aligned */
   uint32_t* status;     /* [1], QNRE_CACHE_* bits */
-  int32_t* scratch;     /* 4 * pages + 4 words, overwritten by qnre_cache_reserve */
+  int32_t* scratch;     /* 4 * pages + 4 words, overwritten by qnre_cache_reserve; calls that may overlap do not share it */
   int32_t layers, pages, heads, page_size, head_dim, rows, max_blocks;
   int32_t dtype; /* QNRE_DTYPE_BF16 or QNRE_DTYPE_FP16 */
 } qnre_cache_t;
@@ -638,7 +638,8 @@ qnre_status_t qnre_cache_copy_pages(const qnre_cache_t* cache, const int32_t* sr
  *   be its gradient input exactly), and the fp32 [D] sums dq_norm_w, dk_norm_w over all
  *   tokens and heads, taken in a fixed order.  gq, gk: the output gradients (views).
  *   Rows at a bad position get NaN and make the weights' gradients NaN.
- *   workspace: qnre_qk_norm_rope_workspace_bytes(D), 16-byte aligned.
+ *   workspace: qnre_qk_norm_rope_workspace_bytes(D), 16-byte aligned, contents undefined before and after; calls
+ *   that may overlap (on different streams) need one each.
  *
  * qnre_qkv_norm_rope_append -- qnre_qk_norm_rope over the new tokens [n, S, ...] of the
  *   rows rows[i] (device int32 [n]), with k and v written into layer `layer` of the cache
@@ -679,7 +680,10 @@ qnre_status_t qnre_qkv_norm_rope_append(const qnre_tensor4_t* q, const qnre_tens
  *   scale    > 0, finite.
  *   out      device, contiguous [n, nodes, Hq, D] of the dtype, 16-byte aligned; a node that sees nothing gets 0.
  *   lse      device fp32 [n, nodes, Hq] or NULL: log of the softmax sum (-inf where nothing is seen).
- *   workspace  qnre_tree_attention_workspace_bytes(D), 16-byte aligned.
+ *   workspace  qnre_tree_attention_workspace_bytes(D), 16-byte aligned, contents undefined before and after; calls
+ *            that may overlap (on different streams) need one each.
+ * More than 2^31-1 tiles of 128 tokens (of max_blocks * page_size tokens a row, each K head and group of rows counted,
+ * four more a unit) -> QNRE_ERR_CAPACITY.
  * What lies in slots that a node does not see never reaches its result, not even NaN.
  * The result does not depend on timing: sums are taken in an order that the lengths fix.
  */
