@@ -271,3 +271,30 @@ def test_graph_replay_on_grown_rows():
     c.keys = [k[:L + 3] for k, L in zip(c.keys, c.lens)]
     c.values = [v[:L + 3] for v, L in zip(c.values, c.lens)]
     c.check(out.cpu(), lse.cpu())
+
+
+@pytest.mark.parametrize("lens,nodes,Hq,Hk,dtype", [
+    ([1000, 700, 1300, 128, 129, 1, 900, 1100], 2, 28, 14, "bf16"),  # runs of several tiles that span units, one tile alone
+    ([1500, 1023, 900, 255, 1, 640], 20, 28, 14, "fp16"),
+    ([384, 2, 1400, 900], 40, 14, 14, "fp16"),
+])
+def test_narrow_heads_over_runs_of_tiles(lens, nodes, Hq, Hk, dtype):
+    """D = 64, scores rising along the context; then a draft's infinite values, seen by itself alone."""
+    c = Case(lens, nodes, Hq, Hk, 64, 16, dtype, seed=21)
+    for i, L in enumerate(lens):
+        T = L + nodes
+        ramp = torch.linspace(-2.0, 5.0, T)[:, None, None]
+        c.keys[i] = (c.q[i, 0, ::Hq // Hk].float()[None] * ramp * 0.4).to(c.dt)
+        for x in range(T):
+            c.k[1, c.table[c.rows[i], x // 16], :, x % 16] = c.keys[i][x]
+    c.masks = [[1 << t for t in range(nodes)] for _ in lens]
+    clean = c.run()
+    c.check(*clean)
+    for i, L in enumerate(lens):
+        x = L + nodes - 1
+        c.v[1, c.table[c.rows[i], x // 16], :, x % 16, 33] = float("inf")
+    out, lse = c.run()
+    assert torch.equal(out[:, :-1], clean[0][:, :-1]) and torch.equal(lse, clean[1])
+    assert torch.isinf(out[:, -1, :, 33]).all()
+    cols = [x for x in range(64) if x != 33]
+    assert torch.equal(out[:, -1][..., cols], clean[0][:, -1][..., cols])

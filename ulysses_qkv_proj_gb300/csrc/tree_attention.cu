@@ -60,14 +60,21 @@ using namespace qnre;
 using namespace qnre::api;
 
 constexpr int kTile = 128;     // cached tokens a tile, rows a unit
-// Softmax warps: with REP = 1 two threads share a row, each half of a tile's tokens.  Then the K and V TMA warps and
-// the warps that issue S and O products.
-template <int REP>
-constexpr int kSoftThreads = REP == 1 ? 256 : 128;
-template <int REP>
-constexpr int kThreads = kSoftThreads<REP> + 128;
+// Softmax warps: with REP = 1 two threads share a row, each half of a tile's tokens.  Else one thread a row and copy,
+// and at D = 64, where a tile's bytes arrive faster than four warps finish its softmax (1400 cycles against 1800), two
+// groups of four warps that take alternate tiles, each with an O of its own (at D = 128 tensor memory has no room for a
+// second, and a tile's bytes take 2800 cycles).  32 requests of 130..16000 tokens, 64 heads on 8: 45.2 us against 48.6
+// with one group, 4 trees of 40 nodes, 14 heads: 32.3 against 37.0, one request of 4097 tokens 11.1 against 10.9; at
+// REP = 1 two groups are slower (16 trees of 32 nodes, 32 heads on 8: 45.5 against 43.3).  Then the K and V TMA warps
+// and the warps that issue S and O products.
+template <int D, int REP>
+constexpr int kGroups = D == 64 && REP > 1 ? 2 : 1;
+template <int D, int REP>
+constexpr int kSoftThreads = REP == 1 ? 256 : 128 * kGroups<D, REP>;
+template <int D, int REP>
+constexpr int kThreads = kSoftThreads<D, REP> + 128;
 constexpr int kMaxCtas = 152;  // one a SM
-constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D, P 2 x 64
+constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D or 2 x 64, P 2 x 64
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 constexpr int kMaxCluster = 4;  // row tiles that share K and V
 constexpr int kUnitCost = 4;  // a unit's start and end, in tiles
@@ -105,19 +112,20 @@ struct Smem {
   static constexpr int kQ = 0;
   static constexpr int kK = kTileBytes;
   static constexpr int kV = kK + kKStages * kTileBytes;
-  static constexpr int kJoin = kV + kVStages * kTileBytes;               // REP > 1: float [128][33]
-  static constexpr int kMl = kJoin + (REP > 1 ? 128 * 33 * 4 : 0);       // float [128][2]; REP = 1: [2][2][128]
-  static constexpr int kLen = kMl + (REP > 1 ? 128 * 2 * 4 : 2048);      // int2 [kRequests]
+  static constexpr int kSoft = kSoftThreads<D, REP>;
+  static constexpr int kJoin = kV + kVStages * kTileBytes;               // REP > 1: float [kSoft][33]
+  static constexpr int kMl = kJoin + (REP > 1 ? kSoft * 33 * 4 : 0);     // float [kSoft][2]; REP = 1: [2][2][128]
+  static constexpr int kLen = kMl + (REP > 1 ? kSoft * 2 * 4 : 2048);    // int2 [kRequests]
   static constexpr int kPre = kLen + kRequests * 8;                      // int [kRequests + 1]
   static constexpr int kBars = (kPre + (kRequests + 1) * 4 + 15) / 16 * 16;
   static constexpr int kWords = kBars + 8 * (2 * kKStages + 2 * kVStages + 13);
-  static constexpr int kBytes = kWords + 24;
+  static constexpr int kBytes = kWords + 32;
   static_assert(kBytes <= 232448, "one CTA's shared memory");
 };
 
 // Words shared by the roles.
 struct Words {
-  unsigned long long bad_nodes[2];  // drafts with non-finite V elements, of even and odd segments
+  unsigned long long bad_nodes[3];  // drafts with non-finite V elements, segments in turn
   uint32_t tmem, abort;
 };
 
@@ -192,9 +200,9 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
 }
 
 // Among the softmax threads; among the two warps that share 32 rows.
-template <int REP>
+template <int THREADS>
 __device__ __forceinline__ void soft_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads<REP>) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 __device__ __forceinline__ void pair_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory"); }
 
@@ -418,8 +426,8 @@ __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, u
   }
 }
 
-// O += P V, tile after tile.
-template <typename L, int D, bool BF16, bool MC>
+// O += P V, tile after tile; with two groups of softmax warps even and odd tiles each have an O.
+template <typename L, int D, bool BF16, bool MC, int GROUPS>
 __device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
                             volatile uint32_t* abort_flag) {
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
@@ -441,8 +449,8 @@ __device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, 
       const uint64_t v = desc_at(ring0, slot * L::kTileBytes);
 #pragma unroll
       for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_f16_ts(tmem + kTmemO, tmem + kTmemP + b * 64 + kk * 8, desc_at(v, kk * 2048), kIdesc,
-                    (!first || kk > 0) ? 1u : 0u);
+        umma_f16_ts(tmem + kTmemO + (GROUPS == 2 ? b * 64 : 0), tmem + kTmemP + b * 64 + kk * 8, desc_at(v, kk * 2048),
+                    kIdesc, (t - s.t0 >= GROUPS || kk > 0) ? 1u : 0u);
       ptx::umma_commit(bars.pvdone + 8 * b);
       if (MC)
         umma_commit_multicast(bars.vempty + 8 * slot, everyone);
@@ -536,9 +544,13 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
   constexpr int kCols = kSplit ? 64 : kTile / REP;  // tokens of a tile this thread looks at
   constexpr int kRows = 128 / REP;     // unit rows
   constexpr int kOut = kSplit ? D / 2 : D;  // columns of O this thread scales and writes
+  constexpr int kTwo = kGroups<D, REP> == 2, kSoft = kSoftThreads<D, REP>;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int ur = tid % kRows, copy = tid / kRows, c0 = copy * kCols;
+  const uint32_t group = kTwo ? tid / 128 : 0;  // of alternate tiles
+  const int ur = tid % kRows, copy = (kSplit ? tid : tid % 128) / kRows, c0 = copy * kCols;
+  const int part = tid / kRows;  // of a row's results
   const int o0 = kSplit ? copy * kOut : 0;
+  const uint32_t o_at = kTmemO + group * 64;
   const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
   float* join = reinterpret_cast<float*>(smem_base + L::kJoin);
   float* ml = reinterpret_cast<float*>(smem_base + L::kMl);
@@ -549,7 +561,7 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
 #pragma unroll
     for (int i = 0; i < 32; ++i) zero[i] = 0;
 #pragma unroll
-    for (int c = 0; c < 128; c += 32) tmem_st_x32(tmem + lane_base + kTmemP + c, zero);
+    for (int c = 0; c < (kTwo ? 64 : 128); c += 32) tmem_st_x32(tmem + lane_base + kTmemP + group * 64 + c, zero);
     tmem_st_wait();
   }
   const int ur_node = ur / a.G, ur_head = ur - ur_node * a.G;
@@ -584,8 +596,10 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
     float m = -INFINITY, l = 0.f;
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
+      if (kTwo && b != group) continue;
       uint32_t v[kCols / 32][32];
-      // P's buffer is free once the product two tiles back is done (long ago, by now)
+      // P's buffer is free once the product two tiles back is done (long ago, by now; with two groups, this
+      // group's last: waiting for it only before P is stored changes nothing)
       wait(bars.pvdone + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
       wait(bars.sfull + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status);
       __syncwarp();  // the tensor-memory instructions are warp-wide
@@ -626,25 +640,27 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         mx = fmaxf(mx, at[(copy ^ 1) * 128]);
       }
       const bool grow = mx > m + kRescale;
-      if (t == s.t0) {
+      if (t - s.t0 < (kTwo ? 2 : 1)) {
         m = mx;
       } else if (__any_sync(0xFFFFFFFFu, grow)) {
-        const uint32_t last = g - 1;
-        wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
-        __syncwarp();
-        ptx::tc_fence_after_sync();
+        if (!kTwo) {  // (else O's last product was two tiles back)
+          const uint32_t last = g - 1;
+          wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
+          __syncwarp();
+          ptx::tc_fence_after_sync();
+        }
         const float f = grow ? exp2_fast(m - mx) : 1.f;
         if (grow) m = mx;
         l *= f;
 #pragma unroll 1
         for (int c = o0; c < o0 + kOut; c += 32) {
           uint32_t o[32];
-          ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
+          ptx::tmem_ld_32x32b_x32(tmem + lane_base + o_at + c, o);
           ptx::tmem_ld_wait();
           tmem_fence_regs(o);
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st_x32(tmem + lane_base + kTmemO + c, o);
+          tmem_st_x32(tmem + lane_base + o_at + c, o);
         }
         tmem_st_wait();
       }
@@ -679,7 +695,7 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         const int x = tid % 128, pos = t * kTile + x, pieces = D / 8 / (kSplit ? 2 : 1);
         if (pos >= s.len && clean_v_row<D, BF16>(smem_base + L::kV + slot * L::kTileBytes + x * 128, pos < s.total,
                                                  kSplit ? copy * pieces : 0, (kSplit ? copy * pieces : 0) + pieces))
-          atomicOr(bad_nodes + (seg & 1u), 1ull << (pos - s.len));
+          atomicOr(bad_nodes + seg % 3, 1ull << (pos - s.len));
         __syncwarp();
       }
       tmem_st_wait();
@@ -701,13 +717,15 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       ml[2 * tid] = m;
       ml[2 * tid + 1] = l;
     }
-    const uint32_t last = g - 1;
-    wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
-    // every warp has come past the segment before: its word is the next one's
-    if (tid == 0) bad_nodes[(seg & 1u) ^ 1u] = 0;
-    soft_sync<REP>();
+    // this group's last product of the segment (a segment of one tile leaves the other group none)
+    const uint32_t last = kTwo && ((g - 1) & 1u) != group ? g - 2 : g - 1;
+    const bool any = !kTwo || last + (s.t1 - s.t0) + 1 > g;
+    if (any) wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
+    soft_sync<kSoft>();
     ptx::tc_fence_after_sync();
-    const uint64_t bad = row_ok ? bad_nodes[seg & 1u] & bits : 0;
+    // every warp has read the word of the segment before, and none uses it again before the next segment's end
+    if (tid == 0) bad_nodes[(seg + 2) % 3] = 0;
+    const uint64_t bad = row_ok ? bad_nodes[seg % 3] & bits : 0;
     float f = 1.f;  // of this copy's part
     if (kSplit) {
       l += ml[(g & 1u) * 256 + (tid ^ 128)];
@@ -715,9 +733,9 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
     } else {
       float M = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int c = 0; c < REP; ++c) M = fmaxf(M, ml[2 * (c * kRows + ur)]);
+      for (int c = 0; c < kSoft / kRows; ++c) M = fmaxf(M, ml[2 * (c * kRows + ur)]);
 #pragma unroll
-      for (int c = 0; c < REP; ++c) {
+      for (int c = 0; c < kSoft / kRows; ++c) {
         const float mc = ml[2 * (c * kRows + ur)];
         sum += ml[2 * (c * kRows + ur) + 1] * (mc == -INFINITY ? 0.f : exp2_fast(mc - M));
       }
@@ -728,12 +746,12 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
     const float inv = !s.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
     const long long orow = (static_cast<long long>(s.req) * a.nodes + node) * a.Hq + head;
     const long long prow = static_cast<long long>(s.slot) * 128 + ur;
-    constexpr int kPer = 32 / REP;  // columns of a block of 32 this thread writes, from jc on
-    const int jc = kSplit ? 0 : copy * kPer;
+    constexpr int kPer = kSplit ? 32 : 32 / (kSoft / kRows);  // columns of a block of 32 this thread writes, from jc on
+    const int jc = kSplit ? 0 : part * kPer;
 #pragma unroll 1
     for (int c = o0; c < o0 + kOut; c += 32) {
       uint32_t o[32];
-      ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
+      ptx::tmem_ld_32x32b_x32(tmem + lane_base + o_at + c, o);
       ptx::tmem_ld_wait();
       tmem_fence_regs(o);
       if (c + 32 == o0 + kOut) {
@@ -747,15 +765,15 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         for (int i = 0; i < kPer; ++i) x[i] = __uint_as_float(o[i]);
       } else {  // the copies of a row lie in different warps
 #pragma unroll
-        for (int i = 0; i < 32; ++i) join[tid * 33 + i] = __uint_as_float(o[i]) * f;
-        soft_sync<REP>();
+        for (int i = 0; i < 32; ++i) join[tid * 33 + i] = any ? __uint_as_float(o[i]) * f : 0.f;
+        soft_sync<kSoft>();
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           x[i] = 0.f;
 #pragma unroll
-          for (int k = 0; k < REP; ++k) x[i] += join[(k * kRows + ur) * 33 + jc + i];
+          for (int k = 0; k < kSoft / kRows; ++k) x[i] += join[(k * kRows + ur) * 33 + jc + i];
         }
-        soft_sync<REP>();
+        soft_sync<kSoft>();
       }
       if (bad != 0) {
 #pragma unroll
@@ -765,13 +783,16 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
 #pragma unroll
       for (int i = 0; i < kPer; ++i) x[i] = row_ok ? x[i] * inv : 0.f;
       if (in_out && s.whole) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c + jc) * 2);
+        uint32_t w[kPer / 2];
 #pragma unroll
-        for (int i = 0; i < kPer / 8; ++i) {
-          uint32_t w[4];
+        for (int e = 0; e < kPer / 2; ++e) w[e] = pack2<BF16>(x[2 * e], x[2 * e + 1]);
+        char* dst = a.out + (orow * D + c + jc) * 2;
+        if constexpr (kPer >= 8) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack2<BF16>(x[8 * i + 2 * e], x[8 * i + 2 * e + 1]);
-          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < kPer / 8; ++i)
+            reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
         }
       } else if (in_out) {
         float4* dst = reinterpret_cast<float4*>(a.part_o);
@@ -782,7 +803,7 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
       }
       __syncwarp();
     }
-    if (in_out && copy == 0) {
+    if (in_out && part == 0) {
       if (!s.whole)
         reinterpret_cast<float2*>(a.part_ml)[prow] = make_float2(m, l);
       else if (a.lse != nullptr)
@@ -792,12 +813,12 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
 }
 
 template <int D, bool BF16, int REP, bool MC, bool SMALL>
-__global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads<D, REP>, 1) attention_kernel(const __grid_constant__ AttnArgs a) {
   using L = Smem<D, REP, SMALL>;
   extern __shared__ __align__(1024) char smem_base[];
   const uint32_t smem = ptx::smem_addr(smem_base);
   Words* words = reinterpret_cast<Words*>(smem_base + L::kWords);
-  constexpr int kSoftWarps = kSoftThreads<REP> / 32;
+  constexpr int kSoftWarps = kSoftThreads<D, REP> / 32;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   int* pre = reinterpret_cast<int*>(smem_base + L::kPre);
   int2* lens = reinterpret_cast<int2*>(smem_base + L::kLen);
@@ -826,7 +847,7 @@ __global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __gri
   if (warp == kSoftWarps) ptx::tmem_alloc(ptx::smem_addr(&words->tmem), 512);
   if (warp == kSoftWarps + 1 && lane == 0) {
     words->abort = 0;
-    words->bad_nodes[0] = words->bad_nodes[1] = 0;
+    words->bad_nodes[0] = words->bad_nodes[1] = words->bad_nodes[2] = 0;
     for (int i = 0; i < L::kKStages; ++i) {
       ptx::mbar_init(bars.kfull + 8 * i, 1);
       ptx::mbar_init(bars.kempty + 8 * i, a.cl);
@@ -839,8 +860,8 @@ __global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __gri
     ptx::mbar_init(bars.qempty, 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bars.sfull + 8 * i, 1);
-      ptx::mbar_init(bars.sfree + 8 * i, kSoftWarps);
-      ptx::mbar_init(bars.pready + 8 * i, kSoftWarps);
+      ptx::mbar_init(bars.sfree + 8 * i, kSoftWarps / kGroups<D, REP>);
+      ptx::mbar_init(bars.pready + 8 * i, kSoftWarps / kGroups<D, REP>);
       ptx::mbar_init(bars.pvdone + 8 * i, 1);
     }
     ptx::mbar_init(bars.ofree, kSoftWarps);
@@ -856,7 +877,7 @@ __global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __gri
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int units = a.Hk * a.row_groups;
   const int room = a.c.max_blocks * a.c.page_size;
-  for (int i = tid; i < a.n; i += kThreads<REP>) {
+  for (int i = tid; i < a.n; i += kThreads<D, REP>) {
     const int row = a.rows[i];
     int len = 0, cnt = 0;
     if (row >= 0 && row < a.c.rows) {
@@ -935,7 +956,7 @@ __global__ void __launch_bounds__(kThreads<REP>, 1) attention_kernel(const __gri
       }
     }
     a.desc[blockIdx.x] = d;
-    run_outputs<L, D, BF16, MC>(a, bars, smem, tmem, cur, &words->abort);
+    run_outputs<L, D, BF16, MC, kGroups<D, REP>>(a, bars, smem, tmem, cur, &words->abort);
   }
   __syncwarp();
   ptx::tc_fence_before_sync();
@@ -1091,7 +1112,7 @@ qnre_status_t launch_attention(const AttnArgs& a, int sms, cudaStream_t stream) 
     ready.fetch_or(1ull << dev);
   }
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(kThreads<REP>);
+  cfg.blockDim = dim3(kThreads<D, REP>);
   cfg.dynamicSmemBytes = Smem<D, REP, SMALL>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
