@@ -305,7 +305,7 @@ __device__ __forceinline__ void umma_commit_multicast(uint32_t bar, uint16_t mas
 // One warp brings Q and K, another V.  With MC each CTA of the cluster fetches its share of a tile's boxes for
 // all of them.
 template <typename L, int D, int REP, bool MC>
-__device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem, Cursor cur, int kv,
+__device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem, Cursor cur, Seg s, bool more, int kv,
                              volatile uint32_t* abort_flag) {
   constexpr int kHalves = D / 64;
   const int lane = threadIdx.x % 32;
@@ -326,8 +326,7 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
     while (ptx::global_timer_ns() - t0 < 50000) {
     }
   };
-  Seg s;
-  for (uint32_t seg = 0; cur.next(s); ++seg) {
+  for (uint32_t seg = 0; more; ++seg, more = cur.next(s)) {
     const int row = a.rows[s.req];
     const bool fetches = active && row >= 0 && row < a.c.rows;
     const int32_t* table = a.c.table + static_cast<long long>(fetches ? row : 0) * a.c.max_blocks;
@@ -389,16 +388,15 @@ __device__ __forceinline__ void drain_mma(uint32_t bar) {
 
 // S = Q K^T, tile after tile, across units: two ahead of the softmax as far as S's two buffers allow.
 template <typename L, int D, bool BF16, bool MC>
-__device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
-                           volatile uint32_t* abort_flag) {
+__device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur, Seg s,
+                           bool more, volatile uint32_t* abort_flag) {
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
   constexpr uint32_t kIdesc = (1u << 4) | kFmt | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
   const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kK, 16, 1024);
   const uint64_t q = ptx::smem_desc_sw128(smem + L::kQ, 16, 1024);
   const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
   uint32_t g = 0, slot = 0, phase = 0;
-  Seg s;
-  for (uint32_t seg = 0; cur.next(s); ++seg) {
+  for (uint32_t seg = 0; more; ++seg, more = cur.next(s)) {
     if (!wait(bars.qfull, seg & 1u, abort_flag, a.c.status)) return drain_mma(bars.drain);
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
@@ -428,16 +426,15 @@ __device__ void run_scores(const AttnArgs& a, const Bars& bars, uint32_t smem, u
 
 // O += P V, tile after tile; with two groups of softmax warps even and odd tiles each have an O.
 template <typename L, int D, bool BF16, bool MC, int GROUPS>
-__device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur,
-                            volatile uint32_t* abort_flag) {
+__device__ void run_outputs(const AttnArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur, Seg s,
+                            bool more, volatile uint32_t* abort_flag) {
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
   constexpr uint32_t kIdesc =
       (1u << 4) | kFmt | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
   const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kV, kTile * 128, 1024);
   const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
   uint32_t g = 0, slot = 0, phase = 0;
-  Seg s;
-  for (uint32_t seg = 0; cur.next(s); ++seg) {
+  for (uint32_t seg = 0; more; ++seg, more = cur.next(s)) {
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
       const bool first = t == s.t0;
@@ -539,7 +536,8 @@ __device__ __noinline__ bool clean_v_row(char* row, bool token, int first, int l
 
 template <typename L, int D, bool BF16, int REP>
 __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base, uint32_t smem, uint32_t tmem,
-                            Cursor cur, volatile uint32_t* abort_flag, unsigned long long* bad_nodes) {
+                            Cursor cur, Seg next, bool more, volatile uint32_t* abort_flag,
+                            unsigned long long* bad_nodes) {
   constexpr bool kSplit = REP == 1;    // two threads a row, one maximum and one O
   constexpr int kCols = kSplit ? 64 : kTile / REP;  // tokens of a tile this thread looks at
   constexpr int kRows = 128 / REP;     // unit rows
@@ -582,9 +580,8 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
   };
 
   uint32_t g = 0;
-  Seg s, next;
+  Seg s;
   RowInfo row{}, next_row{};
-  bool more = cur.next(next);
   if (more) next_row = row_info(next);
   for (uint32_t seg = 0; more; ++seg) {
     s = next;
@@ -931,32 +928,35 @@ __global__ void __launch_bounds__(kThreads<D, REP>, 1) attention_kernel(const __
     if (pre[mid] <= cur.cur) lo = mid; else hi = mid - 1;
   }
   cur.req = lo;
+  // The first unit's part is found here, once for all roles: the roles' own copies of this code start with an empty
+  // instruction cache (1700 cycles to the first part; one request 13.8 us, so 13.5).
+  Seg first;
+  const bool more = cur.next(first);
 
   if (warp < kSoftWarps) {
-    run_softmax<L, D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, &words->abort, words->bad_nodes);
+    run_softmax<L, D, BF16, REP>(a, bars, smem_base, smem, tmem, cur, first, more, &words->abort, words->bad_nodes);
   } else if (warp == kSoftWarps || warp == kSoftWarps + 3) {
-    run_producer<L, D, REP, MC>(a, bars, smem, cur, warp == kSoftWarps ? 0 : 1, &words->abort);
+    run_producer<L, D, REP, MC>(a, bars, smem, cur, first, more, warp == kSoftWarps ? 0 : 1, &words->abort);
   } else if (warp == kSoftWarps + 1) {
-    if (lane == 0) run_scores<L, D, BF16, MC>(a, bars, smem, tmem, cur, &words->abort);
+    if (lane == 0) run_scores<L, D, BF16, MC>(a, bars, smem, tmem, cur, first, more, &words->abort);
   } else if (lane == 0) {
     // does this run go on with a unit that the one before it began?  Then name it for the join
     Desc d{};
-    Cursor look = cur;
-    Seg s;
-    if (look.next(s) && s.t0 > 0) {
+    const Seg& s = first;
+    if (more && s.t0 > 0) {
       const int tiles = Cursor::tiles_of(s.total);
-      const int first = pre[s.req] + (s.kvh * a.row_groups + s.rt / a.cl) * (tiles + kUnitCost) + kUnitCost;
-      if (first >= start_of(cluster - 1)) {
+      const int begin = pre[s.req] + (s.kvh * a.row_groups + s.rt / a.cl) * (tiles + kUnitCost) + kUnitCost;
+      if (begin >= start_of(cluster - 1)) {
         int lo = cluster, hi = clusters - 1;  // the last cluster whose run starts by its last tile
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
-          if (start_of(mid) <= first + tiles - 1) lo = mid; else hi = mid - 1;
+          if (start_of(mid) <= begin + tiles - 1) lo = mid; else hi = mid - 1;
         }
         d = Desc{lo - cluster + 2, s.req, s.kvh, s.rt, cluster - 1, {0, 0, 0}};
       }
     }
     a.desc[blockIdx.x] = d;
-    run_outputs<L, D, BF16, MC, kGroups<D, REP>>(a, bars, smem, tmem, cur, &words->abort);
+    run_outputs<L, D, BF16, MC, kGroups<D, REP>>(a, bars, smem, tmem, cur, first, more, &words->abort);
   }
   __syncwarp();
   ptx::tc_fence_before_sync();
