@@ -279,3 +279,67 @@ def test_native_reads_agree_with_python_ones(lib, monkeypatch):
     # base.float() makes a new tensor each time only in the list above, so addresses agree
     assert with_native == without
     assert any(isinstance(x, str) for x in without) and any(isinstance(x, bytes) for x in without)
+
+
+class _Stream:
+    cuda_stream = 0
+
+
+def test_whole_native_calls_refuse_as_the_python_ones(lib, monkeypatch):
+    """A norm, its gradient and an append with one argument wrong at a time: the same error with and without _marshal."""
+    torch = pytest.importorskip("torch")
+    if qb._native is None:
+        pytest.skip("_marshal is not built")
+    bf = torch.bfloat16
+    good = dict(q=torch.zeros((2, 3, 4, 64), dtype=bf), k=torch.zeros((2, 3, 2, 64), dtype=bf),
+                v=torch.zeros((2, 3, 2, 64), dtype=bf), wq=torch.ones(64, dtype=bf), wk=torch.ones(64, dtype=bf),
+                table=torch.zeros((8, 32)), pos=torch.zeros((2, 3), dtype=torch.int32),
+                qo=torch.zeros((2, 3, 4, 64), dtype=bf), ko=torch.zeros((2, 3, 2, 64), dtype=bf),
+                gq=torch.zeros((2, 3, 4, 64), dtype=bf), gk=torch.zeros((2, 3, 2, 64), dtype=bf),
+                dwq=torch.zeros(64), dwk=torch.zeros(64), ws=torch.zeros(1 << 20, dtype=torch.uint8),
+                rows=torch.zeros(2, dtype=torch.int32), counts=None, layer=0, style="rotate_half")
+    pool = torch.zeros((1, 4, 2, 8, 64), dtype=bf)
+    cache = qb.PagedCache(pool, torch.zeros_like(pool), torch.zeros((3, 2), dtype=torch.int32),
+                          torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32))
+    s = _Stream()
+    calls = [
+        lambda a: qb.qnre_qk_norm_rope(a["q"], a["k"], a["wq"], a["wk"], a["table"], a["pos"], a["qo"], a["ko"],
+                                       rope_style=a["style"], stream=s),
+        lambda a: qb.qnre_qk_norm_rope_backward(a["gq"], a["gk"], a["q"], a["k"], a["wq"], a["wk"], a["table"], a["pos"],
+                                                a["qo"], a["ko"], a["dwq"], a["dwk"], a["ws"], rope_style=a["style"],
+                                                stream=s),
+        lambda a: qb.qnre_qkv_norm_rope_append(a["q"], a["k"], a["v"], a["wq"], a["wk"], a["table"], a["pos"], a["qo"], cache,
+                                               a["layer"], a["rows"], a["counts"], rope_style=a["style"], stream=s),
+    ]
+    wrong = [("style", "none"), ("layer", 5), ("layer", -1), ("rows", torch.zeros(3, dtype=torch.int32)),
+             ("rows", torch.zeros(2, dtype=torch.int64)), ("counts", torch.zeros((2, 1), dtype=torch.int32)),
+             ("ws", torch.zeros(16, dtype=torch.uint8)), ("ws", torch.zeros((1 << 11, 1 << 10), dtype=torch.uint8).t())]
+    for name in ("q", "k", "v", "qo", "ko", "gq", "gk"):
+        t = good[name]
+        wrong += [(name, t[0]), (name, t.float()), (name, t.half()), (name, t.to_sparse()), (name, t[..., :32]),
+                  (name, t.transpose(2, 3)), (name, t.double())]
+    for name in ("wq", "wk", "dwq", "dwk"):
+        t = good[name]
+        wrong += [(name, t[:32]), (name, t.half()), (name, t[None]), (name, torch.zeros((64, 2), dtype=t.dtype)[:, 0])]
+    wrong += [("table", good["table"][0]), ("table", good["table"].t()), ("table", good["table"].double()),
+              ("table", torch.zeros((8, 24))), ("pos", good["pos"].long()), ("pos", good["pos"][:1]), ("pos", good["pos"].t())]
+
+    def outcomes():
+        r = []
+        for name, value in wrong:
+            for i, call in enumerate(calls):
+                # (an argument that the call has, so that a launch is never reached)
+                if name in ((("v", "rows", "counts", "layer", "gq", "gk", "dwq", "dwk", "ws")),
+                            ("v", "rows", "counts", "layer"), ("ko", "gq", "gk", "dwq", "dwk", "ws"))[i]:
+                    continue
+                try:
+                    call({**good, name: value})
+                    r.append((name, i, None))
+                except Exception as e:  # the Python reads of a sparse tensor raise torch's own errors
+                    r.append((name, i, type(e).__name__, str(e)))
+        return r
+
+    with_native = outcomes()
+    assert all(len(x) == 4 for x in with_native)
+    monkeypatch.setattr(qb, "_native", None)
+    assert with_native == outcomes()

@@ -170,6 +170,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.qnre_verify_tree.argtypes = [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_int, c_int, c_i64] + [c_vp] * 9
     lib.qnre_tree_masks.restype = c_int
     lib.qnre_tree_masks.argtypes = [c_vp, c_int, c_int, c_vp, c_vp, c_vp]
+    for name in ("qnre_qk_norm_rope", "qnre_qk_norm_rope_backward", "qnre_qkv_norm_rope_append"):
+        _entry[name] = ctypes.cast(getattr(lib, name), c_vp).value
     _lib = lib
     return lib
 
@@ -521,7 +523,7 @@ class PagedCache:
                               _i32("PagedCache", block_table), _i32("PagedCache", seq_lens),
                               _i32("PagedCache", page_refs), self.status_word.data_ptr(), self.scratch.data_ptr(),
                               layers, pages, heads, page_size, head_dim, rows, block_table.shape[1], _dtype_code(k))
-        self.handle = ctypes.byref(self._struct)
+        self.handle, self.address = ctypes.byref(self._struct), ctypes.addressof(self._struct)
 
     def status(self, clear: bool = True) -> int:
         """The CACHE_* bits kernels have set (waits for the current stream)."""
@@ -552,6 +554,7 @@ def _load_dtypes():
 
 
 _native = None  # the _marshal module once load_library has found it
+_entry: Dict[str, int] = {}  # addresses of the entry points that it calls itself
 
 
 def _sizes(t):
@@ -667,9 +670,14 @@ def qnre_qk_norm_rope(q, k, q_norm_w, k_norm_w, cos_sin, positions, q_out, k_out
                       stream=None) -> None:
     """Per-head RMSNorm and rotation of q [B, S, Hq, D] and k [B, S, Hk, D] (views; in place allowed)."""
     where = "qnre_qk_norm_rope"
+    lib, style = load_library(), ROPE_STYLES.get(rope_style, -1)
+    if _native is not None:
+        st = _native.norm(_entry[where], q, k, q_norm_w, k_norm_w, cos_sin, positions, q_out, k_out, style, _stream_ptr,
+                          stream)
+        if st is not None:
+            return _check(st, where)
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
-    _check(load_library().qnre_qk_norm_rope(*head, ROPE_STYLES.get(rope_style, -1), pos, _view4(q_out),
-                                            _view4(k_out), _stream_ptr(stream)), where)
+    _check(lib.qnre_qk_norm_rope(*head, style, pos, _view4(q_out), _view4(k_out), _stream_ptr(stream)), where)
 
 
 def qk_norm_rope_workspace(q, k=None):
@@ -685,10 +693,16 @@ def qnre_qk_norm_rope_backward(gq, gk, q, k, q_norm_w, k_norm_w, cos_sin, positi
                                workspace, rope_style: str = "rotate_half", stream=None) -> None:
     """Gradient of qnre_qk_norm_rope: dq, dk (input dtype) and the fp32 weight gradients."""
     where = "qnre_qk_norm_rope_backward"
+    lib, style = load_library(), ROPE_STYLES.get(rope_style, -1)
+    if _native is not None:
+        st = _native.norm_backward(_entry[where], gq, gk, q, k, q_norm_w, k_norm_w, cos_sin, positions, dq, dk, dq_norm_w,
+                                   dk_norm_w, workspace, style, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
     D = q.shape[-1]
-    _check(load_library().qnre_qk_norm_rope_backward(
-        _view4(gq), _view4(gk), *head, ROPE_STYLES.get(rope_style, -1), pos, _view4(dq), _view4(dk), _f32(where, dq_norm_w, D), _f32(where, dk_norm_w, D), _contig(workspace, where),
+    _check(lib.qnre_qk_norm_rope_backward(
+        _view4(gq), _view4(gk), *head, style, pos, _view4(dq), _view4(dk), _f32(where, dq_norm_w, D), _f32(where, dk_norm_w, D), _contig(workspace, where),
         workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
 
 
@@ -696,10 +710,16 @@ def qnre_qkv_norm_rope_append(q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q
                               rows, counts=None, rope_style: str = "rotate_half", stream=None) -> None:
     """qnre_qk_norm_rope of the rows' new tokens [n, S, ...]; k and v go into the cache behind seq_lens."""
     where = "qnre_qkv_norm_rope_append"
+    lib, style = load_library(), ROPE_STYLES.get(rope_style, -1)
+    if _native is not None:
+        st = _native.append(_entry[where], q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q_out, cache.address, layer,
+                            rows, counts, style, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
     n = q.shape[0]
-    _check(load_library().qnre_qkv_norm_rope_append(
-        head[0], head[1], _view4(v), *head[2:], ROPE_STYLES.get(rope_style, -1), pos, _view4(q_out), cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)
+    _check(lib.qnre_qkv_norm_rope_append(
+        head[0], head[1], _view4(v), *head[2:], style, pos, _view4(q_out), cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)
 
 
 def qnre_tree_masks(parents, masks=None, depths=None, stream=None) -> None:

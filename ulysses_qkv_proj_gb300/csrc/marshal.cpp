@@ -1,12 +1,18 @@
 // marshal.cpp -- what the Python binding reads off torch tensors, in one native call each: a decode step's kernels
 // run for a few microseconds, and a tensor's shape, strides, dtype and pointer cost one microsecond of
-// Python attribute reads (0.1 here).  Built where torch's headers are found; the binding falls back to Python
-// reads without it, with the same checks and the same errors.
+// Python attribute reads (0.1 here).  The calls of the norm family are made whole from here, as their kernels are the
+// shortest and their arguments the most: an append 6.5 us -> 3.7 on a Grace core, a gradient 8.6 -> 4.6.  Built where torch's
+// headers are found; the binding falls back to Python reads without it, with the same checks and the same errors.
+// Everything here answers None where a read fails, or throws (a sparse tensor's strides): the binding's Python reads
+// then name what is wrong.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <Python.h>
 
+#include <climits>
+#include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/qnre.h"
 
@@ -24,44 +30,74 @@ int code_of(const at::Tensor& t) {
   }
 }
 
-// view4(tensor) -> the bytes of its qnre_tensor4_t, or None where it is no rank-4 tensor of a known float type.
-PyObject* view4(PyObject*, PyObject* obj) {
-  if (!THPVariable_Check(obj)) Py_RETURN_NONE;
+template <typename F>
+PyObject* guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    Py_RETURN_NONE;
+  }
+}
+
+bool read_view4(PyObject* obj, qnre_tensor4_t* v) {
+  if (!THPVariable_Check(obj)) return false;
   const at::Tensor& t = THPVariable_Unpack(obj);
   const int code = code_of(t);
-  if (t.dim() != 4 || code < 0 || code > QNRE_DTYPE_FP32) Py_RETURN_NONE;
-  qnre_tensor4_t v;
-  std::memset(&v, 0, sizeof(v));
-  v.data = t.data_ptr();
+  if (t.dim() != 4 || code < 0 || code > QNRE_DTYPE_FP32) return false;
+  std::memset(v, 0, sizeof(*v));
+  v->data = t.data_ptr();
   for (int i = 0; i < 4; ++i) {
-    v.shape[i] = t.size(i);
-    v.stride[i] = t.stride(i);
+    v->shape[i] = t.size(i);
+    v->stride[i] = t.stride(i);
   }
-  v.dtype = code;
-  return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&v), sizeof(v));
+  v->dtype = code;
+  return true;
+}
+
+// The address of a contiguous tensor of that type and shape.
+template <typename T>
+bool read_pointer(PyObject* obj, int code, std::initializer_list<int64_t> shape, T** out) {
+  if (!THPVariable_Check(obj)) return false;
+  const at::Tensor& t = THPVariable_Unpack(obj);
+  if (code_of(t) != code || !t.is_contiguous() || !t.sizes().equals(at::IntArrayRef(shape))) return false;
+  *out = static_cast<T*>(t.data_ptr());
+  return true;
+}
+
+// view4(tensor) -> the bytes of its qnre_tensor4_t, or None where it is no rank-4 tensor of a known float type.
+PyObject* view4(PyObject*, PyObject* obj) {
+  return guarded([&]() -> PyObject* {
+    qnre_tensor4_t v;
+    if (!read_view4(obj, &v)) Py_RETURN_NONE;
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&v), sizeof(v));
+  });
 }
 
 // pointer(tensor, code, *shape) -> its address, or None unless it is contiguous, of that type and (where given) shape.
 PyObject* pointer(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n < 2 || !THPVariable_Check(args[0])) Py_RETURN_NONE;
-  const at::Tensor& t = THPVariable_Unpack(args[0]);
-  if (code_of(t) != PyLong_AsLong(args[1]) || !t.is_contiguous()) Py_RETURN_NONE;
-  if (n > 2) {
-    if (t.dim() != n - 2) Py_RETURN_NONE;
-    for (Py_ssize_t i = 0; i < n - 2; ++i)
-      if (t.size(i) != PyLong_AsLongLong(args[2 + i])) Py_RETURN_NONE;
-  }
-  return PyLong_FromVoidPtr(t.data_ptr());
+  return guarded([&]() -> PyObject* {
+    if (n < 2 || !THPVariable_Check(args[0])) Py_RETURN_NONE;
+    const at::Tensor& t = THPVariable_Unpack(args[0]);
+    if (code_of(t) != PyLong_AsLong(args[1]) || !t.is_contiguous()) Py_RETURN_NONE;
+    if (n > 2) {
+      if (t.dim() != n - 2) Py_RETURN_NONE;
+      for (Py_ssize_t i = 0; i < n - 2; ++i)
+        if (t.size(i) != PyLong_AsLongLong(args[2 + i])) Py_RETURN_NONE;
+    }
+    return PyLong_FromVoidPtr(t.data_ptr());
+  });
 }
 
 // sizes(tensor) -> its shape as a plain tuple.
 PyObject* sizes(PyObject*, PyObject* obj) {
-  if (!THPVariable_Check(obj)) Py_RETURN_NONE;
-  const at::Tensor& t = THPVariable_Unpack(obj);
-  PyObject* r = PyTuple_New(t.dim());
-  if (r == nullptr) return nullptr;
-  for (int64_t i = 0; i < t.dim(); ++i) PyTuple_SET_ITEM(r, i, PyLong_FromLongLong(t.size(i)));
-  return r;
+  return guarded([&]() -> PyObject* {
+    if (!THPVariable_Check(obj)) Py_RETURN_NONE;
+    const at::Tensor& t = THPVariable_Unpack(obj);
+    PyObject* r = PyTuple_New(t.dim());
+    if (r == nullptr) return nullptr;
+    for (int64_t i = 0; i < t.dim(); ++i) PyTuple_SET_ITEM(r, i, PyLong_FromLongLong(t.size(i)));
+    return r;
+  });
 }
 
 // type_code(tensor) -> as code_of.
@@ -69,9 +105,145 @@ PyObject* type_code(PyObject*, PyObject* obj) {
   return PyLong_FromLong(THPVariable_Check(obj) ? code_of(THPVariable_Unpack(obj)) : -1);
 }
 
+// ------------------------------------------------------------------ whole calls
+// name(entry point's address, its arguments in the binding's order.., style code, stream reader, stream) -> status, or
+// None where an argument does not read.  The stream is asked for last, as the binding does.
+
+bool read_int(PyObject* obj, int* out) {
+  const long x = PyLong_Check(obj) ? PyLong_AsLong(obj) : LONG_MAX;
+  if (PyErr_Occurred()) PyErr_Clear();
+  if (x > INT_MAX || x < INT_MIN) return false;
+  *out = static_cast<int>(x);
+  return true;
+}
+
+// What the three calls share: q, k, the norm weights, the table and the positions, six arguments.
+struct Head {
+  qnre_tensor4_t q, k;
+  void *wq, *wk;
+  float* cos_sin;
+  int64_t n_pos;
+  int rot;
+  int32_t* positions;
+};
+
+bool read_head(PyObject* const* args, PyObject* positions, Head* h) {
+  if (!read_view4(args[0], &h->q) || !read_view4(args[1], &h->k)) return false;
+  const int64_t dim = h->q.shape[3];
+  if (!read_pointer(args[2], h->q.dtype, {dim}, &h->wq) || !read_pointer(args[3], h->k.dtype, {dim}, &h->wk)) return false;
+  if (!THPVariable_Check(args[4])) return false;
+  const at::Tensor& table = THPVariable_Unpack(args[4]);
+  if (table.dim() != 2 || table.size(1) > INT_MAX) return false;
+  h->n_pos = table.size(0);
+  h->rot = static_cast<int>(table.size(1));
+  if (!read_pointer(args[4], QNRE_DTYPE_FP32, {table.size(0), table.size(1)}, &h->cos_sin)) return false;
+  h->positions = nullptr;
+  return positions == Py_None || read_pointer(positions, 3, {h->q.shape[0], h->q.shape[1]}, &h->positions);
+}
+
+bool read_entry(PyObject* obj, void** fn) {
+  *fn = PyLong_AsVoidPtr(obj);
+  if (PyErr_Occurred()) PyErr_Clear();
+  return *fn != nullptr;
+}
+
+// stream(reader, stream) -> false with a Python error set.
+bool read_stream(PyObject* reader, PyObject* stream, qnre_stream_t* out) {
+  PyObject* r = PyObject_CallOneArg(reader, stream);
+  if (r == nullptr) return false;
+  *out = r == Py_None ? nullptr : reinterpret_cast<qnre_stream_t>(PyLong_AsVoidPtr(r));
+  Py_DECREF(r);
+  return PyErr_Occurred() == nullptr;
+}
+
+// norm(fn, q, k, wq, wk, cos_sin, positions, q_out, k_out, style, reader, stream)
+PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    Head h;
+    qnre_tensor4_t qo, ko;
+    int style;
+    qnre_stream_t stream;
+    if (n != 12 || !read_entry(args[0], &fn) || !read_head(args + 1, args[6], &h) || !read_view4(args[7], &qo) ||
+        !read_view4(args[8], &ko) || !read_int(args[9], &style))
+      Py_RETURN_NONE;
+    if (!read_stream(args[10], args[11], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_qk_norm_rope)>(fn)(&h.q, &h.k, h.wq, h.wk, h.cos_sin, h.n_pos, h.rot, style,
+                                                            h.positions, &qo, &ko, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// norm_backward(fn, gq, gk, q, k, wq, wk, cos_sin, positions, dq, dk, dwq, dwk, workspace, style, reader, stream)
+PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    Head h;
+    qnre_tensor4_t gq, gk, dq, dk;
+    float *dwq, *dwk;
+    int style;
+    qnre_stream_t stream;
+    if (n != 17 || !read_entry(args[0], &fn) || !read_view4(args[1], &gq) || !read_view4(args[2], &gk) ||
+        !read_head(args + 3, args[8], &h) || !read_view4(args[9], &dq) || !read_view4(args[10], &dk) ||
+        !read_pointer(args[11], QNRE_DTYPE_FP32, {h.q.shape[3]}, &dwq) ||
+        !read_pointer(args[12], QNRE_DTYPE_FP32, {h.q.shape[3]}, &dwk) || !THPVariable_Check(args[13]) ||
+        !read_int(args[14], &style))
+      Py_RETURN_NONE;
+    const at::Tensor& ws = THPVariable_Unpack(args[13]);
+    if (!ws.is_contiguous()) Py_RETURN_NONE;
+    void* ws_data = ws.data_ptr();
+    const uint64_t ws_bytes = ws.nbytes();
+    if (!read_stream(args[15], args[16], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_qk_norm_rope_backward)>(fn)(&gq, &gk, &h.q, &h.k, h.wq, h.wk, h.cos_sin, h.n_pos,
+                                                                     h.rot, style, h.positions, &dq, &dk, dwq, dwk,
+                                                                     ws_data, ws_bytes, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// append(fn, q, k, v, wq, wk, cos_sin, positions, q_out, cache address, layer, rows, counts, style, reader, stream)
+PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    void *fn, *cache;
+    Head h;
+    qnre_tensor4_t v, qo;
+    int32_t *rows, *counts = nullptr;
+    int layer, style;
+    qnre_stream_t stream;
+    if (n != 16) Py_RETURN_NONE;
+    PyObject* const head[] = {args[1], args[2], args[4], args[5], args[6]};
+    if (!read_entry(args[0], &fn) || !read_head(head, args[7], &h) || !read_view4(args[3], &v) ||
+        !read_view4(args[8], &qo) || !read_entry(args[9], &cache) || !read_int(args[10], &layer) ||
+        !read_pointer(args[11], 3, {h.q.shape[0]}, &rows) ||
+        (args[12] != Py_None && !read_pointer(args[12], 3, {h.q.shape[0]}, &counts)) || !read_int(args[13], &style))
+      Py_RETURN_NONE;
+    if (!read_stream(args[14], args[15], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_qkv_norm_rope_append)>(fn)(
+        &h.q, &h.k, &v, h.wq, h.wk, h.cos_sin, h.n_pos, h.rot, style, h.positions, &qo,
+        static_cast<const qnre_cache_t*>(cache), layer, rows, counts, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+template <typename F>
+PyCFunction fast(F f) {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
+}
+
 PyMethodDef methods[] = {{"view4", view4, METH_O, nullptr},
-                         {"pointer", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pointer)), METH_FASTCALL,
-                          nullptr},
+                         {"pointer", fast(pointer), METH_FASTCALL, nullptr},
+                         {"norm", fast(norm), METH_FASTCALL, nullptr},
+                         {"norm_backward", fast(norm_backward), METH_FASTCALL, nullptr},
+                         {"append", fast(append), METH_FASTCALL, nullptr},
                          {"sizes", sizes, METH_O, nullptr},
                          {"type_code", type_code, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
