@@ -343,3 +343,74 @@ def test_whole_native_calls_refuse_as_the_python_ones(lib, monkeypatch):
     assert all(len(x) == 4 for x in with_native)
     monkeypatch.setattr(qb, "_native", None)
     assert with_native == outcomes()
+
+
+def test_whole_native_cache_and_tree_calls_refuse_as_the_python_ones(lib, monkeypatch):
+    """The same of the cache's bookkeeping, the attention and the verification."""
+    torch = pytest.importorskip("torch")
+    if qb._native is None:
+        pytest.skip("_marshal is not built")
+    bf, i32 = torch.bfloat16, torch.int32
+    pool = torch.zeros((1, 4, 2, 8, 64), dtype=bf)
+    cache = qb.PagedCache(pool, torch.zeros_like(pool), torch.zeros((3, 2), dtype=i32), torch.zeros(3, dtype=i32),
+                          torch.zeros(4, dtype=i32))
+    s = _Stream()
+    rows = [torch.zeros(2, dtype=i32), torch.zeros(3, dtype=i32), torch.zeros((2, 1), dtype=i32),
+            torch.zeros(2, dtype=torch.int64), torch.zeros(4, dtype=i32)[::2], torch.zeros(2), torch.zeros(2, dtype=i32).to_sparse(),
+            torch.zeros(1025, dtype=i32)]
+    path = [torch.zeros((2, 3), dtype=i32), torch.zeros((2, 65), dtype=i32), torch.zeros(2, dtype=i32),
+            torch.zeros((3, 2), dtype=i32).t(), torch.zeros((2, 0), dtype=i32), torch.zeros((2, 3))]
+    good = dict(q=torch.zeros((2, 3, 4, 64), dtype=bf), rows=rows[0], mask=torch.zeros((2, 3), dtype=torch.int64),
+                out=torch.zeros((2, 3, 4, 64), dtype=bf), lse=torch.zeros((2, 3, 4)), counts=rows[0], scale=0.125, layer=0,
+                ws=torch.zeros(64 << 20, dtype=torch.uint8))
+    probs = dict(target=torch.rand((2, 3, 50)), draft=torch.rand((2, 3, 50)), tokens=torch.zeros((2, 3), dtype=i32),
+                 parents=torch.zeros((2, 3), dtype=i32), accept=torch.zeros((2, 3)), sample=torch.zeros(2),
+                 path=torch.zeros((2, 3), dtype=i32), counts=torch.zeros(2, dtype=i32), next=torch.zeros(2, dtype=i32),
+                 nodes=None)
+    att_wrong = [("q", good["q"][0]), ("q", good["q"].half()), ("q", good["q"][:, :, :3]), ("q", good["q"].to_sparse()),
+                 ("rows", rows[1]), ("rows", rows[3]), ("mask", good["mask"].int()), ("mask", good["mask"][:1]),
+                 ("mask", good["mask"].t()), ("out", good["out"].half()), ("out", good["out"][:, :2]),
+                 ("out", good["out"].transpose(0, 1)), ("lse", good["lse"].double()), ("lse", good["lse"][0]),
+                 ("counts", rows[1]), ("scale", -1.0), ("scale", float("nan")), ("scale", 0), ("scale", float("inf")),
+                 ("layer", 1), ("layer", -1), ("ws", None), ("ws", good["ws"][:64]), ("ws", good["ws"][::2])]
+    ver_wrong = [("target", probs["target"][0]), ("target", probs["target"].double()), ("target", probs["target"].transpose(1, 2)),
+                 ("target", probs["target"].to_sparse()), ("draft", probs["draft"][:, :2]), ("draft", probs["draft"].half()),
+                 ("tokens", probs["tokens"].long()), ("parents", probs["parents"][:1]), ("accept", probs["accept"].double()),
+                 ("sample", probs["sample"][:1]), ("path", probs["path"].t()), ("counts", torch.zeros(2)),
+                 ("next", torch.zeros(3, dtype=i32)), ("nodes", torch.zeros(3, dtype=i32)), ("tokens", probs["path"]),
+                 ("next", probs["counts"])]
+
+    def outcomes():
+        r = []
+
+        def note(call):
+            try:
+                call()
+                r.append(None)
+            except Exception as e:
+                r.append((type(e).__name__, str(e)))
+
+        for bad in rows[1:]:
+            for two in (lambda a, b: qb.qnre_cache_truncate(cache, a, b, s), lambda a, b: qb.qnre_cache_fork(cache, a, b, s),
+                        lambda a, b: qb.qnre_cache_reserve(cache, a, b, s),
+                        lambda a, b: qb.qnre_cache_copy_pages(cache, a, b, s)):
+                note(lambda: two(bad, rows[0]))
+                note(lambda: two(rows[0], bad))
+            note(lambda: qb.qnre_cache_compact(cache, bad, path[0], rows[0], s))
+            note(lambda: qb.qnre_cache_compact(cache, rows[0], path[0], bad, s))
+        for bad in path[1:]:
+            note(lambda: qb.qnre_cache_compact(cache, rows[0], bad, rows[0], s))
+        for name, value in att_wrong:
+            a = {**good, name: value}
+            note(lambda: qb.qnre_tree_attention(a["q"], cache, a["layer"], a["rows"], a["mask"], a["out"], a["lse"],
+                                                a["counts"], a["scale"], a["ws"], s))
+        for name, value in ver_wrong:
+            a = {**probs, name: value}
+            note(lambda: qb.qnre_verify_tree(a["target"], a["draft"], a["tokens"], a["parents"], a["accept"], a["sample"],
+                                             a["path"], a["counts"], a["next"], a["nodes"], s))
+        return r
+
+    with_native = outcomes()
+    assert None not in with_native
+    monkeypatch.setattr(qb, "_native", None)
+    assert with_native == outcomes()

@@ -170,7 +170,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.qnre_verify_tree.argtypes = [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_int, c_int, c_i64] + [c_vp] * 9
     lib.qnre_tree_masks.restype = c_int
     lib.qnre_tree_masks.argtypes = [c_vp, c_int, c_int, c_vp, c_vp, c_vp]
-    for name in ("qnre_qk_norm_rope", "qnre_qk_norm_rope_backward", "qnre_qkv_norm_rope_append"):
+    for name in ("qnre_qk_norm_rope", "qnre_qk_norm_rope_backward", "qnre_qkv_norm_rope_append", "qnre_tree_attention",
+                 "qnre_verify_tree", "qnre_cache_truncate", "qnre_cache_fork", "qnre_cache_reserve",
+                 "qnre_cache_compact", "qnre_cache_copy_pages"):
         _entry[name] = ctypes.cast(getattr(lib, name), c_vp).value
     _lib = lib
     return lib
@@ -204,7 +206,7 @@ def _dtype_code(t) -> int:
 
 # A decode step's kernels run for a few microseconds, so the calls' own cost counts: the current
 # stream is read as a raw handle (0.4 us on a Grace core; building the Stream object takes 2.9), a view
-# is packed in one go (1.0 us; field by field 2.4), and the decoding calls read their tensors natively (_marshal)
+# is packed in one go (1.0 us; field by field 2.4), and the decoding calls are read and made natively (_marshal)
 # where that module was built: None from it means that a check failed, and the Python checks then say which.
 def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
@@ -620,40 +622,65 @@ def _weight(where: str, w, dim: int, like) -> int:
 
 def qnre_cache_truncate(cache: PagedCache, rows, lens, stream=None) -> None:
     """Row rows[i] keeps its first lens[i] tokens; the blocks past them are released (0 frees the row)."""
-    where, n = "qnre_cache_truncate", rows.numel()
-    _check(load_library().qnre_cache_truncate(cache.handle, _i32(where, rows, n), _i32(where, lens, n), n,
-                                              _stream_ptr(stream)), where)
+    where, lib = "qnre_cache_truncate", load_library()
+    if _native is not None:
+        st = _native.cache_rows(_entry[where], cache.address, rows, lens, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    n = rows.numel()
+    _check(lib.qnre_cache_truncate(cache.handle, _i32(where, rows, n), _i32(where, lens, n), n,
+                                   _stream_ptr(stream)), where)
 
 
 def qnre_cache_fork(cache: PagedCache, src, dst, stream=None) -> None:
     """Empty row dst[i] becomes a copy of row src[i] that shares its pages."""
-    where, n = "qnre_cache_fork", src.numel()
-    _check(load_library().qnre_cache_fork(cache.handle, _i32(where, src, n), _i32(where, dst, n), n,
-                                          _stream_ptr(stream)), where)
+    where, lib = "qnre_cache_fork", load_library()
+    if _native is not None:
+        st = _native.cache_rows(_entry[where], cache.address, src, dst, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    n = src.numel()
+    _check(lib.qnre_cache_fork(cache.handle, _i32(where, src, n), _i32(where, dst, n), n,
+                               _stream_ptr(stream)), where)
 
 
 def qnre_cache_reserve(cache: PagedCache, rows, counts, stream=None) -> None:
     """Pages of its own for the next counts[i] tokens of row rows[i] (lowest free pages, copy on write)."""
-    where, n = "qnre_cache_reserve", rows.numel()
-    _check(load_library().qnre_cache_reserve(cache.handle, _i32(where, rows, n), _i32(where, counts, n), n,
-                                             _stream_ptr(stream)), where)
+    where, lib = "qnre_cache_reserve", load_library()
+    if _native is not None:
+        st = _native.cache_rows(_entry[where], cache.address, rows, counts, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    n = rows.numel()
+    _check(lib.qnre_cache_reserve(cache.handle, _i32(where, rows, n), _i32(where, counts, n), n,
+                                  _stream_ptr(stream)), where)
 
 
 def qnre_cache_compact(cache: PagedCache, rows, path, counts, stream=None) -> None:
     """Keep the accepted nodes path[i][:counts[i]] of row rows[i]'s drafts; its length grows by counts[i]."""
-    where, n = "qnre_cache_compact", rows.numel()
+    where, lib = "qnre_cache_compact", load_library()
+    if _native is not None:
+        st = _native.compact(_entry[where], cache.address, rows, path, counts, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    n = rows.numel()
     shape = _sizes(path)
     if len(shape) != 2:
         raise QnreError(1, f"{where}: path must be [n, nodes]")
-    _check(load_library().qnre_cache_compact(cache.handle, _i32(where, rows, n), _i32(where, path, n, shape[1]),
-                                             _i32(where, counts, n), n, shape[1], _stream_ptr(stream)), where)
+    _check(lib.qnre_cache_compact(cache.handle, _i32(where, rows, n), _i32(where, path, n, shape[1]),
+                                  _i32(where, counts, n), n, shape[1], _stream_ptr(stream)), where)
 
 
 def qnre_cache_copy_pages(cache: PagedCache, src, dst, stream=None) -> None:
     """Page src[i] to page dst[i] in every layer."""
-    where, n = "qnre_cache_copy_pages", src.numel()
-    _check(load_library().qnre_cache_copy_pages(cache.handle, _i32(where, src, n), _i32(where, dst, n), n,
-                                                _stream_ptr(stream)), where)
+    where, lib = "qnre_cache_copy_pages", load_library()
+    if _native is not None:
+        st = _native.cache_rows(_entry[where], cache.address, src, dst, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    n = src.numel()
+    _check(lib.qnre_cache_copy_pages(cache.handle, _i32(where, src, n), _i32(where, dst, n), n,
+                                     _stream_ptr(stream)), where)
 
 
 def _norm_inputs(where: str, q, k, q_norm_w, k_norm_w, cos_sin, positions):
@@ -771,14 +798,19 @@ def qnre_tree_attention(q, cache: PagedCache, layer: int, rows, mask, out, lse=N
                         workspace=None, stream=None) -> None:
     """Attention of drafted nodes q [n, nodes, Hq, D] over their rows' tokens and the nodes of mask (int64 [n, nodes];
     None: a chain) into out (contiguous); scale defaults to 1/sqrt(D)."""
-    where = "qnre_tree_attention"
+    where, lib = "qnre_tree_attention", load_library()
+    if _native is not None:
+        st = _native.attention(_entry[where], q, cache.address, layer, rows, mask, out, lse, counts, scale, workspace,
+                               _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
     tq = _view4(q)
     n, nodes, heads, dim = _sizes(q)
     to = _same(where, out, q)
     tm = _i64(where, mask, n, nodes)
     if workspace is None:
         raise QnreError(1, f"{where}: workspace is missing (tree_attention_workspace)")
-    _check(load_library().qnre_tree_attention(
+    _check(lib.qnre_tree_attention(
         tq, cache.handle, layer, _i32(where, rows, n), tm, _i32(where, counts, n),
         dim ** -0.5 if scale is None else scale, to,
         None if lse is None else _f32(where, lse, n, nodes, heads), _contig(workspace, where),
@@ -789,7 +821,12 @@ def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sampl
                      node_counts=None, stream=None) -> None:
     """Walk drafted trees against target_probs [n, nodes, V] (fp32; draft_probs alike or None) with given random
     numbers; fills path [n, nodes], counts [n] and next_token [n] (int32)."""
-    where = "qnre_verify_tree"
+    where, lib = "qnre_verify_tree", load_library()
+    if _native is not None:
+        st = _native.verify(_entry[where], target_probs, draft_probs, tokens, parents, accept_u, sample_u, path, counts,
+                            next_token, node_counts, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
     shape = _sizes(target_probs)
     if len(shape) != 3:
         raise QnreError(1, f"{where}: target_probs must be [n, nodes, vocab]")
@@ -807,7 +844,7 @@ def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sampl
             if t.dtype is not _float32 or t.shape != shape or (t.stride(2) != 1 and vocab > 1):
                 raise QnreError(1, f"{where}: probabilities are float32 [n, nodes, vocab], each row contiguous")
             rows += [t.data_ptr(), t.stride(0), t.stride(1)]
-    _check(load_library().qnre_verify_tree(
+    _check(lib.qnre_verify_tree(
         *rows, n, nodes, vocab, _i32(where, tokens, n, nodes), _i32(where, parents, n, nodes),
         _i32(where, node_counts, n), _f32(where, accept_u, n, nodes), _f32(where, sample_u, n),
         _i32(where, path, n, nodes), _i32(where, counts, n), _i32(where, next_token, n), _stream_ptr(stream)), where)

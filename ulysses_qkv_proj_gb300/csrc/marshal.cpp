@@ -1,8 +1,8 @@
 // marshal.cpp -- what the Python binding reads off torch tensors, in one native call each: a decode step's kernels
 // run for a few microseconds, and a tensor's shape, strides, dtype and pointer cost one microsecond of
-// Python attribute reads (0.1 here).  The calls of the norm family are made whole from here, as their kernels are the
-// shortest and their arguments the most: an append 6.5 us -> 3.7 on a Grace core, a gradient 8.6 -> 4.6.  Built where torch's
-// headers are found; the binding falls back to Python reads without it, with the same checks and the same errors.
+// Python attribute reads (0.1 here).  The decoding calls are made whole from here: an append 6.5 us -> 3.7 on a Grace core,
+// a gradient 8.6 -> 4.6, a verification 6.9 -> 3.3, an attention 8.4 -> 5.4.  Built where torch's headers are found; the
+// binding falls back to Python reads without it, with the same checks and the same errors.
 // Everything here answers None where a read fails, or throws (a sparse tensor's strides): the binding's Python reads
 // then name what is wrong.
 #include <torch/csrc/autograd/python_variable.h>
@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <initializer_list>
@@ -234,6 +235,133 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// attention(fn, q, cache address, layer, rows, mask, out, lse, counts, scale, workspace, reader, stream)
+PyObject* attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    void *fn, *cache, *out;
+    qnre_tensor4_t q;
+    int layer;
+    int32_t *rows, *counts = nullptr;
+    uint64_t* mask = nullptr;
+    float* lse = nullptr;
+    qnre_stream_t stream;
+    if (n != 13 || !read_entry(args[0], &fn) || !read_view4(args[1], &q) || !read_entry(args[2], &cache) ||
+        !read_int(args[3], &layer) || !read_pointer(args[4], 3, {q.shape[0]}, &rows) ||
+        (args[5] != Py_None && !read_pointer(args[5], 4, {q.shape[0], q.shape[1]}, &mask)) ||
+        !read_pointer(args[6], q.dtype, {q.shape[0], q.shape[1], q.shape[2], q.shape[3]}, &out) ||
+        (args[7] != Py_None &&
+         !read_pointer(args[7], QNRE_DTYPE_FP32, {q.shape[0], q.shape[1], q.shape[2]}, &lse)) ||
+        (args[8] != Py_None && !read_pointer(args[8], 3, {q.shape[0]}, &counts)) ||
+        (args[9] != Py_None && !PyFloat_Check(args[9])) || !THPVariable_Check(args[10]))
+      Py_RETURN_NONE;
+    const double scale = args[9] == Py_None ? std::pow(static_cast<double>(q.shape[3]), -0.5) : PyFloat_AS_DOUBLE(args[9]);
+    const at::Tensor& ws = THPVariable_Unpack(args[10]);
+    if (!ws.is_contiguous()) Py_RETURN_NONE;
+    void* ws_data = ws.data_ptr();
+    const uint64_t ws_bytes = ws.nbytes();
+    if (!read_stream(args[11], args[12], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_tree_attention)>(fn)(&q, static_cast<const qnre_cache_t*>(cache), layer, rows, mask,
+                                                              counts, static_cast<float>(scale), out, lse, ws_data,
+                                                              ws_bytes, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// Rows of probabilities [n, nodes, vocab], each contiguous, or None.
+struct Rows {
+  const float* data = nullptr;
+  int64_t stride0 = 0, stride1 = 0;
+};
+
+bool read_rows(PyObject* obj, at::IntArrayRef shape, Rows* r) {
+  if (!THPVariable_Check(obj)) return false;
+  const at::Tensor& t = THPVariable_Unpack(obj);
+  if (t.scalar_type() != at::kFloat || !t.sizes().equals(shape)) return false;
+  const bool whole = t.is_contiguous();
+  if (!whole && t.stride(2) != 1 && shape[2] > 1) return false;
+  r->data = static_cast<const float*>(t.data_ptr());
+  r->stride0 = whole ? shape[1] * shape[2] : t.stride(0);
+  r->stride1 = whole ? shape[2] : t.stride(1);
+  return true;
+}
+
+// verify(fn, target, draft, tokens, parents, accept_u, sample_u, path, counts, next, node_counts, reader, stream)
+PyObject* verify(PyObject*, PyObject* const* args, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    Rows target, draft;
+    int32_t *tokens, *parents, *path, *counts, *next, *node_counts = nullptr;
+    float *accept, *sample;
+    qnre_stream_t stream;
+    if (argc != 13 || !read_entry(args[0], &fn) || !THPVariable_Check(args[1])) Py_RETURN_NONE;
+    const at::IntArrayRef shape = THPVariable_Unpack(args[1]).sizes();
+    if (shape.size() != 3 || shape[0] > INT_MAX || shape[1] > INT_MAX) Py_RETURN_NONE;
+    const int64_t n = shape[0], nodes = shape[1];
+    if (!read_rows(args[1], shape, &target) || (args[2] != Py_None && !read_rows(args[2], shape, &draft)) ||
+        !read_pointer(args[3], 3, {n, nodes}, &tokens) || !read_pointer(args[4], 3, {n, nodes}, &parents) ||
+        !read_pointer(args[5], QNRE_DTYPE_FP32, {n, nodes}, &accept) ||
+        !read_pointer(args[6], QNRE_DTYPE_FP32, {n}, &sample) || !read_pointer(args[7], 3, {n, nodes}, &path) ||
+        !read_pointer(args[8], 3, {n}, &counts) || !read_pointer(args[9], 3, {n}, &next) ||
+        (args[10] != Py_None && !read_pointer(args[10], 3, {n}, &node_counts)))
+      Py_RETURN_NONE;
+    if (!read_stream(args[11], args[12], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_verify_tree)>(fn)(
+        target.data, target.stride0, target.stride1, draft.data, draft.stride0, draft.stride1, static_cast<int>(n),
+        static_cast<int>(nodes), shape[2], tokens, parents, node_counts, accept, sample, path, counts, next, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// cache_rows(fn, cache address, first, second, reader, stream): truncate, fork, reserve, copy_pages
+PyObject* cache_rows(PyObject*, PyObject* const* args, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    void *fn, *cache;
+    int32_t *first, *second;
+    qnre_stream_t stream;
+    if (argc != 6 || !read_entry(args[0], &fn) || !read_entry(args[1], &cache) || !THPVariable_Check(args[2]))
+      Py_RETURN_NONE;
+    const int64_t n = THPVariable_Unpack(args[2]).numel();
+    if (n > INT_MAX || !read_pointer(args[2], 3, {n}, &first) || !read_pointer(args[3], 3, {n}, &second)) Py_RETURN_NONE;
+    if (!read_stream(args[4], args[5], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_cache_truncate)>(fn)(static_cast<const qnre_cache_t*>(cache), first, second,
+                                                              static_cast<int>(n), stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// compact(fn, cache address, rows, path, counts, reader, stream)
+PyObject* compact(PyObject*, PyObject* const* args, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    void *fn, *cache;
+    int32_t *rows, *path, *counts;
+    qnre_stream_t stream;
+    if (argc != 7 || !read_entry(args[0], &fn) || !read_entry(args[1], &cache) || !THPVariable_Check(args[2]) ||
+        !THPVariable_Check(args[3]))
+      Py_RETURN_NONE;
+    const int64_t n = THPVariable_Unpack(args[2]).numel();
+    const at::IntArrayRef shape = THPVariable_Unpack(args[3]).sizes();
+    if (n > INT_MAX || shape.size() != 2 || shape[1] > INT_MAX || !read_pointer(args[2], 3, {n}, &rows) ||
+        !read_pointer(args[3], 3, {n, shape[1]}, &path) || !read_pointer(args[4], 3, {n}, &counts))
+      Py_RETURN_NONE;
+    if (!read_stream(args[5], args[6], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_cache_compact)>(fn)(static_cast<const qnre_cache_t*>(cache), rows, path, counts,
+                                                             static_cast<int>(n), static_cast<int>(shape[1]), stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
 template <typename F>
 PyCFunction fast(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -244,6 +372,10 @@ PyMethodDef methods[] = {{"view4", view4, METH_O, nullptr},
                          {"norm", fast(norm), METH_FASTCALL, nullptr},
                          {"norm_backward", fast(norm_backward), METH_FASTCALL, nullptr},
                          {"append", fast(append), METH_FASTCALL, nullptr},
+                         {"attention", fast(attention), METH_FASTCALL, nullptr},
+                         {"verify", fast(verify), METH_FASTCALL, nullptr},
+                         {"cache_rows", fast(cache_rows), METH_FASTCALL, nullptr},
+                         {"compact", fast(compact), METH_FASTCALL, nullptr},
                          {"sizes", sizes, METH_O, nullptr},
                          {"type_code", type_code, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
