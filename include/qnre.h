@@ -566,6 +566,7 @@ qnre_status_t ulysses_sage2_scatter_qkv(const qnre_tensor4_t* q, const qnre_tens
  * page block_table[r][p / page_size].  A page of one layer keeps each head's
  * tokens together: page_size * head_dim values in a run.  page_refs counts
  * the rows that hold a page; 0 means free.  Blocks a row does not hold are -1.
+ * A length below 0 counts as 0.
  */
 typedef struct {
   void* k;              /* [layers, pages, heads, page_size, head_dim], contiguous, 16-byte aligned */

@@ -212,3 +212,30 @@ def test_copy_pages_and_graph_replay():
         assert b.sim.reserve([0, 1], [5, 5])
         b.sim.compact([0, 1], path.tolist(), kept.tolist())
     b.check()
+
+
+@pytest.mark.parametrize("length", [-1, -100, -2 ** 31])
+def test_lengths_below_zero_count_as_none(length):
+    """Truncate, compact, fork and reserve of a row with such a length leave the other rows' blocks alone."""
+    b = Both(page=8, pages=40, rows=6, blocks=9)
+    b.grow([0, 1, 2, 3, 5], [64, 60, 63, 20, 9])
+    b.grow([0, 2], [6, 9])
+    for call in ("truncate", "compact", "reserve"):
+        b.cache.seq_lens[3] = length
+        b.sim.lens[3] = 0
+        if call == "truncate":
+            b.truncate([3], [5])
+        elif call == "compact":
+            assert b.reserve([3], [4])
+            b.cache.seq_lens[3] = length
+            b.compact([3], [[0, 2, 3]], [3])
+        else:
+            assert b.reserve([3], [30])
+            b.cache.seq_lens[3] = b.sim.lens[3] = 0
+        b.check()
+    b.truncate([3], [0])
+    b.cache.seq_lens[3] = length
+    b.sim.lens[3] = 0
+    b.fork([3], [4])
+    b.cache.seq_lens[3] = 0
+    b.check()

@@ -23,6 +23,8 @@ struct CacheView {
     atomicOr(status, QNRE_CACHE_BAD_ROW);
     return false;
   }
+  // Tokens of a valid row; a length below 0 counts as none, so that no block number is ever negative.
+  __device__ __forceinline__ int length(int row) const { return max(lens[row], 0); }
   // Page of token `pos` of a valid row, or -1 (none, or a table entry outside the cache).
   __device__ __forceinline__ int page_of(int row, int pos) const {
     const int block = pos / page_size;

@@ -36,7 +36,7 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Releases the blocks of `row` from `first` on (one warp).
+// Releases the blocks of `row` from `first` >= 0 on (one warp).
 __device__ __forceinline__ void release_from(const CacheView& c, int row, int first, int lane) {
   int32_t* table = c.table + static_cast<long long>(row) * c.max_blocks;
   for (int j = first + lane; j < c.max_blocks; j += 32) {
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(128) truncate_kernel(CacheView c, const int32_
   if (i >= n) return;
   const int row = rows[i];
   if (!c.row_ok(row)) return;
-  const int old = c.lens[row];
+  const int old = c.length(row);
   const int len = min(old, max(lens[i], 0));
   __syncwarp();
   if (lane == 0) c.lens[row] = len;
@@ -78,14 +78,15 @@ __global__ void __launch_bounds__(128) fork_kernel(CacheView c, const int32_t* s
   if (!c.row_ok(s) || !c.row_ok(d)) return;
   const int32_t* from = c.table + static_cast<long long>(s) * c.max_blocks;
   int32_t* to = c.table + static_cast<long long>(d) * c.max_blocks;
-  const int len = c.lens[s];
+  const int len = c.length(s);
   const bool used = s == d || c.lens[d] != 0 || to[0] >= 0;
   __syncwarp();
   if (used) {
     if (lane == 0) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
     return;
   }
-  const int blocks = min((len + c.page_size - 1) / c.page_size, c.max_blocks);
+  const long long touched = (static_cast<long long>(len) + c.page_size - 1) / c.page_size;
+  const int blocks = static_cast<int>(min(touched, static_cast<long long>(c.max_blocks)));
   for (int j = lane; j < blocks; j += 32) {
     const int page = from[j];
     to[j] = page;
@@ -133,7 +134,7 @@ struct Window {
 __device__ __forceinline__ Window window_of(const CacheView& c, const int32_t* rows, const int32_t* counts, int i) {
   Window w{rows[i], 0, 0, 0, true};
   if (w.row < 0 || w.row >= c.rows) return w;
-  w.len = max(c.lens[w.row], 0);
+  w.len = c.length(w.row);
   const int count = counts[i];
   if (count <= 0) return w;
   w.first = w.len / c.page_size;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CacheView c, cons
     if (part == 0 && threadIdx.x == 0) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
     return;
   }
-  const int len = c.lens[row];
+  const int len = c.length(row);
   for (int j = threadIdx.x; j < count; j += kCopyThreads) {
     const int node = path[static_cast<long long>(i) * nodes + j];
     from[j] = to[j] = -1;

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
     if (APPEND) {
       const int row = a.rows[b];
       const bool row_ok = row >= 0 && row < a.cache.rows;
-      at = row_ok ? a.cache.lens[row] : 0;
+      at = row_ok ? a.cache.length(row) : 0;
       pos = static_cast<long long>(at) + s;
       if (kind != 0) {
         if (a.counts != nullptr && s >= a.counts[b]) continue;

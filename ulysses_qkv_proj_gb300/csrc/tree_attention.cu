@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(kThreads<D, REP>, 1) attention_kernel(const __
     const int row = a.rows[i];
     int len = 0, cnt = 0;
     if (row >= 0 && row < a.c.rows) {
-      len = min(max(a.c.lens[row], 0), room);
+      len = min(a.c.length(row), room);
       cnt = a.counts != nullptr ? min(max(a.counts[i], 0), a.nodes) : a.nodes;
     } else if (blockIdx.x == 0) {
       atomicOr(a.c.status, QNRE_CACHE_BAD_ROW);
