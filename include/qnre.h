@@ -555,8 +555,9 @@ qnre_status_t ulysses_sage2_scatter_qkv(const qnre_tensor4_t* q, const qnre_tens
 /* Bits of a cache's status word (set by kernels, never cleared by them). */
 #define QNRE_CACHE_NO_PAGES 0x1u   /* a reserve needed more free pages than there were: it changed nothing */
 #define QNRE_CACHE_BAD_ROW 0x2u    /* a row index outside [0, rows), a fork onto a row in use: skipped */
-#define QNRE_CACHE_BAD_PAGE 0x4u   /* a token's page was missing or outside the cache: a write or move was skipped,
-                                      an attention read it as zeros */
+#define QNRE_CACHE_BAD_PAGE 0x4u   /* a token's page was missing or outside the cache, or, where it was to be written or
+                                      kept, held by another row too: an append skipped it, a compact kept the tokens
+                                      before it, an attention read a missing one as zeros */
 #define QNRE_CACHE_BAD_REFS 0x8u   /* a page was released more often than it was taken */
 #define QNRE_CACHE_WAIT_TIMEOUT 0x10u /* a pipeline wait of the attention kernel ran past its limit; outputs incomplete */
 
@@ -603,6 +604,8 @@ typedef struct {
  *   seq_lens + path[i][j] moves to seq_lens + j for j < counts[i], in every layer; the
  *   length grows by counts[i] and blocks past it are released.  path[i] ascends
  *   strictly from path[i][0] >= 0.  path is [n, nodes] int32, nodes <= QNRE_MAX_NODES.
+ *   Kept tokens lie in pages that no other row holds (qnre_cache_reserve sees to that): the row grows
+ *   up to the first that would not, or whose own or source page is missing (QNRE_CACHE_BAD_PAGE).
  * qnre_cache_copy_pages -- page src[i] to page dst[i] in every layer; the destinations
  *   are distinct and no source.
  *   rows, lens, counts, src, dst: device int32 [n].
@@ -645,7 +648,8 @@ qnre_status_t qnre_cache_copy_pages(const qnre_cache_t* cache, const int32_t* sr
  * qnre_qkv_norm_rope_append -- qnre_qk_norm_rope over the new tokens [n, S, ...] of the
  *   rows rows[i] (device int32 [n]), with k and v written into layer `layer` of the cache
  *   as tokens seq_lens + s, s < min(counts[i], S) (counts NULL: all S).  The pages must be
- *   there (qnre_cache_reserve); lengths do not change (qnre_cache_compact).  v is a view like k.
+ *   there and held by no other row (qnre_cache_reserve), else the token is skipped and QNRE_CACHE_BAD_PAGE set;
+ *   lengths do not change (qnre_cache_compact).  v is a view like k.
  *   positions NULL: seq_lens + s.  Every token's q_out is written.
  */
 qnre_status_t qnre_qk_norm_rope(const qnre_tensor4_t* q, const qnre_tensor4_t* k, const void* q_norm_w,

@@ -239,3 +239,83 @@ def test_lengths_below_zero_count_as_none(length):
     b.fork([3], [4])
     b.cache.seq_lens[3] = 0
     b.check()
+
+
+def _append(b, rows, tokens, gen):
+    """Appends `tokens` random tokens to each row in layer 0; returns what v holds."""
+    heads, dim = b.sim.k.shape[2], b.sim.k.shape[4]
+    n = len(rows)
+    qkv = torch.randn((n, tokens, 3 * heads, dim), generator=gen).to(b.sim.k.dtype).cuda()
+    q, k, v = qkv[:, :, :heads], qkv[:, :, heads:2 * heads], qkv[:, :, 2 * heads:]
+    w = torch.ones(dim, dtype=qkv.dtype, device="cuda")
+    out = torch.empty((n, tokens, heads, dim), dtype=qkv.dtype, device="cuda")
+    b.qb.qnre_qkv_norm_rope_append(q, k, v, w, w, D.angles(256, dim).cuda(), None, out, b.cache, 0, _i32(rows))
+    assert torch.isfinite(out).all()
+    return v.cpu()
+
+
+def test_a_refused_reserve_leaves_shared_pages_alone():
+    """Two forks, no free page for their copies: their drafts go nowhere and their lengths stay."""
+    b = Both(page=16, pages=2)
+    b.grow([0], [20])
+    b.fork([0], [1])
+    b.check()
+    assert not b.reserve([0, 1], [3, 3])
+    b.check(b.qb.CACHE_NO_PAGES)
+    gen = torch.Generator().manual_seed(1)
+    _append(b, [0, 1], 3, gen)
+    b.check(b.qb.CACHE_BAD_PAGE)
+    for path in ([0, 1, 2], [0, 2, -1], [1, 2, -1]):
+        b.qb.qnre_cache_compact(b.cache, _i32([0, 1]), _i32([path, path]), _i32([2, 2]))
+        b.check(b.qb.CACHE_BAD_PAGE)
+    # with the other row gone the page is this row's own again
+    b.truncate([1], [0])
+    v = _append(b, [0], 3, gen)
+    assert b.cache.status() == 0
+    page = b.sim.table[0][1]
+    for s in range(3):
+        assert torch.equal(b.cache.v[0, page, :, 4 + s].cpu(), v[0, s])
+    b.qb.qnre_cache_compact(b.cache, _i32([0]), _i32([[0, 2, -1]]), _i32([2]))
+    assert b.cache.status() == 0 and b.cache.seq_lens.tolist()[:2] == [22, 0]
+    assert torch.equal(b.cache.v[0, page, :, 5].cpu(), v[0, 2])
+
+
+def test_append_skips_the_shared_page_and_fills_the_next():
+    """A shared open page and an own one behind it: only the own one takes its tokens."""
+    b = Both(page=8, pages=4, layers=1)
+    b.grow([0], [13])
+    b.fork([0], [1])
+    own = 3
+    b.cache.block_table[1, 2] = own
+    b.cache.page_refs[own] = 1
+    before = b.cache.v.cpu().clone()
+    v = _append(b, [1], 6, torch.Generator().manual_seed(2))
+    assert b.cache.status() == b.qb.CACHE_BAD_PAGE
+    after = b.cache.v.cpu()
+    for s in range(3):
+        assert torch.equal(after[0, own, :, s], v[0, 3 + s])
+    after[0, own, :, :3] = before[0, own, :, :3]
+    assert torch.equal(after, before)
+
+
+@pytest.mark.parametrize("path,kept", [([0, 1, 2, 3, 4], 2), ([0, 1, 3, 4, 5], 2), ([0, 2, 3, 4, 5], 1), ([2, 3, 4, 5, 6], 0),
+                                       ([1, 2, 3, 4, 5], 1), ([0, 1], 2)])
+@pytest.mark.parametrize("layers", [1, 8])
+def test_lengths_stay_within_the_pages_a_row_holds(path, kept, layers):
+    """Two more slots in the last page and none behind it: tokens that would lie, or come from, past it are not kept."""
+    b = Both(page=8, pages=8, blocks=3, layers=layers, heads=4)
+    b.grow([0, 2], [14, 9])
+    assert b.reserve([0], [2])
+    listed = len(path)
+    b.qb.qnre_cache_compact(b.cache, _i32([0, 2]), _i32([path, [0] * listed]), _i32([listed, 0]))
+    b.sim.compact([0, 2], [path[:kept], []], [kept, 0])
+    b.check(b.qb.CACHE_BAD_PAGE if kept < listed else 0)
+
+
+def test_lengths_stay_within_the_table():
+    b = Both(page=8, pages=20, blocks=3)
+    b.grow([1], [22])
+    assert b.reserve([1], [2])
+    b.qb.qnre_cache_compact(b.cache, _i32([1]), _i32([list(range(40))]), _i32([40]))
+    b.sim.compact([1], [[0, 1]], [2])
+    b.check(b.qb.CACHE_BAD_PAGE)

@@ -312,36 +312,46 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(CacheView c, c
 }
 
 // A compact: a cluster of CTAs takes a row, moves its accepted tokens, and when all of them have, its first CTA grows
-// the length and releases the blocks past it.  One thread owns 16 bytes of a head's channels for one
+// the length and releases the blocks past it.  Tokens are kept up to the first one that would lie in a page that is missing
+// or that other rows hold too, or whose source is missing: nothing is written to a shared page, and the length never passes
+// what the row's own pages hold.  Every CTA looks for itself and the first one grows by the least that any of them found.
+// One thread owns 16 bytes of a head's channels for one
 // (layer, K or V, head) and takes the tokens in ascending order, eight at a time: a later token's source is
 // never an earlier one's destination (path ascends strictly, so path[j'] >= j' > j), so reads stay ahead of writes
 // without any ordering between threads.
 __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CacheView c, const int32_t* rows, const int32_t* path,
                                                                const int32_t* counts, int nodes, int lanes, int ctas) {
   __shared__ long long from[QNRE_MAX_NODES], to[QNRE_MAX_NODES];  // head 0's byte offsets in layer 0, -1: skip
+  __shared__ int kept, least;  // tokens; the cluster's least in its first CTA
+  if (threadIdx.x == 0) kept = least = QNRE_MAX_NODES;
+  __syncthreads();
+  ptx::cluster_arrive();  // `least` stands
   pdl_wait();
   const int i = blockIdx.x / ctas, part = blockIdx.x % ctas;
   const int row = rows[i];
-  const int count = min(max(counts[i], 0), nodes);
+  const int listed = min(max(counts[i], 0), nodes);
   if (row < 0 || row >= c.rows) {
     if (part == 0 && threadIdx.x == 0) atomicOr(c.status, QNRE_CACHE_BAD_ROW);
+    __syncwarp();
+    ptx::cluster_wait();
     return;
   }
   const int len = c.length(row);
-  for (int j = threadIdx.x; j < count; j += kCopyThreads) {
+  for (int j = threadIdx.x; j < listed; j += kCopyThreads) {
     const int node = path[static_cast<long long>(i) * nodes + j];
     from[j] = to[j] = -1;
-    if (node == j) continue;
-    const int ps = node >= 0 && len <= 0x7FFFFFFF - node ? c.page_of(row, len + node) : -1;
     const int pd = len <= 0x7FFFFFFF - j ? c.page_of(row, len + j) : -1;
-    if (ps < 0 || pd < 0) {
+    const int ps = node == j ? pd : (node >= 0 && len <= 0x7FFFFFFF - node ? c.page_of(row, len + node) : -1);
+    if (ps < 0 || pd < 0 || c.refs[pd] > 1) {
+      atomicMin(&kept, j);
       atomicOr(c.status, QNRE_CACHE_BAD_PAGE);
-      continue;
+    } else if (node != j) {
+      from[j] = c.token_offset(0, ps, 0, len + node);
+      to[j] = c.token_offset(0, pd, 0, len + j);
     }
-    from[j] = c.token_offset(0, ps, 0, len + node);
-    to[j] = c.token_offset(0, pd, 0, len + j);
   }
   __syncthreads();
+  const int count = min(kept, listed);
   const int row_vecs = c.head_dim / 8;
   const long long head_bytes = static_cast<long long>(c.page_size) * c.head_dim * 2;
   const long long layer_bytes = static_cast<long long>(c.pages) * c.heads * head_bytes;
@@ -362,11 +372,18 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CacheView c, cons
         if (j0 + e < count && from[j0 + e] >= 0) *reinterpret_cast<uint4*>(pool + to[j0 + e]) = r[e];
     }
   }
+  __syncwarp();
+  ptx::cluster_wait();
+  if (threadIdx.x == 0 && count < listed)
+    asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(
+                     ptx::mapa_shared(ptx::smem_addr(&least), 0)),
+                 "r"(count)
+                 : "memory");
   // every CTA of the row has read its length and table and made its moves
   __syncwarp();
   ptx::cluster_sync();
   if (part == 0 && threadIdx.x < 32) {
-    const int grown = static_cast<int>(min(static_cast<long long>(len) + count, 0x7FFFFFFFll));
+    const int grown = static_cast<int>(min(static_cast<long long>(len) + min(listed, least), 0x7FFFFFFFll));
     if (threadIdx.x == 0) c.lens[row] = grown;
     const long long first = (static_cast<long long>(grown) + c.page_size - 1) / c.page_size;
     if (first < c.max_blocks) release_from(c, row, static_cast<int>(first), threadIdx.x);

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
     const int h0 = chunk * step, h1 = min(h0 + step, heads);
     const View& in = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
 
-    int page = -1, at = 0;
+    int page = -1, at = 0, holders = 0;
     long long pos = s;
     if (APPEND) {
       const int row = a.rows[b];
@@ -239,6 +239,8 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
           if (lane == 0) atomicOr(a.cache.status, row_ok ? QNRE_CACHE_BAD_PAGE : QNRE_CACHE_BAD_ROW);
           continue;
         }
+        // a page that other rows hold too is not written; the count arrives while the values do
+        holders = a.cache.refs[page];
       }
     }
     auto out_row = [&](int h) -> char* {
@@ -246,8 +248,11 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
       return (kind == 0 ? a.q_out : a.k_out).row(b, s, h);
     };
     if (APPEND && kind == 2) {
-      for (int h = h0 + sub; h < h1; h += kRows)
-        reinterpret_cast<uint4*>(out_row(h))[l] = reinterpret_cast<const uint4*>(in.row(b, s, h))[l];
+      for (int h = h0 + sub; h < h1; h += kRows) {
+        const uint4 x = reinterpret_cast<const uint4*>(in.row(b, s, h))[l];
+        if (holders <= 1) reinterpret_cast<uint4*>(out_row(h))[l] = x;
+      }
+      if (holders > 1 && lane == 0) atomicOr(a.cache.status, QNRE_CACHE_BAD_PAGE);
       continue;
     }
     // the first heads are on their way before the position and its angles are asked for
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
         other_channels<RH, BF16>(raw[u], ang, y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = mul2(fma2(x[i], w[i], mul2(y[i], wp[i])), r2);
-        if (h + u * kRows < h1) *reinterpret_cast<uint4*>(dst) = pack<BF16>(o);
+        if (h + u * kRows < h1 && (!APPEND || holders <= 1)) *reinterpret_cast<uint4*>(dst) = pack<BF16>(o);
         dst += dst_step;
       }
     }
