@@ -689,6 +689,7 @@ qnre_status_t qnre_qkv_norm_rope_append(const qnre_tensor4_t* q, const qnre_tens
  *            that may overlap (on different streams) need one each.
  * More than 2^31-1 tiles of 128 tokens (of max_blocks * page_size tokens a row, each K head and group of rows counted,
  * four more a unit) -> QNRE_ERR_CAPACITY.
+ * The cache's k and v lie in the current device's own memory (else QNRE_ERR_INVALID_ARG).
  * What lies in slots that a node does not see never reaches its result, not even NaN.
  * The result does not depend on timing: sums are taken in an order that the lengths fix.
  */

@@ -414,3 +414,86 @@ def test_whole_native_cache_and_tree_calls_refuse_as_the_python_ones(lib, monkey
     assert None not in with_native
     monkeypatch.setattr(qb, "_native", None)
     assert with_native == outcomes()
+
+
+def _calls(torch, cache, dev="cpu"):
+    """Every decoding call as (name, arguments by name, call of them); all of them would be accepted on one device."""
+    bf, i32 = torch.bfloat16, torch.int32
+    z = lambda *s, dtype=bf: torch.zeros(s, dtype=dtype, device=dev)
+    norm = dict(q=z(2, 3, 4, 64), k=z(2, 3, 2, 64), wq=z(64), wk=z(64), table=z(8, 32, dtype=torch.float32),
+                pos=z(2, 3, dtype=i32))
+    outs = dict(qo=z(2, 3, 4, 64), ko=z(2, 3, 2, 64))
+    rows = dict(a=z(2, dtype=i32), b=z(2, dtype=i32))
+    s = _Stream()
+    r = [("norm", {**norm, **outs}, lambda a: qb.qnre_qk_norm_rope(a["q"], a["k"], a["wq"], a["wk"], a["table"], a["pos"], a["qo"],
+                                                                   a["ko"], stream=s)),
+         ("backward", {**norm, **outs, "gq": z(2, 3, 4, 64), "gk": z(2, 3, 2, 64), "dwq": z(64, dtype=torch.float32),
+                       "dwk": z(64, dtype=torch.float32), "ws": z(1 << 20, dtype=torch.uint8)},
+          lambda a: qb.qnre_qk_norm_rope_backward(a["gq"], a["gk"], a["q"], a["k"], a["wq"], a["wk"], a["table"], a["pos"], a["qo"],
+                                                  a["ko"], a["dwq"], a["dwk"], a["ws"], stream=s)),
+         ("append", {**norm, "v": z(2, 3, 2, 64), "qo": outs["qo"], "rows": rows["a"], "counts": rows["b"]},
+          lambda a: qb.qnre_qkv_norm_rope_append(a["q"], a["k"], a["v"], a["wq"], a["wk"], a["table"], a["pos"], a["qo"], cache, 0,
+                                                 a["rows"], a["counts"], stream=s)),
+         ("compact", {**rows, "path": z(2, 3, dtype=i32)},
+          lambda a: qb.qnre_cache_compact(cache, a["a"], a["path"], a["b"], s)),
+         ("masks", dict(parents=z(2, 3, dtype=i32), masks=z(2, 3, dtype=torch.int64), depths=z(2, 3, dtype=i32)),
+          lambda a: qb.qnre_tree_masks(a["parents"], a["masks"], a["depths"], s)),
+         ("attention", dict(q=z(2, 3, 4, 64), rows=rows["a"], mask=z(2, 3, dtype=torch.int64), out=z(2, 3, 4, 64),
+                            lse=z(2, 3, 4, dtype=torch.float32), counts=rows["b"], ws=z(64 << 20, dtype=torch.uint8)),
+          lambda a: qb.qnre_tree_attention(a["q"], cache, 0, a["rows"], a["mask"], a["out"], a["lse"], a["counts"], None, a["ws"], s)),
+         ("verify", dict(target=z(2, 3, 50, dtype=torch.float32), draft=z(2, 3, 50, dtype=torch.float32), tokens=z(2, 3, dtype=i32),
+                         parents=z(2, 3, dtype=i32), accept=z(2, 3, dtype=torch.float32), sample=z(2, dtype=torch.float32),
+                         path=z(2, 3, dtype=i32), counts=z(2, dtype=i32), next=z(2, dtype=i32), nodes=z(2, dtype=i32)),
+          lambda a: qb.qnre_verify_tree(a["target"], a["draft"], a["tokens"], a["parents"], a["accept"], a["sample"], a["path"],
+                                        a["counts"], a["next"], a["nodes"], s))]
+    for name in ("truncate", "fork", "reserve", "copy_pages"):
+        call = getattr(qb, "qnre_cache_" + name)
+        r.append((name, rows, lambda a, call=call: call(cache, a["a"], a["b"], s)))
+    return r
+
+
+class _Entries:
+    """Stands in for the library: every entry point answers 0 and notes that it was reached."""
+
+    def __init__(self):
+        self.reached = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.reached.append(name) or 0
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_tensors_of_another_device_are_refused(lib, monkeypatch, native):
+    """One argument at a time on another device (meta), then all on the CPU of a machine that has CUDA."""
+    torch = pytest.importorskip("torch")
+    if native and qb._native is None:
+        pytest.skip("_marshal is not built")
+    pool = lambda dev: [torch.zeros((1, 4, 2, 8, 64), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    i = lambda dev, *s: torch.zeros(s, dtype=torch.int32, device=dev)
+    cache = qb.PagedCache(*pool("cpu"), i("cpu", 3, 2), i("cpu", 3), i("cpu", 4))
+    for at in range(5):
+        dev = ["cpu"] * 5
+        dev[at] = "meta"
+        k, v = pool(dev[0])[0], pool(dev[1])[1]
+        with pytest.raises(qb.QnreError, match="one device"):
+            qb.PagedCache(k, v, i(dev[2], 3, 2), i(dev[3], 3), i(dev[4], 4))
+    if not native:
+        monkeypatch.setattr(qb, "_native", None)
+    fake = _Entries()
+    monkeypatch.setattr(qb, "load_library", lambda *a: fake)
+    for name, args, call in _calls(torch, cache):
+        for key in args:
+            with pytest.raises(qb.QnreError, match="current CUDA device"):
+                call({**args, key: args[key].to("meta")})
+    assert not fake.reached
+    # a machine with CUDA: the same tensors, all on the CPU, do not reach an entry point either (the native reads ask
+    # torch's library itself, so only the Python ones can be told that there is one)
+    if not native:
+        for name, args, call in _calls(torch, cache):
+            call(args)
+        assert len(fake.reached) == 11
+        monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+        for name, args, call in _calls(torch, cache):
+            with pytest.raises(qb.QnreError, match="current CUDA device"):
+                call(args)
+        assert len(fake.reached) == 11

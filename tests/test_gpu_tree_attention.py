@@ -298,3 +298,33 @@ def test_narrow_heads_over_runs_of_tiles(lens, nodes, Hq, Hk, dtype):
     assert torch.isinf(out[:, -1, :, 33]).all()
     cols = [x for x in range(64) if x != 33]
     assert torch.equal(out[:, -1][..., cols], clean[0][:, -1][..., cols])
+
+
+def test_pools_and_tensors_outside_this_gpu_are_refused():
+    """Pools in the host's memory, at the C entry itself (with one row tile and with several); then tensors of the CPU."""
+    import ctypes
+    qb = _qb()
+    lib = qb.load_library()
+    c = Case([20, 3], 20, 16, 2, 128, 16, "bf16", seed=2)
+    for nodes in (1, 20):
+        q = c.q[:, :nodes].contiguous().cuda()
+        c.run()
+        ws = qb.tree_attention_workspace(q, c.cache)
+        rows = torch.tensor(c.rows, dtype=torch.int32).cuda()
+        out = torch.full_like(q, 5.0)
+        pinned = [t.pin_memory() for t in (c.k, c.v)]
+        for which in range(2):
+            s = qb._Cache.from_buffer_copy(c.cache._struct)
+            setattr(s, "kv"[which], pinned[which].data_ptr())
+            st = lib.qnre_tree_attention(qb._view4(q), ctypes.byref(s), c.layer, rows.data_ptr(), None, None, c.scale,
+                                         out.data_ptr(), None, ws.data_ptr(), ws.numel(), qb._stream_ptr(None))
+            assert st == 1
+        with pytest.raises(qb.QnreError):
+            qb.qnre_tree_attention(q, c.cache, c.layer, rows.cpu(), None, out, workspace=ws)
+        with pytest.raises(qb.QnreError):
+            qb.qnre_tree_attention(q, c.cache, c.layer, rows, None, out.cpu(), workspace=ws)
+        torch.cuda.synchronize()
+        assert (out == 5.0).all()
+    cpu = qb.PagedCache(c.k, c.v, c.table, c.seq, torch.ones(c.k.shape[1], dtype=torch.int32))
+    with pytest.raises(qb.QnreError):
+        qb.qnre_cache_truncate(cpu, rows.cpu(), rows.cpu())

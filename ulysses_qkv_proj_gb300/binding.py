@@ -517,6 +517,8 @@ class PagedCache:
         rows = seq_lens.numel()
         if block_table.dim() != 2 or block_table.shape[0] != rows or page_refs.numel() != pages:
             raise QnreError(1, "PagedCache: block_table [rows, max_blocks], seq_lens [rows], page_refs [pages]")
+        if any(t.device != k.device for t in (v, block_table, seq_lens, page_refs)):
+            raise QnreError(1, "PagedCache: every tensor must lie on one device")
         self.k, self.v = k, v
         self.block_table, self.seq_lens, self.page_refs = block_table, seq_lens, page_refs
         self.status_word = torch.zeros(1, dtype=torch.int32, device=k.device)
@@ -620,67 +622,86 @@ def _weight(where: str, w, dim: int, like) -> int:
     return w.data_ptr()
 
 
+def _on_device(where: str, *tensors) -> None:
+    """Every tensor given (None passes) lies on one device, and that is the current CUDA device, where the kernels run.
+    (Where there is no CUDA at all tensors of the CPU pass: the entry points check them and launch nothing.)"""
+    import torch
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) == 1:
+        d = devices.pop()
+        if d.type == "cuda" and d.index == torch.cuda.current_device():
+            return
+        if d.type == "cpu" and not torch.cuda.is_available():
+            return
+    raise QnreError(1, f"{where}: every tensor must lie on the current CUDA device")
+
+
 def qnre_cache_truncate(cache: PagedCache, rows, lens, stream=None) -> None:
     """Row rows[i] keeps its first lens[i] tokens; the blocks past them are released (0 frees the row)."""
     where, lib = "qnre_cache_truncate", load_library()
     if _native is not None:
-        st = _native.cache_rows(_entry[where], cache.address, rows, lens, _stream_ptr, stream)
+        st = _native.cache_rows(_entry[where], cache.address, cache.k, rows, lens, _stream_ptr, stream)
         if st is not None:
             return _check(st, where)
     n = rows.numel()
-    _check(lib.qnre_cache_truncate(cache.handle, _i32(where, rows, n), _i32(where, lens, n), n,
-                                   _stream_ptr(stream)), where)
+    args = _i32(where, rows, n), _i32(where, lens, n), n
+    _on_device(where, cache.k, rows, lens)
+    _check(lib.qnre_cache_truncate(cache.handle, *args, _stream_ptr(stream)), where)
 
 
 def qnre_cache_fork(cache: PagedCache, src, dst, stream=None) -> None:
     """Empty row dst[i] becomes a copy of row src[i] that shares its pages."""
     where, lib = "qnre_cache_fork", load_library()
     if _native is not None:
-        st = _native.cache_rows(_entry[where], cache.address, src, dst, _stream_ptr, stream)
+        st = _native.cache_rows(_entry[where], cache.address, cache.k, src, dst, _stream_ptr, stream)
         if st is not None:
             return _check(st, where)
     n = src.numel()
-    _check(lib.qnre_cache_fork(cache.handle, _i32(where, src, n), _i32(where, dst, n), n,
-                               _stream_ptr(stream)), where)
+    args = _i32(where, src, n), _i32(where, dst, n), n
+    _on_device(where, cache.k, src, dst)
+    _check(lib.qnre_cache_fork(cache.handle, *args, _stream_ptr(stream)), where)
 
 
 def qnre_cache_reserve(cache: PagedCache, rows, counts, stream=None) -> None:
     """Pages of its own for the next counts[i] tokens of row rows[i] (lowest free pages, copy on write)."""
     where, lib = "qnre_cache_reserve", load_library()
     if _native is not None:
-        st = _native.cache_rows(_entry[where], cache.address, rows, counts, _stream_ptr, stream)
+        st = _native.cache_rows(_entry[where], cache.address, cache.k, rows, counts, _stream_ptr, stream)
         if st is not None:
             return _check(st, where)
     n = rows.numel()
-    _check(lib.qnre_cache_reserve(cache.handle, _i32(where, rows, n), _i32(where, counts, n), n,
-                                  _stream_ptr(stream)), where)
+    args = _i32(where, rows, n), _i32(where, counts, n), n
+    _on_device(where, cache.k, rows, counts)
+    _check(lib.qnre_cache_reserve(cache.handle, *args, _stream_ptr(stream)), where)
 
 
 def qnre_cache_compact(cache: PagedCache, rows, path, counts, stream=None) -> None:
     """Keep the accepted nodes path[i][:counts[i]] of row rows[i]'s drafts; its length grows by counts[i]."""
     where, lib = "qnre_cache_compact", load_library()
     if _native is not None:
-        st = _native.compact(_entry[where], cache.address, rows, path, counts, _stream_ptr, stream)
+        st = _native.compact(_entry[where], cache.address, cache.k, rows, path, counts, _stream_ptr, stream)
         if st is not None:
             return _check(st, where)
     n = rows.numel()
     shape = _sizes(path)
     if len(shape) != 2:
         raise QnreError(1, f"{where}: path must be [n, nodes]")
-    _check(lib.qnre_cache_compact(cache.handle, _i32(where, rows, n), _i32(where, path, n, shape[1]),
-                                  _i32(where, counts, n), n, shape[1], _stream_ptr(stream)), where)
+    args = _i32(where, rows, n), _i32(where, path, n, shape[1]), _i32(where, counts, n), n, shape[1]
+    _on_device(where, cache.k, rows, path, counts)
+    _check(lib.qnre_cache_compact(cache.handle, *args, _stream_ptr(stream)), where)
 
 
 def qnre_cache_copy_pages(cache: PagedCache, src, dst, stream=None) -> None:
     """Page src[i] to page dst[i] in every layer."""
     where, lib = "qnre_cache_copy_pages", load_library()
     if _native is not None:
-        st = _native.cache_rows(_entry[where], cache.address, src, dst, _stream_ptr, stream)
+        st = _native.cache_rows(_entry[where], cache.address, cache.k, src, dst, _stream_ptr, stream)
         if st is not None:
             return _check(st, where)
     n = src.numel()
-    _check(lib.qnre_cache_copy_pages(cache.handle, _i32(where, src, n), _i32(where, dst, n), n,
-                                     _stream_ptr(stream)), where)
+    args = _i32(where, src, n), _i32(where, dst, n), n
+    _on_device(where, cache.k, src, dst)
+    _check(lib.qnre_cache_copy_pages(cache.handle, *args, _stream_ptr(stream)), where)
 
 
 def _norm_inputs(where: str, q, k, q_norm_w, k_norm_w, cos_sin, positions):
@@ -704,7 +725,9 @@ def qnre_qk_norm_rope(q, k, q_norm_w, k_norm_w, cos_sin, positions, q_out, k_out
         if st is not None:
             return _check(st, where)
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
-    _check(lib.qnre_qk_norm_rope(*head, style, pos, _view4(q_out), _view4(k_out), _stream_ptr(stream)), where)
+    args = *head, style, pos, _view4(q_out), _view4(k_out)
+    _on_device(where, q, k, q_norm_w, k_norm_w, cos_sin, positions, q_out, k_out)
+    _check(lib.qnre_qk_norm_rope(*args, _stream_ptr(stream)), where)
 
 
 def qk_norm_rope_workspace(q, k=None):
@@ -728,9 +751,10 @@ def qnre_qk_norm_rope_backward(gq, gk, q, k, q_norm_w, k_norm_w, cos_sin, positi
             return _check(st, where)
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
     D = q.shape[-1]
-    _check(lib.qnre_qk_norm_rope_backward(
-        _view4(gq), _view4(gk), *head, style, pos, _view4(dq), _view4(dk), _f32(where, dq_norm_w, D), _f32(where, dk_norm_w, D), _contig(workspace, where),
-        workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
+    args = (_view4(gq), _view4(gk), *head, style, pos, _view4(dq), _view4(dk), _f32(where, dq_norm_w, D),
+            _f32(where, dk_norm_w, D), _contig(workspace, where), workspace.numel() * workspace.element_size())
+    _on_device(where, gq, gk, q, k, q_norm_w, k_norm_w, cos_sin, positions, dq, dk, dq_norm_w, dk_norm_w, workspace)
+    _check(lib.qnre_qk_norm_rope_backward(*args, _stream_ptr(stream)), where)
 
 
 def qnre_qkv_norm_rope_append(q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q_out, cache: PagedCache, layer: int,
@@ -739,14 +763,16 @@ def qnre_qkv_norm_rope_append(q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q
     where = "qnre_qkv_norm_rope_append"
     lib, style = load_library(), ROPE_STYLES.get(rope_style, -1)
     if _native is not None:
-        st = _native.append(_entry[where], q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q_out, cache.address, layer,
-                            rows, counts, style, _stream_ptr, stream)
+        st = _native.append(_entry[where], q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q_out, cache.address, cache.k,
+                            layer, rows, counts, style, _stream_ptr, stream)
         if st is not None:
             return _check(st, where)
     head, pos = _norm_inputs(where, q, k, q_norm_w, k_norm_w, cos_sin, positions)
     n = q.shape[0]
-    _check(lib.qnre_qkv_norm_rope_append(
-        head[0], head[1], _view4(v), *head[2:], style, pos, _view4(q_out), cache.handle, layer, _i32(where, rows, n), _i32(where, counts, n), _stream_ptr(stream)), where)
+    args = (head[0], head[1], _view4(v), *head[2:], style, pos, _view4(q_out), cache.handle, layer, _i32(where, rows, n),
+            _i32(where, counts, n))
+    _on_device(where, q, k, v, q_norm_w, k_norm_w, cos_sin, positions, q_out, cache.k, rows, counts)
+    _check(lib.qnre_qkv_norm_rope_append(*args, _stream_ptr(stream)), where)
 
 
 def qnre_tree_masks(parents, masks=None, depths=None, stream=None) -> None:
@@ -755,8 +781,9 @@ def qnre_tree_masks(parents, masks=None, depths=None, stream=None) -> None:
     if parents.dim() != 2:
         raise QnreError(1, f"{where}: parents must be [n, nodes]")
     n, nodes = _sizes(parents)
-    _check(load_library().qnre_tree_masks(_i32(where, parents), n, nodes, _i64(where, masks, n, nodes),
-                                          _i32(where, depths, n, nodes), _stream_ptr(stream)), where)
+    args = _i32(where, parents), n, nodes, _i64(where, masks, n, nodes), _i32(where, depths, n, nodes)
+    _on_device(where, parents, masks, depths)
+    _check(load_library().qnre_tree_masks(*args, _stream_ptr(stream)), where)
 
 
 def tree_attention_workspace(q, cache: PagedCache):
@@ -800,8 +827,8 @@ def qnre_tree_attention(q, cache: PagedCache, layer: int, rows, mask, out, lse=N
     None: a chain) into out (contiguous); scale defaults to 1/sqrt(D)."""
     where, lib = "qnre_tree_attention", load_library()
     if _native is not None:
-        st = _native.attention(_entry[where], q, cache.address, layer, rows, mask, out, lse, counts, scale, workspace,
-                               _stream_ptr, stream)
+        st = _native.attention(_entry[where], q, cache.address, cache.k, layer, rows, mask, out, lse, counts, scale,
+                               workspace, _stream_ptr, stream)
         if st is not None:
             return _check(st, where)
     tq = _view4(q)
@@ -810,11 +837,11 @@ def qnre_tree_attention(q, cache: PagedCache, layer: int, rows, mask, out, lse=N
     tm = _i64(where, mask, n, nodes)
     if workspace is None:
         raise QnreError(1, f"{where}: workspace is missing (tree_attention_workspace)")
-    _check(lib.qnre_tree_attention(
-        tq, cache.handle, layer, _i32(where, rows, n), tm, _i32(where, counts, n),
-        dim ** -0.5 if scale is None else scale, to,
-        None if lse is None else _f32(where, lse, n, nodes, heads), _contig(workspace, where),
-        workspace.numel() * workspace.element_size(), _stream_ptr(stream)), where)
+    args = (tq, cache.handle, layer, _i32(where, rows, n), tm, _i32(where, counts, n),
+            dim ** -0.5 if scale is None else scale, to, None if lse is None else _f32(where, lse, n, nodes, heads),
+            _contig(workspace, where), workspace.numel() * workspace.element_size())
+    _on_device(where, q, cache.k, rows, mask, out, lse, counts, workspace)
+    _check(lib.qnre_tree_attention(*args, _stream_ptr(stream)), where)
 
 
 def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sample_u, path, counts, next_token,
@@ -844,7 +871,8 @@ def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sampl
             if t.dtype is not _float32 or t.shape != shape or (t.stride(2) != 1 and vocab > 1):
                 raise QnreError(1, f"{where}: probabilities are float32 [n, nodes, vocab], each row contiguous")
             rows += [t.data_ptr(), t.stride(0), t.stride(1)]
-    _check(lib.qnre_verify_tree(
-        *rows, n, nodes, vocab, _i32(where, tokens, n, nodes), _i32(where, parents, n, nodes),
-        _i32(where, node_counts, n), _f32(where, accept_u, n, nodes), _f32(where, sample_u, n),
-        _i32(where, path, n, nodes), _i32(where, counts, n), _i32(where, next_token, n), _stream_ptr(stream)), where)
+    args = (*rows, n, nodes, vocab, _i32(where, tokens, n, nodes), _i32(where, parents, n, nodes),
+            _i32(where, node_counts, n), _f32(where, accept_u, n, nodes), _f32(where, sample_u, n),
+            _i32(where, path, n, nodes), _i32(where, counts, n), _i32(where, next_token, n))
+    _on_device(where, target_probs, draft_probs, tokens, parents, accept_u, sample_u, path, counts, next_token, node_counts)
+    _check(lib.qnre_verify_tree(*args, _stream_ptr(stream)), where)

@@ -5,6 +5,8 @@
 // binding falls back to Python reads without it, with the same checks and the same errors.
 // Everything here answers None where a read fails, or throws (a sparse tensor's strides): the binding's Python reads
 // then name what is wrong.
+#include <ATen/Context.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <Python.h>
@@ -63,6 +65,22 @@ bool read_pointer(PyObject* obj, int code, std::initializer_list<int64_t> shape,
   if (code_of(t) != code || !t.is_contiguous() || !t.sizes().equals(at::IntArrayRef(shape))) return false;
   *out = static_cast<T*>(t.data_ptr());
   return true;
+}
+
+// Every tensor given (None passes) lies on one device, and that is the current CUDA device, where the kernels run.  (Where
+// there is no CUDA at all tensors of the CPU pass: the entry points check them and launch nothing.)
+bool on_device(std::initializer_list<PyObject*> objs) {
+  const at::Tensor* first = nullptr;
+  for (PyObject* o : objs) {
+    if (o == Py_None) continue;
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (first == nullptr) first = &t;
+    if (t.device() != first->device()) return false;
+  }
+  if (first == nullptr) return false;
+  if (!first->is_cuda()) return first->is_cpu() && !at::hasCUDA();
+  return first->device() == c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice();
 }
 
 // view4(tensor) -> the bytes of its qnre_tensor4_t, or None where it is no rank-4 tensor of a known float type.
@@ -166,7 +184,8 @@ PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int style;
     qnre_stream_t stream;
     if (n != 12 || !read_entry(args[0], &fn) || !read_head(args + 1, args[6], &h) || !read_view4(args[7], &qo) ||
-        !read_view4(args[8], &ko) || !read_int(args[9], &style))
+        !read_view4(args[8], &ko) || !read_int(args[9], &style) ||
+        !on_device({args[1], args[2], args[3], args[4], args[5], args[6], args[7], args[8]}))
       Py_RETURN_NONE;
     if (!read_stream(args[10], args[11], &stream)) return nullptr;
     int st;
@@ -191,7 +210,9 @@ PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
         !read_head(args + 3, args[8], &h) || !read_view4(args[9], &dq) || !read_view4(args[10], &dk) ||
         !read_pointer(args[11], QNRE_DTYPE_FP32, {h.q.shape[3]}, &dwq) ||
         !read_pointer(args[12], QNRE_DTYPE_FP32, {h.q.shape[3]}, &dwk) || !THPVariable_Check(args[13]) ||
-        !read_int(args[14], &style))
+        !read_int(args[14], &style) ||
+        !on_device({args[1], args[2], args[3], args[4], args[5], args[6], args[7], args[8], args[9], args[10], args[11],
+                    args[12], args[13]}))
       Py_RETURN_NONE;
     const at::Tensor& ws = THPVariable_Unpack(args[13]);
     if (!ws.is_contiguous()) Py_RETURN_NONE;
@@ -208,7 +229,7 @@ PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// append(fn, q, k, v, wq, wk, cos_sin, positions, q_out, cache address, layer, rows, counts, style, reader, stream)
+// append(fn, q, k, v, wq, wk, cos_sin, positions, q_out, cache address, its k, layer, rows, counts, style, reader, stream)
 PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     void *fn, *cache;
@@ -217,14 +238,15 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int32_t *rows, *counts = nullptr;
     int layer, style;
     qnre_stream_t stream;
-    if (n != 16) Py_RETURN_NONE;
+    if (n != 17) Py_RETURN_NONE;
     PyObject* const head[] = {args[1], args[2], args[4], args[5], args[6]};
     if (!read_entry(args[0], &fn) || !read_head(head, args[7], &h) || !read_view4(args[3], &v) ||
-        !read_view4(args[8], &qo) || !read_entry(args[9], &cache) || !read_int(args[10], &layer) ||
-        !read_pointer(args[11], 3, {h.q.shape[0]}, &rows) ||
-        (args[12] != Py_None && !read_pointer(args[12], 3, {h.q.shape[0]}, &counts)) || !read_int(args[13], &style))
+        !read_view4(args[8], &qo) || !read_entry(args[9], &cache) || !read_int(args[11], &layer) ||
+        !read_pointer(args[12], 3, {h.q.shape[0]}, &rows) ||
+        (args[13] != Py_None && !read_pointer(args[13], 3, {h.q.shape[0]}, &counts)) || !read_int(args[14], &style) ||
+        !on_device({args[1], args[2], args[3], args[4], args[5], args[6], args[7], args[8], args[10], args[12], args[13]}))
       Py_RETURN_NONE;
-    if (!read_stream(args[14], args[15], &stream)) return nullptr;
+    if (!read_stream(args[15], args[16], &stream)) return nullptr;
     int st;
     Py_BEGIN_ALLOW_THREADS;
     st = reinterpret_cast<decltype(&qnre_qkv_norm_rope_append)>(fn)(
@@ -235,7 +257,7 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// attention(fn, q, cache address, layer, rows, mask, out, lse, counts, scale, workspace, reader, stream)
+// attention(fn, q, cache address, its k, layer, rows, mask, out, lse, counts, scale, workspace, reader, stream)
 PyObject* attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     void *fn, *cache, *out;
@@ -245,21 +267,23 @@ PyObject* attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     uint64_t* mask = nullptr;
     float* lse = nullptr;
     qnre_stream_t stream;
-    if (n != 13 || !read_entry(args[0], &fn) || !read_view4(args[1], &q) || !read_entry(args[2], &cache) ||
-        !read_int(args[3], &layer) || !read_pointer(args[4], 3, {q.shape[0]}, &rows) ||
-        (args[5] != Py_None && !read_pointer(args[5], 4, {q.shape[0], q.shape[1]}, &mask)) ||
-        !read_pointer(args[6], q.dtype, {q.shape[0], q.shape[1], q.shape[2], q.shape[3]}, &out) ||
-        (args[7] != Py_None &&
-         !read_pointer(args[7], QNRE_DTYPE_FP32, {q.shape[0], q.shape[1], q.shape[2]}, &lse)) ||
-        (args[8] != Py_None && !read_pointer(args[8], 3, {q.shape[0]}, &counts)) ||
-        (args[9] != Py_None && !PyFloat_Check(args[9])) || !THPVariable_Check(args[10]))
+    if (n != 14 || !read_entry(args[0], &fn) || !read_view4(args[1], &q) || !read_entry(args[2], &cache) ||
+        !read_int(args[4], &layer) || !read_pointer(args[5], 3, {q.shape[0]}, &rows) ||
+        (args[6] != Py_None && !read_pointer(args[6], 4, {q.shape[0], q.shape[1]}, &mask)) ||
+        !read_pointer(args[7], q.dtype, {q.shape[0], q.shape[1], q.shape[2], q.shape[3]}, &out) ||
+        (args[8] != Py_None &&
+         !read_pointer(args[8], QNRE_DTYPE_FP32, {q.shape[0], q.shape[1], q.shape[2]}, &lse)) ||
+        (args[9] != Py_None && !read_pointer(args[9], 3, {q.shape[0]}, &counts)) ||
+        (args[10] != Py_None && !PyFloat_Check(args[10])) || !THPVariable_Check(args[11]) ||
+        !on_device({args[1], args[3], args[5], args[6], args[7], args[8], args[9], args[11]}))
       Py_RETURN_NONE;
-    const double scale = args[9] == Py_None ? std::pow(static_cast<double>(q.shape[3]), -0.5) : PyFloat_AS_DOUBLE(args[9]);
-    const at::Tensor& ws = THPVariable_Unpack(args[10]);
+    const double scale =
+        args[10] == Py_None ? std::pow(static_cast<double>(q.shape[3]), -0.5) : PyFloat_AS_DOUBLE(args[10]);
+    const at::Tensor& ws = THPVariable_Unpack(args[11]);
     if (!ws.is_contiguous()) Py_RETURN_NONE;
     void* ws_data = ws.data_ptr();
     const uint64_t ws_bytes = ws.nbytes();
-    if (!read_stream(args[11], args[12], &stream)) return nullptr;
+    if (!read_stream(args[12], args[13], &stream)) return nullptr;
     int st;
     Py_BEGIN_ALLOW_THREADS;
     st = reinterpret_cast<decltype(&qnre_tree_attention)>(fn)(&q, static_cast<const qnre_cache_t*>(cache), layer, rows, mask,
@@ -305,7 +329,8 @@ PyObject* verify(PyObject*, PyObject* const* args, Py_ssize_t argc) {
         !read_pointer(args[5], QNRE_DTYPE_FP32, {n, nodes}, &accept) ||
         !read_pointer(args[6], QNRE_DTYPE_FP32, {n}, &sample) || !read_pointer(args[7], 3, {n, nodes}, &path) ||
         !read_pointer(args[8], 3, {n}, &counts) || !read_pointer(args[9], 3, {n}, &next) ||
-        (args[10] != Py_None && !read_pointer(args[10], 3, {n}, &node_counts)))
+        (args[10] != Py_None && !read_pointer(args[10], 3, {n}, &node_counts)) ||
+        !on_device({args[1], args[2], args[3], args[4], args[5], args[6], args[7], args[8], args[9], args[10]}))
       Py_RETURN_NONE;
     if (!read_stream(args[11], args[12], &stream)) return nullptr;
     int st;
@@ -318,17 +343,19 @@ PyObject* verify(PyObject*, PyObject* const* args, Py_ssize_t argc) {
   });
 }
 
-// cache_rows(fn, cache address, first, second, reader, stream): truncate, fork, reserve, copy_pages
+// cache_rows(fn, cache address, its k, first, second, reader, stream): truncate, fork, reserve, copy_pages
 PyObject* cache_rows(PyObject*, PyObject* const* args, Py_ssize_t argc) {
   return guarded([&]() -> PyObject* {
     void *fn, *cache;
     int32_t *first, *second;
     qnre_stream_t stream;
-    if (argc != 6 || !read_entry(args[0], &fn) || !read_entry(args[1], &cache) || !THPVariable_Check(args[2]))
+    if (argc != 7 || !read_entry(args[0], &fn) || !read_entry(args[1], &cache) || !THPVariable_Check(args[3]))
       Py_RETURN_NONE;
-    const int64_t n = THPVariable_Unpack(args[2]).numel();
-    if (n > INT_MAX || !read_pointer(args[2], 3, {n}, &first) || !read_pointer(args[3], 3, {n}, &second)) Py_RETURN_NONE;
-    if (!read_stream(args[4], args[5], &stream)) return nullptr;
+    const int64_t n = THPVariable_Unpack(args[3]).numel();
+    if (n > INT_MAX || !read_pointer(args[3], 3, {n}, &first) || !read_pointer(args[4], 3, {n}, &second) ||
+        !on_device({args[2], args[3], args[4]}))
+      Py_RETURN_NONE;
+    if (!read_stream(args[5], args[6], &stream)) return nullptr;
     int st;
     Py_BEGIN_ALLOW_THREADS;
     st = reinterpret_cast<decltype(&qnre_cache_truncate)>(fn)(static_cast<const qnre_cache_t*>(cache), first, second,
@@ -338,21 +365,22 @@ PyObject* cache_rows(PyObject*, PyObject* const* args, Py_ssize_t argc) {
   });
 }
 
-// compact(fn, cache address, rows, path, counts, reader, stream)
+// compact(fn, cache address, its k, rows, path, counts, reader, stream)
 PyObject* compact(PyObject*, PyObject* const* args, Py_ssize_t argc) {
   return guarded([&]() -> PyObject* {
     void *fn, *cache;
     int32_t *rows, *path, *counts;
     qnre_stream_t stream;
-    if (argc != 7 || !read_entry(args[0], &fn) || !read_entry(args[1], &cache) || !THPVariable_Check(args[2]) ||
-        !THPVariable_Check(args[3]))
+    if (argc != 8 || !read_entry(args[0], &fn) || !read_entry(args[1], &cache) || !THPVariable_Check(args[3]) ||
+        !THPVariable_Check(args[4]))
       Py_RETURN_NONE;
-    const int64_t n = THPVariable_Unpack(args[2]).numel();
-    const at::IntArrayRef shape = THPVariable_Unpack(args[3]).sizes();
-    if (n > INT_MAX || shape.size() != 2 || shape[1] > INT_MAX || !read_pointer(args[2], 3, {n}, &rows) ||
-        !read_pointer(args[3], 3, {n, shape[1]}, &path) || !read_pointer(args[4], 3, {n}, &counts))
+    const int64_t n = THPVariable_Unpack(args[3]).numel();
+    const at::IntArrayRef shape = THPVariable_Unpack(args[4]).sizes();
+    if (n > INT_MAX || shape.size() != 2 || shape[1] > INT_MAX || !read_pointer(args[3], 3, {n}, &rows) ||
+        !read_pointer(args[4], 3, {n, shape[1]}, &path) || !read_pointer(args[5], 3, {n}, &counts) ||
+        !on_device({args[2], args[3], args[4], args[5]}))
       Py_RETURN_NONE;
-    if (!read_stream(args[5], args[6], &stream)) return nullptr;
+    if (!read_stream(args[6], args[7], &stream)) return nullptr;
     int st;
     Py_BEGIN_ALLOW_THREADS;
     st = reinterpret_cast<decltype(&qnre_cache_compact)>(fn)(static_cast<const qnre_cache_t*>(cache), rows, path, counts,

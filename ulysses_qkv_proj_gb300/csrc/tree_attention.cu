@@ -1094,6 +1094,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
   if (lse != nullptr && i4 == 0) lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
+// Memory of device `dev` itself: K and V of more than one row tile come by cluster multicast, which is for a GPU's own
+// memory alone, so pools of another device or of the host are refused, whatever the number of nodes.
+bool own_memory(const void* p, int dev) {
+  cudaPointerAttributes at{};
+  return cudaPointerGetAttributes(&at, p) == cudaSuccess && at.type == cudaMemoryTypeDevice && at.device == dev;
+}
+
 constexpr uint64_t kDescBytes = 152 * sizeof(Desc);
 constexpr uint64_t kMlBytes = 2ull * kMaxCtas * 128 * 2 * 4;
 
@@ -1217,6 +1224,12 @@ qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* c
       if (overlaps(w, r)) return QNRE_ERR_ALIAS;
   if (overlaps(ro, rw) || overlaps(ro, rl) || overlaps(rw, rl)) return QNRE_ERR_ALIAS;
 
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return QNRE_ERR_CUDA;
+  if (!own_memory(cache->k, dev) || !own_memory(cache->v, dev)) return QNRE_ERR_INVALID_ARG;
+
   AttnArgs a{};
   a.c = view_of(cache);
   a.layer = layer;
@@ -1253,10 +1266,6 @@ qnre_status_t qnre_tree_attention(const qnre_tensor4_t* q, const qnre_cache_t* c
   if (!encode_tiled_16bit(&a.tq, own.data, bf16, 4, q_dims, q_strides, q_box) ||
       !encode_tiled_16bit(&a.tk, cache->k, bf16, 4, dims, strides, box) ||
       !encode_tiled_16bit(&a.tv, cache->v, bf16, 4, dims, strides, box))
-    return QNRE_ERR_CUDA;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return QNRE_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (D == 128) return bf16 ? launch_size<128, true>(a, sms, s) : launch_size<128, false>(a, sms, s);
