@@ -690,7 +690,8 @@ qnre_status_t qnre_qkv_norm_rope_append(const qnre_tensor4_t* q, const qnre_tens
  * More than 2^31-1 tiles of 128 tokens (of max_blocks * page_size tokens a row, each K head and group of rows counted,
  * four more a unit) -> QNRE_ERR_CAPACITY.
  * The cache's k and v lie in the current device's own memory (else QNRE_ERR_INVALID_ARG).
- * What lies in slots that a node does not see never reaches its result, not even NaN.
+ * What lies in slots that a node does not see never reaches its result, not even NaN; infinite or NaN values of V that it
+ * does see give their sum, whatever their weights are rounded to.
  * The result does not depend on timing: sums are taken in an order that the lengths fix.
  */
 qnre_status_t qnre_tree_attention_workspace_bytes(int head_dim, uint64_t* bytes);

@@ -328,3 +328,71 @@ def test_pools_and_tensors_outside_this_gpu_are_refused():
     cpu = qb.PagedCache(c.k, c.v, c.table, c.seq, torch.ones(c.k.shape[1], dtype=torch.int32))
     with pytest.raises(qb.QnreError):
         qb.qnre_cache_truncate(cpu, rows.cpu(), rows.cpu())
+
+
+def _place(c, i, x, col, val):
+    """Element `col` of V of token x of request i, in every head."""
+    c.v[c.layer, c.table[c.rows[i], x // c.page], :, x % c.page, col] = val
+    c.values[i][x, :, col] = val
+
+
+SEEN = [  # lens, nodes, Hq, Hk, dim, page, dtype: rows laid out four times, twice, once, and shared by row tiles
+    ([300, 5, 1000], 1, 8, 2, 128, 16, "bf16"),
+    ([300, 5, 1000], 1, 8, 2, 64, 24, "fp16"),
+    ([257, 128, 700], 5, 16, 2, 128, 16, "fp16"),
+    ([257, 128, 700], 5, 16, 2, 64, 16, "bf16"),
+    ([300, 130, 1000], 16, 14, 2, 128, 32, "bf16"),
+    ([300, 130, 1000], 16, 14, 2, 64, 32, "fp16"),
+    ([300, 130], 40, 16, 2, 128, 16, "bf16"),
+    ([300, 130], 64, 8, 2, 64, 16, "fp16"),
+    ([40000], 1, 8, 2, 128, 64, "bf16"),            # units that span many CTAs
+    ([40000], 20, 16, 2, 64, 64, "fp16"),
+]
+
+
+@pytest.mark.parametrize("lens,nodes,Hq,Hk,dim,page,dtype", SEEN)
+def test_infinite_values_in_the_context(lens, nodes, Hq, Hk, dim, page, dtype):
+    """+inf, -inf, both, and NaN in V of cached tokens, first, last and between; one request stays finite."""
+    c = Case(lens, nodes, Hq, Hk, dim, page, dtype, seed=nodes + dim)
+    finite = [v.clone() for v in c.values]
+    inf = float("inf")
+    for i, L in enumerate(lens):
+        if i == 1:
+            continue
+        for x, col, val in ((0, 3, inf), (L - 1, 20, -inf), (L // 2, 33, inf), (1, 33, -inf), (L // 3, dim - 1, float("nan")),
+                            (L - 1, dim - 2, inf), (2, dim - 2, inf)):
+            _place(c, i, x, col, val)
+    out, lse = c.run()
+    special, want = [3, 20, 33, dim - 1, dim - 2], torch.tensor([inf, -inf, float("nan"), float("nan"), inf])
+    for i in range(len(lens)):
+        if i != 1:
+            got = out[i][..., special].float()
+            assert torch.equal(torch.isnan(got), torch.isnan(want).expand_as(got))
+            assert torch.equal(got.nan_to_num(0.0, inf, -inf), want.nan_to_num(0.0, inf, -inf).expand_as(got))
+            out[i][..., special] = 0
+            finite[i][..., special] = 0
+    c.values = finite
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("nodes,Hq", [(1, 8), (5, 16), (16, 14)])
+@pytest.mark.parametrize("dtype,below", [("bf16", 40.0), ("fp16", 25.0)])
+def test_infinite_values_of_hardly_any_weight(nodes, Hq, dtype, below):
+    """The infinite token's score lies far below another's: its weight counts, however few bits it is rounded to."""
+    c = Case([200], nodes, Hq, 2, 128, 16, dtype, seed=3)
+    c.q[:] = 0
+    c.q[..., 0] = 8.0
+    for x in range(200 + nodes):
+        c.keys[0][x] = 0
+        c.keys[0][x, :, 0] = 0.0 if x else below / (8.0 * c.scale)
+        c.k[1, c.table[c.rows[0], x // 16], :, x % 16] = c.keys[0][x]
+    c.masks = [[(1 << 64) - 1 >> 64 - nodes] * nodes]
+    _place(c, 0, 77, 5, float("inf"))
+    _place(c, 0, 78, 100, float("-inf"))
+    out, lse = c.run()
+    assert (out[0, ..., 5] == float("inf")).all() and (out[0, ..., 100] == float("-inf")).all()
+    for x, col in ((77, 5), (78, 100)):
+        c.values[0][x, :, col] = 0
+    out[0, ..., 5] = out[0, ..., 100] = 0
+    c.values[0][:, :, [5, 100]] = 0
+    c.check(out, lse)

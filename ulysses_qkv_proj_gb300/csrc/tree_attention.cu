@@ -27,7 +27,11 @@
 //
 // Slots that a row does not see must not reach it, whatever they hold: scores are replaced before use; V rows of
 // slots past the drafts are zeroed in shared memory, and non-finite V elements of drafted nodes (which
-// some rows see and others do not) are zeroed there and added to the rows that see them at the end.
+// some rows see and others do not) are zeroed there and added to the rows that see them at the end.  Every row sees the
+// context, whose V stays as it is; but an infinite element meets zeros of P in the other copies of a row (or where a weight
+// rounds to nothing), and 0 inf is NaN.  So when a row's sum is not finite the context is searched, and a channel that
+// holds non-finite elements gets their sum: infinity, or NaN for a NaN or for both signs.  Each warp votes on its own rows and
+// searches alone: a vote of all softmax warps would be a barrier more for every unit (16 trees of 32 nodes +1.5 %).
 //
 // Bound: HBM up to 128 rows; above, the bytes that enter an SM (64 KB of K and V a tile of 1024 cycles of
 // tensor work, at 34 bytes a cycle and SM).  Measured (device time): 64 requests of 130..32000 tokens, 64 heads on 8,
@@ -509,6 +513,39 @@ __device__ __noinline__ float add_nonfinite(const AttnArgs& a, int row, int kvh,
   return x;
 }
 
+// Which of the 32 channels from `c` on hold +inf, -inf or NaN in V of the tokens [first, last) (a whole warp).
+struct Kinds {
+  uint32_t plus, minus, nan;
+};
+template <bool BF16>
+__device__ __noinline__ Kinds search_context(const AttnArgs& a, int row, int kvh, int first, int last, int c) {
+  Kinds k{0, 0, 0};
+  for (int pos = first + static_cast<int>(threadIdx.x % 32); pos < last; pos += 32) {
+    const int page = a.c.page_of(row, pos);
+    if (page < 0) continue;
+    const uint4* at = reinterpret_cast<const uint4*>(a.c.v + a.c.token_offset(a.layer, page, kvh, pos) + c * 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 w = at[i];
+      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t x = words[e / 2] >> (e % 2 * 16) & 0xFFFFu;
+        if (nonfinite_mask<BF16>(x) & 0xFFFFu) {
+          const float f = to_float<BF16>(x);
+          const uint32_t bit = 1u << (8 * i + e);
+          k.plus |= f > 0.f ? bit : 0u;
+          k.minus |= f < 0.f ? bit : 0u;
+          k.nan |= f != f ? bit : 0u;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  return Kinds{__reduce_or_sync(0xFFFFFFFFu, k.plus), __reduce_or_sync(0xFFFFFFFFu, k.minus),
+               __reduce_or_sync(0xFFFFFFFFu, k.nan)};
+}
+
 // Pieces [first, last) of a V row of a tile past the context: slots without a token are zeroed; in drafted ones the non-finite
 // elements are, and true is returned.
 template <int D, bool BF16>
@@ -771,6 +808,20 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
           for (int k = 0; k < kSoft / kRows; ++k) x[i] += join[(k * kRows + ur) * 33 + jc + i];
         }
         soft_sync<kSoft>();
+      }
+      uint64_t odd = 0;  // 0 x is 0 for every finite x
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) odd = fma2(pair(x[i], x[i + 1]), 0, odd);
+      float odd0, odd1;
+      unpair(odd, odd0, odd1);
+      if (__any_sync(0xFFFFFFFFu, row_ok && odd0 + odd1 != 0.f)) {  // (NaN compares unequal)
+        const Kinds k = search_context<BF16>(a, a.rows[s.req], s.kvh, s.t0 * kTile, min(s.t1 * kTile, s.len), c);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const uint32_t bit = 1u << (jc + i);
+          if ((k.plus | k.minus | k.nan) & bit)
+            x[i] = (k.nan | (k.plus & k.minus)) & bit ? NAN : (k.plus & bit ? INFINITY : -INFINITY);
+        }
       }
       if (bad != 0) {
 #pragma unroll
