@@ -396,3 +396,34 @@ def test_infinite_values_of_hardly_any_weight(nodes, Hq, dtype, below):
     out[0, ..., 5] = out[0, ..., 100] = 0
     c.values[0][:, :, [5, 100]] = 0
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("nodes", [1, 10, 20])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_many_small_weights_under_a_large_one(nodes, dtype):
+    """10^5 tokens 17.5 nats under one score keep their share.  On top of the roundings above, fp16 weights below
+    2^-21 of the largest are off by up to 2^-32 of it each.  As many requests of the same row as there are
+    multiprocessors, so that a row's tokens are not divided."""
+    T, n = 100000, torch.cuda.get_device_properties(0).multi_processor_count
+    c = Case([T - nodes], nodes, 4, 1, 64, 64, dtype, seed=nodes)
+    c.q[:] = 0
+    c.q[..., 0] = 8.0
+    c.keys[0][:] = 0
+    c.keys[0][7, :, 0] = 17.5 / (8.0 * c.scale)
+    c.values[0].abs_()
+    c.values[0][7] = 0
+    blocks = -(-T // 64)
+    for pool, vals in ((c.k, c.keys[0]), (c.v, c.values[0])):
+        whole = torch.zeros((blocks * 64, 1, 64), dtype=c.dt)
+        whole[:T] = vals
+        pool[c.layer, c.table[c.rows[0], :blocks].long()] = whole.view(blocks, 64, 1, 64).transpose(1, 2)
+    c.q, c.rows, c.masks = c.q.expand(n, -1, -1, -1).contiguous(), c.rows * n, [[(1 << nodes) - 1] * nodes] * n
+    out, lse = c.run()
+    assert c.cache.status() == 0
+    ref, rl, size = D.attention(c.q[0, :1], c.keys[0], c.values[0], torch.ones((1, T), dtype=torch.bool), c.scale)
+    half = D.half_step(c.dt)
+    rel = (64 + 16) * 2.0 ** -24 * 17.5 + 2.0 ** -20
+    small = 2.0 ** -32 * c.values[0].double().sum(0).repeat_interleave(4, 0) if dtype == "fp16" else 0.0
+    assert (ref > 0.001).all()
+    assert ((out.double() - ref).abs() <= half * ref * 1.02 + (half + 2 * rel) * size + small + 1e-7).all()
+    assert ((lse.double() - rl).abs() <= 2 * rel + 1e-6 * rl.abs() + 1e-6).all()

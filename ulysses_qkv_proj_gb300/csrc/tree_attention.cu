@@ -14,9 +14,11 @@
 // memory; boxes of the largest power of two that divides the page, the page numbers fetched a tile ahead); one
 // thread issues S = Q K^T (tcgen05.mma, fp32 S in tensor memory, two buffers), another O += P V (P from tensor
 // memory), so that neither waits behind the other; the softmax warps make one pass over S with a running
-// maximum and sum in base 2.  P is rounded to the inputs' type (relative 2^-8 for bf16, 2^-11 for fp16; its sum
-// is kept of the unrounded values in fp32); O is rescaled only when a row's maximum grows by more than 2^8, so
-// that P stays below 2^8 and O below 2^8 sum|v|.
+// maximum and sum in base 2.  P is rounded to the inputs' type, as the second product's operands have one type (relative
+// 2^-8 for bf16, 2^-11 for fp16; its sum is kept of the unrounded values in fp32); O is rescaled only when a row's maximum
+// grows by more than 2^8.  fp16 has few exponents: P is formed 2^7 times larger there (kLift), so that it stays below
+// 2^15 and is normal down to 2^-21 of the row's maximum; smaller weights are off by at most 2^-32 of the maximum's.
+// Without that the share of 10^5 tokens under one strong score 17.5 nats above them was lost whole.
 //
 // Units of few rows would leave lanes idle: with up to 32 (64) rows they are laid out REP = 4 (2) times, copy
 // c looking at its own 128 / REP tokens of each tile.  P is zero outside that block, so one O accumulator of 128
@@ -82,6 +84,8 @@ constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O 
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 constexpr int kMaxCluster = 4;  // row tiles that share K and V
 constexpr int kUnitCost = 4;  // a unit's start and end, in tiles
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;  // log2 of the factor on P, O and the sum alike; a part's "maximum" is less it
 constexpr float kRescale = 8.f;  // log2 growth of a row's maximum that O is rescaled at
 
 // A unit that spans clusters c0 .. c0 + parts - 1, written by its second one for combine_kernel.
@@ -673,6 +677,7 @@ __device__ void run_softmax(const AttnArgs& a, const Bars& bars, char* smem_base
         pair_sync(warp % 4);
         mx = fmaxf(mx, at[(copy ^ 1) * 128]);
       }
+      mx -= kLift<BF16>;  // m: the row's maximum less the lift, which leaves O / l and m + log2 l as they are
       const bool grow = mx > m + kRescale;
       if (t - s.t0 < (kTwo ? 2 : 1)) {
         m = mx;
