@@ -276,3 +276,27 @@ def test_gradient_replays_from_a_graph():
     run(eager)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+
+
+@pytest.mark.parametrize("S,Hq,dim,style,dtype", [(262144, 64, 128, "rotate_half", "bf16"), (1 << 20, 16, 64, "interleaved", "fp16"),
+                                                  (3000000, 1, 128, "interleaved", "bf16")])
+def test_weight_gradients_of_large_batches(S, Hq, dim, style, dtype):
+    """Millions of equal terms, whose sums' roundings all lie on one side.
+
+    Tolerance: a term's own 16 roundings, and one for each addition it passes: 62 and 64 in its thread's lower levels,
+    one for each 1024 steps (of one or two terms) of the thread, 32 in the block, 42 among the blocks."""
+    qb, dt = _qb(), DT[dtype]
+    proj, qw, kw, gen = _inputs(1, 1, 1, 1, dim, dt, 11)
+    g = torch.randn((1, 1, 2, dim), generator=gen).to(dt)
+    cs, pos = D.angles(8, dim), 5
+    x, kx = (proj[:, :, i:i + 1].cuda().expand(1, S, h, dim).contiguous() for i, h in ((0, Hq), (1, 1)))
+    gq, gk = (g[:, :, i:i + 1].cuda().expand(1, S, h, dim).contiguous() for i, h in ((0, Hq), (1, 1)))
+    dw = [torch.empty(dim, device="cuda") for _ in range(2)]
+    qb.qnre_qk_norm_rope_backward(gq, gk, x, kx, qw.cuda(), kw.cuda(), cs.cuda(),
+                                  torch.full((1, S), pos, dtype=torch.int32, device="cuda"), gq, gk, *dw,
+                                  qb.qk_norm_rope_workspace(x), rope_style=style)
+    for got, i, heads, w in ((dw[0], 0, Hq, qw), (dw[1], 1, 1, kw)):
+        _, one, _, size = D.norm_rope_grad(g[:, :, i:i + 1], proj[:, :, i:i + 1], w, cs, torch.full((1, 1), pos), style)
+        n = S * heads
+        adds = 62 + 64 + n / (304 * 8 * 1024) + 32 + 42
+        _close(got, n * one, n * (2.0 ** -20 * size + adds * 2.0 ** -24 * one.abs()), "dw")
