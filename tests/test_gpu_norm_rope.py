@@ -300,3 +300,42 @@ def test_weight_gradients_of_large_batches(S, Hq, dim, style, dtype):
         n = S * heads
         adds = 62 + 64 + n / (304 * 8 * 1024) + 32 + 42
         _close(got, n * one, n * (2.0 ** -20 * size + adds * 2.0 ** -24 * one.abs()), "dw")
+
+
+@pytest.mark.parametrize("B", [1, 3])
+def test_head_major_bands_in_place(B):
+    """q and k as head bands of one [B, H, S, D] buffer: normalised in place, their gradients in place, and an append."""
+    qb, dt = _qb(), torch.bfloat16
+    S, Hq, Hk, dim = 20, 6, 2, 128
+    proj, qw, kw, gen = _inputs(B, S, Hq, Hk, dim, dt, 12)
+    cs, pos = D.angles(S, dim), torch.arange(S).expand(B, S)
+    w = qw.cuda(), kw.cuda()
+
+    def bands(x):
+        v = x.transpose(1, 2).contiguous().cuda().transpose(1, 2)      # [B, S, H, D] over [B, H, S, D]
+        return v, v[:, :, :Hq], v[:, :, Hq:Hq + Hk], v[:, :, Hq + Hk:]
+
+    _, q, k, v = bands(proj)
+    qb.qnre_qk_norm_rope(q, k, *w, cs.cuda(), None, q, k)
+    for got, x, wt in ((q, proj[:, :, :Hq], qw), (k, proj[:, :, Hq:Hq + Hk], kw)):
+        ref = D.norm_rope(x, wt, cs, pos, "rotate_half")
+        _close(got, ref, _fwd_tol(ref, x, wt, cs, "rotate_half", dt), "in place")
+    assert torch.equal(v.cpu(), proj[:, :, Hq + Hk:])
+
+    g = torch.randn((B, S, Hq + 2 * Hk, dim), generator=gen).to(dt)
+    (_, q, k, _), (_, gq, gk, _) = bands(proj), bands(g)
+    dw = [torch.empty(dim, device="cuda") for _ in range(2)]
+    qb.qnre_qk_norm_rope_backward(gq, gk, q, k, *w, cs.cuda(), None, gq, gk, *dw, qb.qk_norm_rope_workspace(q))
+    for got, i, n, wt in ((gq, 0, Hq, qw), (gk, Hq, Hk, kw)):
+        dx, _, size, _ = D.norm_rope_grad(g[:, :, i:i + n], proj[:, :, i:i + n], wt, cs, pos, "rotate_half")
+        _close(got, dx, D.half_step(dt) * dx.abs() * 1.01 + 2.0 ** -16 * size + 2.0 ** -25, "dx")
+
+    cache = qb.alloc_paged_cache(1, 4 * B, Hk, 8, dim, B, 4)
+    rows, room = torch.arange(B, dtype=torch.int32, device="cuda"), torch.full((B,), S, dtype=torch.int32, device="cuda")
+    qb.qnre_cache_reserve(cache, rows, room)
+    _, q, k, v = bands(proj)
+    qb.qnre_qkv_norm_rope_append(q, k, v, *w, cs.cuda(), None, q, cache, 0, rows)
+    ref = D.norm_rope(proj[:, :, :Hq], qw, cs, pos, "rotate_half")
+    _close(q, ref, _fwd_tol(ref, proj[:, :, :Hq], qw, cs, "rotate_half", dt), "append")
+    page = cache.block_table[:, 2].long()
+    assert torch.equal(cache.v[0, page, :, 1].cpu(), proj[:, 17, Hq + Hk:]) and cache.status() == 0

@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 namespace qnre {
@@ -65,6 +66,50 @@ inline bool rows_vectorisable(const qnre_tensor4_t* t, int esz) {
   for (int i = 0; i < 3; ++i)
     if ((t->stride[i] * esz) % 16 != 0) return false;
   return true;
+}
+
+// Whether two views of one element size share an element.  q and k are often bands of one buffer, token-major or head-major,
+// so their spans meet although no element does.  A common element means that the distance of the bases is a sum of whole
+// steps, of each axis from -(b's extent - 1) to a's (where both step alike, else each its own).  From the longest
+// step down only those counts are tried that the shorter steps can make up for: one or two an axis where strides nest.
+// After kOverlapTries counts (strides that do not nest) the views are taken to meet.
+constexpr int kOverlapTries = 4096;
+
+struct Step {
+  int64_t stride, lo, hi, rest;  // rest: how far the shorter steps reach
+};
+
+inline bool steps_reach(const Step* s, int n, int64_t d, int* tries) {
+  if (n == 0) return d == 0;
+  auto floor_div = [](int64_t a, int64_t b) { return a >= 0 ? a / b : -((-a + b - 1) / b); };
+  const int64_t lo = std::max(s->lo, -floor_div(s->rest - d, s->stride));
+  const int64_t hi = std::min(s->hi, floor_div(s->rest + d, s->stride));
+  for (int64_t i = lo; i <= hi; ++i) {
+    if (--*tries < 0 || steps_reach(s + 1, n - 1, d - i * s->stride, tries)) return true;
+  }
+  return false;
+}
+
+inline bool views_overlap(const qnre_tensor4_t* a, ByteRange ra, const qnre_tensor4_t* b, ByteRange rb) {
+  if (!overlaps(ra, rb)) return false;
+  const int esz = dtype_size(a->dtype);
+  const int64_t bytes = static_cast<const char*>(b->data) - static_cast<const char*>(a->data);
+  if (esz != dtype_size(b->dtype) || bytes % esz != 0) return true;
+  Step s[8];
+  int n = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t na = a->shape[i] - 1, nb = b->shape[i] - 1;
+    if (na > 0 && nb > 0 && a->stride[i] == b->stride[i]) {
+      s[n++] = {a->stride[i], -nb, na, 0};
+    } else {
+      if (na > 0) s[n++] = {a->stride[i], 0, na, 0};
+      if (nb > 0) s[n++] = {b->stride[i], -nb, 0, 0};
+    }
+  }
+  std::sort(s, s + n, [](const Step& x, const Step& y) { return x.stride > y.stride; });
+  for (int i = n - 2; i >= 0; --i) s[i].rest = s[i + 1].rest + std::max(-s[i + 1].lo, s[i + 1].hi) * s[i + 1].stride;
+  int tries = kOverlapTries;
+  return steps_reach(s, n, bytes / esz, &tries);
 }
 
 }  // namespace api

@@ -642,26 +642,6 @@ qnre_status_t check_out(const qnre_tensor4_t* out, const qnre_tensor4_t* like, B
   return QNRE_OK;
 }
 
-// q and k are often head bands of one projection buffer, so their spans meet although no
-// element does.  Where both views step their batch and sequence by the same multiples of one
-// period, they are apart when their head bands are, modulo that period.
-bool views_overlap(const qnre_tensor4_t* a, ByteRange ra, const qnre_tensor4_t* b, ByteRange rb) {
-  if (!overlaps(ra, rb)) return false;
-  int64_t period = 0;
-  for (int i = 0; i < 2; ++i) {
-    if (a->shape[i] <= 1) continue;
-    if (a->stride[i] != b->stride[i]) return true;
-    period = period == 0 ? a->stride[i] : std::min(period, a->stride[i]);
-  }
-  if (period == 0) return true;  // one head band each, and they meet
-  for (int i = 0; i < 2; ++i)
-    if (a->shape[i] > 1 && a->stride[i] % period != 0) return true;
-  auto band = [](const qnre_tensor4_t* t) { return (t->shape[2] - 1) * t->stride[2] + t->shape[3]; };
-  int64_t m = (static_cast<const char*>(b->data) - static_cast<const char*>(a->data)) / 2 % period;
-  if (m < 0) m += period;
-  return m < band(a) || m + band(b) > period;
-}
-
 }  // namespace
 
 extern "C" {
