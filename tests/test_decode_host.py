@@ -497,3 +497,19 @@ def test_tensors_of_another_device_are_refused(lib, monkeypatch, native):
             with pytest.raises(qb.QnreError, match="current CUDA device"):
                 call(args)
         assert len(fake.reached) == 11
+
+
+def test_the_build_goes_on_without_the_native_reads(monkeypatch, tmp_path, capsys):
+    """g++ that fails on torch's headers: printed, no older module left, nothing raised."""
+    pytest.importorskip("torch")
+    import types
+    from ulysses_qkv_proj_gb300 import build
+    old = tmp_path / "_marshal.so"
+    old.write_bytes(b"older")
+    monkeypatch.setattr(build, "MARSHAL_PATH", str(old))
+    monkeypatch.setattr(build.shutil, "which", lambda name: "/usr/bin/" + name)
+    monkeypatch.setattr(build.os.path, "exists", lambda p, real=os.path.exists: p.endswith("Python.h") or real(p))
+    monkeypatch.setattr(build.subprocess, "run",
+                        lambda *a, **k: types.SimpleNamespace(returncode=1, stdout="", stderr="no such header"))
+    assert build.build_marshal() == ""
+    assert not old.exists() and "no such header" in capsys.readouterr().err

@@ -44,7 +44,8 @@ def sources():
 
 def build_marshal() -> str:
     """Compile _marshal.so (csrc/marshal.cpp), the binding's native reads of torch tensors.  Returns its path, or
-    "" where torch's or Python's headers are missing: the binding then reads tensors in Python."""
+    "" where torch's or Python's headers are missing or g++ does not take them: the binding then reads tensors in
+    Python.  A failure is printed, and no older _marshal.so stays behind it."""
     try:
         import torch
         from torch.utils import cpp_extension
@@ -60,7 +61,11 @@ def build_marshal() -> str:
            "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{libs}"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"g++ failed on marshal.cpp:\n{res.stdout}\n{res.stderr}")
+        sys.stderr.write(f"g++ failed on marshal.cpp, the binding will read tensors in Python:\n{res.stdout}\n{res.stderr}\n")
+        for path in (tmp, MARSHAL_PATH):
+            if os.path.exists(path):
+                os.remove(path)
+        return ""
     os.replace(tmp, MARSHAL_PATH)
     return MARSHAL_PATH
 
