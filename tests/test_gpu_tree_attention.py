@@ -427,3 +427,27 @@ def test_many_small_weights_under_a_large_one(nodes, dtype):
     assert (ref > 0.001).all()
     assert ((out.double() - ref).abs() <= half * ref * 1.02 + (half + 2 * rel) * size + small + 1e-7).all()
     assert ((lse.double() - rl).abs() <= 2 * rel + 1e-6 * rl.abs() + 1e-6).all()
+
+
+@pytest.mark.parametrize("nodes,Hq,Hk,dtype", [
+    (13, 16, 2, "bf16"),        # 104 rows a K head: one row tile
+    (20, 16, 2, "fp16"),        # 160: two that share K and V
+    (64, 8, 1, "bf16"),         # 512: four
+    (5, 16, 2, "bf16"),         # 40: rows laid out twice
+])
+def test_trees_of_more_requests_than_the_small_table_holds(nodes, Hq, Hk, dtype):
+    """100 requests at D = 128: the long table of lengths, and with more than 64 rows two V tiles in flight."""
+    rng = random.Random(nodes)
+    c = Case([rng.choice([0, 1, 127, 128, 129, rng.randint(2, 400)]) for _ in range(100)], nodes, Hq, Hk, 128, 16, dtype,
+             seed=nodes)
+    out, lse = c.run()
+    c.check(out, lse)
+    # an infinite value in the context of some requests
+    for i in range(0, 100, 7):
+        if c.lens[i] > 0:
+            _place(c, i, c.lens[i] - 1, 17, float("inf"))
+    out, _ = c.run()
+    for i in range(100):
+        hit = i % 7 == 0 and c.lens[i] > 0
+        assert (out[i, ..., 17] == float("inf")).all() if hit else torch.isfinite(out[i]).all()
+        assert torch.isfinite(out[i][..., :17]).all() and torch.isfinite(out[i][..., 18:]).all()
