@@ -451,3 +451,60 @@ def test_trees_of_more_requests_than_the_small_table_holds(nodes, Hq, Hk, dtype)
         hit = i % 7 == 0 and c.lens[i] > 0
         assert (out[i, ..., 17] == float("inf")).all() if hit else torch.isfinite(out[i]).all()
         assert torch.isfinite(out[i][..., :17]).all() and torch.isfinite(out[i][..., 18:]).all()
+
+
+@pytest.mark.parametrize("layers", [1, 3])
+def test_pools_past_two_to_the_31_elements(layers):
+    """The last pages of pools of 2.3e9 elements: append, compact, copy on write, page copies and attention."""
+    qb = _qb()
+    pages, heads, page, dim, nodes = 70000 // layers, 4, 64, 128, 5
+    gen = torch.Generator().manual_seed(layers)
+    cache = qb.alloc_paged_cache(layers, pages, heads, page, dim, 3, 4)
+    assert cache.k.numel() > 2 ** 31 - 10 ** 6 and layers * pages * heads * page * dim * 2 > 2 ** 32
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    cache.page_refs.fill_(1)
+    cache.page_refs[pages - 8:] = 0         # the free pages are the last ones
+    row, layer, total = i32([1]), layers - 1, 0
+    w = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+    cs = torch.zeros((512, dim), device="cuda")
+    cs[:, :dim // 2] = 1.0                  # no rotation
+    keys, values, q = [], [], None
+    for chunk in (60, 60, 60, nodes):
+        x = torch.randn((1, chunk, 3 * heads, dim), generator=gen).bfloat16().cuda()
+        q = torch.empty((1, chunk, heads, dim), dtype=x.dtype, device="cuda")
+        qb.qnre_cache_reserve(cache, row, i32([chunk]))
+        qb.qnre_qkv_norm_rope_append(x[:, :, :heads], x[:, :, heads:2 * heads], x[:, :, 2 * heads:], w, w, cs, None, q, cache,
+                                     layer, row)
+        kept = list(range(0, chunk, 2)) if chunk != nodes else list(range(nodes))
+        k = D.norm_rope(x[:, :, heads:2 * heads].cpu(), w.cpu(), cs.cpu(), torch.zeros((1, chunk), dtype=torch.int32), "rotate_half")
+        keys.append(k[0, kept])
+        values.append(x[0, kept, 2 * heads:].cpu())
+        if chunk != nodes:
+            qb.qnre_cache_compact(cache, row, i32([kept + [-1] * (chunk - len(kept))]), i32([len(kept)]))
+            total += len(kept)
+    assert cache.status() == 0 and cache.seq_lens.tolist() == [0, total, 0]
+    keys, values = torch.cat(keys), torch.cat(values)
+    half = D.half_step(torch.bfloat16)
+
+    def check(r):
+        at = torch.arange(total + nodes, device="cuda")
+        stored = cache.k[layer, cache.block_table[r][at // page].long(), :, at % page].cpu()
+        assert ((stored.double() - keys).abs() <= half * 1.01 * keys.abs() + 2.0 ** -18 * keys.abs() + 2.0 ** -25).all()
+        out = torch.empty_like(q)
+        qb.qnre_tree_attention(q, cache, layer, i32([r]), None, out, workspace=qb.tree_attention_workspace(q, cache))
+        see = torch.ones((nodes, total + nodes), dtype=torch.bool).tril(total)
+        ref, _, size = D.attention(q[0].cpu(), stored, values, see, dim ** -0.5)
+        # unit norm weights: |q| = |k| = sqrt(dim) up to their rounding
+        rel = (dim + 16) * 2.0 ** -24 * dim ** 0.5 * 1.01 + 2.0 ** -20
+        assert ((out[0].cpu().double() - ref).abs() <= half * ref.abs() * 1.02 + (half + 2 * rel) * size + 1e-7).all()
+        assert cache.status() == 0
+
+    check(1)
+    # a fork and its copy of the open page
+    qb.qnre_cache_fork(cache, row, i32([2]))
+    qb.qnre_cache_reserve(cache, i32([2]), i32([nodes]))
+    a, b = cache.block_table[1, total // page].long(), cache.block_table[2, total // page].long()
+    assert a != b and torch.equal(cache.v[layer, a, :, :total % page], cache.v[layer, b, :, :total % page])
+    check(2)
+    qb.qnre_cache_copy_pages(cache, b[None].int(), i32([0]))
+    assert torch.equal(cache.k[layer, b], cache.k[layer, 0]) and torch.equal(cache.v[layer, b], cache.v[layer, 0])
