@@ -8,9 +8,9 @@
 //
 // Bound: the bookkeeping is launch and load latency.  Release, reserve and compact of a serving step, 64 rows and
 // 8 layers: 18.8 us on the device with a warp a row in the reserve (each round a chain of four loads, done twice) and the
-// lengths in a launch of their own after the moves; 14.2 with the windows as one list, a thread a block, and a
-// cluster a row in the compact.  The page copies of a fork's reserve are HBM bandwidth (64 copies of a 2 MB page: 32.4 us
-// with the fork and the release before it, 235 MB).
+// lengths in a launch of their own after the moves; 14.5 with the windows as one list, a thread a block, and a
+// cluster a row in the compact; 15.0 since the compact looks at the counts of the pages that it writes.  The page copies of a
+// fork's reserve are HBM bandwidth (64 copies of a 2 MB page: 34.2 us with the fork and the release before it, 235 MB).
 #include "../../include/qnre.h"
 #include "cache.cuh"
 #include "ptx.cuh"

@@ -17,7 +17,8 @@
 // blocks 205; streaming stores +2 %).  The gradient (18881 tokens of 70 heads, fp16, 1.02 GB): 282 us
 // with plain loads, 209 with the next heads' loads in flight, 183 packed with all heads of a token in one
 // item, 175 with the loads through a ring in shared memory (two stages of 16 KB a block in flight; three
-// blocks a SM 185, four 246; 16 heads an item 174, 8 205), 164 back to back on warm pages (178 before).
+// blocks a SM 185, four 246; 16 heads an item 174, 8 205), 165 back to back on warm pages (178 before); 167
+// with the weights' sums in three levels.
 #include "../../include/qnre.h"
 #include "cache.cuh"
 

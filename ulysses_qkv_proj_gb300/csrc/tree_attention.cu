@@ -44,7 +44,8 @@
 // 17; multicast, page numbers ahead - / 109 / 48 / 15.3; three tiles of K and of V in flight 237 / 100 / 48 / 15.2;
 // cheaper unit ends, a unit's cost four tiles (2: 102 / 53, 8: 100 / 48 cold) 234 / 91 / 37 / 14.3; eight warps a row in
 // the join of few rows, its parts counted beforehand 234 / 87 / 37 / 13.2; parts of more than 64 rows written eight
-// rows to a line - / 84 / - / -.  Tried and left: Q in tensor memory with P over S (108) or one P buffer (106), the pass
+// rows to a line - / 84 / - / -; the vote on non-finite sums 230 / 84 / 36.8 / 13.0, from 230 / 84 / 36.7 / 12.8 on the same
+// machine.  Tried and left: Q in tensor memory with P over S (108) or one P buffer (106), the pass
 // with a standing maximum 32 columns at a time (101), a CTA pair multiplying as one (98), two row tiles a CTA on the same
 // K and V (117: P lies in S's place, so each tile is product, scores, softmax in a row, 4170 cycles for the two).
 #include "../../include/qnre.h"
