@@ -502,7 +502,7 @@ CACHE_WAIT_TIMEOUT = 0x10
 
 
 class PagedCache:
-    """A paged K/V cache over tensors the caller owns (qnre_cache_t).
+    """A paged K/V cache over tensors the caller owns, all on one device (qnre_cache_t).
 
     k, v         bf16 or fp16 [layers, pages, heads, page_size, head_dim]
     block_table  int32 [rows, max_blocks], -1 where a row holds no page
