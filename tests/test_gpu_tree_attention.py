@@ -508,3 +508,28 @@ def test_pools_past_two_to_the_31_elements(layers):
     check(2)
     qb.qnre_cache_copy_pages(cache, b[None].int(), i32([0]))
     assert torch.equal(cache.k[layer, b], cache.k[layer, 0]) and torch.equal(cache.v[layer, b], cache.v[layer, 0])
+
+
+@pytest.mark.parametrize("L", [200, 40000])
+@pytest.mark.parametrize("nodes,Hq", [(1, 8), (5, 16), (16, 14), (40, 16)])
+def test_infinite_values_whose_weight_is_below_any_float(L, nodes, Hq):
+    """A score 200 nats above all others, at either end of rows that one CTA has or many: infinities far from it count."""
+    for strong in (0, L - 1):
+        c = Case([L], nodes, Hq, 2, 128, 64, "bf16", seed=4)
+        T = L + nodes
+        c.q[:] = 0
+        c.q[..., 0] = 8.0
+        c.keys[0][:] = 0
+        c.keys[0][strong, :, 0] = 200.0 / (8.0 * c.scale)
+        whole = torch.zeros((-(-T // 64) * 64, 2, 128), dtype=c.dt)
+        whole[:T] = c.keys[0]
+        c.k[1, c.table[c.rows[0], :len(whole) // 64].long()] = whole.view(-1, 64, 2, 128).transpose(1, 2)
+        c.masks = [[(1 << 64) - 1 >> 64 - nodes] * nodes]
+        _place(c, 0, L // 2, 5, float("inf"))
+        _place(c, 0, L - 1 - strong, 100, float("-inf"))
+        _place(c, 0, L, 64, float("inf"))           # the root's own draft
+        out, lse = c.run()
+        want = c.values[0][strong].repeat_interleave(Hq // 2, 0).expand(nodes, -1, -1).clone()
+        want[..., 5], want[..., 100], want[..., 64] = float("inf"), float("-inf"), float("inf")
+        assert torch.equal(out[0], want)
+        assert c.cache.status() == 0

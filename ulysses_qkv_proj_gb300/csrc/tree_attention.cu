@@ -1029,6 +1029,9 @@ __global__ void __launch_bounds__(kThreads<D, REP>, 1) attention_kernel(const __
   }
 }
 
+// 2^x for the join of parts, x <= 0: never 0, so that a part with an infinite sum stays one under a far larger maximum.
+__device__ __forceinline__ float part_weight(float x) { return fmaxf(exp2_fast(x), 1.4e-45f); }
+
 // Joins the parts of the units that span CTAs: block x is the unit's second CTA.
 // Up to 64 rows: WARPS warps a row, each with every WARPS-th part, so that a row of many parts (few rows of a long
 // context) costs one round of loads.
@@ -1057,7 +1060,7 @@ __global__ void __launch_bounds__(256) combine_few_kernel(const Desc* desc, cons
   for (int i = sub; i < d.parts; i += WARPS) {
     const long long at = row_of(i);
     const float2 ml = reinterpret_cast<const float2*>(part_ml)[at];
-    const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - M);
+    const float w = ml.x == -INFINITY ? 0.f : part_weight(ml.x - M);
     const float* o = part_o + at * D + lane * kPer;
     l = fmaf(ml.y, w, l);
     if (kPer == 4) {
@@ -1129,14 +1132,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const Desc* desc, const fl
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) mx = fmaxf(mx, ml[k].x);
-    const float f = M == -INFINITY ? 0.f : exp2_fast(M - mx);
+    const float f = M == -INFINITY ? 0.f : part_weight(M - mx);
     M = mx;
     l *= f;
     acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (i0 + k >= d.parts) break;
-      const float w = ml[k].x == -INFINITY ? 0.f : exp2_fast(ml[k].x - M);
+      const float w = ml[k].x == -INFINITY ? 0.f : part_weight(ml[k].x - M);
       l = fmaf(ml[k].y, w, l);
       acc.x = fmaf(v[k].x, w, acc.x);
       acc.y = fmaf(v[k].y, w, acc.y);
