@@ -738,6 +738,79 @@ qnre_status_t qnre_verify_tree(const float* target_probs, int64_t target_stride0
 qnre_status_t qnre_tree_masks(const int32_t* parents, int n, int nodes, uint64_t* masks, int32_t* depths,
                               qnre_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Many answers from one prompt: tables of scaled rotary positions, attention that
+ * reads a prompt's pages once for all rows that share them, sampling from logits.
+ * ------------------------------------------------------------------------ */
+
+#define QNRE_MAX_VOCAB 786432 /* logits of a row that qnre_sample and qnre_filter_probs serve */
+
+/* How qnre_rope_table scales rotary frequencies f_i = theta^(-2 i / rot). */
+typedef enum {
+  QNRE_ROPE_SCALE_NONE = 0,
+  QNRE_ROPE_SCALE_LINEAR = 1,     /* f_i / factor */
+  QNRE_ROPE_SCALE_BASE = 2,       /* theta * factor^(rot / (rot - 2)) in theta's place */
+  QNRE_ROPE_SCALE_YARN = 3,       /* f_i (r / factor + 1 - r); r ramps from 0 to 1 over the pairs i between the ones that
+                                     make `high` and `low` turns over `original` positions (their numbers rounded outward) */
+  QNRE_ROPE_SCALE_WAVELENGTH = 4  /* f_i (s + (1 - s) / factor); s ramps over the turns original f_i / 2 pi themselves, from
+                                     0 at `low` to 1 at `high` */
+} qnre_rope_scale_t;
+
+typedef struct {
+  int32_t kind;      /* qnre_rope_scale_t */
+  double factor;     /* > 0 */
+  double original;   /* positions the model was trained on (YARN, WAVELENGTH) */
+  double low, high;  /* 0 < low < high (YARN, WAVELENGTH) */
+  double magnitude;  /* factor on every cosine and sine */
+} qnre_rope_scaling_t;
+
+/*
+ * qnre_rope_table -- the cos_sin table that the norm, append and projection calls take, for
+ * positions first .. first + n_pos - 1:
+ *
+ *   cos_sin[p - first] = magnitude [cos(p f_0) .. cos(p f_{rot/2-1}) | sin(p f_0) .. sin(p f_{rot/2-1})]
+ *
+ *   cos_sin  device fp32 [n_pos, rot], 16-byte aligned; rot a multiple of 16 up to 128.
+ *   theta    > 1, finite.   first >= 0, first + n_pos <= 2^31.
+ *   scaling  host struct or NULL (unscaled, magnitude 1).
+ * Angles are exact to the 64-bit rounding of their frequency at every position.  n_pos == 0 is an empty call.
+ */
+qnre_status_t qnre_rope_table(float* cos_sin, int64_t n_pos, int rot, int64_t first, double theta,
+                              const qnre_rope_scaling_t* scaling, qnre_stream_t stream);
+
+/*
+ * qnre_sample -- one token for each row of logits, by given random numbers.  With m the row's largest logit
+ * and T its temperature:
+ *
+ *   weight   w_x = exp((l_x - m) / T)
+ *   min_p    leaves tokens with w_x >= min_p; of those
+ *   top_k    leaves the top_k first in order of logit, equal ones by index; of those
+ *   top_p    leaves each one before which (in that order) less than top_p of their weight lies, the first always;
+ *   token    the lowest x whose running sum of the weights left, by index, exceeds u times their sum.
+ *
+ * T <= 0 (or NaN): the lowest x of the largest logit.  Off: top_k <= 0 or >= vocab, top_p >= 1 (or NaN),
+ * min_p <= 0 (or NaN).  A logit of -inf or NaN is never drawn; where there is no other the token is -1.  A logit of +inf
+ * leaves only such ones.  u below 0 (or NaN) counts as 0, from 1 on it draws the last token that is left.
+ *
+ *   logits   device bf16, fp16 or fp32 (dtype), row i at base + i*stride elements, vocab values each.
+ *   temperature, top_p, min_p  device fp32 [n] or NULL (1, off, off);  top_k  device int32 [n] or NULL (off).
+ *   u        device fp32 [n], in [0, 1).      tokens  device int32 [n].
+ * 1 <= vocab <= QNRE_MAX_VOCAB, n <= 2^20.  n == 0 is an empty call.
+ * Weights are formed to 2^-42 and summed as integers, so that tokens agree with a 64-bit evaluation except where a
+ * number lies within about 1e-12 of a border, and do not depend on timing.
+ *
+ * qnre_filter_probs -- the same settings as probabilities: w_x over the sum of the weights left, 0 for the
+ *   rest (one 1 for T <= 0; a row without any token is all 0), as qnre_verify_tree takes them.
+ *   logits   row (i, j) at base + i*stride0 + j*stride1; settings by i.   probs  device fp32 [n, nodes, vocab], contiguous.
+ * nodes <= QNRE_MAX_NODES.
+ */
+qnre_status_t qnre_sample(const void* logits, int64_t stride, int32_t dtype, int n, int64_t vocab, const float* temperature,
+                          const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+                          qnre_stream_t stream);
+qnre_status_t qnre_filter_probs(const void* logits, int64_t stride0, int64_t stride1, int32_t dtype, int n, int nodes,
+                                int64_t vocab, const float* temperature, const int32_t* top_k, const float* top_p,
+                                const float* min_p, float* probs, qnre_stream_t stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

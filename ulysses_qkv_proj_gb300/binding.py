@@ -8,13 +8,16 @@ The names follow the C ABI: `qnre_forward`, `qnre_forward_noalloc`,
 `qnre_plan_create` / `qnre_plan_destroy`, and the speculative-decoding calls
 over a `PagedCache` (`qnre_qk_norm_rope` and its gradient,
 `qnre_qkv_norm_rope_append`, `qnre_cache_*`, `qnre_tree_masks`,
-`qnre_tree_attention`, `qnre_verify_tree`).  Tensors are torch CUDA tensors;
+`qnre_tree_attention`, `qnre_verify_tree`) and the calls for many answers from one
+prompt (`qnre_rope_table`, `qnre_cache_shared_prefix`, `qnre_prefix_attention`,
+`qnre_sample`, `qnre_filter_probs`).  Tensors are torch CUDA tensors;
 torch supplies device memory and the current stream, nothing else.  Every
 failure status raises `QnreError`; a missing library raises at first use.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 import struct
@@ -32,6 +35,7 @@ STATUS_NAMES = {
 }
 LAYOUTS = {"bshd": 0, "fused": 1}
 ROPE_STYLES = {"rotate_half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3, "wavelength": 4}
 FLAG_EPILOGUE_OFF = 0x1
 FLAG_W_MULTICAST = 0x2
 FLAG_ONE_PAIR = 0x4
@@ -70,6 +74,11 @@ class _Cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "block_table", "seq_lens", "page_refs", "status", "scratch")] + \
         [(n, ctypes.c_int32) for n in ("layers", "pages", "heads", "page_size", "head_dim", "rows", "max_blocks",
                                        "dtype")]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32)] + \
+        [(n, ctypes.c_double) for n in ("factor", "original", "low", "high", "magnitude")]
 
 
 _lib = None
@@ -170,9 +179,15 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.qnre_verify_tree.argtypes = [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_int, c_int, c_i64] + [c_vp] * 9
     lib.qnre_tree_masks.restype = c_int
     lib.qnre_tree_masks.argtypes = [c_vp, c_int, c_int, c_vp, c_vp, c_vp]
+    lib.qnre_rope_table.restype = c_int
+    lib.qnre_rope_table.argtypes = [c_vp, c_i64, c_int, c_i64, ctypes.c_double, ctypes.POINTER(_RopeScaling), c_vp]
+    lib.qnre_sample.restype = c_int
+    lib.qnre_sample.argtypes = [c_vp, c_i64, i32, c_int, c_i64] + [c_vp] * 7
+    lib.qnre_filter_probs.restype = c_int
+    lib.qnre_filter_probs.argtypes = [c_vp, c_i64, c_i64, i32, c_int, c_int, c_i64] + [c_vp] * 6
     for name in ("qnre_qk_norm_rope", "qnre_qk_norm_rope_backward", "qnre_qkv_norm_rope_append", "qnre_tree_attention",
                  "qnre_verify_tree", "qnre_cache_truncate", "qnre_cache_fork", "qnre_cache_reserve",
-                 "qnre_cache_compact", "qnre_cache_copy_pages"):
+                 "qnre_cache_compact", "qnre_cache_copy_pages", "qnre_sample", "qnre_filter_probs"):
         _entry[name] = ctypes.cast(getattr(lib, name), c_vp).value
     _lib = lib
     return lib
@@ -876,3 +891,71 @@ def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sampl
             _i32(where, path, n, nodes), _i32(where, counts, n), _i32(where, next_token, n))
     _on_device(where, target_probs, draft_probs, tokens, parents, accept_u, sample_u, path, counts, next_token, node_counts)
     _check(lib.qnre_verify_tree(*args, _stream_ptr(stream)), where)
+
+
+# ---------------------------------------------------------------------------
+# Many answers from one prompt
+# ---------------------------------------------------------------------------
+MAX_VOCAB = 786432
+
+
+def qnre_rope_table(cos_sin, theta: float = 1e4, first: int = 0, scaling: str = "none", factor: float = 1.0,
+                    original: float = 0.0, low: float = 1.0, high: Optional[float] = None,
+                    magnitude: Optional[float] = None, stream=None) -> None:
+    """Fill cos_sin (fp32 [n_pos, rot]) with rows [cos | sin] of positions first.., frequencies scaled as `scaling` says
+    (none, linear, base, yarn, wavelength).  high defaults to 32 turns (yarn) or 4 (wavelength), magnitude to
+    0.1 ln(factor) + 1 for yarn and 1 otherwise."""
+    where = "qnre_rope_table"
+    lib = load_library()
+    kind = ROPE_SCALINGS.get(scaling, -1)
+    shape = _sizes(cos_sin)
+    if len(shape) != 2:
+        raise QnreError(1, f"{where}: cos_sin must be [n_pos, rot]")
+    if high is None:
+        high = 32.0 if kind == 3 else 4.0
+    if magnitude is None:
+        magnitude = 0.1 * math.log(factor) + 1.0 if kind == 3 and factor > 0 else 1.0
+    args = _f32(where, cos_sin), *shape, first, theta, ctypes.byref(_RopeScaling(kind, factor, original, low, high, magnitude))
+    _on_device(where, cos_sin)
+    _check(lib.qnre_rope_table(*args, _stream_ptr(stream)), where)
+
+
+def _settings(where: str, n: int, temperature, top_k, top_p, min_p):
+    return [None if temperature is None else _f32(where, temperature, n), _i32(where, top_k, n),
+            *(None if t is None else _f32(where, t, n) for t in (top_p, min_p))]
+
+
+def qnre_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> None:
+    """Draw tokens (int32 [n]) from logits [n, vocab] (bf16, fp16 or fp32, each row contiguous) by the random numbers u
+    (fp32 [n]); temperature, top_p and min_p are fp32 [n], top_k int32 [n], None where not used."""
+    where, lib = "qnre_sample", load_library()
+    if _native is not None:
+        st = _native.sample(_entry[where], logits, u, tokens, temperature, top_k, top_p, min_p, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise QnreError(1, f"{where}: logits must be [n, vocab], each row contiguous")
+    n, vocab = logits.shape
+    code = _dtype_code(logits)
+    args = (logits.data_ptr(), logits.stride(0), code, n, vocab, *_settings(where, n, temperature, top_k, top_p, min_p),
+            _f32(where, u, n), _i32(where, tokens, n))
+    _on_device(where, logits, u, tokens, temperature, top_k, top_p, min_p)
+    _check(lib.qnre_sample(*args, _stream_ptr(stream)), where)
+
+
+def qnre_filter_probs(logits, probs, temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> None:
+    """Probabilities (fp32 [n, nodes, vocab], as qnre_verify_tree takes them) of logits [n, nodes, vocab] under the settings
+    of qnre_sample, one set a request."""
+    where, lib = "qnre_filter_probs", load_library()
+    if _native is not None:
+        st = _native.filter(_entry[where], logits, probs, temperature, top_k, top_p, min_p, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    if logits.dim() != 3 or (logits.stride(2) != 1 and logits.shape[2] > 1):
+        raise QnreError(1, f"{where}: logits must be [n, nodes, vocab], each row contiguous")
+    n, nodes, vocab = logits.shape
+    code = _dtype_code(logits)
+    args = (logits.data_ptr(), logits.stride(0), logits.stride(1), code, n, nodes, vocab,
+            *_settings(where, n, temperature, top_k, top_p, min_p), _f32(where, probs, n, nodes, vocab))
+    _on_device(where, logits, probs, temperature, top_k, top_p, min_p)
+    _check(lib.qnre_filter_probs(*args, _stream_ptr(stream)), where)

@@ -390,6 +390,78 @@ PyObject* compact(PyObject*, PyObject* const* args, Py_ssize_t argc) {
   });
 }
 
+// Logits with `rank` axes, each row contiguous, and the settings of its requests: five arguments.
+struct Logits {
+  const void* data;
+  int64_t shape[3], stride[3];
+  int dtype;
+  float *temperature = nullptr, *top_p = nullptr, *min_p = nullptr;
+  int32_t* top_k = nullptr;
+};
+
+bool read_logits(PyObject* obj, PyObject* const* settings, int rank, Logits* g) {
+  if (!THPVariable_Check(obj)) return false;
+  const at::Tensor& t = THPVariable_Unpack(obj);
+  g->dtype = code_of(t);
+  if (t.dim() != rank || g->dtype < 0 || g->dtype > QNRE_DTYPE_FP32) return false;
+  for (int i = 0; i < rank; ++i) {
+    g->shape[i] = t.size(i);
+    g->stride[i] = t.stride(i);
+  }
+  if (g->stride[rank - 1] != 1 && g->shape[rank - 1] > 1) return false;
+  g->data = t.data_ptr();
+  const int64_t n = g->shape[0];
+  return n <= INT_MAX && (settings[0] == Py_None || read_pointer(settings[0], QNRE_DTYPE_FP32, {n}, &g->temperature)) &&
+         (settings[1] == Py_None || read_pointer(settings[1], 3, {n}, &g->top_k)) &&
+         (settings[2] == Py_None || read_pointer(settings[2], QNRE_DTYPE_FP32, {n}, &g->top_p)) &&
+         (settings[3] == Py_None || read_pointer(settings[3], QNRE_DTYPE_FP32, {n}, &g->min_p));
+}
+
+// sample(fn, logits, u, tokens, temperature, top_k, top_p, min_p, reader, stream)
+PyObject* sample(PyObject*, PyObject* const* args, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    Logits g;
+    float* u;
+    int32_t* tokens;
+    qnre_stream_t stream;
+    if (argc != 10 || !read_entry(args[0], &fn) || !read_logits(args[1], args + 4, 2, &g) ||
+        !read_pointer(args[2], QNRE_DTYPE_FP32, {g.shape[0]}, &u) || !read_pointer(args[3], 3, {g.shape[0]}, &tokens) ||
+        !on_device({args[1], args[2], args[3], args[4], args[5], args[6], args[7]}))
+      Py_RETURN_NONE;
+    if (!read_stream(args[8], args[9], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_sample)>(fn)(g.data, g.stride[0], g.dtype, static_cast<int>(g.shape[0]), g.shape[1],
+                                                      g.temperature, g.top_k, g.top_p, g.min_p, u, tokens, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// filter(fn, logits, probs, temperature, top_k, top_p, min_p, reader, stream)
+PyObject* filter(PyObject*, PyObject* const* args, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    Logits g;
+    float* probs;
+    qnre_stream_t stream;
+    if (argc != 9 || !read_entry(args[0], &fn) || !read_logits(args[1], args + 3, 3, &g) || g.shape[1] > INT_MAX ||
+        !read_pointer(args[2], QNRE_DTYPE_FP32, {g.shape[0], g.shape[1], g.shape[2]}, &probs) ||
+        !on_device({args[1], args[2], args[3], args[4], args[5], args[6]}))
+      Py_RETURN_NONE;
+    if (!read_stream(args[7], args[8], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_filter_probs)>(fn)(g.data, g.stride[0], g.stride[1], g.dtype,
+                                                            static_cast<int>(g.shape[0]), static_cast<int>(g.shape[1]),
+                                                            g.shape[2], g.temperature, g.top_k, g.top_p, g.min_p, probs,
+                                                            stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
 template <typename F>
 PyCFunction fast(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -404,6 +476,8 @@ PyMethodDef methods[] = {{"view4", view4, METH_O, nullptr},
                          {"verify", fast(verify), METH_FASTCALL, nullptr},
                          {"cache_rows", fast(cache_rows), METH_FASTCALL, nullptr},
                          {"compact", fast(compact), METH_FASTCALL, nullptr},
+                         {"sample", fast(sample), METH_FASTCALL, nullptr},
+                         {"filter", fast(filter), METH_FASTCALL, nullptr},
                          {"sizes", sizes, METH_O, nullptr},
                          {"type_code", type_code, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
