@@ -779,6 +779,43 @@ qnre_status_t qnre_rope_table(float* cos_sin, int64_t n_pos, int rot, int64_t fi
                               const qnre_rope_scaling_t* scaling, qnre_stream_t stream);
 
 /*
+ * qnre_cache_shared_prefix -- for each group of the call's rows the tokens that all of them hold in the same
+ * pages: shared[g] is a multiple of page_size, the most for which every row of the group has that many tokens and
+ * the same pages under them (0 for a group of fewer than two rows, or with a row outside the cache).
+ *
+ *   rows     device int32 [n].
+ *   groups   device int32 [n_groups + 1], ascending in [0, n]: group g is rows[groups[g]] .. rows[groups[g+1] - 1].
+ *   shared   device int32 [n_groups].
+ * n_groups <= QNRE_MAX_CALL_ROWS; n_groups == 0 is an empty call.
+ *
+ * qnre_prefix_attention -- qnre_tree_attention in which the rows of a group read their common tokens once for all of them,
+ * and whose scores may be capped and biased by distance:
+ *
+ *   s(t, x) = scale q[i, t, h] . k_x;  softcap > 0: s <- softcap tanh(s / softcap)
+ *   slopes:  s <- s + slopes[h] (pos(x) - pos(t)), pos of a cached token its number, of node j seq_lens + depths[i][j]
+ *
+ *   q, rows, mask, counts, scale, out, lse  as for qnre_tree_attention.
+ *   groups, n_groups, shared  as qnre_cache_shared_prefix takes and gives them, for these rows and the tables as they are
+ *            (a smaller multiple of page_size serves, too; what exceeds a member's tokens is cut off); n_groups == 0 and
+ *            NULL: no row shares.  Rows of the call outside every group are served alone.
+ *   depths   device int32 [n, nodes] or NULL (node j at depth j); read only with slopes.
+ *   softcap  >= 0, finite; 0: none.      slopes  device fp32 [Hq] or NULL.
+ *   workspace  qnre_prefix_attention_workspace_bytes (n_groups: 0 or any other), 16-byte aligned, contents undefined before
+ *            and after; calls that may overlap (on different streams) need one each.
+ * Limits, errors and the care for masked and non-finite values are those of qnre_tree_attention; n nodes Hq <= 2^31-1.
+ * The groups' rows come in any order of the cache's rows, and a row may stand in the call more than once.
+ */
+qnre_status_t qnre_cache_shared_prefix(const qnre_cache_t* cache, const int32_t* rows, int n, const int32_t* groups,
+                                       int n_groups, int32_t* shared, qnre_stream_t stream);
+qnre_status_t qnre_prefix_attention_workspace_bytes(int n, int nodes, int q_heads, int kv_heads, int head_dim, int n_groups,
+                                                    uint64_t* bytes);
+qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t* cache, int layer, const int32_t* rows,
+                                    const int32_t* groups, int n_groups, const int32_t* shared, const uint64_t* mask,
+                                    const int32_t* depths, const int32_t* counts, float scale, float softcap,
+                                    const float* slopes, void* out, float* lse, void* workspace, uint64_t workspace_bytes,
+                                    qnre_stream_t stream);
+
+/*
  * qnre_sample -- one token for each row of logits, by given random numbers.  With m the row's largest logit
  * and T its temperature:
  *

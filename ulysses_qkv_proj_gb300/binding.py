@@ -181,13 +181,21 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.qnre_tree_masks.argtypes = [c_vp, c_int, c_int, c_vp, c_vp, c_vp]
     lib.qnre_rope_table.restype = c_int
     lib.qnre_rope_table.argtypes = [c_vp, c_i64, c_int, c_i64, ctypes.c_double, ctypes.POINTER(_RopeScaling), c_vp]
+    lib.qnre_cache_shared_prefix.restype = c_int
+    lib.qnre_cache_shared_prefix.argtypes = [cache, c_vp, c_int, c_vp, c_int, c_vp, c_vp]
+    lib.qnre_prefix_attention_workspace_bytes.restype = c_int
+    lib.qnre_prefix_attention_workspace_bytes.argtypes = [c_int] * 6 + [ctypes.POINTER(ctypes.c_uint64)]
+    lib.qnre_prefix_attention.restype = c_int
+    lib.qnre_prefix_attention.argtypes = [t4, cache, c_int, c_vp, c_vp, c_int, c_vp, c_vp, c_vp, c_vp, ctypes.c_float,
+                                          ctypes.c_float, c_vp, c_vp, c_vp, c_vp, ctypes.c_uint64, c_vp]
     lib.qnre_sample.restype = c_int
     lib.qnre_sample.argtypes = [c_vp, c_i64, i32, c_int, c_i64] + [c_vp] * 7
     lib.qnre_filter_probs.restype = c_int
     lib.qnre_filter_probs.argtypes = [c_vp, c_i64, c_i64, i32, c_int, c_int, c_i64] + [c_vp] * 6
     for name in ("qnre_qk_norm_rope", "qnre_qk_norm_rope_backward", "qnre_qkv_norm_rope_append", "qnre_tree_attention",
                  "qnre_verify_tree", "qnre_cache_truncate", "qnre_cache_fork", "qnre_cache_reserve",
-                 "qnre_cache_compact", "qnre_cache_copy_pages", "qnre_sample", "qnre_filter_probs"):
+                 "qnre_cache_compact", "qnre_cache_copy_pages", "qnre_sample", "qnre_filter_probs",
+                 "qnre_cache_shared_prefix", "qnre_prefix_attention"):
         _entry[name] = ctypes.cast(getattr(lib, name), c_vp).value
     _lib = lib
     return lib
@@ -918,6 +926,58 @@ def qnre_rope_table(cos_sin, theta: float = 1e4, first: int = 0, scaling: str = 
     args = _f32(where, cos_sin), *shape, first, theta, ctypes.byref(_RopeScaling(kind, factor, original, low, high, magnitude))
     _on_device(where, cos_sin)
     _check(lib.qnre_rope_table(*args, _stream_ptr(stream)), where)
+
+
+def qnre_cache_shared_prefix(cache: PagedCache, rows, groups, shared, stream=None) -> None:
+    """shared[g] = tokens that rows[groups[g]:groups[g + 1]] all hold in the same pages (whole pages; int32 lists)."""
+    where, lib = "qnre_cache_shared_prefix", load_library()
+    if _native is not None:
+        st = _native.shared_prefix(_entry[where], cache.address, cache.k, rows, groups, shared, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    n, n_groups = rows.numel(), shared.numel()
+    args = _i32(where, rows, n), n, _i32(where, groups, n_groups + 1), n_groups, _i32(where, shared, n_groups)
+    _on_device(where, cache.k, rows, groups, shared)
+    _check(lib.qnre_cache_shared_prefix(cache.handle, *args, _stream_ptr(stream)), where)
+
+
+def prefix_attention_workspace(q, cache: PagedCache, groups: bool = True):
+    """The scratch tensor qnre_prefix_attention needs for queries like q on this cache (without groups less)."""
+    import torch
+    n = ctypes.c_uint64()
+    _check(load_library().qnre_prefix_attention_workspace_bytes(q.shape[0], q.shape[1], q.shape[2], cache.k.shape[2],
+                                                                q.shape[3], 1 if groups else 0, ctypes.byref(n)),
+           "qnre_prefix_attention_workspace_bytes")
+    return torch.empty(n.value, dtype=torch.uint8, device=q.device)
+
+
+def qnre_prefix_attention(q, cache: PagedCache, layer: int, rows, groups, shared, mask, out, lse=None, counts=None,
+                          depths=None, scale=None, softcap=0.0, slopes=None, workspace=None, stream=None) -> None:
+    """qnre_tree_attention whose groups of rows (groups and shared as qnre_cache_shared_prefix takes and gives them, or None)
+    read their common tokens once; scores capped by softcap tanh(s / softcap) where softcap > 0, and biased by
+    slopes[h] (pos_key - pos_query) where slopes (fp32 [Hq]) are given (depths: int32 [n, nodes], None for a chain)."""
+    where, lib = "qnre_prefix_attention", load_library()
+    if _native is not None:
+        st = _native.prefix_attention(_entry[where], q, cache.address, cache.k, layer, rows, groups, shared, mask, out, lse,
+                                      counts, depths, scale, softcap, slopes, workspace, _stream_ptr, stream)
+        if st is not None:
+            return _check(st, where)
+    tq = _view4(q)
+    n, nodes, heads, dim = _sizes(q)
+    to = _same(where, out, q)
+    tm = _i64(where, mask, n, nodes)
+    if workspace is None:
+        raise QnreError(1, f"{where}: workspace is missing (prefix_attention_workspace)")
+    if (groups is None) != (shared is None):
+        raise QnreError(1, f"{where}: groups and shared go together")
+    n_groups = 0 if shared is None else shared.numel()
+    args = (tq, cache.handle, layer, _i32(where, rows, n), _i32(where, groups, n_groups + 1), n_groups,
+            _i32(where, shared, n_groups), tm, _i32(where, depths, n, nodes), _i32(where, counts, n),
+            dim ** -0.5 if scale is None else scale, softcap, None if slopes is None else _f32(where, slopes, heads), to,
+            None if lse is None else _f32(where, lse, n, nodes, heads), _contig(workspace, where),
+            workspace.numel() * workspace.element_size())
+    _on_device(where, q, cache.k, rows, groups, shared, mask, out, lse, counts, depths, slopes, workspace)
+    _check(lib.qnre_prefix_attention(*args, _stream_ptr(stream)), where)
 
 
 def _settings(where: str, n: int, temperature, top_k, top_p, min_p):

@@ -390,6 +390,86 @@ PyObject* compact(PyObject*, PyObject* const* args, Py_ssize_t argc) {
   });
 }
 
+// A list of group starts and one entry a group, or None for both.
+bool read_groups(PyObject* starts, PyObject* entries, int32_t** groups, int* n_groups, int32_t** shared) {
+  *groups = *shared = nullptr;
+  *n_groups = 0;
+  if (starts == Py_None && entries == Py_None) return true;
+  if (!THPVariable_Check(entries)) return false;
+  const int64_t count = THPVariable_Unpack(entries).numel();
+  if (count >= INT_MAX || !read_pointer(starts, 3, {count + 1}, groups) || !read_pointer(entries, 3, {count}, shared))
+    return false;
+  *n_groups = static_cast<int>(count);
+  return true;
+}
+
+// shared_prefix(fn, cache address, its k, rows, groups, shared, reader, stream)
+PyObject* shared_prefix(PyObject*, PyObject* const* args, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    void *fn, *cache;
+    int32_t *rows, *groups, *shared;
+    int n_groups;
+    qnre_stream_t stream;
+    if (argc != 8 || !read_entry(args[0], &fn) || !read_entry(args[1], &cache) || !THPVariable_Check(args[3]))
+      Py_RETURN_NONE;
+    const int64_t n = THPVariable_Unpack(args[3]).numel();
+    if (n > INT_MAX || !read_pointer(args[3], 3, {n}, &rows) || args[4] == Py_None ||
+        !read_groups(args[4], args[5], &groups, &n_groups, &shared) || !on_device({args[2], args[3], args[4], args[5]}))
+      Py_RETURN_NONE;
+    if (!read_stream(args[6], args[7], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_cache_shared_prefix)>(fn)(static_cast<const qnre_cache_t*>(cache), rows,
+                                                                   static_cast<int>(n), groups, n_groups, shared, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// prefix_attention(fn, q, cache address, its k, layer, rows, groups, shared, mask, out, lse, counts, depths, scale, softcap,
+// slopes, workspace, reader, stream)
+PyObject* prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    void *fn, *cache, *out;
+    qnre_tensor4_t q;
+    int layer, n_groups;
+    int32_t *rows, *groups, *shared, *counts = nullptr, *depths = nullptr;
+    uint64_t* mask = nullptr;
+    float *lse = nullptr, *slopes = nullptr;
+    qnre_stream_t stream;
+    if (argc != 19 || !read_entry(args[0], &fn) || !read_view4(args[1], &q) || !read_entry(args[2], &cache) ||
+        !read_int(args[4], &layer) || !read_pointer(args[5], 3, {q.shape[0]}, &rows) ||
+        !read_groups(args[6], args[7], &groups, &n_groups, &shared) ||
+        (args[8] != Py_None && !read_pointer(args[8], 4, {q.shape[0], q.shape[1]}, &mask)) ||
+        !read_pointer(args[9], q.dtype, {q.shape[0], q.shape[1], q.shape[2], q.shape[3]}, &out) ||
+        (args[10] != Py_None &&
+         !read_pointer(args[10], QNRE_DTYPE_FP32, {q.shape[0], q.shape[1], q.shape[2]}, &lse)) ||
+        (args[11] != Py_None && !read_pointer(args[11], 3, {q.shape[0]}, &counts)) ||
+        (args[12] != Py_None && !read_pointer(args[12], 3, {q.shape[0], q.shape[1]}, &depths)) ||
+        (args[13] != Py_None && !PyFloat_Check(args[13])) || !PyFloat_Check(args[14]) ||
+        (args[15] != Py_None && !read_pointer(args[15], QNRE_DTYPE_FP32, {q.shape[2]}, &slopes)) ||
+        !THPVariable_Check(args[16]) ||
+        !on_device({args[1], args[3], args[5], args[6], args[7], args[8], args[9], args[10], args[11], args[12], args[15],
+                    args[16]}))
+      Py_RETURN_NONE;
+    const double scale =
+        args[13] == Py_None ? std::pow(static_cast<double>(q.shape[3]), -0.5) : PyFloat_AS_DOUBLE(args[13]);
+    const at::Tensor& ws = THPVariable_Unpack(args[16]);
+    if (!ws.is_contiguous()) Py_RETURN_NONE;
+    void* ws_data = ws.data_ptr();
+    const uint64_t ws_bytes = ws.nbytes();
+    const float softcap = static_cast<float>(PyFloat_AS_DOUBLE(args[14]));
+    if (!read_stream(args[17], args[18], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_prefix_attention)>(fn)(
+        &q, static_cast<const qnre_cache_t*>(cache), layer, rows, groups, n_groups, shared, mask, depths, counts,
+        static_cast<float>(scale), softcap, slopes, out, lse, ws_data, ws_bytes, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
 // Logits with `rank` axes, each row contiguous, and the settings of its requests: five arguments.
 struct Logits {
   const void* data;
@@ -476,6 +556,8 @@ PyMethodDef methods[] = {{"view4", view4, METH_O, nullptr},
                          {"verify", fast(verify), METH_FASTCALL, nullptr},
                          {"cache_rows", fast(cache_rows), METH_FASTCALL, nullptr},
                          {"compact", fast(compact), METH_FASTCALL, nullptr},
+                         {"shared_prefix", fast(shared_prefix), METH_FASTCALL, nullptr},
+                         {"prefix_attention", fast(prefix_attention), METH_FASTCALL, nullptr},
                          {"sample", fast(sample), METH_FASTCALL, nullptr},
                          {"filter", fast(filter), METH_FASTCALL, nullptr},
                          {"sizes", sizes, METH_O, nullptr},
