@@ -5,15 +5,23 @@
 //   o = sum_x p_x v_x,  p = softmax(cap tanh(scale q.k_x / cap) + slope (pos_x - pos_q)) over the tokens a node sees
 //
 // A softmax over two sets of tokens is the join of two softmaxes, so each row has two parts: its group's common tokens,
-// where all members' nodes and query heads of a K head are rows of one matrix product (128 to a unit, several units
-// to a cluster that fetches K and V for all of them by multicast), and its own tokens behind them.  Both are cut into units and
-// tiles as in tree_attention.cu and dealt out in equal runs; whole clusters take one kind or the other, in the
-// proportion of their tiles, so that both kinds run side by side in one launch.  A second kernel joins a row's parts: the
-// group's, in the order of its tiles, then its own.  Everything is found from lengths in device memory by each CTA itself
-// (the number of common tokens too), so a captured call follows them, and the order of sums depends on them alone.
+// where all members' nodes and query heads of a K head are rows of one matrix product, and its own tokens behind them.
+// Units are 128 rows of (request, node, query head of a K head).  A unit of common tokens sees every tile; as many of them as a
+// cluster has CTAs fetch K and V for one another by multicast, what is left over of a group goes to single CTAs.  A unit
+// of own tokens holds the same rows of up to 128 requests (16 of one node with 8 heads) and runs through the requests' tiles
+// one request after another: a tile's P is zero for the others' rows, so they share the unit's start and end, which cost as much
+// as three tiles, and the softmax of one request's tile runs beside the next one's, as their rows lie with
+// different warps.  Clusters and single CTAs take equal runs of tiles in proportion to the work, side by side in one
+// launch.  A second kernel joins a row's parts: the group's in the order of its tiles, then its own.  Everything is found from
+// lengths in device memory by each CTA itself (the number of common tokens too), so a captured call follows them, and the
+// order of sums depends on them alone.
 //
 // In a CTA the roles are those of tree_attention.cu: two TMA warps, two threads that issue the products, eight softmax
-// warps of which two threads share a row of 128.  Few rows leave lanes idle, which costs nothing where HBM is the limit.
+// warps of which two threads share a row of 128.
+//
+// Values that a row must not see: as in tree_attention.cu scores are replaced before use and V behind a row's tokens is zeroed.  A
+// non-finite V of one request's own tokens would meet the zeros of the others' P, and 0 inf is NaN.  So a row whose own part is
+// not finite is marked, and the join computes that part again by itself, token by token (own_part): slow, and only there.
 #include "../../include/qnre.h"
 #include "attention_tile.cuh"
 #include "cache.cuh"
@@ -41,32 +49,35 @@ constexpr int kMaxCtas = 152;  // one a SM
 constexpr int kTmemS = 0, kTmemO = 256, kTmemP = 384;  // columns: S 2 x 128, O D, P 2 x 64
 constexpr int kMaxCluster = 4;
 constexpr int kUnitCost = 4;  // a unit's start and end, in tiles
-constexpr int kSmall = 64;    // requests whose table is short enough for a third V tile at D = 128
-constexpr int kSmallLen = 1 << 24;
+constexpr int kSmallRequests = 128, kSmallGroups = 31, kSmallBlocks = 32;  // (see Smem)
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Where a unit's results are: `parts` runs of it from CTA `cta` on; 0: one piece, in the rows' own places; -1: in the output.
+// Where a unit's results are: `parts` runs of it from CTA `cta` on, `step` apart; 0: one piece, in the rows' own places.
 struct Desc {
-  int cta, parts;
+  int cta, step, parts;
 };
 
 struct PrefixArgs {
-  CUtensorMap tk, tv, tq_group, tq_row;
+  CUtensorMap tk, tv, tq;
   CacheView c;
   const int32_t *rows, *groups, *shared, *counts, *depths;
   const uint64_t* mask;
   const float* slopes;
   char* out;
   float* lse;
-  int* first_of;      // [n]: the first request of the group whose common tokens a request reads, or -1
-  Desc* row_units;    // [n][Hk][row_tiles]
-  Desc* group_units;  // [n][Hk][row_tiles], by the first request of the unit
-  float2* part_ml;    // [2 kMaxCtas 128 + rows of both kinds]: maximum (base 2), sum
+  int2* requests;     // [n]: the first request of the group whose common tokens a request reads, or -1; how many
+  Desc* row_units;    // [n][Hk][row_tiles], by the first request of the unit
+  Desc* group_units;  // the same
+  float4* part_ml;    // [2 kMaxCtas 128 + rows of both kinds]: maximum (base 2), sum, marks of either half of the columns
   float4* part_o;     // the same rows of D, laid out by piece_of
   long long own_rows, group_rows;  // where the rows' own places begin, for each kind
-  float scale_log2, cap_in, cap_log2;  // capped: 2 log2(e) scale / cap, cap log2(e)
+  float scale_log2, cap_in, cap_log2;  // capped: scale / cap, cap log2(e)
+  float cap_near, cap_poly[4];         // the nearer polynomial of run_softmax in powers of q.k, and up to where it serves
+  const char* q;
+  long long q_stride[3];  // bytes
   int layer, n, n_groups, nodes, Hq, Hk, G, box, cl;
-  int unit_nodes, unit_members, row_tiles;  // nodes and members of a unit; tiles of one request's nodes
+  int unit_nodes, unit_members, row_tiles;  // nodes and requests of a unit; units that one request's nodes take
+  int warp_members;                         // requests whose rows one warp has
 };
 
 // Eight rows' pieces of 16 bytes lie side by side, so that the threads that write, a row each, fill whole lines.
@@ -75,29 +86,36 @@ __device__ __forceinline__ long long piece_of(long long row, int i) {
   return ((row >> 3) * (D / 4) + i) * 8 + (row & 7);
 }
 
-// Shared memory: as many tiles of K and V in flight as fit.
+// Shared memory.  Three tiles of K and of V in flight feed the products (two of V: 2200 cycles a shared tile instead of
+// 1840); at D = 128 they leave 3 KB, which tables of up to 128 requests and 31 groups fit into (SMALL).
 template <int D, bool SMALL>
 struct Smem {
-  static constexpr int kRequests = SMALL ? kSmall : QNRE_MAX_CALL_ROWS;
+  static constexpr int kRequests = SMALL ? kSmallRequests : QNRE_MAX_CALL_ROWS;
+  static constexpr int kGroups = SMALL ? kSmallGroups : QNRE_MAX_CALL_ROWS;
+  static constexpr int kBlocks = SMALL ? kSmallBlocks : QNRE_MAX_CALL_ROWS;
+  static constexpr int kMlBuffers = SMALL ? 1 : 2;
   static constexpr int kKStages = D == 128 ? 3 : 5;
   static constexpr int kVStages = D == 128 ? (SMALL ? 3 : 2) : 5;
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kQ = 0;
   static constexpr int kK = kTileBytes;
   static constexpr int kV = kK + kKStages * kTileBytes;
-  static constexpr int kMl = kV + kVStages * kTileBytes;   // float [2][2][128]
-  static constexpr int kItems = kMl + 2048;                // int2 [kRequests]
-  static constexpr int kExtra = kItems + kRequests * 8;    // int [kRequests] (SMALL: in the items)
-  static constexpr int kPre = kExtra + (SMALL ? 0 : kRequests * 4);  // int [kRequests + 1]
-  static constexpr int kBars = (kPre + (kRequests + 1) * 4 + 7) / 8 * 8;
+  static constexpr int kBars = kV + kVStages * kTileBytes;
   static constexpr int kWords = kBars + 8 * (2 * kKStages + 2 * kVStages + 13);
-  static constexpr int kBytes = kWords + 32;
+  static constexpr int kMl = kWords + 32;                           // float [kMlBuffers][2][128]
+  static constexpr int kBase = kMl + kMlBuffers * 1024;             // int [kRequests]
+  static constexpr int kLen = kBase + kRequests * 4;
+  static constexpr int kCommon = kLen + kRequests * 4;              // int [kGroups]
+  static constexpr int kStarts = kCommon + kGroups * 4;             // int [kGroups + 1]
+  static constexpr int kSingle = kStarts + kGroups * 4 + 4;         // int [kBlocks + kGroups + 1]
+  static constexpr int kWide = kSingle + (kBlocks + kGroups) * 4 + 4;  // int [kGroups + 1]
+  static constexpr int kDrafts = kWide + kGroups * 4 + 4;           // uint8 [kRequests]
+  static constexpr int kBytes = kDrafts + kRequests;
   static_assert(kBytes <= 232448, "one CTA's shared memory");
-  static_assert(6 * (QNRE_MAX_CALL_ROWS + 1) * 4 <= kKStages * kTileBytes, "the first tables lie where K will");
 };
 
 struct Words {
-  unsigned long long bad_nodes[3];  // drafts with non-finite V elements, segments in turn
+  unsigned long long marked[3];  // requests of a unit (pairs of them, above 64) with non-finite drafts, segments in turn
   uint32_t tmem, abort;
 };
 
@@ -105,60 +123,70 @@ struct Bars {
   uint32_t kfull, kempty, vfull, vempty, qfull, qempty, sfull, sfree, pready, pvdone, ofree, drain, drain2;
 };
 
+// The tables that every CTA makes for itself.
+struct Tables {
+  int *base, *len;           // requests: tokens of their own from base on, context up to len
+  uint8_t* drafts;           // behind it
+  int *starts, *common;      // groups: first requests, common tokens
+  int *single, *wide;        // where the items begin in the run of the single CTAs and of the clusters
+  int blocks, n_groups;      // single items: blocks of requests, then what the clusters leave of each group
+};
+
 // One unit's part of a CTA's run.
 struct Seg {
-  int item, kvh, rt, t0, t1;
-  int base, len, total;  // its tokens: context [base, len), drafts up to total
-  int start, members;    // of a group
-  int begin;             // the run's place of its first tile
-  bool whole;
+  bool group, whole;
+  int kvh, rt, t0, t1;
+  int start, members;  // requests
+  int tokens;          // of a group
+  int begin, tiles;    // the run's place of its first tile
   int slot;
 };
 
-// A CTA's run over the units of its kind.
-template <bool SMALL>
-struct Cursor {
-  const int* pre;
-  const int2* items;
-  const int* extra;
-  int cur, end, item, cl, rank, row_tiles, unit_members, index, count, quot, rem;  // run `index` of `count`
-  bool group;
+__device__ __forceinline__ int tiles_of(int tokens) { return tokens > 0 ? (tokens + kTile - 1) / kTile : 1; }
 
-  __device__ __forceinline__ static int tiles_of(int tokens) { return tokens > 0 ? (tokens + kTile - 1) / kTile : 1; }
-  __device__ __forceinline__ static int clusters_of(int members, int unit_members, int row_tiles, int cl) {
-    return ((members + unit_members - 1) / unit_members * row_tiles + cl - 1) / cl;
-  }
+// A CTA's run over the units of its kind.
+struct Cursor {
+  Tables t;
+  const int* pre;
+  int cur, end, item, index, count, quot, rem;  // run `index` of `count`
+  int n, Hk, cl, rank, row_tiles, unit_members;
+  bool wide;
+
+  // Units of a group for one K head, and those of them that clusters take.
+  __device__ __forceinline__ int units_of(int members) const { return (members + unit_members - 1) / unit_members * row_tiles; }
+  __device__ __forceinline__ int shared_units(int units) const { return cl > 1 ? units / cl * cl : 0; }
   __device__ __forceinline__ int start_of(int c) const { return c * quot + c * rem / count; }
   __device__ __forceinline__ bool next(Seg& s) {
     while (cur < end) {
       while (cur >= pre[item + 1]) ++item;
-      const int2 it = items[item];
-      s.item = item;
-      if (group) {
-        s.base = 0;
-        s.start = it.x >> 16;
-        s.members = it.x & 0xFFFF;
-        s.len = s.total = it.y;
+      s.group = wide || item >= t.blocks;
+      int per_head = row_tiles, first = 0;
+      if (s.group) {
+        const int g = wide ? item : item - t.blocks;
+        s.start = t.starts[g];
+        s.members = t.starts[g + 1] - s.start;
+        s.tokens = t.common[g];
+        const int units = units_of(s.members), full = shared_units(units);
+        per_head = wide ? full / cl : units - full;
+        first = wide ? 0 : full;
       } else {
-        s.base = it.x;
-        s.len = SMALL ? it.y >> 7 : it.y;
-        s.total = s.len + (SMALL ? it.y & 127 : extra[item]);
-        s.start = item;
-        s.members = 1;
+        s.start = item * unit_members;
+        s.members = min(unit_members, n - s.start);
+        s.tokens = 0;
       }
-      const int tiles = tiles_of(s.total - s.base), per = tiles + kUnitCost;
+      const int per = (pre[item + 1] - pre[item]) / (per_head * Hk);
       const int off = cur - pre[item];
       const int unit = off / per, o = off - unit * per;
       const int take = min(per - o, end - cur);
+      s.tiles = per - kUnitCost;
       s.begin = cur - o + kUnitCost;
       cur += take;
       s.t0 = max(0, o - kUnitCost);
       s.t1 = max(0, o + take - kUnitCost);
       if (s.t0 == s.t1) continue;  // the unit's cost falls to this CTA, its tiles to the next
-      const int per_head = group ? clusters_of(s.members, unit_members, row_tiles, cl) : row_tiles;
       s.kvh = unit / per_head;
-      s.rt = (unit - s.kvh * per_head) * cl + rank;
-      s.whole = s.t0 == 0 && s.t1 == tiles;
+      s.rt = first + (unit - s.kvh * per_head) * (wide ? cl : 1) + rank;
+      s.whole = s.t0 == 0 && s.t1 == s.tiles;
       // a CTA goes on with one unit at most, and leaves one unfinished at most
       s.slot = 2 * static_cast<int>(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
       return true;
@@ -167,26 +195,57 @@ struct Cursor {
   }
 };
 
+// The way through the requests' tiles of a unit of own tokens: one request after another, in steps of the requests whose rows
+// one warp has, so that neighbours lie with different warps.  (Turns of a tile each, over four requests in different
+// quarters, cost more in bookkeeping than they overlap: 128 rows in 6 groups 127 us against 121.)
+struct Walk {
+  int mi, column, tile, tiles, step, members;
+  int base, len, total;  // of the request
+  const int *bases, *lens;
+  const uint8_t* drafts;  // from the unit's first request on
+
+  __device__ __forceinline__ void enter() {
+    base = bases[mi];
+    len = lens[mi];
+    total = len + drafts[mi];
+    tiles = tiles_of(total - base);
+  }
+  __device__ __forceinline__ void next_request() {
+    mi += step;
+    if (mi >= members) mi = ++column;
+    enter();
+  }
+  __device__ __forceinline__ void begin(const Tables& t, const Seg& s, int requests_a_warp) {
+    if (s.group) return;
+    step = requests_a_warp;
+    members = s.members;
+    bases = t.base + s.start;
+    lens = t.len + s.start;
+    drafts = t.drafts + s.start;
+    mi = column = 0;
+    tile = s.t0;
+    for (enter(); tile >= tiles; next_request()) tile -= tiles;
+  }
+  __device__ __forceinline__ void next() {  // (not behind the unit's last tile)
+    if (++tile < tiles) return;
+    tile = 0;
+    next_request();
+  }
+};
+
 // What row `ur` of a unit stands for.
 struct UnitRow {
-  int request, node, head;
+  int member, node, head;  // member: of the unit
   bool there;
 };
-__device__ __forceinline__ UnitRow unit_row(const PrefixArgs& a, const Seg& s, bool group, int ur) {
-  const int q = ur / a.G;
+__device__ __forceinline__ int unit_tile(const PrefixArgs& a, const Seg& s) { return s.group ? s.rt / a.row_tiles : 0; }
+__device__ __forceinline__ UnitRow unit_row(const PrefixArgs& a, const Seg& s, int ur) {
+  const int q = ur / a.G, tile = unit_tile(a, s), block = s.rt - tile * a.row_tiles;
   UnitRow r;
-  if (group) {
-    const int tile = s.rt / a.row_tiles, block = s.rt - tile * a.row_tiles;
-    const int mi = q / a.unit_nodes, member = tile * a.unit_members + mi;
-    r.node = block * a.unit_nodes + q - mi * a.unit_nodes;
-    r.request = s.start + member;
-    r.there = mi < a.unit_members && member < s.members && r.node < a.nodes;
-  } else {
-    r.node = s.rt * a.unit_nodes + q;
-    r.request = s.item;
-    r.there = q < a.unit_nodes && r.node < a.nodes;
-  }
-  r.head = s.kvh * a.G + ur - q * a.G;
+  r.member = q / a.unit_nodes;
+  r.node = block * a.unit_nodes + q - r.member * a.unit_nodes;
+  r.head = ur - q * a.G;
+  r.there = r.member < a.unit_members && tile * a.unit_members + r.member < s.members && r.node < a.nodes;
   return r;
 }
 
@@ -194,21 +253,20 @@ __device__ __forceinline__ UnitRow unit_row(const PrefixArgs& a, const Seg& s, b
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
 
 // ------------------------------------------------------------------ TMA warps
-// One warp brings Q and K, another V.  With `share` each CTA of the cluster fetches its share of a tile's boxes for all.
-template <typename L, int D, bool SMALL>
-__device__ void run_producer(const PrefixArgs& a, const Bars& bars, uint32_t smem, Cursor<SMALL> cur, Seg s, bool more,
-                             int kv, bool share, volatile uint32_t* abort_flag) {
+// One warp brings K, another Q and V (so that K of the next unit does not wait for the last use of Q).  With `share` each CTA of the cluster fetches its share of a tile's boxes for all.
+template <typename L, int D>
+__device__ void run_producer(const PrefixArgs& a, const Bars& bars, uint32_t smem, Cursor cur, Seg s, bool more, int kv,
+                             bool share, volatile uint32_t* abort_flag) {
   constexpr int kHalves = D / 64;
   const int lane = threadIdx.x % 32;
   const int chunk = lane / kHalves, half = lane % kHalves;
   const bool active = chunk < kTile / a.box && (!share || lane % a.cl == cur.rank);
-  const int ps = a.c.page_size, step = kTile / ps, step_off = kTile - step * ps;
+  const int ps = a.c.page_size;
   const int none = a.c.layers * a.c.pages;  // past the end: the box is filled with zeros
   const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
   const CUtensorMap* map = kv ? &a.tv : &a.tk;
-  const CUtensorMap* q_map = cur.group ? &a.tq_group : &a.tq_row;
   const uint32_t dst = smem + (kv ? L::kV : L::kK) + half * (kTile * 128) + chunk * a.box * 128;
-  const uint32_t q_bytes = static_cast<uint32_t>(D * 2 * a.G * a.unit_nodes * (cur.group ? a.unit_members : 1));
+  const uint32_t q_bytes = static_cast<uint32_t>(D * 2 * a.G * a.unit_nodes * a.unit_members);
   const uint32_t full = kv ? bars.vfull : bars.kfull, empty = kv ? bars.vempty : bars.kempty;
   const uint32_t stages = kv ? L::kVStages : L::kKStages;
   uint32_t slot = 0, phase = 1;
@@ -218,34 +276,56 @@ __device__ void run_producer(const PrefixArgs& a, const Bars& bars, uint32_t sme
     }
   };
   for (uint32_t seg = 0; more; ++seg, more = cur.next(s)) {
-    const int row = a.rows[s.start];
-    const bool fetches = active && row >= 0 && row < a.c.rows;
-    const int32_t* table = a.c.table + static_cast<long long>(fetches ? row : 0) * a.c.max_blocks;
-    int pos = s.base + s.t0 * kTile + chunk * a.box;
-    int block = pos / ps, off = pos - block * ps;
-    auto look = [&]() -> int { return fetches && pos < s.total && block < a.c.max_blocks ? __ldg(table + block) : -1; };
-    int entry = look();
-    if (kv == 0) {  // the unit's Q rows (one buffer: the last unit's scores are done)
+    if (kv == 1) {  // the unit's Q rows (one buffer: the last unit's scores are done)
       if (!wait(bars.qempty, (seg & 1u) ^ 1u, abort_flag, a.c.status)) return settle();
       if (lane == 0) ptx::mbar_arrive_expect_tx(bars.qfull, q_bytes);
       __syncwarp();
-      const int tile = cur.group ? s.rt / a.row_tiles : 0;
+      const int tile = unit_tile(a, s);
       const int node = (s.rt - tile * a.row_tiles) * a.unit_nodes, request = s.start + tile * a.unit_members;
       if (lane < kHalves)
-        tma_load_4d(smem + L::kQ + lane * (kTile * 128), q_map, bars.qfull, lane * 64, s.kvh * a.G, node, request);
+        tma_load_4d(smem + L::kQ + lane * (kTile * 128), &a.tq, bars.qfull, lane * 64, s.kvh * a.G, node, request);
     }
+    Walk walk;
+    walk.begin(cur.t, s, a.warp_members);
+    // the tile ahead: this lane's token, the tokens' end, and its entry of the block table
+    bool fetches = false;
+    const int32_t* table = nullptr;
+    int pos = 0, end = 0, entry = -1, off = 0;
+    auto enter = [&](int request) {
+      const int row = __ldg(a.rows + request);
+      fetches = active && row >= 0 && row < a.c.rows;
+      table = a.c.table + static_cast<long long>(fetches ? row : 0) * a.c.max_blocks;
+    };
+    auto look = [&] {
+      const int block = pos / ps;
+      off = pos - block * ps;
+      entry = fetches && pos < end && block < a.c.max_blocks ? __ldg(table + block) : -1;
+    };
+    if (s.group) {
+      enter(s.start);
+      pos = s.t0 * kTile + chunk * a.box;
+      end = s.tokens;
+    } else {
+      enter(s.start + walk.mi);
+      pos = walk.base + walk.tile * kTile + chunk * a.box;
+      end = walk.total;
+    }
+    look();
     for (int t = s.t0; t < s.t1; ++t) {
       const bool there = entry >= 0 && entry < a.c.pages;
-      if (fetches && !there && pos < s.total) atomicOr(a.c.status, QNRE_CACHE_BAD_PAGE);
+      if (fetches && !there && pos < end) atomicOr(a.c.status, QNRE_CACHE_BAD_PAGE);
       const int page = there ? a.layer * a.c.pages + entry : none, at = off;
-      pos += kTile;
-      block += step;
-      off += step_off;
-      if (off >= ps) {
-        off -= ps;
-        ++block;
+      if (t + 1 < s.t1) {  // the next tile's entry is on its way while this tile's place is waited for
+        if (s.group) {
+          pos += kTile;
+        } else {
+          walk.next();
+          enter(s.start + walk.mi);
+          pos = walk.base + walk.tile * kTile + chunk * a.box;
+          end = walk.total;
+        }
+        look();
       }
-      entry = look();  // on its way while this tile's place is waited for
       if (!wait(empty + 8 * slot, phase, abort_flag, a.c.status)) return settle();
       if (lane == 0) ptx::mbar_arrive_expect_tx(full + 8 * slot, L::kTileBytes);
       __syncwarp();
@@ -272,8 +352,8 @@ __device__ __forceinline__ void release(uint32_t bar, bool share, uint16_t every
 }
 
 // S = Q K^T, tile after tile, across units.
-template <typename L, int D, bool BF16, bool SMALL>
-__device__ void run_scores(const PrefixArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor<SMALL> cur, Seg s,
+template <typename L, int D, bool BF16>
+__device__ void run_scores(const PrefixArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur, Seg s,
                            bool more, bool share, volatile uint32_t* abort_flag) {
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
   constexpr uint32_t kIdesc = (1u << 4) | kFmt | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
@@ -307,8 +387,8 @@ __device__ void run_scores(const PrefixArgs& a, const Bars& bars, uint32_t smem,
 }
 
 // O += P V, tile after tile; names the places of the units begun here for the join.
-template <typename L, int D, bool BF16, bool SMALL>
-__device__ void run_outputs(const PrefixArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor<SMALL> cur, Seg s,
+template <typename L, int D, bool BF16>
+__device__ void run_outputs(const PrefixArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur, Seg s,
                             bool more, bool share, volatile uint32_t* abort_flag) {
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
   constexpr uint32_t kIdesc =
@@ -318,21 +398,18 @@ __device__ void run_outputs(const PrefixArgs& a, const Bars& bars, uint32_t smem
   uint32_t g = 0, slot = 0, phase = 0;
   for (uint32_t seg = 0; more; ++seg, more = cur.next(s)) {
     if (s.t0 == 0) {
-      int parts = !cur.group && s.base == 0 ? -1 : 0;
+      int parts = 0;
       if (!s.whole) {
-        const int last = s.begin + Cursor<SMALL>::tiles_of(s.total - s.base) - 1;
         int lo = cur.index, hi = cur.count - 1;  // the last run that starts by the last tile
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
-          if (cur.start_of(mid) <= last) lo = mid; else hi = mid - 1;
+          if (cur.start_of(mid) <= s.begin + s.tiles - 1) lo = mid; else hi = mid - 1;
         }
         parts = lo - cur.index + 1;
       }
-      const Desc d{static_cast<int>(blockIdx.x), parts};
-      const int tile = cur.group ? s.rt / a.row_tiles : 0, block = s.rt - tile * a.row_tiles;
-      const int request = s.start + tile * a.unit_members;
-      if (tile * a.unit_members < s.members)
-        (cur.group ? a.group_units : a.row_units)[(request * a.Hk + s.kvh) * a.row_tiles + block] = d;
+      const int tile = unit_tile(a, s), request = s.start + tile * a.unit_members;
+      (s.group ? a.group_units : a.row_units)[(request * a.Hk + s.kvh) * a.row_tiles + s.rt - tile * a.row_tiles] =
+          Desc{static_cast<int>(blockIdx.x), share ? a.cl : 1, parts};
     }
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
@@ -366,37 +443,36 @@ __device__ __forceinline__ float rcp_fast(float x) {
 
 // Two threads a row, half a tile each.  SCORED: scores are capped or biased, and come out in base 2; else the scale is
 // applied with the maximum.
-template <typename L, int D, bool BF16, bool SMALL, bool SCORED>
-__device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_base, uint32_t tmem, Cursor<SMALL> cur,
-                            Seg next, bool more, volatile uint32_t* abort_flag, unsigned long long* bad_nodes) {
+template <typename L, int D, bool BF16, bool SCORED>
+__device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_base, uint32_t tmem, Cursor cur, Seg next,
+                            bool more, volatile uint32_t* abort_flag, unsigned long long* marked) {
   constexpr int kCols = kTile / 2, kOut = D / 2;  // tokens of a tile, columns of O this thread has
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int ur = tid % 128, copy = tid / 128, c0 = copy * kCols, o0 = copy * kOut;
   const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
   float* ml = reinterpret_cast<float*>(smem_base + L::kMl);
   const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
-  const int room = a.c.max_blocks * a.c.page_size;
+  const int mark_shift = a.unit_members > 64 ? 1 : 0;
 
   // what this thread's row of a segment is
   struct RowInfo {
     UnitRow at;
     bool row_ok;    // of a node that sees anything
+    int request;
     uint64_t bits;  // the drafts it sees
     int place;      // its position
     float slope;    // in base 2
   };
   auto row_info = [&](const Seg& s) {
-    RowInfo r{unit_row(a, s, cur.group, ur), false, 0, 0, 0.f};
+    RowInfo r{unit_row(a, s, ur), false, 0, 0, 0, 0.f};
     if (!r.at.there) return r;
-    const int i = r.at.request;
+    const int i = r.request = s.start + unit_tile(a, s) * a.unit_members + r.at.member;
     r.row_ok = a.counts == nullptr || r.at.node < a.counts[i];
-    if (!cur.group)
+    if (!s.group)
       r.bits = a.mask != nullptr ? a.mask[static_cast<long long>(i) * a.nodes + r.at.node] : (2ull << r.at.node) - 1;
     if (SCORED && a.slopes != nullptr) {
-      r.slope = a.slopes[r.at.head] * kLog2e;
-      const int row = cur.group ? a.rows[i] : 0;
-      const int len = cur.group ? (row >= 0 && row < a.c.rows ? min(a.c.length(row), room) : 0) : s.len;
-      r.place = len + (a.depths != nullptr ? a.depths[static_cast<long long>(i) * a.nodes + r.at.node] : r.at.node);
+      r.slope = a.slopes[s.kvh * a.G + r.at.head] * kLog2e;
+      r.place = cur.t.len[i] + (a.depths != nullptr ? a.depths[static_cast<long long>(i) * a.nodes + r.at.node] : r.at.node);
     }
     return r;
   };
@@ -409,125 +485,185 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
     s = next;
     row = next_row;
     const bool in_out = row.at.there, row_ok = row.row_ok;
-    const int slots = s.total - s.len;  // drafts that have a place
-    const uint64_t bits = slots < 64 ? row.bits & ((1ull << slots) - 1) : row.bits;
-    const int table_row = a.rows[s.start];
+    Walk walk;
+    walk.begin(cur.t, s, a.warp_members);
     float m = -INFINITY, l = 0.f;
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
-      const int pos0 = s.base + t * kTile;
-      uint32_t v[kCols / 32][32];
+      int pos0 = t * kTile, len = s.tokens, total = s.tokens, member = 0;
+      int filled = (total + a.box - 1) & -a.box;  // TMA has zeroed V from here on
+      bool mine = true;  // a row that sees this tile
+      if (!s.group) {
+        member = walk.mi;
+        pos0 = walk.base + walk.tile * kTile;
+        len = walk.len;
+        total = walk.total;
+        filled = walk.base + ((total - walk.base + a.box - 1) & -a.box);
+        mine = row.at.member == member;
+        if (t + 1 < s.t1) walk.next();
+      }
+      const bool active = __any_sync(0xFFFFFFFFu, mine);
+      const bool tail = pos0 + kTile > len;
       wait(bars.pvdone + 8 * b, ((g >> 1) & 1u) ^ 1u, abort_flag, a.c.status);
-      wait(bars.sfull + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status);
-      __syncwarp();  // the tensor-memory instructions are warp-wide
-      ptx::tc_fence_after_sync();
+      uint32_t p[kCols / 2];
+      if (active) {
+        uint32_t v[kCols / 32][32];
+        wait(bars.sfull + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status);
+        __syncwarp();  // the tensor-memory instructions are warp-wide
+        ptx::tc_fence_after_sync();
 #pragma unroll
-      for (int j = 0; j < kCols / 32; ++j)
-        ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemS + b * 128 + c0 + 32 * j, v[j]);
-      ptx::tmem_ld_wait();
+        for (int j = 0; j < kCols / 32; ++j)
+          ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemS + b * 128 + c0 + 32 * j, v[j]);
+        ptx::tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < kCols / 32; ++j) tmem_fence_regs(v[j]);
-      ptx::tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bars.sfree + 8 * b);
+        for (int j = 0; j < kCols / 32; ++j) tmem_fence_regs(v[j]);
+        ptx::tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars.sfree + 8 * b);
 
-      const bool tail = pos0 + kTile > s.len;
-      if (SCORED) {
-        if (a.cap_log2 > 0.f) {  // tanh x = 1 - 2 / (1 + e^2x): to 2^-23 of the cap, however large the score
-#pragma unroll
-          for (int i = 0; i < kCols; ++i) {
-            const float e = exp2_fast(__uint_as_float(v[i / 32][i % 32]) * a.cap_in);
-            v[i / 32][i % 32] = __float_as_uint(fmaf(rcp_fast(e + 1.f), -2.f * a.cap_log2, a.cap_log2));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kCols; ++i)
-            v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) * a.scale_log2);
-        }
-        if (a.slopes != nullptr) {
+        if (SCORED) {
+          // c tanh(x / c) = x + x (x / c)^2 P: the odd polynomial P is fitted by least squares up to 0.6 (8e-8 relative) and up
+          // to 1 (6e-8); beyond, for a warp that holds any such score, 1 - 2 / (1 + e^2z): to 2^-22 of the cap, however large.
           const int d0 = pos0 + c0;
-          const float at0 = row.slope * static_cast<float>(d0 - row.place);
+          const float at0 = SCORED && a.slopes != nullptr ? row.slope * static_cast<float>(d0 - row.place) : 0.f;
+          const uint64_t start2 = pair(at0, at0);
+          auto each_pair = [&](auto f) {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i)
-            v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) + fmaf(row.slope, static_cast<float>(i), at0));
-          if (tail && a.depths != nullptr && !cur.group) {  // a draft lies at its depth, not at its slot
+            for (int i = 0; i < kCols; i += 2) {
+              uint32_t *x0 = &v[i / 32][i % 32], *x1 = &v[i / 32][(i + 1) % 32];
+              float y0, y1;
+              unpair(f(pair(__uint_as_float(*x0), __uint_as_float(*x1))), y0, y1);
+              *x0 = __float_as_uint(y0);
+              *x1 = __float_as_uint(y1);
+            }
+          };
+          float most = 0.f;
+          if (a.cap_log2 > 0.f) {
+            float most1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < kCols; i += 4) {
+              most = max3(most, fabsf(__uint_as_float(v[i / 32][i % 32])), fabsf(__uint_as_float(v[i / 32][(i + 1) % 32])));
+              most1 = max3(most1, fabsf(__uint_as_float(v[i / 32][(i + 2) % 32])), fabsf(__uint_as_float(v[i / 32][(i + 3) % 32])));
+            }
+            most = fmaxf(most, most1) * a.cap_in;
+          }
+          auto both = [](float x) { return pair(x, x); };
+          if (a.cap_log2 <= 0.f) {
+            each_pair([&](uint64_t x) { return fma2(x, scale2, start2); });
+          } else if (!__any_sync(0xFFFFFFFFu, most > a.cap_near)) {
+            const uint64_t k0 = both(a.cap_poly[0]), k1 = both(a.cap_poly[1]), k2 = both(a.cap_poly[2]), k3 = both(a.cap_poly[3]);
+            each_pair([&](uint64_t x) {
+              const uint64_t y = fma2(x, scale2, 0), z = fma2(x, x, 0);
+              return fma2(y, fma2(z, fma2(z, fma2(z, fma2(z, k3, k2), k1), k0), 0), fma2(x, scale2, start2));
+            });
+          } else if (!__any_sync(0xFFFFFFFFu, most > 1.f)) {
+            const uint64_t in2 = both(a.cap_in);
+            each_pair([&](uint64_t x) {
+              const uint64_t y = fma2(x, scale2, 0), t = fma2(x, in2, 0), z = fma2(t, t, 0);
+              uint64_t k = fma2(z, both(0.0010582602117210627f), both(-0.006259326823055744f));
+              k = fma2(z, k, both(0.020359747111797333f));
+              k = fma2(z, k, both(-0.05349870026111603f));
+              k = fma2(z, k, both(0.13326409459114075f));
+              k = fma2(z, k, both(-0.33332985639572144f));
+              return fma2(y, fma2(z, k, 0), fma2(x, scale2, start2));
+            });
+          } else {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) {
+              const float e = exp2_fast(__uint_as_float(v[i / 32][i % 32]) * a.cap_in * 2.885390043258667f);  // 2 log2(e)
+              v[i / 32][i % 32] = __float_as_uint(fmaf(rcp_fast(e + 1.f), -2.f * a.cap_log2, a.cap_log2 + at0));
+            }
+          }
+          if (a.slopes != nullptr) {
+#pragma unroll
+            for (int i = 1; i < kCols; ++i)
+              v[i / 32][i % 32] = __float_as_uint(fmaf(row.slope, static_cast<float>(i), __uint_as_float(v[i / 32][i % 32])));
+            if (tail && a.depths != nullptr && !s.group) {  // a draft lies at its depth, not at its slot
+              const int32_t* depths = a.depths + static_cast<long long>(s.start + member) * a.nodes;
 #pragma unroll 1
-            for (int j = max(s.len - d0, 0); j < min(s.total - d0, kCols); ++j) {
-              const int node = d0 + j - s.len;
-              const float off = row.slope * static_cast<float>(a.depths[static_cast<long long>(s.item) * a.nodes + node] - node);
+              for (int j = max(len - d0, 0); j < min(total - d0, kCols); ++j) {
+                const int node = d0 + j - len;
+                const float off = row.slope * static_cast<float>(depths[node] - node);
 #pragma unroll
-              for (int i = 0; i < kCols; ++i)
-                if (i == j) v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) + off);
+                for (int i = 0; i < kCols; ++i)
+                  if (i == j) v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) + off);
+              }
             }
           }
         }
-      }
-      if (tail) {
+        if (tail) {
+          const int slots = total - len;  // drafts that have a place
+          const uint64_t bits = slots < 64 ? row.bits & ((1ull << slots) - 1) : row.bits;
 #pragma unroll
-        for (int j = 0; j < kCols / 32; ++j) {
-          const uint32_t see = seen_word(pos0 + c0 + 32 * j - s.len, bits);
+          for (int j = 0; j < kCols / 32; ++j) {
+            const uint32_t see = seen_word(pos0 + c0 + 32 * j - len, bits);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(see & (1u << i))) v[j][i] = 0xFF800000u;
+            for (int i = 0; i < 32; ++i)
+              if (!(see & (1u << i))) v[j][i] = 0xFF800000u;
+          }
         }
-      }
-      float mx0 = -INFINITY, mx1 = -INFINITY;
+        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < kCols / 32; ++j)
+        for (int j = 0; j < kCols / 32; ++j)
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          mx0 = max3(mx0, __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
-          mx1 = max3(mx1, __uint_as_float(v[j][i + 2]), __uint_as_float(v[j][i + 3]));
+          for (int i = 0; i < 32; i += 4) {
+            mx0 = max3(mx0, __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
+            mx1 = max3(mx1, __uint_as_float(v[j][i + 2]), __uint_as_float(v[j][i + 3]));
+          }
+        float mx = fmaxf(mx0, mx1) * (SCORED ? 1.f : a.scale_log2);
+        {  // with the other half's (two buffers: one is written again only when its tile's product is done)
+          float* at = ml + (L::kMlBuffers == 2 ? b * 256 : 0) + ur;
+          if (L::kMlBuffers == 1) pair_sync(warp % 4);
+          at[copy * 128] = mx;
+          pair_sync(warp % 4);
+          mx = fmaxf(mx, at[(copy ^ 1) * 128]);
         }
-      float mx = fmaxf(mx0, mx1) * (SCORED ? 1.f : a.scale_log2);
-      {  // with the other half's; two buffers, as the next tile's may be written before this is read
-        float* at = ml + b * 256 + ur;
-        at[copy * 128] = mx;
-        pair_sync(warp % 4);
-        mx = fmaxf(mx, at[(copy ^ 1) * 128]);
-      }
-      mx -= kLift<BF16>;  // m: the row's maximum less the lift, which leaves O / l and m + log2 l as they are
-      const bool grow = mx > m + kRescale;
-      if (t == s.t0) {
-        m = mx;
-      } else if (__any_sync(0xFFFFFFFFu, grow)) {
-        const uint32_t last = g - 1;
-        wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
-        __syncwarp();
-        ptx::tc_fence_after_sync();
-        const float f = grow ? exp2_fast(m - mx) : 1.f;
-        if (grow) m = mx;
-        l *= f;
+        if (!mine) mx = -INFINITY;
+        mx -= kLift<BF16>;  // m: the row's maximum less the lift, which leaves O / l and m + log2 l as they are
+        const bool grow = mx > m + kRescale, fresh = m == -INFINITY;  // (a row that has seen nothing has no O to rescale)
+        if (__any_sync(0xFFFFFFFFu, grow && !fresh)) {
+          const uint32_t last = g - 1;
+          wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
+          __syncwarp();
+          ptx::tc_fence_after_sync();
+          const float f = grow && !fresh ? exp2_fast(m - mx) : 1.f;
+          l *= f;
 #pragma unroll 1
-        for (int c = o0; c < o0 + kOut; c += 32) {
-          uint32_t o[32];
-          ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
-          ptx::tmem_ld_wait();
-          tmem_fence_regs(o);
+          for (int c = o0; c < o0 + kOut; c += 32) {
+            uint32_t o[32];
+            ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
+            ptx::tmem_ld_wait();
+            tmem_fence_regs(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st_x32(tmem + lane_base + kTmemO + c, o);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_x32(tmem + lane_base + kTmemO + c, o);
+          }
+          tmem_st_wait();
         }
-        tmem_st_wait();
-      }
-      const float ms = m == -INFINITY ? 0.f : m;
-      const uint64_t neg = pair(-ms, -ms);
-      uint32_t p[kCols / 2];
-      uint64_t sum[2] = {0, 0};
+        if (grow) m = mx;
+        // (a row that does not see the tile gets zeros; what is not finite in its scores marks it, as in V)
+        const float ms = mine ? (m == -INFINITY ? 0.f : m) : INFINITY;
+        const uint64_t neg = pair(-ms, -ms);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) {
-        float e0, e1;
-        const uint64_t x = pair(__uint_as_float(v[i / 16][(2 * i) % 32]), __uint_as_float(v[i / 16][(2 * i + 1) % 32]));
-        unpair(SCORED ? add2(x, neg) : fma2(x, scale2, neg), e0, e1);
-        e0 = exp2_fast(e0);
-        e1 = exp2_fast(e1);
-        sum[i & 1] = add2(sum[i & 1], pair(e0, e1));
-        p[i] = pack2<BF16>(e0, e1);
-      }
-      {
+        for (int i = 0; i < kCols / 2; ++i) {
+          float e0, e1;
+          const uint64_t x = pair(__uint_as_float(v[i / 16][(2 * i) % 32]), __uint_as_float(v[i / 16][(2 * i + 1) % 32]));
+          unpair(SCORED ? add2(x, neg) : fma2(x, scale2, neg), e0, e1);
+          e0 = exp2_fast(e0);
+          e1 = exp2_fast(e1);
+          sum[i & 1] = add2(sum[i & 1], pair(e0, e1));
+          p[i] = pack2<BF16>(e0, e1);
+        }
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
+      } else {  // the tile of a request whose rows other warps have
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        if (lane == 0) ptx::mbar_arrive(bars.sfree + 8 * b);
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) p[i] = 0;
       }
       tmem_st_x32(tmem + lane_base + kTmemP + b * 64 + c0 / 2, p);
       if (tail) {
@@ -535,9 +671,9 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
         wait(bars.vfull + 8 * slot, (g / L::kVStages) & 1u, abort_flag, a.c.status);
         const int x = tid % 128, pos = pos0 + x;
         constexpr int kPieces = D / 16;
-        if (pos >= s.len && clean_v_row<D, BF16>(smem_base + L::kV + slot * L::kTileBytes + x * 128, pos < s.total,
-                                                 copy * kPieces, (copy + 1) * kPieces))
-          atomicOr(bad_nodes + seg % 3, 1ull << (pos - s.len));
+        if (pos >= len && pos < filled && clean_v_row<D, BF16>(smem_base + L::kV + slot * L::kTileBytes + x * 128, pos < total,
+                                               copy * kPieces, (copy + 1) * kPieces))
+          atomicOr(marked + seg % 3, 1ull << (member >> mark_shift));
         __syncwarp();
       }
       tmem_st_wait();
@@ -553,27 +689,32 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
     if (more) next_row = row_info(next);  // on its way during this segment's end
 
     // ---------------- the segment's result
-    ml[(g & 1u) * 256 + tid] = l;  // (the buffer that the last tile did not use)
     const uint32_t last = g - 1;
     wait(bars.pvdone + 8 * (last & 1u), (last >> 1) & 1u, abort_flag, a.c.status);
+    ml[tid] = l;  // (every warp is done with the maxima of its tiles)
     soft_sync();
     ptx::tc_fence_after_sync();
     // every warp has read the word of the segment before, and none uses it again before the next segment's end
-    if (tid == 0) bad_nodes[(seg + 2) % 3] = 0;
-    const uint64_t bad = row_ok ? bad_nodes[seg % 3] & bits : 0;
-    l += ml[(g & 1u) * 256 + (tid ^ 128)];
+    if (tid == 0) marked[(seg + 2) % 3] = 0;
+    bool mark = row_ok && !s.group && (marked[seg % 3] >> (row.at.member >> mark_shift) & 1);
+    l += ml[tid ^ 128];
     pair_sync(warp % 4);  // read by both before the next tile's maxima go there
-    const bool done = s.whole && !cur.group && s.base == 0;  // no other part of these rows
+    const bool done = s.whole && !s.group && in_out && cur.t.base[row.request] == 0;  // no other part of this row
     const float inv = !done ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
-    const long long token = static_cast<long long>(row.at.request) * a.nodes + row.at.node;
-    const long long orow = token * a.Hq + row.at.head;
-    const int head = row.at.head - s.kvh * a.G;
-    const long long prow =
-        s.whole ? (cur.group ? a.group_rows : a.own_rows) +
-                      (static_cast<long long>(s.kvh) * a.n * a.nodes + token) * a.G + head
-                : static_cast<long long>(s.slot) * 128 + ur;
+    const long long token = static_cast<long long>(row.request) * a.nodes + row.at.node;
+    const long long orow = token * a.Hq + s.kvh * a.G + row.at.head;
+    const long long prow = s.whole ? (s.group ? a.group_rows : a.own_rows) +
+                                         (static_cast<long long>(s.kvh) * a.n * a.nodes + token) * a.G + row.at.head
+                                   : static_cast<long long>(s.slot) * 128 + ur;
+    // Warps without rows, and such whose requests have no tile here, have nothing to read.
+    const bool any = __any_sync(0xFFFFFFFFu, in_out && (done || m != -INFINITY || l != 0.f));
+    if (!any) {
+      ptx::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars.ofree);
+    }
 #pragma unroll 1
-    for (int c = o0; c < o0 + kOut; c += 32) {
+    for (int c = o0; any && c < o0 + kOut; c += 32) {
       uint32_t o[32];
       ptx::tmem_ld_32x32b_x32(tmem + lane_base + kTmemO + c, o);
       ptx::tmem_ld_wait();
@@ -591,9 +732,12 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
       for (int i = 0; i < 32; i += 2) odd = fma2(pair(x[i], x[i + 1]), 0, odd);
       float odd0, odd1;
       unpair(odd, odd0, odd1);
-      if (__any_sync(0xFFFFFFFFu, row_ok && odd0 + odd1 != 0.f)) {  // (NaN compares unequal)
-        const Kinds k = search_context<BF16>(a.c, a.layer, table_row, s.kvh, s.base + s.t0 * kTile,
-                                             min(s.base + s.t1 * kTile, s.len), c);
+      const bool strange = row_ok && odd0 + odd1 != 0.f;  // (NaN compares unequal)
+      if (!s.group) {
+        mark |= strange;
+      } else if (__any_sync(0xFFFFFFFFu, strange)) {
+        const Kinds k = search_context<BF16>(a.c, a.layer, a.rows[s.start], s.kvh, s.t0 * kTile,
+                                             min(s.t1 * kTile, s.tokens), c);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const uint32_t bit = 1u << i;
@@ -601,44 +745,40 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
             x[i] = (k.nan | (k.plus & k.minus)) & bit ? NAN : (k.plus & bit ? INFINITY : -INFINITY);
         }
       }
-      if (bad != 0) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          x[i] = add_nonfinite<BF16>(a.c, a.layer, table_row, s.kvh, s.len, s.base + s.t0 * kTile, s.base + s.t1 * kTile,
-                                     bad, c + i, x[i]);
-      }
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] = row_ok ? x[i] * inv : 0.f;
-      if (in_out && done) {
+      if (done) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = pack2<BF16>(x[2 * e], x[2 * e + 1]);
         uint4* dst = reinterpret_cast<uint4*>(a.out + (orow * D + c) * 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      } else if (in_out) {
+      } else if (in_out && (m != -INFINITY || l != 0.f)) {  // (the join leaves out what has seen nothing)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           a.part_o[piece_of<D>(prow, c / 4 + i)] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
       }
       __syncwarp();
     }
-    if (in_out && copy == 0) {
-      if (!done)
-        a.part_ml[prow] = make_float2(m, l);
-      else if (a.lse != nullptr)
-        a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if (in_out) {
+      float* dst = reinterpret_cast<float*>(a.part_ml + prow);
+      if (copy == 0) {
+        *reinterpret_cast<float2*>(dst) = make_float2(m, l);
+        if (done && a.lse != nullptr) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      }
+      dst[2 + copy] = mark ? 1.f : 0.f;
     }
   }
 }
 
-// Running sums (or maxima) of x[1 .. n], by one warp.
-template <bool MAXIMUM>
-__device__ __forceinline__ void scan_table(int* x, int n) {
+// x[0 .. n) to its running sums (or maxima), x given by f; one warp.
+template <bool MAXIMUM, typename F>
+__device__ __forceinline__ void scan_table(int* x, int n, F f) {
   const int lane = threadIdx.x % 32;
   int carry = 0;
   for (int base = 0; base < n; base += 32) {
-    int v = base + lane < n ? x[base + lane] : 0;
+    int v = base + lane < n ? f(base + lane) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
@@ -658,9 +798,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   Words* words = reinterpret_cast<Words*>(smem_base + L::kWords);
   constexpr int kSoftWarps = kSoftThreads / 32;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  int* pre = reinterpret_cast<int*>(smem_base + L::kPre);
-  int2* items = reinterpret_cast<int2*>(smem_base + L::kItems);
-  int* extra = reinterpret_cast<int*>(smem_base + L::kExtra);
   Bars bars;
   {
     uint32_t at = smem + L::kBars;
@@ -683,126 +820,125 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     bars.drain = take(1);
     bars.drain2 = take(1);
   }
+  auto table = [&](int at) { return reinterpret_cast<int*>(smem_base + at); };
+  Cursor cur;
+  Tables& t = cur.t;
+  t.base = table(L::kBase);
+  t.len = table(L::kLen);
+  t.drafts = reinterpret_cast<uint8_t*>(smem_base + L::kDrafts);
+  t.starts = table(L::kStarts);
+  t.common = table(L::kCommon);
+  t.single = table(L::kSingle);
+  t.wide = table(L::kWide);
+  t.blocks = (a.n + a.unit_members - 1) / a.unit_members;
+  t.n_groups = a.n_groups;
+  cur.n = a.n;
+  cur.Hk = a.Hk;
+  cur.cl = a.cl;
+  cur.row_tiles = a.row_tiles;
+  cur.unit_members = a.unit_members;
   if (warp == kSoftWarps) ptx::tmem_alloc(ptx::smem_addr(&words->tmem), 512);
   if (warp == kSoftWarps + 1 && lane == 0) {
     words->abort = 0;
-    words->bad_nodes[0] = words->bad_nodes[1] = words->bad_nodes[2] = 0;
+    words->marked[0] = words->marked[1] = words->marked[2] = 0;
     ptx::prefetch_tensormap(&a.tk);
     ptx::prefetch_tensormap(&a.tv);
-    ptx::prefetch_tensormap(&a.tq_group);
-    ptx::prefetch_tensormap(&a.tq_row);
+    ptx::prefetch_tensormap(&a.tq);
   }
-  // Lengths, common tokens, and the first tile of each item in the two concatenated runs; the tables lie where K will.
-  constexpr int kMost = QNRE_MAX_CALL_ROWS + 1;
-  int* starts = reinterpret_cast<int*>(smem_base + L::kK);
-  int* common = starts + kMost;  // tokens of each group
-  int* lens = common + kMost;
-  int* drafts = lens + kMost;
-  int* row_pre = drafts + kMost;
-  int* group_pre = row_pre + kMost;
+  for (int i = tid; i < t.blocks; i += kThreads) t.single[i + 1] = 0;
+
+  // Lengths, common tokens, and where the items begin in the two concatenated runs.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int ps = a.c.page_size, room = a.c.max_blocks * ps;
-  for (int g = tid; g <= a.n_groups; g += kThreads) {
-    starts[g] = a.n_groups > 0 ? min(max(a.groups[g], 0), a.n) : 0;
-    common[g] = g < a.n_groups ? min(max(a.shared[g], 0), room) / ps * ps : 0;
-  }
-  for (int i = tid; i < a.n; i += kThreads) {
-    const int row = a.rows[i];
-    int len = 0, cnt = 0;
+  for (int i = tid; i < max(a.n, a.n_groups + 1); i += kThreads) {
+    const int row = i < a.n ? a.rows[i] : -1;
+    const int start = a.n_groups > 0 && i <= a.n_groups ? a.groups[i] : 0;
+    const int common = i < a.n_groups ? a.shared[i] : 0;
+    int cnt = i < a.n && a.counts != nullptr ? min(max(a.counts[i], 0), a.nodes) : a.nodes;
+    int len = 0;
     if (row >= 0 && row < a.c.rows) {
       len = min(a.c.length(row), room);
-      cnt = a.counts != nullptr ? min(max(a.counts[i], 0), a.nodes) : a.nodes;
-    } else if (blockIdx.x == 0) {
-      atomicOr(a.c.status, QNRE_CACHE_BAD_ROW);
+    } else {
+      cnt = 0;
+      if (i < a.n && blockIdx.x == 0) atomicOr(a.c.status, QNRE_CACHE_BAD_ROW);
     }
-    lens[i] = len;
-    drafts[i] = min(len + cnt, room) - len;
+    if (i <= a.n_groups) t.starts[i] = min(max(start, 0), a.n);
+    if (i < a.n_groups) t.common[i] = min(max(common, 0), room) / ps * ps;
+    if (i < a.n) {
+      t.len[i] = len;
+      t.drafts[i] = static_cast<uint8_t>(min(len + cnt, room) - len);
+    }
   }
   __syncthreads();
-  if (warp == 0) scan_table<true>(starts, a.n_groups + 1);  // (ascending, whatever is given)
-  __syncthreads();
-  auto group_of = [&](int i) {  // the last group that starts by i, or -1 where it ends before i
-    int lo = -1, hi = a.n_groups - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (starts[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    return lo >= 0 && i < starts[lo + 1] ? lo : -1;
-  };
   if (a.n_groups > 0) {
-    for (int i = tid; i < a.n; i += kThreads) {  // no more than every member has
-      const int g = group_of(i);
-      if (g >= 0) atomicMin(&common[g], starts[g + 1] - starts[g] > 1 ? lens[i] / ps * ps : 0);
+    if (warp == 0) scan_table<true>(t.starts, a.n_groups + 1, [&](int i) { return t.starts[i]; });  // (ascending, whatever is given)
+    __syncthreads();
+    for (int i = tid; i < a.n; i += kThreads) {
+      int lo = -1, hi = a.n_groups - 1;  // the last group that starts by i
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (t.starts[mid] <= i) lo = mid; else hi = mid - 1;
+      }
+      const int g = lo >= 0 && i < t.starts[lo + 1] ? lo : -1;
+      t.base[i] = g;
+      // no more than every member has, in whole pages; nothing where there is only one
+      if (g >= 0) atomicMin(&t.common[g], t.starts[g + 1] - t.starts[g] > 1 ? t.len[i] / ps * ps : 0);
     }
     __syncthreads();
   }
-  using Run = Cursor<SMALL>;
   for (int i = tid; i < a.n; i += kThreads) {
-    const int g = a.n_groups > 0 ? group_of(i) : -1;
-    const int base = g >= 0 ? common[g] : 0;
-    row_pre[i + 1] = (Run::tiles_of(lens[i] + drafts[i] - base) + kUnitCost) * a.Hk * a.row_tiles;
-    if (blockIdx.x == 0) a.first_of[i] = base > 0 ? starts[g] : -1;
+    const int g = a.n_groups > 0 ? t.base[i] : -1;
+    const int base = g >= 0 ? t.common[g] : 0;
+    t.base[i] = base;
+    atomicAdd(&t.single[i / a.unit_members + 1], tiles_of(t.len[i] + t.drafts[i] - base));
+    if (blockIdx.x == 0) a.requests[i] = make_int2(base > 0 ? t.starts[g] : -1, base);
   }
-  for (int g = tid; g < a.n_groups; g += kThreads) {
-    const int members = starts[g + 1] - starts[g];
-    group_pre[g + 1] = members > 0 && common[g] > 0
-                           ? (Run::tiles_of(common[g]) + kUnitCost) * a.Hk *
-                                 Run::clusters_of(members, a.unit_members, a.row_tiles, a.cl)
-                           : 0;
-  }
-  if (tid == 0) row_pre[0] = group_pre[0] = 0;
   __syncthreads();
-  if (warp == 0) scan_table<false>(row_pre + 1, a.n);
-  if (warp == 1) scan_table<false>(group_pre + 1, a.n_groups);
+  // one warp each: a unit's tiles and its start and end, times units
+  auto group_items = [&](int g, bool wide) {
+    const int members = t.starts[g + 1] - t.starts[g], units = cur.units_of(members), full = cur.shared_units(units);
+    return t.common[g] > 0 ? (tiles_of(t.common[g]) + kUnitCost) * a.Hk * (wide ? full / a.cl : units - full) : 0;
+  };
+  const int n_single = t.blocks + a.n_groups;
+  if (warp == 0) {
+    scan_table<false>(t.single + 1, n_single, [&](int i) {
+      return i < t.blocks ? (t.single[i + 1] + kUnitCost) * a.Hk * a.row_tiles : group_items(i - t.blocks, false);
+    });
+    if (lane == 0) t.single[0] = 0;
+  } else if (warp == 1) {
+    scan_table<false>(t.wide + 1, a.n_groups, [&](int g) { return group_items(g, true); });
+    if (lane == 0) t.wide[0] = 0;
+  }
   __syncthreads();
 
-  // The clusters that take groups: in proportion to the tiles, so that the longest run of either kind is the shortest.
-  const int W_rows = row_pre[a.n], W_groups = group_pre[a.n_groups];
+  // The clusters that share tiles: in proportion to the work, so that the longest run of either kind is the shortest.
+  const int W_single = t.single[n_single], W_wide = t.wide[a.n_groups];
   const int clusters = static_cast<int>(gridDim.x) / a.cl;
-  int for_groups = 0;
-  if (W_groups > 0) {
-    const float wide = static_cast<float>(W_groups) * a.cl;
-    const int low = static_cast<int>(clusters * (wide / (wide + W_rows)));
+  int for_wide = 0;
+  if (W_wide > 0) {
+    const float wide = static_cast<float>(W_wide) * a.cl;
+    const int low = static_cast<int>(clusters * (wide / (wide + W_single)));
     auto longest = [&](int c) {
       return c < 1 || c >= clusters ? 3e38f
-                                    : fmaxf(static_cast<float>(W_groups) / c,
-                                            static_cast<float>(W_rows) / static_cast<float>((clusters - c) * a.cl));
+                                    : fmaxf(static_cast<float>(W_wide) / c,
+                                            static_cast<float>(W_single) / static_cast<float>((clusters - c) * a.cl));
     };
-    for_groups = longest(low) <= longest(low + 1) ? low : low + 1;
-    for_groups = min(max(for_groups, 1), clusters - 1);
+    for_wide = longest(low) <= longest(low + 1) ? low : low + 1;
+    for_wide = min(max(for_wide, 1), clusters - 1);
   }
   const int cluster = static_cast<int>(blockIdx.x) / a.cl;
-  Run cur;
-  cur.group = cluster < for_groups;
-  const bool share = cur.group && a.cl > 1;
-  cur.pre = pre;
-  cur.items = items;
-  cur.extra = extra;
-  cur.cl = cur.group ? a.cl : 1;
+  const bool share = cluster < for_wide;
+  cur.wide = share;
+  cur.pre = share ? t.wide : t.single;
   cur.rank = share ? static_cast<int>(ptx::cluster_ctarank()) : 0;
-  cur.row_tiles = a.row_tiles;
-  cur.unit_members = a.unit_members;
-  const int W = cur.group ? W_groups : W_rows;
-  cur.index = cur.group ? cluster : static_cast<int>(blockIdx.x) - for_groups * a.cl;
-  cur.count = min(cur.group ? for_groups : (clusters - for_groups) * a.cl, W);
+  const int W = share ? W_wide : W_single;
+  cur.index = share ? cluster : static_cast<int>(blockIdx.x) - for_wide * a.cl;
+  cur.count = min(share ? for_wide : (clusters - for_wide) * a.cl, W);
   cur.quot = W / cur.count;
   cur.rem = W - cur.quot * cur.count;
   cur.cur = cur.index < cur.count ? cur.start_of(cur.index) : 0;
   cur.end = cur.index < cur.count ? cur.start_of(cur.index + 1) : 0;
-  const int n_items = cur.group ? a.n_groups : a.n;
-  for (int i = tid; i <= n_items; i += kThreads) {
-    pre[i] = cur.group ? group_pre[i] : row_pre[i];
-    if (i == n_items) break;
-    if (cur.group) {
-      items[i] = make_int2(starts[i] << 16 | (starts[i + 1] - starts[i]), common[i]);
-    } else {
-      const int g = a.n_groups > 0 ? group_of(i) : -1;
-      const int base = g >= 0 ? common[g] : 0;
-      items[i] = make_int2(base, SMALL ? lens[i] << 7 | drafts[i] : lens[i]);
-      if (!SMALL) extra[i] = drafts[i];
-    }
-  }
   if (warp == kSoftWarps + 1 && lane == 0) {
     const uint32_t readers = share ? a.cl : 1;
     for (int i = 0; i < L::kKStages; ++i) {
@@ -826,29 +962,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     ptx::mbar_init(bars.drain2, 1);
     ptx::fence_mbar_init();
   }
-  ptx::fence_proxy_async_smem();  // the tables were there before K is
   ptx::tc_fence_before_sync();
   __syncthreads();
-  if (a.cl > 1) ptx::cluster_sync();  // every CTA's barriers stand, and its tables are read, before another sends to it
+  if (a.cl > 1) ptx::cluster_sync();  // every CTA's barriers stand before another sends to it
   ptx::tc_fence_after_sync();
   const uint32_t tmem = words->tmem;
-  int lo = 0, hi = n_items - 1;
+  int lo = 0, hi = (share ? a.n_groups : n_single) - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (pre[mid] <= cur.cur) lo = mid; else hi = mid - 1;
+    if (cur.pre[mid] <= cur.cur) lo = mid; else hi = mid - 1;
   }
   cur.item = lo;
   Seg first;  // found once for all roles
   const bool more = cur.next(first);
 
   if (warp < kSoftWarps) {
-    run_softmax<L, D, BF16, SMALL, SCORED>(a, bars, smem_base, tmem, cur, first, more, &words->abort, words->bad_nodes);
+    run_softmax<L, D, BF16, SCORED>(a, bars, smem_base, tmem, cur, first, more, &words->abort, words->marked);
   } else if (warp == kSoftWarps || warp == kSoftWarps + 3) {
-    run_producer<L, D, SMALL>(a, bars, smem, cur, first, more, warp == kSoftWarps ? 0 : 1, share, &words->abort);
+    run_producer<L, D>(a, bars, smem, cur, first, more, warp == kSoftWarps ? 0 : 1, share, &words->abort);
   } else if (warp == kSoftWarps + 1) {
-    if (lane == 0) run_scores<L, D, BF16, SMALL>(a, bars, smem, tmem, cur, first, more, share, &words->abort);
+    if (lane == 0) run_scores<L, D, BF16>(a, bars, smem, tmem, cur, first, more, share, &words->abort);
   } else if (lane == 0) {
-    run_outputs<L, D, BF16, SMALL>(a, bars, smem, tmem, cur, first, more, share, &words->abort);
+    run_outputs<L, D, BF16>(a, bars, smem, tmem, cur, first, more, share, &words->abort);
   }
   __syncwarp();
   ptx::tc_fence_before_sync();
@@ -865,81 +1000,167 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------ join
-struct JoinArgs {
-  const int* first_of;
-  const Desc *row_units, *group_units;
-  const float2* part_ml;
-  const float4* part_o;
-  char* out;
-  float* lse;
-  long long own_rows, group_rows, rows;  // rows: of the output
-  int n, nodes, Hq, Hk, G, cl, unit_nodes, unit_members, row_tiles;
+// A row's part over its own tokens, token by token in fp32 (base 2), for rows that met a non-finite V: columns [4 i4, 4 i4 + 4).
+// Non-finite elements of V that it sees count whatever their weight.
+struct OwnPart {
+  float m, l;
+  float4 o;
 };
+template <int D, bool BF16>
+__device__ __noinline__ OwnPart own_part(const PrefixArgs& a, int i, int node, int kvh, int h, int i4) {
+  OwnPart r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  float strange[4] = {0.f, 0.f, 0.f, 0.f};
+  float* o[4] = {&r.o.x, &r.o.y, &r.o.z, &r.o.w};
+  const int row = a.rows[i], cnt = a.counts != nullptr ? min(max(a.counts[i], 0), a.nodes) : a.nodes;
+  if (row < 0 || row >= a.c.rows || node >= cnt) return r;
+  const int room = a.c.max_blocks * a.c.page_size, len = min(a.c.length(row), room), total = min(len + cnt, room);
+  const long long at = static_cast<long long>(i) * a.nodes;
+  const uint64_t bits = a.mask != nullptr ? a.mask[at + node] : (2ull << node) - 1;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + i * a.q_stride[0] + node * a.q_stride[1] +
+                                                        (kvh * a.G + h) * a.q_stride[2]);
+  const float slope = a.slopes != nullptr ? a.slopes[kvh * a.G + h] * kLog2e : 0.f;
+  const int place = a.depths != nullptr ? a.depths[at + node] : node;
+  for (int x = a.requests[i].y; x < total; ++x) {
+    if (x >= len && !(bits >> (x - len) & 1)) continue;
+    const int page = a.c.page_of(row, x);  // (a missing one is read as zeros)
+    const long long off = page >= 0 ? a.c.token_offset(a.layer, page, kvh, x) : 0;
+    const uint32_t* k = reinterpret_cast<const uint32_t*>(a.c.k + off);
+    float s = 0.f;
+    for (int e = 0; page >= 0 && e < D / 2; ++e) {
+      s = fmaf(to_float<BF16>(q[e] & 0xFFFFu), to_float<BF16>(k[e] & 0xFFFFu), s);
+      s = fmaf(to_float<BF16>(q[e] >> 16), to_float<BF16>(k[e] >> 16), s);
+    }
+    s = a.cap_log2 > 0.f ? fmaf(rcp_fast(exp2_fast(s * a.cap_in * 2.885390043258667f) + 1.f), -2.f * a.cap_log2, a.cap_log2) : s * a.scale_log2;
+    if (a.slopes != nullptr) {
+      const int key = x >= len && a.depths != nullptr ? a.depths[at + x - len] : x - len;
+      s += slope * static_cast<float>(key - place);
+    }
+    if (s > r.m) {
+      const float f = r.m == -INFINITY ? 0.f : exp2_fast(r.m - s);
+      r.m = s;
+      r.l *= f;
+      for (int e = 0; e < 4; ++e) *o[e] *= f;
+    }
+    const float w = s == -INFINITY ? 0.f : exp2_fast(s - (r.m == -INFINITY ? 0.f : r.m));
+    r.l += w;
+    if (page < 0) continue;
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v + off) + 4 * i4;
+    for (int e = 0; e < 4; ++e) {
+      const float f = to_float<BF16>(v[e]);
+      if (nonfinite_mask<BF16>(v[e]) & 0xFFFFu)
+        strange[e] += f;
+      else
+        *o[e] = fmaf(f, w, *o[e]);
+    }
+  }
+  for (int e = 0; e < 4; ++e)
+    if (strange[e] != 0.f) *o[e] = strange[e];  // (NaN compares unequal)
+  return r;
+}
 
 // A thread has four columns of a row, a warp eight rows' (whole lines of the parts).  Rows go by K head, request, node, head.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) join_kernel(const JoinArgs a) {
+// TEAMS of 256 threads take every TEAMS-th part of the block's rows: few rows have many parts.
+template <int D, bool BF16, int TEAMS>
+__global__ void __launch_bounds__(256 * TEAMS) join_kernel(const __grid_constant__ PrefixArgs a) {
   constexpr int kWarps = D / 16;  // that share eight rows
+  __shared__ float sums[TEAMS > 1 ? TEAMS - 1 : 1][6][256];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const long long rr = (static_cast<long long>(blockIdx.x) * (8 / kWarps) + warp / kWarps) * 8 + lane % 8;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % 8, team = threadIdx.x / 256;
+  const int rr = (blockIdx.x * (8 / kWarps) + warp / kWarps) * 8 + lane % 8;  // (at most 2^31 - 1 rows)
   const int i4 = warp % kWarps * 4 + lane / 8;
-  if (rr >= a.rows) return;
-  const int per_head = a.n * a.nodes * a.G;  // (below 2^31 / Hk)
-  const int kvh = static_cast<int>(rr / per_head), in_head = static_cast<int>(rr - static_cast<long long>(kvh) * per_head);
+  const int per_head = a.n * a.nodes * a.G;
+  const bool there = rr < per_head * a.Hk;
+  const int kvh = there ? rr / per_head : 0, in_head = there ? rr - kvh * per_head : 0;
   const int token = in_head / a.G, h = in_head - token * a.G;
   const int i = token / a.nodes, node = token - i * a.nodes;
   const int block = node / a.unit_nodes, in_block = node - block * a.unit_nodes;
-  const Desc own = a.row_units[(i * a.Hk + kvh) * a.row_tiles + block];
-  if (own.parts < 0) return;
-  const int first = a.first_of[i];
-  const int own_parts = max(own.parts, 1), own_ur = in_block * a.G + h;
-  Desc group{0, 0};
-  int group_parts = 0, group_ur = 0;
-  if (first >= 0) {
-    const int mi = (i - first) % a.unit_members;
-    group = a.group_units[((i - mi) * a.Hk + kvh) * a.row_tiles + block];
-    group_parts = max(group.parts, 1);
-    group_ur = (mi * a.unit_nodes + in_block) * a.G + h;
-  }
-  const int parts = group_parts + own_parts;
-  auto row_of = [&](int p) -> long long {
-    if (p < group_parts)
-      return group.parts == 0 ? a.group_rows + rr : static_cast<long long>(2 * (group.cta + p * a.cl) + (p == 0 ? 1 : 0)) * 128 + group_ur;
-    p -= group_parts;
-    return own.parts == 0 ? a.own_rows + rr : static_cast<long long>(2 * (own.cta + p) + (p == 0 ? 1 : 0)) * 128 + own_ur;
+  const int2 request = a.requests[i];
+  auto unit = [&](const Desc* units, int member) { return units[((i - member) * a.Hk + kvh) * a.row_tiles + block]; };
+  // places of a unit's runs: p-th run of `d`, whose rows of this request begin at member `member`
+  auto row_of = [&](const Desc& d, int member, long long whole, int p) -> long long {
+    return d.parts == 0 ? whole + (there ? rr : 0)
+                        : static_cast<long long>(2 * (d.cta + p * d.step) + (p == 0 ? 1 : 0)) * 128 +
+                              (member * a.unit_nodes + in_block) * a.G + h;
   };
+  const int own_member = i % a.unit_members;
+  const Desc own = unit(a.row_units, own_member);
+  const int own_parts = max(own.parts, 1);
+  Desc group{0, 0, 0};
+  int group_member = 0, group_parts = 0;
+  if (request.x >= 0) {
+    group_member = (i - request.x) % a.unit_members;
+    group = unit(a.group_units, group_member);
+    group_parts = max(group.parts, 1);
+  }
   float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = 0; p0 < parts; p0 += 4) {  // four parts' loads at once
-    float2 ml[4];
-    float4 v[4];
-    float mx = M;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool there = p0 + k < parts;
-      const long long row = row_of(there ? p0 + k : p0);
-      ml[k] = a.part_ml[row];
-      v[k] = a.part_o[piece_of<D>(row, i4)];
-      if (!there) ml[k].x = -INFINITY;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, ml[k].x);
-    const float f = M == -INFINITY ? 0.f : part_weight(M - mx);
+  auto add = [&](float m1, float l1, float4 o1) {
+    if (m1 == -INFINITY && l1 == 0.f) return;  // nothing seen
+    const float mx = fmaxf(M, m1);
+    const float f = M == -INFINITY ? 0.f : part_weight(M - mx), w = m1 == -INFINITY ? 1.f : part_weight(m1 - mx);
     M = mx;
-    l *= f;
-    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    l = fmaf(l1, w, l * f);
+    acc.x = fmaf(o1.x, w, acc.x * f);
+    acc.y = fmaf(o1.y, w, acc.y * f);
+    acc.z = fmaf(o1.z, w, acc.z * f);
+    acc.w = fmaf(o1.w, w, acc.w * f);
+  };
+  const int parts = group_parts + own_parts;
+  bool marked = false;
+  for (int p0 = team; p0 < parts; p0 += 4 * TEAMS) {  // four parts' loads at once
+    float4 ml[4], v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (p0 + k >= parts) break;
-      const float w = ml[k].x == -INFINITY ? 0.f : part_weight(ml[k].x - M);
-      l = fmaf(ml[k].y, w, l);
-      acc.x = fmaf(v[k].x, w, acc.x);
-      acc.y = fmaf(v[k].y, w, acc.y);
-      acc.z = fmaf(v[k].z, w, acc.z);
-      acc.w = fmaf(v[k].w, w, acc.w);
+      const int p = min(p0 + k * TEAMS, parts - 1);
+      const long long row = p < group_parts ? row_of(group, group_member, a.group_rows, p)
+                                            : row_of(own, own_member, a.own_rows, p - group_parts);
+      ml[k] = a.part_ml[row];
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (parts > 1 || own.parts > 0) v[k] = a.part_o[piece_of<D>(row, i4)];
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int p = p0 + k * TEAMS;
+      if (p >= parts) break;
+      if (p >= group_parts && (ml[k].z != 0.f || ml[k].w != 0.f)) marked = true;
+      add(ml[k].x, ml[k].y, v[k]);
+    }
+  }
+  if (TEAMS > 1) {  // the teams' sums, in their order
+    const int at = threadIdx.x % 256;
+    if (team > 0) {
+      float(*mine)[256] = sums[team - 1];
+      mine[0][at] = marked ? NAN : M;
+      mine[1][at] = l;
+      mine[2][at] = acc.x;
+      mine[3][at] = acc.y;
+      mine[4][at] = acc.z;
+      mine[5][at] = acc.w;
+    }
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll
+    for (int k = 0; k < TEAMS - 1; ++k) {
+      const float m1 = sums[k][0][at];
+      if (m1 != m1)
+        marked = true;
+      else
+        add(m1, sums[k][1][at], make_float4(sums[k][2][at], sums[k][3][at], sums[k][4][at], sums[k][5][at]));
+    }
+  }
+  if (!there) return;
+  if (request.x < 0 && own.parts == 0 && !marked) return;  // the output is there
+  if (marked) {  // the group's parts again, and this row's own
+    M = -INFINITY;
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < group_parts; ++p) {
+      const long long row = row_of(group, group_member, a.group_rows, p);
+      add(a.part_ml[row].x, a.part_ml[row].y, a.part_o[piece_of<D>(row, i4)]);
+    }
+    const OwnPart r = own_part<D, BF16>(a, i, node, kvh, h, i4);
+    add(r.m, r.l, r.o);
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   const long long orow = static_cast<long long>(token) * a.Hq + kvh * a.G + h;
@@ -991,48 +1212,47 @@ qnre_status_t launch_prefix(const PrefixArgs& a, int sms, cudaStream_t stream) {
   if (ctas < 2 * a.cl) return QNRE_ERR_CUDA;  // both kinds of units need a cluster
   cfg.gridDim = dim3(ctas);
   if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return QNRE_ERR_CUDA;
-  const JoinArgs j{a.first_of, a.row_units, a.group_units, a.part_ml, a.part_o, a.out, a.lse, a.own_rows, a.group_rows,
-                   static_cast<long long>(a.n) * a.nodes * a.Hq, a.n, a.nodes, a.Hq, a.Hk, a.G, a.cl, a.unit_nodes,
-                   a.unit_members, a.row_tiles};
   constexpr int kJoinRows = 1024 / D;  // a block
-  cfg.gridDim = dim3(static_cast<unsigned>((j.rows + kJoinRows - 1) / kJoinRows));
-  cfg.blockDim = dim3(256);
+  const int64_t rows = static_cast<int64_t>(a.n) * a.nodes * a.Hq;
+  const bool few = rows <= kJoinRows * 2 * sms;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
+  cfg.blockDim = dim3(few ? 1024 : 256);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return from_cuda(cudaLaunchKernelEx(&cfg, join_kernel<D, BF16>, j));
+  return from_cuda(few ? cudaLaunchKernelEx(&cfg, join_kernel<D, BF16, 4>, a) : cudaLaunchKernelEx(&cfg, join_kernel<D, BF16, 1>, a));
 }
 
 template <int D, bool BF16>
 qnre_status_t launch_size(const PrefixArgs& a, bool scored, int sms, cudaStream_t stream) {
-  // only D = 128 has a use for the shorter table
-  const bool small = D == 128 && a.n <= kSmall && a.n_groups <= kSmall && a.c.max_blocks * a.c.page_size < kSmallLen;
-  if (small) {
+  // only D = 128 has a use for the short tables
+  const int blocks = (a.n + a.unit_members - 1) / a.unit_members;
+  if (D == 128 && a.n <= kSmallRequests && a.n_groups <= kSmallGroups && blocks <= kSmallBlocks) {
     return scored ? launch_prefix<D, BF16, D == 128, true>(a, sms, stream)
                   : launch_prefix<D, BF16, D == 128, false>(a, sms, stream);
   }
   return scored ? launch_prefix<D, BF16, false, true>(a, sms, stream) : launch_prefix<D, BF16, false, false>(a, sms, stream);
 }
 
-// The workspace: words of requests and units, the parts of the CTAs' runs, and, where rows may share, a place of its own for
-// each row's part of either kind.
+// The workspace: words of requests and units, the parts of the CTAs' runs, and a place of its own for each row's part over
+// its own tokens and, where rows may share, over the common ones.
 struct Layout {
-  uint64_t first_of, row_units, group_units, ml, o, bytes;
+  uint64_t requests, row_units, group_units, ml, o, bytes;
   int64_t own_rows, group_rows;
 };
 
 Layout layout_of(int64_t n, int64_t nodes, int64_t Hq, int64_t Hk, int D, bool groups) {
   const int64_t unit_nodes = std::min<int64_t>(nodes, kTile / (Hq / Hk)), tiles = (nodes + unit_nodes - 1) / unit_nodes;
-  const int64_t slots = 2ll * kMaxCtas * 128, rows = groups ? (n * nodes * Hq + 7) / 8 * 8 : 0;
+  const int64_t slots = 2ll * kMaxCtas * 128, rows = (n * nodes * Hq + 7) / 8 * 8;
   Layout l;
   auto up = [](uint64_t x) { return (x + 15) / 16 * 16; };
-  l.first_of = 0;
-  l.row_units = up(n * 4);
+  l.requests = 0;
+  l.row_units = up(n * sizeof(int2));
   l.group_units = l.row_units + up(n * Hk * tiles * sizeof(Desc));
   l.ml = l.group_units + (groups ? up(n * Hk * tiles * sizeof(Desc)) : 0);
   l.own_rows = slots;
   l.group_rows = slots + rows;
-  l.o = l.ml + (slots + 2 * rows) * 8;
-  l.bytes = l.o + static_cast<uint64_t>(slots + 2 * rows) * D * 4;
+  l.o = l.ml + (slots + (groups ? 2 : 1) * rows) * sizeof(float4);
+  l.bytes = l.o + static_cast<uint64_t>(slots + (groups ? 2 * rows : 0)) * D * 4;
   return l;
 }
 
@@ -1214,12 +1434,13 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
   a.unit_nodes = std::min(nodes, kTile / a.G);
   a.row_tiles = (nodes + a.unit_nodes - 1) / a.unit_nodes;
   a.unit_members = a.row_tiles > 1 ? 1 : std::max(1, kTile / a.G / nodes);
+  a.warp_members = std::max(1, 32 / (a.G * a.unit_nodes));
   // CTAs of a cluster: the units that a group of average size has for a K head
   const int members = n_groups > 0 ? (n + n_groups - 1) / n_groups : 0;
   const int units = (members + a.unit_members - 1) / a.unit_members * a.row_tiles;
   a.cl = std::min(std::max(units, 1), kMaxCluster);
   const int64_t tiles = (static_cast<int64_t>(cache->max_blocks) * cache->page_size + kTile - 1) / kTile + kUnitCost;
-  if (a.n * tiles * a.Hk * a.row_tiles > 0x7FFFFFFF || static_cast<int64_t>(out_rows) > 0x7FFFFFFF) return QNRE_ERR_CAPACITY;
+  if (2 * a.n * tiles * a.Hk * a.row_tiles > 0x7FFFFFFF || static_cast<int64_t>(out_rows) > 0x7FFFFF00) return QNRE_ERR_CAPACITY;
   a.box = std::min(a.cl > 1 ? kTile / kMaxCluster : kTile, cache->page_size & -cache->page_size);
   a.rows = rows;
   a.groups = groups;
@@ -1231,16 +1452,24 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
   a.out = static_cast<char*>(out);
   a.lse = lse;
   char* ws = static_cast<char*>(workspace);
-  a.first_of = reinterpret_cast<int*>(ws + l.first_of);
+  a.requests = reinterpret_cast<int2*>(ws + l.requests);
   a.row_units = reinterpret_cast<Desc*>(ws + l.row_units);
   a.group_units = reinterpret_cast<Desc*>(ws + l.group_units);
-  a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+  a.part_ml = reinterpret_cast<float4*>(ws + l.ml);
   a.part_o = reinterpret_cast<float4*>(ws + l.o);
   a.own_rows = l.own_rows;
   a.group_rows = l.group_rows;
   a.scale_log2 = scale * kLog2e;
   a.cap_log2 = softcap * kLog2e;
-  a.cap_in = softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f;
+  a.cap_in = softcap > 0.f ? scale / softcap : 0.f;
+  constexpr double kNear[4] = {-0.33332598209381104, 0.13313116133213043, -0.05221179127693176, 0.015612608753144741};
+  a.cap_near = 0.6f;
+  double power = 1.0;
+  for (int i = 0; i < 4; ++i) {
+    power *= static_cast<double>(a.cap_in) * a.cap_in;
+    a.cap_poly[i] = static_cast<float>(kNear[i] * power);
+    if (!std::isnormal(a.cap_poly[i])) a.cap_near = -1.f;  // (a cap of a millionth, or of thousands)
+  }
   const bool bf16 = cache->dtype == QNRE_DTYPE_BF16;
   const uint64_t D = cache->head_dim, ps = cache->page_size, H = cache->heads;
   const uint64_t dims[4] = {D, ps, H, static_cast<uint64_t>(cache->layers) * cache->pages};
@@ -1249,10 +1478,11 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
   const uint64_t q_dims[4] = {D, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.nodes), static_cast<uint64_t>(a.n)};
   const uint64_t q_strides[3] = {static_cast<uint64_t>(own.stride[2]) * 2, static_cast<uint64_t>(own.stride[1]) * 2,
                                  static_cast<uint64_t>(own.stride[0]) * 2};
-  uint32_t q_box[4] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.unit_nodes), 1};
-  if (!encode_tiled_16bit(&a.tq_row, own.data, bf16, 4, q_dims, q_strides, q_box)) return QNRE_ERR_CUDA;
-  q_box[3] = static_cast<uint32_t>(a.unit_members);
-  if (!encode_tiled_16bit(&a.tq_group, own.data, bf16, 4, q_dims, q_strides, q_box) ||
+  const uint32_t q_box[4] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.unit_nodes),
+                             static_cast<uint32_t>(a.unit_members)};
+  a.q = static_cast<const char*>(own.data);
+  for (int i = 0; i < 3; ++i) a.q_stride[i] = own.stride[i] * 2;
+  if (!encode_tiled_16bit(&a.tq, own.data, bf16, 4, q_dims, q_strides, q_box) ||
       !encode_tiled_16bit(&a.tk, cache->k, bf16, 4, dims, strides, box) ||
       !encode_tiled_16bit(&a.tv, cache->v, bf16, 4, dims, strides, box))
     return QNRE_ERR_CUDA;
