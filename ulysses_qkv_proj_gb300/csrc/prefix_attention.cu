@@ -72,12 +72,13 @@ struct PrefixArgs {
   float4* part_o;     // the same rows of D, laid out by piece_of
   long long own_rows, group_rows;  // where the rows' own places begin, for each kind
   float scale_log2, cap_in, cap_log2;  // capped: scale / cap, cap log2(e)
-  float cap_near, cap_poly[4];         // the nearer polynomial of run_softmax in powers of q.k, and up to where it serves
+  float cap_near, cap_poly[3];         // the nearer polynomial of run_softmax in powers of q.k, and up to where it serves
   const char* q;
   long long q_stride[3];  // bytes
   int layer, n, n_groups, nodes, Hq, Hk, G, box, cl;
   int unit_nodes, unit_members, row_tiles;  // nodes and requests of a unit; units that one request's nodes take
   int warp_members;                         // requests whose rows one warp has
+  bool backward;  // tiles from the last to the first: where the bias favours near tokens the maxima do not grow tile by tile
 };
 
 // Eight rows' pieces of 16 bytes lie side by side, so that the threads that write, a row each, fill whole lines.
@@ -204,6 +205,7 @@ struct Walk {
   const int *bases, *lens;
   const uint8_t* drafts;  // from the unit's first request on
 
+  __device__ __forceinline__ int position(bool backward) const { return base + (backward ? tiles - 1 - tile : tile) * kTile; }
   __device__ __forceinline__ void enter() {
     base = bases[mi];
     len = lens[mi];
@@ -232,6 +234,8 @@ struct Walk {
     next_request();
   }
 };
+
+__device__ __forceinline__ int group_position(const Seg& s, int t, bool backward) { return (backward ? s.tiles - 1 - t : t) * kTile; }
 
 // What row `ur` of a unit stands for.
 struct UnitRow {
@@ -303,11 +307,11 @@ __device__ void run_producer(const PrefixArgs& a, const Bars& bars, uint32_t sme
     };
     if (s.group) {
       enter(s.start);
-      pos = s.t0 * kTile + chunk * a.box;
+      pos = group_position(s, s.t0, a.backward) + chunk * a.box;
       end = s.tokens;
     } else {
       enter(s.start + walk.mi);
-      pos = walk.base + walk.tile * kTile + chunk * a.box;
+      pos = walk.position(a.backward) + chunk * a.box;
       end = walk.total;
     }
     look();
@@ -317,11 +321,11 @@ __device__ void run_producer(const PrefixArgs& a, const Bars& bars, uint32_t sme
       const int page = there ? a.layer * a.c.pages + entry : none, at = off;
       if (t + 1 < s.t1) {  // the next tile's entry is on its way while this tile's place is waited for
         if (s.group) {
-          pos += kTile;
+          pos = group_position(s, t + 1, a.backward) + chunk * a.box;
         } else {
           walk.next();
           enter(s.start + walk.mi);
-          pos = walk.base + walk.tile * kTile + chunk * a.box;
+          pos = walk.position(a.backward) + chunk * a.box;
           end = walk.total;
         }
         look();
@@ -490,12 +494,12 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
     float m = -INFINITY, l = 0.f;
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
-      int pos0 = t * kTile, len = s.tokens, total = s.tokens, member = 0;
+      int pos0 = group_position(s, t, a.backward), len = s.tokens, total = s.tokens, member = 0;
       int filled = (total + a.box - 1) & -a.box;  // TMA has zeroed V from here on
       bool mine = true;  // a row that sees this tile
       if (!s.group) {
         member = walk.mi;
-        pos0 = walk.base + walk.tile * kTile;
+        pos0 = walk.position(a.backward);
         len = walk.len;
         total = walk.total;
         filled = walk.base + ((total - walk.base + a.box - 1) & -a.box);
@@ -521,18 +525,23 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bars.sfree + 8 * b);
 
+        float offset = 0.f;  // (SCORED) of the first eight columns; the next ones' lie 8 slopes apart
         if (SCORED) {
-          // c tanh(x / c) = x + x (x / c)^2 P: the odd polynomial P is fitted by least squares up to 0.6 (8e-8 relative) and up
-          // to 1 (6e-8); beyond, for a warp that holds any such score, 1 - 2 / (1 + e^2z): to 2^-22 of the cap, however large.
+          // c tanh(x / c) = x + x (x / c)^2 P: the polynomial P is fitted by least squares up to 0.35 (4e-8 relative) and up to
+          // 1 (6e-8); beyond, for a warp that holds any such score, 1 - 2 / (1 + e^2z): to 2^-22 of the cap, however large.
+          // The distance bias of a column is slope (i % 8), added here, and its eight columns' offset, added to their maximum and
+          // with the row's maximum before the exponential.
           const int d0 = pos0 + c0;
-          const float at0 = SCORED && a.slopes != nullptr ? row.slope * static_cast<float>(d0 - row.place) : 0.f;
-          const uint64_t start2 = pair(at0, at0);
+          uint64_t within[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) within[i] = pair(row.slope * (2 * i), row.slope * (2 * i + 1));
+          offset = a.slopes != nullptr ? row.slope * static_cast<float>(d0 - row.place) : 0.f;
           auto each_pair = [&](auto f) {
 #pragma unroll
             for (int i = 0; i < kCols; i += 2) {
               uint32_t *x0 = &v[i / 32][i % 32], *x1 = &v[i / 32][(i + 1) % 32];
               float y0, y1;
-              unpair(f(pair(__uint_as_float(*x0), __uint_as_float(*x1))), y0, y1);
+              unpair(f(pair(__uint_as_float(*x0), __uint_as_float(*x1)), within[i / 2 % 4]), y0, y1);
               *x0 = __float_as_uint(y0);
               *x1 = __float_as_uint(y1);
             }
@@ -549,45 +558,48 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
           }
           auto both = [](float x) { return pair(x, x); };
           if (a.cap_log2 <= 0.f) {
-            each_pair([&](uint64_t x) { return fma2(x, scale2, start2); });
+            each_pair([&](uint64_t x, uint64_t bias) { return fma2(x, scale2, bias); });
           } else if (!__any_sync(0xFFFFFFFFu, most > a.cap_near)) {
-            const uint64_t k0 = both(a.cap_poly[0]), k1 = both(a.cap_poly[1]), k2 = both(a.cap_poly[2]), k3 = both(a.cap_poly[3]);
-            each_pair([&](uint64_t x) {
-              const uint64_t y = fma2(x, scale2, 0), z = fma2(x, x, 0);
-              return fma2(y, fma2(z, fma2(z, fma2(z, fma2(z, k3, k2), k1), k0), 0), fma2(x, scale2, start2));
-            });
+            const uint64_t k0 = both(a.cap_poly[0]), k1 = both(a.cap_poly[1]), k2 = both(a.cap_poly[2]);
+            auto near = [&](uint64_t y, uint64_t z, uint64_t lead) {
+              return fma2(y, fma2(z, fma2(z, fma2(z, k2, k1), k0), 0), lead);
+            };
+            if (a.slopes == nullptr)
+              each_pair([&](uint64_t x, uint64_t) {
+                const uint64_t y = fma2(x, scale2, 0);
+                return near(y, fma2(x, x, 0), y);
+              });
+            else
+              each_pair([&](uint64_t x, uint64_t bias) {
+                return near(fma2(x, scale2, 0), fma2(x, x, 0), fma2(x, scale2, bias));
+              });
           } else if (!__any_sync(0xFFFFFFFFu, most > 1.f)) {
             const uint64_t in2 = both(a.cap_in);
-            each_pair([&](uint64_t x) {
+            each_pair([&](uint64_t x, uint64_t bias) {
               const uint64_t y = fma2(x, scale2, 0), t = fma2(x, in2, 0), z = fma2(t, t, 0);
               uint64_t k = fma2(z, both(0.0010582602117210627f), both(-0.006259326823055744f));
               k = fma2(z, k, both(0.020359747111797333f));
               k = fma2(z, k, both(-0.05349870026111603f));
               k = fma2(z, k, both(0.13326409459114075f));
               k = fma2(z, k, both(-0.33332985639572144f));
-              return fma2(y, fma2(z, k, 0), fma2(x, scale2, start2));
+              return fma2(y, fma2(z, k, 0), fma2(x, scale2, bias));
             });
           } else {
 #pragma unroll
             for (int i = 0; i < kCols; ++i) {
               const float e = exp2_fast(__uint_as_float(v[i / 32][i % 32]) * a.cap_in * 2.885390043258667f);  // 2 log2(e)
-              v[i / 32][i % 32] = __float_as_uint(fmaf(rcp_fast(e + 1.f), -2.f * a.cap_log2, a.cap_log2 + at0));
+              v[i / 32][i % 32] = __float_as_uint(fmaf(rcp_fast(e + 1.f), -2.f * a.cap_log2, a.cap_log2 + row.slope * (i % 8)));
             }
           }
-          if (a.slopes != nullptr) {
-#pragma unroll
-            for (int i = 1; i < kCols; ++i)
-              v[i / 32][i % 32] = __float_as_uint(fmaf(row.slope, static_cast<float>(i), __uint_as_float(v[i / 32][i % 32])));
-            if (tail && a.depths != nullptr && !s.group) {  // a draft lies at its depth, not at its slot
-              const int32_t* depths = a.depths + static_cast<long long>(s.start + member) * a.nodes;
+          if (tail && a.slopes != nullptr && a.depths != nullptr && !s.group) {  // a draft lies at its depth, not at its slot
+            const int32_t* depths = a.depths + static_cast<long long>(s.start + member) * a.nodes;
 #pragma unroll 1
-              for (int j = max(len - d0, 0); j < min(total - d0, kCols); ++j) {
-                const int node = d0 + j - len;
-                const float off = row.slope * static_cast<float>(depths[node] - node);
+            for (int j = max(len - d0, 0); j < min(total - d0, kCols); ++j) {
+              const int node = d0 + j - len;
+              const float off = row.slope * static_cast<float>(depths[node] - node);
 #pragma unroll
-                for (int i = 0; i < kCols; ++i)
-                  if (i == j) v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) + off);
-              }
+              for (int i = 0; i < kCols; ++i)
+                if (i == j) v[i / 32][i % 32] = __float_as_uint(__uint_as_float(v[i / 32][i % 32]) + off);
             }
           }
         }
@@ -604,12 +616,17 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
         }
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < kCols / 32; ++j)
+        for (int k = 0; k < kCols / 8; ++k) {
+          const uint32_t* x = &v[k / 4][k % 4 * 8];
+          float m0 = SCORED ? -INFINITY : mx0, m1 = SCORED ? -INFINITY : mx1;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            mx0 = max3(mx0, __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
-            mx1 = max3(mx1, __uint_as_float(v[j][i + 2]), __uint_as_float(v[j][i + 3]));
+          for (int i = 0; i < 8; i += 4) {
+            m0 = max3(m0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            m1 = max3(m1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
           }
+          mx0 = SCORED ? fmaxf(mx0, fmaxf(m0, m1) + fmaf(row.slope, 8.f * k, offset)) : m0;
+          mx1 = SCORED ? mx1 : m1;
+        }
         float mx = fmaxf(mx0, mx1) * (SCORED ? 1.f : a.scale_log2);
         {  // with the other half's (two buffers: one is written again only when its tile's product is done)
           float* at = ml + (L::kMlBuffers == 2 ? b * 256 : 0) + ur;
@@ -643,12 +660,16 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
         if (grow) m = mx;
         // (a row that does not see the tile gets zeros; what is not finite in its scores marks it, as in V)
         const float ms = mine ? (m == -INFINITY ? 0.f : m) : INFINITY;
-        const uint64_t neg = pair(-ms, -ms);
+        uint64_t neg = pair(-ms, -ms);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < kCols / 2; ++i) {
           float e0, e1;
           const uint64_t x = pair(__uint_as_float(v[i / 16][(2 * i) % 32]), __uint_as_float(v[i / 16][(2 * i + 1) % 32]));
+          if (SCORED && i % 4 == 0) {
+            const float off = fmaf(row.slope, 2.f * i, offset) - ms;
+            neg = pair(off, off);
+          }
           unpair(SCORED ? add2(x, neg) : fma2(x, scale2, neg), e0, e1);
           e0 = exp2_fast(e0);
           e1 = exp2_fast(e1);
@@ -736,8 +757,9 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
       if (!s.group) {
         mark |= strange;
       } else if (__any_sync(0xFFFFFFFFu, strange)) {
-        const Kinds k = search_context<BF16>(a.c, a.layer, a.rows[s.start], s.kvh, s.t0 * kTile,
-                                             min(s.t1 * kTile, s.tokens), c);
+        const int from = a.backward ? s.tiles - s.t1 : s.t0;
+        const Kinds k = search_context<BF16>(a.c, a.layer, a.rows[s.start], s.kvh, from * kTile,
+                                             min((from + s.t1 - s.t0) * kTile, s.tokens), c);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const uint32_t bit = 1u << i;
@@ -917,12 +939,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   const int clusters = static_cast<int>(gridDim.x) / a.cl;
   int for_wide = 0;
   if (W_wide > 0) {
-    const float wide = static_cast<float>(W_wide) * a.cl;
-    const int low = static_cast<int>(clusters * (wide / (wide + W_single)));
+    // (a single CTA's tile takes a fifth longer: masks, cleaning, and its units' ends come more often)
+    const float wide = static_cast<float>(W_wide) * a.cl, single = 1.2f * static_cast<float>(W_single);
+    const int low = static_cast<int>(clusters * (wide / (wide + single)));
     auto longest = [&](int c) {
       return c < 1 || c >= clusters ? 3e38f
                                     : fmaxf(static_cast<float>(W_wide) / c,
-                                            static_cast<float>(W_single) / static_cast<float>((clusters - c) * a.cl));
+                                            single / static_cast<float>((clusters - c) * a.cl));
     };
     for_wide = longest(low) <= longest(low + 1) ? low : low + 1;
     for_wide = min(max(for_wide, 1), clusters - 1);
@@ -1449,6 +1472,7 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
   a.depths = depths;
   a.mask = mask;
   a.slopes = slopes;
+  a.backward = slopes != nullptr;
   a.out = static_cast<char*>(out);
   a.lse = lse;
   char* ws = static_cast<char*>(workspace);
@@ -1462,10 +1486,10 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
   a.scale_log2 = scale * kLog2e;
   a.cap_log2 = softcap * kLog2e;
   a.cap_in = softcap > 0.f ? scale / softcap : 0.f;
-  constexpr double kNear[4] = {-0.33332598209381104, 0.13313116133213043, -0.05221179127693176, 0.015612608753144741};
-  a.cap_near = 0.6f;
+  constexpr double kNear[3] = {-0.33332663774490356, 0.1329982578754425, -0.04914848133921623};
+  a.cap_near = 0.35f;
   double power = 1.0;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 3; ++i) {
     power *= static_cast<double>(a.cap_in) * a.cap_in;
     a.cap_poly[i] = static_cast<float>(kNear[i] * power);
     if (!std::isnormal(a.cap_poly[i])) a.cap_near = -1.f;  // (a cap of a millionth, or of thousands)
