@@ -743,7 +743,7 @@ qnre_status_t qnre_tree_masks(const int32_t* parents, int n, int nodes, uint64_t
  * reads a prompt's pages once for all rows that share them, sampling from logits.
  * ------------------------------------------------------------------------ */
 
-#define QNRE_MAX_VOCAB 786432 /* logits of a row that qnre_sample and qnre_filter_probs serve */
+#define QNRE_MAX_VOCAB 1048576 /* logits of a row that qnre_sample and qnre_filter_probs serve */
 
 /* How qnre_rope_table scales rotary frequencies f_i = theta^(-2 i / rot). */
 typedef enum {
@@ -827,14 +827,14 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
  *
  * T <= 0 (or NaN): the lowest x of the largest logit.  Off: top_k <= 0 or >= vocab, top_p >= 1 (or NaN),
  * min_p <= 0 (or NaN).  A logit of -inf or NaN is never drawn; where there is no other the token is -1.  A logit of +inf
- * leaves only such ones.  u below 0 (or NaN) counts as 0, from 1 on it draws the last token that is left.
+ * counts as the largest finite float.  u below 0 (or NaN) counts as 0, from 1 on it draws the last token that is left.
  *
  *   logits   device bf16, fp16 or fp32 (dtype), row i at base + i*stride elements, vocab values each.
  *   temperature, top_p, min_p  device fp32 [n] or NULL (1, off, off);  top_k  device int32 [n] or NULL (off).
  *   u        device fp32 [n], in [0, 1).      tokens  device int32 [n].
  * 1 <= vocab <= QNRE_MAX_VOCAB, n <= 2^20.  n == 0 is an empty call.
- * Weights are formed to 2^-42 and summed as integers, so that tokens agree with a 64-bit evaluation except where a
- * number lies within about 1e-12 of a border, and do not depend on timing.
+ * Weights are formed to 2^-30 and summed as integers, so that tokens agree with a 64-bit evaluation except where a
+ * number lies within about 1e-10 of a border, and do not depend on timing.
  *
  * qnre_filter_probs -- the same settings as probabilities: w_x over the sum of the weights left, 0 for the
  *   rest (one 1 for T <= 0; a row without any token is all 0), as qnre_verify_tree takes them.

@@ -904,7 +904,7 @@ def qnre_verify_tree(target_probs, draft_probs, tokens, parents, accept_u, sampl
 # ---------------------------------------------------------------------------
 # Many answers from one prompt
 # ---------------------------------------------------------------------------
-MAX_VOCAB = 786432
+MAX_VOCAB = 1048576
 
 
 def qnre_rope_table(cos_sin, theta: float = 1e4, first: int = 0, scaling: str = "none", factor: float = 1.0,

@@ -4,23 +4,25 @@
 //   kept: w_x >= min_p; of those the top_k first; of those the ones before which less than top_p of their weight lies
 //   token = lowest x whose running sum of kept weights (by index) exceeds u times their total
 //
-// A cluster of up to 16 CTAs takes one row and holds it in shared memory, so a row is read from HBM once whatever
-// passes follow.  Nothing is sorted but the few tokens around a cut:
+// A cluster of up to 16 CTAs takes one row.  Few rows are held in its shared memory (KEEP), so that the passes that follow cost
+// little latency; with many rows a CTA's share is longer, and the passes read it again, from L2 as far as it reaches.  Nothing is
+// sorted but the few tokens around a cut:
 //
 //   max        while the row arrives; every CTA learns it through the cluster's shared memory,
-//   histogram  counts over 4096 bins of (max - l) / T, which orders tokens coarsely; each CTA adds up its share of the
-//              bins over the cluster.  The bin of the top_k-th token is exact from the counts.  For top_p the counts
-//              bound the weight above each bin from both sides (a bin spans a factor e^(1/256)), so the tokens that the
-//              cut can fall on lie in a window of a few bins,
-//   cut        the tokens of that bin or window go to the first CTA's list, which sorts them and finds the last one kept;
-//              lists that overflow (ties, logits out of the bins' range) are cut by four rounds of eight key bits,
+//   histogram  counts over 4096 bins of log2(e) (max - l) / T, 1/128 wide, which orders tokens coarsely; each CTA adds up its
+//              share of the bins over the cluster.  The bin of the top_k-th token is exact from the counts.  For top_p
+//              the counts bound the weight above each bin, and the one behind it, from both sides (a bin spans 0.54 %), so
+//              the cut falls into one of a few bins, whose weights are then added up exactly,
+//   cut        the tokens of the one bin go to the first CTA, which sorts them and finds the last one kept; bins of more
+//              than 1024 (ties, logits beyond the bins' range) are cut by four rounds of eight key bits,
 //   draw       the kept weight by warps' runs of places; the run that holds the number is added up place by place.
 //
 // Numbers.  A token is right only if no sum is wrong by more than its distance from a border, and with 10^5 borders
-// 32-bit sums would miss one draw in a hundred.  So weights are integers of 2^-(63 - ceil log2 V) of the largest: the
-// exponent is formed as a pair of floats, its leading ten binary places taken from a table of 2^(-j/1024) and the rest by
-// a cubic (Weight; 2^-42 relative at worst, 2^-44 near the largest, 40 instructions, where fp64 runs at a 64th of the rate).  Integer sums
-// do not depend on their order, so counters and lists filled in any order change no result.
+// 32-bit sums would miss one draw in a hundred.  So weights are integers of 2^-(62 - ceil log2 V) of the largest with 31 leading
+// bits of their own: the exponent is formed as a pair of floats, its leading ten binary places taken from a table of
+// 2^(-j/1024) and the rest by a cubic (Weight; 2^-30 relative at worst, and sums of V of them far closer, as their errors are
+// independent; about 40 instructions, none of them a conversion or 64 bits wide but the last).  Integer sums do not depend
+// on their order, so counters and lists filled in any order change no result.
 #include "../../include/qnre.h"
 #include "api_util.cuh"
 #include "ptx.cuh"
@@ -45,14 +47,14 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kGrain = kWarps * 128;     // places of a CTA come in multiples of this: a float4 a lane, warp by warp
 constexpr int kBins = 4096;
-constexpr float kRange = 16.f;           // (max - l) / T that the bins cover; the last holds all beyond
+constexpr int kBinShift = 3;             // a bin is 2^3 steps of 2^-10 in log2; the last holds all beyond 32
 constexpr int kList = 1024;
-constexpr int kMaxSlice = 49152;         // places of a CTA
-static_assert(kMaxSlice * kMaxCluster == QNRE_MAX_VOCAB, "the largest row");
+constexpr int kWindow = 16;              // bins that a cut by weight is sought in
+constexpr int kResident = 152 * 4;       // CTAs that the machine about holds at once
+constexpr int kKeepSlice = 12288;        // places of a CTA that it holds in shared memory (two or three such CTAs a SM)
 constexpr int kMassBits = 40;            // of the histogram's bounds on weights
-constexpr int kFixedBytes = kBins * 4 + kList * 8 + 3 * 256 * 4;  // shared memory before the row
+constexpr int kFixedBytes = kBins * 4 + 2 * kList * 8 + 3 * 256 * 4;  // shared memory before the row
 constexpr double kLog2e = 1.4426950408889634074;
-constexpr float kBinLog2 = kRange * 1.44269504f / kBins;  // a bin's span in powers of two
 
 struct SampleArgs {
   const void* logits;
@@ -61,12 +63,16 @@ struct SampleArgs {
   const int32_t* top_k;
   int32_t* tokens;
   float* probs;
-  int rows_per, vocab, slice, scale;  // rows of a request; places of a CTA; binary places of a weight
+  int rows_per, vocab, slice, up;  // rows of a request; places of a CTA; binary places of a weight beyond 31
 };
 
-// 2^(-j/1024) in units of 2^-63, from 2^(-i/32) and 2^(-i/1024).
+// 2^(-j/1024) in units of 2^-31, as an integer and as a float, from 2^(-i/32) and 2^(-i/1024).
+struct Power {
+  uint32_t bits;
+  float value;
+};
 struct PowerTable {
-  uint64_t at[1024];
+  Power at[1024];
 };
 constexpr uint64_t kCoarse[32] = {
     0x8000000000000000ull, 0x7D41D96DB915019Dull, 0x7A92BE8A92436616ull, 0x77F25CCDEE6D7AE6ull,
@@ -94,7 +100,11 @@ constexpr uint64_t product63(uint64_t a, uint64_t b) {  // a b 2^-63, rounded
 }
 constexpr PowerTable make_powers() {
   PowerTable t{};
-  for (int j = 0; j < 1024; ++j) t.at[j] = product63(kCoarse[j / 32], kFine[j % 32]);
+  for (int j = 0; j < 1024; ++j) {
+    const uint64_t x = product63(kCoarse[j / 32], kFine[j % 32]);
+    t.at[j].bits = static_cast<uint32_t>((x + (1ull << 31)) >> 32);
+    t.at[j].value = static_cast<float>(t.at[j].bits);
+  }
   return t;
 }
 __device__ const PowerTable kPowers = make_powers();
@@ -102,37 +112,38 @@ __device__ const PowerTable kPowers = make_powers();
 // A row's scale: weights are 2^(-y), y = (max - l) c, c = log2(e) / T as a pair of floats.
 struct Weight {
   float max, ch, cl;
+  static constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
+  static constexpr float kLimit = 4095.f;
 
-  // y = whole + fraction; false where the weight is below 2^-`limit`.  The value is mantissa 2^-(63 + whole).
-  __device__ __forceinline__ bool operator()(float l, float limit, uint64_t& mantissa, int& whole) const {
-    mantissa = 1ull << 63;
-    whole = 0;
-    if (l == max) return true;
-    const float d = max - l, back = d - max, err = (max - (d - back)) - (l + back);  // d + err = max - l
-    const float p = d * ch;
-    if (!(p < limit)) return false;  // (NaN, too: an infinite distance times c = 0)
-    const float e = fmaf(d, ch, -p) + fmaf(d, cl, err * ch);
-    whole = static_cast<int>(p);
-    const float places = (p - static_cast<float>(whole)) * 8388608.f;  // of 2^-23
-    const int lead = static_cast<int>(places);
-    const float rest = (places - static_cast<float>(lead)) + e * 8388608.f;
-    // y mod 2^-10: 13 of those places and the rest, which may be a little below 0 or above 1
-    const int low = lead & 8191, part = __float2int_rn(rest * 16777216.f);                     // 2^-23, 2^-47
-    const float t = (static_cast<float>(low) + rest) * 8.262958294867817e-08f;                 // ln 2 2^-23
-    const int curve = __float2int_rn(t * t * fmaf(t, -0.16666667f, 0.5f) * 140737488355328.f);  // t^2/2 - t^3/6, 2^-47
-    // 1 - e^-t in units of 2^-64, with ln 2 to 2^-41 of a place of 2^-23 and to 2^-31 of the rest
-    const long long loss = low * 1524246769572ll + (static_cast<long long>(part) * 1488522236 >> 14) - (static_cast<long long>(curve) << 17);
-    const uint64_t power = __ldg(&kPowers.at[lead >> 13]);
-    mantissa = loss >= 0 ? power - __umul64hi(power, static_cast<uint64_t>(loss))
-                         : power + __umul64hi(power, static_cast<uint64_t>(-loss));
-    return true;
+  // y in steps of 2^-10, rounded (ordered as the logits are); y itself stays in p, without its last places.
+  __device__ __forceinline__ int steps(float l, float& p) const {
+    p = fminf(fminf(max - l, 3.4028234664e38f) * ch, kLimit);
+    return __float_as_int(fmaf(p, 1024.f, kMagic)) - __float_as_int(kMagic);
   }
-  __device__ __forceinline__ uint64_t fixed(float l, int scale) const {
-    uint64_t m;
-    int whole;
-    if (!(*this)(l, 64.f, m, whole)) return 0;
-    const int shift = whole + 63 - scale;
-    return shift > 63 ? 0 : (m + (1ull << (shift - 1))) >> shift;
+  __device__ __forceinline__ int bin(float l) const {
+    float p;
+    return min(steps(l, p) >> kBinShift, kBins - 1);
+  }
+  // 2^-y = m 2^-(31 + n)
+  __device__ __forceinline__ uint32_t operator()(float l, int& n) const {
+    float p;
+    const int k = steps(l, p);
+    const float d = max - l, back = d - max, err = (max - (d - back)) - (l + back);  // d + err = max - l
+    const float e = fmaf(d, ch, -p) + fmaf(d, cl, err * ch);                          // y = p + e
+    const float r = fmaf(e, 1024.f, fmaf(p, 1024.f, static_cast<float>(-k)));         // behind the steps
+    const float t = r * 0.00067690154f;                                               // ln 2 / 1024
+    const float c = t * fmaf(t, fmaf(t, -0.16666667f, 0.5f), -1.f);                   // e^-t - 1
+    const Power power = kPowers.at[k & 1023];
+    n = k >> 10;
+    return power.bits + (__float_as_int(fmaf(power.value, c, kMagic)) - __float_as_int(kMagic));
+  }
+  // In units of 2^-scale, scale = 31 + `up`.
+  __device__ __forceinline__ uint64_t fixed(float l, int up) const {
+    int n;
+    const uint32_t m = (*this)(l, n);
+    if (n <= up) return static_cast<uint64_t>(m) << (up - n);
+    const int down = n - up;
+    return down > 31 ? 0 : (m + (1u << (down - 1))) >> down;
   }
 };
 
@@ -145,11 +156,11 @@ __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// What a row keeps: larger keys than `key`, and of that key the tokens up to `last`.
+// What a row keeps: larger logits than `least`, and of that the tokens up to `last`.
 struct Cut {
-  uint32_t key;
+  float least;
   int last;
-  __device__ __forceinline__ bool keeps(uint32_t k, int index) const { return k > key || (k == key && index <= last); }
+  __device__ __forceinline__ bool keeps(float l, int index) const { return l > least || (l == least && index <= last); }
 };
 
 struct Shared {
@@ -159,8 +170,9 @@ struct Shared {
   float max[kMaxCluster];
   uint64_t before;                   // what lies before the first bin found
   Cut cut;
-  uint32_t list_count;
-  int bin[2], tie, low, high;
+  uint32_t window[3][kWindow];       // of these bins: tokens, weights' low and high words
+  uint32_t put_count, list_count;
+  int bin[4], tie, low, high;
 };
 
 template <typename T>
@@ -187,11 +199,6 @@ __device__ __forceinline__ void remote_store(void* p, uint32_t rank, uint32_t v)
 __device__ __forceinline__ void remote_store64(void* p, uint32_t rank, uint64_t v) {
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(in_cta(p, rank)), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t remote_add(uint32_t* p, uint32_t rank, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(in_cta(p, rank)), "r"(v) : "memory");
-  return old;
-}
 __device__ __forceinline__ void remote_min(int* p, uint32_t rank, int v) {
   asm volatile("red.shared::cluster.min.s32 [%0], %1;" ::"r"(in_cta(p, rank)), "r"(v) : "memory");
 }
@@ -212,15 +219,18 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v) {  // inclusive
 }
 
 // One row, as this CTA of its cluster sees it.
+template <typename T, bool KEEP>
 struct Row {
+  static constexpr int kVec = 16 / sizeof(T);
   Shared& sh;
   uint32_t* hist;    // [kBins]
-  uint64_t* list;    // [kList]: (~key, index); the first CTA's
+  uint64_t* own;     // [kList]: tokens that this CTA put there, as (~key, index)
+  uint64_t* list;    // [kList]: those of one bin from all CTAs; the first CTA's
   uint32_t* rounds;  // [3][256]: counts, weights' low and high words
-  float* logit;      // [slice]
+  float* logit;      // [slice] (KEEP)
+  const T* src;      // the row
   uint32_t ncta, rank;
-  int place0, shift, run, scale;  // places are index + shift; `run` of them to a warp, in order
-  float bin_scale;
+  int place0, shift, end, run, up;  // places are index + shift, up to end; `run` of them to a warp, in order
   Weight weight;
   Cut cut;
   unsigned uses;
@@ -228,27 +238,64 @@ struct Row {
   __device__ __forceinline__ static int warp() { return threadIdx.x / 32; }
   __device__ __forceinline__ static int lane() { return threadIdx.x % 32; }
 
-  __device__ __forceinline__ uint64_t weigh(float l) const { return weight.fixed(l, scale); }
-  __device__ __forceinline__ int bin_of(float l) const {
-    return min(static_cast<int>((weight.max - l) * bin_scale), kBins - 1);
+  __device__ __forceinline__ uint64_t weigh(float l) const { return weight.fixed(l, up); }
+
+  // Eight or four logits from place `place` on (a 16-byte boundary); what is no logit of the row, or NaN, as -inf.
+  __device__ __forceinline__ void load(int place, float (&v)[kVec]) const {
+    if (place >= shift && place + kVec <= end) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + (place - shift)));
+      const T* t = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[i] = to_float(t[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        v[i] = place + i >= shift && place + i < end ? to_float(src[place + i - shift]) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = v[i] != v[i] ? -INFINITY : fminf(v[i], 3.4028234664e38f);
+  }
+  __device__ __forceinline__ float at(int y) const {  // place y of this CTA
+    if (KEEP) return logit[y];
+    const int place = place0 + y;
+    const float v = place >= shift && place < end ? to_float(src[place - shift]) : -INFINITY;
+    return v != v ? -INFINITY : fminf(v, 3.4028234664e38f);
   }
 
   // f(logit, index) for every place of this warp's run.
   template <typename F>
   __device__ __forceinline__ void sweep(F f) const {
-    for (int y = warp() * run + lane() * 4; y < (warp() + 1) * run; y += 128) {
-      const float4 v = *reinterpret_cast<const float4*>(logit + y);
-      const int index = place0 + y - shift;
-      f(v.x, index);
-      f(v.y, index + 1);
-      f(v.z, index + 2);
-      f(v.w, index + 3);
+    const int from = warp() * run, to = from + run;
+    if (KEEP) {
+      for (int y = from + lane() * 4; y < to; y += 128) {
+        const float4 v = *reinterpret_cast<const float4*>(logit + y);
+        const int index = place0 + y - shift;
+        f(v.x, index);
+        f(v.y, index + 1);
+        f(v.z, index + 2);
+        f(v.w, index + 3);
+      }
+    } else {
+      constexpr int kAhead = 16 / kVec;  // 16 logits of a lane on their way at a time
+      for (int y0 = from + lane() * kVec; y0 < to; y0 += 32 * kVec * kAhead) {
+        float v[kAhead][kVec];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (y0 + 32 * kVec * k < to) load(place0 + y0 + 32 * kVec * k, v[k]);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (y0 + 32 * kVec * k < to) {
+            const int index = place0 + y0 + 32 * kVec * k - shift;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) f(v[k][i], index + i);
+          }
+      }
     }
   }
   template <typename F>
   __device__ __forceinline__ void sweep_kept(F f) const {
     sweep([&](float l, int index) {
-      if (cut.keeps(key_of(l), index)) f(l, index);
+      if (cut.keeps(l, index)) f(l, index);
     });
   }
 
@@ -293,10 +340,13 @@ struct Row {
     return t;
   }
 
-  // sh.bin[0], sh.bin[1]: the first bins whose running sums of f(bin).x and .y reach the targets (the last bin where
-  // none does), sh.before the sum of x before the first.  Bins lie in the CTAs' histograms by equal shares.  Returns the sums.
-  template <typename F>
-  __device__ Pair find_bins(F f, uint64_t target_x, uint64_t target_y) {
+  // sh.bin[i]: the first bins whose running sums of f(bin) reach targets[i] (x for the even i, y for the odd; the last bin where
+  // none does); sh.before what lies before the first of them in x, sh.high its own x.  Targets come from the totals.
+  struct Targets {
+    uint64_t at[4];
+  };
+  template <typename F, typename G>
+  __device__ Pair find_bins(F f, G targets_of) {
     const int share = kBins / ncta, per = share / kThreads, b0 = rank * share + threadIdx.x * per;
     Pair own{0, 0};
     for (int i = 0; i < per; ++i) {
@@ -304,7 +354,7 @@ struct Row {
       own.x += v.x;
       own.y += v.y;
     }
-    if (threadIdx.x == 0) sh.bin[0] = sh.bin[1] = kBins - 1;
+    if (threadIdx.x < 4) sh.bin[threadIdx.x] = kBins - 1;
     const uint64_t sx = warp_scan(own.x), sy = warp_scan(own.y);
     const Pair all = exchange(own.x, own.y);
     Pair before = before_cta();
@@ -314,22 +364,28 @@ struct Row {
       before.x += sh.warp[0][i];
       before.y += sh.warp[1][i];
     }
-    const bool here_x = before.x < target_x && before.x + own.x >= target_x;
-    const bool here_y = before.y < target_y && before.y + own.y >= target_y;
-    if (here_x || here_y) {
-      bool seek_x = here_x, seek_y = here_y;
-      for (int i = 0; i < per; ++i) {
-        const Pair v = f(b0 + i);
-        if (seek_x && before.x + v.x >= target_x) {
-          seek_x = false;
+    const Targets t = targets_of(all);
+    uint32_t seek = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t from = i % 2 ? before.y : before.x, to = from + (i % 2 ? own.y : own.x);
+      if (from < t.at[i] && to >= t.at[i]) seek |= 1u << i;
+    }
+    if (seek != 0) {
+      for (int b = b0; b < b0 + per && seek != 0; ++b) {
+        const Pair v = f(b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t to = i % 2 ? before.y + v.y : before.x + v.x;
+          if ((seek >> i & 1) == 0 || to < t.at[i]) continue;
+          seek &= ~(1u << i);
           for (uint32_t r = 0; r < ncta; ++r) {
-            remote_store(&sh.bin[0], r, b0 + i);
-            remote_store64(&sh.before, r, before.x);
+            remote_store(&sh.bin[i], r, b);
+            if (i == 0) {
+              remote_store64(&sh.before, r, before.x);
+              remote_store(&sh.high, r, static_cast<uint32_t>(v.x));
+            }
           }
-        }
-        if (seek_y && before.y + v.y >= target_y) {
-          seek_y = false;
-          for (uint32_t r = 0; r < ncta; ++r) remote_store(&sh.bin[1], r, b0 + i);
         }
         before.x += v.x;
         before.y += v.y;
@@ -340,13 +396,36 @@ struct Row {
     return all;
   }
 
-  // Kept tokens go to the first CTA's list; only the first kList find room.
+  // This CTA's tokens that a cut may fall on; only the first kList find room.
   __device__ __forceinline__ void put(float l, int index) {
-    const uint32_t at = remote_add(&sh.list_count, 0, 1);
-    if (at < kList)
-      remote_store64(&list[at], 0, static_cast<uint64_t>(~key_of(l)) << 32 | static_cast<uint32_t>(index));
+    const uint32_t at = atomicAdd(&sh.put_count, 1u);
+    if (at < kList) own[at] = static_cast<uint64_t>(~key_of(l)) << 32 | static_cast<uint32_t>(index);
   }
   __device__ __forceinline__ static float logit_of(uint64_t entry) { return of_key(~static_cast<uint32_t>(entry >> 32)); }
+
+  // The first CTA: the cluster's tokens of bin b into its list; returns how many (all were put, and a barrier passed).
+  __device__ int gather(int b) {
+    uint32_t counts[kMaxCluster], all = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) {
+      counts[i] = i < static_cast<int>(ncta) ? remote_load(&sh.put_count, i) : 0;
+      all += counts[i];
+    }
+    for (uint32_t at = threadIdx.x; at < all; at += kThreads) {
+      uint32_t i = 0, in = at;
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k)
+        if (i == k && in >= counts[k]) {
+          in -= counts[k];
+          ++i;
+        }
+      uint64_t entry;
+      asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(entry) : "r"(in_cta(&own[in], i)) : "memory");
+      if (weight.bin(logit_of(entry)) == b) list[atomicAdd(&sh.list_count, 1u)] = entry;
+    }
+    __syncthreads();
+    return static_cast<int>(sh.list_count);
+  }
 
   __device__ void sort_list(int m) {  // ascending (bitonic), padded to a power of two
     int size = 32;
@@ -367,17 +446,17 @@ struct Row {
       }
   }
 
-  // Cuts off what lies in bins [b0, b1] behind the first tokens that make up `want`, counted as tokens or by weight.
-  // The list holds the kept tokens of those bins (after a cluster barrier).
+  // Cuts off what lies in bins [b0, b1] behind the first tokens that make up `want`, counted as tokens or by weight; where
+  // b0 = b1 and the bin's `m` tokens fit the list, they were put there (and a cluster barrier passed).
   template <bool BY_WEIGHT>
-  __device__ void cut_at(uint64_t want, int b0, int b1) {
-    const uint32_t m = remote_load(&sh.list_count, 0);
-    if (m > kList) {
+  __device__ void cut_at(uint64_t want, int b0, int b1, uint32_t m, bool room) {
+    if (b0 != b1 || m > kList || !room) {
       const Rounds found = cut_by_rounds<BY_WEIGHT>(*this, want, b0, b1);
       cut = found.cut;
       uses = found.uses;
-    } else if (m > 0) {
+    } else {
       if (rank == 0) {
+        m = gather(b0);
         sort_list(m);
         int stay;  // entries before which less than `want` lies
         if (BY_WEIGHT) {
@@ -411,7 +490,7 @@ struct Row {
         const uint64_t entry = list[max(stay - 1, 0)];
         const int last = static_cast<int>(static_cast<uint32_t>(entry)) - (stay > 0 ? 0 : 1);
         if (threadIdx.x < ncta) {
-          remote_store(&sh.cut.key, threadIdx.x, ~static_cast<uint32_t>(entry >> 32));
+          remote_store(&sh.cut.least, threadIdx.x, __float_as_uint(logit_of(entry)));
           remote_store(&sh.cut.last, threadIdx.x, static_cast<uint32_t>(last));
         }
         __syncwarp();
@@ -419,7 +498,7 @@ struct Row {
       ptx::cluster_sync();
       cut = sh.cut;
     }
-    if (threadIdx.x == 0) sh.list_count = 0;  // (all read it before the last barrier)
+    if (threadIdx.x == 0) sh.put_count = sh.list_count = 0;  // (read before the last barrier)
   }
 
   // (a copy, so that the caller's row stays in registers)
@@ -433,8 +512,9 @@ struct Row {
 
 // The same without a list, for bins of many tokens (ties, or logits beyond the bins' range): four rounds of eight bits of
 // the key, then the ties by index.
+template <typename T, bool KEEP>
 template <bool BY_WEIGHT>
-__device__ __noinline__ Row::Rounds Row::cut_by_rounds(Row r, uint64_t want, int b0, int b1) {
+__device__ __noinline__ typename Row<T, KEEP>::Rounds Row<T, KEEP>::cut_by_rounds(Row r, uint64_t want, int b0, int b1) {
   Shared& sh = r.sh;
   uint32_t* rounds = r.rounds;
   uint32_t prefix = 0;
@@ -448,7 +528,7 @@ __device__ __noinline__ Row::Rounds Row::cut_by_rounds(Row r, uint64_t want, int
     __syncthreads();
     r.sweep_kept([&](float l, int) {
       const uint32_t k = key_of(l);
-      const int b = r.bin_of(l);
+      const int b = r.weight.bin(l);
       if (b < b0 || b > b1 || (level < 24 && (k ^ prefix) >> (level + 8) != 0)) return;
       const int digit = 255 - (k >> level & 255);  // the largest first
       atomicAdd(&rounds[digit], 1u);
@@ -497,17 +577,18 @@ __device__ __noinline__ Row::Rounds Row::cut_by_rounds(Row r, uint64_t want, int
     stay = w > 0 ? (want + w - 1) / w : count_here;
   }
   const Cut old = r.cut;
-  Cut cut{prefix, INT_MAX};
+  const float least = of_key(prefix);
+  Cut cut{least, INT_MAX};
   if (stay < count_here) {
     uint32_t ties = 0;
-    r.sweep([&](float l, int index) { ties += key_of(l) == prefix && old.keeps(prefix, index); });
+    r.sweep([&](float l, int index) { ties += l == least && old.keeps(l, index); });
     r.exchange(ties, 0);
     uint64_t seen = r.before_cta().x;
     for (int i = 0; i < r.warp(); ++i) seen += sh.warp[0][i];
     if (seen < stay && seen + sh.warp[0][r.warp()] >= stay) {
       for (int y = r.warp() * r.run + r.lane(); y < (r.warp() + 1) * r.run; y += 32) {
         const int index = r.place0 + y - r.shift;
-        const bool tie = key_of(r.logit[y]) == prefix && old.keeps(prefix, index);
+        const bool tie = r.at(y) == least && old.keeps(least, index);
         const uint32_t votes = __ballot_sync(0xFFFFFFFFu, tie);
         if (tie && seen + __popc(votes & (0xFFFFFFFFu >> (31 - r.lane()))) == stay)
           for (uint32_t i = 0; i < r.ncta; ++i) remote_store(&sh.tie, i, static_cast<uint32_t>(index));
@@ -521,13 +602,13 @@ __device__ __noinline__ Row::Rounds Row::cut_by_rounds(Row r, uint64_t want, int
     cut.last = sh.tie;
     __syncthreads();
   } else {
-    cut.last = old.key == prefix ? old.last : INT_MAX;
+    cut.last = old.least == least ? old.last : INT_MAX;
   }
   return Rounds{cut, r.uses};
 }
 
-template <typename T, bool FILTER>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
+template <typename T, bool FILTER, bool KEEP>
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a) {
   __shared__ Shared sh;
   extern __shared__ __align__(16) char dynamic[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -538,25 +619,27 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   const long long line = blockIdx.x / ncta;
   const int req = static_cast<int>(line / a.rows_per);
   const T* src = static_cast<const T*>(a.logits) + req * a.stride0 + (line - static_cast<long long>(req) * a.rows_per) * a.stride1;
-  constexpr int kVec = 16 / sizeof(T);
+  using R = Row<T, KEEP>;
 
-  Row r{sh,
+  R r{sh,
         reinterpret_cast<uint32_t*>(dynamic),
         reinterpret_cast<uint64_t*>(dynamic + kBins * 4),
-        reinterpret_cast<uint32_t*>(dynamic + kBins * 4 + kList * 8),
+        reinterpret_cast<uint64_t*>(dynamic + kBins * 4 + kList * 8),
+        reinterpret_cast<uint32_t*>(dynamic + kBins * 4 + 2 * kList * 8),
         reinterpret_cast<float*>(dynamic + kFixedBytes),
+        src,
         ncta,
         ptx::cluster_ctarank(),
         0,
         static_cast<int>(reinterpret_cast<uintptr_t>(src) % 16 / sizeof(T)),  // place 0 lies on a 16-byte boundary
+        0,
         a.slice / kWarps,
-        a.scale,
-        0.f,
+        a.up,
         Weight{0.f, 0.f, 0.f},
-        Cut{0, 0},
+        Cut{-INFINITY, -1},
         0};
   r.place0 = static_cast<int>(r.rank) * a.slice;
-  const int end = a.vocab + r.shift;
+  r.end = a.vocab + r.shift;
 
   const float temperature = a.temperature != nullptr ? a.temperature[req] : 1.f;
   const int top_k = a.top_k != nullptr ? a.top_k[req] : 0;
@@ -567,34 +650,32 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
 
   // ---------------- the row, and its maximum
   float mx = -INFINITY;
-  for (int y = tid * kVec; y < a.slice; y += kThreads * kVec) {
-    const int place = r.place0 + y;
-    float v[kVec];
-    if (place >= r.shift && place + kVec <= end) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src + (place - r.shift)));
-      const T* t = reinterpret_cast<const T*>(&w);
+  constexpr int kVec = R::kVec, kAhead = 16 / kVec;
+  for (int y0 = tid * kVec; y0 < a.slice; y0 += kThreads * kVec * kAhead) {
+    float v[kAhead][kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = to_float(t[i]);
-    } else {
+    for (int k = 0; k < kAhead; ++k)
+      if (y0 + kThreads * kVec * k < a.slice) r.load(r.place0 + y0 + kThreads * kVec * k, v[k]);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        v[i] = place + i >= r.shift && place + i < end ? to_float(src[place + i - r.shift]) : -INFINITY;
+    for (int k = 0; k < kAhead; ++k) {
+      const int y = y0 + kThreads * kVec * k;
+      if (y >= a.slice) break;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) mx = fmaxf(mx, v[k][i]);
+      if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < kVec; i += 4)
+          *reinterpret_cast<float4*>(r.logit + y + i) = make_float4(v[k][i], v[k][i + 1], v[k][i + 2], v[k][i + 3]);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      if (v[i] != v[i]) v[i] = -INFINITY;  // a NaN counts as left out
-      mx = fmaxf(mx, v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kVec; i += 4)
-      *reinterpret_cast<float4*>(r.logit + y + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
   }
   if (!greedy && (by_count || by_weight))
     for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(r.hist)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) {
-    sh.list_count = 0;
+    sh.put_count = sh.list_count = 0;
     sh.tie = INT_MAX;
   }
+  if (tid < 3 * kWindow) sh.window[0][tid] = 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
   float* warp_max = reinterpret_cast<float*>(sh.scratch);
@@ -615,10 +696,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
   // ---------------- which tokens are kept, and their weight
   const double c = kLog2e / static_cast<double>(temperature);
   r.weight.max = mx;
-  r.weight.ch = static_cast<float>(c);
-  r.weight.cl = isinf(r.weight.ch) ? 0.f : static_cast<float>(c - static_cast<double>(r.weight.ch));
-  r.bin_scale = kBins / (kRange * temperature);
-  r.cut = Cut{key_of(-INFINITY), -1};
+  r.weight.ch = fminf(static_cast<float>(c), 3.4028234664e38f);
+  r.weight.cl = c > 3e38 ? 0.f : static_cast<float>(c - static_cast<double>(r.weight.ch));
   uint64_t total = 0;
   if (mx == -INFINITY) {
     // none
@@ -632,16 +711,16 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
       for (uint32_t i = 0; i < ncta; ++i) remote_min(&sh.tie, i, lowest);
     __syncwarp();
     ptx::cluster_sync();
-    r.cut = Cut{key_of(mx), sh.tie};
+    r.cut = Cut{mx, sh.tie};
     total = 1;
   } else {
     if (min_p > 0.f) {  // l >= max + T ln min_p, the bound rounded up to the next float
       const double least = static_cast<double>(mx) + static_cast<double>(temperature) * log(static_cast<double>(min_p));
-      if (least > -INFINITY) r.cut.key = max(r.cut.key, key_of(__double2float_ru(least)) - 1);
+      if (least > -INFINITY) r.cut.least = nextafterf(__double2float_ru(least), -INFINITY);
     }
     uint64_t kept = 0;  // this thread's
     r.sweep_kept([&](float l, int) {
-      if (by_count || by_weight) atomicAdd(&r.hist[r.bin_of(l)], 1u);
+      if (by_count || by_weight) atomicAdd(&r.hist[r.weight.bin(l)], 1u);
       if (!by_count) kept += r.weigh(l);
     });
     int k_bin = kBins;
@@ -658,15 +737,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
     if (by_count) {
       const uint64_t want = top_k;
-      const auto all = r.find_bins([&](int b) { return Row::Pair{r.hist[b], 0}; }, want, ~0ull);
+      const auto all = r.find_bins([&](int b) { return typename R::Pair{r.hist[b], 0}; },
+                                   [&](typename R::Pair) { return typename R::Targets{{want, ~0ull, ~0ull, ~0ull}}; });
       if (want < all.x) {
         k_bin = sh.bin[0];
         k_rest = static_cast<uint32_t>(want - sh.before);
-        r.sweep_kept([&](float l, int index) {
-          if (r.bin_of(l) == k_bin) r.put(l, index);
-        });
+        const uint32_t m = sh.high;
+        if (m <= kList)
+          r.sweep_kept([&](float l, int index) {
+            if (r.weight.bin(l) == k_bin) r.put(l, index);
+          });
         ptx::cluster_sync();
-        r.template cut_at<false>(k_rest, k_bin, k_bin);
+        r.template cut_at<false>(k_rest, k_bin, k_bin, m, true);
       }
       r.sweep_kept([&](float l, int) { kept += r.weigh(l); });
     }
@@ -674,47 +756,94 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     if (by_weight) {
       // The most and the least weight that each bin can hold bound the bins that the cut can fall into.
       const double part = static_cast<double>(fmaxf(top_p, 0.f)) * static_cast<double>(total);
-      const double coarse = part * exp2(static_cast<double>(kMassBits - a.scale));
+      const uint64_t want = max(static_cast<uint64_t>(ceil(part)), static_cast<uint64_t>(1));
+      const double coarse = part * exp2(static_cast<double>(kMassBits - 31 - a.up));
       auto bounds = [&](int b) {
         const uint64_t n = b < k_bin ? r.hist[b] : (b == k_bin ? k_rest : 0);
-        const float most = exp2f(kMassBits - b * kBinLog2), least = exp2f(kMassBits - (b + 1) * kBinLog2);
-        return Row::Pair{n * (static_cast<uint64_t>(most * 1.00001f) + 1),
-                         b + 1 < kBins ? n * static_cast<uint64_t>(least * 0.99999f) : 0};
+        // (a bin's steps are rounded: it reaches half a step of 2^-10 to either side)
+        constexpr float kSpan = 1.f / (1 << (10 - kBinShift)), kHalf = 1.f / 2048.f;
+        const float most = exp2f(kMassBits + kHalf - b * kSpan), least = exp2f(kMassBits + kHalf - (b + 1) * kSpan);
+        return typename R::Pair{n * (static_cast<uint64_t>(most * 1.00001f) + 1),
+                                b + 1 < kBins ? n * static_cast<uint64_t>(least * 0.99999f) : 0};
       };
-      r.find_bins(bounds, max(static_cast<uint64_t>(coarse * 0.99999), static_cast<uint64_t>(1)),
-                  static_cast<uint64_t>(coarse * 1.00001) + 1);
-      const int first = sh.bin[0], last = max(sh.bin[0], sh.bin[1]);
+      // The sum up to a bin is at most the bounds' own and what the least behind it leaves of the total; at least likewise.
+      const double sum = static_cast<double>(total) * exp2(static_cast<double>(kMassBits - 31 - a.up));
+      r.find_bins(bounds, [&](typename R::Pair all) {
+        auto target = [](double x) { return x > 1.0 ? static_cast<uint64_t>(x) : static_cast<uint64_t>(1); };
+        const double low = coarse * (1 - 1e-7), high = coarse * (1 + 1e-7) + 1;
+        return typename R::Targets{{target(low), target(low - sum + static_cast<double>(all.y) - 1),
+                                    target(high - sum + static_cast<double>(all.x) + 1), target(high)}};
+      });
+      const int first = max(sh.bin[0], sh.bin[1]), last = max(first, min(sh.bin[2], sh.bin[3]));
+      const bool narrow = last - first < kWindow;
       kept = 0;
       r.sweep_kept([&](float l, int index) {
-        const int b = r.bin_of(l);
-        if (b < first) kept += r.weigh(l);
-        if (b >= first && b <= last) r.put(l, index);
+        const int b = r.weight.bin(l);
+        if (b > last) return;
+        const uint64_t w = r.weigh(l);
+        if (b < first) {
+          kept += w;
+        } else if (narrow) {
+          r.put(l, index);
+          const uint32_t low = static_cast<uint32_t>(w), old = atomicAdd(&sh.window[1][b - first], low);
+          atomicAdd(&sh.window[0][b - first], 1u);
+          atomicAdd(&sh.window[2][b - first], static_cast<uint32_t>(w >> 32) + (old + low < old ? 1u : 0u));
+        }
       });
-      const uint64_t above = r.exchange(kept, 0).x, want = max(static_cast<uint64_t>(ceil(part)), static_cast<uint64_t>(1));
-      r.template cut_at<true>(want - min(want, above), first, last);
+      uint64_t above = r.exchange(kept, 0).x;
+      int at = first;
+      uint32_t m = 0;
+      bool room = true;
+      if (narrow) {  // the bin that the cut falls into, by every CTA alike: warp 0 adds up the cluster's windows
+        if (warp == 0) {
+          uint64_t sum = 0;
+          uint32_t n = 0;
+          if (lane < kWindow)
+            for (uint32_t i = 0; i < ncta; ++i) {
+              n += remote_load(&sh.window[0][lane], i);
+              sum += remote_load(&sh.window[1][lane], i) + (static_cast<uint64_t>(remote_load(&sh.window[2][lane], i)) << 32);
+            }
+          const bool full = lane < static_cast<int>(ncta) && remote_load(&sh.put_count, lane) > kList;
+          const uint64_t upto = above + warp_scan(sum);
+          const uint32_t hit = __ballot_sync(0xFFFFFFFFu, n > 0 && upto >= want), any = __ballot_sync(0xFFFFFFFFu, n > 0);
+          const int pick = hit != 0 ? __ffs(hit) - 1 : (any != 0 ? 31 - __clz(any) : 0);
+          const bool crowded = __any_sync(0xFFFFFFFFu, full);
+          if (lane == pick) {
+            sh.low = crowded ? -1 : pick;
+            sh.high = static_cast<int>(n);
+            sh.scratch[0] = upto - sum;
+          }
+        }
+        __syncthreads();
+        room = sh.low >= 0;
+        m = sh.high;
+        if (room) {
+          at = first + sh.low;
+          above = sh.scratch[0];
+        }
+        ptx::cluster_sync();  // (all have read the windows before a list is gathered and the counts are reset)
+      }
+      const int to = narrow && room ? at : last;
+      if (!narrow || !room || m > 0) r.template cut_at<true>(want - min(want, above), at, to, m, narrow && room);
       r.sweep_kept([&](float l, int) {
-        const int b = r.bin_of(l);
-        if (b >= first && b <= last) kept += r.weigh(l);
+        if (r.weight.bin(l) >= first) kept += r.weigh(l);
       });
       total = r.exchange(kept, 0).x;
     }
   }
 
   if (FILTER) {
-    const float inv = static_cast<float>(exp2(static_cast<double>(a.scale)) / static_cast<double>(total)) * 4.656612873077393e-10f;  // 2^-31
+    const float inv = static_cast<float>(exp2(static_cast<double>(a.up)) / static_cast<double>(total));
     const int lo = max(r.place0 - r.shift, 0), hi = min(r.place0 + a.slice - r.shift, a.vocab);
     float* out = a.probs + line * a.vocab;
-    const float* logit = r.logit + r.shift - r.place0;  // by index
     auto prob = [&](int x) {
-      const float l = logit[x];
-      if (total == 0 || !r.cut.keeps(key_of(l), x)) return 0.f;
+      const float l = r.at(x + r.shift - r.place0);
+      if (total == 0 || !r.cut.keeps(l, x)) return 0.f;
       if (greedy) return 1.f;
-      uint64_t m;
-      int whole;
-      if (!r.weight(l, 160.f, m, whole)) return 0.f;
-      const int half = whole / 2;
-      return __uint2float_rn(static_cast<uint32_t>(m >> 32)) * inv * __int_as_float((127 - half) << 23) *
-             __int_as_float((127 - whole + half) << 23);
+      int n;
+      const uint32_t m = r.weight(l, n);
+      if (n > 160) return 0.f;
+      return __uint2float_rn(m) * inv * __int_as_float((127 - n / 2) << 23) * __int_as_float((127 - n + n / 2) << 23);
     };
     const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(out) / 4 % 4);  // out - lead lies on 16 bytes
     for (int x = (lo + lead) / 4 * 4 - lead + tid * 4; x < hi; x += kThreads * 4) {
@@ -740,8 +869,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
       while (w + 1 < kWarps && before + sh.warp[0][w] <= t) before += sh.warp[0][w++];
       for (int base = w * r.run; base < (w + 1) * r.run; base += kThreads) {
         const int y = base + tid, index = r.place0 + y - r.shift;
-        const bool in = y < (w + 1) * r.run && r.cut.keeps(key_of(r.logit[min(y, a.slice - 1)]), index);
-        const uint64_t mine = in ? r.weigh(r.logit[y]) : 0, upto = warp_scan(mine);
+        const float l = y < (w + 1) * r.run ? r.at(y) : -INFINITY;
+        const uint64_t mine = r.cut.keeps(l, index) ? r.weigh(l) : 0, upto = warp_scan(mine);
         if (lane == 31) sh.scratch[warp] = upto;
         __syncthreads();
         uint64_t run = before + upto;
@@ -758,36 +887,28 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
 }
 
 // Per device, once for each kernel: shared memory beyond 48 KB and clusters of more than eight CTAs.
-template <typename T, bool FILTER>
+template <typename T, bool FILTER, bool KEEP>
 bool prepare_kernel() {
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = 1ull << (dev & 63);
   if (ready.load() & bit) return true;
-  const auto kernel = sample_kernel<T, FILTER>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFixedBytes + kMaxSlice * 4) != cudaSuccess ||
+  const auto kernel = sample_kernel<T, FILTER, KEEP>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFixedBytes + kKeepSlice * 4) != cudaSuccess ||
       cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return false;
   ready.fetch_or(bit);
   return true;
 }
 
-template <typename T, bool FILTER>
-qnre_status_t launch(SampleArgs a, int64_t rows, qnre_stream_t stream) {
-  if (!prepare_kernel<T, FILTER>()) return QNRE_ERR_CUDA;
-  // As many CTAs a row as the machine holds at once, while each keeps a grain of places; and as many as hold the row.
-  const int64_t places = a.vocab + 16 / sizeof(T) - 1;
-  unsigned cluster = kMaxCluster;
-  while (cluster > 1 && (rows * cluster > 152 * 3 || places <= static_cast<int64_t>(cluster / 2) * kGrain)) cluster /= 2;
-  while (cluster < kMaxCluster && places > static_cast<int64_t>(cluster) * 16384) cluster *= 2;
-  a.slice = static_cast<int>(((places + cluster - 1) / cluster + kGrain - 1) / kGrain * kGrain);
-  a.scale = 62;
-  while (a.scale > 0 && (int64_t{1} << (62 - a.scale)) < a.vocab) --a.scale;
+template <typename T, bool FILTER, bool KEEP>
+qnre_status_t launch(const SampleArgs& a, int64_t rows, unsigned cluster, qnre_stream_t stream) {
+  if (!prepare_kernel<T, FILTER, KEEP>()) return QNRE_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kFixedBytes + a.slice * 4;
+  cfg.dynamicSmemBytes = kFixedBytes + (KEEP ? a.slice * 4 : 0);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -798,7 +919,20 @@ qnre_status_t launch(SampleArgs a, int64_t rows, qnre_stream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return from_cuda(cudaLaunchKernelEx(&cfg, sample_kernel<T, FILTER>, a));
+  return from_cuda(cudaLaunchKernelEx(&cfg, sample_kernel<T, FILTER, KEEP>, a));
+}
+
+template <typename T, bool FILTER>
+qnre_status_t choose(SampleArgs a, int64_t rows, qnre_stream_t stream) {
+  // As many CTAs a row as the machine holds at once, while each keeps a grain of places.
+  const int64_t places = a.vocab + 16 / sizeof(T) - 1;
+  unsigned cluster = kMaxCluster;
+  while (cluster > 1 && (rows * cluster > kResident || places <= static_cast<int64_t>(cluster / 2) * kGrain)) cluster /= 2;
+  a.slice = static_cast<int>(((places + cluster - 1) / cluster + kGrain - 1) / kGrain * kGrain);
+  a.up = 31;  // sums of V weights stay below 2^63
+  while ((int64_t{1} << (31 - a.up)) < a.vocab) --a.up;
+  return a.slice <= kKeepSlice ? launch<T, FILTER, true>(a, rows, cluster, stream)
+                               : launch<T, FILTER, false>(a, rows, cluster, stream);
 }
 
 template <bool FILTER>
@@ -827,9 +961,9 @@ qnre_status_t run(const void* logits, int64_t stride0, int64_t stride1, int32_t 
                static_cast<int>(vocab), 0, 0};
   const int64_t rows = static_cast<int64_t>(n) * nodes;
   switch (dtype) {
-    case QNRE_DTYPE_FP32: return launch<float, FILTER>(a, rows, stream);
-    case QNRE_DTYPE_BF16: return launch<__nv_bfloat16, FILTER>(a, rows, stream);
-    default: return launch<__half, FILTER>(a, rows, stream);
+    case QNRE_DTYPE_FP32: return choose<float, FILTER>(a, rows, stream);
+    case QNRE_DTYPE_BF16: return choose<__nv_bfloat16, FILTER>(a, rows, stream);
+    default: return choose<__half, FILTER>(a, rows, stream);
   }
 }
 
