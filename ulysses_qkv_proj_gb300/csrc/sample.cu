@@ -48,12 +48,14 @@ constexpr int kMaxCluster = 16;
 constexpr int kGrain = kWarps * 128;     // places of a CTA come in multiples of this: a float4 a lane, warp by warp
 constexpr int kBins = 4096;
 constexpr int kBinShift = 3;             // a bin is 2^3 steps of 2^-10 in log2; the last holds all beyond 32
-constexpr int kList = 1024;
-constexpr int kWindow = 16;              // bins that a cut by weight is sought in
+constexpr int kList = 1024;              // tokens of one bin that are sorted
+constexpr int kOwn = 2048;               // tokens that a CTA lists
+constexpr int kWindow = 32;              // bins that a cut by weight is sought in (16-bit logits leave gaps of up to 20)
 constexpr int kResident = 152 * 4;       // CTAs that the machine about holds at once
+constexpr int64_t kInL2 = 96ll << 20;
 constexpr int kKeepSlice = 12288;        // places of a CTA that it holds in shared memory (two or three such CTAs a SM)
 constexpr int kMassBits = 40;            // of the histogram's bounds on weights
-constexpr int kFixedBytes = kBins * 4 + 2 * kList * 8 + 3 * 256 * 4;  // shared memory before the row
+constexpr int kFixedBytes = kBins * 4 + kOwn * 8 + kList * 8 + 3 * 256 * 4;  // shared memory before the row
 constexpr double kLog2e = 1.4426950408889634074;
 
 struct SampleArgs {
@@ -109,6 +111,15 @@ constexpr PowerTable make_powers() {
 }
 __device__ const PowerTable kPowers = make_powers();
 
+// Logits as integers of the same order (larger logit, larger key); both zeros have one key.
+__device__ __forceinline__ uint32_t key_of(float l) {
+  const uint32_t b = __float_as_uint(l + 0.f);
+  return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
 // A row's scale: weights are 2^(-y), y = (max - l) c, c = log2(e) / T as a pair of floats.
 struct Weight {
   float max, ch, cl;
@@ -123,6 +134,20 @@ struct Weight {
   __device__ __forceinline__ int bin(float l) const {
     float p;
     return min(steps(l, p) >> kBinShift, kBins - 1);
+  }
+  // The least logit of bin b or before (a whole warp: 32 places of the range of floats at a time).
+  __device__ float least_of(int b) const {
+    if (b >= kBins - 1) return -3.4028234664e38f;
+    if (b < 0) return INFINITY;
+    uint32_t lo = key_of(-3.4028234664e38f) - 1, hi = key_of(max);  // beyond the bin; within
+    while (hi - lo > 1) {
+      const uint32_t step = (hi - lo + 31) / 32, k = min(lo + (threadIdx.x % 32 + 1) * step, hi);
+      const uint32_t within = __ballot_sync(0xFFFFFFFFu, bin(of_key(k)) <= b);
+      const uint32_t first = __ffs(within) - 1;
+      hi = min(lo + (first + 1) * step, hi);
+      lo += first * step;
+    }
+    return of_key(hi);
   }
   // 2^-y = m 2^-(31 + n)
   __device__ __forceinline__ uint32_t operator()(float l, int& n) const {
@@ -147,15 +172,6 @@ struct Weight {
   }
 };
 
-// Logits as integers of the same order (larger logit, larger key); both zeros have one key.
-__device__ __forceinline__ uint32_t key_of(float l) {
-  const uint32_t b = __float_as_uint(l + 0.f);
-  return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
-}
-__device__ __forceinline__ float of_key(uint32_t k) {
-  return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
-}
-
 // What a row keeps: larger logits than `least`, and of that the tokens up to `last`.
 struct Cut {
   float least;
@@ -171,6 +187,7 @@ struct Shared {
   uint64_t before;                   // what lies before the first bin found
   Cut cut;
   uint32_t window[3][kWindow];       // of these bins: tokens, weights' low and high words
+  uint32_t runs[2][kWarps];          // a list's weight in each run, low and high words
   uint32_t put_count, list_count;
   int bin[4], tie, low, high;
 };
@@ -224,7 +241,7 @@ struct Row {
   static constexpr int kVec = 16 / sizeof(T);
   Shared& sh;
   uint32_t* hist;    // [kBins]
-  uint64_t* own;     // [kList]: tokens that this CTA put there, as (~key, index)
+  uint64_t* own;     // [kOwn]: tokens that this CTA put there, as (~key, index)
   uint64_t* list;    // [kList]: those of one bin from all CTAs; the first CTA's
   uint32_t* rounds;  // [3][256]: counts, weights' low and high words
   float* logit;      // [slice] (KEEP)
@@ -234,6 +251,7 @@ struct Row {
   Weight weight;
   Cut cut;
   unsigned uses;
+  bool listed;       // `own` holds all that may still be kept
 
   __device__ __forceinline__ static int warp() { return threadIdx.x / 32; }
   __device__ __forceinline__ static int lane() { return threadIdx.x % 32; }
@@ -253,13 +271,13 @@ struct Row {
         v[i] = place + i >= shift && place + i < end ? to_float(src[place + i - shift]) : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = v[i] != v[i] ? -INFINITY : fminf(v[i], 3.4028234664e38f);
+    for (int i = 0; i < kVec; ++i) v[i] = clean(v[i]);
   }
+  __device__ __forceinline__ static float clean(float v) { return fminf(fmaxf(v, -INFINITY), 3.4028234664e38f); }  // (NaN: -inf)
   __device__ __forceinline__ float at(int y) const {  // place y of this CTA
     if (KEEP) return logit[y];
     const int place = place0 + y;
-    const float v = place >= shift && place < end ? to_float(src[place - shift]) : -INFINITY;
-    return v != v ? -INFINITY : fminf(v, 3.4028234664e38f);
+    return place >= shift && place < end ? clean(to_float(src[place - shift])) : -INFINITY;
   }
 
   // f(logit, index) for every place of this warp's run.
@@ -297,6 +315,41 @@ struct Row {
     sweep([&](float l, int index) {
       if (cut.keeps(l, index)) f(l, index);
     });
+  }
+
+  // f(logit, index) for every kept token, from the CTA's list where it holds them all.
+  template <typename F>
+  __device__ __forceinline__ void each_kept(F f) const {
+    if (!listed) return sweep_kept(f);
+    for (uint32_t i = threadIdx.x; i < sh.put_count; i += kThreads) {
+      const uint64_t entry = own[i];
+      const float l = logit_of(entry);
+      const int index = static_cast<int>(static_cast<uint32_t>(entry));
+      if (cut.keeps(l, index)) f(l, index);
+    }
+  }
+  // A thread's share of its run's sum of the kept tokens' weights that pick(logit) names.
+  template <typename F>
+  __device__ __forceinline__ uint64_t kept_weight(F pick) {
+    uint64_t sum = 0;
+    if (!listed) {
+      sweep_kept([&](float l, int) {
+        if (pick(l)) sum += weigh(l);
+      });
+      return sum;
+    }
+    if (threadIdx.x < 2 * kWarps) sh.runs[0][threadIdx.x] = 0;
+    __syncthreads();
+    each_kept([&](float l, int index) {
+      if (pick(l)) add_to(sh.runs[0], sh.runs[1], (index + shift - place0) / run, weigh(l));
+    });
+    __syncthreads();
+    return lane() == 0 ? sh.runs[0][warp()] | static_cast<uint64_t>(sh.runs[1][warp()]) << 32 : 0;
+  }
+  // A 64-bit sum in two words, by two atomics.
+  __device__ __forceinline__ static void add_to(uint32_t* low, uint32_t* high, int at, uint64_t w) {
+    const uint32_t part = static_cast<uint32_t>(w), old = atomicAdd(&low[at], part);
+    atomicAdd(&high[at], static_cast<uint32_t>(w >> 32) + (old + part < old ? 1u : 0u));
   }
 
   struct Pair {
@@ -396,14 +449,14 @@ struct Row {
     return all;
   }
 
-  // This CTA's tokens that a cut may fall on; only the first kList find room.
+  // This CTA's tokens that a cut may fall on, or (listed) all that may be kept; only the first kOwn find room.
   __device__ __forceinline__ void put(float l, int index) {
     const uint32_t at = atomicAdd(&sh.put_count, 1u);
-    if (at < kList) own[at] = static_cast<uint64_t>(~key_of(l)) << 32 | static_cast<uint32_t>(index);
+    if (at < kOwn) own[at] = static_cast<uint64_t>(~key_of(l)) << 32 | static_cast<uint32_t>(index);
   }
   __device__ __forceinline__ static float logit_of(uint64_t entry) { return of_key(~static_cast<uint32_t>(entry >> 32)); }
 
-  // The first CTA: the cluster's tokens of bin b into its list; returns how many (all were put, and a barrier passed).
+  // The first CTA: the cluster's kept tokens of bin b into its list (no more than kList); returns how many (all were put, and a barrier passed).
   __device__ int gather(int b) {
     uint32_t counts[kMaxCluster], all = 0;
 #pragma unroll
@@ -421,7 +474,9 @@ struct Row {
         }
       uint64_t entry;
       asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(entry) : "r"(in_cta(&own[in], i)) : "memory");
-      if (weight.bin(logit_of(entry)) == b) list[atomicAdd(&sh.list_count, 1u)] = entry;
+      const float l = logit_of(entry);
+      if (weight.bin(l) == b && cut.keeps(l, static_cast<int>(static_cast<uint32_t>(entry))))
+        list[atomicAdd(&sh.list_count, 1u)] = entry;
     }
     __syncthreads();
     return static_cast<int>(sh.list_count);
@@ -498,7 +553,11 @@ struct Row {
       ptx::cluster_sync();
       cut = sh.cut;
     }
-    if (threadIdx.x == 0) sh.put_count = sh.list_count = 0;  // (read before the last barrier)
+    if (threadIdx.x == 0) {  // (read before the last barrier)
+      sh.list_count = 0;
+      if (!listed) sh.put_count = 0;
+    }
+    __syncthreads();
   }
 
   // (a copy, so that the caller's row stays in registers)
@@ -533,9 +592,7 @@ __device__ __noinline__ typename Row<T, KEEP>::Rounds Row<T, KEEP>::cut_by_round
       const int digit = 255 - (k >> level & 255);  // the largest first
       atomicAdd(&rounds[digit], 1u);
       if (BY_WEIGHT) {
-        const uint64_t w = r.weigh(l);
-        const uint32_t part = static_cast<uint32_t>(w), old = atomicAdd(&rounds[256 + digit], part);
-        atomicAdd(&rounds[512 + digit], static_cast<uint32_t>(w >> 32) + (old + part < old ? 1u : 0u));
+        add_to(rounds + 256, rounds + 512, digit, r.weigh(l));
       }
     });
     __syncthreads();
@@ -608,7 +665,7 @@ __device__ __noinline__ typename Row<T, KEEP>::Rounds Row<T, KEEP>::cut_by_round
 }
 
 template <typename T, bool FILTER, bool KEEP>
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const SampleArgs a) {
   __shared__ Shared sh;
   extern __shared__ __align__(16) char dynamic[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -624,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
   R r{sh,
         reinterpret_cast<uint32_t*>(dynamic),
         reinterpret_cast<uint64_t*>(dynamic + kBins * 4),
-        reinterpret_cast<uint64_t*>(dynamic + kBins * 4 + kList * 8),
-        reinterpret_cast<uint32_t*>(dynamic + kBins * 4 + 2 * kList * 8),
+        reinterpret_cast<uint64_t*>(dynamic + kBins * 4 + kOwn * 8),
+        reinterpret_cast<uint32_t*>(dynamic + kBins * 4 + kOwn * 8 + kList * 8),
         reinterpret_cast<float*>(dynamic + kFixedBytes),
         src,
         ncta,
@@ -637,7 +694,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         a.up,
         Weight{0.f, 0.f, 0.f},
         Cut{-INFINITY, -1},
-        0};
+        0,
+        false};
   r.place0 = static_cast<int>(r.rank) * a.slice;
   r.end = a.vocab + r.shift;
 
@@ -650,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 
   // ---------------- the row, and its maximum
   float mx = -INFINITY;
-  constexpr int kVec = R::kVec, kAhead = 16 / kVec;
+  constexpr int kVec = R::kVec, kAhead = 32 / kVec;
   for (int y0 = tid * kVec; y0 < a.slice; y0 += kThreads * kVec * kAhead) {
     float v[kAhead][kVec];
 #pragma unroll
@@ -676,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     sh.tie = INT_MAX;
   }
   if (tid < 3 * kWindow) sh.window[0][tid] = 0;
+  static_assert(3 * kWindow <= kThreads && kWindow == 32, "a lane a bin");
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
   float* warp_max = reinterpret_cast<float*>(sh.scratch);
@@ -743,14 +802,18 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         k_bin = sh.bin[0];
         k_rest = static_cast<uint32_t>(want - sh.before);
         const uint32_t m = sh.high;
-        if (m <= kList)
+        const bool all_listed = sh.before + m <= kOwn;
+        const float from = r.weight.least_of(k_bin), to = all_listed ? INFINITY : r.weight.least_of(k_bin - 1);
+        if (all_listed || m <= kList)
           r.sweep_kept([&](float l, int index) {
-            if (r.weight.bin(l) == k_bin) r.put(l, index);
+            if (l >= from && l < to) r.put(l, index);
           });
+        __syncthreads();
         ptx::cluster_sync();
+        r.listed = all_listed;
         r.template cut_at<false>(k_rest, k_bin, k_bin, m, true);
       }
-      r.sweep_kept([&](float l, int) { kept += r.weigh(l); });
+      kept = r.kept_weight([](float) { return true; });
     }
     total = r.exchange(kept, 0).x;
     if (by_weight) {
@@ -776,21 +839,40 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
       });
       const int first = max(sh.bin[0], sh.bin[1]), last = max(first, min(sh.bin[2], sh.bin[3]));
       const bool narrow = last - first < kWindow;
+      // The weight before the window, the window's by bins, and its tokens; with what lies before them where that is little.
+      bool list_now = false;
+      if (!r.listed) {
+        const int share = kBins / ncta;
+        uint64_t tokens = 0;
+        for (int b = r.rank * share + tid; b < static_cast<int>(r.rank + 1) * share; b += kThreads)
+          if (b <= last) tokens += r.hist[b];
+        list_now = r.exchange(tokens, 0).x <= kOwn;
+      }
+      if (r.listed && tid < 2 * kWarps) sh.runs[0][tid] = 0;
+      __syncthreads();
       kept = 0;
-      r.sweep_kept([&](float l, int index) {
+      const float from = r.weight.least_of(last);
+      r.each_kept([&](float l, int index) {
+        if (l < from) return;
         const int b = r.weight.bin(l);
-        if (b > last) return;
+        if (!r.listed && (list_now || (narrow && b >= first))) r.put(l, index);
+        if (b >= first && !narrow) return;
         const uint64_t w = r.weigh(l);
-        if (b < first) {
-          kept += w;
-        } else if (narrow) {
-          r.put(l, index);
-          const uint32_t low = static_cast<uint32_t>(w), old = atomicAdd(&sh.window[1][b - first], low);
+        if (b >= first) {
           atomicAdd(&sh.window[0][b - first], 1u);
-          atomicAdd(&sh.window[2][b - first], static_cast<uint32_t>(w >> 32) + (old + low < old ? 1u : 0u));
+          R::add_to(sh.window[1], sh.window[2], b - first, w);
+        } else if (r.listed) {
+          R::add_to(sh.runs[0], sh.runs[1], (index + r.shift - r.place0) / r.run, w);
+        } else {
+          kept += w;
         }
       });
+      if (r.listed) {
+        __syncthreads();
+        kept = lane == 0 ? sh.runs[0][warp] | static_cast<uint64_t>(sh.runs[1][warp]) << 32 : 0;
+      }
       uint64_t above = r.exchange(kept, 0).x;
+      r.listed |= list_now;
       int at = first;
       uint32_t m = 0;
       bool room = true;
@@ -798,12 +880,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
         if (warp == 0) {
           uint64_t sum = 0;
           uint32_t n = 0;
-          if (lane < kWindow)
-            for (uint32_t i = 0; i < ncta; ++i) {
-              n += remote_load(&sh.window[0][lane], i);
-              sum += remote_load(&sh.window[1][lane], i) + (static_cast<uint64_t>(remote_load(&sh.window[2][lane], i)) << 32);
-            }
-          const bool full = lane < static_cast<int>(ncta) && remote_load(&sh.put_count, lane) > kList;
+          for (uint32_t i = 0; i < ncta; ++i) {
+            n += remote_load(&sh.window[0][lane], i);
+            sum += remote_load(&sh.window[1][lane], i) + (static_cast<uint64_t>(remote_load(&sh.window[2][lane], i)) << 32);
+          }
+          const bool full = lane < static_cast<int>(ncta) && remote_load(&sh.put_count, lane) > kOwn;
           const uint64_t upto = above + warp_scan(sum);
           const uint32_t hit = __ballot_sync(0xFFFFFFFFu, n > 0 && upto >= want), any = __ballot_sync(0xFFFFFFFFu, n > 0);
           const int pick = hit != 0 ? __ffs(hit) - 1 : (any != 0 ? 31 - __clz(any) : 0);
@@ -825,9 +906,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
       }
       const int to = narrow && room ? at : last;
       if (!narrow || !room || m > 0) r.template cut_at<true>(want - min(want, above), at, to, m, narrow && room);
-      r.sweep_kept([&](float l, int) {
-        if (r.weight.bin(l) >= first) kept += r.weigh(l);
-      });
+      const float before = r.weight.least_of(first - 1);
+      kept += r.kept_weight([&](float l) { return l < before; });
       total = r.exchange(kept, 0).x;
     }
   }
@@ -836,21 +916,34 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
     const float inv = static_cast<float>(exp2(static_cast<double>(a.up)) / static_cast<double>(total));
     const int lo = max(r.place0 - r.shift, 0), hi = min(r.place0 + a.slice - r.shift, a.vocab);
     float* out = a.probs + line * a.vocab;
-    auto prob = [&](int x) {
-      const float l = r.at(x + r.shift - r.place0);
-      if (total == 0 || !r.cut.keeps(l, x)) return 0.f;
-      if (greedy) return 1.f;
+    auto prob = [&](float l, int x) {
+      if (!r.cut.keeps(l, x)) return 0.f;
       int n;
       const uint32_t m = r.weight(l, n);
       if (n > 160) return 0.f;
       return __uint2float_rn(m) * inv * __int_as_float((127 - n / 2) << 23) * __int_as_float((127 - n + n / 2) << 23);
     };
+    // few tokens: zeros, then the tokens' own
+    const bool sparse = total == 0 || greedy || r.listed;
     const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(out) / 4 % 4);  // out - lead lies on 16 bytes
     for (int x = (lo + lead) / 4 * 4 - lead + tid * 4; x < hi; x += kThreads * 4) {
       if (x >= lo && x + 4 <= hi) {
-        __stcs(reinterpret_cast<float4*>(out + x), make_float4(prob(x), prob(x + 1), prob(x + 2), prob(x + 3)));
+        float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!sparse) {
+          const int y = x + r.shift - r.place0;
+          p = make_float4(prob(r.at(y), x), prob(r.at(y + 1), x + 1), prob(r.at(y + 2), x + 2), prob(r.at(y + 3), x + 3));
+        }
+        __stcs(reinterpret_cast<float4*>(out + x), p);
       } else {
-        for (int i = max(x, lo); i < min(x + 4, hi); ++i) out[i] = prob(i);
+        for (int i = max(x, lo); i < min(x + 4, hi); ++i) out[i] = sparse ? 0.f : prob(r.at(i + r.shift - r.place0), i);
+      }
+    }
+    if (sparse && total != 0) {
+      __syncthreads();
+      if (greedy) {
+        if (tid == 0 && r.cut.last >= lo && r.cut.last < hi) out[r.cut.last] = 1.f;
+      } else {
+        r.each_kept([&](float l, int x) { out[x] = prob(l, x); });
       }
     }
   } else if (total == 0 || greedy) {
@@ -928,6 +1021,10 @@ qnre_status_t choose(SampleArgs a, int64_t rows, qnre_stream_t stream) {
   const int64_t places = a.vocab + 16 / sizeof(T) - 1;
   unsigned cluster = kMaxCluster;
   while (cluster > 1 && (rows * cluster > kResident || places <= static_cast<int64_t>(cluster / 2) * kGrain)) cluster /= 2;
+  // Rows that are read again should fit in L2 together.
+  while (cluster < kMaxCluster && places > static_cast<int64_t>(cluster) * kKeepSlice &&
+         std::min<int64_t>(kResident / cluster, rows) * places * static_cast<int64_t>(sizeof(T)) > kInL2)
+    cluster *= 2;
   a.slice = static_cast<int>(((places + cluster - 1) / cluster + kGrain - 1) / kGrain * kGrain);
   a.up = 31;  // sums of V weights stay below 2^63
   while ((int64_t{1} << (31 - a.up)) < a.vocab) --a.up;
