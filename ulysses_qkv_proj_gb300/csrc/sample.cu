@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
   const float temperature = a.temperature != nullptr ? a.temperature[req] : 1.f;
   const int top_k = a.top_k != nullptr ? a.top_k[req] : 0;
   const float top_p = a.top_p != nullptr ? a.top_p[req] : 1.f;
-  const float min_p = a.min_p != nullptr ? fminf(a.min_p[req], 1.f) : 0.f;
+  const float min_p = a.min_p != nullptr && a.min_p[req] > 0.f ? fminf(a.min_p[req], 1.f) : 0.f;
   const bool greedy = !(temperature > 0.f);
   const bool by_count = top_k > 0 && top_k < a.vocab, by_weight = top_p < 1.f;
 
