@@ -280,11 +280,13 @@ struct Row {
     return place >= shift && place < end ? clean(to_float(src[place - shift])) : -INFINITY;
   }
 
-  // f(logit, index) for every place of this warp's run.
-  template <typename F>
-  __device__ __forceinline__ void sweep(F f) const {
+  // f(logit, index) for every place of this warp's run, and some behind it as -inf, and after() behind each few: all lanes call
+  // together.  The loops stay short: with 16 logits unrolled the passes that weigh ran out of the instruction cache.
+  template <typename F, typename G>
+  __device__ __forceinline__ void sweep(F f, G after) const {
     const int from = warp() * run, to = from + run;
     if (KEEP) {
+#pragma unroll 1
       for (int y = from + lane() * 4; y < to; y += 128) {
         const float4 v = *reinterpret_cast<const float4*>(logit + y);
         const int index = place0 + y - shift;
@@ -292,23 +294,27 @@ struct Row {
         f(v.y, index + 1);
         f(v.z, index + 2);
         f(v.w, index + 3);
+        after();
       }
     } else {
-      constexpr int kAhead = 16 / kVec;  // 16 logits of a lane on their way at a time
-      for (int y0 = from + lane() * kVec; y0 < to; y0 += 32 * kVec * kAhead) {
-        float v[kAhead][kVec];
+      float v[kVec], next[kVec];
+      load(from + lane() * kVec < to ? place0 + from + lane() * kVec : end, v);
+#pragma unroll 1
+      for (int first = from; first < to; first += 32 * kVec) {
+        const int y = first + lane() * kVec, ahead = y + 32 * kVec;
+        load(ahead < to ? place0 + ahead : end, next);
+        const int index = place0 + y - shift;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (y0 + 32 * kVec * k < to) load(place0 + y0 + 32 * kVec * k, v[k]);
+        for (int i = 0; i < kVec; ++i) f(v[i], index + i);
+        after();
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (y0 + 32 * kVec * k < to) {
-            const int index = place0 + y0 + 32 * kVec * k - shift;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) f(v[k][i], index + i);
-          }
+        for (int i = 0; i < kVec; ++i) v[i] = next[i];
       }
     }
+  }
+  template <typename F>
+  __device__ __forceinline__ void sweep(F f) const {
+    sweep(f, [] {});
   }
   template <typename F>
   __device__ __forceinline__ void sweep_kept(F f) const {
@@ -345,6 +351,33 @@ struct Row {
     });
     __syncthreads();
     return lane() == 0 ? sh.runs[0][warp()] | static_cast<uint64_t>(sh.runs[1][warp()]) << 32 : 0;
+  }
+  // This warp's share of the weight of the kept tokens from `least` on, of which `few` are handed to f instead.  Kept
+  // tokens are packed in shared memory (the histogram's, which is done with) until there are enough for all lanes: weighed where
+  // they lie, a few of 32 lanes would cost as much as all.
+  template <typename P, typename F>
+  __device__ __forceinline__ uint64_t packed_weight(float least, P few, F f) {
+    constexpr int kRoom = kBins / kWarps;
+    float* queue = reinterpret_cast<float*>(hist) + warp() * kRoom;
+    uint64_t sum = 0;
+    int fill = 0;
+    auto flush = [&] {
+      __syncwarp();
+      for (int i = lane(); i < fill; i += 32) sum += weigh(queue[i]);
+      __syncwarp();
+      fill = 0;
+    };
+    sweep([&](float l, int index) {
+      const bool kept = l >= least && cut.keeps(l, index), apart = kept && few(l);
+      const uint32_t votes = __ballot_sync(0xFFFFFFFFu, kept && !apart);
+      if (kept && !apart) queue[fill + __popc(votes & ((1u << lane()) - 1u))] = l;
+      fill += __popc(votes);
+      if (apart) f(l, index);
+    }, [&] {
+      if (fill > kRoom - 32 * kVec) flush();
+    });
+    flush();
+    return sum;
   }
   // A 64-bit sum in two words, by two atomics.
   __device__ __forceinline__ static void add_to(uint32_t* low, uint32_t* high, int at, uint64_t w) {
@@ -850,23 +883,32 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
       }
       if (r.listed && tid < 2 * kWarps) sh.runs[0][tid] = 0;
       __syncthreads();
+      const float from = r.weight.least_of(last), before = r.weight.least_of(first - 1);
+      auto in_window = [&](float l) {
+        const int b = r.weight.bin(l) - first;
+        atomicAdd(&sh.window[0][b], 1u);
+        R::add_to(sh.window[1], sh.window[2], b, r.weigh(l));
+      };
       kept = 0;
-      const float from = r.weight.least_of(last);
-      r.each_kept([&](float l, int index) {
-        if (l < from) return;
-        const int b = r.weight.bin(l);
-        if (!r.listed && (list_now || (narrow && b >= first))) r.put(l, index);
-        if (b >= first && !narrow) return;
-        const uint64_t w = r.weigh(l);
-        if (b >= first) {
-          atomicAdd(&sh.window[0][b - first], 1u);
-          R::add_to(sh.window[1], sh.window[2], b - first, w);
-        } else if (r.listed) {
-          R::add_to(sh.runs[0], sh.runs[1], (index + r.shift - r.place0) / r.run, w);
-        } else {
-          kept += w;
-        }
-      });
+      if (!r.listed && !list_now) {
+        kept = r.packed_weight(from, [&](float l) { return l < before; }, [&](float l, int index) {
+          if (!narrow) return;
+          r.put(l, index);
+          in_window(l);
+        });
+      } else {
+        r.each_kept([&](float l, int index) {
+          if (l < from) return;
+          if (list_now) r.put(l, index);
+          if (l < before) {
+            if (narrow) in_window(l);
+          } else if (r.listed) {
+            R::add_to(sh.runs[0], sh.runs[1], (index + r.shift - r.place0) / r.run, r.weigh(l));
+          } else {
+            kept += r.weigh(l);
+          }
+        });
+      }
       if (r.listed) {
         __syncthreads();
         kept = lane == 0 ? sh.runs[0][warp] | static_cast<uint64_t>(sh.runs[1][warp]) << 32 : 0;
@@ -906,7 +948,6 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
       }
       const int to = narrow && room ? at : last;
       if (!narrow || !room || m > 0) r.template cut_at<true>(want - min(want, above), at, to, m, narrow && room);
-      const float before = r.weight.least_of(first - 1);
       kept += r.kept_weight([&](float l) { return l < before; });
       total = r.exchange(kept, 0).x;
     }
