@@ -799,7 +799,8 @@ qnre_status_t qnre_rope_table(float* cos_sin, int64_t n_pos, int rot, int64_t fi
  *            (a smaller multiple of page_size serves, too; what exceeds a member's tokens is cut off); n_groups == 0 and
  *            NULL: no row shares.  Rows of the call outside every group are served alone.
  *   depths   device int32 [n, nodes] or NULL (node j at depth j); read only with slopes.
- *   softcap  >= 0, finite; 0: none.      slopes  device fp32 [Hq] or NULL.
+ *   softcap  0: none; else at least 1e-30, finite, and so that scale / softcap is (QNRE_ERR_UNSUPPORTED).
+ *   slopes   device fp32 [Hq] or NULL.
  *   workspace  qnre_prefix_attention_workspace_bytes (n_groups: 0 or any other), 16-byte aligned, contents undefined before
  *            and after; calls that may overlap (on different streams) need one each.
  * Limits, errors and the care for masked and non-finite values are those of qnre_tree_attention; n nodes Hq <= 2^31-1.

@@ -90,7 +90,7 @@ def attention(lib, **kw):
     (dict(q=view(A + 200 * MB, [1025, 1, 8, 128])), 5), (dict(q=view(A + 200 * MB + 8, [2, 4, 8, 128])), 3),
     (dict(q=view(A + 200 * MB, [2, 1, 258, 128])), 2),
     (dict(layer=2), 1), (dict(layer=-1), 1), (dict(scale=0.0), 1), (dict(scale=NAN), 1), (dict(scale=INF), 1), (dict(cap=-1.0), 1),
-    (dict(cap=NAN), 1), (dict(cap=INF), 1), (dict(g=-1), 1), (dict(g=1025), 5), (dict(groups=None), 1), (dict(shared=None), 1),
+    (dict(cap=NAN), 1), (dict(cap=INF), 1), (dict(cap=1e-31), 2), (dict(cap=1e-20, scale=1e30), 2), (dict(g=-1), 1), (dict(g=1025), 5), (dict(groups=None), 1), (dict(shared=None), 1),
     (dict(rows=None), 1), (dict(rows=A + 2), 3), (dict(groups=A + 211 * MB + 2), 3), (dict(shared=A + 212 * MB + 1), 3),
     (dict(mask=A + 213 * MB + 4), 3), (dict(depths=A + 213 * MB + 2), 3), (dict(counts=A + 213 * MB + 2), 3),
     (dict(slopes=A + 213 * MB + 2), 3), (dict(out=None), 1), (dict(out=A + 220 * MB + 8), 3), (dict(ws=None), 1),

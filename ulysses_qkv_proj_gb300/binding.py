@@ -195,7 +195,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     for name in ("qnre_qk_norm_rope", "qnre_qk_norm_rope_backward", "qnre_qkv_norm_rope_append", "qnre_tree_attention",
                  "qnre_verify_tree", "qnre_cache_truncate", "qnre_cache_fork", "qnre_cache_reserve",
                  "qnre_cache_compact", "qnre_cache_copy_pages", "qnre_sample", "qnre_filter_probs",
-                 "qnre_cache_shared_prefix", "qnre_prefix_attention"):
+                 "qnre_cache_shared_prefix", "qnre_prefix_attention", "qnre_rope_table"):
         _entry[name] = ctypes.cast(getattr(lib, name), c_vp).value
     _lib = lib
     return lib
@@ -916,13 +916,18 @@ def qnre_rope_table(cos_sin, theta: float = 1e4, first: int = 0, scaling: str = 
     where = "qnre_rope_table"
     lib = load_library()
     kind = ROPE_SCALINGS.get(scaling, -1)
-    shape = _sizes(cos_sin)
-    if len(shape) != 2:
-        raise QnreError(1, f"{where}: cos_sin must be [n_pos, rot]")
     if high is None:
         high = 32.0 if kind == 3 else 4.0
     if magnitude is None:
         magnitude = 0.1 * math.log(factor) + 1.0 if kind == 3 and factor > 0 else 1.0
+    if _native is not None:
+        st = _native.rope_table(_entry[where], cos_sin, theta, first, kind, factor, original, low, high, magnitude, _stream_ptr,
+                                stream)
+        if st is not None:
+            return _check(st, where)
+    shape = _sizes(cos_sin)
+    if len(shape) != 2:
+        raise QnreError(1, f"{where}: cos_sin must be [n_pos, rot]")
     args = _f32(where, cos_sin), *shape, first, theta, ctypes.byref(_RopeScaling(kind, factor, original, low, high, magnitude))
     _on_device(where, cos_sin)
     _check(lib.qnre_rope_table(*args, _stream_ptr(stream)), where)

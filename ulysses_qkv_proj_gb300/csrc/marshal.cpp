@@ -470,6 +470,45 @@ PyObject* prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t argc) {
   });
 }
 
+bool read_double(PyObject* obj, double* out) {
+  if (PyFloat_Check(obj)) {
+    *out = PyFloat_AS_DOUBLE(obj);
+    return true;
+  }
+  if (!PyLong_Check(obj)) return false;
+  *out = PyLong_AsDouble(obj);
+  const bool read = PyErr_Occurred() == nullptr;
+  if (!read) PyErr_Clear();
+  return read;
+}
+
+// rope_table(fn, cos_sin, theta, first, kind, factor, original, low, high, magnitude, reader, stream)
+PyObject* rope_table(PyObject*, PyObject* const* args, Py_ssize_t argc) {
+  return guarded([&]() -> PyObject* {
+    void* fn;
+    float* out;
+    double theta;
+    int first;
+    qnre_rope_scaling_t s;
+    qnre_stream_t stream;
+    if (argc != 12 || !read_entry(args[0], &fn) || !THPVariable_Check(args[1])) Py_RETURN_NONE;
+    const at::Tensor& t = THPVariable_Unpack(args[1]);
+    if (t.dim() != 2 || t.size(1) > INT_MAX || !read_pointer(args[1], QNRE_DTYPE_FP32, {t.size(0), t.size(1)}, &out) ||
+        !read_double(args[2], &theta) || !read_int(args[3], &first) || !read_int(args[4], &s.kind) ||
+        !read_double(args[5], &s.factor) || !read_double(args[6], &s.original) || !read_double(args[7], &s.low) ||
+        !read_double(args[8], &s.high) || !read_double(args[9], &s.magnitude) || !on_device({args[1]}))
+      Py_RETURN_NONE;
+    const int64_t n_pos = t.size(0);
+    const int rot = static_cast<int>(t.size(1));
+    if (!read_stream(args[10], args[11], &stream)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = reinterpret_cast<decltype(&qnre_rope_table)>(fn)(out, n_pos, rot, first, theta, &s, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
 // Logits with `rank` axes, each row contiguous, and the settings of its requests: five arguments.
 struct Logits {
   const void* data;
@@ -558,6 +597,7 @@ PyMethodDef methods[] = {{"view4", view4, METH_O, nullptr},
                          {"compact", fast(compact), METH_FASTCALL, nullptr},
                          {"shared_prefix", fast(shared_prefix), METH_FASTCALL, nullptr},
                          {"prefix_attention", fast(prefix_attention), METH_FASTCALL, nullptr},
+                         {"rope_table", fast(rope_table), METH_FASTCALL, nullptr},
                          {"sample", fast(sample), METH_FASTCALL, nullptr},
                          {"filter", fast(filter), METH_FASTCALL, nullptr},
                          {"sizes", sizes, METH_O, nullptr},

@@ -1408,6 +1408,7 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
       layer >= cache->layers || !(scale > 0.f) || !std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap) ||
       n_groups < 0)
     return QNRE_ERR_INVALID_ARG;
+  if (softcap > 0.f && !(softcap >= 1e-30f && std::isfinite(scale / softcap))) return QNRE_ERR_UNSUPPORTED;
   if (own.shape[2] / cache->heads > kTile) return QNRE_ERR_UNSUPPORTED;
   if (own.shape[1] > QNRE_MAX_NODES || own.shape[2] > 65535 || n_groups > QNRE_MAX_CALL_ROWS) return QNRE_ERR_CAPACITY;
   if (!rows_vectorisable(&own, 2)) return QNRE_ERR_ALIGNMENT;
