@@ -52,6 +52,20 @@ constexpr int kUnitCost = 4;  // a unit's start and end, in tiles
 constexpr int kSmallRequests = 128, kSmallGroups = 31, kSmallBlocks = 32;  // (see Smem)
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Division of 0 <= x < 2^31 by a number that the host knows: a product and a shift (the divide is some 200 cycles of latency,
+// and every CTA's setup and every unit have several).
+struct Divisor {
+  uint32_t mul, shift;
+  static Divisor of(int d) {
+    uint32_t shift = 31;
+    while ((1ull << (shift - 31)) < static_cast<uint32_t>(d)) ++shift;
+    return Divisor{static_cast<uint32_t>((1ull << shift) / static_cast<uint32_t>(d) + 1), shift};  // (mul at most 2^31 + 1)
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * mul >> shift);
+  }
+};
+
 // Where a unit's results are: `parts` runs of it from CTA `cta` on, `step` apart; 0: one piece, in the rows' own places.
 struct Desc {
   int cta, step, parts;
@@ -78,6 +92,7 @@ struct PrefixArgs {
   int layer, n, n_groups, nodes, Hq, Hk, G, box, cl;
   int unit_nodes, unit_members, row_tiles;  // nodes and requests of a unit; units that one request's nodes take
   int warp_members;                         // requests whose rows one warp has
+  Divisor by_page, by_G, by_nodes, by_members, by_tiles, by_cl;  // of page_size, G, unit_nodes, unit_members, row_tiles, cl
   bool backward;  // tiles from the last to the first: where the bias favours near tokens the maxima do not grow tile by tile
 };
 
@@ -151,11 +166,12 @@ struct Cursor {
   const int* pre;
   int cur, end, item, index, count, quot, rem;  // run `index` of `count`
   int n, Hk, cl, rank, row_tiles, unit_members;
+  Divisor by_members, by_cl;
   bool wide;
 
   // Units of a group for one K head, and those of them that clusters take.
-  __device__ __forceinline__ int units_of(int members) const { return (members + unit_members - 1) / unit_members * row_tiles; }
-  __device__ __forceinline__ int shared_units(int units) const { return cl > 1 ? units / cl * cl : 0; }
+  __device__ __forceinline__ int units_of(int members) const { return by_members(members + unit_members - 1) * row_tiles; }
+  __device__ __forceinline__ int shared_units(int units) const { return cl > 1 ? by_cl(units) * cl : 0; }
   __device__ __forceinline__ int start_of(int c) const { return c * quot + c * rem / count; }
   __device__ __forceinline__ bool next(Seg& s) {
     while (cur < end) {
@@ -168,7 +184,7 @@ struct Cursor {
         s.members = t.starts[g + 1] - s.start;
         s.tokens = t.common[g];
         const int units = units_of(s.members), full = shared_units(units);
-        per_head = wide ? full / cl : units - full;
+        per_head = wide ? by_cl(full) : units - full;
         first = wide ? 0 : full;
       } else {
         s.start = item * unit_members;
@@ -242,11 +258,11 @@ struct UnitRow {
   int member, node, head;  // member: of the unit
   bool there;
 };
-__device__ __forceinline__ int unit_tile(const PrefixArgs& a, const Seg& s) { return s.group ? s.rt / a.row_tiles : 0; }
+__device__ __forceinline__ int unit_tile(const PrefixArgs& a, const Seg& s) { return s.group ? a.by_tiles(s.rt) : 0; }
 __device__ __forceinline__ UnitRow unit_row(const PrefixArgs& a, const Seg& s, int ur) {
-  const int q = ur / a.G, tile = unit_tile(a, s), block = s.rt - tile * a.row_tiles;
+  const int q = a.by_G(ur), tile = unit_tile(a, s), block = s.rt - tile * a.row_tiles;
   UnitRow r;
-  r.member = q / a.unit_nodes;
+  r.member = a.by_nodes(q);
   r.node = block * a.unit_nodes + q - r.member * a.unit_nodes;
   r.head = ur - q * a.G;
   r.there = r.member < a.unit_members && tile * a.unit_members + r.member < s.members && r.node < a.nodes;
@@ -301,7 +317,7 @@ __device__ void run_producer(const PrefixArgs& a, const Bars& bars, uint32_t sme
       table = a.c.table + static_cast<long long>(fetches ? row : 0) * a.c.max_blocks;
     };
     auto look = [&] {
-      const int block = pos / ps;
+      const int block = a.by_page(pos);
       off = pos - block * ps;
       entry = fetches && pos < end && block < a.c.max_blocks ? __ldg(table + block) : -1;
     };
@@ -852,13 +868,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   t.common = table(L::kCommon);
   t.single = table(L::kSingle);
   t.wide = table(L::kWide);
-  t.blocks = (a.n + a.unit_members - 1) / a.unit_members;
+  t.blocks = a.by_members(a.n + a.unit_members - 1);
   t.n_groups = a.n_groups;
   cur.n = a.n;
   cur.Hk = a.Hk;
   cur.cl = a.cl;
   cur.row_tiles = a.row_tiles;
   cur.unit_members = a.unit_members;
+  cur.by_members = a.by_members;
+  cur.by_cl = a.by_cl;
   if (warp == kSoftWarps) ptx::tmem_alloc(ptx::smem_addr(&words->tmem), 512);
   if (warp == kSoftWarps + 1 && lane == 0) {
     words->abort = 0;
@@ -886,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       if (i < a.n && blockIdx.x == 0) atomicOr(a.c.status, QNRE_CACHE_BAD_ROW);
     }
     if (i <= a.n_groups) t.starts[i] = min(max(start, 0), a.n);
-    if (i < a.n_groups) t.common[i] = min(max(common, 0), room) / ps * ps;
+    if (i < a.n_groups) t.common[i] = a.by_page(min(max(common, 0), room)) * ps;
     if (i < a.n) {
       t.len[i] = len;
       t.drafts[i] = static_cast<uint8_t>(min(len + cnt, room) - len);
@@ -905,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       const int g = lo >= 0 && i < t.starts[lo + 1] ? lo : -1;
       t.base[i] = g;
       // no more than every member has, in whole pages; nothing where there is only one
-      if (g >= 0) atomicMin(&t.common[g], t.starts[g + 1] - t.starts[g] > 1 ? t.len[i] / ps * ps : 0);
+      if (g >= 0) atomicMin(&t.common[g], t.starts[g + 1] - t.starts[g] > 1 ? a.by_page(t.len[i]) * ps : 0);
     }
     __syncthreads();
   }
@@ -913,23 +931,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int g = a.n_groups > 0 ? t.base[i] : -1;
     const int base = g >= 0 ? t.common[g] : 0;
     t.base[i] = base;
-    atomicAdd(&t.single[i / a.unit_members + 1], tiles_of(t.len[i] + t.drafts[i] - base));
+    atomicAdd(&t.single[a.by_members(i) + 1], tiles_of(t.len[i] + t.drafts[i] - base));
     if (blockIdx.x == 0) a.requests[i] = make_int2(base > 0 ? t.starts[g] : -1, base);
   }
+  for (int g = kThreads - 1 - tid; g < a.n_groups; g += kThreads) {  // a unit's tiles and its start and end, times units
+    const int units = cur.units_of(t.starts[g + 1] - t.starts[g]), full = cur.shared_units(units);
+    const int each = t.common[g] > 0 ? (tiles_of(t.common[g]) + kUnitCost) * a.Hk : 0;
+    t.single[t.blocks + g + 1] = each * (units - full);
+    t.wide[g + 1] = each * a.by_cl(full);
+  }
   __syncthreads();
-  // one warp each: a unit's tiles and its start and end, times units
-  auto group_items = [&](int g, bool wide) {
-    const int members = t.starts[g + 1] - t.starts[g], units = cur.units_of(members), full = cur.shared_units(units);
-    return t.common[g] > 0 ? (tiles_of(t.common[g]) + kUnitCost) * a.Hk * (wide ? full / a.cl : units - full) : 0;
-  };
   const int n_single = t.blocks + a.n_groups;
   if (warp == 0) {
     scan_table<false>(t.single + 1, n_single, [&](int i) {
-      return i < t.blocks ? (t.single[i + 1] + kUnitCost) * a.Hk * a.row_tiles : group_items(i - t.blocks, false);
+      return i < t.blocks ? (t.single[i + 1] + kUnitCost) * a.Hk * a.row_tiles : t.single[i + 1];
     });
     if (lane == 0) t.single[0] = 0;
   } else if (warp == 1) {
-    scan_table<false>(t.wide + 1, a.n_groups, [&](int g) { return group_items(g, true); });
+    scan_table<false>(t.wide + 1, a.n_groups, [&](int g) { return t.wide[g + 1]; });
     if (lane == 0) t.wide[0] = 0;
   }
   __syncthreads();
@@ -1459,10 +1478,16 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
   a.row_tiles = (nodes + a.unit_nodes - 1) / a.unit_nodes;
   a.unit_members = a.row_tiles > 1 ? 1 : std::max(1, kTile / a.G / nodes);
   a.warp_members = std::max(1, 32 / (a.G * a.unit_nodes));
+  a.by_page = Divisor::of(cache->page_size);
+  a.by_G = Divisor::of(a.G);
+  a.by_nodes = Divisor::of(a.unit_nodes);
+  a.by_members = Divisor::of(a.unit_members);
+  a.by_tiles = Divisor::of(a.row_tiles);
   // CTAs of a cluster: the units that a group of average size has for a K head
   const int members = n_groups > 0 ? (n + n_groups - 1) / n_groups : 0;
   const int units = (members + a.unit_members - 1) / a.unit_members * a.row_tiles;
   a.cl = std::min(std::max(units, 1), kMaxCluster);
+  a.by_cl = Divisor::of(a.cl);
   const int64_t tiles = (static_cast<int64_t>(cache->max_blocks) * cache->page_size + kTile - 1) / kTile + kUnitCost;
   if (2 * a.n * tiles * a.Hk * a.row_tiles > 0x7FFFFFFF || static_cast<int64_t>(out_rows) > 0x7FFFFF00) return QNRE_ERR_CAPACITY;
   a.box = std::min(a.cl > 1 ? kTile / kMaxCluster : kTile, cache->page_size & -cache->page_size);
