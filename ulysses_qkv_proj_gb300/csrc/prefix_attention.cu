@@ -810,19 +810,19 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
   }
 }
 
-// x[0 .. n) to its running sums (or maxima), x given by f; one warp.
-template <bool MAXIMUM, typename F>
-__device__ __forceinline__ void scan_table(int* x, int n, F f) {
+// x[0 .. n) to its running sums or maxima; one warp.  One copy of the code: a CTA runs its setup once, so each line of it is
+// fetched from L2.
+__device__ __noinline__ void scan_table(int* x, int n, bool maximum) {
   const int lane = threadIdx.x % 32;
   int carry = 0;
   for (int base = 0; base < n; base += 32) {
-    int v = base + lane < n ? f(base + lane) : 0;
-#pragma unroll
+    int v = base + lane < n ? x[base + lane] : 0;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-      if (lane >= o) v = MAXIMUM ? max(v, u) : v + u;
+      if (lane >= o) v = maximum ? max(v, u) : v + u;
     }
-    v = MAXIMUM ? max(v, carry) : v + carry;
+    v = maximum ? max(v, carry) : v + carry;
     if (base + lane < n) x[base + lane] = v;
     carry = __shfl_sync(0xFFFFFFFFu, v, 31);
   }
@@ -885,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     ptx::prefetch_tensormap(&a.tv);
     ptx::prefetch_tensormap(&a.tq);
   }
-  for (int i = tid; i < t.blocks; i += kThreads) t.single[i + 1] = 0;
+  for (int i = tid; i < t.blocks; i += kThreads) t.single[i + 1] = kUnitCost * a.Hk * a.row_tiles;
 
   // Lengths, common tokens, and where the items begin in the two concatenated runs.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   }
   __syncthreads();
   if (a.n_groups > 0) {
-    if (warp == 0) scan_table<true>(t.starts, a.n_groups + 1, [&](int i) { return t.starts[i]; });  // (ascending, whatever is given)
+    if (warp == 0) scan_table(t.starts, a.n_groups + 1, true);  // (ascending, whatever is given)
     __syncthreads();
     for (int i = tid; i < a.n; i += kThreads) {
       int lo = -1, hi = a.n_groups - 1;  // the last group that starts by i
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int g = a.n_groups > 0 ? t.base[i] : -1;
     const int base = g >= 0 ? t.common[g] : 0;
     t.base[i] = base;
-    atomicAdd(&t.single[a.by_members(i) + 1], tiles_of(t.len[i] + t.drafts[i] - base));
+    atomicAdd(&t.single[a.by_members(i) + 1], tiles_of(t.len[i] + t.drafts[i] - base) * a.Hk * a.row_tiles);
     if (blockIdx.x == 0) a.requests[i] = make_int2(base > 0 ? t.starts[g] : -1, base);
   }
   for (int g = kThreads - 1 - tid; g < a.n_groups; g += kThreads) {  // a unit's tiles and its start and end, times units
@@ -942,15 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   }
   __syncthreads();
   const int n_single = t.blocks + a.n_groups;
-  if (warp == 0) {
-    scan_table<false>(t.single + 1, n_single, [&](int i) {
-      return i < t.blocks ? (t.single[i + 1] + kUnitCost) * a.Hk * a.row_tiles : t.single[i + 1];
-    });
-    if (lane == 0) t.single[0] = 0;
-  } else if (warp == 1) {
-    scan_table<false>(t.wide + 1, a.n_groups, [&](int g) { return t.wide[g + 1]; });
-    if (lane == 0) t.wide[0] = 0;
-  }
+  if (tid == 0) t.single[0] = t.wide[0] = 0;
+  if (warp < 2) scan_table((warp == 0 ? t.single : t.wide) + 1, warp == 0 ? n_single : a.n_groups, false);
   __syncthreads();
 
   // The clusters that share tiles: in proportion to the work, so that the longest run of either kind is the shortest.
