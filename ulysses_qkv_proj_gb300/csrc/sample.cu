@@ -68,13 +68,10 @@ struct SampleArgs {
   int rows_per, vocab, slice, up;  // rows of a request; places of a CTA; binary places of a weight beyond 31
 };
 
-// 2^(-j/1024) in units of 2^-31, as an integer and as a float, from 2^(-i/32) and 2^(-i/1024).
-struct Power {
-  uint32_t bits;
-  float value;
-};
-struct PowerTable {
-  Power at[1024];
+// 2^(-j/1024) in units of 2^-31, from 2^(-i/32) and 2^(-i/1024).  Each CTA holds it in shared memory: 32 lanes' places of it lie
+// in as many lines, and from L1 a warp's loads cost more than all else that weighs a token.
+struct alignas(16) PowerTable {
+  uint32_t at[1024];
 };
 constexpr uint64_t kCoarse[32] = {
     0x8000000000000000ull, 0x7D41D96DB915019Dull, 0x7A92BE8A92436616ull, 0x77F25CCDEE6D7AE6ull,
@@ -104,8 +101,7 @@ constexpr PowerTable make_powers() {
   PowerTable t{};
   for (int j = 0; j < 1024; ++j) {
     const uint64_t x = product63(kCoarse[j / 32], kFine[j % 32]);
-    t.at[j].bits = static_cast<uint32_t>((x + (1ull << 31)) >> 32);
-    t.at[j].value = static_cast<float>(t.at[j].bits);
+    t.at[j] = static_cast<uint32_t>((x + (1ull << 31)) >> 32);
   }
   return t;
 }
@@ -122,6 +118,7 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 
 // A row's scale: weights are 2^(-y), y = (max - l) c, c = log2(e) / T as a pair of floats.
 struct Weight {
+  const uint32_t* power;
   float max, ch, cl;
   static constexpr float kMagic = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, in the low bits
   static constexpr float kLimit = 4095.f;
@@ -158,9 +155,10 @@ struct Weight {
     const float r = fmaf(e, 1024.f, fmaf(p, 1024.f, static_cast<float>(-k)));         // behind the steps
     const float t = r * 0.00067690154f;                                               // ln 2 / 1024
     const float c = t * fmaf(t, fmaf(t, -0.16666667f, 0.5f), -1.f);                   // e^-t - 1
-    const Power power = kPowers.at[k & 1023];
+    const uint32_t bits = power[k & 1023];
+    const float value = __uint_as_float((bits >> 7) + (156u << 23));                  // bits, to 23 places
     n = k >> 10;
-    return power.bits + (__float_as_int(fmaf(power.value, c, kMagic)) - __float_as_int(kMagic));
+    return bits + (__float_as_int(fmaf(value, c, kMagic)) - __float_as_int(kMagic));
   }
   // In units of 2^-scale, scale = 31 + `up`.
   __device__ __forceinline__ uint64_t fixed(float l, int up) const {
@@ -180,6 +178,7 @@ struct Cut {
 };
 
 struct Shared {
+  PowerTable power;
   uint64_t sums[2][2][kMaxCluster];  // two sums of each of the cluster's CTAs, two uses in turn
   uint64_t warp[2][kWarps];
   uint64_t scratch[kWarps];
@@ -701,6 +700,8 @@ template <typename T, bool FILTER, bool KEEP>
 __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const SampleArgs a) {
   __shared__ Shared sh;
   extern __shared__ __align__(16) char dynamic[];
+  static_assert(sizeof(PowerTable) == kThreads * sizeof(uint4), "16 bytes a thread");
+  reinterpret_cast<uint4*>(sh.power.at)[threadIdx.x] = reinterpret_cast<const uint4*>(kPowers.at)[threadIdx.x];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint32_t ncta;
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
         0,
         a.slice / kWarps,
         a.up,
-        Weight{0.f, 0.f, 0.f},
+        Weight{sh.power.at, 0.f, 0.f, 0.f},
         Cut{-INFINITY, -1},
         0,
         false};
@@ -946,9 +947,12 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
         }
         ptx::cluster_sync();  // (all have read the windows before a list is gathered and the counts are reset)
       }
+      const bool whole = r.listed;
+      r.listed |= narrow && room && m > 0;  // (of what lies behind `before`, all that may be kept)
       const int to = narrow && room ? at : last;
       if (!narrow || !room || m > 0) r.template cut_at<true>(want - min(want, above), at, to, m, narrow && room);
       kept += r.kept_weight([&](float l) { return l < before; });
+      r.listed = whole;
       total = r.exchange(kept, 0).x;
     }
   }
