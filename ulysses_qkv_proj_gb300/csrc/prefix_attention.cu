@@ -22,6 +22,16 @@
 // Values that a row must not see: as in tree_attention.cu scores are replaced before use and V behind a row's tokens is zeroed.  A
 // non-finite V of one request's own tokens would meet the zeros of the others' P, and 0 inf is NaN.  So a row whose own part is
 // not finite is marked, and the join computes that part again by itself, token by token (own_part): slow, and only there.
+//
+// Bound: long common prefixes and many rows, by a tile's two products and its softmax, which share the SM's tensor memory
+// and issue slots: 128 tokens by 128 rows of D = 128 take 1840 cycles where the products alone are 1024.  128 requests of 64 + 8
+// heads with 6 prefixes of 1500 to 30011 tokens take 115 us (the tensor pipe busy 44 % of it), against 642 when each request reads
+// its prefix.  Own tokens, by the bytes that a few rows each need: 48 requests of up to 3000 own tokens 85 us, floor 27.  Short
+// calls, by latency: 8 requests of 2011 + up to 400 tokens 17.7 us, of them the setup 4, a unit's start and end 4, the join 3.
+// Blocks of many requests' own tokens brought the first case from 124 us to 117, a form with smaller tables and a third V stage
+// to 115, the capped case 122 -> 107, and the polynomial for tanh 107 -> 85.  Divisors as products took the setup from 9500
+// cycles to 7640.  Tried and left: turns
+// of four requests' tiles in a block (127 us for 121).
 #include "../../include/qnre.h"
 #include "attention_tile.cuh"
 #include "cache.cuh"
@@ -273,7 +283,8 @@ __device__ __forceinline__ UnitRow unit_row(const PrefixArgs& a, const Seg& s, i
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
 
 // ------------------------------------------------------------------ TMA warps
-// One warp brings K, another Q and V (so that K of the next unit does not wait for the last use of Q).  With `share` each CTA of the cluster fetches its share of a tile's boxes for all.
+// One warp brings K, another Q and V (so that K of the next unit does not wait for the last use of Q).  With `share` each CTA
+// of the cluster fetches its share of a tile's boxes for all.
 template <typename L, int D>
 __device__ void run_producer(const PrefixArgs& a, const Bars& bars, uint32_t smem, Cursor cur, Seg s, bool more, int kv,
                              bool share, volatile uint32_t* abort_flag) {

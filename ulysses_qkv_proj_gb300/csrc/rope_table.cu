@@ -9,7 +9,9 @@
 // polynomials of odd and even powers, fitted for the least relative error by weighted least squares (4e-9 and
 // 6e-11 before rounding; evaluated in fp32 at most 0.8 and 1.0 units in the last place off, 0.3 on average).
 //
-// Bound: HBM writes (a thread forms four pairs of a row and writes two 16-byte pieces).
+// Bound: HBM writes: 524288 positions of 512 bytes take 44.2 us, 6.1 TB/s.  A thread forms four pairs of a row and writes two
+// 16-byte pieces, and goes on to the same pairs of three more rows, so that the frequencies are loaded once for four (with sincospif
+// and a row a thread it was bound by instructions and took 129 us).
 #include "../../include/qnre.h"
 #include "api_util.cuh"
 
