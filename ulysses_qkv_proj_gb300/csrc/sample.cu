@@ -210,6 +210,14 @@ template <>
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <>
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16(x); }
+template <>
+__device__ __forceinline__ __half from_float(float x) { return __float2half(x); }
 
 // Words of the cluster's CTAs, by the address of this CTA's own.
 __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
@@ -268,20 +276,20 @@ struct Row {
 
   __device__ __forceinline__ uint64_t weigh(float l) const { return weight.fixed(l, up); }
 
-  // Eight or four logits from place `place` on (a 16-byte boundary); what is no logit of the row, or NaN, as -inf.
-  __device__ __forceinline__ void load(int place, float (&v)[kVec]) const {
-    if (place >= shift && place + kVec <= end) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + (place - shift)));
-      const T* t = reinterpret_cast<const T*>(&w);
+  // Eight or four logits from place `place` on (a 16-byte boundary), as they lie in memory; what is no logit of the row as -inf.
+  __device__ __forceinline__ uint4 fetch(int place) const {
+    if (place >= shift && place + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(src + (place - shift)));
+    uint4 w;
+    T* t = reinterpret_cast<T*>(&w);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = to_float(t[i]);
-    } else {
+    for (int i = 0; i < kVec; ++i)
+      t[i] = place + i >= shift && place + i < end ? src[place + i - shift] : from_float<T>(-INFINITY);
+    return w;
+  }
+  __device__ __forceinline__ static void decode(uint4 w, float (&v)[kVec]) {  // (NaN: -inf)
+    const T* t = reinterpret_cast<const T*>(&w);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        v[i] = place + i >= shift && place + i < end ? to_float(src[place + i - shift]) : -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = clean(v[i]);
+    for (int i = 0; i < kVec; ++i) v[i] = clean(to_float(t[i]));
   }
   __device__ __forceinline__ static float clean(float v) { return fminf(fmaxf(v, -INFINITY), 3.4028234664e38f); }  // (NaN: -inf)
   __device__ __forceinline__ float at(int y) const {  // place y of this CTA
@@ -307,18 +315,18 @@ struct Row {
         after();
       }
     } else {
-      float v[kVec], next[kVec];
-      load(from + lane() * kVec < to ? place0 + from + lane() * kVec : end, v);
+      // (the next words stay as they are: converted here they would be waited for before this step's work)
+      uint4 next = fetch(from + lane() * kVec < to ? place0 + from + lane() * kVec : end);
 #pragma unroll 1
       for (int first = from; first < to; first += 32 * kVec) {
         const int y = first + lane() * kVec, ahead = y + 32 * kVec;
-        load(ahead < to ? place0 + ahead : end, next);
+        float v[kVec];
+        decode(next, v);
+        next = fetch(ahead < to ? place0 + ahead : end);
         const int index = place0 + y - shift;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) f(v[i], index + i);
         after();
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = next[i];
       }
     }
   }
@@ -756,20 +764,22 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
   float mx = -INFINITY;
   constexpr int kVec = R::kVec, kAhead = 32 / kVec;
   for (int y0 = tid * kVec; y0 < a.slice; y0 += kThreads * kVec * kAhead) {
-    float v[kAhead][kVec];
+    uint4 words[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (y0 + kThreads * kVec * k < a.slice) r.load(r.place0 + y0 + kThreads * kVec * k, v[k]);
+      if (y0 + kThreads * kVec * k < a.slice) words[k] = r.fetch(r.place0 + y0 + kThreads * kVec * k);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int y = y0 + kThreads * kVec * k;
       if (y >= a.slice) break;
+      float v[kVec];
+      R::decode(words[k], v);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) mx = fmaxf(mx, v[k][i]);
+      for (int i = 0; i < kVec; ++i) mx = fmaxf(mx, v[i]);
       if (KEEP) {
 #pragma unroll
         for (int i = 0; i < kVec; i += 4)
-          *reinterpret_cast<float4*>(r.logit + y + i) = make_float4(v[k][i], v[k][i + 1], v[k][i + 2], v[k][i + 3]);
+          *reinterpret_cast<float4*>(r.logit + y + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
   }
