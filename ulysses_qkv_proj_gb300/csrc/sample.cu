@@ -171,13 +171,12 @@ struct Weight {
     n = k >> 10;
     return bits + (__float_as_int(fmaf(value, c, kMagic)) - __float_as_int(kMagic));
   }
-  // In units of 2^-scale, scale = 31 + `up`.
+  // In units of 2^-(31 + up), rounded; without a branch, so that a lane's logits overlap.
   __device__ __forceinline__ uint64_t fixed(float l, int up) const {
     int n;
-    const uint32_t m = (*this)(l, n);
-    if (n <= up) return static_cast<uint64_t>(m) << (up - n);
-    const int down = n - up;
-    return down > 31 ? 0 : (m + (1u << (down - 1))) >> down;
+    const uint64_t x = static_cast<uint64_t>((*this)(l, n)) << up;
+    n = min(n, 63);  // (nothing is left of 2^61 and less; up is 31 for a single token alone)
+    return (x + ((1ull << n) >> 1)) >> n;
   }
 };
 
@@ -747,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
         a.slice / kWarps,
         a.up,
         Weight{sh.power.at, 0.f, 0.f, 0.f},
-        Cut{-INFINITY, -1},
+        Cut{-INFINITY, INT_MIN},  // (places before the row's first have indexes below 0)
         0,
         false};
   r.place0 = static_cast<int>(r.rank) * a.slice;
@@ -834,10 +833,25 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
       if (least > -INFINITY) r.cut.least = nextafterf(__double2float_ru(least), -INFINITY);
     }
     uint64_t kept = 0;  // this thread's
-    r.sweep_kept([&](float l, int) {
-      if (by_count || by_weight) atomicAdd(&r.hist[r.weight.bin(l)], 1u);
-      if (!by_count) kept += r.weigh(l);
-    });
+    // Without a bound every logit is weighed, so that a lane's are not branches of their own (and -inf is taken out: behind
+    // an infinite temperature its weight is 1).
+    auto weigh = [&](float l) {
+      const uint64_t w = r.weigh(l);
+      return l > -INFINITY ? w : 0;
+    };
+    if (min_p > 0.f || by_count) {
+      r.sweep_kept([&](float l, int) {
+        if (by_count || by_weight) atomicAdd(&r.hist[r.weight.bin(l)], 1u);
+        if (!by_count) kept += r.weigh(l);
+      });
+    } else if (by_weight) {
+      r.sweep([&](float l, int) {
+        if (l > -INFINITY) atomicAdd(&r.hist[r.weight.bin(l)], 1u);
+        kept += weigh(l);
+      });
+    } else {
+      r.sweep([&](float l, int) { kept += weigh(l); });
+    }
     int k_bin = kBins;
     uint32_t k_rest = 0;  // what is kept of it
     if (by_count || by_weight) {
