@@ -24,16 +24,17 @@
 // independent; none of its instructions is a conversion or 64 bits wide but the last).  Integer sums do not depend
 // on their order, so counters and lists filled in any order change no result.
 //
-// Bound: for few rows, latency: one row of 32003 logits takes 7.8 us (6.1 in the kernel, of them 1.9 the maximum over the
-// cluster, 1.9 the weights, 2 the draw), 20 rows with top_k 24 (each phase's code runs once, so it is fetched as it runs). For
-// many rows, the passes over every logit: counting 32 of them costs 10 cycles of the SM (an atomic each, on 32 banks),
-// weighing them 10 and more, so 256 rows of 131075 take 253 us where reading them once would take 10, and 1024 such rows
-// written as probabilities 673 us. What the passes cost before: logits read in runs of 16 (out of the instruction cache) 1014;
-// weights looked up in L1 318; kept tokens weighed where they lie, not packed, 412; the window's weights in a pass of their
-// own, 30 more.
-// Tried and left: more and smaller CTAs for many rows (8 an SM: 246, but 64 rows 149 for 93; 16 an SM: 285), skipping groups
-// of logits that nobody keeps (331 for 318), loads of 8 bytes (262 for 253), zeros written before the cut is known (24.7 for
-// 24.3).
+// Bound: for few rows, latency: one row of 32003 logits takes 6.9 us (about 2 each for the maximum over the cluster, the
+// weights and the draw), 20 rows with top_k 24 (each phase's code runs once, so it is fetched as it runs). For many rows,
+// instructions: counting and weighing a logit are some 60, and every SM issues at about half its rate behind fixed latencies,
+// so 256 rows of 131075 take 235 us where reading them once would take 10, and 1024 such rows written as probabilities 590.
+// What the passes cost those 256 rows on the way (each of the later steps with the ones before): logits read in runs of 16,
+// out of the instruction cache, 1014 us; short loops 412; kept tokens packed before they are weighed 318; powers from shared
+// memory rather than L1, and the window's weights from the CTA's list rather than a pass of their own, 253; words converted
+// when their turn comes 243; no branch around a weight 235.
+// Tried and left: more and smaller CTAs for many rows (8 an SM: 246 us for 253, but 64 rows 149 for 93; 16 an SM: 285),
+// skipping groups of logits that nobody keeps (331 for 318), loads of 8 bytes (262 for 253), zeros written before the cut is
+// known (24.7 for 24.3), four packed weights at a time (237 for 236).
 #include "../../include/qnre.h"
 #include "api_util.cuh"
 #include "ptx.cuh"
@@ -80,7 +81,7 @@ struct SampleArgs {
 };
 
 // 2^(-j/1024) in units of 2^-31, from 2^(-i/32) and 2^(-i/1024).  Each CTA holds it in shared memory: 32 lanes' places of it lie
-// in as many lines, and from L1 a warp's loads cost more than all else that weighs a token.
+// in as many lines, so that from L1 each look-up of a warp took some 30 turns.
 struct alignas(16) PowerTable {
   uint32_t at[1024];
 };
