@@ -104,6 +104,16 @@ def test_prefix_attention_arguments(lib, kw, want):
     assert attention(lib, **kw) == want
 
 
+@pytest.mark.parametrize("name", ["out", "lse", "ws"])
+@pytest.mark.parametrize("at", [128, 129, 131])
+def test_prefix_attention_keeps_off_the_cache_state(lib, name, at):
+    c = cache(rows=4, max_blocks=4)
+    if name == "ws":  # (it would reach the query otherwise)
+        c = cache(block_table=A + 300 * MB, seq_lens=A + 301 * MB, status=A + 303 * MB)
+        at += 172
+    assert attention(lib, c=c, **{name: A + at * MB}) == 4
+
+
 def test_prefix_workspace(lib):
     def need(*a):
         n = ctypes.c_uint64()

@@ -323,14 +323,14 @@ __device__ void run_producer(const PrefixArgs& a, const Bars& bars, uint32_t sme
     const int32_t* table = nullptr;
     int pos = 0, end = 0, entry = -1, off = 0;
     auto enter = [&](int request) {
-      const int row = __ldg(a.rows + request);
+      const int row = a.rows[request];
       fetches = active && row >= 0 && row < a.c.rows;
       table = a.c.table + static_cast<long long>(fetches ? row : 0) * a.c.max_blocks;
     };
     auto look = [&] {
       const int block = a.by_page(pos);
       off = pos - block * ps;
-      entry = fetches && pos < end && block < a.c.max_blocks ? __ldg(table + block) : -1;
+      entry = fetches && pos < end && block < a.c.max_blocks ? table[block] : -1;
     };
     if (s.group) {
       enter(s.start);
@@ -1340,8 +1340,8 @@ __global__ void __launch_bounds__(1024) shared_prefix_kernel(CacheView c, const 
         const int b = b0 + k * 32 + lane;
         mine[k] = first[k] = -1;
         if (b < blocks) {
-          mine[k] = __ldg(table + b);
-          first[k] = __ldg(table0 + b);
+          mine[k] = table[b];
+          first[k] = table0[b];
         }
       }
 #pragma unroll
@@ -1456,7 +1456,10 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
                              words(mask, tokens * 8),
                              words(depths, tokens * 4),
                              words(counts, static_cast<uint64_t>(n) * 4),
-                             words(slopes, static_cast<uint64_t>(Hq) * 4)};
+                             words(slopes, static_cast<uint64_t>(Hq) * 4),
+                             span(cache->block_table, static_cast<uint64_t>(cache->rows) * cache->max_blocks * 4),
+                             span(cache->seq_lens, static_cast<uint64_t>(cache->rows) * 4),
+                             span(cache->status, 4)};
   for (int i = 0; i < 3; ++i) {
     for (const ByteRange& r : reads)
       if (overlaps(writes[i], r)) return QNRE_ERR_ALIAS;

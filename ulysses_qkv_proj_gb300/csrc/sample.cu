@@ -278,7 +278,7 @@ struct Row {
 
   // Eight or four logits from place `place` on (a 16-byte boundary), as they lie in memory; what is no logit of the row as -inf.
   __device__ __forceinline__ uint4 fetch(int place) const {
-    if (place >= shift && place + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(src + (place - shift)));
+    if (place >= shift && place + kVec <= end) return *reinterpret_cast<const uint4*>(src + (place - shift));
     uint4 w;
     T* t = reinterpret_cast<T*>(&w);
 #pragma unroll
