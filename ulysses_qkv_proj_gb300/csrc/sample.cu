@@ -11,8 +11,9 @@
 //   max        while the row arrives; every CTA learns it through the cluster's shared memory,
 //   histogram  counts over 4096 bins of log2(e) (max - l) / T, 1/128 wide, which orders tokens coarsely; each CTA adds up its
 //              share of the bins over the cluster.  The bin of the top_k-th token is exact from the counts.  For top_p
-//              the counts bound the weight above each bin, and the one behind it, from both sides (a bin spans 0.54 %), so
-//              the cut falls into one of a few bins, whose weights are then added up exactly,
+//              the counts bound the weight up to each bin, and the one behind it, from both sides (a bin spans 0.54 %), so
+//              the cut falls into one of a few bins; one pass then adds up exactly the weight before them, theirs by bins
+//              and the row's, which the bounds do without,
 //   cut        the tokens of the one bin go to the first CTA, which sorts them and finds the last one kept; bins of more
 //              than 1024 (ties, logits beyond the bins' range) are cut by four rounds of eight key bits,
 //   draw       the kept weight by warps' runs of places; the run that holds the number is added up place by place.
@@ -199,7 +200,7 @@ struct Shared {
   uint32_t window[3][kWindow];       // of these bins: tokens, weights' low and high words
   uint32_t runs[2][kWarps];          // a list's weight in each run, low and high words
   uint32_t put_count, list_count;
-  int bin[4], tie, low, high;
+  int bin[2], tie, low, high;
 };
 
 template <typename T>
@@ -444,13 +445,10 @@ struct Row {
     return t;
   }
 
-  // sh.bin[i]: the first bins whose running sums of f(bin) reach targets[i] (x for the even i, y for the odd; the last bin where
-  // none does); sh.before what lies before the first of them in x, sh.high its own x.  Targets come from the totals.
-  struct Targets {
-    uint64_t at[4];
-  };
+  // sh.bin[i]: the first bin with which reach(the bins' sum, i, their running sum) holds (the last bin where none does; never
+  // before the first token); sh.before what lies before the first of them in x, sh.high its own x.
   template <typename F, typename G>
-  __device__ Pair find_bins(F f, G targets_of) {
+  __device__ Pair find_bins(F f, G reach) {
     const int share = kBins / ncta, per = share / kThreads, b0 = rank * share + threadIdx.x * per;
     Pair own{0, 0};
     for (int i = 0; i < per; ++i) {
@@ -458,7 +456,7 @@ struct Row {
       own.x += v.x;
       own.y += v.y;
     }
-    if (threadIdx.x < 4) sh.bin[threadIdx.x] = kBins - 1;
+    if (threadIdx.x < 2) sh.bin[threadIdx.x] = kBins - 1;
     const uint64_t sx = warp_scan(own.x), sy = warp_scan(own.y);
     const Pair all = exchange(own.x, own.y);
     Pair before = before_cta();
@@ -468,20 +466,17 @@ struct Row {
       before.x += sh.warp[0][i];
       before.y += sh.warp[1][i];
     }
-    const Targets t = targets_of(all);
     uint32_t seek = 0;
+    const Pair upto{before.x + own.x, before.y + own.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t from = i % 2 ? before.y : before.x, to = from + (i % 2 ? own.y : own.x);
-      if (from < t.at[i] && to >= t.at[i]) seek |= 1u << i;
-    }
+    for (int i = 0; i < 2; ++i)
+      if (!reach(all, i, before) && reach(all, i, upto)) seek |= 1u << i;
     if (seek != 0) {
       for (int b = b0; b < b0 + per && seek != 0; ++b) {
         const Pair v = f(b);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t to = i % 2 ? before.y + v.y : before.x + v.x;
-          if ((seek >> i & 1) == 0 || to < t.at[i]) continue;
+        for (int i = 0; i < 2; ++i) {
+          if ((seek >> i & 1) == 0 || !reach(all, i, Pair{before.x + v.x, before.y + v.y})) continue;
           seek &= ~(1u << i);
           for (uint32_t r = 0; r < ncta; ++r) {
             remote_store(&sh.bin[i], r, b);
@@ -840,15 +835,15 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
       const uint64_t w = r.weigh(l);
       return l > -INFINITY ? w : 0;
     };
-    if (min_p > 0.f || by_count) {
+    const bool late = by_weight && !by_count && !(min_p > 0.f);  // weighed when the cut's bins are known
+    if (late) {
+      r.sweep([&](float l, int) {
+        if (l > -INFINITY) atomicAdd(&r.hist[r.weight.bin(l)], 1u);
+      });
+    } else if (min_p > 0.f || by_count) {
       r.sweep_kept([&](float l, int) {
         if (by_count || by_weight) atomicAdd(&r.hist[r.weight.bin(l)], 1u);
         if (!by_count) kept += r.weigh(l);
-      });
-    } else if (by_weight) {
-      r.sweep([&](float l, int) {
-        if (l > -INFINITY) atomicAdd(&r.hist[r.weight.bin(l)], 1u);
-        kept += weigh(l);
       });
     } else {
       r.sweep([&](float l, int) { kept += weigh(l); });
@@ -868,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
     if (by_count) {
       const uint64_t want = top_k;
       const auto all = r.find_bins([&](int b) { return typename R::Pair{r.hist[b], 0}; },
-                                   [&](typename R::Pair) { return typename R::Targets{{want, ~0ull, ~0ull, ~0ull}}; });
+                                   [&](typename R::Pair, int i, typename R::Pair upto) { return i == 0 && upto.x >= want; });
       if (want < all.x) {
         k_bin = sh.bin[0];
         k_rest = static_cast<uint32_t>(want - sh.before);
@@ -886,12 +881,11 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
       }
       kept = r.kept_weight([](float) { return true; });
     }
-    total = r.exchange(kept, 0).x;
+    if (!late) total = r.exchange(kept, 0).x;
     if (by_weight) {
-      // The most and the least weight that each bin can hold bound the bins that the cut can fall into.
-      const double part = static_cast<double>(fmaxf(top_p, 0.f)) * static_cast<double>(total);
-      const uint64_t want = max(static_cast<uint64_t>(ceil(part)), static_cast<uint64_t>(1));
-      const double coarse = part * exp2(static_cast<double>(kMassBits - 31 - a.up));
+      // The most and the least weight that each bin can hold bound the bins that the cut can fall into: with X up to a bin and Y
+      // behind it, it lies no further where X >= p (X + Y), or (1 - p) X >= p Y, for the least X and the most Y, and
+      // no earlier where not even the most X and the least Y fulfil that.  (The total does not have to be known for that.)
       auto bounds = [&](int b) {
         const uint64_t n = b < k_bin ? r.hist[b] : (b == k_bin ? k_rest : 0);
         // (a bin's steps are rounded: it reaches half a step of 2^-10 to either side)
@@ -900,15 +894,13 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
         return typename R::Pair{n * (static_cast<uint64_t>(most * 1.00001f) + 1),
                                 b + 1 < kBins ? n * static_cast<uint64_t>(least * 0.99999f) : 0};
       };
-      // The sum up to a bin is at most the bounds' own and what the least behind it leaves of the total; at least likewise.
-      const double sum = static_cast<double>(total) * exp2(static_cast<double>(kMassBits - 31 - a.up));
-      r.find_bins(bounds, [&](typename R::Pair all) {
-        auto target = [](double x) { return x > 1.0 ? static_cast<uint64_t>(x) : static_cast<uint64_t>(1); };
-        const double low = coarse * (1 - 1e-7), high = coarse * (1 + 1e-7) + 1;
-        return typename R::Targets{{target(low), target(low - sum + static_cast<double>(all.y) - 1),
-                                    target(high - sum + static_cast<double>(all.x) + 1), target(high)}};
+      const uint64_t p = __float2ull_rz(fmaxf(top_p, 0.f) * 18446744073709551616.f), rest = ~p;  // 2^-64
+      r.find_bins(bounds, [&](typename R::Pair all, int i, typename R::Pair upto) {  // (3: what rounding down may lose)
+        if (upto.x == 0) return false;
+        if (i == 0) return __umul64hi(upto.x, rest) + __umul64hi(upto.y, p) + 3 >= __umul64hi(all.y, p);
+        return __umul64hi(upto.y, rest) + __umul64hi(upto.x, p) >= __umul64hi(all.x, p) + 3;
       });
-      const int first = max(sh.bin[0], sh.bin[1]), last = max(first, min(sh.bin[2], sh.bin[3]));
+      const int first = sh.bin[0], last = max(first, sh.bin[1]);
       const bool narrow = last - first < kWindow;
       // The weight before the window, the window's by bins, and its tokens; with what lies before them where that is little.
       bool list_now = false;
@@ -922,24 +914,36 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
       if (r.listed && tid < 2 * kWarps) sh.runs[0][tid] = 0;
       __syncthreads();
       const float from = r.weight.least_of(last), before = r.weight.least_of(first - 1);
-      auto in_window = [&](float l) {
+      auto in_window = [&](float l, uint64_t w) {
         const int b = r.weight.bin(l) - first;
         atomicAdd(&sh.window[0][b], 1u);
-        R::add_to(sh.window[1], sh.window[2], b, r.weigh(l));
+        R::add_to(sh.window[1], sh.window[2], b, w);
       };
       kept = 0;
-      if (!r.listed && !list_now) {
+      uint64_t weighed = 0;  // (late) this thread's of all tokens
+      if (late) {
+        r.sweep([&](float l, int index) {
+          const uint64_t w = weigh(l);
+          const bool above = l >= before;
+          weighed += w;
+          kept += above ? w : 0;
+          if (l >= from && (list_now || (narrow && !above))) {
+            r.put(l, index);
+            if (narrow && !above) in_window(l, w);
+          }
+        });
+      } else if (!r.listed && !list_now) {
         kept = r.packed_weight(from, [&](float l) { return l < before; }, [&](float l, int index) {
           if (!narrow) return;
           r.put(l, index);
-          in_window(l);
+          in_window(l, r.weigh(l));
         });
       } else {
         r.each_kept([&](float l, int index) {
           if (l < from) return;
           if (list_now) r.put(l, index);
           if (l < before) {
-            if (narrow) in_window(l);
+            if (narrow) in_window(l, r.weigh(l));
           } else if (r.listed) {
             R::add_to(sh.runs[0], sh.runs[1], (index + r.shift - r.place0) / r.run, r.weigh(l));
           } else {
@@ -951,7 +955,11 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 3 : 4) sample_kernel(const Sa
         __syncthreads();
         kept = lane == 0 ? sh.runs[0][warp] | static_cast<uint64_t>(sh.runs[1][warp]) << 32 : 0;
       }
-      uint64_t above = r.exchange(kept, 0).x;
+      const auto sums = r.exchange(kept, weighed);
+      if (late) total = sums.y;
+      uint64_t above = sums.x;
+      const double part = static_cast<double>(fmaxf(top_p, 0.f)) * static_cast<double>(total);
+      const uint64_t want = max(static_cast<uint64_t>(ceil(part)), static_cast<uint64_t>(1));
       r.listed |= list_now;
       int at = first;
       uint32_t m = 0;
