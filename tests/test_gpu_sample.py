@@ -107,6 +107,17 @@ def test_cluster_sizes(n, V, dtype):
           m=cycle([0.0, 0.0, 0.01]))
 
 
+@pytest.mark.parametrize("n,V,dtype", [(306, 26000, "bf16"), (306, 26000, "fp32"), (9, 26001, "fp16"), (18, 900, "fp32")])
+def test_a_top_p_cut_lies_anywhere(n, V, dtype):
+    """Also where the counts leave more bins than the window has (a cut in a gap of logits far apart, few levels)."""
+    p = [0.0, 1e-6, 0.01, 0.3, 0.5, 0.8, 0.9, 0.99, 0.9999]
+    T = [1.0, 0.3, 2.5, 0.7]
+    x = bell(n, V, dtype, seed=V + n)
+    x[1::3] = x[1::3] * 4
+    x[2::6] = torch.round(x[2::6])
+    check(x, p=[p[i % 9] for i in range(n)], T=[T[i // 9 % 4] for i in range(n)])
+
+
 @pytest.mark.parametrize("levels", [1, 2, 5, 60])
 @pytest.mark.parametrize("V", [500, 5000, 70000])
 def test_ties_go_by_index(levels, V):

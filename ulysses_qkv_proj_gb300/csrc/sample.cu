@@ -28,14 +28,14 @@
 // Bound: for few rows, latency: one row of 32003 logits takes 6.9 us (about 2 each for the maximum over the cluster, the
 // weights and the draw), 20 rows with top_k 24 (each phase's code runs once, so it is fetched as it runs). For many rows,
 // instructions: counting and weighing a logit are some 60, and every SM issues at about half its rate behind fixed latencies,
-// so 256 rows of 131075 take 235 us where reading them once would take 10, and 1024 such rows written as probabilities 590.
-// What the passes cost those 256 rows on the way (each of the later steps with the ones before): logits read in runs of 16,
-// out of the instruction cache, 1014 us; short loops 412; kept tokens packed before they are weighed 318; powers from shared
-// memory rather than L1, and the window's weights from the CTA's list rather than a pass of their own, 253; words converted
-// when their turn comes 243; no branch around a weight 235.
+// so 256 rows of 131075 take 188 us where reading them once would take 10, and 1024 such rows written as probabilities 545.
+// What the passes cost those 256 rows on the way (each step with the ones before): logits read in runs of 16, out of the
+// instruction cache, 1014 us; short loops 412; kept tokens packed before they are weighed 318; powers from shared memory
+// rather than L1, and the window's weights from the CTA's list rather than a pass of their own, 253; words converted when
+// their turn comes 243; no branch around a weight 235; a top_p row weighed once, after its counts, 188.
 // Tried and left: more and smaller CTAs for many rows (8 an SM: 246 us for 253, but 64 rows 149 for 93; 16 an SM: 285),
-// skipping groups of logits that nobody keeps (331 for 318), loads of 8 bytes (262 for 253), zeros written before the cut is
-// known (24.7 for 24.3), four packed weights at a time (237 for 236).
+// skipping groups of logits that nobody keeps (331 for 318), loads of 8 bytes (262 for 253), two loads ahead (192 for 188),
+// zeros written before the cut is known (24.7 for 24.3), four packed weights at a time (237 for 236).
 #include "../../include/qnre.h"
 #include "api_util.cuh"
 #include "ptx.cuh"
