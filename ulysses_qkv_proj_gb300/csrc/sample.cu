@@ -632,7 +632,7 @@ __device__ __noinline__ typename Row<T, KEEP>::Rounds Row<T, KEEP>::cut_by_round
       sh.high = 0;
     }
     __syncthreads();
-    r.sweep_kept([&](float l, int) {
+    r.each_kept([&](float l, int) {  // (from the CTAs' lists where these hold the bins' tokens)
       const uint32_t k = key_of(l);
       const int b = r.weight.bin(l);
       if (b < b0 || b > b1 || (level < 24 && (k ^ prefix) >> (level + 8) != 0)) return;
