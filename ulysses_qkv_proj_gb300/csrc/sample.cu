@@ -15,7 +15,8 @@
 //              the cut falls into one of a few bins; one pass then adds up exactly the weight before them, theirs by bins
 //              and the row's, which the bounds do without,
 //   cut        the tokens of the one bin go to the first CTA, which sorts them and finds the last one kept; bins of more
-//              than 1024 (ties, logits beyond the bins' range) are cut by four rounds of eight key bits,
+//              than 1024 (ties, logits beyond the bins' range) are cut by four rounds of eight key bits
+//              (over the CTAs' lists where these hold them: 64 rows of mixed settings 84 -> 65 us),
 //   draw       the kept weight by warps' runs of places; the run that holds the number is added up place by place.
 //
 // Numbers.  A token is right only if no sum is wrong by more than its distance from a border, and with 10^5 borders
