@@ -19,9 +19,11 @@
 // In a CTA the roles are those of tree_attention.cu: two TMA warps, two threads that issue the products, eight softmax
 // warps of which two threads share a row of 128.
 //
-// Values that a row must not see: as in tree_attention.cu scores are replaced before use and V behind a row's tokens is zeroed.  A
-// non-finite V of one request's own tokens would meet the zeros of the others' P, and 0 inf is NaN.  So a row whose own part is
-// not finite is marked, and the join computes that part again by itself, token by token (own_part): slow, and only there.
+// Values that a row must not see: as in tree_attention.cu scores are replaced before use and V behind a row's tokens is zeroed.  In
+// a unit of several requests a row's P is zero, whatever its scores, in the tiles of the others, and as 0 inf is NaN the
+// non-finite elements of V are zeroed before the product, in the context by the warp that issues it.  That
+// request's rows are marked, and the join gives them their infinite and NaN columns, which it looks up in V (own_strange); all
+// else is the product's, so nothing that one request holds changes a bit of another's result or its time.
 //
 // Bound: long common prefixes and many rows, by a tile's two products and its softmax, which share the SM's tensor memory
 // and issue slots: 128 tokens by 128 rows of D = 128 take 1840 cycles where the products alone are 1024.  128 requests of 64 + 8
@@ -97,8 +99,6 @@ struct PrefixArgs {
   long long own_rows, group_rows;  // where the rows' own places begin, for each kind
   float scale_log2, cap_in, cap_log2;  // capped: scale / cap, cap log2(e)
   float cap_near, cap_poly[3];         // the nearer polynomial of run_softmax in powers of q.k, and up to where it serves
-  const char* q;
-  long long q_stride[3];  // bytes
   int layer, n, n_groups, nodes, Hq, Hk, G, box, cl;
   int unit_nodes, unit_members, row_tiles;  // nodes and requests of a unit; units that one request's nodes take
   int warp_members;                         // requests whose rows one warp has
@@ -417,18 +417,59 @@ __device__ void run_scores(const PrefixArgs& a, const Bars& bars, uint32_t smem,
   }
 }
 
-// O += P V, tile after tile; names the places of the units begun here for the join.
-template <typename L, int D, bool BF16>
-__device__ void run_outputs(const PrefixArgs& a, const Bars& bars, uint32_t smem, uint32_t tmem, Cursor cur, Seg s,
-                            bool more, bool share, volatile uint32_t* abort_flag) {
+// Zeros the infinite and NaN elements in the first `rows` rows of a V tile; true where there are any (a whole warp).
+template <int D, bool BF16>
+__device__ __forceinline__ bool clean_v_tile(uint32_t tile, int rows) {
+  constexpr int kPieces = D / 8;
+  const int lane = threadIdx.x % 32;
+  bool found = false;
+#pragma unroll 1
+  for (int x = lane; x < rows; x += 32) {
+    const uint32_t row = tile + x * 128;
+    uint32_t sum[4] = {0, 0, 0, 0};  // 0 x is 0 for every finite x
+#pragma unroll 16
+    for (int i = 0; i < kPieces; ++i) {
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(row + (i / 8) * (kTile * 128) + ((i ^ lane) % 8) * 16)
+                   : "memory");
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (BF16)
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[e]) : "r"(w[e]), "r"(0));
+        else
+          asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum[e]) : "r"(w[e]), "r"(0));
+      }
+    }
+    if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0)
+      found |= clean_v_row<D, BF16>(reinterpret_cast<char*>(__cvta_shared_to_generic(row)), true, 0, kPieces);
+  }
+  return found;
+}
+
+// The same as a call: where the softmax takes all registers, a copy in line cost its schedule more (24 drafted trees with cap and
+// bias 107 us, in line 113; 128 requests' plain scores 126 and 122, 64 channels with a cap 104 and 97).
+template <int D, bool BF16>
+__device__ __noinline__ bool clean_v_tile_apart(uint32_t tile, int rows) {
+  return clean_v_tile<D, BF16>(tile, rows);
+}
+
+// O += P V, tile after tile; names the places of the units begun here for the join.  Lane 0 issues; in units of several requests the
+// warp takes the infinite and NaN elements out of the context's V first, while the softmax of the tile runs.
+template <typename L, int D, bool BF16, bool APART>
+__device__ void run_outputs(const PrefixArgs& a, const Bars& bars, char* smem_base, uint32_t tmem, Cursor cur, Seg s,
+                            bool more, bool share, volatile uint32_t* abort_flag, unsigned long long* marked) {
   constexpr uint32_t kFmt = BF16 ? (1u << 7 | 1u << 10) : 0u;
   constexpr uint32_t kIdesc =
       (1u << 4) | kFmt | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) | ((128u >> 4) << 24);
-  const uint64_t ring0 = ptx::smem_desc_sw128(smem + L::kV, kTile * 128, 1024);
+  const uint64_t ring0 = ptx::smem_desc_sw128(ptx::smem_addr(smem_base) + L::kV, kTile * 128, 1024);
   const uint16_t everyone = static_cast<uint16_t>((1u << a.cl) - 1u);
+  const int lane = threadIdx.x % 32, mark_shift = a.unit_members > 64 ? 1 : 0;
   uint32_t g = 0, slot = 0, phase = 0;
+  bool stopped = false;  // lane 0: a wait ran out
   for (uint32_t seg = 0; more; ++seg, more = cur.next(s)) {
-    if (s.t0 == 0) {
+    if (s.t0 == 0 && lane == 0) {
       int parts = 0;
       if (!s.whole) {
         int lo = cur.index, hi = cur.count - 1;  // the last run that starts by the last tile
@@ -442,27 +483,53 @@ __device__ void run_outputs(const PrefixArgs& a, const Bars& bars, uint32_t smem
       (s.group ? a.group_units : a.row_units)[(request * a.Hk + s.kvh) * a.row_tiles + s.rt - tile * a.row_tiles] =
           Desc{static_cast<int>(blockIdx.x), share ? a.cl : 1, parts};
     }
+    const bool mixed = !s.group && a.unit_members > 1;
+    Walk walk;
+    if (mixed) {
+      __syncwarp();  // lane 0 has seen every tile before: a wait for one of the ring's next phases means that phase
+      walk.begin(cur.t, s, a.warp_members);
+    }
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
       const bool first = t == s.t0;
-      if (!wait(bars.vfull + 8 * slot, phase, abort_flag, a.c.status) ||
-          (first && !wait(bars.ofree, (seg & 1u) ^ 1u, abort_flag, a.c.status)) ||
-          !wait(bars.pready + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status))
-        return drain_mma(bars.drain2);
-      ptx::tc_fence_after_sync();
-      const uint64_t v = desc_at(ring0, slot * L::kTileBytes);
+      if (mixed) {
+        const int context = min(walk.len - walk.position(a.backward), kTile);  // (tokens behind it: by the softmax threads)
+        const int member = walk.mi;
+        if (t + 1 < s.t1) walk.next();
+        if (context > 0 && wait(bars.vfull + 8 * slot, phase, abort_flag, a.c.status)) {
+          const uint32_t v = ptx::smem_addr(smem_base) + L::kV + slot * L::kTileBytes;
+          if (APART ? clean_v_tile_apart<D, BF16>(v, context) : clean_v_tile<D, BF16>(v, context)) {
+            atomicOr(marked + seg % 3, 1ull << (member >> mark_shift));
+            __threadfence_block();
+          }
+        }
+        __syncwarp();
+      }
+      if (lane == 0 && !stopped) {
+        if (!wait(bars.vfull + 8 * slot, phase, abort_flag, a.c.status) ||
+            (first && !wait(bars.ofree, (seg & 1u) ^ 1u, abort_flag, a.c.status)) ||
+            !wait(bars.pready + 8 * b, (g >> 1) & 1u, abort_flag, a.c.status)) {
+          drain_mma(bars.drain2);
+          stopped = true;
+        } else {
+          ptx::tc_fence_after_sync();
+          const uint64_t v = desc_at(ring0, slot * L::kTileBytes);
 #pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_f16_ts(tmem + kTmemO, tmem + kTmemP + b * 64 + kk * 8, desc_at(v, kk * 2048), kIdesc,
-                    (t > s.t0 || kk > 0) ? 1u : 0u);
-      ptx::umma_commit(bars.pvdone + 8 * b);
-      release(bars.vempty + 8 * slot, share, everyone);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_f16_ts(tmem + kTmemO, tmem + kTmemP + b * 64 + kk * 8, desc_at(v, kk * 2048), kIdesc,
+                        (t > s.t0 || kk > 0) ? 1u : 0u);
+          ptx::umma_commit(bars.pvdone + 8 * b);
+          release(bars.vempty + 8 * slot, share, everyone);
+        }
+      }
+      if (mixed) __syncwarp();  // (lanes that waited for the next tile meanwhile could hold lane 0 up)
       if (++slot == L::kVStages) {
         slot = 0;
         phase ^= 1u;
       }
     }
   }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax warps
@@ -685,8 +752,7 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
           tmem_st_wait();
         }
         if (grow) m = mx;
-        // (a row that does not see the tile gets zeros; what is not finite in its scores marks it, as in V)
-        const float ms = mine ? (m == -INFINITY ? 0.f : m) : INFINITY;
+        const float ms = mine ? (m == -INFINITY ? 0.f : m) : INFINITY;  // (a row that does not see the tile gets zeros)
         uint64_t neg = pair(-ms, -ms);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -705,7 +771,13 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
         }
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);
-        l += s0 + s1;
+        s0 += s1;
+        if (__any_sync(0xFFFFFFFFu, !mine && s0 != 0.f)) {  // infinite or NaN scores of another request's keys (NaN is not 0)
+          if (!mine) s0 = 0.f;
+#pragma unroll
+          for (int i = 0; i < kCols / 2; ++i) p[i] = mine ? p[i] : 0u;
+        }
+        l += s0;
       } else {  // the tile of a request whose rows other warps have
         __syncwarp();
         ptx::tc_fence_after_sync();
@@ -1028,8 +1100,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     run_producer<L, D>(a, bars, smem, cur, first, more, warp == kSoftWarps ? 0 : 1, share, &words->abort);
   } else if (warp == kSoftWarps + 1) {
     if (lane == 0) run_scores<L, D, BF16>(a, bars, smem, tmem, cur, first, more, share, &words->abort);
-  } else if (lane == 0) {
-    run_outputs<L, D, BF16>(a, bars, smem, tmem, cur, first, more, share, &words->abort);
+  } else {
+    run_outputs<L, D, BF16, SCORED && D == 128>(a, bars, smem_base, tmem, cur, first, more, share, &words->abort, words->marked);
   }
   __syncwarp();
   ptx::tc_fence_before_sync();
@@ -1046,62 +1118,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------ join
-// A row's part over its own tokens, token by token in fp32 (base 2), for rows that met a non-finite V: columns [4 i4, 4 i4 + 4).
-// Non-finite elements of V that it sees count whatever their weight.
-struct OwnPart {
-  float m, l;
-  float4 o;
-};
+// The sums of the infinite and NaN elements of V that a row sees among its own tokens, whatever their weights, in columns
+// [4 i4, 4 i4 + 4); 0 where there are none.
 template <int D, bool BF16>
-__device__ __noinline__ OwnPart own_part(const PrefixArgs& a, int i, int node, int kvh, int h, int i4) {
-  OwnPart r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  float strange[4] = {0.f, 0.f, 0.f, 0.f};
-  float* o[4] = {&r.o.x, &r.o.y, &r.o.z, &r.o.w};
+__device__ __noinline__ float4 own_strange(const PrefixArgs& a, int i, int node, int kvh, int i4) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
   const int row = a.rows[i], cnt = a.counts != nullptr ? min(max(a.counts[i], 0), a.nodes) : a.nodes;
-  if (row < 0 || row >= a.c.rows || node >= cnt) return r;
-  const int room = a.c.max_blocks * a.c.page_size, len = min(a.c.length(row), room), total = min(len + cnt, room);
-  const long long at = static_cast<long long>(i) * a.nodes;
-  const uint64_t bits = a.mask != nullptr ? a.mask[at + node] : (2ull << node) - 1;
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + i * a.q_stride[0] + node * a.q_stride[1] +
-                                                        (kvh * a.G + h) * a.q_stride[2]);
-  const float slope = a.slopes != nullptr ? a.slopes[kvh * a.G + h] * kLog2e : 0.f;
-  const int place = a.depths != nullptr ? a.depths[at + node] : node;
-  for (int x = a.requests[i].y; x < total; ++x) {
-    if (x >= len && !(bits >> (x - len) & 1)) continue;
-    const int page = a.c.page_of(row, x);  // (a missing one is read as zeros)
-    const long long off = page >= 0 ? a.c.token_offset(a.layer, page, kvh, x) : 0;
-    const uint32_t* k = reinterpret_cast<const uint32_t*>(a.c.k + off);
-    float s = 0.f;
-    for (int e = 0; page >= 0 && e < D / 2; ++e) {
-      s = fmaf(to_float<BF16>(q[e] & 0xFFFFu), to_float<BF16>(k[e] & 0xFFFFu), s);
-      s = fmaf(to_float<BF16>(q[e] >> 16), to_float<BF16>(k[e] >> 16), s);
-    }
-    s = a.cap_log2 > 0.f ? fmaf(rcp_fast(exp2_fast(s * a.cap_in * 2.885390043258667f) + 1.f), -2.f * a.cap_log2, a.cap_log2) : s * a.scale_log2;
-    if (a.slopes != nullptr) {
-      const int key = x >= len && a.depths != nullptr ? a.depths[at + x - len] : x - len;
-      s += slope * static_cast<float>(key - place);
-    }
-    if (s > r.m) {
-      const float f = r.m == -INFINITY ? 0.f : exp2_fast(r.m - s);
-      r.m = s;
-      r.l *= f;
-      for (int e = 0; e < 4; ++e) *o[e] *= f;
-    }
-    const float w = s == -INFINITY ? 0.f : exp2_fast(s - (r.m == -INFINITY ? 0.f : r.m));
-    r.l += w;
-    if (page < 0) continue;
-    const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v + off) + 4 * i4;
-    for (int e = 0; e < 4; ++e) {
-      const float f = to_float<BF16>(v[e]);
-      if (nonfinite_mask<BF16>(v[e]) & 0xFFFFu)
-        strange[e] += f;
-      else
-        *o[e] = fmaf(f, w, *o[e]);
+  if (row >= 0 && row < a.c.rows && node < cnt) {
+    const int ps = a.c.page_size, room = a.c.max_blocks * ps, len = min(a.c.length(row), room), total = min(len + cnt, room);
+    const uint64_t bits = a.mask != nullptr ? a.mask[static_cast<long long>(i) * a.nodes + node] : (2ull << node) - 1;
+    for (int x0 = a.requests[i].y; x0 < total; x0 += ps) {  // (whole pages are common)
+      const int page = a.c.page_of(row, x0), end = min(x0 + ps, total);
+      if (page < 0) continue;  // read as zeros
+      const char* v = a.c.v + a.c.token_offset(a.layer, page, kvh, x0) + 8 * i4;
+#pragma unroll 4
+      for (int x = x0; x < end; ++x, v += 2 * D) {
+        const uint2 w = *reinterpret_cast<const uint2*>(v);
+        if (((nonfinite_mask<BF16>(w.x) | nonfinite_mask<BF16>(w.y)) == 0) || (x >= len && !(bits >> (x - len) & 1))) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t bits16 = (e < 2 ? w.x : w.y) >> (e % 2 * 16) & 0xFFFFu;
+          if (nonfinite_mask<BF16>(bits16) & 0xFFFFu) sum[e] += to_float<BF16>(bits16);
+        }
+      }
     }
   }
-  for (int e = 0; e < 4; ++e)
-    if (strange[e] != 0.f) *o[e] = strange[e];  // (NaN compares unequal)
-  return r;
+  return make_float4(sum[0], sum[1], sum[2], sum[3]);
 }
 
 // A thread has four columns of a row, a warp eight rows' (whole lines of the parts).  Rows go by K head, request, node, head.
@@ -1109,7 +1151,7 @@ __device__ __noinline__ OwnPart own_part(const PrefixArgs& a, int i, int node, i
 template <int D, bool BF16, int TEAMS>
 __global__ void __launch_bounds__(256 * TEAMS) join_kernel(const __grid_constant__ PrefixArgs a) {
   constexpr int kWarps = D / 16;  // that share eight rows
-  __shared__ float sums[TEAMS > 1 ? TEAMS - 1 : 1][6][256];
+  __shared__ float sums[TEAMS > 1 ? TEAMS - 1 : 1][7][256];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % 8, team = threadIdx.x / 256;
@@ -1177,41 +1219,51 @@ __global__ void __launch_bounds__(256 * TEAMS) join_kernel(const __grid_constant
     const int at = threadIdx.x % 256;
     if (team > 0) {
       float(*mine)[256] = sums[team - 1];
-      mine[0][at] = marked ? NAN : M;
+      mine[0][at] = M;
       mine[1][at] = l;
       mine[2][at] = acc.x;
       mine[3][at] = acc.y;
       mine[4][at] = acc.z;
       mine[5][at] = acc.w;
+      mine[6][at] = marked ? 1.f : 0.f;
     }
     __syncthreads();
     if (team > 0) return;
 #pragma unroll
     for (int k = 0; k < TEAMS - 1; ++k) {
-      const float m1 = sums[k][0][at];
-      if (m1 != m1)
-        marked = true;
-      else
-        add(m1, sums[k][1][at], make_float4(sums[k][2][at], sums[k][3][at], sums[k][4][at], sums[k][5][at]));
+      marked |= sums[k][6][at] != 0.f;
+      add(sums[k][0][at], sums[k][1][at], make_float4(sums[k][2][at], sums[k][3][at], sums[k][4][at], sums[k][5][at]));
     }
   }
   if (!there) return;
-  if (request.x < 0 && own.parts == 0 && !marked) return;  // the output is there
-  if (marked) {  // the group's parts again, and this row's own
-    M = -INFINITY;
-    l = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool there_already = request.x < 0 && own.parts == 0;
+  if (there_already && !marked) return;
+  const long long orow = static_cast<long long>(token) * a.Hq + kvh * a.G + h;
+  uint2* dst = reinterpret_cast<uint2*>(a.out + (orow * D + 4 * i4) * 2);
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (marked && l != 0.f) {  // infinite and NaN columns, the common tokens' among them; the others are right
+    float4 strange = own_strange<D, BF16>(a, i, node, kvh, i4);
+    auto join_in = [](float& sum, float x) {
+      if (!(fabsf(x) <= 3.4028234664e38f)) sum += x;
+    };
     for (int p = 0; p < group_parts; ++p) {
       const long long row = row_of(group, group_member, a.group_rows, p);
-      add(a.part_ml[row].x, a.part_ml[row].y, a.part_o[piece_of<D>(row, i4)]);
+      if (a.part_ml[row].x == -INFINITY && a.part_ml[row].y == 0.f) continue;
+      const float4 c = a.part_o[piece_of<D>(row, i4)];
+      join_in(strange.x, c.x), join_in(strange.y, c.y), join_in(strange.z, c.z), join_in(strange.w, c.w);
     }
-    const OwnPart r = own_part<D, BF16>(a, i, node, kvh, h, i4);
-    add(r.m, r.l, r.o);
+    if (there_already) {
+      const uint2 w = *dst;
+      o = make_float4(to_float<BF16>(w.x & 0xFFFFu), to_float<BF16>(w.x >> 16), to_float<BF16>(w.y & 0xFFFFu),
+                      to_float<BF16>(w.y >> 16));
+    }
+    o = make_float4(strange.x != 0.f ? strange.x : o.x, strange.y != 0.f ? strange.y : o.y, strange.z != 0.f ? strange.z : o.z,
+                    strange.w != 0.f ? strange.w : o.w);  // (NaN compares unequal)
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  const long long orow = static_cast<long long>(token) * a.Hq + kvh * a.G + h;
-  *reinterpret_cast<uint2*>(a.out + (orow * D + 4 * i4) * 2) =
-      make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+  if (there_already && l == 0.f) return;
+  *dst = make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
+  if (there_already) return;
   if (a.lse != nullptr && i4 == 0) a.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -1537,8 +1589,6 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
                                  static_cast<uint64_t>(own.stride[0]) * 2};
   const uint32_t q_box[4] = {64, static_cast<uint32_t>(a.G), static_cast<uint32_t>(a.unit_nodes),
                              static_cast<uint32_t>(a.unit_members)};
-  a.q = static_cast<const char*>(own.data);
-  for (int i = 0; i < 3; ++i) a.q_stride[i] = own.stride[i] * 2;
   if (!encode_tiled_16bit(&a.tq, own.data, bf16, 4, q_dims, q_strides, q_box) ||
       !encode_tiled_16bit(&a.tk, cache->k, bf16, 4, dims, strides, box) ||
       !encode_tiled_16bit(&a.tv, cache->v, bf16, 4, dims, strides, box))
