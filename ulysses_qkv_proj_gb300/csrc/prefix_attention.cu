@@ -19,11 +19,12 @@
 // In a CTA the roles are those of tree_attention.cu: two TMA warps, two threads that issue the products, eight softmax
 // warps of which two threads share a row of 128.
 //
-// Values that a row must not see: as in tree_attention.cu scores are replaced before use and V behind a row's tokens is zeroed.  In
-// a unit of several requests a row's P is zero, whatever its scores, in the tiles of the others, and as 0 inf is NaN the
-// non-finite elements of V are zeroed before the product, in the context by the warp that issues it.  That
-// request's rows are marked, and the join gives them their infinite and NaN columns, which it looks up in V (own_strange); all
-// else is the product's, so nothing that one request holds changes a bit of another's result or its time.
+// Values that a row must not see: as in tree_attention.cu scores are replaced before use.  In a unit of several requests a row's
+// P is zero, whatever its scores, in the tiles of the others, and as 0 inf is NaN the warp that issues the product
+// zeroes V's non-finite elements before it, and V behind a request's tokens.  (It has the time, while the softmax of the tile runs;
+// where the softmax threads cleaned the last tokens' V themselves, the four cases below took 24.8, 123, 97 and 108 us for 22.9, 123,
+// 89 and 102.)  The rows of a request with such an element are marked, and the join gives them their infinite and NaN columns,
+// which it looks up in V (own_strange); all else is the product's, so nothing that one request holds changes a bit of another's result.
 //
 // Bound: long common prefixes and many rows, by a tile's two products and its softmax, which share the SM's tensor memory
 // and issue slots: 128 tokens by 128 rows of D = 128 take 1840 cycles where the products alone are 1024.  128 requests of 64 + 8
@@ -417,22 +418,23 @@ __device__ void run_scores(const PrefixArgs& a, const Bars& bars, uint32_t smem,
   }
 }
 
-// Zeros the infinite and NaN elements in the first `rows` rows of a V tile; true where there are any (a whole warp).
+// Makes a V tile fit for zero weights (a whole warp): rows [from, to) without their infinite and NaN elements, rows [to, end),
+// which hold no token, zero.  True where there were any such elements.
 template <int D, bool BF16>
-__device__ __forceinline__ bool clean_v_tile(uint32_t tile, int rows) {
+__device__ __forceinline__ bool clean_v_tile(uint32_t tile, int from, int to, int end) {
   constexpr int kPieces = D / 8;
   const int lane = threadIdx.x % 32;
+  auto piece_at = [&](int x, int i) { return tile + x * 128 + (i / 8) * (kTile * 128) + ((i ^ lane) % 8) * 16; };
   bool found = false;
 #pragma unroll 1
-  for (int x = lane; x < rows; x += 32) {
-    const uint32_t row = tile + x * 128;
+  for (int x = from + lane; x < to; x += 32) {
     uint32_t sum[4] = {0, 0, 0, 0};  // 0 x is 0 for every finite x
 #pragma unroll 16
     for (int i = 0; i < kPieces; ++i) {
       uint32_t w[4];
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "r"(row + (i / 8) * (kTile * 128) + ((i ^ lane) % 8) * 16)
+                   : "r"(piece_at(x, i))
                    : "memory");
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -443,7 +445,15 @@ __device__ __forceinline__ bool clean_v_tile(uint32_t tile, int rows) {
       }
     }
     if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0)
-      found |= clean_v_row<D, BF16>(reinterpret_cast<char*>(__cvta_shared_to_generic(row)), true, 0, kPieces);
+      found |= clean_v_row<D, BF16>(reinterpret_cast<char*>(__cvta_shared_to_generic(tile + x * 128)), true, 0, kPieces);
+  }
+  if (to < end) {
+#pragma unroll 1
+    for (int x = to + lane; x < end; x += 32)
+#pragma unroll 1
+      for (int i = 0; i < kPieces; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(piece_at(x, i)), "r"(0) : "memory");
+    ptx::fence_proxy_async_smem();
   }
   return found;
 }
@@ -451,8 +461,8 @@ __device__ __forceinline__ bool clean_v_tile(uint32_t tile, int rows) {
 // The same as a call: where the softmax takes all registers, a copy in line cost its schedule more (24 drafted trees with cap and
 // bias 107 us, in line 113; 128 requests' plain scores 126 and 122, 64 channels with a cap 104 and 97).
 template <int D, bool BF16>
-__device__ __noinline__ bool clean_v_tile_apart(uint32_t tile, int rows) {
-  return clean_v_tile<D, BF16>(tile, rows);
+__device__ __noinline__ bool clean_v_tile_apart(uint32_t tile, int from, int to, int end) {
+  return clean_v_tile<D, BF16>(tile, from, to, end);
 }
 
 // O += P V, tile after tile; names the places of the units begun here for the join.  Lane 0 issues; in units of several requests the
@@ -483,22 +493,22 @@ __device__ void run_outputs(const PrefixArgs& a, const Bars& bars, char* smem_ba
       (s.group ? a.group_units : a.row_units)[(request * a.Hk + s.kvh) * a.row_tiles + s.rt - tile * a.row_tiles] =
           Desc{static_cast<int>(blockIdx.x), share ? a.cl : 1, parts};
     }
-    const bool mixed = !s.group && a.unit_members > 1;
     Walk walk;
-    if (mixed) {
+    if (!s.group) {
       __syncwarp();  // lane 0 has seen every tile before: a wait for one of the ring's next phases means that phase
       walk.begin(cur.t, s, a.warp_members);
     }
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
       const bool first = t == s.t0;
-      if (mixed) {
-        const int context = min(walk.len - walk.position(a.backward), kTile);  // (tokens behind it: by the softmax threads)
-        const int member = walk.mi;
+      if (!s.group) {
+        const int pos0 = walk.position(a.backward), tokens = walk.total - walk.base, member = walk.mi;
+        const int from = a.unit_members > 1 ? 0 : max(walk.len - pos0, 0);  // (alone, a request meets its own context's values)
+        const int to = min(walk.total - pos0, kTile), end = min(((tokens + a.box - 1) & -a.box) + walk.base - pos0, kTile);
         if (t + 1 < s.t1) walk.next();
-        if (context > 0 && wait(bars.vfull + 8 * slot, phase, abort_flag, a.c.status)) {
+        if (from < end && wait(bars.vfull + 8 * slot, phase, abort_flag, a.c.status)) {
           const uint32_t v = ptx::smem_addr(smem_base) + L::kV + slot * L::kTileBytes;
-          if (APART ? clean_v_tile_apart<D, BF16>(v, context) : clean_v_tile<D, BF16>(v, context)) {
+          if (APART ? clean_v_tile_apart<D, BF16>(v, from, to, end) : clean_v_tile<D, BF16>(v, from, to, end)) {
             atomicOr(marked + seg % 3, 1ull << (member >> mark_shift));
             __threadfence_block();
           }
@@ -522,7 +532,7 @@ __device__ void run_outputs(const PrefixArgs& a, const Bars& bars, char* smem_ba
           release(bars.vempty + 8 * slot, share, everyone);
         }
       }
-      if (mixed) __syncwarp();  // (lanes that waited for the next tile meanwhile could hold lane 0 up)
+      if (!s.group) __syncwarp();  // (lanes that waited for the next tile meanwhile could hold lane 0 up)
       if (++slot == L::kVStages) {
         slot = 0;
         phase ^= 1u;
@@ -589,14 +599,12 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t b = g & 1u;
       int pos0 = group_position(s, t, a.backward), len = s.tokens, total = s.tokens, member = 0;
-      int filled = (total + a.box - 1) & -a.box;  // TMA has zeroed V from here on
       bool mine = true;  // a row that sees this tile
       if (!s.group) {
         member = walk.mi;
         pos0 = walk.position(a.backward);
         len = walk.len;
         total = walk.total;
-        filled = walk.base + ((total - walk.base + a.box - 1) & -a.box);
         mine = row.at.member == member;
         if (t + 1 < s.t1) walk.next();
       }
@@ -786,16 +794,6 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
         for (int i = 0; i < kCols / 2; ++i) p[i] = 0;
       }
       tmem_st_x32(tmem + lane_base + kTmemP + b * 64 + c0 / 2, p);
-      if (tail) {
-        const uint32_t slot = g % L::kVStages;
-        wait(bars.vfull + 8 * slot, (g / L::kVStages) & 1u, abort_flag, a.c.status);
-        const int x = tid % 128, pos = pos0 + x;
-        constexpr int kPieces = D / 16;
-        if (pos >= len && pos < filled && clean_v_row<D, BF16>(smem_base + L::kV + slot * L::kTileBytes + x * 128, pos < total,
-                                               copy * kPieces, (copy + 1) * kPieces))
-          atomicOr(marked + seg % 3, 1ull << (member >> mark_shift));
-        __syncwarp();
-      }
       tmem_st_wait();
       ptx::tc_fence_before_sync();
       __syncwarp();
