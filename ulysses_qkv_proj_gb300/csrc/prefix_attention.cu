@@ -1117,30 +1117,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 
 // ------------------------------------------------------------------ join
 // The sums of the infinite and NaN elements of V that a row sees among its own tokens, whatever their weights, in columns
-// [4 i4, 4 i4 + 4); 0 where there are none.
+// [4 i4, 4 i4 + 4); 0 where there are none.  Eight lanes have the same columns and take every eighth token.
 template <int D, bool BF16>
 __device__ __noinline__ float4 own_strange(const PrefixArgs& a, int i, int node, int kvh, int i4) {
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   const int row = a.rows[i], cnt = a.counts != nullptr ? min(max(a.counts[i], 0), a.nodes) : a.nodes;
   if (row >= 0 && row < a.c.rows && node < cnt) {
-    const int ps = a.c.page_size, room = a.c.max_blocks * ps, len = min(a.c.length(row), room), total = min(len + cnt, room);
+    const int room = a.c.max_blocks * a.c.page_size, len = min(a.c.length(row), room), total = min(len + cnt, room);
     const uint64_t bits = a.mask != nullptr ? a.mask[static_cast<long long>(i) * a.nodes + node] : (2ull << node) - 1;
-    for (int x0 = a.requests[i].y; x0 < total; x0 += ps) {  // (whole pages are common)
-      const int page = a.c.page_of(row, x0), end = min(x0 + ps, total);
-      if (page < 0) continue;  // read as zeros
-      const char* v = a.c.v + a.c.token_offset(a.layer, page, kvh, x0) + 8 * i4;
 #pragma unroll 4
-      for (int x = x0; x < end; ++x, v += 2 * D) {
-        const uint2 w = *reinterpret_cast<const uint2*>(v);
-        if (((nonfinite_mask<BF16>(w.x) | nonfinite_mask<BF16>(w.y)) == 0) || (x >= len && !(bits >> (x - len) & 1))) continue;
+    for (int x = a.requests[i].y + static_cast<int>(threadIdx.x % 8); x < total; x += 8) {
+      const int page = a.c.page_of(row, x);  // (a missing one is read as zeros)
+      uint2 w = make_uint2(0, 0);
+      if (page >= 0) w = *reinterpret_cast<const uint2*>(a.c.v + a.c.token_offset(a.layer, page, kvh, x) + 8 * i4);
+      if (((nonfinite_mask<BF16>(w.x) | nonfinite_mask<BF16>(w.y)) == 0) || (x >= len && !(bits >> (x - len) & 1))) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t bits16 = (e < 2 ? w.x : w.y) >> (e % 2 * 16) & 0xFFFFu;
-          if (nonfinite_mask<BF16>(bits16) & 0xFFFFu) sum[e] += to_float<BF16>(bits16);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t bits16 = (e < 2 ? w.x : w.y) >> (e % 2 * 16) & 0xFFFFu;
+        if (nonfinite_mask<BF16>(bits16) & 0xFFFFu) sum[e] += to_float<BF16>(bits16);
       }
     }
   }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], o);
   return make_float4(sum[0], sum[1], sum[2], sum[3]);
 }
 
@@ -1233,6 +1235,14 @@ __global__ void __launch_bounds__(256 * TEAMS) join_kernel(const __grid_constant
       add(sums[k][0][at], sums[k][1][at], make_float4(sums[k][2][at], sums[k][3][at], sums[k][4][at], sums[k][5][at]));
     }
   }
+  marked = marked && there && l != 0.f;
+  float4 strange = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (uint32_t rows = __ballot_sync(0xFFFFFFFFu, marked) & 0xFFu; rows != 0; rows &= rows - 1) {  // the warp's, one after another
+    const int from = __ffs(rows) - 1;
+    const float4 x = own_strange<D, BF16>(a, __shfl_sync(0xFFFFFFFFu, i, from), __shfl_sync(0xFFFFFFFFu, node, from),
+                                          __shfl_sync(0xFFFFFFFFu, kvh, from), i4);
+    if (lane % 8 == from) strange = x;
+  }
   if (!there) return;
   const bool there_already = request.x < 0 && own.parts == 0;
   if (there_already && !marked) return;
@@ -1240,8 +1250,7 @@ __global__ void __launch_bounds__(256 * TEAMS) join_kernel(const __grid_constant
   uint2* dst = reinterpret_cast<uint2*>(a.out + (orow * D + 4 * i4) * 2);
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (marked && l != 0.f) {  // infinite and NaN columns, the common tokens' among them; the others are right
-    float4 strange = own_strange<D, BF16>(a, i, node, kvh, i4);
+  if (marked) {  // infinite and NaN columns, the common tokens' among them; the others are right
     auto join_in = [](float& sum, float x) {
       if (!(fabsf(x) <= 3.4028234664e38f)) sum += x;
     };
@@ -1259,7 +1268,6 @@ __global__ void __launch_bounds__(256 * TEAMS) join_kernel(const __grid_constant
     o = make_float4(strange.x != 0.f ? strange.x : o.x, strange.y != 0.f ? strange.y : o.y, strange.z != 0.f ? strange.z : o.z,
                     strange.w != 0.f ? strange.w : o.w);  // (NaN compares unequal)
   }
-  if (there_already && l == 0.f) return;
   *dst = make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
   if (there_already) return;
   if (a.lse != nullptr && i4 == 0) a.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
