@@ -91,3 +91,47 @@ def test_infinite_values_under_caps_and_biases(cap, slopes, dim, dtype):
     columns = torch.ones(c.q.shape[2:], dtype=torch.bool)
     columns[:2, 5] = columns[2:, 6] = columns[2:, 8] = False
     check_closely(c, out, lse, range(c.n), columns)
+
+
+@pytest.mark.parametrize("cap", [1e4, 30.0])
+@pytest.mark.parametrize("kw", [dict(Hq=7, Hk=1, nodes=5), dict(Hq=4, Hk=2, nodes=2, dim=64, dtype="fp16"), dict(Hq=14, Hk=2, nodes=1)])
+def test_unused_slots_do_not_choose_the_arithmetic(cap, kw):
+    """K in slots behind a row's tokens: zeros, or values far beyond the cap; the same bits, and as near as scores that small come."""
+    c = Case([(5, 96), (3, 32)], [21, 3, 130], cap=cap, seed=33, alone=1, **kw)
+    unused = torch.isnan(c.k)
+    got = []
+    for filling in (0.0, 3000.0):
+        c.k[unused] = filling
+        got.append(c.run())
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    if cap > 100:
+        check_closely(c, *got[1], range(c.n))
+
+
+@pytest.mark.parametrize("cap", [1e4, 50.0])
+@pytest.mark.parametrize("grouped", [True, False])
+def test_scores_beyond_the_cap_stay_with_their_row(cap, grouped):
+    """One request's queries grow until its scores pass the cap; the others keep their bits."""
+    c = Case([(6, 160), (3, 64)], [21, 3, 130], nodes=2, Hq=4, Hk=2, cap=cap, seed=34)
+    want, want_lse = c.run(groups=grouped)
+    c.q[2] *= 4 * cap
+    out, lse = c.run(groups=grouped)
+    others = [j for j in range(c.n) if j != 2]
+    assert torch.equal(out[others], want[others]) and torch.equal(lse[others], want_lse[others])
+    c.check(out, lse, only=[2])
+
+
+@pytest.mark.parametrize("cap", [1e4, 30.0])
+def test_hidden_drafts_do_not_choose_the_arithmetic(cap):
+    """One draft's K grows far beyond the cap; the nodes whose masks do not name it keep their bits."""
+    c = Case([(4, 96)], [21, 3], nodes=9, Hq=4, Hk=2, cap=cap, slopes=True, seed=35)
+    want, want_lse = c.run()
+    c.keys[1][c.lens[1] + 2] *= 1e4
+    c.fill()
+    out, lse = c.run()
+    sees = [m >> 2 & 1 for m in c.masks[1]]
+    assert 0 < sum(sees) < 9
+    for i in range(c.n):
+        rows = [t for t in range(9) if i != 1 or not sees[t]]
+        assert torch.equal(out[i, rows], want[i, rows]) and torch.equal(lse[i, rows], want_lse[i, rows])
+    c.check(out, lse, only=[1])

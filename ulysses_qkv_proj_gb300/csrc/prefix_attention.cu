@@ -549,6 +549,11 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
+// Of the drafts that a row's mask names, those that have a place (`slots`).
+__device__ __forceinline__ uint64_t seen_drafts(int slots, uint64_t mask) {
+  return slots < 64 ? mask & ((1ull << slots) - 1) : mask;
+}
+
 // Two threads a row, half a tile each.  SCORED: scores are capped or biased, and come out in base 2; else the scale is
 // applied with the maximum.
 template <typename L, int D, bool BF16, bool SCORED>
@@ -630,7 +635,8 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
         float offset = 0.f;  // (SCORED) of the first eight columns; the next ones' lie 8 slopes apart
         if (SCORED) {
           // c tanh(x / c) = x + x (x / c)^2 P: the polynomial P is fitted by least squares up to 0.35 (4e-8 relative) and up to
-          // 1 (6e-8); beyond, for a warp that holds any such score, 1 - 2 / (1 + e^2z): to 2^-22 of the cap, however large.
+          // 1 (6e-8); beyond, 1 - 2 / (1 + e^2z): to 2^-22 of the cap, however large.  The largest score that a thread's row sees
+          // of its half tile says which, so that no other row, unused slot or hidden draft changes a bit of it.
           // The distance bias of a column is slope (i % 8), added here, and its eight columns' offset, added to their maximum and
           // with the row's maximum before the exponential.
           const int d0 = pos0 + c0;
@@ -651,17 +657,29 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
           float most = 0.f;
           if (a.cap_log2 > 0.f) {
             float most1 = 0.f;
+            if (!tail) {
 #pragma unroll
-            for (int i = 0; i < kCols; i += 4) {
-              most = max3(most, fabsf(__uint_as_float(v[i / 32][i % 32])), fabsf(__uint_as_float(v[i / 32][(i + 1) % 32])));
-              most1 = max3(most1, fabsf(__uint_as_float(v[i / 32][(i + 2) % 32])), fabsf(__uint_as_float(v[i / 32][(i + 3) % 32])));
+              for (int i = 0; i < kCols; i += 4) {
+                most = max3(most, fabsf(__uint_as_float(v[i / 32][i % 32])), fabsf(__uint_as_float(v[i / 32][(i + 1) % 32])));
+                most1 = max3(most1, fabsf(__uint_as_float(v[i / 32][(i + 2) % 32])), fabsf(__uint_as_float(v[i / 32][(i + 3) % 32])));
+              }
+            } else {
+              const uint64_t bits = seen_drafts(total - len, row.bits);
+#pragma unroll
+              for (int j = 0; j < kCols / 32; ++j) {
+                const uint32_t see = seen_word(pos0 + c0 + 32 * j - len, bits);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                  most = max3(most, see & (1u << i) ? fabsf(__uint_as_float(v[j][i])) : 0.f,
+                              see & (2u << i) ? fabsf(__uint_as_float(v[j][i + 1])) : 0.f);
+              }
             }
-            most = fmaxf(most, most1) * a.cap_in;
+            most = mine && row_ok ? fmaxf(most, most1) * a.cap_in : 0.f;
           }
           auto both = [](float x) { return pair(x, x); };
           if (a.cap_log2 <= 0.f) {
             each_pair([&](uint64_t x, uint64_t bias) { return fma2(x, scale2, bias); });
-          } else if (!__any_sync(0xFFFFFFFFu, most > a.cap_near)) {
+          } else if (most <= a.cap_near) {
             const uint64_t k0 = both(a.cap_poly[0]), k1 = both(a.cap_poly[1]), k2 = both(a.cap_poly[2]);
             auto near = [&](uint64_t y, uint64_t z, uint64_t lead) {
               return fma2(y, fma2(z, fma2(z, fma2(z, k2, k1), k0), 0), lead);
@@ -675,7 +693,7 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
               each_pair([&](uint64_t x, uint64_t bias) {
                 return near(fma2(x, scale2, 0), fma2(x, x, 0), fma2(x, scale2, bias));
               });
-          } else if (!__any_sync(0xFFFFFFFFu, most > 1.f)) {
+          } else if (most <= 1.f) {
             const uint64_t in2 = both(a.cap_in);
             each_pair([&](uint64_t x, uint64_t bias) {
               const uint64_t y = fma2(x, scale2, 0), t = fma2(x, in2, 0), z = fma2(t, t, 0);
@@ -693,6 +711,7 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
               v[i / 32][i % 32] = __float_as_uint(fmaf(rcp_fast(e + 1.f), -2.f * a.cap_log2, a.cap_log2 + row.slope * (i % 8)));
             }
           }
+          __syncwarp();
           if (tail && a.slopes != nullptr && a.depths != nullptr && !s.group) {  // a draft lies at its depth, not at its slot
             const int32_t* depths = a.depths + static_cast<long long>(s.start + member) * a.nodes;
 #pragma unroll 1
@@ -706,8 +725,7 @@ __device__ void run_softmax(const PrefixArgs& a, const Bars& bars, char* smem_ba
           }
         }
         if (tail) {
-          const int slots = total - len;  // drafts that have a place
-          const uint64_t bits = slots < 64 ? row.bits & ((1ull << slots) - 1) : row.bits;
+          const uint64_t bits = seen_drafts(total - len, row.bits);
 #pragma unroll
           for (int j = 0; j < kCols / 32; ++j) {
             const uint32_t see = seen_word(pos0 + c0 + 32 * j - len, bits);
