@@ -1,0 +1,21 @@
+"""More refusals of the calls for many answers: the cache's own state, tables whose numbers leave their range."""
+import ctypes
+
+import pytest
+
+from test_decode_host import A, MB, cache, lib  # noqa: F401
+from test_many_answers_host import attention
+
+
+@pytest.mark.parametrize("name", ["out", "lse", "ws"])
+@pytest.mark.parametrize("state", [dict(page_refs=0), dict(scratch=0), dict(scratch=-16 * 4 - 12)])
+def test_outputs_keep_off_page_counts_and_scratch(lib, name, state):
+    """No output may lie over page_refs or scratch (the last case: over its last word alone)."""
+    at = dict(out=A + 220 * MB, lse=A + 230 * MB, ws=A + 240 * MB)[name]
+    assert attention(lib, c=cache(**{k: at + x for k, x in state.items()})) == 4
+
+
+@pytest.mark.parametrize("state", [dict(page_refs=0), dict(scratch=0), dict(scratch=-16 * 4 - 12)])
+def test_common_lengths_keep_off_page_counts_and_scratch(lib, state):
+    c = cache(**{k: A + 202 * MB + x for k, x in state.items()})
+    assert lib.qnre_cache_shared_prefix(ctypes.byref(c), A + 200 * MB, 4, A + 201 * MB, 2, A + 202 * MB, None) == 4

@@ -73,5 +73,8 @@ inline uint64_t pool_bytes(const qnre_cache_t* c) {
   return static_cast<uint64_t>(c->layers) * c->pages * c->heads * c->page_size * c->head_dim * 2;
 }
 
+// Bytes of the cache's scratch.
+inline uint64_t scratch_bytes(const qnre_cache_t* c) { return (4 * static_cast<uint64_t>(c->pages) + 4) * 4; }
+
 }  // namespace api
 }  // namespace qnre

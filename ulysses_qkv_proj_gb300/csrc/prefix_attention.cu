@@ -1457,6 +1457,7 @@ qnre_status_t qnre_cache_shared_prefix(const qnre_cache_t* cache, const int32_t*
                           span(cache->block_table, static_cast<uint64_t>(cache->rows) * cache->max_blocks * 4),
                           span(cache->seq_lens, static_cast<uint64_t>(cache->rows) * 4),
                           span(cache->page_refs, static_cast<uint64_t>(cache->pages) * 4), span(cache->status, 4),
+                          span(cache->scratch, scratch_bytes(cache)),
                           span(cache->k, pool_bytes(cache)), span(cache->v, pool_bytes(cache))};
   for (const ByteRange& r : in)
     if (overlaps(w, r)) return QNRE_ERR_ALIAS;
@@ -1535,7 +1536,9 @@ qnre_status_t qnre_prefix_attention(const qnre_tensor4_t* q, const qnre_cache_t*
                              words(slopes, static_cast<uint64_t>(Hq) * 4),
                              span(cache->block_table, static_cast<uint64_t>(cache->rows) * cache->max_blocks * 4),
                              span(cache->seq_lens, static_cast<uint64_t>(cache->rows) * 4),
-                             span(cache->status, 4)};
+                             span(cache->page_refs, static_cast<uint64_t>(cache->pages) * 4),
+                             span(cache->status, 4),
+                             span(cache->scratch, scratch_bytes(cache))};
   for (int i = 0; i < 3; ++i) {
     for (const ByteRange& r : reads)
       if (overlaps(writes[i], r)) return QNRE_ERR_ALIAS;
