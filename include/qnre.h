@@ -773,7 +773,7 @@ typedef struct {
  *   cos_sin  device fp32 [n_pos, rot], 16-byte aligned; rot a multiple of 16 up to 128.
  *   theta    > 1, finite.   first >= 0, first + n_pos <= 2^31.
  *   scaling  host struct or NULL (unscaled, magnitude 1).
- * Angles are exact to the 64-bit rounding of their frequency at every position.  n_pos == 0 is an empty call.
+ * Angles are those of the frequencies rounded to 64-bit floats, to p 2^-65 of a turn at position p.  n_pos == 0 is an empty call.
  */
 qnre_status_t qnre_rope_table(float* cos_sin, int64_t n_pos, int rot, int64_t first, double theta,
                               const qnre_rope_scaling_t* scaling, qnre_stream_t stream);

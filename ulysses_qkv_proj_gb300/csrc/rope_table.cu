@@ -2,10 +2,11 @@
 //
 //   row p = m [cos(p f_0) .. cos(p f_{h-1}) | sin(p f_0) .. sin(p f_{h-1})],  h = rot / 2
 //
-// The h frequencies are formed once on the host in 64 bits and passed as fractions of a turn in units of 2^-64.  A phase
-// is then one integer product modulo 2^64: the multiples of a turn fall off exactly, so position 2^31 keeps the 2^-53 of its
-// frequency and no angle is ever reduced in floating point.  The quarter turn is taken off the integer too, and the rest, in
-// [-1/8, 1/8] turn, becomes a float that keeps its leading bits however small it is.  Sine and cosine of it are
+// The h frequencies are formed once on the host in 64 bits and passed as fractions of a turn, rounded to units of 2^-64.  A phase
+// is then one integer product modulo 2^64: the multiples of a turn fall off exactly, so that position p adds at most p 2^-65 of a
+// turn (2^-34 at the last one) to what the 64-bit rounding of its frequency is, and no angle is ever reduced in floating
+// point.  The quarter turn is taken off the integer too, and the rest, in [-1/8, 1/8] turn, becomes a float that
+// keeps its leading bits however small it is.  Sine and cosine of it are
 // polynomials of odd and even powers, fitted for the least relative error by weighted least squares (4e-9 and
 // 6e-11 before rounding; evaluated in fp32 at most 0.8 and 1.0 units in the last place off, 0.3 on average).
 //
@@ -126,7 +127,7 @@ extern "C" qnre_status_t qnre_rope_table(float* cos_sin, int64_t n_pos, int rot,
       f = f * (keep + (1.0 - keep) / s.factor);
     }
     const double turns = f / two_pi;  // a whole turn a position changes nothing
-    a.turn[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+    a.turn[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(turns - std::floor(turns), 64)));
   }
   const int64_t per = kThreads / a.quads;
   a.rows = n_pos >= per * 152 * 64 ? 4 : 1;  // few rows: as many threads as there are
