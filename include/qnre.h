@@ -771,7 +771,7 @@ typedef struct {
  *   cos_sin[p - first] = magnitude [cos(p f_0) .. cos(p f_{rot/2-1}) | sin(p f_0) .. sin(p f_{rot/2-1})]
  *
  *   cos_sin  device fp32 [n_pos, rot], 16-byte aligned; rot a multiple of 16 up to 128.
- *   theta    > 1, finite.   first >= 0, first + n_pos <= 2^31.
+ *   theta    > 1, finite.   first >= 0, first + n_pos <= 2^31.   Scaled frequencies and the magnitude as a float: finite.
  *   scaling  host struct or NULL (unscaled, magnitude 1).
  * Angles are those of the frequencies rounded to 64-bit floats, to p 2^-65 of a turn at position p.  n_pos == 0 is an empty call.
  */

@@ -5,6 +5,7 @@ import pytest
 
 from test_decode_host import A, MB, cache, lib  # noqa: F401
 from test_many_answers_host import attention
+from ulysses_qkv_proj_gb300 import binding as qb
 
 
 @pytest.mark.parametrize("name", ["out", "lse", "ws"])
@@ -19,3 +20,15 @@ def test_outputs_keep_off_page_counts_and_scratch(lib, name, state):
 def test_common_lengths_keep_off_page_counts_and_scratch(lib, state):
     c = cache(**{k: A + 202 * MB + x for k, x in state.items()})
     assert lib.qnre_cache_shared_prefix(ctypes.byref(c), A + 200 * MB, 4, A + 201 * MB, 2, A + 202 * MB, None) == 4
+
+
+@pytest.mark.parametrize("kw", [
+    dict(kind=1, factor=1e-310), dict(kind=3, factor=1e-310, original=100.0), dict(kind=4, factor=1e-310, original=10.0),
+    dict(magnitude=1e39), dict(magnitude=-3.5e38), dict(kind=2, factor=1e-310, theta=1.5),
+])
+def test_tables_out_of_range(lib, kw):
+    """Frequencies or a magnitude that no float holds."""
+    f = dict(kind=0, factor=2.0, original=4096.0, low=1.0, high=32.0, magnitude=1.0, theta=1e4)
+    f.update(kw)
+    s = qb._RopeScaling(*[f[k] for k in ("kind", "factor", "original", "low", "high", "magnitude")])
+    assert lib.qnre_rope_table(A, 8, 64, 0, f["theta"], ctypes.byref(s), None) == 1

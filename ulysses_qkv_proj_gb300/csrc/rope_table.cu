@@ -86,7 +86,7 @@ extern "C" qnre_status_t qnre_rope_table(float* cos_sin, int64_t n_pos, int rot,
   qnre_rope_scaling_t s{QNRE_ROPE_SCALE_NONE, 1.0, 0.0, 0.0, 0.0, 1.0};
   if (scaling != nullptr) s = *scaling;
   if (n_pos < 0 || first < 0 || rot < 1 || rot % 16 != 0 || !(theta > 1.0) || !std::isfinite(theta) ||
-      !std::isfinite(s.magnitude))
+      !std::isfinite(static_cast<float>(s.magnitude)))
     return QNRE_ERR_INVALID_ARG;
   const bool ramp = s.kind == QNRE_ROPE_SCALE_YARN || s.kind == QNRE_ROPE_SCALE_WAVELENGTH;
   if (s.kind < QNRE_ROPE_SCALE_NONE || s.kind > QNRE_ROPE_SCALE_WAVELENGTH) return QNRE_ERR_INVALID_ARG;
@@ -126,6 +126,7 @@ extern "C" qnre_status_t qnre_rope_table(float* cos_sin, int64_t n_pos, int rot,
       const double keep = std::min(std::max((s.original * f / two_pi - s.low) / (s.high - s.low), 0.0), 1.0);
       f = f * (keep + (1.0 - keep) / s.factor);
     }
+    if (!std::isfinite(f)) return QNRE_ERR_INVALID_ARG;  // (a factor so small that a quotient leaves the range)
     const double turns = f / two_pi;  // a whole turn a position changes nothing
     a.turn[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(turns - std::floor(turns), 64)));
   }
