@@ -24,3 +24,10 @@ def test_slowest_frequencies_are_rounded(units):
     want = torch.sin(2 * math.pi * units * 2.0 ** -64 * p)
     err = (out[:, rot // 2].cpu().double() - want).abs()
     assert (err <= 2 * math.pi * p * 2.0 ** -65 + 2.0 ** -22 * want).all()
+
+
+@pytest.mark.parametrize("factor,want", [(0.25, 1.0), (1.0, 1.0), (4.0, 0.1 * math.log(4.0) + 1.0)])
+def test_default_magnitude_grows_with_stretched_tables_alone(factor, want):
+    out = torch.empty((1, 64), device="cuda")
+    _qb().qnre_rope_table(out, scaling="yarn", factor=factor, original=4096.0)
+    assert (out[0, :32].cpu() - want).abs().max() <= 2.0 ** -23 and not out[0, 32:].any()

@@ -912,14 +912,14 @@ def qnre_rope_table(cos_sin, theta: float = 1e4, first: int = 0, scaling: str = 
                     magnitude: Optional[float] = None, stream=None) -> None:
     """Fill cos_sin (fp32 [n_pos, rot]) with rows [cos | sin] of positions first.., frequencies scaled as `scaling` says
     (none, linear, base, yarn, wavelength).  high defaults to 32 turns (yarn) or 4 (wavelength), magnitude to
-    0.1 ln(factor) + 1 for yarn and 1 otherwise."""
+    0.1 ln(factor) + 1 for yarn with a factor above 1, and to 1 otherwise."""
     where = "qnre_rope_table"
     lib = load_library()
     kind = ROPE_SCALINGS.get(scaling, -1)
     if high is None:
         high = 32.0 if kind == 3 else 4.0
     if magnitude is None:
-        magnitude = 0.1 * math.log(factor) + 1.0 if kind == 3 and factor > 0 else 1.0
+        magnitude = 0.1 * math.log(factor) + 1.0 if kind == 3 and factor > 1 else 1.0
     if _native is not None:
         st = _native.rope_table(_entry[where], cos_sin, theta, first, kind, factor, original, low, high, magnitude, _stream_ptr,
                                 stream)
