@@ -157,6 +157,7 @@ struct Angles {
   int partner;
 };
 
+// (Plain loads, not read-only ones: the kernels start beside the launch before theirs, which may write the table.)
 template <bool RH, bool BACK>
 __device__ __forceinline__ Angles load_angles(const float* row, int rot, int l, int lane) {
   Angles a;
@@ -176,7 +177,7 @@ __device__ __forceinline__ Angles load_angles(const float* row, int rot, int l, 
     a.partner = low ? lane + half / 8 : lane - half / 8;
     const float4* c4 = reinterpret_cast<const float4*>(row + i0);
     const float4* s4 = reinterpret_cast<const float4*>(row + half + i0);
-    const float4 c0 = __ldg(c4), c1 = __ldg(c4 + 1), s0 = __ldg(s4), s1 = __ldg(s4 + 1);
+    const float4 c0 = c4[0], c1 = c4[1], s0 = s4[0], s1 = s4[1];
     const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
     const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
@@ -185,8 +186,8 @@ __device__ __forceinline__ Angles load_angles(const float* row, int rot, int l, 
       a.s[e] = low != BACK ? -s[e] : s[e];
     }
   } else {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + 4 * l));
+    const float4 c = *reinterpret_cast<const float4*>(row + 4 * l);
+    const float4 s = *reinterpret_cast<const float4*>(row + half + 4 * l);
     const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const __grid_con
       Pairs c, sn;
       pairs_of(ang.c, c);
       pairs_of(ang.s, sn);
-      const uint4 raw = __ldg(static_cast<const uint4*>(kind == 0 ? a.wq : a.wk) + l);
+      const uint4 raw = static_cast<const uint4*>(kind == 0 ? a.wq : a.wk)[l];
       unpack<BF16>(raw, w);
       other_channels<RH, BF16>(raw, ang, wp);
 #pragma unroll
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_grad_kernel(const __gri
     const long long place_of = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp;
     const long long first = kind == 0 ? place_of : stride - 1 - place_of;
     Pairs w;
-    unpack<BF16>(__ldg(static_cast<const uint4*>(kind == 0 ? a.wq : a.wk) + l), w);
+    unpack<BF16>(static_cast<const uint4*>(kind == 0 ? a.wq : a.wk)[l], w);
 
     struct Item {
       long long token;

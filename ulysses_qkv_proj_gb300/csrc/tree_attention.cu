@@ -212,7 +212,8 @@ __device__ void run_producer(const AttnArgs& a, const Bars& bars, uint32_t smem,
     const int32_t* table = a.c.table + static_cast<long long>(fetches ? row : 0) * a.c.max_blocks;
     int pos = s.t0 * kTile + chunk * a.box;
     int block = pos / ps, off = pos - block * ps;
-    auto look = [&]() -> int { return fetches && block < a.c.max_blocks ? __ldg(table + block) : -1; };
+    // (a plain load, not a read-only one: the kernel starts beside the launch that writes the table)
+    auto look = [&]() -> int { return fetches && block < a.c.max_blocks ? table[block] : -1; };
     int entry = look();
     if (kv == 0) {  // the unit's Q rows, REP times
       // (one buffer: the last unit's results are still being written when its last scores are done)

@@ -133,13 +133,14 @@ struct Row {
     p -= shift;
     q -= shift;
   }
+  // (Plain loads, not read-only ones: this kernel starts beside the launch that writes the rows, qnre_filter_probs.)
   __device__ __forceinline__ float4 load(const float* row, int y) const {
-    if (y >= shift && y + 4 <= end && (row == p || alike)) return __ldg(reinterpret_cast<const float4*>(row + y));
+    if (y >= shift && y + 4 <= end && (row == p || alike)) return *reinterpret_cast<const float4*>(row + y);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (y >= shift && y < end) v.x = __ldg(row + y);
-    if (y + 1 >= shift && y + 1 < end) v.y = __ldg(row + y + 1);
-    if (y + 2 >= shift && y + 2 < end) v.z = __ldg(row + y + 2);
-    if (y + 3 >= shift && y + 3 < end) v.w = __ldg(row + y + 3);
+    if (y >= shift && y < end) v.x = row[y];
+    if (y + 1 >= shift && y + 1 < end) v.y = row[y + 1];
+    if (y + 2 >= shift && y + 2 < end) v.z = row[y + 2];
+    if (y + 3 >= shift && y + 3 < end) v.w = row[y + 3];
     return v;
   }
 };
