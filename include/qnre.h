@@ -803,7 +803,9 @@ qnre_status_t qnre_rope_table(float* cos_sin, int64_t n_pos, int rot, int64_t fi
  *   slopes   device fp32 [Hq] or NULL.
  *   workspace  qnre_prefix_attention_workspace_bytes (n_groups: 0 or any other), 16-byte aligned, contents undefined before
  *            and after; calls that may overlap (on different streams) need one each.
- * Limits, errors and the care for masked and non-finite values are those of qnre_tree_attention; n nodes Hq <= 2^31-1.
+ * Limits, errors and the care for masked and non-finite values are those of qnre_tree_attention, but that half as many tiles
+ * are served (common and own ones are counted apart); n nodes Hq <= 2^31-1.  No request's values change a bit of another's
+ * result, and a capped score is computed as its own row's scores ask for.  Outputs may not lie over any of the cache's memory.
  * The groups' rows come in any order of the cache's rows, and a row may stand in the call more than once.
  */
 qnre_status_t qnre_cache_shared_prefix(const qnre_cache_t* cache, const int32_t* rows, int n, const int32_t* groups,

@@ -21,20 +21,24 @@
 //
 // Values that a row must not see: as in tree_attention.cu scores are replaced before use.  In a unit of several requests a row's
 // P is zero, whatever its scores, in the tiles of the others, and as 0 inf is NaN the warp that issues the product
-// zeroes V's non-finite elements before it, and V behind a request's tokens.  (It has the time, while the softmax of the tile runs;
-// where the softmax threads cleaned the last tokens' V themselves, the four cases below took 24.8, 123, 97 and 108 us for 22.9, 123,
-// 89 and 102.)  The rows of a request with such an element are marked, and the join gives them their infinite and NaN columns,
-// which it looks up in V (own_strange); all else is the product's, so nothing that one request holds changes a bit of another's result.
+// zeroes V's non-finite elements before it, and V behind a request's tokens.  (It has the time, while the softmax of the tile
+// runs.  Where the softmax threads cleaned the last tokens' V themselves, 8, 128, 48 and 24 requests took 24.8, 123, 97 and 108
+// us, the search for common tokens included, for 22.9, 123, 89 and 102.)  The rows of a request with such an element are marked,
+// and the join gives them their infinite and NaN columns, which it looks up in V (own_strange); all else is the product's, so
+// nothing that one request holds changes a bit of another's result.
 //
-// Bound: long common prefixes and many rows, by a tile's two products and its softmax, which share the SM's tensor memory
-// and issue slots: 128 tokens by 128 rows of D = 128 take 1840 cycles where the products alone are 1024.  128 requests of 64 + 8
-// heads with 6 prefixes of 1500 to 30011 tokens take 115 us (the tensor pipe busy 44 % of it), against 642 when each request reads
-// its prefix.  Own tokens, by the bytes that a few rows each need: 48 requests of up to 3000 own tokens 85 us, floor 27.  Short
-// calls, by latency: 8 requests of 2011 + up to 400 tokens 17.7 us, of them the setup 4, a unit's start and end 4, the join 3.
+// Bound: long common prefixes and many rows, by a tile of 128 tokens by 128 rows of D = 128: 1840 cycles where its products alone
+// are 1024.  That is what the softmax takes, and about what TMA takes to bring its 64 KB into an SM (34 bytes a cycle); the two
+// were not told apart.  128 requests of 64 + 8 heads with 6 prefixes of 1500 to 30011 tokens take 115 us (the tensor pipe busy 44 %
+// of it), against 658 when each request reads its prefix: 72 tiles a CTA are 65-70 us of them, setup and join 7, and the rest is
+// own tiles and units' ends, which were not measured apart.  Own tokens, by latency and the bytes that a few rows each
+// need: 48 requests of up to 3000 own tokens under a cap 86 us, floor 27, over 4000 cycles a tile, as one pair of warps has a
+// tile's one live row.  Short calls, by latency: 8 requests of 2011 + up to 400 tokens 16.3 us, of them the setup 4, a
+// unit's start and end 4, the join 3.
 // Blocks of many requests' own tokens brought the first case from 124 us to 117, a form with smaller tables and a third V stage
 // to 115, the capped case 122 -> 107, and the polynomial for tanh 107 -> 85.  Divisors as products took the setup from 9500
-// cycles to 7640.  Tried and left: turns
-// of four requests' tiles in a block (127 us for 121).
+// cycles to 7640.  Tried and left: turns of four requests' tiles in a block (127 us for 121); V cleaned by softmax warps without a
+// row of the tile (the four cases of more_operators.py 22.7, 129, 110 and 126 us), by the TMA warp a ring behind (25, 148, 100, 117).
 #include "../../include/qnre.h"
 #include "attention_tile.cuh"
 #include "cache.cuh"
@@ -72,7 +76,7 @@ struct Divisor {
   static Divisor of(int d) {
     uint32_t shift = 31;
     while ((1ull << (shift - 31)) < static_cast<uint32_t>(d)) ++shift;
-    return Divisor{static_cast<uint32_t>((1ull << shift) / static_cast<uint32_t>(d) + 1), shift};  // (mul at most 2^31 + 1)
+    return Divisor{static_cast<uint32_t>((1ull << shift) / static_cast<uint32_t>(d) + 1), shift};  // (mul is below 2^32)
   }
   __device__ __forceinline__ int operator()(int x) const {
     return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * mul >> shift);
@@ -459,7 +463,7 @@ __device__ __forceinline__ bool clean_v_tile(uint32_t tile, int from, int to, in
 }
 
 // The same as a call: where the softmax takes all registers, a copy in line cost its schedule more (24 drafted trees with cap and
-// bias 107 us, in line 113; 128 requests' plain scores 126 and 122, 64 channels with a cap 104 and 97).
+// bias 106 us, in line 116; 128 requests' plain scores 129 and 121, 64 channels with a cap 95 and 94).
 template <int D, bool BF16>
 __device__ __noinline__ bool clean_v_tile_apart(uint32_t tile, int from, int to, int end) {
   return clean_v_tile<D, BF16>(tile, from, to, end);
